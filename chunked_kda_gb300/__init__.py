@@ -19,7 +19,10 @@ __all__ = ["kda_gate_fwd", "kda_chunk_workspace_bytes", "kda_chunk_workspace_byt
            "kda_chunk_fwd", "kda_chunk_fwd_ex",
            "kda_chunk_fwd_noalloc", "kda_recurrent_fwd", "KdaError", "GATE_PRE", "GATE_SAFE",
            "GATE_NONSAFE", "GATE_LOG2", "FLAG_K_L2NORM", "FLAG_BETA_LOGITS", "kda_recurrent_fwd_ex",
-           "FLAG_Q_L2NORM", "NOALLOC_SCRATCH_BYTES", "library_path", "load_library"]
+           "FLAG_Q_L2NORM", "NOALLOC_SCRATCH_BYTES", "library_path", "load_library",
+           "kda_decay_chunk_workspace_bytes", "kda_decay_chunk_fwd", "kda_decay_recurrent_fwd",
+           "kda_gated_norm_fwd", "kda_block_norm_fwd", "kda_short_conv_fwd", "ACT_NONE",
+           "ACT_SIGMOID", "ACT_SILU"]
 
 GATE_PRE = 0
 GATE_SAFE = 1
@@ -29,6 +32,7 @@ NOALLOC_SCRATCH_BYTES = 16 << 20  # KDA_NOALLOC_SCRATCH_BYTES in include/kda.h
 FLAG_Q_L2NORM = 1  # KDA_FLAG_Q_L2NORM
 FLAG_K_L2NORM = 2  # KDA_FLAG_K_L2NORM
 FLAG_BETA_LOGITS = 4  # KDA_FLAG_BETA_LOGITS
+ACT_NONE, ACT_SIGMOID, ACT_SILU = 0, 1, 2  # kda_act
 _F32, _BF16 = 0, 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -89,6 +93,21 @@ def load_library():
                                               vp]
         lib.kda_chunk_fwd_noalloc.restype = ctypes.c_int
         for fn in (lib.kda_gate_fwd, lib.kda_chunk_fwd, lib.kda_recurrent_fwd):
+            fn.restype = ctypes.c_int
+        i64, size = ctypes.c_int64, ctypes.c_size_t
+        lib.kda_decay_chunk_workspace_bytes.argtypes = [i32] * 7
+        lib.kda_decay_chunk_workspace_bytes.restype = size
+        lib.kda_decay_chunk_fwd.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32,
+                                            i32, i32, i32, vp, i32, vp, size, vp, vp]
+        lib.kda_decay_recurrent_fwd.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32,
+                                                i32, i32, i32, i32, vp, i32, vp]
+        lib.kda_gated_norm_fwd.argtypes = [vp, vp, i32, vp, f32, i32, i64, i32, vp, vp]
+        lib.kda_block_norm_fwd.argtypes = [vp, i32, vp, i32, vp, vp, i32, f32, vp, vp, f32, i64, i32,
+                                           vp, vp, vp]
+        lib.kda_short_conv_fwd.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32,
+                                           vp, vp]
+        for fn in (lib.kda_decay_chunk_fwd, lib.kda_decay_recurrent_fwd, lib.kda_gated_norm_fwd,
+                   lib.kda_block_norm_fwd, lib.kda_short_conv_fwd):
             fn.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_status_string.restype = ctypes.c_char_p
@@ -365,3 +384,7 @@ def kda_recurrent_fwd_ex(q, k, v, g, beta, A_log=None, dt_bias=None, mode=GATE_L
         lower_bound, _ptr(beta), _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), n, B,
         T, H, K, V, _ptr(o), _dt(o, "o"), Hk, flags, _stream(stream)))
     return o, final_state
+
+
+from ._block import (kda_block_norm_fwd, kda_decay_chunk_fwd, kda_decay_chunk_workspace_bytes,  # noqa: E402
+                     kda_decay_recurrent_fwd, kda_gated_norm_fwd, kda_short_conv_fwd)

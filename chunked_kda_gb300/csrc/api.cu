@@ -58,6 +58,10 @@ kda_status check_gate(kda_gate_mode mode, const float* A_log, float lower_bound)
 
 namespace kda {
 void record_error(const char* msg) { g_last_error = msg; }
+kda_status launch_status(cudaError_t e) { return cuda_status(e); }
+kda_status check_sequences(const int32_t* cu, int n_seqs, int B, int T, int H, int* N) {
+    return check_layout(cu, n_seqs, B, T, H, N);
+}
 
 // The host checks of the chunked forward, shared by kda_chunk_fwd_ex and kda_chunk_fwd_noalloc;
 // fills *N (logical sequences)

@@ -83,6 +83,36 @@ struct ChunkMap {
         len = min(C, eos - t0);
         return len > 0;
     }
+    // map() for operators with work for an empty sequence too (its state): a sequence's first slot
+    // fills n, t0 == bos and len = 0 where it has no token.  n = -1: the slot belongs to none;
+    // true: the slot has tokens.
+    __device__ bool map_first(int x, int& n, int& t0, int& len, int& bos, int& eos) const {
+        if (!cu) {
+            const int per = max(1, (T + C - 1) / C);
+            n = x / per;
+            const int c = x - n * per;
+            if (n >= N) { n = -1; return false; }
+            bos = n * T;
+            eos = bos + T;
+            t0 = bos + c * C;
+            len = min(C, eos - t0);
+            return len > 0;
+        }
+        n = -1;
+        int lo = 0, hi = N - 1;  // the largest n with floor(cu[n] / C) + n <= x
+        while (lo <= hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(cu + mid) / C + mid <= x) { n = mid; lo = mid + 1; } else { hi = mid - 1; }
+        }
+        if (n < 0) return false;
+        bos = __ldg(cu + n);
+        eos = __ldg(cu + n + 1);
+        const long c = x - (bos / C + n);
+        if (c > 0 && bos + c * C >= eos) { n = -1; return false; }  // behind the sequence's last chunk
+        t0 = bos + (int)c * C;
+        len = min(C, eos - t0);
+        return len > 0;
+    }
     // first slot of sequence n
     __device__ int first_slot(int n, int bos) const {
         return cu ? (bos / C + n) : n * ((T + C - 1) / C);

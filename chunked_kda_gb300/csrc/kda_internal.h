@@ -75,6 +75,80 @@ struct RecArgs {
     int Hk = 0;          // query / key heads (a divisor of H; value head h reads h / (H / Hk))
 };
 
+// linear attention with a decay for each head
+struct DecayArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    bool qkv_bf16;
+    const float* decay;  // natural log: [B, T, H] (per_token) or [H]
+    bool per_token;
+    const float* h0;
+    float* hT;
+    const int32_t* cu;
+    int N;  // logical sequences (B when dense)
+    int B, T, H, Hk, K, V;
+    void* o;
+    bool o_f32;  // o is float32 (else the qkv dtype)
+    void* ws;
+    int* status;
+    cudaStream_t stream;
+};
+
+struct GatedNormArgs {
+    const void* x;
+    const void* gate;
+    bool bf16;
+    const float* weight;  // or null
+    float eps;
+    int act;
+    long rows;
+    int V;
+    void* y;
+    cudaStream_t stream;
+};
+
+struct BlockNormArgs {
+    const void* x;
+    bool bf16;             // x, gate and y
+    const void* residual;  // or null
+    bool res_bf16;         // residual and h
+    const float* post_w;   // or null: no norm of x
+    const void* gate;      // or null
+    int act;
+    float scale;
+    const float* channel_scale;  // or null
+    const float* pre_w;          // or null: y = h
+    float eps;
+    long rows;
+    int D;
+    void* h;
+    void* y;
+    cudaStream_t stream;
+};
+
+struct ConvArgs {
+    const void* x;
+    bool bf16;  // x, states and y
+    const float* weight;
+    const float* bias;
+    int act;
+    int W;
+    const void* s0;
+    void* s1;
+    const int32_t* cu;
+    int N, B, T, D;
+    void* y;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_decay_recurrent(const DecayArgs& a);
+size_t decay_chunk_workspace_bytes(bool qkv_bf16, int B, int T, int H, int K, int V, int N, bool packed);
+cudaError_t launch_decay_chunk(const DecayArgs& a);
+cudaError_t launch_gated_norm(const GatedNormArgs& a);
+cudaError_t launch_block_norm(const BlockNormArgs& a);
+cudaError_t launch_short_conv(const ConvArgs& a);
+
 cudaError_t launch_gate(const GateArgs& a);
 cudaError_t launch_recurrent(const RecArgs& a);
 
@@ -122,6 +196,10 @@ inline Path select_path(bool qkv_bf16, int K, int V, int C, int mode, int H, boo
 
 // sets the message kda_last_error() returns on this host thread
 void record_error(const char* msg);
+// the status of a launch, its CUDA error recorded as that message
+kda_status launch_status(cudaError_t e);
+// B, T, H, cu_seqlens and n_seqs of an entry point; fills *N (logical sequences)
+kda_status check_sequences(const int32_t* cu, int n_seqs, int B, int T, int H, int* N);
 
 // every host check of the chunked forward (layout and size limits, dtypes, head dims, chunk
 // size, gate mode and bound, null and misaligned pointers), shared by kda_chunk_fwd_ex and

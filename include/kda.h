@@ -336,7 +336,112 @@ kda_status kda_recurrent_fwd_ex(const void* q, const void* k, const void* v, kda
                                 int V, void* o, kda_dtype o_dtype, int n_qk_heads,
                                 unsigned flags, kda_stream_t stream);
 
-/* static, NUL-terminated description of a status code */
+/*
+ * ---------------------------------------------------------------------------
+ * The operators around the recurrence in a linear-attention block: linear
+ * attention with a decay for each head, the gated norm of its heads, the norm
+ * around the block, and the short causal convolution in front.  Forward only.
+ * Conventions (device pointers, 16-byte alignment, packed sequences, host
+ * checks, no allocation, no synchronisation, graph capture) as above.
+ * ---------------------------------------------------------------------------
+ */
+
+/* the activation of a gate or of the convolution's output */
+typedef enum {
+    KDA_ACT_NONE = 0,    /* z (the gate multiplies as it is) */
+    KDA_ACT_SIGMOID = 1, /* 1 / (1 + exp(-z)) */
+    KDA_ACT_SILU = 2     /* z / (1 + exp(-z)) */
+} kda_act;
+
+/*
+ * Linear attention with a decay for each head.  Per head, FP32 state S (K x V):
+ *
+ *     S_t = exp(a_t) S_{t-1} + k_t v_t^T;   o_t = S_t^T q_t / sqrt(K)
+ *
+ *   q, k       [B, T, n_qk_heads, K], dtype qkv_dtype; value head h (of H)
+ *              reads query / key head h / (H / n_qk_heads); 0 means H heads
+ *   v, o       [B, T, H, V]; o_dtype the qkv dtype or KDA_F32
+ *   decay      float32, natural log: [B, T, H] (decay_per_token != 0) or [H],
+ *              the same for all tokens.  -inf clears the state at its token;
+ *              a <= 0 is the meant range.
+ *   states     [N, H, K, V] float32; final_state may be initial_state
+ *   K, V       any value from 1 to 256
+ *   status     as for kda_chunk_fwd_ex
+ *
+ * kda_decay_chunk_fwd is the form for prompts: it works in chunks of tokens,
+ *     o_i = ( exp(G_i) S_in^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j ) / sqrt(K)
+ *     S_out = exp(G_l) S_in + sum_j exp(G_l - G_j) k_j v_j^T
+ * with G the running sum of a in the chunk and l its last token.  Its scratch is
+ * kda_decay_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for
+ * dense inputs).  kda_decay_recurrent_fwd is the form for single tokens and
+ * computes token by token in FP32.
+ */
+size_t kda_decay_chunk_workspace_bytes(kda_dtype qkv_dtype, int B, int T, int H, int K, int V,
+                                       int n_seqs);
+
+kda_status kda_decay_chunk_fwd(const void* q, const void* k, const void* v, kda_dtype qkv_dtype,
+                               const float* decay, int decay_per_token,
+                               const float* initial_state, float* final_state,
+                               const int32_t* cu_seqlens, int n_seqs, int B, int T, int H,
+                               int n_qk_heads, int K, int V, void* o, kda_dtype o_dtype,
+                               void* workspace, size_t workspace_bytes, int32_t* status,
+                               kda_stream_t stream);
+
+kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
+                                   kda_dtype qkv_dtype, const float* decay, int decay_per_token,
+                                   const float* initial_state, float* final_state,
+                                   const int32_t* cu_seqlens, int n_seqs, int B, int T, int H,
+                                   int n_qk_heads, int K, int V, void* o, kda_dtype o_dtype,
+                                   kda_stream_t stream);
+
+/*
+ * Gated norm of the heads' outputs: per row of V elements
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate)
+ *
+ *   x, gate, y  [rows, V], dtype (KDA_F32 or KDA_BF16); y may be x or gate
+ *   weight      [V] float32 or NULL (= 1)
+ */
+kda_status kda_gated_norm_fwd(const void* x, const void* gate, kda_dtype dtype,
+                              const float* weight, float eps, kda_act act, int64_t rows, int V,
+                              void* y, kda_stream_t stream);
+
+/*
+ * The norm around a block, with its gate, residual and scale: per row of D elements
+ *     n = x [/ sqrt(mean(x^2) + eps) * post_weight] [* act(gate)]
+ *     h = [residual +] scale [* channel_scale] * n
+ *     y = h [/ sqrt(mean(h^2) + eps) * pre_weight]
+ * each bracket present where its pointer is not NULL.  x is a block's output, h the
+ * residual stream behind it, y the next block's input.
+ *
+ *   x, gate, y       [rows, D], dtype
+ *   residual, h_out  [rows, D], residual_dtype; h_out may be residual
+ *   weights, scales  [D] float32
+ *   h_out, y_out     either may be NULL.  y comes from h before its rounding.
+ */
+kda_status kda_block_norm_fwd(const void* x, kda_dtype dtype, const void* residual,
+                              kda_dtype residual_dtype, const float* post_weight,
+                              const void* gate, kda_act act, float scale,
+                              const float* channel_scale, const float* pre_weight, float eps,
+                              int64_t rows, int D, void* h_out, void* y_out,
+                              kda_stream_t stream);
+
+/*
+ * Short causal convolution of each channel, in front of the recurrence:
+ *     y_t[d] = act(bias[d] + sum_{w < W} weight[d][w] x_{t-W+1+w}[d])
+ * where the rows before a sequence's first token come from its state.
+ *
+ *   x, y        [B, T, D], dtype
+ *   weight      [D, W] float32, W from 2 to 8; bias [D] float32 or NULL
+ *   states      [N, W-1, D], dtype: the last W-1 inputs, the oldest first.
+ *               initial_state NULL = zeros; final_state NULL = not written;
+ *               both may be one buffer (single tokens: every sequence one token).
+ *               An empty sequence passes its state through.
+ */
+kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weight,
+                              const float* bias, kda_act act, int W, const void* initial_state,
+                              void* final_state, const int32_t* cu_seqlens, int n_seqs, int B,
+                              int T, int D, void* y, kda_stream_t stream);
+
 /*
  * Diagnostics of the tensor-core paths' bounded waits.  Every mbarrier wait of the fused
  * and two-pass chunked kernels gives up after a fixed number of polls; a CTA whose wait gave
@@ -369,6 +474,7 @@ kda_status kda_fused_wait_timeouts(unsigned int* count, int reset);
  */
 kda_status kda_test_hooks(int wait_timeout_chunk, int sm_count, int one_launch, int two_pass_d128);
 
+/* static, NUL-terminated description of a status code */
 const char* kda_status_string(kda_status status);
 
 /* the last error detail recorded by a failed call on this host thread ("" if none) */
