@@ -1,0 +1,914 @@
+// Linear attention with a decay for each head in chunks of 64 tokens, bf16 inputs, on the tensor
+// cores (tcgen05 with TMEM accumulators, TMA loads).
+//
+// Per chunk of a (sequence, head, block of value channels), G_i the decay's sum in log2 units up to
+// and including row i, l the last row, s = 1/sqrt(K):
+//   P[i][j] = 2^(G_i - G_j) (q_i . k_j)  for j <= i, else 0                     (bf16 operand)
+//   o_i     = s (2^G_i S^T q_i + sum_j P[i][j] v_j)
+//   S      <- 2^G_l S + sum_j (2^(G_l - G_j) k_j) v_j^T                         (FP32)
+// as four products, value channels (M = 128) on TMEM lanes:
+//   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += v^T kd.
+// q, k and v enter the products as they are; O1's row factor 2^G_i and s are applied to the FP32
+// results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
+// difference of an integer and of a fraction part (64-bit fixed-point sums), exact whatever the sums.
+//
+// Roundings: P and the copy of S that O1 reads are bf16 (each adds the output's own rounding once
+// more; both in quadrature keep o's error within 1.45 of one rounding).  The state is a float32 output and
+// feeds every later chunk, so the scaled keys kd are split into three bf16 terms (24 bits) and S is
+// accumulated from all three: 3 x 256 of the chunk's ~1400 tensor-pipe clocks.
+//
+// One CTA per unit and SM, 25 warps: 0-1 P, 2 decay factors, 3 loads and the state's products, 4-11
+// state, 12-15 output, 16-23 scaled keys, 24 the output's products.  Every wait is bounded (a CTA that gives up lets its copies and MMAs
+// finish, frees its TMEM and returns).
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "kda_internal.h"
+#include "sm100.cuh"
+
+namespace kda {
+namespace decay {
+
+using namespace sm100;
+
+__device__ unsigned int g_decay_timeouts = 0;
+
+constexpr int C = 64, NTHR = 800, NS = 3, NG = 8;
+
+// barriers
+enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P = B_QK + 2, B_SBF = B_P + 2, B_KD, B_STATE = B_KD + 2, B_INTER, B_O,
+       B_OFREE = B_O + 2, B_DRAIN = B_OFREE + 2, B_DRAIN2, B_NEVER, NBAR };
+
+// The decay factors of a chunk, one slot of a ring of NG (written when the chunk is loaded, read
+// last by its output warps, at most NS + 3 chunks later): byte offsets of its float arrays.
+constexpr uint32_t GT_G = 0;       // [64][2] G_i as integer and fraction
+constexpr uint32_t GT_ROW = 512;   // [64] s 2^G_i
+constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j)
+constexpr uint32_t GT_HALF = 1024; // [32] 2^(G_31 - G_j)
+constexpr uint32_t GT_LAST = 1152; // 2^G_l
+constexpr uint32_t GT_BYTES = 1168;
+
+template <int KD, int VB>
+struct Layout {
+    static constexpr uint32_t QB = C * KD * 2, VBYTES = C * VB * 2, STAGE = 2 * QB + VBYTES;
+    static constexpr uint32_t KM = NS * STAGE, KL = KM + QB, P = KL + QB, O = P + 2 * C * C * 2, G = O + VBYTES;
+    static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = BAR + 8 * NBAR, END = MISC + 16;
+    // an A operand of 64 rows or channels is read as 128: up to 8 KB behind its tile
+    static constexpr uint32_t BYTES = END + 1024 + 64;
+};
+// TMEM columns: S^T, its bf16 copy, two buffers of QK and of O1, O2
+constexpr uint32_t TM_S = 0, TM_SB = 128, TM_QK = 192, TM_O1 = 320, TM_O2 = 448, TM_COLS = 512;
+
+struct Params {
+    const float* decay;
+    int decay_stride;  // floats between tokens (H, or 0 for one decay per head)
+    const float* h0;
+    float* hT;
+    const int32_t* cu;
+    void* o;
+    int N, T, H, hr, K, V;
+    int seg;        // tokens of a segment (a multiple of C), 0: whole sequences
+    float* ws;      // segment states [slot][h][K][V]
+    float* wdec;    // segment decays [slot][h]
+    int* status;
+    int stall_chunk;
+};
+
+struct Sync {
+    uint32_t bars;
+    volatile uint32_t* abort_flag;
+    int* status;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
+    __device__ __forceinline__ void give_up() const {
+        atomicAdd(&g_decay_timeouts, 1u);
+        if (status) atomicOr(status, 1);
+        *abort_flag = 1u;
+    }
+    // (out of line: one copy, so that the loops stay in the instruction caches)
+    __device__ __noinline__ void slow_wait(int i, uint32_t parity, uint32_t limit) const {
+        if (!*abort_flag && !mbar_wait_unless(bar(i), parity, abort_flag, limit)) give_up();
+    }
+    __device__ __forceinline__ bool ready(int i, uint32_t parity) const { return mbar_try_wait(bar(i), parity, 0); }
+    __device__ __forceinline__ bool aborted() const { return *abort_flag != 0u; }
+    // A whole warp's wait, the same answer in every lane: false when a wait has given up and this
+    // one's phase has not come.
+    __device__ __forceinline__ bool warp_wait(int i, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
+        slow_wait(i, parity, 1u << 22);
+        return __all_sync(0xffffffffu, !aborted());
+    }
+};
+
+// A product's operand in shared memory: the descriptor's low word changes with the address (16-byte
+// units), its high word (stride 1024 bytes between groups of 8 rows, 128-byte swizzle) does not.
+__device__ __forceinline__ uint32_t lo_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }               // K-major
+__device__ __forceinline__ uint32_t lo_mn(uint32_t addr) { return (addr >> 4) | ((8192u >> 4) << 16); }    // MN-major, 64 apart
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)DESC_HI << 32) | lo; }
+// True in one lane of a converged warp.  The products are issued inside a branch on this: there
+// their descriptors stay in uniform registers and a product of 128 x 64 x 16 issues in 31 to 48
+// clocks, its own time; in a branch on the lane number, or each predicated, it took 50 to 85.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// the issued stores have read their shared memory / are complete
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ float lds(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 lds2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void sts2(uint32_t a, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void ld_s128(uint32_t a, uint32_t* v) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void ld32(uint32_t t, float* v) {
+    tmem_ld16(t, v);
+    tmem_ld16(t + 16, v + 16);
+}
+// 16 lanes x 32 columns: thread t gets lanes t / 4 and t / 4 + 8 and of each eight columns the pair
+// 2 (t % 4), 2 (t % 4) + 1: v[4 g + 0..1] the first lane's, v[4 g + 2..3] the second's
+__device__ __forceinline__ void ld16x32(uint32_t t, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// two FP32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+// four 8 x 8 matrices of 16-bit elements, each stored transposed; lane i holds the address of
+// (transposed) row i % 8 of matrix i / 8
+__device__ __forceinline__ void stmatrix4_t(uint32_t a, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+// The upper bf16 halves of two floats as a pair, and what they leave.  Cutting three times gives a
+// float's 24 significant bits as three bf16 terms exactly: 8 + 8 + 8 (a cut leaves a remainder that
+// the next term holds, as a rounding would, without a conversion).
+__device__ __forceinline__ uint32_t cut(float2& x) {
+    const uint32_t top = 0xFFFF0000u, a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    x = fma2(make_float2(__uint_as_float(a & top), __uint_as_float(b & top)), make_float2(-1.f, -1.f), x);
+    return __byte_perm(a, b, 0x7632);
+}
+
+// kStates: only the state a segment adds (no queries, no output), for the segments' scan.
+template <int KD, int VB, typename OT, bool kStates>
+__global__ void __launch_bounds__(NTHR, 1)
+decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, Params p) {
+    using L = Layout<KD, VB>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::MISC);
+    const Sync sy{sb + L::BAR, misc + 1, p.status};
+    // (the aligned base is not known to be shared memory: a slot's floats are read by address)
+    auto gates = [&](int c) { return sb + L::G + (uint32_t)(c % NG) * GT_BYTES; };
+    const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), l = tid & 31;
+
+    // ---- the unit: heads fastest, then value blocks
+    const int h = blockIdx.x, vb = blockIdx.y, slot = blockIdx.z;
+    int n, bos, eos;
+    bool first = true, last = true;
+    if (p.seg == 0) {
+        n = slot;
+        if (p.cu) { bos = __ldg(p.cu + n); eos = __ldg(p.cu + n + 1); }
+        else      { bos = n * p.T; eos = bos + p.T; }
+    } else {
+        const ChunkMap cm{p.cu, p.N, p.T, p.seg};
+        int t0, len, b0, e0;
+        cm.map_first(slot, n, t0, len, b0, e0);
+        if (n < 0) return;
+        first = t0 == b0;
+        last = t0 + len >= e0;
+        bos = t0;
+        eos = t0 + len;
+        if (kStates && last) return;  // nothing follows it
+    }
+    const int nt = __shfl_sync(0xffffffffu, (eos - bos + C - 1) / C, 0);
+    const int hq = h / p.hr, vc0 = vb * VB;
+
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) {
+            int count = 1;
+            if (i >= B_FULL && i < B_FULL + NS) count = 2;                 // the loads and the decay factors
+            if (i >= B_FREE && i < B_FREE + NS) count = kStates ? 1 : 2;   // the products of both issuing warps
+            if (i == B_P || i == B_P + 1) count = 2;                       // two P warps
+            if (i == B_OFREE || i == B_OFREE + 1) count = 4;               // four output warps
+            if (i >= B_SBF && i < B_KD + 2) count = 8;                     // eight warps
+            mbar_init(sy.bar(i), count);
+        }
+        fence_mbar_init();
+        misc[1] = 0;
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_o);
+    }
+    if (w == 3) tmem_alloc(sb + L::MISC, TM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
+
+    if (w < 2) {
+        // ------------------------------------------------ P = QK with the decays, bf16, K-major rows
+        if constexpr (!kStates) {
+            const int i = 32 * w + l;
+            const float scale = rsqrtf((float)p.K), log2_scale = -0.5f * log2f((float)p.K);
+            if (w == 0)  // the upper right quarter of both buffers stays zero
+                for (int x = 0; x < 8; ++x) st_s128(sb + L::P + (x >> 2) * (C * C * 2) + sw128(i, 4 + (x & 3)), 0, 0, 0, 0);
+#pragma unroll 1
+            for (int c = 0; c < nt; ++c) {
+                const int b = c & 1;
+                if (!sy.warp_wait(B_FULL + c % NS, (c / NS) & 1)) break;                // the decay factors
+                if (!sy.warp_wait(B_QK + b, (c >> 1) & 1)) break;
+                if (c >= 2 && !sy.warp_wait(B_O + b, ((c - 2) >> 1) & 1)) break;        // this P buffer's last reader
+                tc_fence_after();
+                const uint32_t gt = gates(c), row = sb + L::P + b * (C * C * 2);
+                float2 gi = lds2(gt + GT_G + 8 * i);
+                const uint32_t qk = tmem + TM_QK + 64 * b + ((uint32_t)(32 * w) << 16);
+                if (w == 1) {
+                    // rows behind column 31: the factor parts into a row's and a column's, both <= 1
+                    const float2 gh = lds2(gt + GT_G + 8 * 31);
+                    const float fr = scale * ex2_fast((gi.x - gh.x) + (gi.y - gh.y));
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 32; j0 += 16) {
+                        float x[16];
+                        uint32_t out[8];
+                        tmem_ld16(qk + j0, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 f = lds4(gt + GT_HALF + 4 * (j0 + j));
+                            out[j / 2] = pack_bf16(x[j] * (f.x * fr), x[j + 1] * (f.y * fr));
+                            out[j / 2 + 1] = pack_bf16(x[j + 2] * (f.z * fr), x[j + 3] * (f.w * fr));
+                        }
+                        st_s128(row + sw128(i, j0 >> 3), out[0], out[1], out[2], out[3]);
+                        st_s128(row + sw128(i, (j0 >> 3) + 1), out[4], out[5], out[6], out[7]);
+                    }
+                }
+                gi.y += log2_scale;
+#pragma unroll 1
+                for (int j0 = 0; j0 < 32; j0 += 16) {
+                    float x[16];
+                    uint32_t out[8];
+                    tmem_ld16(qk + 32 * w + j0, x);
+                    tmem_wait_ld();
+                    const int last = l - j0;  // columns up to this one of the sixteen
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float4 g = lds4(gt + GT_G + 8 * (32 * w + j0 + j));
+                        const float f0 = ex2_fast((gi.x - g.x) + (gi.y - g.y)), f1 = ex2_fast((gi.x - g.z) + (gi.y - g.w));
+                        out[j / 2] = pack_bf16(j <= last ? x[j] * f0 : 0.f, j + 1 <= last ? x[j + 1] * f1 : 0.f);
+                    }
+                    const int ch = 4 * w + (j0 >> 3);
+                    st_s128(row + sw128(i, ch), out[0], out[1], out[2], out[3]);
+                    st_s128(row + sw128(i, ch + 1), out[4], out[5], out[6], out[7]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (l == 0) mbar_arrive(sy.bar(B_P + b));
+            }
+        }
+    } else if (w == 2) {
+        // ------------------------------------------------ decay factors
+        const float kScale = rsqrtf((float)p.K);
+        const float* dp = p.decay + h;
+        auto raw = [&](int t) { return t < eos ? __ldg(dp + (size_t)t * p.decay_stride) : 0.f; };
+        float a0 = raw(bos + 2 * l), a1 = raw(bos + 2 * l + 1);
+        long long total = 0;  // the whole segment's log2 decay in 2^-24 units
+#pragma unroll 1
+        for (int c = 0; c < nt; ++c) {
+            const int s = c % NS, t0 = bos + c * C;
+            const float x0 = a0, x1 = a1;
+            a0 = raw(t0 + C + 2 * l);
+            a1 = raw(t0 + C + 2 * l + 1);
+            // A log2 decay as an integer and a fraction in 2^-24 units (clamped: 2^-1024 is zero for
+            // a float32).  Integer sums of both are exact.
+            auto fixed = [](float a, int& ip) {
+                constexpr float kRest = 1.9259629911267e-8f;  // log2(e) - kLog2e
+                const float x = fminf(fmaxf(a * kLog2e, -1024.f), 1024.f), fl = floorf(x);
+                const float e = fabsf(x) < 1024.f ? fmaf(a, kLog2e, -x) + a * kRest : 0.f;
+                ip = (int)fl;
+                return __float2int_rn(((x - fl) + e) * 16777216.f);
+            };
+            int i0, i1;
+            const int f0 = fixed(x0, i0), f1 = fixed(x1, i1);
+            int ii = i0 + i1, ff = f0 + f1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int yi = __shfl_up_sync(0xffffffffu, ii, m), yf = __shfl_up_sync(0xffffffffu, ff, m);
+                if (l >= m) { ii += yi; ff += yf; }
+            }
+            int I[2] = {ii - i1, ii}, F[2] = {ff - f1, ff};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // the fraction into [0, 1)
+                I[e] += F[e] >> 24;
+                F[e] &= 0xFFFFFF;
+            }
+            const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
+            const int Ih = __shfl_sync(0xffffffffu, I[1], 15), Fh = __shfl_sync(0xffffffffu, F[1], 15);
+            const float poison = __any_sync(0xffffffffu, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 0.f;  // a NaN decay
+            total += ((long long)Il << 24) + Fl;
+            auto pow2i = [](int n) { return __int_as_float(min(max(n + 127, 0), 255) << 23); };
+            // 2^(n + f / 2^24), |f| < 2^24: the power of the nearest integer times the power series
+            // of the rest (|z| <= ln(2) / 2: the first left out term is below 2^-26)
+            auto pow2 = [&](int n, int f) {
+                const int r = (f + (1 << 23)) >> 24;
+                const float z = (float)(f - (r << 24)) * (0.69314718f / 16777216.f);
+                float y = fmaf(1.f / 5040.f, z, 1.f / 720.f);
+                y = fmaf(y, z, 1.f / 120.f);
+                y = fmaf(y, z, 1.f / 24.f);
+                y = fmaf(y, z, 1.f / 6.f);
+                y = fmaf(y, z, 0.5f);
+                y = fmaf(y, z, 1.f);
+                return fmaf(y, z, 1.f) * pow2i(n + r);
+            };
+            auto fast2 = [&](int n, int f) { return ex2_fast((float)f * (1.f / 16777216.f)) * pow2i(n); };
+            // the slot's last readers are done: chunk c - NS is loaded (and its FULL phase complete),
+            // so the products of c - 2 NS are done, which the output warps of c - NG preceded
+            if (c >= NS && !sy.warp_wait(B_FULL + s, ((c / NS) - 1) & 1)) break;
+            const uint32_t gt = gates(c);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * l + e;
+                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + poison);
+                sts(gt + GT_ROW + 4 * i, kScale * fast2(I[e], F[e]) + poison);
+                sts(gt + GT_KEY + 4 * i, pow2(Il - I[e], Fl - F[e]) + poison);
+                if (l < 16) sts(gt + GT_HALF + 4 * i, fast2(Ih - I[e], Fh - F[e]) + poison);
+            }
+            if (l == 0) sts(gt + GT_LAST, pow2(Il, Fl) + poison);
+            __syncwarp();
+            if (l == 0) mbar_arrive(sy.bar(B_FULL + s));
+            if (kStates && c == nt - 1 && l == 0 && vb == 0) {
+                const long long t = max(total, -(300ll << 24));
+                p.wdec[(size_t)slot * p.H + h] = pow2((int)(t >> 24), (int)(t & 0xFFFFFF)) + poison;
+            }
+        }
+    } else if (w == 3) {
+        // ------------------------------------------------ loads, the state's products
+        constexpr uint32_t id_s = idesc_bf16(128, KD, 1, 1);
+        auto load = [&](int c) {
+            if (elect()) {
+                const uint32_t st = sb + (c % NS) * L::STAGE, full = sy.bar(B_FULL + c % NS);
+                const int t0 = bos + c * C;
+                mbar_arrive_expect_tx(full, (kStates ? L::QB : 2 * L::QB) + L::VBYTES);
+#pragma unroll
+                for (int x = 0; x < KD / 64; ++x) {
+                    if constexpr (!kStates) tma_load_3d(st + x * 8192, &tm_q, 64 * x, hq, t0, full);
+                    tma_load_3d(st + L::QB + x * 8192, &tm_k, 64 * x, hq, t0, full);
+                }
+#pragma unroll
+                for (int x = 0; x < VB / 64; ++x) tma_load_3d(st + 2 * L::QB + x * 8192, &tm_v, vc0 + 64 * x, h, t0, full);
+            }
+            __syncwarp();
+        };
+        int loaded = 0;
+        for (; loaded < min(nt, NS); ++loaded) load(loaded);
+#pragma unroll 1
+        for (int c = 0; c < nt; ++c) {
+            const int s = c % NS;
+            const uint32_t k = lo_mn(sb + s * L::STAGE + L::QB), v = lo_mn(sb + s * L::STAGE + 2 * L::QB);
+            if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
+            if (!sy.warp_wait(B_SBF, c & 1) || !sy.warp_wait(B_KD + (c & 1), (c >> 1) & 1)) break;
+            tc_fence_after();
+            if (elect()) {  // S^T += v^T kd, the three terms of kd
+#pragma unroll
+                for (int term = 0; term < 3; ++term) {
+                    const uint32_t kd = term == 0 ? k : lo_mn(sb + (term == 1 ? L::KM : L::KL));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_bf16(tmem + TM_S, desc(v + kk * 128), desc(kd + kk * 128), id_s, 1);
+                }
+                umma_commit(sy.bar(B_STATE));
+                if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
+            }
+            __syncwarp();
+            // the stage of the chunk before this one is free by now
+            if (c > 0 && loaded < nt) {
+                if (!sy.warp_wait(B_FREE + (c - 1) % NS, ((c - 1) / NS) & 1)) break;
+                load(loaded++);
+            }
+        }
+        if (__any_sync(0xffffffffu, sy.aborted())) {  // leave no copy and no MMA in flight behind
+            if (elect()) {
+                umma_commit(sy.bar(B_DRAIN));
+                mbar_wait(sy.bar(B_DRAIN), 0);
+                // (a stage's last load; where its decay factors do not come any more, the second arrival is made here)
+                for (int c = max(0, loaded - NS); c < loaded; ++c)
+                    if (!mbar_wait(sy.bar(B_FULL + c % NS), (c / NS) & 1, 1u << 12)) {
+                        mbar_arrive(sy.bar(B_FULL + c % NS));
+                        mbar_wait(sy.bar(B_FULL + c % NS), (c / NS) & 1);
+                    }
+            }
+            __syncwarp();
+        }
+    } else if (w == 24) {
+        // ------------------------------------------------ the output's products
+        if constexpr (!kStates) {
+            constexpr uint32_t id_nk = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 0);
+            auto qk = [&](int c) {
+                const uint32_t a = lo_k(sb + (c % NS) * L::STAGE), b = a + (L::QB >> 4), to = tmem + TM_QK + 64 * (c & 1);
+                if (elect()) {
+#pragma unroll
+                    for (int kk = 0; kk < KD / 16; ++kk) {
+                        const uint32_t d = (kk >> 2) * 512 + (kk & 3) * 2;
+                        umma_bf16(to, desc(a + d), desc(b + d), id_nk, kk > 0);
+                    }
+                    umma_commit(sy.bar(B_QK + (c & 1)));
+                }
+                __syncwarp();
+            };
+            bool ok = true;
+            if (nt > 0) {
+                ok = sy.warp_wait(B_FULL, 0);
+                tc_fence_after();
+                if (ok) qk(0);
+            }
+#pragma unroll 1
+            for (int c = 0; c < nt && ok; ++c) {
+                const int s = c % NS, b = c & 1;
+                const uint32_t q = lo_k(sb + s * L::STAGE), v = lo_mn(sb + s * L::STAGE + 2 * L::QB), pb = lo_k(sb + L::P + b * (C * C * 2));
+                // the next chunk's scores as soon as it is loaded, else behind this chunk's products;
+                // the last chunk's P and keys, which waited for this buffer's last scores, are done
+                const bool more = c + 1 < nt;
+                bool next = !more;
+                if (c >= 1 && !sy.warp_wait(B_KD + (b ^ 1), ((c - 1) >> 1) & 1)) break;
+                if (more && __all_sync(0xffffffffu, sy.ready(B_FULL + (c + 1) % NS, ((c + 1) / NS) & 1))) {
+                    tc_fence_after();
+                    qk(c + 1);
+                    next = true;
+                }
+                if (!sy.warp_wait(B_SBF, c & 1)) break;
+                if (c >= 2 && !sy.warp_wait(B_OFREE + b, ((c - 2) >> 1) & 1)) break;
+                tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int kk = 0; kk < KD / 16; ++kk)
+                        umma_bf16_ta(tmem + TM_O1 + 64 * b, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_nk, kk > 0);
+                    umma_commit(sy.bar(B_INTER));
+                }
+                __syncwarp();
+                if (!sy.warp_wait(B_P + b, (c >> 1) & 1)) break;
+                // v's rows behind the sequence are cleared with the last chunk's keys
+                if (!more && !sy.warp_wait(B_KD + b, (c >> 1) & 1)) break;
+                // (O2 has one buffer)
+                if (c >= 1 && !sy.warp_wait(B_OFREE + (b ^ 1), ((c - 1) >> 1) & 1)) break;
+                tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_bf16(tmem + TM_O2, desc(v + kk * 128), desc(pb + kk * 2), id_o2, kk > 0);
+                    umma_commit(sy.bar(B_O + b));
+                    if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
+                }
+                __syncwarp();
+                if (!next) {
+                    if (!sy.warp_wait(B_FULL + (c + 1) % NS, ((c + 1) / NS) & 1)) break;
+                    tc_fence_after();
+                    qk(c + 1);
+                }
+            }
+            if (__any_sync(0xffffffffu, sy.aborted())) {
+                if (elect()) {
+                    umma_commit(sy.bar(B_DRAIN2));
+                    mbar_wait(sy.bar(B_DRAIN2), 0);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (w < 12) {
+        // ------------------------------------------------ state: S^T in TMEM, lane = value channel
+        const int vl = 32 * (w & 3) + l;
+        const uint32_t lane = (uint32_t)(32 * (w & 3)) << 16;
+        const int c0 = w < 8 ? 0 : KD / 2, c1 = c0 + KD / 2;  // this warp's key channels
+        const bool mine = vl < VB && vc0 + vl < p.V;
+        const size_t st = ((size_t)n * p.H + h) * (size_t)p.K * p.V + vc0 + vl;
+        const size_t sg = ((size_t)slot * p.H + h) * (size_t)p.K * p.V + vc0 + vl;
+        // a cut sequence's segments take their incoming states from the scan
+        const float* src = kStates ? nullptr : first && last ? (p.h0 ? p.h0 + st : nullptr) : p.ws + sg;
+        float* dst = kStates ? p.ws + sg : (last && p.hT) ? p.hT + st : nullptr;
+        if (nt == 0) {  // an empty sequence passes its state through
+            if (dst && mine)
+                for (int j = c0; j < c1; ++j) dst[(size_t)j * p.V] = src ? src[(size_t)j * p.V] : 0.f;
+        } else {
+#pragma unroll 1
+            for (int x = c0; x < c1; x += 16) {
+                uint32_t r[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) r[j] = (src && mine) ? __float_as_uint(src[(size_t)(x + j) * p.V]) : 0u;
+                __syncwarp();
+                tmem_st16(tmem + TM_S + lane + x, r);
+            }
+            tmem_wait_st();
+        }
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < nt; ++c) {
+            if (!(ok = sy.warp_wait(B_FULL + c % NS, (c / NS) & 1))) break;
+            const float gl = lds(gates(c) + GT_LAST);
+            if (c > 0) {
+                if (!(ok = sy.warp_wait(B_STATE, (c - 1) & 1))) break;
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int x = c0; x < c1; x += 32) {
+                float v[32];
+                ld32(tmem + TM_S + lane + x, v);
+                if (!kStates && c > 0 && x == c0 && !(ok = sy.warp_wait(B_INTER, (c - 1) & 1))) break;
+                tmem_wait_ld();
+                uint32_t r[16];
+                if constexpr (!kStates) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                    tmem_st16(tmem + TM_SB + lane + x / 2, r);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 u = mul2(make_float2(v[16 * y + j], v[16 * y + j + 1]), make_float2(gl, gl));
+                        r[j] = __float_as_uint(u.x);
+                        r[j + 1] = __float_as_uint(u.y);
+                    }
+                    tmem_st16(tmem + TM_S + lane + x + 16 * y, r);
+                }
+            }
+            if (!ok) break;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (l == 0) mbar_arrive(sy.bar(B_SBF));
+        }
+        if (nt > 0 && ok) ok = sy.warp_wait(B_STATE, (nt - 1) & 1);
+        if (!kStates && nt > 0 && ok) ok = sy.warp_wait(B_INTER, (nt - 1) & 1);
+        if (nt > 0 && ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = c0; x < c1; x += 32) {
+                float v[32];
+                ld32(tmem + TM_S + lane + x, v);
+                tmem_wait_ld();
+                if (dst && mine) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) dst[(size_t)(x + j) * p.V] = v[j];
+                }
+                __syncwarp();
+            }
+        }
+    } else if (w < 16) {
+        // ------------------------------------------------ output rows
+        if constexpr (!kStates) {
+            const int vl = 32 * (w & 3) + l;
+            const uint32_t lane = (uint32_t)(32 * (w & 3)) << 16;
+            constexpr bool kStaged = sizeof(OT) == 2;
+            // a bf16 row segment would be written 64 bytes a warp and token: it goes through shared
+            // memory (the TMA layout) and leaves as one tile, or row by row at a sequence's end
+            const bool mine = vl < VB;
+#pragma unroll 1
+            for (int c = 0; c < nt; ++c) {
+                const int b = c & 1, t0 = bos + c * C, len = min(C, eos - t0);
+                if (kStaged && c > 0) {
+                    if (tid == 384) bulk_wait_read();
+                    bar_sync(1, 128);  // (all four warps have copied their rows of the last chunk, too)
+                }
+                const bool ok = sy.warp_wait(B_O + b, (c >> 1) & 1);
+                tc_fence_after();
+                const uint32_t gt = gates(c) + GT_ROW;
+                OT* dst = (OT*)p.o + ((size_t)t0 * p.H + h) * p.V + vc0;
+                const size_t step = (size_t)p.H * p.V;
+                auto taken = [&] {  // both buffers have been read
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (l == 0) mbar_arrive(sy.bar(B_OFREE + b));
+                };
+                if (!ok) {
+                    if (!kStaged) break;
+                } else if constexpr (kStaged) {
+                    // pieces of 16 channels x 32 tokens: fragments of 8 x 8, stored transposed
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t at = tmem + lane + ((uint32_t)(16 * (x >> 1)) << 16) + 32 * (x & 1);
+                        float o1[16], o2[16];
+                        ld16x32(at + TM_O1 + 64 * b, o1);
+                        ld16x32(at + TM_O2, o2);
+                        if (x < 3) tmem_wait_ld();
+                        else taken();
+                        const int ch = 4 * (w & 3) + 2 * (x >> 1) + ((l >> 3) & 1);  // the 16-byte piece of this lane's address
+                        const uint32_t base = sb + L::O + (ch >> 3) * 8192u;
+#pragma unroll
+                        for (int g = 0; g < 4; g += 2) {
+                            uint32_t r[4];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float2 f = lds2(gt + 4 * (32 * (x & 1) + 8 * (g + e) + 2 * (l & 3)));
+                                const float *a1 = o1 + 4 * (g + e), *a2 = o2 + 4 * (g + e);
+                                const float2 y0 = fma2(f, make_float2(a1[0], a1[1]), make_float2(a2[0], a2[1]));
+                                const float2 y1 = fma2(f, make_float2(a1[2], a1[3]), make_float2(a2[2], a2[3]));
+                                r[2 * e] = pack_bf16(y0.x, y0.y);
+                                r[2 * e + 1] = pack_bf16(y1.x, y1.y);
+                            }
+                            if (32 * (w & 3) < VB)
+                                stmatrix4_t(base + sw128(32 * (x & 1) + 8 * (g + (l >> 4)) + (l & 7), ch & 7), r);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        float o1[16], o2[16];
+                        tmem_ld16(tmem + TM_O1 + 64 * b + lane + 16 * x, o1);
+                        tmem_ld16(tmem + TM_O2 + lane + 16 * x, o2);
+                        if (x < 3) tmem_wait_ld();
+                        else taken();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float r = fmaf(lds(gt + 4 * (16 * x + j)), o1[j], o2[j]);
+                            if (mine && 16 * x + j < len) dst[(16 * x + j) * step + vl] = to_out<OT>(r);
+                        }
+                    }
+                }
+                if constexpr (kStaged) {
+                    fence_proxy_async_smem();
+                    bar_sync(1, 128);
+                    if (sy.aborted()) {
+                        // (as the other warps: each chunk has the same barriers)
+                    } else if (len == C) {
+                        if (tid == 384) {
+#pragma unroll
+                            for (int x = 0; x < VB / 64; ++x) tma_store_3d(&tm_o, sb + L::O + x * 8192, vc0 + 64 * x, h, t0);
+                            bulk_commit();
+                        }
+                    } else {
+                        for (int x = tid - 384; x < len * (VB / 8); x += 128) {
+                            const int row = x / (VB / 8), ch = x % (VB / 8);
+                            uint32_t v[4];
+                            ld_s128(sb + L::O + (ch >> 3) * 8192u + sw128(row, ch & 7), v);
+                            *reinterpret_cast<uint4*>(dst + row * step + 8 * ch) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                }
+            }
+            if (kStaged && tid == 384) bulk_wait();
+        }
+    } else if (w < 24) {
+        // ------------------------------------------------ scaled keys, three bf16 terms
+        // The first term replaces k (once the scores have read it); the lower two share buffers with
+        // the last chunk's, so they wait for its state product, with the remainders in registers.
+        const int kt = tid - 512;
+        constexpr int NP = C * (KD / 8) / 256;  // 16-byte pieces of a thread; eight lanes cover a row of a 64-channel half
+        auto where = [&](int y) {
+            const int x = kt + 256 * y;
+            return (x >> 9) * 8192u + sw128((x >> 3) & 63, x & 7);
+        };
+#pragma unroll 1
+        for (int c = 0; c < nt; ++c) {
+            const int s = c % NS, len = min(C, eos - (bos + c * C));
+            const uint32_t kb = sb + s * L::STAGE + L::QB, vt = kb + L::QB, gt = gates(c) + GT_KEY;
+            if (!sy.warp_wait(B_FULL + s, (c / NS) & 1)) break;
+            if (!kStates && !sy.warp_wait(B_QK + (c & 1), (c >> 1) & 1)) break;
+            float2 rest[NP][4];
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                const int row = ((kt + 256 * y) >> 3) & 63;
+                uint32_t kw[4], hi[4];
+                ld_s128(kb + where(y), kw);
+                const float f = lds(gt + 4 * row);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (row >= len) kw[e] = 0;
+                    rest[y][e] = mul2(make_float2(bf_lo(kw[e]), bf_hi(kw[e])), make_float2(f, f));
+                    hi[e] = cut(rest[y][e]);
+                }
+                st_s128(kb + where(y), hi[0], hi[1], hi[2], hi[3]);
+            }
+            if (len < C)  // rows behind the sequence: another one's, or anything
+                for (int x = kt; x < C * (VB / 8); x += 256) {
+                    const int row = (x >> 3) & 63, half = x >> 9, piece = x & 7;
+                    if (row >= len) st_s128(vt + half * 8192u + sw128(row, piece), 0, 0, 0, 0);
+                }
+            if (c > 0 && !sy.warp_wait(B_STATE, (c - 1) & 1)) break;
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                uint32_t mid[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mid[e] = cut(rest[y][e]);
+                    lo[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
+                }
+                st_s128(sb + L::KM + where(y), mid[0], mid[1], mid[2], mid[3]);
+                st_s128(sb + L::KL + where(y), lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (l == 0) mbar_arrive(sy.bar(B_KD + (c & 1)));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (w == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TM_COLS);
+    }
+}
+
+// The segments' states in order: each segment's addition becomes its incoming state.
+__global__ void __launch_bounds__(256) decay_scan_kernel(const float* __restrict__ h0, float* ws, const float* __restrict__ wdec,
+                                                         ChunkMap cm, int H, int KV) {
+    const int n = blockIdx.z, h = blockIdx.y, e = 4 * (blockIdx.x * 256 + threadIdx.x);
+    if (e >= KV) return;
+    int bos, eos;
+    if (cm.cu) { bos = __ldg(cm.cu + n); eos = __ldg(cm.cu + n + 1); }
+    else       { bos = n * cm.T; eos = bos + cm.T; }
+    const int ns = (eos - bos + cm.C - 1) / cm.C;
+    if (ns < 2) return;
+    const int s0 = cm.first_slot(n, bos);
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h0) S = *reinterpret_cast<const float4*>(h0 + ((size_t)n * H + h) * KV + e);
+    // the first segment's too: the last one may write its final state over h0
+    float4* from = reinterpret_cast<float4*>(ws + ((size_t)s0 * H + h) * KV + e);
+    float4 add = *from;
+    *from = S;
+    for (int s = 0; s + 1 < ns; ++s) {
+        const float d = __ldg(wdec + (size_t)(s0 + s) * H + h);
+        float* next = ws + ((size_t)(s0 + s + 1) * H + h) * KV + e;
+        float4 add2 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s + 2 < ns) add2 = *reinterpret_cast<const float4*>(next);
+        S.x = fmaf(d, S.x, add.x);
+        S.y = fmaf(d, S.y, add.y);
+        S.z = fmaf(d, S.z, add.z);
+        S.w = fmaf(d, S.w, add.w);
+        *reinterpret_cast<float4*>(next) = S;
+        add = add2;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* ptr = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// [tokens, H, D] bf16, box of 64 channels x 1 head x 64 tokens, 128-byte swizzle
+bool make_map(CUtensorMap* m, const void* base, long tokens, int H, int D) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+    const cuuint32_t box[3] = {64, 1, 64}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens of a segment (0: whole sequences).  One CTA per SM runs a unit (a sequence's head and
+// value block) in order, so few units leave SMs idle: the time axis is then cut into segments whose
+// added states come from a first pass over k and v (half of the call's bytes once more) and a scan.
+// That pays when whole sequences fill less than half of the SMs, and segments stay at least four
+// chunks long (a segment costs its state twice through memory, one chunk's worth of bytes).
+int plan_segment(int B, int T, int H, int vblocks, int N, bool packed) {
+    const int sms = planned_sm_count();
+    const long units = (long)N * H * vblocks;
+    if (sms <= 0 || units == 0 || 2 * units > sms) return 0;
+    const long tokens = packed ? T : (long)N * T;
+    long per = (tokens * H * vblocks + sms - 1) / sms;  // tokens of a unit for one CTA per SM
+    per = (per + C - 1) / C * C;
+    if (!packed) {  // whole segments per sequence, evenly
+        const long ns = sms / units;
+        per = ((T + ns - 1) / ns + C - 1) / C * C;
+    }
+    if (per < 4 * C) per = 4 * C;
+    return 2 * per > T ? 0 : (int)per;
+}
+
+struct Plan {
+    int seg, slots;
+    size_t states, bytes;
+};
+Plan plan(int B, int T, int H, int K, int V, int N, bool packed) {
+    Plan pl{0, N, 0, 0};
+    const int vblocks = V > 128 ? 2 : 1;
+    pl.seg = plan_segment(B, T, H, vblocks, N, packed);
+    if (pl.seg == 0) return pl;
+    pl.slots = packed ? T / pl.seg + N + 1 : N * ((T + pl.seg - 1) / pl.seg);
+    pl.states = (size_t)pl.slots * H * K * V * sizeof(float);
+    pl.bytes = pl.states + ((size_t)pl.slots * H * sizeof(float) + 255) / 256 * 256;
+    return pl;
+}
+
+template <int KD, int VB, typename OT>
+cudaError_t run(const DecayArgs& a) {
+    using L = Layout<KD, VB>;
+    CUtensorMap mq, mk, mv, mo;  // (mo is a stand-in for a float32 o, which leaves by plain stores)
+    const long tokens = (long)a.B * a.T;
+    if (tokens == 0) {  // nothing to load; the maps are never used
+        if (!a.hT) return cudaSuccess;
+    }
+    const void* some = a.hT;
+    if (!make_map(&mq, tokens ? a.q : some, tokens ? tokens : 1, a.Hk, KD) ||
+        !make_map(&mk, tokens ? a.k : some, tokens ? tokens : 1, a.Hk, KD) ||
+        !make_map(&mv, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V) ||
+        !make_map(&mo, tokens && !a.o_f32 ? a.o : tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
+        return cudaErrorInvalidValue;
+    const Plan pl = plan(a.B, a.T, a.H, a.K, a.V, a.N, a.cu != nullptr);
+    Params p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, pl.seg,
+             (float*)a.ws, (float*)((char*)a.ws + pl.states), a.status, hook_stall_chunk()};
+    const dim3 grid(a.H, (a.V + VB - 1) / VB, pl.slots);
+    cudaError_t e;
+    if (pl.seg) {
+        auto states = decay_chunk_kernel<KD, VB, __nv_bfloat16, true>;
+        e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+        if (e != cudaSuccess) return e;
+        states<<<grid, NTHR, L::BYTES, a.stream>>>(mq, mk, mv, mo, p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int KV = a.K * a.V;
+        decay_scan_kernel<<<dim3((KV / 4 + 255) / 256, a.H, a.N), 256, 0, a.stream>>>(
+            a.h0, p.ws, p.wdec, ChunkMap{a.cu, a.N, a.T, pl.seg}, a.H, KV);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    auto kern = decay_chunk_kernel<KD, VB, OT, false>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, NTHR, L::BYTES, a.stream>>>(mq, mk, mv, mo, p);
+    return cudaGetLastError();
+}
+
+template <typename OT>
+cudaError_t run_dims(const DecayArgs& a) {
+    if (a.K == 64) return a.V == 64 ? run<64, 64, OT>(a) : run<64, 128, OT>(a);
+    return a.V == 64 ? run<128, 64, OT>(a) : run<128, 128, OT>(a);
+}
+
+}  // namespace decay
+
+bool decay_tensor_dims(bool bf16, int K, int V) {
+    return bf16 && (K == 64 || K == 128) && (V == 64 || V == 128 || V == 256);
+}
+
+size_t decay_tensor_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed) {
+    return decay::plan(B, T, H, K, V, N, packed).bytes;
+}
+
+cudaError_t launch_decay_tensor(const DecayArgs& a) {
+    return a.o_f32 ? decay::run_dims<float>(a) : decay::run_dims<__nv_bfloat16>(a);
+}
+
+cudaError_t read_decay_timeouts(unsigned* count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, decay::g_decay_timeouts, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(decay::g_decay_timeouts, &zero, sizeof(unsigned));
+    }
+    return e;
+}
+
+}  // namespace kda
