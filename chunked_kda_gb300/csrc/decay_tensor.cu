@@ -8,7 +8,11 @@
 //   S      <- 2^G_l S + sum_j (2^(G_l - G_j) k_j) v_j^T                         (FP32)
 // as four products, value channels (M = 128) on TMEM lanes:
 //   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += v^T kd.
-// q, k and v enter the products as they are; O1's row factor 2^G_i and s are applied to the FP32
+// The stored state is S 2^-E.  Where the decay is slow, E' = E + G_l and the keys carry 2^(G_l - G_j - E')
+// = 2^-(E + G_j): nothing has to be multiplied between two chunks' state products, and S is rounded once
+// less.  Before |E| passes 32 the stored state is scaled (factor 2^(E + G_l)) and E starts again at 0.
+//
+// q, k and v enter the products as they are; O1's row factor s 2^(E + G_i) is applied to the FP32
 // results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
 // difference of an integer and of a fraction part (64-bit fixed-point sums), exact whatever the sums.
 //
@@ -36,16 +40,17 @@ __device__ unsigned int g_decay_timeouts = 0;
 constexpr int C = 64, NTHR = 800, NS = 3, NG = 8;
 
 // barriers
-enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P = B_QK + 2, B_SBF = B_P + 2, B_KD, B_STATE = B_KD + 2, B_INTER, B_O,
+enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P = B_QK + 2, B_S = B_P + 2, B_SBF, B_KD, B_STATE = B_KD + 2, B_INTER, B_O,
        B_OFREE = B_O + 2, B_DRAIN = B_OFREE + 2, B_DRAIN2, B_NEVER, NBAR };
 
 // The decay factors of a chunk, one slot of a ring of NG (written when the chunk is loaded, read
 // last by its output warps, at most NS + 3 chunks later): byte offsets of its float arrays.
 constexpr uint32_t GT_G = 0;       // [64][2] G_i as integer and fraction
-constexpr uint32_t GT_ROW = 512;   // [64] s 2^G_i
-constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j)
+constexpr uint32_t GT_ROW = 512;   // [64] s 2^(E + G_i)
+constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j - E')
 constexpr uint32_t GT_HALF = 1024; // [32] 2^(G_31 - G_j)
-constexpr uint32_t GT_LAST = 1152; // 2^G_l
+constexpr uint32_t GT_LAST = 1152; // the stored state's factor before this chunk's keys, 1: none
+constexpr uint32_t GT_OUT = 1156;  // 2^E'
 constexpr uint32_t GT_BYTES = 1168;
 
 template <int KD, int VB>
@@ -237,7 +242,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (i >= B_FREE && i < B_FREE + NS) count = kStates ? 1 : 2;   // the products of both issuing warps
             if (i == B_P || i == B_P + 1) count = 2;                       // two P warps
             if (i == B_OFREE || i == B_OFREE + 1) count = 4;               // four output warps
-            if (i >= B_SBF && i < B_KD + 2) count = 8;                     // eight warps
+            if (i >= B_S && i < B_KD + 2) count = 8;                       // eight warps
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
@@ -320,6 +325,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const float* dp = p.decay + h;
         auto raw = [&](int t) { return t < eos ? __ldg(dp + (size_t)t * p.decay_stride) : 0.f; };
         float a0 = raw(bos + 2 * l), a1 = raw(bos + 2 * l + 1);
+        int Ei = 0, Ef = 0;   // the stored state's exponent: integer, and fraction in 2^-24 units
         long long total = 0;  // the whole segment's log2 decay in 2^-24 units
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
@@ -368,6 +374,11 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 y = fmaf(y, z, 1.f);
                 return fmaf(y, z, 1.f) * pow2i(n + r);
             };
+            // this chunk's keys and row factors, and the exponent behind it
+            int ni = Ei + Il, nf = Ef + Fl;
+            ni += nf >> 24;
+            nf &= 0xFFFFFF;
+            const bool renew = ni < -32 || ni >= 32;
             auto fast2 = [&](int n, int f) { return ex2_fast((float)f * (1.f / 16777216.f)) * pow2i(n); };
             // the slot's last readers are done: chunk c - NS is loaded (and its FULL phase complete),
             // so the products of c - 2 NS are done, which the output warps of c - NG preceded
@@ -377,11 +388,17 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * l + e;
                 sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + poison);
-                sts(gt + GT_ROW + 4 * i, kScale * fast2(I[e], F[e]) + poison);
-                sts(gt + GT_KEY + 4 * i, pow2(Il - I[e], Fl - F[e]) + poison);
+                const int rf = Ef + F[e];
+                sts(gt + GT_ROW + 4 * i, kScale * fast2(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + poison);
+                sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e], Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
                 if (l < 16) sts(gt + GT_HALF + 4 * i, fast2(Ih - I[e], Fh - F[e]) + poison);
             }
-            if (l == 0) sts(gt + GT_LAST, pow2(Il, Fl) + poison);
+            if (l == 0) {
+                sts(gt + GT_LAST, (renew ? pow2(ni, nf) : 1.f) + poison);
+                sts(gt + GT_OUT, renew ? 1.f : pow2(ni, nf));
+            }
+            Ei = renew ? 0 : ni;
+            Ef = renew ? 0 : nf;
             __syncwarp();
             if (l == 0) mbar_arrive(sy.bar(B_FULL + s));
             if (kStates && c == nt - 1 && l == 0 && vb == 0) {
@@ -414,7 +431,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int s = c % NS;
             const uint32_t k = lo_mn(sb + s * L::STAGE + L::QB), v = lo_mn(sb + s * L::STAGE + 2 * L::QB);
             if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
-            if (!sy.warp_wait(B_SBF, c & 1) || !sy.warp_wait(B_KD + (c & 1), (c >> 1) & 1)) break;
+            if (!sy.warp_wait(B_S, c & 1) || !sy.warp_wait(B_KD + (c & 1), (c >> 1) & 1)) break;
             tc_fence_after();
             if (elect()) {  // S^T += v^T kd, the three terms of kd
 #pragma unroll
@@ -553,39 +570,50 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!(ok = sy.warp_wait(B_STATE, (c - 1) & 1))) break;
                 tc_fence_after();
             }
-#pragma unroll 1
-            for (int x = c0; x < c1; x += 32) {
+            auto arrive = [&](int bar) {
+                tc_fence_before();
+                __syncwarp();
+                if (l == 0) mbar_arrive(sy.bar(bar));
+            };
+            constexpr int NC = KD / 2;  // this warp's columns
+            uint32_t r[NC / 2];         // their bf16 copy
+#pragma unroll
+            for (int x = 0; x < NC; x += 32) {
+                if (kStates && gl == 1.f) break;
                 float v[32];
-                ld32(tmem + TM_S + lane + x, v);
-                if (!kStates && c > 0 && x == c0 && !(ok = sy.warp_wait(B_INTER, (c - 1) & 1))) break;
+                ld32(tmem + TM_S + lane + c0 + x, v);
                 tmem_wait_ld();
-                uint32_t r[16];
-                if constexpr (!kStates) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                    tmem_st16(tmem + TM_SB + lane + x / 2, r);
-                }
+                for (int j = 0; j < 16; ++j) r[x / 2 + j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                if (gl != 1.f) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t u[16];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 u = mul2(make_float2(v[16 * y + j], v[16 * y + j + 1]), make_float2(gl, gl));
-                        r[j] = __float_as_uint(u.x);
-                        r[j + 1] = __float_as_uint(u.y);
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 t = mul2(make_float2(v[16 * y + j], v[16 * y + j + 1]), make_float2(gl, gl));
+                            u[j] = __float_as_uint(t.x);
+                            u[j + 1] = __float_as_uint(t.y);
+                        }
+                        tmem_st16(tmem + TM_S + lane + c0 + x + 16 * y, u);
                     }
-                    tmem_st16(tmem + TM_S + lane + x + 16 * y, r);
                 }
             }
-            if (!ok) break;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (l == 0) mbar_arrive(sy.bar(B_SBF));
+            if (gl != 1.f) tmem_wait_st();
+            arrive(B_S);
+            if constexpr (!kStates) {
+                if (c > 0 && !(ok = sy.warp_wait(B_INTER, (c - 1) & 1))) break;
+#pragma unroll
+                for (int x = 0; x < NC / 2; x += 16) tmem_st16(tmem + TM_SB + lane + c0 / 2 + x, r + x);
+                tmem_wait_st();
+                arrive(B_SBF);
+            }
         }
         if (nt > 0 && ok) ok = sy.warp_wait(B_STATE, (nt - 1) & 1);
         if (!kStates && nt > 0 && ok) ok = sy.warp_wait(B_INTER, (nt - 1) & 1);
         if (nt > 0 && ok) {
             tc_fence_after();
+            const float out = lds(gates(nt - 1) + GT_OUT);
 #pragma unroll 1
             for (int x = c0; x < c1; x += 32) {
                 float v[32];
@@ -593,7 +621,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_wait_ld();
                 if (dst && mine) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) dst[(size_t)(x + j) * p.V] = v[j];
+                    for (int j = 0; j < 32; ++j) dst[(size_t)(x + j) * p.V] = v[j] * out;
                 }
                 __syncwarp();
             }
