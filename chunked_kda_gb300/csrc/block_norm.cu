@@ -73,11 +73,58 @@ __device__ __forceinline__ void store_e(T* p, const float* r) {
 template <typename T>
 __device__ __forceinline__ float gate_value(float z, int act) {
     if (act == 0) return z;
-    const float s = 1.f / (1.f + (sizeof(T) == 2 ? __expf(-z) : expf(-z)));
+    const float s = sizeof(T) == 2 ? __fdividef(1.f, 1.f + __expf(-z)) : 1.f / (1.f + expf(-z));
     return act == 2 ? z * s : s;
 }
 
-// Gated norm: one warp per row, lanes step over the row in pieces of E elements.
+// Gated norm, rows of NV vectors: G = 32 / 2^k lanes share a row, a vector of 16 bytes each (V of at
+// most 32 vectors), so a warp holds 32 / G rows at a time, and R such groups of rows with all their
+// loads issued before the first sum.  Memory bounds it: 16384 x 64 rows of 128 bf16 (805 MB) in
+// RATE.  One row per thread group instead of R = 2 leaves too few bytes in flight.
+template <typename T, int G, int R>
+__global__ void __launch_bounds__(256) gated_norm_rows_kernel(const T* __restrict__ x, const T* __restrict__ z,
+                                                              const float* __restrict__ w, float eps, int act,
+                                                              long rows, int V, T* __restrict__ y) {
+    constexpr int E = Vec<T>::N, RW = 32 / G;
+    const int lane = threadIdx.x & 31, c = (lane % G) * E;
+    const long row0 = ((long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (RW * R) + lane / G;
+    const bool on = c < V;
+    float a[R][E], g[R][E], wv[E];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const long row = row0 + r * RW;
+        const bool in = on && row < rows;
+#pragma unroll
+        for (int i = 0; i < E; ++i) a[r][i] = 0.f;
+        if (in) {
+            Vec<T>::load(x + row * V + c, a[r]);
+            Vec<T>::load(z + row * V + c, g[r]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) wv[i] = 1.f;
+    if (w && on) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) Vec<float>::load(w + c + i, wv + i);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const long row = row0 + r * RW;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum = fmaf(a[r][i], a[r][i], sum);
+#pragma unroll
+        for (int m = G / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float rs = rsqrtf(sum / V + eps);
+        if (!on || row >= rows) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) a[r][i] = a[r][i] * rs * wv[i] * gate_value<T>(g[r][i], act);
+        Vec<T>::store(y + row * V + c, a[r]);
+    }
+}
+
+// Gated norm, any row length: one warp per row, lanes step over the row in pieces of E elements,
+// twice.
 template <typename T, int E>
 __global__ void __launch_bounds__(256) gated_norm_kernel(const T* __restrict__ x, const T* __restrict__ z,
                                                          const float* __restrict__ w, float eps, int act,
@@ -107,23 +154,107 @@ __global__ void __launch_bounds__(256) gated_norm_kernel(const T* __restrict__ x
     }
 }
 
-// sum over the block's 256 threads, the same value in all of them
+// sum over the block's threads, the same value in all of them; `red` is used once
+template <int NT>
 __device__ __forceinline__ float block_sum(float s, float* red) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    __syncthreads();  // the readers of an earlier sum are done
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    float t = 0.f;
+    if constexpr (NT > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i];
-    return t;
+        for (int i = 0; i < NT / 32; ++i) s += red[i];
+    }
+    return s;
 }
 
-// Block norm: one block per row, three passes over it.
+// E elements of h (before the residual where there is one) from x
+template <typename T, int E>
+__device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c, float rs, float* h) {
+    float t[E];
+    if (a.post_w) {
+        load_e<float, E>(a.post_w + c, t);
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[i] = h[i] * rs * t[i];
+    }
+    if (z) {
+        load_e<T, E>(z + c, t);
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[i] *= gate_value<T>(t[i], a.act);
+    }
+    if (a.channel_scale) {
+        load_e<float, E>(a.channel_scale + c, t);
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[i] *= t[i];
+    }
+}
+
+// Block norm, one block of NT threads per row, the row in registers between the two norms: P pieces
+// of 8 elements a thread.  Memory bounds it: 16384 rows of 8192 (bf16, float32 stream; 1.61 GB) in
+// RATE.  Rows of many threads keep few registers a thread, so that several rows are in flight on an
+// SM while others wait for their sums.
+template <typename T, typename R, int NT, int P>
+__global__ void __launch_bounds__(NT) block_norm_kernel(BlockNormArgs a) {
+    __shared__ float red[2][NT / 32];
+    const long row = blockIdx.x;
+    const int D = a.D;
+    const T* x = (const T*)a.x + row * D;
+    const T* z = a.gate ? (const T*)a.gate + row * D : nullptr;
+    const R* r = a.residual ? (const R*)a.residual + row * D : nullptr;
+    float h[P][8], t[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = 8 * (threadIdx.x + p * NT);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[p][i] = t[p][i] = 0.f;
+        if (c < D) {
+            load_e<T, 8>(x + c, h[p]);
+            if (r) load_e<R, 8>(r + c, t[p]);
+        }
+    }
+    float rs = 1.f;
+    if (a.post_w) {
+        float sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(h[p][i], h[p][i], sum);
+        rs = rsqrtf(block_sum<NT>(sum, red[0]) / D + a.eps);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = 8 * (threadIdx.x + p * NT);
+        if (c >= D) continue;
+        scaled<T, 8>(a, z, c, rs, h[p]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[p][i] = fmaf(a.scale, h[p][i], t[p][i]);
+            sum = fmaf(h[p][i], h[p][i], sum);
+        }
+        if (a.h) store_e<R, 8>((R*)a.h + row * D + c, h[p]);
+    }
+    if (!a.y) return;
+    const float rp = a.pre_w ? rsqrtf(block_sum<NT>(sum, red[1]) / D + a.eps) : 1.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = 8 * (threadIdx.x + p * NT);
+        if (c >= D) continue;
+        if (a.pre_w) {
+            float w[8];
+            load_e<float, 8>(a.pre_w + c, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[p][i] *= rp * w[i];
+        }
+        store_e<T, 8>((T*)a.y + row * D + c, h[p]);
+    }
+}
+
+// Rows that no block holds in registers, or of a length that is not whole vectors: three passes.
 template <typename T, typename R, int E>
-__global__ void __launch_bounds__(256) block_norm_kernel(BlockNormArgs a) {
-    __shared__ float red[8];
+__global__ void __launch_bounds__(256) block_norm_any_kernel(BlockNormArgs a) {
+    __shared__ float red[2][8];
     const long row = blockIdx.x;
     const int D = a.D;
     const T* x = (const T*)a.x + row * D;
@@ -138,71 +269,74 @@ __global__ void __launch_bounds__(256) block_norm_kernel(BlockNormArgs a) {
 #pragma unroll
             for (int i = 0; i < E; ++i) sum = fmaf(xv[i], xv[i], sum);
         }
-        rs = rsqrtf(block_sum(sum, red) / D + a.eps);
+        rs = rsqrtf(block_sum<256>(sum, red[0]) / D + a.eps);
     }
     auto hidden = [&](int c, float* h) {
-        float t[E];
         load_e<T, E>(x + c, h);
-        if (a.post_w) {
-            load_e<float, E>(a.post_w + c, t);
+        scaled<T, E>(a, z, c, rs, h);
+        float t[E];
+        if (r) load_e<R, E>(r + c, t);
 #pragma unroll
-            for (int i = 0; i < E; ++i) h[i] = h[i] * rs * t[i];
-        }
-        if (z) {
-            load_e<T, E>(z + c, t);
-#pragma unroll
-            for (int i = 0; i < E; ++i) h[i] *= gate_value<T>(t[i], a.act);
-        }
-        if (a.channel_scale) {
-            load_e<float, E>(a.channel_scale + c, t);
-#pragma unroll
-            for (int i = 0; i < E; ++i) h[i] *= t[i];
-        }
-        if (r) {
-            load_e<R, E>(r + c, t);
-#pragma unroll
-            for (int i = 0; i < E; ++i) h[i] = fmaf(a.scale, h[i], t[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) h[i] *= a.scale;
-        }
+        for (int i = 0; i < E; ++i) h[i] = fmaf(a.scale, h[i], r ? t[i] : 0.f);
     };
     float sum = 0.f;
-    for (int c = threadIdx.x * E; c < D; c += 256 * E) {
-        float h[E];
-        hidden(c, h);
+    if (a.pre_w)
+        for (int c = threadIdx.x * E; c < D; c += 256 * E) {
+            float h[E];
+            hidden(c, h);
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum = fmaf(h[i], h[i], sum);
-    }
-    const float rp = a.pre_w ? rsqrtf(block_sum(sum, red) / D + a.eps) : 1.f;
+            for (int i = 0; i < E; ++i) sum = fmaf(h[i], h[i], sum);
+        }
+    const float rp = a.pre_w ? rsqrtf(block_sum<256>(sum, red[1]) / D + a.eps) : 1.f;
     for (int c = threadIdx.x * E; c < D; c += 256 * E) {
         float h[E], t[E];
         hidden(c, h);
-        if (a.pre_w) load_e<float, E>(a.pre_w + c, t);
-        float yv[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) yv[i] = a.pre_w ? h[i] * rp * t[i] : h[i];
         if (a.h) store_e<R, E>((R*)a.h + row * D + c, h);
-        if (a.y) store_e<T, E>((T*)a.y + row * D + c, yv);
+        if (a.pre_w) {
+            load_e<float, E>(a.pre_w + c, t);
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] *= rp * t[i];
+        }
+        if (a.y) store_e<T, E>((T*)a.y + row * D + c, h);
     }
 }
 
 template <typename T, typename R>
 cudaError_t launch_block(const BlockNormArgs& a) {
-    if (a.D % 8 == 0) block_norm_kernel<T, R, 8><<<(unsigned)a.rows, 256, 0, a.stream>>>(a);
-    else block_norm_kernel<T, R, 1><<<(unsigned)a.rows, 256, 0, a.stream>>>(a);
+    const unsigned g = (unsigned)a.rows;
+    // threads for a row: one piece of 8 elements each up to 4096 elements, two up to 16384
+    if (a.D % 8 != 0) block_norm_any_kernel<T, R, 1><<<g, 256, 0, a.stream>>>(a);
+    else if (a.D <= 256) block_norm_kernel<T, R, 32, 1><<<g, 32, 0, a.stream>>>(a);
+    else if (a.D <= 1024) block_norm_kernel<T, R, 128, 1><<<g, 128, 0, a.stream>>>(a);
+    else if (a.D <= 2048) block_norm_kernel<T, R, 256, 1><<<g, 256, 0, a.stream>>>(a);
+    else if (a.D <= 4096) block_norm_kernel<T, R, 512, 1><<<g, 512, 0, a.stream>>>(a);
+    else if (a.D <= 8192) block_norm_kernel<T, R, 512, 2><<<g, 512, 0, a.stream>>>(a);
+    else if (a.D <= 16384) block_norm_kernel<T, R, 1024, 2><<<g, 1024, 0, a.stream>>>(a);
+    else block_norm_any_kernel<T, R, 8><<<g, 256, 0, a.stream>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, int G>
+void gated_rows(const GatedNormArgs& a) {
+    constexpr int R = 2, rows = 8 * (32 / G) * R;
+    gated_norm_rows_kernel<T, G, R><<<(unsigned)((a.rows + rows - 1) / rows), 256, 0, a.stream>>>(
+        (const T*)a.x, (const T*)a.gate, a.weight, a.eps, a.act, a.rows, a.V, (T*)a.y);
 }
 
 template <typename T>
 cudaError_t launch_gated(const GatedNormArgs& a) {
+    constexpr int E = Vec<T>::N;
     const unsigned grid = (unsigned)((a.rows + 7) / 8);
-    if (a.V % 8 == 0)
-        gated_norm_kernel<T, 8><<<grid, 256, 0, a.stream>>>((const T*)a.x, (const T*)a.gate, a.weight, a.eps,
-                                                            a.act, a.rows, a.V, (T*)a.y);
+    if (a.V % E != 0)
+        gated_norm_kernel<T, 1><<<grid, 256, 0, a.stream>>>((const T*)a.x, (const T*)a.gate, a.weight, a.eps, a.act,
+                                                            a.rows, a.V, (T*)a.y);
+    else if (a.V <= 4 * E) gated_rows<T, 4>(a);
+    else if (a.V <= 8 * E) gated_rows<T, 8>(a);
+    else if (a.V <= 16 * E) gated_rows<T, 16>(a);
+    else if (a.V <= 32 * E) gated_rows<T, 32>(a);
     else
-        gated_norm_kernel<T, 1><<<grid, 256, 0, a.stream>>>((const T*)a.x, (const T*)a.gate, a.weight, a.eps,
-                                                            a.act, a.rows, a.V, (T*)a.y);
+        gated_norm_kernel<T, E><<<grid, 256, 0, a.stream>>>((const T*)a.x, (const T*)a.gate, a.weight, a.eps, a.act,
+                                                            a.rows, a.V, (T*)a.y);
     return cudaGetLastError();
 }
 
