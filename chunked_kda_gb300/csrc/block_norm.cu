@@ -25,7 +25,7 @@ struct Vec<float> {
         r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
     }
     static __device__ __forceinline__ void store(float* p, const float* r) {
-        *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
+        __stcs(reinterpret_cast<float4*>(p), make_float4(r[0], r[1], r[2], r[3]));
     }
 };
 template <>
@@ -47,7 +47,7 @@ struct Vec<__nv_bfloat16> {
             const __nv_bfloat162 b = __floats2bfloat162_rn(r[2 * e], r[2 * e + 1]);
             w[e] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
     }
 };
 // 8 consecutive elements, or one
@@ -77,50 +77,43 @@ __device__ __forceinline__ float gate_value(float z, int act) {
     return act == 2 ? z * s : s;
 }
 
-// Gated norm, rows of NV vectors: G = 32 / 2^k lanes share a row, a vector of 16 bytes each (V of at
-// most 32 vectors), so a warp holds 32 / G rows at a time, and R such groups of rows with all their
-// loads issued before the first sum.  Memory bounds it: 16384 x 64 rows of 128 bf16 (805 MB) in
-// RATE.  One row per thread group instead of R = 2 leaves too few bytes in flight.
-template <typename T, int G, int R>
-__global__ void __launch_bounds__(256) gated_norm_rows_kernel(const T* __restrict__ x, const T* __restrict__ z,
-                                                              const float* __restrict__ w, float eps, int act,
-                                                              long rows, int V, T* __restrict__ y) {
-    constexpr int E = Vec<T>::N, RW = 32 / G;
-    const int lane = threadIdx.x & 31, c = (lane % G) * E;
-    const long row0 = ((long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (RW * R) + lane / G;
-    const bool on = c < V;
-    float a[R][E], g[R][E], wv[E];
+// Gated norm of short rows: G lanes share a row, a vector of 16 bytes each (V of at most 32 vectors),
+// so a warp holds 32 / G rows.  Memory bounds it: 16384 x 64 rows of 128 bf16 (805 MB) in 133 us,
+// 6.0 TB/s.  Small blocks with few registers keep the most bytes in flight: blocks of 256 threads
+// measured 138 us, and two or four rows a lane group, their loads issued together, 158 and 241 us.
+constexpr int kRowThreads = 128;
+template <typename T, int G>
+__global__ void __launch_bounds__(kRowThreads) gated_norm_rows_kernel(const T* __restrict__ x, const T* __restrict__ z,
+                                                                      const float* __restrict__ w, float eps, int act,
+                                                                      long rows, int V, T* __restrict__ y) {
+    constexpr int E = Vec<T>::N;
+    const int c = (threadIdx.x % G) * E;
+    const long row = (long)blockIdx.x * (kRowThreads / G) + threadIdx.x / G;
+    const bool in = c < V && row < rows;
+    float a[E], g[E], wv[E];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const long row = row0 + r * RW;
-        const bool in = on && row < rows;
+    for (int i = 0; i < E; ++i) {
+        a[i] = g[i] = 0.f;
+        wv[i] = 1.f;
+    }
+    if (in) {
+        Vec<T>::load(x + row * V + c, a);
+        Vec<T>::load(z + row * V + c, g);
+        if (w) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) a[r][i] = 0.f;
-        if (in) {
-            Vec<T>::load(x + row * V + c, a[r]);
-            Vec<T>::load(z + row * V + c, g[r]);
+            for (int i = 0; i < E; i += 4) Vec<float>::load(w + c + i, wv + i);
         }
     }
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) wv[i] = 1.f;
-    if (w && on) {
+    for (int i = 0; i < E; ++i) sum = fmaf(a[i], a[i], sum);
 #pragma unroll
-        for (int i = 0; i < E; i += 4) Vec<float>::load(w + c + i, wv + i);
-    }
+    for (int m = G / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    const float rs = rsqrtf(sum / V + eps);
+    if (!in) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const long row = row0 + r * RW;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) sum = fmaf(a[r][i], a[r][i], sum);
-#pragma unroll
-        for (int m = G / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const float rs = rsqrtf(sum / V + eps);
-        if (!on || row >= rows) continue;
-#pragma unroll
-        for (int i = 0; i < E; ++i) a[r][i] = a[r][i] * rs * wv[i] * gate_value<T>(g[r][i], act);
-        Vec<T>::store(y + row * V + c, a[r]);
-    }
+    for (int i = 0; i < E; ++i) a[i] = a[i] * rs * wv[i] * gate_value<T>(g[i], act);
+    Vec<T>::store(y + row * V + c, a);
 }
 
 // Gated norm, any row length: one warp per row, lanes step over the row in pieces of E elements,
@@ -192,8 +185,9 @@ __device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c
 
 // Block norm, one block of NT threads per row, the row in registers between the two norms: P pieces
 // of 8 elements a thread.  Memory bounds it: 16384 rows of 8192 (bf16, float32 stream; 1.61 GB) in
-// RATE.  Rows of many threads keep few registers a thread, so that several rows are in flight on an
-// SM while others wait for their sums.
+// 278 us, 5.8 TB/s.  Rows of many threads keep few registers a thread, so that several rows are in
+// flight on an SM while others wait for their sums: 256 threads of four pieces measured 340 us, 1024
+// of one 287.
 template <typename T, typename R, int NT, int P>
 __global__ void __launch_bounds__(NT) block_norm_kernel(BlockNormArgs a) {
     __shared__ float red[2][NT / 32];
@@ -318,8 +312,8 @@ cudaError_t launch_block(const BlockNormArgs& a) {
 
 template <typename T, int G>
 void gated_rows(const GatedNormArgs& a) {
-    constexpr int R = 2, rows = 8 * (32 / G) * R;
-    gated_norm_rows_kernel<T, G, R><<<(unsigned)((a.rows + rows - 1) / rows), 256, 0, a.stream>>>(
+    constexpr int rows = kRowThreads / G;
+    gated_norm_rows_kernel<T, G><<<(unsigned)((a.rows + rows - 1) / rows), kRowThreads, 0, a.stream>>>(
         (const T*)a.x, (const T*)a.gate, a.weight, a.eps, a.act, a.rows, a.V, (T*)a.y);
 }
 

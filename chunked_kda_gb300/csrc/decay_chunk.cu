@@ -1,15 +1,24 @@
-// Linear attention with a decay for each head, the form for prompts: which kernel runs it.
+// Linear attention with a decay for each head, the form for prompts: which kernels run it.
+//
+//   bf16 with head sizes that the tensor-core kernel has      decay_tensor.cu
+//   else, at most kShort tokens a sequence can have           decay_recurrent.cu: one launch, no scratch
+//   else                                                      decay_simt.cu: FP32, all chunks at once
+// Token by token, T = 128 of 2 heads of 64 x 64 float32 measured 45 us; in chunks, three launches, 31.
 #include "common.cuh"
 #include "kda_internal.h"
 
 namespace kda {
 
+static constexpr int kShort = 32;
+
 size_t decay_chunk_workspace_bytes(bool qkv_bf16, int B, int T, int H, int K, int V, int N, bool packed) {
-    return decay_tensor_dims(qkv_bf16, K, V) ? decay_tensor_workspace_bytes(B, T, H, K, V, N, packed) : 0;
+    if (decay_tensor_dims(qkv_bf16, K, V)) return decay_tensor_workspace_bytes(B, T, H, K, V, N, packed);
+    return T <= kShort ? 0 : decay_simt_workspace_bytes(B, T, H, K, V, N, packed);
 }
 
 cudaError_t launch_decay_chunk(const DecayArgs& a) {
-    return decay_tensor_dims(a.qkv_bf16, a.K, a.V) ? launch_decay_tensor(a) : launch_decay_recurrent(a);
+    if (decay_tensor_dims(a.qkv_bf16, a.K, a.V)) return launch_decay_tensor(a);
+    return a.T <= kShort ? launch_decay_recurrent(a) : launch_decay_simt(a);
 }
 
 }  // namespace kda

@@ -1,0 +1,257 @@
+// Linear attention with a decay for each head in chunks of 64 tokens, in FP32 without tensor cores:
+// float32 inputs (whose 24 bits the tensor cores' operand types do not hold) and head sizes that the
+// tensor-core kernel has no instance for.
+//
+// Three launches, all chunks at once but for the scan:
+//   1. each chunk's addition to the state, A = sum_j 2^(G_l - G_j) k_j v_j^T, and its decay 2^G_l;
+//   2. the scan over a sequence's chunks: the addition's place takes the chunk's incoming state;
+//   3. each chunk's output, o_i = s (2^G_i S^T q_i + sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) v_j).
+// The products are 64 x 64 tiles, 256 threads with 4 x 4 results each, operands in shared memory with
+// the summed index outermost, so that a thread takes its four rows and its four columns as one vector
+// each.  Bound by the FP32 pipe (98 k operations a token and head at K = V = 128).
+#include "common.cuh"
+#include "decay_gates.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace decay {
+namespace {
+
+constexpr int C = 64, NT = 256, LD = 68;  // LD: row stride of a 64-wide shared tile, 16-byte aligned
+
+struct SimtArgs {
+    const float* decay;
+    int decay_stride;
+    const float* h0;
+    float* hT;
+    ChunkMap cm;
+    int H, hr, K, V;
+    float* ws;    // [slot][h][K][V]
+    float* wdec;  // [slot][h]
+};
+
+// the chunk's G as integer and fraction, by warp 0 (a barrier follows)
+__device__ __forceinline__ void chunk_gates(const SimtArgs& p, int h, int t0, int len, int (*sI)[C]) {
+    if (threadIdx.x < 32) {
+        const int l = threadIdx.x;
+        auto a = [&](int i) { return i < len ? __ldg(p.decay + (size_t)(t0 + i) * p.decay_stride + h) : 0.f; };
+        int I[2], F[2];
+        const float a0 = a(2 * l), a1 = a(2 * l + 1);
+        pair_sums(a0, a1, I, F);
+        const bool bad = __any_sync(0xffffffffu, a0 != a0 || a1 != a1);  // a NaN decay
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sI[0][2 * l + e] = I[e];
+            sI[1][2 * l + e] = F[e];
+        }
+        if (l == 0) sI[2][0] = bad;
+    }
+    __syncthreads();
+}
+
+// acc[i][j] += sum_{x < n} A[x][4 ti + i] B[x][4 tj + j]
+__device__ __forceinline__ void tile_product(const float* A, const float* B, int n, int ti, int tj, float (&acc)[4][4]) {
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+        const float4 a = *reinterpret_cast<const float4*>(A + x * LD + 4 * ti);
+        const float4 b = *reinterpret_cast<const float4*>(B + x * LD + 4 * tj);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+    }
+}
+
+// grid (slots, H, K blocks x V blocks of 64)
+template <typename T>
+__global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, const T* __restrict__ v, SimtArgs p) {
+    __shared__ float sk[C * LD], sv[C * LD];
+    __shared__ int sI[3][C];
+    int n, t0, len, bos, eos;
+    if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
+    if (t0 + len >= eos && !p.hT) return;  // nothing follows this chunk
+    const int h = blockIdx.y, nkb = (p.K + 63) / 64, c0 = 64 * (blockIdx.z % nkb), d0 = 64 * (blockIdx.z / nkb);
+    const int tid = threadIdx.x;
+    chunk_gates(p, h, t0, len, sI);
+    const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
+    const int Hk = p.H / p.hr, hq = h / p.hr;
+    for (int x = tid; x < C * 64; x += NT) {
+        const int j = x >> 6, c = x & 63;
+        float kk = 0.f, vv = 0.f;
+        if (j < len) {
+            const float f = pow2(sI[0][C - 1] - sI[0][j], sI[1][C - 1] - sI[1][j]) + poison;
+            if (c0 + c < p.K) kk = to_f32(k[((size_t)(t0 + j) * Hk + hq) * p.K + c0 + c]) * f;
+            if (d0 + c < p.V) vv = to_f32(v[((size_t)(t0 + j) * p.H + h) * p.V + d0 + c]);
+        }
+        sk[j * LD + c] = kk;
+        sv[j * LD + c] = vv;
+    }
+    __syncthreads();
+    const int ti = tid >> 4, tj = tid & 15;
+    float acc[4][4] = {};
+    tile_product(sk, sv, C, ti, tj, acc);
+    float* out = p.ws + ((size_t)blockIdx.x * p.H + h) * p.K * p.V;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = c0 + 4 * ti + i, d = d0 + 4 * tj + j;
+            if (c < p.K && d < p.V) out[(size_t)c * p.V + d] = acc[i][j];
+        }
+    if (tid == 0 && blockIdx.z == 0)
+        p.wdec[(size_t)blockIdx.x * p.H + h] = pow2(max(sI[0][C - 1], -300), sI[1][C - 1]) + poison;
+}
+
+// grid (blocks of 256 state elements, H, sequences): the chunks' incoming states, and the final one
+__global__ void __launch_bounds__(NT) decay_chunk_scan_kernel(SimtArgs p) {
+    const int n = blockIdx.z, h = blockIdx.y, KV = p.K * p.V, e = blockIdx.x * NT + threadIdx.x;
+    if (e >= KV) return;
+    int bos, eos;
+    if (p.cm.cu) { bos = __ldg(p.cm.cu + n); eos = __ldg(p.cm.cu + n + 1); }
+    else         { bos = n * p.cm.T; eos = bos + p.cm.T; }
+    const int ns = (eos - bos + C - 1) / C;
+    const size_t st = ((size_t)n * p.H + h) * KV + e;
+    float S = p.h0 ? p.h0[st] : 0.f;
+    const int s0 = ns > 0 ? p.cm.first_slot(n, bos) : 0;
+    // (eight chunks' additions are loaded before the first is used)
+    constexpr int U = 8;
+    for (int s = 0; s < ns; s += U) {
+        float add[U], dec[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = s + u < ns && (s + u + 1 < ns || p.hT);
+            add[u] = in ? p.ws[((size_t)(s0 + s + u) * p.H + h) * KV + e] : 0.f;
+            dec[u] = in ? __ldg(p.wdec + (size_t)(s0 + s + u) * p.H + h) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= ns) break;
+            p.ws[((size_t)(s0 + s + u) * p.H + h) * KV + e] = S;
+            S = fmaf(dec[u], S, add[u]);
+        }
+    }
+    if (p.hT) p.hT[st] = S;
+}
+
+// grid (slots, H): the chunk's output, all its value channels
+template <typename T, typename OT>
+__global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                       const T* __restrict__ v, OT* __restrict__ o, SimtArgs p) {
+    extern __shared__ float sm[];
+    const int Kp = (p.K + 31) / 32 * 32;
+    float* sq = sm;               // [Kp][LD] q, transposed
+    float* sp = sq + Kp * LD;     // [64][LD] P, transposed
+    float* sx = sp + C * LD;      // [32][LD] a slice of k (transposed), S or v
+    __shared__ int sI[3][C];
+    int n, t0, len, bos, eos;
+    if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
+    const int h = blockIdx.y, tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
+    chunk_gates(p, h, t0, len, sI);
+    const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
+    const int Hk = p.H / p.hr, hq = h / p.hr;
+    const float scale = rsqrtf((float)p.K);
+    for (int x = tid; x < C * Kp; x += NT) {
+        const int i = x / Kp, c = x - i * Kp;
+        sq[c * LD + i] = i < len && c < p.K ? to_f32(q[((size_t)(t0 + i) * Hk + hq) * p.K + c]) : 0.f;
+    }
+    {
+        float acc[4][4] = {};
+        for (int c0 = 0; c0 < Kp; c0 += 32) {
+            __syncthreads();
+            for (int x = tid; x < C * 32; x += NT) {
+                const int j = x >> 5, c = x & 31;
+                sx[c * LD + j] = j < len && c0 + c < p.K ? to_f32(k[((size_t)(t0 + j) * Hk + hq) * p.K + c0 + c]) : 0.f;
+            }
+            __syncthreads();
+            tile_product(sq + c0 * LD, sx, 32, ti, tj, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 4 * ti + i, s = 4 * tj + j;
+                float y = 0.f;
+                if (s <= r) y = acc[i][j] * (pow2(sI[0][r] - sI[0][s], sI[1][r] - sI[1][s]) + poison);
+                sp[s * LD + r] = y;
+            }
+    }
+    const float* S = p.ws + ((size_t)blockIdx.x * p.H + h) * p.K * p.V;
+    for (int d0 = 0; d0 < p.V; d0 += 64) {
+        float acc[4][4] = {};
+        for (int c0 = 0; c0 < Kp; c0 += 32) {
+            __syncthreads();
+            for (int x = tid; x < 32 * 64; x += NT) {
+                const int c = x >> 6, d = x & 63;
+                sx[c * LD + d] = c0 + c < p.K && d0 + d < p.V ? S[(size_t)(c0 + c) * p.V + d0 + d] : 0.f;
+            }
+            __syncthreads();
+            tile_product(sq + c0 * LD, sx, 32, ti, tj, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = pow2(sI[0][4 * ti + i], sI[1][4 * ti + i]) + poison;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] *= f;
+        }
+        for (int j0 = 0; j0 < C; j0 += 32) {
+            __syncthreads();
+            for (int x = tid; x < 32 * 64; x += NT) {
+                const int j = x >> 6, d = x & 63;
+                sx[j * LD + d] = j0 + j < len && d0 + d < p.V ? to_f32(v[((size_t)(t0 + j0 + j) * p.H + h) * p.V + d0 + d]) : 0.f;
+            }
+            __syncthreads();
+            tile_product(sp + j0 * LD, sx, 32, ti, tj, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ti + i;
+            if (r >= len) continue;
+            OT* dst = o + ((size_t)(t0 + r) * p.H + h) * p.V + d0 + 4 * tj;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (d0 + 4 * tj + j < p.V) dst[j] = from_f32<OT>(acc[i][j] * scale);
+        }
+    }
+}
+
+size_t state_bytes(int slots, int H, int K, int V) { return ((size_t)slots * H * K * V * 4 + 255) / 256 * 256; }
+
+template <typename T, typename OT>
+cudaError_t run(const DecayArgs& a) {
+    const ChunkMap cm{a.cu, a.N, a.T, C};
+    const int slots = cm.n_slots();
+    SimtArgs p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, cm, a.H, a.H / a.Hk, a.K, a.V, (float*)a.ws,
+               (float*)((char*)a.ws + state_bytes(slots, a.H, a.K, a.V))};
+    cudaError_t e;
+    if (slots > 0) {
+        const dim3 grid(slots, a.H, ((a.K + 63) / 64) * ((a.V + 63) / 64));
+        decay_add_kernel<T><<<grid, NT, 0, a.stream>>>((const T*)a.k, (const T*)a.v, p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    decay_chunk_scan_kernel<<<dim3((a.K * a.V + NT - 1) / NT, a.H, a.N), NT, 0, a.stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (slots > 0) {
+        auto kern = decay_out_kernel<T, OT>;
+        const int bytes = ((a.K + 31) / 32 * 32 + C + 32) * LD * (int)sizeof(float);
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        kern<<<dim3(slots, a.H), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+}  // namespace decay
+
+size_t decay_simt_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed) {
+    const int slots = packed ? T / decay::C + N + 1 : N * ((T + decay::C - 1) / decay::C);
+    return decay::state_bytes(slots, H, K, V) + ((size_t)slots * H * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_decay_simt(const DecayArgs& a) {
+    if (!a.qkv_bf16) return decay::run<float, float>(a);
+    return a.o_f32 ? decay::run<__nv_bfloat16, float>(a) : decay::run<__nv_bfloat16, __nv_bfloat16>(a);
+}
+
+}  // namespace kda

@@ -27,6 +27,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "decay_gates.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
 
@@ -333,53 +334,16 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const float x0 = a0, x1 = a1;
             a0 = raw(t0 + C + 2 * l);
             a1 = raw(t0 + C + 2 * l + 1);
-            // A log2 decay as an integer and a fraction in 2^-24 units (clamped: 2^-1024 is zero for
-            // a float32).  Integer sums of both are exact.
-            auto fixed = [](float a, int& ip) {
-                constexpr float kRest = 1.9259629911267e-8f;  // log2(e) - kLog2e
-                const float x = fminf(fmaxf(a * kLog2e, -1024.f), 1024.f), fl = floorf(x);
-                const float e = fabsf(x) < 1024.f ? fmaf(a, kLog2e, -x) + a * kRest : 0.f;
-                ip = (int)fl;
-                return __float2int_rn(((x - fl) + e) * 16777216.f);
-            };
-            int i0, i1;
-            const int f0 = fixed(x0, i0), f1 = fixed(x1, i1);
-            int ii = i0 + i1, ff = f0 + f1;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int yi = __shfl_up_sync(0xffffffffu, ii, m), yf = __shfl_up_sync(0xffffffffu, ff, m);
-                if (l >= m) { ii += yi; ff += yf; }
-            }
-            int I[2] = {ii - i1, ii}, F[2] = {ff - f1, ff};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {  // the fraction into [0, 1)
-                I[e] += F[e] >> 24;
-                F[e] &= 0xFFFFFF;
-            }
+            int I[2], F[2];
+            pair_sums(x0, x1, I, F);
             const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
             const int Ih = __shfl_sync(0xffffffffu, I[1], 15), Fh = __shfl_sync(0xffffffffu, F[1], 15);
             const float poison = __any_sync(0xffffffffu, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 0.f;  // a NaN decay
             total += ((long long)Il << 24) + Fl;
-            auto pow2i = [](int n) { return __int_as_float(min(max(n + 127, 0), 255) << 23); };
-            // 2^(n + f / 2^24), |f| < 2^24: the power of the nearest integer times the power series
-            // of the rest (|z| <= ln(2) / 2: the first left out term is below 2^-26)
-            auto pow2 = [&](int n, int f) {
-                const int r = (f + (1 << 23)) >> 24;
-                const float z = (float)(f - (r << 24)) * (0.69314718f / 16777216.f);
-                float y = fmaf(1.f / 5040.f, z, 1.f / 720.f);
-                y = fmaf(y, z, 1.f / 120.f);
-                y = fmaf(y, z, 1.f / 24.f);
-                y = fmaf(y, z, 1.f / 6.f);
-                y = fmaf(y, z, 0.5f);
-                y = fmaf(y, z, 1.f);
-                return fmaf(y, z, 1.f) * pow2i(n + r);
-            };
             // this chunk's keys and row factors, and the exponent behind it
             int ni = Ei + Il, nf = Ef + Fl;
-            ni += nf >> 24;
-            nf &= 0xFFFFFF;
+            carry(ni, nf);
             const bool renew = ni < -32 || ni >= 32;
-            auto fast2 = [&](int n, int f) { return ex2_fast((float)f * (1.f / 16777216.f)) * pow2i(n); };
             // the slot's last readers are done: chunk c - NS is loaded (and its FULL phase complete),
             // so the products of c - 2 NS are done, which the output warps of c - NG preceded
             if (c >= NS && !sy.warp_wait(B_FULL + s, ((c / NS) - 1) & 1)) break;
@@ -389,9 +353,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int i = 2 * l + e;
                 sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + poison);
                 const int rf = Ef + F[e];
-                sts(gt + GT_ROW + 4 * i, kScale * fast2(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + poison);
+                sts(gt + GT_ROW + 4 * i, kScale * pow2_fast(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + poison);
                 sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e], Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
-                if (l < 16) sts(gt + GT_HALF + 4 * i, fast2(Ih - I[e], Fh - F[e]) + poison);
+                if (l < 16) sts(gt + GT_HALF + 4 * i, pow2_fast(Ih - I[e], Fh - F[e]) + poison);
             }
             if (l == 0) {
                 sts(gt + GT_LAST, (renew ? pow2(ni, nf) : 1.f) + poison);

@@ -149,6 +149,9 @@ cudaError_t launch_decay_chunk(const DecayArgs& a);
 bool decay_tensor_dims(bool qkv_bf16, int K, int V);
 size_t decay_tensor_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed);
 cudaError_t launch_decay_tensor(const DecayArgs& a);
+// its FP32 kernels: any dtype, any K and V up to 256
+size_t decay_simt_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed);
+cudaError_t launch_decay_simt(const DecayArgs& a);
 cudaError_t read_decay_timeouts(unsigned* count, bool reset);
 cudaError_t launch_gated_norm(const GatedNormArgs& a);
 cudaError_t launch_block_norm(const BlockNormArgs& a);
