@@ -5,25 +5,32 @@
 // and including row i, l the last row, s = 1/sqrt(K):
 //   P[i][j] = 2^(G_i - G_j) (q_i . k_j)  for j <= i, else 0                     (bf16 operand)
 //   o_i     = s (2^G_i S^T q_i + sum_j P[i][j] v_j)
-//   S      <- 2^G_l S + sum_j (2^(G_l - G_j) k_j) v_j^T                         (FP32)
+//   S      <- 2^G_l S + sum_j k_j (2^(G_l - G_j) v_j)^T                         (FP32)
 // as four products, value channels (M = 128) on TMEM lanes:
-//   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += v^T kd.
-// The stored state is S 2^-E.  Where the decay is slow, E' = E + G_l and the keys carry 2^(G_l - G_j - E')
+//   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += vd^T k.
+// The stored state is S 2^-E.  Where the decay is slow, E' = E + G_l and the values carry 2^(G_l - G_j - E')
 // = 2^-(E + G_j): nothing has to be multiplied between two chunks' state products, and S is rounded once
 // less.  Before |E| passes 32 the stored state is scaled (factor 2^(E + G_l)) and E starts again at 0.
 //
 // q, k and v enter the products as they are; O1's row factor s 2^(E + G_i) is applied to the FP32
 // results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
-// difference of an integer and of a fraction part (64-bit fixed-point sums), exact whatever the sums.
+// difference of an integer and of a fraction part (integer sums), exact whatever the sums.
 //
 // Roundings: P and the copy of S that O1 reads are bf16 (each adds the output's own rounding once
 // more; both in quadrature keep o's error within 1.45 of one rounding).  The state is a float32 output and
-// feeds every later chunk, so the scaled keys kd are split into three bf16 terms (24 bits) and S is
-// accumulated from all three: 3 x 256 of the chunk's ~1400 tensor-pipe clocks.
+// feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits) and S is accumulated
+// from all three.
 //
-// One CTA per unit and SM, 25 warps: 0-1 P, 2 decay factors, 3 loads and the state's products, 4-11
-// state, 12-15 output, 16-23 scaled keys, 24 the output's products.  Every wait is bounded (a CTA that gives up lets its copies and MMAs
-// finish, frees its TMEM and returns).
+// What bounds it is shared memory's 128 bytes a clock next to HBM: per chunk at K = V = 128 the loads
+// write 48 KB, the products read 120 KB, the warps and the stores about 60 KB.  That is why the scaled
+// values are the operand that lies in TMEM, straight from registers: scaled keys in shared memory cost
+// 48 KB of writes and 48 KB of reads more a chunk (3340 against CLOCKS clocks).
+//
+// One CTA per unit and SM, 28 warps: 0-3 P, 4-11 state, 12-15 output, 16-23 scaled values, 24 the output's
+// products, 25 decay factors, 26 the state's products, 27 loads and scores.  Every wait is bounded (a CTA
+// that gives up lets its copies and MMAs finish, frees its TMEM and returns).  The roles' loops are kept
+// rolled and short: together they have to fit the instruction caches (unrolled, "no instruction" was 40 %
+// of all stalls and a chunk took twice as long).
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -38,32 +45,32 @@ using namespace sm100;
 
 __device__ unsigned int g_decay_timeouts = 0;
 
-constexpr int C = 64, NTHR = 800, NS = 3, NG = 8;
+constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1;
 
 // barriers
-enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P = B_QK + 2, B_S = B_P + 2, B_SBF, B_KD, B_STATE = B_KD + 2, B_INTER, B_O,
-       B_OFREE = B_O + 2, B_DRAIN = B_OFREE + 2, B_DRAIN2, B_NEVER, NBAR };
+enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + 2, B_SBF, B_VD, B_STATE, B_INTER, B_O,
+       B_OFREE = B_O + 2, B_DRAIN, B_DRAIN2, B_DRAIN3, B_NEVER, NBAR };
 
 // The decay factors of a chunk, one slot of a ring of NG (written when the chunk is loaded, read
 // last by its output warps, at most NS + 3 chunks later): byte offsets of its float arrays.
 constexpr uint32_t GT_G = 0;       // [64][2] G_i as integer and fraction
 constexpr uint32_t GT_ROW = 512;   // [64] s 2^(E + G_i)
-constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j - E')
-constexpr uint32_t GT_HALF = 1024; // [32] 2^(G_31 - G_j)
-constexpr uint32_t GT_LAST = 1152; // the stored state's factor before this chunk's keys, 1: none
-constexpr uint32_t GT_OUT = 1156;  // 2^E'
-constexpr uint32_t GT_BYTES = 1168;
+constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j - E'), the values' factors
+constexpr uint32_t GT_COL = 1024;  // [64] 2^(G_m - G_j), m the last of j's 16 rows
+constexpr uint32_t GT_LAST = 1280; // the stored state's factor before this chunk's product, 1: none
+constexpr uint32_t GT_OUT = 1284;  // 2^E'
+constexpr uint32_t GT_BYTES = 1296;
 
 template <int KD, int VB>
 struct Layout {
     static constexpr uint32_t QB = C * KD * 2, VBYTES = C * VB * 2, STAGE = 2 * QB + VBYTES;
-    static constexpr uint32_t KM = NS * STAGE, KL = KM + QB, P = KL + QB, O = P + 2 * C * C * 2, G = O + VBYTES;
+    static constexpr uint32_t P = NS * STAGE, O = P + 2 * C * C * 2, G = O + VBYTES;
     static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = BAR + 8 * NBAR, END = MISC + 16;
-    // an A operand of 64 rows or channels is read as 128: up to 8 KB behind its tile
+    // an A operand of 64 value channels is read as 128: up to 8 KB behind its tile
     static constexpr uint32_t BYTES = END + 1024 + 64;
 };
-// TMEM columns: S^T, its bf16 copy, two buffers of QK and of O1, O2
-constexpr uint32_t TM_S = 0, TM_SB = 128, TM_QK = 192, TM_O1 = 320, TM_O2 = 448, TM_COLS = 512;
+// TMEM columns: S^T, its bf16 copy, the three terms of the scaled values, QK, O1, O2
+constexpr uint32_t TM_S = 0, TM_SB = 128, TM_VD = 192, TM_QK = 288, TM_O1 = 352, TM_O2 = 416, TM_COLS = 512;
 
 struct Params {
     const float* decay;
@@ -94,7 +101,6 @@ struct Sync {
     __device__ __noinline__ void slow_wait(int i, uint32_t parity, uint32_t limit) const {
         if (!*abort_flag && !mbar_wait_unless(bar(i), parity, abort_flag, limit)) give_up();
     }
-    __device__ __forceinline__ bool ready(int i, uint32_t parity) const { return mbar_try_wait(bar(i), parity, 0); }
     __device__ __forceinline__ bool aborted() const { return *abort_flag != 0u; }
     // A whole warp's wait, the same answer in every lane: false when a wait has given up and this
     // one's phase has not come.
@@ -168,6 +174,14 @@ __device__ __forceinline__ void ld16x32(uint32_t t, float* v) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void ld16x16(uint32_t t, float* v) {  // the same for 16 columns
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 // two FP32 operations in one instruction
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -186,6 +200,23 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // (transposed) row i % 8 of matrix i / 8
 __device__ __forceinline__ void stmatrix4_t(uint32_t a, const uint32_t* r) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+// four 8 x 8 matrices of 16-bit elements, each transposed on the way (addresses as above)
+__device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// 16 lanes x 16 columns: of each four columns, thread t has column t % 4 of lanes t / 4 and t / 4 + 8
+__device__ __forceinline__ void st16x16(uint32_t t, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t a, const uint32_t* r) {  // as they are
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
@@ -241,9 +272,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int count = 1;
             if (i >= B_FULL && i < B_FULL + NS) count = 2;                 // the loads and the decay factors
             if (i >= B_FREE && i < B_FREE + NS) count = kStates ? 1 : 2;   // the products of both issuing warps
-            if (i == B_P || i == B_P + 1) count = 2;                       // two P warps
-            if (i == B_OFREE || i == B_OFREE + 1) count = 4;               // four output warps
-            if (i >= B_S && i < B_KD + 2) count = 8;                       // eight warps
+            if (i == B_P || i == B_P + 1) count = 4;                       // four P warps
+            if (i == B_OFREE) count = 4;                                   // four output warps
+            if (i >= B_S && i <= B_VD) count = 8;                          // eight warps
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
@@ -253,66 +284,73 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_o);
     }
-    if (w == 3) tmem_alloc(sb + L::MISC, TM_COLS);
+    if (w == 26) tmem_alloc(sb + L::MISC, TM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
 
-    if (w < 2) {
+    if (w < 4) {
         // ------------------------------------------------ P = QK with the decays, bf16, K-major rows
+        // A warp's 16 rows (QK's 64 rows lie on the first 16 lanes of each quarter of TMEM) in
+        // fragments of 8 x 8: a thread has rows l / 4 and l / 4 + 8, and of eight columns a pair.
         if constexpr (!kStates) {
-            const int i = 32 * w + l;
+            const int r0 = 16 * w + (l >> 2), cp = 2 * (l & 3);
             const float scale = rsqrtf((float)p.K), log2_scale = -0.5f * log2f((float)p.K);
-            if (w == 0)  // the upper right quarter of both buffers stays zero
-                for (int x = 0; x < 8; ++x) st_s128(sb + L::P + (x >> 2) * (C * C * 2) + sw128(i, 4 + (x & 3)), 0, 0, 0, 0);
+            // where a lane's row of the four stored blocks goes (columns 16 cb: piece 2 cb more)
+            const int srow = 16 * w + (l & 15), spiece = l >> 4;
+            for (int x = l; x < 2 * 16 * 8; x += 32) {  // the blocks right of the diagonal stay zero
+                const int row = 16 * w + (x & 15), piece = (x >> 4) & 7;
+                if (piece > 2 * w + 1) st_s128(sb + L::P + (x >> 7) * (C * C * 2) + sw128(row, piece), 0, 0, 0, 0);
+            }
 #pragma unroll 1
             for (int c = 0; c < nt; ++c) {
                 const int b = c & 1;
                 if (!sy.warp_wait(B_FULL + c % NS, (c / NS) & 1)) break;                // the decay factors
-                if (!sy.warp_wait(B_QK + b, (c >> 1) & 1)) break;
+                if (!sy.warp_wait(B_QK, c & 1)) break;
                 if (c >= 2 && !sy.warp_wait(B_O + b, ((c - 2) >> 1) & 1)) break;        // this P buffer's last reader
                 tc_fence_after();
-                const uint32_t gt = gates(c), row = sb + L::P + b * (C * C * 2);
-                float2 gi = lds2(gt + GT_G + 8 * i);
-                const uint32_t qk = tmem + TM_QK + 64 * b + ((uint32_t)(32 * w) << 16);
-                if (w == 1) {
-                    // rows behind column 31: the factor parts into a row's and a column's, both <= 1
-                    const float2 gh = lds2(gt + GT_G + 8 * 31);
-                    const float fr = scale * ex2_fast((gi.x - gh.x) + (gi.y - gh.y));
+                const uint32_t gt = gates(c), to = sb + L::P + b * (C * C * 2), qk = tmem + TM_QK + ((uint32_t)(32 * w) << 16);
+                float2 g0 = lds2(gt + GT_G + 8 * r0), g1 = lds2(gt + GT_G + 8 * (r0 + 8));
+                // left of the diagonal block the factor parts into a row's and a column's, both <= 1
 #pragma unroll 1
-                    for (int j0 = 0; j0 < 32; j0 += 16) {
-                        float x[16];
-                        uint32_t out[8];
-                        tmem_ld16(qk + j0, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 f = lds4(gt + GT_HALF + 4 * (j0 + j));
-                            out[j / 2] = pack_bf16(x[j] * (f.x * fr), x[j + 1] * (f.y * fr));
-                            out[j / 2 + 1] = pack_bf16(x[j + 2] * (f.z * fr), x[j + 3] * (f.w * fr));
-                        }
-                        st_s128(row + sw128(i, j0 >> 3), out[0], out[1], out[2], out[3]);
-                        st_s128(row + sw128(i, (j0 >> 3) + 1), out[4], out[5], out[6], out[7]);
-                    }
-                }
-                gi.y += log2_scale;
-#pragma unroll 1
-                for (int j0 = 0; j0 < 32; j0 += 16) {
-                    float x[16];
-                    uint32_t out[8];
-                    tmem_ld16(qk + 32 * w + j0, x);
+                for (int cb = 0; cb < w; ++cb) {
+                    float x[8];
+                    ld16x16(qk + 16 * cb, x);
+                    const float2 gm = lds2(gt + GT_G + 8 * (16 * cb + 15));
+                    const float f0 = scale * ex2_fast((g0.x - gm.x) + (g0.y - gm.y));
+                    const float f1 = scale * ex2_fast((g1.x - gm.x) + (g1.y - gm.y));
                     tmem_wait_ld();
-                    const int last = l - j0;  // columns up to this one of the sixteen
+                    uint32_t r[4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float4 g = lds4(gt + GT_G + 8 * (32 * w + j0 + j));
-                        const float f0 = ex2_fast((gi.x - g.x) + (gi.y - g.y)), f1 = ex2_fast((gi.x - g.z) + (gi.y - g.w));
-                        out[j / 2] = pack_bf16(j <= last ? x[j] * f0 : 0.f, j + 1 <= last ? x[j + 1] * f1 : 0.f);
+                    for (int g = 0; g < 2; ++g) {
+                        const float2 f = lds2(gt + GT_COL + 4 * (16 * cb + 8 * g + cp));
+                        const float2 y0 = mul2(make_float2(x[4 * g], x[4 * g + 1]), mul2(f, make_float2(f0, f0)));
+                        const float2 y1 = mul2(make_float2(x[4 * g + 2], x[4 * g + 3]), mul2(f, make_float2(f1, f1)));
+                        r[2 * g] = pack_bf16(y0.x, y0.y);
+                        r[2 * g + 1] = pack_bf16(y1.x, y1.y);
                     }
-                    const int ch = 4 * w + (j0 >> 3);
-                    st_s128(row + sw128(i, ch), out[0], out[1], out[2], out[3]);
-                    st_s128(row + sw128(i, ch + 1), out[4], out[5], out[6], out[7]);
+                    stmatrix4(to + sw128(srow, 2 * cb + spiece), r);
+                }
+                {
+                    float x[8];
+                    ld16x16(qk + 16 * w, x);
+                    g0.y += log2_scale;
+                    g1.y += log2_scale;
+                    tmem_wait_ld();
+                    uint32_t r[4];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int j = 8 * g + cp, i = l >> 2;  // within the block
+                        const float4 gj = lds4(gt + GT_G + 8 * (16 * w + j));
+                        const float y0 = x[4 * g] * ex2_fast((g0.x - gj.x) + (g0.y - gj.y));
+                        const float y1 = x[4 * g + 1] * ex2_fast((g0.x - gj.z) + (g0.y - gj.w));
+                        const float y2 = x[4 * g + 2] * ex2_fast((g1.x - gj.x) + (g1.y - gj.y));
+                        const float y3 = x[4 * g + 3] * ex2_fast((g1.x - gj.z) + (g1.y - gj.w));
+                        r[2 * g] = pack_bf16(j <= i ? y0 : 0.f, j + 1 <= i ? y1 : 0.f);
+                        r[2 * g + 1] = pack_bf16(j <= i + 8 ? y2 : 0.f, j + 1 <= i + 8 ? y3 : 0.f);
+                    }
+                    stmatrix4(to + sw128(srow, 2 * w + spiece), r);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -320,7 +358,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (l == 0) mbar_arrive(sy.bar(B_P + b));
             }
         }
-    } else if (w == 2) {
+    } else if (w == 25) {
         // ------------------------------------------------ decay factors
         const float kScale = rsqrtf((float)p.K);
         const float* dp = p.decay + h;
@@ -337,10 +375,10 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int I[2], F[2];
             pair_sums(x0, x1, I, F);
             const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
-            const int Ih = __shfl_sync(0xffffffffu, I[1], 15), Fh = __shfl_sync(0xffffffffu, F[1], 15);
+            const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
             const float poison = __any_sync(0xffffffffu, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 0.f;  // a NaN decay
             total += ((long long)Il << 24) + Fl;
-            // this chunk's keys and row factors, and the exponent behind it
+            // this chunk's value and row factors, and the exponent behind it
             int ni = Ei + Il, nf = Ef + Fl;
             carry(ni, nf);
             const bool renew = ni < -32 || ni >= 32;
@@ -355,7 +393,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int rf = Ef + F[e];
                 sts(gt + GT_ROW + 4 * i, kScale * pow2_fast(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + poison);
                 sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e], Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
-                if (l < 16) sts(gt + GT_HALF + 4 * i, pow2_fast(Ih - I[e], Fh - F[e]) + poison);
+                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]) + poison);
             }
             if (l == 0) {
                 sts(gt + GT_LAST, (renew ? pow2(ni, nf) : 1.f) + poison);
@@ -370,114 +408,132 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 p.wdec[(size_t)slot * p.H + h] = pow2((int)(t >> 24), (int)(t & 0xFFFFFF)) + poison;
             }
         }
-    } else if (w == 3) {
-        // ------------------------------------------------ loads, the state's products
-        constexpr uint32_t id_s = idesc_bf16(128, KD, 1, 1);
-        auto load = [&](int c) {
-            if (elect()) {
-                const uint32_t st = sb + (c % NS) * L::STAGE, full = sy.bar(B_FULL + c % NS);
-                const int t0 = bos + c * C;
-                mbar_arrive_expect_tx(full, (kStates ? L::QB : 2 * L::QB) + L::VBYTES);
+    } else if (w == 27) {
+        // ------------------------------------------------ loads, and the scores QK
+        // Both as early as they can: a chunk's loads when its stage is free, its scores when it is
+        // loaded and P has been formed from the last chunk's.
+        // (One copy of each in the loop: a warp that issues from several places misses in the
+        // instruction caches.)
+        int c = 0, nq = kStates ? nt : 0;
+        uint32_t idle = 0;
+        auto ready = [&](int bar, int parity, uint32_t ns) {
+            return __all_sync(0xffffffffu, mbar_try_wait(sy.bar(bar), parity, ns));
+        };
+#pragma unroll 1
+        while (c < nt || nq < nt) {
+            bool moved = false;
+            if (c < nt && (c < NS || ready(B_FREE + c % NS, ((c / NS) - 1) & 1, nq < nt ? 0 : 1000))) {
+                if (elect()) {
+                    const uint32_t st = sb + (c % NS) * L::STAGE, full = sy.bar(B_FULL + c % NS);
+                    const int t0 = bos + c * C;
+                    mbar_arrive_expect_tx(full, (kStates ? L::QB : 2 * L::QB) + L::VBYTES);
 #pragma unroll
-                for (int x = 0; x < KD / 64; ++x) {
-                    if constexpr (!kStates) tma_load_3d(st + x * 8192, &tm_q, 64 * x, hq, t0, full);
-                    tma_load_3d(st + L::QB + x * 8192, &tm_k, 64 * x, hq, t0, full);
+                    for (int x = 0; x < KD / 64; ++x) {
+                        if constexpr (!kStates) tma_load_3d(st + x * 8192, &tm_q, 64 * x, hq, t0, full);
+                        tma_load_3d(st + L::QB + x * 8192, &tm_k, 64 * x, hq, t0, full);
+                    }
+#pragma unroll
+                    for (int x = 0; x < VB / 64; ++x) tma_load_3d(st + 2 * L::QB + x * 8192, &tm_v, vc0 + 64 * x, h, t0, full);
+                    // The stages hold the chunks in work and one ahead, too few bytes in flight for
+                    // the memory: the tiles behind them come into L2 meanwhile
+                    if (c + kAhead < nt) {
+#pragma unroll
+                        for (int x = 0; x < KD / 64; ++x) {
+                            if constexpr (!kStates) tma_prefetch_l2_3d(&tm_q, 64 * x, hq, t0 + kAhead * C);
+                            tma_prefetch_l2_3d(&tm_k, 64 * x, hq, t0 + kAhead * C);
+                        }
+#pragma unroll
+                        for (int x = 0; x < VB / 64; ++x) tma_prefetch_l2_3d(&tm_v, vc0 + 64 * x, h, t0 + kAhead * C);
+                    }
                 }
+                __syncwarp();
+                ++c;
+                moved = true;
+            }
+            if constexpr (!kStates) {
+                if (nq < c && (nq < 1 || ready(B_P + ((nq - 1) & 1), ((nq - 1) >> 1) & 1, 0)) &&
+                    ready(B_FULL + nq % NS, (nq / NS) & 1, 200)) {
+                    const uint32_t qa = lo_k(sb + (nq % NS) * L::STAGE), ka = qa + (L::QB >> 4);
+                    tc_fence_after();
+                    if (elect()) {
 #pragma unroll
-                for (int x = 0; x < VB / 64; ++x) tma_load_3d(st + 2 * L::QB + x * 8192, &tm_v, vc0 + 64 * x, h, t0, full);
+                        for (int kk = 0; kk < KD / 16; ++kk) {
+                            const uint32_t d = (kk >> 2) * 512 + (kk & 3) * 2;
+                            umma_bf16(tmem + TM_QK, desc(qa + d), desc(ka + d), idesc_bf16(64, 64, 0, 0), kk > 0);
+                        }
+                        umma_commit(sy.bar(B_QK));
+                    }
+                    __syncwarp();
+                    ++nq;
+                    moved = true;
+                }
+            }
+            idle = moved ? 0 : idle + 1;
+            if (idle >= (1u << 24) && l == 0) sy.give_up();
+            if ((idle & 255u) == 255u && __any_sync(0xffffffffu, sy.aborted())) break;
+        }
+        if (__any_sync(0xffffffffu, sy.aborted())) {  // leave no copy and no MMA in flight behind
+            if (elect()) {
+                umma_commit(sy.bar(B_DRAIN3));
+                mbar_wait(sy.bar(B_DRAIN3), 0);
+                // (where a chunk's decay factors do not come any more, their arrival is made here)
+                for (int x = max(0, c - NS); x < c; ++x)
+                    if (!mbar_wait(sy.bar(B_FULL + x % NS), (x / NS) & 1, 1u << 12)) {
+                        mbar_arrive(sy.bar(B_FULL + x % NS));
+                        mbar_wait(sy.bar(B_FULL + x % NS), (x / NS) & 1);
+                    }
             }
             __syncwarp();
-        };
-        int loaded = 0;
-        for (; loaded < min(nt, NS); ++loaded) load(loaded);
+        }
+    } else if (w == 26) {
+        // ------------------------------------------------ the state's products
+        constexpr uint32_t id_s = idesc_bf16(128, KD, 0, 1);
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS;
-            const uint32_t k = lo_mn(sb + s * L::STAGE + L::QB), v = lo_mn(sb + s * L::STAGE + 2 * L::QB);
+            const uint32_t k = lo_mn(sb + s * L::STAGE + L::QB);
             if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
-            if (!sy.warp_wait(B_S, c & 1) || !sy.warp_wait(B_KD + (c & 1), (c >> 1) & 1)) break;
+            if (!sy.warp_wait(B_S, c & 1) || !sy.warp_wait(B_VD, c & 1)) break;
             tc_fence_after();
-            if (elect()) {  // S^T += v^T kd, the three terms of kd
+            if (elect()) {  // S^T += vd^T k, the three terms of vd
 #pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    const uint32_t kd = term == 0 ? k : lo_mn(sb + (term == 1 ? L::KM : L::KL));
+                for (int term = 0; term < 3; ++term)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) umma_bf16(tmem + TM_S, desc(v + kk * 128), desc(kd + kk * 128), id_s, 1);
-                }
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tmem + TM_S, tmem + TM_VD + 32 * term + 8 * kk, desc(k + kk * 128), id_s, 1);
                 umma_commit(sy.bar(B_STATE));
                 if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
             }
             __syncwarp();
-            // the stage of the chunk before this one is free by now
-            if (c > 0 && loaded < nt) {
-                if (!sy.warp_wait(B_FREE + (c - 1) % NS, ((c - 1) / NS) & 1)) break;
-                load(loaded++);
-            }
         }
-        if (__any_sync(0xffffffffu, sy.aborted())) {  // leave no copy and no MMA in flight behind
+        if (__any_sync(0xffffffffu, sy.aborted())) {  // let the MMAs in flight finish
             if (elect()) {
                 umma_commit(sy.bar(B_DRAIN));
                 mbar_wait(sy.bar(B_DRAIN), 0);
-                // (a stage's last load; where its decay factors do not come any more, the second arrival is made here)
-                for (int c = max(0, loaded - NS); c < loaded; ++c)
-                    if (!mbar_wait(sy.bar(B_FULL + c % NS), (c / NS) & 1, 1u << 12)) {
-                        mbar_arrive(sy.bar(B_FULL + c % NS));
-                        mbar_wait(sy.bar(B_FULL + c % NS), (c / NS) & 1);
-                    }
             }
             __syncwarp();
         }
     } else if (w == 24) {
         // ------------------------------------------------ the output's products
         if constexpr (!kStates) {
-            constexpr uint32_t id_nk = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 0);
-            auto qk = [&](int c) {
-                const uint32_t a = lo_k(sb + (c % NS) * L::STAGE), b = a + (L::QB >> 4), to = tmem + TM_QK + 64 * (c & 1);
-                if (elect()) {
-#pragma unroll
-                    for (int kk = 0; kk < KD / 16; ++kk) {
-                        const uint32_t d = (kk >> 2) * 512 + (kk & 3) * 2;
-                        umma_bf16(to, desc(a + d), desc(b + d), id_nk, kk > 0);
-                    }
-                    umma_commit(sy.bar(B_QK + (c & 1)));
-                }
-                __syncwarp();
-            };
-            bool ok = true;
-            if (nt > 0) {
-                ok = sy.warp_wait(B_FULL, 0);
-                tc_fence_after();
-                if (ok) qk(0);
-            }
+            constexpr uint32_t id_o1 = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 0);
 #pragma unroll 1
-            for (int c = 0; c < nt && ok; ++c) {
+            for (int c = 0; c < nt; ++c) {
                 const int s = c % NS, b = c & 1;
                 const uint32_t q = lo_k(sb + s * L::STAGE), v = lo_mn(sb + s * L::STAGE + 2 * L::QB), pb = lo_k(sb + L::P + b * (C * C * 2));
-                // the next chunk's scores as soon as it is loaded, else behind this chunk's products;
-                // the last chunk's P and keys, which waited for this buffer's last scores, are done
-                const bool more = c + 1 < nt;
-                bool next = !more;
-                if (c >= 1 && !sy.warp_wait(B_KD + (b ^ 1), ((c - 1) >> 1) & 1)) break;
-                if (more && __all_sync(0xffffffffu, sy.ready(B_FULL + (c + 1) % NS, ((c + 1) / NS) & 1))) {
-                    tc_fence_after();
-                    qk(c + 1);
-                    next = true;
-                }
                 if (!sy.warp_wait(B_SBF, c & 1)) break;
-                if (c >= 2 && !sy.warp_wait(B_OFREE + b, ((c - 2) >> 1) & 1)) break;
+                if (c >= 1 && !sy.warp_wait(B_OFREE, (c - 1) & 1)) break;  // the output warps have read the last chunk's
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int kk = 0; kk < KD / 16; ++kk)
-                        umma_bf16_ta(tmem + TM_O1 + 64 * b, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_nk, kk > 0);
+                        umma_bf16_ta(tmem + TM_O1, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_o1, kk > 0);
                     umma_commit(sy.bar(B_INTER));
                 }
                 __syncwarp();
                 if (!sy.warp_wait(B_P + b, (c >> 1) & 1)) break;
-                // v's rows behind the sequence are cleared with the last chunk's keys
-                if (!more && !sy.warp_wait(B_KD + b, (c >> 1) & 1)) break;
-                // (O2 has one buffer)
-                if (c >= 1 && !sy.warp_wait(B_OFREE + (b ^ 1), ((c - 1) >> 1) & 1)) break;
+                // v's rows behind the sequence are cleared with the last chunk's scaled values
+                if (c + 1 == nt && !sy.warp_wait(B_VD, c & 1)) break;
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
@@ -486,11 +542,6 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
                 }
                 __syncwarp();
-                if (!next) {
-                    if (!sy.warp_wait(B_FULL + (c + 1) % NS, ((c + 1) / NS) & 1)) break;
-                    tc_fence_after();
-                    qk(c + 1);
-                }
             }
             if (__any_sync(0xffffffffu, sy.aborted())) {
                 if (elect()) {
@@ -615,7 +666,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (l == 0) mbar_arrive(sy.bar(B_OFREE + b));
+                    if (l == 0) mbar_arrive(sy.bar(B_OFREE));
                 };
                 if (!ok) {
                     if (!kStaged) break;
@@ -625,7 +676,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t at = tmem + lane + ((uint32_t)(16 * (x >> 1)) << 16) + 32 * (x & 1);
                         float o1[16], o2[16];
-                        ld16x32(at + TM_O1 + 64 * b, o1);
+                        ld16x32(at + TM_O1, o1);
                         ld16x32(at + TM_O2, o2);
                         if (x < 3) tmem_wait_ld();
                         else taken();
@@ -651,7 +702,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         float o1[16], o2[16];
-                        tmem_ld16(tmem + TM_O1 + 64 * b + lane + 16 * x, o1);
+                        tmem_ld16(tmem + TM_O1 + lane + 16 * x, o1);
                         tmem_ld16(tmem + TM_O2 + lane + 16 * x, o2);
                         if (x < 3) tmem_wait_ld();
                         else taken();
@@ -686,61 +737,80 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (kStaged && tid == 384) bulk_wait();
         }
     } else if (w < 24) {
-        // ------------------------------------------------ scaled keys, three bf16 terms
-        // The first term replaces k (once the scores have read it); the lower two share buffers with
-        // the last chunk's, so they wait for its state product, with the remainders in registers.
-        const int kt = tid - 512;
-        constexpr int NP = C * (KD / 8) / 256;  // 16-byte pieces of a thread; eight lanes cover a row of a 64-channel half
-        auto where = [&](int y) {
-            const int x = kt + 256 * y;
-            return (x >> 9) * 8192u + sw128((x >> 3) & 63, x & 7);
-        };
+        // ------------------------------------------------ scaled values, three bf16 terms
+        // A warp's 32 value channels (its quarter of the lanes) x 32 rows: fragments of 8 x 8 read
+        // transposed, so that a thread has a channel's pairs of consecutive rows, as the products
+        // read them from TMEM.  The terms take the place of the last chunk's, so they wait for its
+        // state product in registers.
+        const int qd = w & 3, jh = (w - 16) >> 2;
+        const bool mine = 32 * qd < VB;
+        // a lane's row of the four 8 x 8 blocks of a load: channels + 0, + 8, rows + 0, + 8
+        const int lrow = 32 * jh + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + ((l >> 3) & 1);
+        const uint32_t to = tmem + TM_VD + ((uint32_t)(32 * qd) << 16) + 16 * jh;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS, len = min(C, eos - (bos + c * C));
-            const uint32_t kb = sb + s * L::STAGE + L::QB, vt = kb + L::QB, gt = gates(c) + GT_KEY;
+            const uint32_t kt = sb + s * L::STAGE + L::QB, vt = kt + L::QB, gt = gates(c) + GT_KEY;
             if (!sy.warp_wait(B_FULL + s, (c / NS) & 1)) break;
-            if (!kStates && !sy.warp_wait(B_QK + (c & 1), (c >> 1) & 1)) break;
-            float2 rest[NP][4];
-#pragma unroll
-            for (int y = 0; y < NP; ++y) {
-                const int row = ((kt + 256 * y) >> 3) & 63;
-                uint32_t kw[4], hi[4];
-                ld_s128(kb + where(y), kw);
-                const float f = lds(gt + 4 * row);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (row >= len) kw[e] = 0;
-                    rest[y][e] = mul2(make_float2(bf_lo(kw[e]), bf_hi(kw[e])), make_float2(f, f));
-                    hi[e] = cut(rest[y][e]);
-                }
-                st_s128(kb + where(y), hi[0], hi[1], hi[2], hi[3]);
+            if (len < C) {  // rows behind the sequence (another one's, or anything), for the products
+                const int x0 = tid - 512;
+                for (int x = x0; x < C * (VB / 8); x += 256)
+                    if (((x >> 3) & 63) >= len) st_s128(vt + (x >> 9) * 8192u + sw128((x >> 3) & 63, x & 7), 0, 0, 0, 0);
+                for (int x = x0; x < C * (KD / 8); x += 256)
+                    if (((x >> 3) & 63) >= len) st_s128(kt + (x >> 9) * 8192u + sw128((x >> 3) & 63, x & 7), 0, 0, 0, 0);
+                fence_proxy_async_smem();
             }
-            if (len < C)  // rows behind the sequence: another one's, or anything
-                for (int x = kt; x < C * (VB / 8); x += 256) {
-                    const int row = (x >> 3) & 63, half = x >> 9, piece = x & 7;
-                    if (row >= len) st_s128(vt + half * 8192u + sw128(row, piece), 0, 0, 0, 0);
+            uint32_t hi[2][8];
+            float2 rest[2][8];
+            if (mine) {
+#pragma unroll
+                for (int g = 0; g < 4; g += 2) {
+                    const float2 f0 = lds2(gt + 4 * (32 * jh + 8 * g + 2 * (l & 3)));
+                    const float2 f1 = lds2(gt + 4 * (32 * jh + 8 * g + 8 + 2 * (l & 3)));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {  // sixteen channels each
+                        uint32_t r[4];
+                        ldmatrix4_t(vt + (qd >> 1) * 8192u + sw128(lrow + 8 * g, lpiece + 2 * y), r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float2& x = rest[y][2 * g + e];
+                            x = mul2(make_float2(bf_lo(r[e]), bf_hi(r[e])), e < 2 ? f0 : f1);
+                            if (len < C) {  // (whether or not the row is cleared yet)
+                                const int j = 32 * jh + 8 * g + (e < 2 ? 0 : 8) + 2 * (l & 3);
+                                if (j >= len) x.x = 0.f;
+                                if (j + 1 >= len) x.y = 0.f;
+                            }
+                            hi[y][2 * g + e] = cut(x);
+                        }
+                    }
                 }
+            }
             if (c > 0 && !sy.warp_wait(B_STATE, (c - 1) & 1)) break;
+            tc_fence_after();
+            if (mine) {
 #pragma unroll
-            for (int y = 0; y < NP; ++y) {
-                uint32_t mid[4], lo[4];
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t at = to + ((uint32_t)(16 * y) << 16);
+                    uint32_t r[8];
+                    st16x16(at, hi[y]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mid[e] = cut(rest[y][e]);
-                    lo[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
+                    for (int e = 0; e < 8; ++e) r[e] = cut(rest[y][e]);
+                    st16x16(at + 32, r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        r[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
+                    st16x16(at + 64, r);
                 }
-                st_s128(sb + L::KM + where(y), mid[0], mid[1], mid[2], mid[3]);
-                st_s128(sb + L::KL + where(y), lo[0], lo[1], lo[2], lo[3]);
+                tmem_wait_st();
             }
-            fence_proxy_async_smem();
+            tc_fence_before();
             __syncwarp();
-            if (l == 0) mbar_arrive(sy.bar(B_KD + (c & 1)));
+            if (l == 0) mbar_arrive(sy.bar(B_VD));
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (w == 3) {
+    if (w == 26) {
         tc_fence_after();
         tmem_dealloc(tmem, TM_COLS);
     }
