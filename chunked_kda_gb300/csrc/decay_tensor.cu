@@ -579,20 +579,28 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // a cut sequence's segments take their incoming states from the scan
         const float* src = kStates ? nullptr : first && last ? (p.h0 ? p.h0 + st : nullptr) : p.ws + sg;
         float* dst = kStates ? p.ws + sg : (last && p.hT) ? p.hT + st : nullptr;
-        if (nt == 0) {  // an empty sequence passes its state through
-            if (dst && mine)
-                for (int j = c0; j < c1; ++j) dst[(size_t)j * p.V] = src ? src[(size_t)j * p.V] : 0.f;
-        } else {
+        // the incoming state, 32 rows in flight; an empty sequence's goes straight on
 #pragma unroll 1
-            for (int x = c0; x < c1; x += 16) {
-                uint32_t r[16];
+        for (int x = c0; x < c1; x += 32) {
+            float v[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) r[j] = (src && mine) ? __float_as_uint(src[(size_t)(x + j) * p.V]) : 0u;
-                __syncwarp();
-                tmem_st16(tmem + TM_S + lane + x, r);
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            if (src && mine) {
+                const float* at = src + (size_t)x * p.V;
+#pragma unroll
+                for (int j = 0; j < 32; ++j, at += p.V) v[j] = *at;
             }
-            tmem_wait_st();
+            __syncwarp();
+            if (nt > 0) {
+                tmem_st16(tmem + TM_S + lane + x, reinterpret_cast<uint32_t*>(v));
+                tmem_st16(tmem + TM_S + lane + x + 16, reinterpret_cast<uint32_t*>(v) + 16);
+            } else if (dst && mine) {
+                float* at = dst + (size_t)x * p.V;
+#pragma unroll
+                for (int j = 0; j < 32; ++j, at += p.V) *at = v[j];
+            }
         }
+        tmem_wait_st();
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
@@ -652,8 +660,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ld32(tmem + TM_S + lane + x, v);
                 tmem_wait_ld();
                 if (dst && mine) {
+                    float* at = dst + (size_t)x * p.V;  // (one address carried on, not 32 kept)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) dst[(size_t)(x + j) * p.V] = v[j] * out;
+                    for (int j = 0; j < 32; ++j, at += p.V) *at = v[j] * out;
                 }
                 __syncwarp();
             }
