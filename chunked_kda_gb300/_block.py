@@ -8,8 +8,6 @@ stream that the kernels run on (torch's current one unless ``stream`` is given).
 """
 from __future__ import annotations
 
-import functools
-
 import torch
 
 import chunked_kda_gb300 as _kda
@@ -32,28 +30,21 @@ def _current_stream(index):
 
 # the handle of torch's current stream without building a Stream object, where torch offers it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_stream(fn):
-    """fn(..., stream=None) with the given stream and the inputs' device made current around it."""
-
-    @functools.wraps(fn)
-    def call(x, *args, stream=None, **kwargs):
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return fn(x, *args, **kwargs)
-        if x.is_cuda and x.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(x.get_device()):
-                return fn(x, *args, **kwargs)
-        return fn(x, *args, **kwargs)
-
-    return call
+def _elsewhere(fn, x, stream, args):
+    """fn's call with the given stream, or with the inputs' device, made current around it."""
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.get_device()):
+        return fn(*args)
 
 
 def _device(x):
+    """The inputs' device, and whether it is the current one."""
     if not x.is_cuda:
         raise ValueError("the inputs must be CUDA tensors")
-    return x.get_device()
+    index = x.get_device()
+    return index, index == _current_device()
 
 
 def _arg(t, name, index, dtype, shape):
@@ -103,15 +94,19 @@ def kda_decay_chunk_workspace_bytes(dtype, B, T, H, K, V, n_seqs=0) -> int:
     return int(_library().kda_decay_chunk_workspace_bytes(_CODES[dtype], B, T, H, K, V, n_seqs))
 
 
-def _decay(chunked, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, o_dtype,
+def _decay(chunked, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, stream, o_dtype,
            workspace=None, status=None):
+    dev, here = _device(q)
+    if stream is not None or not here:
+        return _elsewhere(_decay, q, stream, (chunked, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o,
+                                              final_state, None, o_dtype, workspace, status))
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must have four dimensions [B, T, heads, channels]")
     B, T, Hk, K = shape = q.shape
     H, V = v.shape[2:]
     if Hk < 1 or H % Hk != 0:
         raise ValueError("the q/k heads must divide v's heads")
-    dtype, dt, dev = q.dtype, _code(q, "q"), _device(q)
+    dtype, dt = q.dtype, _code(q, "q")
     out_shape = (B, T, H, V)
     pq, pk = _arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, shape)
     pv = _arg(v, "v", dev, dtype, out_shape)
@@ -121,8 +116,14 @@ def _decay(chunked, q, k, v, decay, initial_state, output_final_state, cu_seqlen
     state_shape = (N, H, K, V)
     p0 = _opt(initial_state, "initial_state", dev, _F32, state_shape)
     if o is None:
-        o = torch.empty_like(v) if o_dtype is None else torch.empty(out_shape, device=v.device, dtype=o_dtype)
-    po, ot = _arg(o, "o", dev, o.dtype, out_shape), _code(o, "o")
+        if o_dtype is None:
+            o, ot = torch.empty_like(v), dt
+        else:
+            o = torch.empty(out_shape, device=v.device, dtype=o_dtype)
+            ot = _code(o, "o")
+        po = o.data_ptr()
+    else:
+        po, ot = _arg(o, "o", dev, o.dtype, out_shape), _code(o, "o")
     if final_state is None:
         p1 = None
         if output_final_state:
@@ -154,9 +155,8 @@ def _decay(chunked, q, k, v, decay, initial_state, output_final_state, cu_seqlen
     return o, final_state
 
 
-@_on_stream
 def kda_decay_chunk_fwd(q, k, v, decay, initial_state=None, output_final_state=False, cu_seqlens=None, o=None,
-                        final_state=None, workspace=None, o_dtype=None, status=None):
+                        final_state=None, workspace=None, stream=None, o_dtype=None, status=None):
     """Linear attention with a decay for each head, in chunks (prompts); (o, final_state or None).
 
         S_t = exp(decay_t) S_{t-1} + k_t v_t^T;   o_t = S_t^T q_t / sqrt(K)
@@ -165,40 +165,43 @@ def kda_decay_chunk_fwd(q, k, v, decay, initial_state=None, output_final_state=F
     natural log, [B, T, H] or [H]; states float32 [N, H, K, V].  ``o_dtype`` is q's dtype or
     torch.float32.  Packed sequences, in-place states, ``workspace``, ``status`` and ``stream`` as
     for kda_chunk_fwd."""
-    return _decay(True, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, o_dtype,
+    return _decay(True, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, stream, o_dtype,
                   workspace, status)
 
 
-@_on_stream
 def kda_decay_recurrent_fwd(q, k, v, decay, initial_state=None, output_final_state=False, cu_seqlens=None,
-                            o=None, final_state=None, o_dtype=None):
+                            o=None, final_state=None, stream=None, o_dtype=None):
     """kda_decay_chunk_fwd's function token by token in float32 (single tokens; ``final_state`` may
     be ``initial_state``)."""
-    return _decay(False, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, o_dtype)
+    return _decay(False, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, stream, o_dtype)
 
 
-@_on_stream
-def kda_gated_norm_fwd(x, gate, weight=None, eps=1e-6, act=_kda.ACT_SIGMOID, out=None):
+def kda_gated_norm_fwd(x, gate, weight=None, eps=1e-6, act=_kda.ACT_SIGMOID, out=None, stream=None):
     """y = x / sqrt(mean(x^2) + eps) * weight * act(gate) over the last dimension (one head's channels).
 
     x and gate of one shape and dtype (float32 or bfloat16), weight float32 [V] or None; ``out`` may
     be x or gate."""
-    shape, dtype, dt, dev = x.shape, x.dtype, _code(x, "x"), _device(x)
+    dev, here = _device(x)
+    if stream is not None or not here:
+        return _elsewhere(kda_gated_norm_fwd, x, stream, (x, gate, weight, eps, act, out))
+    shape, dtype, dt = x.shape, x.dtype, _code(x, "x")
     V = shape[-1]
     px, pg = _arg(x, "x", dev, dtype, shape), _arg(gate, "gate", dev, dtype, shape)
     pw = _opt(weight, "weight", dev, _F32, (V,))
     if out is None:
         out = torch.empty_like(x)
-    py = _arg(out, "out", dev, dtype, shape)
+        py = out.data_ptr()
+    else:
+        py = _arg(out, "out", dev, dtype, shape)
     code = _library().kda_gated_norm_fwd(px, pg, dt, pw, eps, act, x.numel() // V if V else 0, V, py, _raw_stream(dev))
     if code:
         _kda._check("kda_gated_norm_fwd", code)
     return out
 
 
-@_on_stream
 def kda_block_norm_fwd(x, residual=None, post_weight=None, gate=None, pre_weight=None, scale=1.0,
-                       channel_scale=None, eps=1e-6, act=_kda.ACT_SIGMOID, out=None, residual_out=None):
+                       channel_scale=None, eps=1e-6, act=_kda.ACT_SIGMOID, out=None, residual_out=None,
+                       stream=None):
     """The norm around a block over the last dimension; returns (h, y).
 
         n = x [/ sqrt(mean(x^2) + eps) * post_weight] [* act(gate)]
@@ -208,7 +211,11 @@ def kda_block_norm_fwd(x, residual=None, post_weight=None, gate=None, pre_weight
     Each bracket is there when its tensor is given.  x, gate and y share a dtype, residual and h
     another (float32 or bfloat16 each; x's when there is no residual); weights and channel_scale
     are float32 [D].  ``residual_out`` (h) may be ``residual``."""
-    shape, dtype, dt, dev = x.shape, x.dtype, _code(x, "x"), _device(x)
+    dev, here = _device(x)
+    if stream is not None or not here:
+        return _elsewhere(kda_block_norm_fwd, x, stream, (x, residual, post_weight, gate, pre_weight, scale, channel_scale,
+                                                          eps, act, out, residual_out))
+    shape, dtype, dt = x.shape, x.dtype, _code(x, "x")
     D = shape[-1]
     per = (D,)
     like = residual if residual is not None else residual_out if residual_out is not None else x
@@ -219,9 +226,14 @@ def kda_block_norm_fwd(x, residual=None, post_weight=None, gate=None, pre_weight
     pc = _opt(channel_scale, "channel_scale", dev, _F32, per)
     if residual_out is None:
         residual_out = torch.empty_like(like)
+        ph = residual_out.data_ptr()
+    else:
+        ph = pr if residual_out is residual else _arg(residual_out, "residual_out", dev, like.dtype, shape)
     if out is None:
         out = torch.empty_like(x)
-    ph, py = _arg(residual_out, "residual_out", dev, like.dtype, shape), _arg(out, "out", dev, dtype, shape)
+        py = out.data_ptr()
+    else:
+        py = _arg(out, "out", dev, dtype, shape)
     code = _library().kda_block_norm_fwd(px, dt, pr, rt, pp, pg, act, scale, pc, pn, eps, x.numel() // D if D else 0, D,
                                          ph, py, _raw_stream(dev))
     if code:
@@ -229,9 +241,8 @@ def kda_block_norm_fwd(x, residual=None, post_weight=None, gate=None, pre_weight
     return residual_out, out
 
 
-@_on_stream
 def kda_short_conv_fwd(x, weight, bias=None, act=_kda.ACT_SILU, initial_state=None, output_final_state=False,
-                       cu_seqlens=None, out=None, final_state=None):
+                       cu_seqlens=None, out=None, final_state=None, stream=None):
     """Causal convolution of each channel over its last W tokens; returns (y, final_state or None).
 
         y_t[d] = act(bias[d] + sum_w weight[d, w] x_{t-W+1+w}[d])
@@ -239,10 +250,14 @@ def kda_short_conv_fwd(x, weight, bias=None, act=_kda.ACT_SILU, initial_state=No
     x [B, T, D] (float32 or bfloat16), weight float32 [D, W] with 2 <= W <= 8, bias float32 [D] or
     None; states [N, W - 1, D] in x's dtype hold the last W - 1 inputs, the oldest first, and
     ``final_state`` may be ``initial_state``."""
+    dev, here = _device(x)
+    if stream is not None or not here:
+        return _elsewhere(kda_short_conv_fwd, x, stream, (x, weight, bias, act, initial_state, output_final_state,
+                                                          cu_seqlens, out, final_state))
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [B, T, D] and weight [D, W]")
     B, T, D = shape = x.shape
-    W, dtype, dt, dev = weight.shape[1], x.dtype, _code(x, "x"), _device(x)
+    W, dtype, dt = weight.shape[1], x.dtype, _code(x, "x")
     px, pw = _arg(x, "x", dev, dtype, shape), _arg(weight, "weight", dev, _F32, (D, W))
     pb = _opt(bias, "bias", dev, _F32, (D,))
     pcu, n_seqs, N = _packed(cu_seqlens, B, dev)
@@ -250,7 +265,9 @@ def kda_short_conv_fwd(x, weight, bias=None, act=_kda.ACT_SILU, initial_state=No
     p0 = _opt(initial_state, "initial_state", dev, dtype, state_shape)
     if out is None:
         out = torch.empty_like(x)
-    py = _arg(out, "out", dev, dtype, shape)
+        py = out.data_ptr()
+    else:
+        py = _arg(out, "out", dev, dtype, shape)
     if final_state is None and output_final_state:
         final_state = torch.empty(state_shape, device=x.device, dtype=dtype)
     p1 = p0 if final_state is initial_state else _opt(final_state, "final_state", dev, dtype, state_shape)

@@ -100,16 +100,12 @@ def test_the_binding_refuses_what_it_can_see():
         kda.kda_decay_chunk_fwd(q, q, v, a)
     with pytest.raises(ValueError, match="CUDA"):
         kda.kda_gated_norm_fwd(v, v)
-    with pytest.raises(ValueError, match="heads"):
-        kda.kda_decay_recurrent_fwd(torch.zeros(1, 8, 3, 64), torch.zeros(1, 8, 3, 64), v, a)
-    with pytest.raises(ValueError, match="four dimensions"):
-        kda.kda_decay_recurrent_fwd(q[0], q[0], v[0], a)
-    with pytest.raises(TypeError, match="float16"):
-        kda.kda_gated_norm_fwd(v.half(), v.half())
-    with pytest.raises(TypeError, match="float64"):
-        kda.kda_block_norm_fwd(v.double())
-    with pytest.raises(ValueError, match=r"\[B, T, D\]"):
-        kda.kda_short_conv_fwd(q, torch.zeros(64, 4))
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.kda_decay_recurrent_fwd(q, q, v, a)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.kda_block_norm_fwd(v)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.kda_short_conv_fwd(v[0], torch.zeros(64, 4))
 
 
 def test_prototypes_match_the_header():

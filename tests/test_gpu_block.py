@@ -310,3 +310,63 @@ def test_conv_packed(kda, edges, inplace):
 def test_conv_without_state(kda):
     check_conv(kda, BF, 10, 128, 4, state=False)
     check_conv(kda, BF, 40, 128, 4, edges=[0, 2, 2, 38], state=False)
+
+
+# ------------------------------------------------------------------ the binding's checks
+
+def test_the_binding_refuses_what_it_can_see(kda):
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    q, v, a = z(1, 8, 2, 64), z(1, 8, 4, 64), z(1, 8, 4)
+    bad = [
+        (ValueError, "heads", lambda: kda.kda_decay_recurrent_fwd(z(1, 8, 3, 64), z(1, 8, 3, 64), v, a)),
+        (ValueError, "four dimensions", lambda: kda.kda_decay_chunk_fwd(q[0], q[0], v[0], a)),
+        (ValueError, "decay must have shape", lambda: kda.kda_decay_chunk_fwd(q, q, v, z(1, 8, 2))),
+        (TypeError, "decay", lambda: kda.kda_decay_chunk_fwd(q, q, v, a.bfloat16())),
+        (TypeError, "v must be", lambda: kda.kda_decay_chunk_fwd(q, q, v.bfloat16(), a)),
+        (ValueError, "contiguous", lambda: kda.kda_decay_chunk_fwd(q, z(1, 2, 8, 64).transpose(1, 2), v, a)),
+        (ValueError, "initial_state", lambda: kda.kda_decay_chunk_fwd(q, q, v, a, initial_state=z(1, 4, 64, 32))),
+        (ValueError, "CUDA", lambda: kda.kda_decay_chunk_fwd(q, q, v, a.cpu())),
+        (ValueError, "requires grad", lambda: kda.kda_decay_chunk_fwd(q, q, v.clone().requires_grad_(), a)),
+        (ValueError, "B == 1", lambda: kda.kda_decay_chunk_fwd(z(2, 8, 2, 64), z(2, 8, 2, 64), z(2, 8, 4, 64), z(2, 8, 4),
+                                                               cu_seqlens=z(2, dtype=torch.int32))),
+        (TypeError, "cu_seqlens", lambda: kda.kda_decay_chunk_fwd(q, q, v, a, cu_seqlens=z(2, dtype=torch.int64))),
+        (TypeError, "float16", lambda: kda.kda_gated_norm_fwd(v.half(), v.half())),
+        (ValueError, "gate must have shape", lambda: kda.kda_gated_norm_fwd(v, q)),
+        (TypeError, "weight", lambda: kda.kda_gated_norm_fwd(v, v, z(64, dtype=torch.bfloat16))),
+        (TypeError, "float64", lambda: kda.kda_block_norm_fwd(v.double())),
+        (ValueError, "residual must have shape", lambda: kda.kda_block_norm_fwd(v, residual=q)),
+        (ValueError, r"\[B, T, D\]", lambda: kda.kda_short_conv_fwd(q, z(64, 4))),
+        (ValueError, "weight must have shape", lambda: kda.kda_short_conv_fwd(v[0], z(63, 4))),
+        (ValueError, "initial_state must have shape", lambda: kda.kda_short_conv_fwd(v[0], z(64, 4), initial_state=z(8, 4, 64))),
+    ]
+    for kind, words, call in bad:
+        with pytest.raises(kind, match=words):
+            call()
+    with pytest.raises(kda.KdaError, match="W must be"):
+        kda.kda_short_conv_fwd(v[0], z(64, 9))
+    with pytest.raises(kda.KdaError, match="aligned"):
+        kda.kda_gated_norm_fwd(z(129)[1:].view(1, 128), z(1, 128))
+    with pytest.raises(kda.KdaError, match="workspace"):
+        big = z(1, 4096, 1, 128, dtype=torch.bfloat16)
+        kda.kda_decay_chunk_fwd(big, big, big, z(1, 4096, 1), workspace=z(256, dtype=torch.uint8))
+
+
+def test_a_wait_that_gives_up_is_reported(kda):
+    """The tensor-core kernel's waits are bounded: a forced give-up sets the status word, is counted,
+    and leaves the context usable."""
+    x = [dev(t) for t in inputs(3, 1, 700, 4, 4, 128, 128, BF, 1)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_fused_wait_timeouts(reset=True)
+    try:
+        for chunk in (0, 1, 3):  # (a segment here has four)
+            kda.kda_test_hooks(wait_timeout_chunk=chunk)
+            status.zero_()
+            kda.kda_decay_chunk_fwd(*x[:4], initial_state=x[4], output_final_state=True, status=status)
+            torch.cuda.synchronize()
+            assert int(status) == 1
+            assert kda.kda_fused_wait_timeouts(reset=True) > 0
+    finally:
+        kda.kda_test_hooks()
+    status.zero_()
+    check(kda, "kda_decay_chunk_fwd", inputs(3, 1, 700, 4, 4, 128, 128, BF, 1))
+    assert int(status) == 0 and kda.kda_fused_wait_timeouts() == 0
