@@ -49,6 +49,48 @@ __device__ __forceinline__ void chunk_gates(const SimtArgs& p, int h, int t0, in
     __syncthreads();
 }
 
+// four consecutive elements of a row of n, the first at c (0 behind the row)
+template <typename T>
+__device__ __forceinline__ void load4(const T* row, int c, int n, float (&r)[4]) {
+    if (n % 4 == 0) {
+        if (c >= n) {
+            r[0] = r[1] = r[2] = r[3] = 0.f;
+        } else if constexpr (sizeof(T) == 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(row + c));
+            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + c));
+            r[0] = sm100::bf_lo(v.x); r[1] = sm100::bf_hi(v.x); r[2] = sm100::bf_lo(v.y); r[3] = sm100::bf_hi(v.y);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = c + e < n ? to_f32(row[c + e]) : 0.f;
+    }
+}
+// [64 rows][nc channels from c0] of q or k, transposed: lanes are rows, so that the stores meet no bank twice
+template <typename T>
+__device__ __forceinline__ void load_transposed(const T* base, size_t stride, int len, int c0, int nc, int n, float* out) {
+    for (int x = threadIdx.x; x < C * (nc / 4); x += NT) {
+        const int i = x & 63, c = 4 * (x >> 6);
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+        if (i < len) load4(base + i * stride, c0 + c, n, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(c + e) * LD + i] = r[e];
+    }
+}
+// [rows][64 columns from c0], as it is, each row times its factor
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* base, size_t stride, int rows, int len, int c0, int n, const float* f, float* out) {
+    for (int x = threadIdx.x; x < rows * 16; x += NT) {
+        const int j = x >> 4, c = 4 * (x & 15);
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j < len) load4(base + j * stride, c0 + c, n, r);
+        const float g = f ? f[j] : 1.f;
+        *reinterpret_cast<float4*>(out + j * LD + c) = f && j >= len ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                                     : make_float4(r[0] * g, r[1] * g, r[2] * g, r[3] * g);
+    }
+}
+
 // acc[i][j] += sum_{x < n} A[x][4 ti + i] B[x][4 tj + j]
 __device__ __forceinline__ void tile_product(const float* A, const float* B, int n, int ti, int tj, float (&acc)[4][4]) {
 #pragma unroll 8
@@ -66,7 +108,8 @@ __device__ __forceinline__ void tile_product(const float* A, const float* B, int
 // grid (slots, H, K blocks x V blocks of 64)
 template <typename T>
 __global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, const T* __restrict__ v, SimtArgs p) {
-    __shared__ float sk[C * LD], sv[C * LD];
+    __shared__ __align__(16) float sk[C * LD], sv[C * LD];
+    __shared__ float sf[C];
     __shared__ int sI[3][C];
     int n, t0, len, bos, eos;
     if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
@@ -76,17 +119,10 @@ __global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, 
     chunk_gates(p, h, t0, len, sI);
     const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
     const int Hk = p.H / p.hr, hq = h / p.hr;
-    for (int x = tid; x < C * 64; x += NT) {
-        const int j = x >> 6, c = x & 63;
-        float kk = 0.f, vv = 0.f;
-        if (j < len) {
-            const float f = pow2(sI[0][C - 1] - sI[0][j], sI[1][C - 1] - sI[1][j]) + poison;
-            if (c0 + c < p.K) kk = to_f32(k[((size_t)(t0 + j) * Hk + hq) * p.K + c0 + c]) * f;
-            if (d0 + c < p.V) vv = to_f32(v[((size_t)(t0 + j) * p.H + h) * p.V + d0 + c]);
-        }
-        sk[j * LD + c] = kk;
-        sv[j * LD + c] = vv;
-    }
+    if (tid < C) sf[tid] = pow2(sI[0][C - 1] - sI[0][tid], sI[1][C - 1] - sI[1][tid]) + poison;
+    __syncthreads();
+    load_rows(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, C, len, c0, p.K, sf, sk);
+    load_rows(v + ((size_t)t0 * p.H + h) * p.V, (size_t)p.H * p.V, C, len, d0, p.V, nullptr, sv);
     __syncthreads();
     const int ti = tid >> 4, tj = tid & 15;
     float acc[4][4] = {};
@@ -138,7 +174,7 @@ __global__ void __launch_bounds__(NT) decay_chunk_scan_kernel(SimtArgs p) {
 template <typename T, typename OT>
 __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, OT* __restrict__ o, SimtArgs p) {
-    extern __shared__ float sm[];
+    extern __shared__ __align__(16) float sm[];
     const int Kp = (p.K + 31) / 32 * 32;
     float* sq = sm;               // [Kp][LD] q, transposed
     float* sp = sq + Kp * LD;     // [64][LD] P, transposed
@@ -151,18 +187,12 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
     const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
     const int Hk = p.H / p.hr, hq = h / p.hr;
     const float scale = rsqrtf((float)p.K);
-    for (int x = tid; x < C * Kp; x += NT) {
-        const int i = x / Kp, c = x - i * Kp;
-        sq[c * LD + i] = i < len && c < p.K ? to_f32(q[((size_t)(t0 + i) * Hk + hq) * p.K + c]) : 0.f;
-    }
+    load_transposed(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sq);
     {
         float acc[4][4] = {};
         for (int c0 = 0; c0 < Kp; c0 += 32) {
             __syncthreads();
-            for (int x = tid; x < C * 32; x += NT) {
-                const int j = x >> 5, c = x & 31;
-                sx[c * LD + j] = j < len && c0 + c < p.K ? to_f32(k[((size_t)(t0 + j) * Hk + hq) * p.K + c0 + c]) : 0.f;
-            }
+            load_transposed(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, c0, 32, p.K, sx);
             __syncthreads();
             tile_product(sq + c0 * LD, sx, 32, ti, tj, acc);
         }
@@ -181,10 +211,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
         float acc[4][4] = {};
         for (int c0 = 0; c0 < Kp; c0 += 32) {
             __syncthreads();
-            for (int x = tid; x < 32 * 64; x += NT) {
-                const int c = x >> 6, d = x & 63;
-                sx[c * LD + d] = c0 + c < p.K && d0 + d < p.V ? S[(size_t)(c0 + c) * p.V + d0 + d] : 0.f;
-            }
+            load_rows(S + (size_t)c0 * p.V, p.V, 32, p.K - c0, d0, p.V, nullptr, sx);
             __syncthreads();
             tile_product(sq + c0 * LD, sx, 32, ti, tj, acc);
         }
@@ -196,10 +223,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
         }
         for (int j0 = 0; j0 < C; j0 += 32) {
             __syncthreads();
-            for (int x = tid; x < 32 * 64; x += NT) {
-                const int j = x >> 6, d = x & 63;
-                sx[j * LD + d] = j0 + j < len && d0 + d < p.V ? to_f32(v[((size_t)(t0 + j0 + j) * p.H + h) * p.V + d0 + d]) : 0.f;
-            }
+            load_rows(v + ((size_t)(t0 + j0) * p.H + h) * p.V, (size_t)p.H * p.V, 32, len - j0, d0, p.V, nullptr, sx);
             __syncthreads();
             tile_product(sp + j0 * LD, sx, 32, ti, tj, acc);
         }
