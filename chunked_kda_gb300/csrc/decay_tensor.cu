@@ -80,6 +80,7 @@ struct Params {
     const int32_t* cu;
     void* o;
     int N, T, H, hr, K, V;
+    int k0;         // this launch's first key channel (a head of 256 takes two launches of 128)
     int seg;        // tokens of a segment (a multiple of C), 0: whole sequences
     float* ws;      // segment states [slot][h][K][V]
     float* wdec;    // segment decays [slot][h]
@@ -446,8 +447,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mbar_arrive_expect_tx(full, (kStates ? L::QB : 2 * L::QB) + L::VBYTES);
 #pragma unroll
                     for (int x = 0; x < KD / 64; ++x) {
-                        if constexpr (!kStates) tma_load_3d(st + x * 8192, &tm_q, 64 * x, hq, t0, full);
-                        tma_load_3d(st + L::QB + x * 8192, &tm_k, 64 * x, hq, t0, full);
+                        if constexpr (!kStates) tma_load_3d(st + x * 8192, &tm_q, p.k0 + 64 * x, hq, t0, full);
+                        tma_load_3d(st + L::QB + x * 8192, &tm_k, p.k0 + 64 * x, hq, t0, full);
                     }
 #pragma unroll
                     for (int x = 0; x < VB / 64; ++x) tma_load_3d(st + 2 * L::QB + x * 8192, &tm_v, vc0 + 64 * x, h, t0, full);
@@ -456,8 +457,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (c + kAhead < nt) {
 #pragma unroll
                         for (int x = 0; x < KD / 64; ++x) {
-                            if constexpr (!kStates) tma_prefetch_l2_3d(&tm_q, 64 * x, hq, t0 + kAhead * C);
-                            tma_prefetch_l2_3d(&tm_k, 64 * x, hq, t0 + kAhead * C);
+                            if constexpr (!kStates) tma_prefetch_l2_3d(&tm_q, p.k0 + 64 * x, hq, t0 + kAhead * C);
+                            tma_prefetch_l2_3d(&tm_k, p.k0 + 64 * x, hq, t0 + kAhead * C);
                         }
 #pragma unroll
                         for (int x = 0; x < VB / 64; ++x) tma_prefetch_l2_3d(&tm_v, vc0 + 64 * x, h, t0 + kAhead * C);
@@ -574,8 +575,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t lane = (uint32_t)(32 * (w & 3)) << 16;
         const int c0 = w < 8 ? 0 : KD / 2, c1 = c0 + KD / 2;  // this warp's key channels
         const bool mine = vl < VB && vc0 + vl < p.V;
-        const size_t st = ((size_t)n * p.H + h) * (size_t)p.K * p.V + vc0 + vl;
-        const size_t sg = ((size_t)slot * p.H + h) * (size_t)p.K * p.V + vc0 + vl;
+        const size_t at = (size_t)p.k0 * p.V + vc0 + vl, st = ((size_t)n * p.H + h) * (size_t)p.K * p.V + at;
+        const size_t sg = ((size_t)slot * p.H + h) * (size_t)p.K * p.V + at;
         // a cut sequence's segments take their incoming states from the scan
         const float* src = kStates ? nullptr : first && last ? (p.h0 ? p.h0 + st : nullptr) : p.ws + sg;
         float* dst = kStates ? p.ws + sg : (last && p.hT) ? p.hT + st : nullptr;
@@ -586,18 +587,18 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
             if (src && mine) {
-                const float* at = src + (size_t)x * p.V;
+                const float* from = src + (size_t)x * p.V;
 #pragma unroll
-                for (int j = 0; j < 32; ++j, at += p.V) v[j] = *at;
+                for (int j = 0; j < 32; ++j, from += p.V) v[j] = *from;
             }
             __syncwarp();
             if (nt > 0) {
                 tmem_st16(tmem + TM_S + lane + x, reinterpret_cast<uint32_t*>(v));
                 tmem_st16(tmem + TM_S + lane + x + 16, reinterpret_cast<uint32_t*>(v) + 16);
             } else if (dst && mine) {
-                float* at = dst + (size_t)x * p.V;
+                float* to = dst + (size_t)x * p.V;
 #pragma unroll
-                for (int j = 0; j < 32; ++j, at += p.V) *at = v[j];
+                for (int j = 0; j < 32; ++j, to += p.V) *to = v[j];
             }
         }
         tmem_wait_st();
@@ -660,9 +661,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ld32(tmem + TM_S + lane + x, v);
                 tmem_wait_ld();
                 if (dst && mine) {
-                    float* at = dst + (size_t)x * p.V;  // (one address carried on, not 32 kept)
+                    float* to = dst + (size_t)x * p.V;  // (one address carried on, not 32 kept)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, at += p.V) *at = v[j] * out;
+                    for (int j = 0; j < 32; ++j, to += p.V) *to = v[j] * out;
                 }
                 __syncwarp();
             }
@@ -873,6 +874,20 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const float* __restrict
     }
 }
 
+// A head of 256 key channels is the sum of two of 128 (scores, outputs and states all split that way):
+// their FP32 outputs added and rounded once.
+template <typename OT>
+__global__ void __launch_bounds__(256) decay_join_kernel(const float* __restrict__ a, const float* __restrict__ b,
+                                                         OT* __restrict__ o, long rows, const int32_t* end, long row4) {
+    const long n4 = (end ? (long)__ldg(end) : rows) * row4;  // (rows behind a packed batch's last sequence stay as they are)
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long)gridDim.x * 256) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(a) + i), y = __ldcs(reinterpret_cast<const float4*>(b) + i);
+        const float r[4] = {x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w};
+        if constexpr (sizeof(OT) == 4) reinterpret_cast<float4*>(o)[i] = make_float4(r[0], r[1], r[2], r[3]);
+        else reinterpret_cast<uint2*>(o)[i] = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
+    }
+}
+
 // ------------------------------------------------------------------ host side
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -920,66 +935,82 @@ int plan_segment(int B, int T, int H, int vblocks, int N, bool packed) {
 
 struct Plan {
     int seg, slots;
-    size_t states, bytes;
+    size_t states, half, bytes;  // the segments' states; one of the two outputs of a head of 256; in all
 };
 Plan plan(int B, int T, int H, int K, int V, int N, bool packed) {
-    Plan pl{0, N, 0, 0};
+    Plan pl{0, N, 0, 0, 0};
     const int vblocks = V > 128 ? 2 : 1;
     pl.seg = plan_segment(B, T, H, vblocks, N, packed);
-    if (pl.seg == 0) return pl;
-    pl.slots = packed ? T / pl.seg + N + 1 : N * ((T + pl.seg - 1) / pl.seg);
-    pl.states = (size_t)pl.slots * H * K * V * sizeof(float);
-    pl.bytes = pl.states + ((size_t)pl.slots * H * sizeof(float) + 255) / 256 * 256;
+    if (pl.seg) {
+        pl.slots = packed ? T / pl.seg + N + 1 : N * ((T + pl.seg - 1) / pl.seg);
+        pl.states = (size_t)pl.slots * H * K * V * sizeof(float);
+        pl.bytes = pl.states + ((size_t)pl.slots * H * sizeof(float) + 255) / 256 * 256;
+    }
+    if (K == 256) {
+        pl.half = ((size_t)B * T * H * V * sizeof(float) + 255) / 256 * 256;
+        pl.bytes += 2 * pl.half;
+    }
     return pl;
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel kern, uint32_t bytes, dim3 grid, cudaStream_t stream, const CUtensorMap (&m)[4], const Params& p) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, NTHR, bytes, stream>>>(m[0], m[1], m[2], m[3], p);
+    return cudaGetLastError();
 }
 
 template <int KD, int VB, typename OT>
 cudaError_t run(const DecayArgs& a) {
     using L = Layout<KD, VB>;
-    CUtensorMap mq, mk, mv, mo;  // (mo is a stand-in for a float32 o, which leaves by plain stores)
+    CUtensorMap m[4];  // q, k, v, o (a stand-in for a float32 o, which leaves by plain stores)
     const long tokens = (long)a.B * a.T;
-    if (tokens == 0) {  // nothing to load; the maps are never used
-        if (!a.hT) return cudaSuccess;
-    }
-    const void* some = a.hT;
-    if (!make_map(&mq, tokens ? a.q : some, tokens ? tokens : 1, a.Hk, KD) ||
-        !make_map(&mk, tokens ? a.k : some, tokens ? tokens : 1, a.Hk, KD) ||
-        !make_map(&mv, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V) ||
-        !make_map(&mo, tokens && !a.o_f32 ? a.o : tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
+    if (tokens == 0 && !a.hT) return cudaSuccess;
+    const void* some = a.hT;  // nothing to load: the maps are never used
+    if (!make_map(m, tokens ? a.q : some, tokens ? tokens : 1, a.Hk, a.K) ||
+        !make_map(m + 1, tokens ? a.k : some, tokens ? tokens : 1, a.Hk, a.K) ||
+        !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V) ||
+        !make_map(m + 3, tokens && !a.o_f32 ? a.o : tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
         return cudaErrorInvalidValue;
     const Plan pl = plan(a.B, a.T, a.H, a.K, a.V, a.N, a.cu != nullptr);
-    Params p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, pl.seg,
-             (float*)a.ws, (float*)((char*)a.ws + pl.states), a.status, hook_stall_chunk()};
+    char* ws = (char*)a.ws;
+    Params p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, 0, pl.seg,
+             (float*)ws, (float*)(ws + pl.states), a.status, hook_stall_chunk()};
     const dim3 grid(a.H, (a.V + VB - 1) / VB, pl.slots);
     cudaError_t e;
     if (pl.seg) {
-        auto states = decay_chunk_kernel<KD, VB, __nv_bfloat16, true>;
-        e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-        if (e != cudaSuccess) return e;
-        states<<<grid, NTHR, L::BYTES, a.stream>>>(mq, mk, mv, mo, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        for (p.k0 = 0; p.k0 < a.K; p.k0 += KD)
+            if ((e = launch(decay_chunk_kernel<KD, VB, __nv_bfloat16, true>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess)
+                return e;
         const int KV = a.K * a.V;
         decay_scan_kernel<<<dim3((KV / 4 + 255) / 256, a.H, a.N), 256, 0, a.stream>>>(
             a.h0, p.ws, p.wdec, ChunkMap{a.cu, a.N, a.T, pl.seg}, a.H, KV);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    auto kern = decay_chunk_kernel<KD, VB, OT, false>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-    if (e != cudaSuccess) return e;
-    kern<<<grid, NTHR, L::BYTES, a.stream>>>(mq, mk, mv, mo, p);
+    p.k0 = 0;
+    if (a.K == KD) return launch(decay_chunk_kernel<KD, VB, OT, false>, L::BYTES, grid, a.stream, m, p);
+    float* half = (float*)(ws + pl.bytes - 2 * pl.half);
+    for (; p.k0 < a.K; p.k0 += KD) {
+        p.o = p.k0 == 0 ? half : half + pl.half / sizeof(float);
+        if ((e = launch(decay_chunk_kernel<KD, VB, float, false>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess) return e;
+    }
+    if (tokens == 0) return cudaSuccess;
+    decay_join_kernel<OT><<<1216, 256, 0, a.stream>>>(half, half + pl.half / sizeof(float), (OT*)a.o, tokens,
+                                                      a.cu ? a.cu + a.N : nullptr, (long)a.H * a.V / 4);
     return cudaGetLastError();
 }
 
 template <typename OT>
 cudaError_t run_dims(const DecayArgs& a) {
     if (a.K == 64) return a.V == 64 ? run<64, 64, OT>(a) : run<64, 128, OT>(a);
-    return a.V == 64 ? run<128, 64, OT>(a) : run<128, 128, OT>(a);
+    return a.V == 64 ? run<128, 64, OT>(a) : run<128, 128, OT>(a);  // (K = 256 in two halves)
 }
 
 }  // namespace decay
 
 bool decay_tensor_dims(bool bf16, int K, int V) {
-    return bf16 && (K == 64 || K == 128) && (V == 64 || V == 128 || V == 256);
+    return bf16 && (K == 64 || K == 128 || K == 256) && (V == 64 || V == 128 || V == 256);
 }
 
 size_t decay_tensor_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed) {

@@ -145,7 +145,7 @@ struct ConvArgs {
 cudaError_t launch_decay_recurrent(const DecayArgs& a);
 size_t decay_chunk_workspace_bytes(bool qkv_bf16, int B, int T, int H, int K, int V, int N, bool packed);
 cudaError_t launch_decay_chunk(const DecayArgs& a);
-// its tensor-core kernels: bf16, K 64 or 128, V 64, 128 or 256
+// its tensor-core kernels: bf16, K and V of 64, 128 or 256
 bool decay_tensor_dims(bool qkv_bf16, int K, int V);
 size_t decay_tensor_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed);
 cudaError_t launch_decay_tensor(const DecayArgs& a);
