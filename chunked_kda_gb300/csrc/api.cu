@@ -177,13 +177,15 @@ kda_status kda_test_hooks(int wait_timeout_chunk, int sm_count, int one_launch, 
 kda_status kda_fused_wait_timeouts(unsigned int* count, int reset) {
     g_last_error.clear();
     if (!count) return fail(KDA_ERR_INVALID_ARG, "null count");
-    unsigned a = 0, b = 0, c = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0;
     kda_status st = cuda_status(kda::read_fused_timeouts(&a, reset != 0));
     if (st != KDA_OK) return st;
     st = cuda_status(kda::read_twopass_timeouts(&b, reset != 0));
     if (st != KDA_OK) return st;
     st = cuda_status(kda::read_decay_timeouts(&c, reset != 0));
-    *count = a + b + c;
+    if (st != KDA_OK) return st;
+    st = cuda_status(kda::read_norm_timeouts(&d, reset != 0));
+    *count = a + b + c + d;
     return st;
 }
 

@@ -10,6 +10,7 @@
 // from h before its rounding.
 #include "common.cuh"
 #include "kda_internal.h"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
@@ -65,6 +66,26 @@ __device__ __forceinline__ void store_e(T* p, const float* r) {
     else {
 #pragma unroll
         for (int i = 0; i < E; i += Vec<T>::N) Vec<T>::store(p + i, r + i);
+    }
+}
+
+// 8 consecutive elements in shared memory
+template <typename T>
+__device__ __forceinline__ void load_s(const T* p, float* r) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
+        }
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[2 * e] = __uint_as_float(w[e] << 16);
+            r[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
     }
 }
 
@@ -163,7 +184,7 @@ __device__ __forceinline__ float block_sum(float s, float* red) {
 }
 
 // E elements of h (before the residual where there is one) from x
-template <typename T, int E>
+template <typename T, int E, bool kShared = false>
 __device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c, float rs, float* h) {
     float t[E];
     if (a.post_w) {
@@ -172,7 +193,8 @@ __device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c
         for (int i = 0; i < E; ++i) h[i] = h[i] * rs * t[i];
     }
     if (z) {
-        load_e<T, E>(z + c, t);
+        if constexpr (kShared) load_s<T>(z + c, t);
+        else load_e<T, E>(z + c, t);
 #pragma unroll
         for (int i = 0; i < E; ++i) h[i] *= gate_value<T>(t[i], a.act);
     }
@@ -245,6 +267,111 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(BlockNormArgs a) {
     }
 }
 
+// Many long rows: two blocks stay on each SM and take every gridDim.x-th row, the rows after the one in
+// work on their way into shared memory (bulk copies, a ring of `stages` rows), so that no load waits
+// for the two sums of the row before it.  16384 rows of 8192 (bf16, float32 stream; 1.61 GB) in 245 us,
+// 6.6 TB/s, against the 278 us of a block per row.  One block of 1024 threads, whose stores wait for
+// its own sums, measured 300 us; two of 256 threads 321; pieces of 4 elements 258.
+// A wait that gives up (a copy that never lands) makes that block's remaining rows NaN and is counted.
+constexpr int kRingThreads = 512;
+constexpr int kRingBytes = 108 * 1024;  // of shared memory for each of the two blocks
+constexpr int kRingStages = 8;
+__device__ unsigned g_norm_timeouts = 0;
+
+template <typename T, typename R>
+__global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(BlockNormArgs a, int stages) {
+    constexpr int P = 2;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float red[2][2][kRingThreads / 32];
+    __shared__ uint64_t full[kRingStages];
+    const int D = a.D, tid = threadIdx.x;
+    const uint32_t xb = D * sizeof(T), rb = a.residual ? D * sizeof(R) : 0, zb = a.gate ? xb : 0, row_bytes = xb + rb + zb;
+    const uint32_t base = sm100::smem_u32(ring);
+    auto bar = [&](int s) { return sm100::smem_u32(&full[s]); };
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) sm100::mbar_init(bar(s), 1);
+        sm100::fence_mbar_init();
+    }
+    __syncthreads();
+    auto load = [&](long row, int s) {  // one thread
+        const uint32_t at = base + s * row_bytes;
+        sm100::mbar_arrive_expect_tx(bar(s), row_bytes);
+        sm100::bulk_load(at, (const T*)a.x + row * D, xb, bar(s));
+        if (rb) sm100::bulk_load(at + xb, (const R*)a.residual + row * D, rb, bar(s));
+        if (zb) sm100::bulk_load(at + xb + rb, (const T*)a.gate + row * D, zb, bar(s));
+    };
+    if (tid == 0)
+        for (int s = 0; s < stages; ++s)
+            if (blockIdx.x + (long)s * gridDim.x < a.rows) load(blockIdx.x + (long)s * gridDim.x, s);
+    int s = 0;
+    uint32_t phase = 0, odd = 0, gave_up = 0;
+    for (long row = blockIdx.x; row < a.rows; row += gridDim.x, odd ^= 1) {
+        if (!sm100::mbar_wait(bar(s), phase, gave_up ? 1u : 1u << 22)) {
+            if (!gave_up && tid == 0) atomicAdd(&g_norm_timeouts, 1u);
+            gave_up = 1;
+        }
+        const T* x = reinterpret_cast<const T*>(ring + s * row_bytes);
+        const R* r = rb ? reinterpret_cast<const R*>(ring + s * row_bytes + xb) : nullptr;
+        const T* z = zb ? reinterpret_cast<const T*>(ring + s * row_bytes + xb + rb) : nullptr;
+        float h[P][8];
+        float rs = 1.f, sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int c = 8 * (tid + p * kRingThreads);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[p][i] = 0.f;
+            if (c < D) load_s<T>(x + c, h[p]);
+            if (gave_up) h[p][0] = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(h[p][i], h[p][i], sum);
+        }
+        if (a.post_w) rs = rsqrtf(block_sum<kRingThreads>(sum, red[odd][0]) / D + a.eps);
+        sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int c = 8 * (tid + p * kRingThreads);
+            if (c >= D) continue;
+            scaled<T, 8, true>(a, z, c, rs, h[p]);
+            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (r) load_s<R>(r + c, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[p][i] = fmaf(a.scale, h[p][i], t[i]);
+                sum = fmaf(h[p][i], h[p][i], sum);
+            }
+            if (a.h) store_e<R, 8>((R*)a.h + row * D + c, h[p]);
+        }
+        // (the sum's barrier also says that every thread has read the row)
+        const float rp = rsqrtf(block_sum<kRingThreads>(sum, red[odd][1]) / D + a.eps);
+        if (tid == 0 && !gave_up && row + (long)stages * gridDim.x < a.rows) load(row + (long)stages * gridDim.x, s);
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+        if (!a.y) continue;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int c = 8 * (tid + p * kRingThreads);
+            if (c >= D) continue;
+            if (a.pre_w) {
+                float w[8];
+                load_e<float, 8>(a.pre_w + c, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[p][i] *= rp * w[i];
+            }
+            store_e<T, 8>((T*)a.y + row * D + c, h[p]);
+        }
+    }
+    if (gave_up && tid == 0)  // the copies still in flight
+        for (int i = 0; i < stages; ++i) {
+            sm100::mbar_wait(bar(s), phase);
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+}
+
 // Rows that no block holds in registers, or of a length that is not whole vectors: three passes.
 template <typename T, typename R, int E>
 __global__ void __launch_bounds__(256) block_norm_any_kernel(BlockNormArgs a) {
@@ -297,6 +424,22 @@ __global__ void __launch_bounds__(256) block_norm_any_kernel(BlockNormArgs a) {
 
 template <typename T, typename R>
 cudaError_t launch_block(const BlockNormArgs& a) {
+    // Rows too long for one piece a thread, enough of them for 8 a multiprocessor, and two fit the ring.
+    // 1.07 to 1.6 GB with / without the ring: 16384 x 8192 bf16 with a float32 stream 250 / 278 us, a bf16 one
+    // 176 / 241, none 160 / 221; 26214 x 5120 260 / 346, gated 294 / 436; float32 332 / 363.  At 4096
+    // and below a block per row is ahead (4096: 250 / 238; 2048: 343 / 231).
+    if (a.D % 8 == 0 && a.D > 8 * kRingThreads && a.D <= 16 * kRingThreads) {
+        const int row_bytes = a.D * (int)((a.gate ? 2 : 1) * sizeof(T) + (a.residual ? sizeof(R) : 0));
+        const int stages = min(kRingStages, kRingBytes / row_bytes), sms = planned_sm_count();
+        if (stages >= 2 && a.rows >= 8l * sms) {
+            auto kern = block_norm_ring_kernel<T, R>;
+            const int bytes = stages * row_bytes;
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e != cudaSuccess) return e;
+            kern<<<2 * sms, kRingThreads, bytes, a.stream>>>(a, stages);
+            return cudaGetLastError();
+        }
+    }
     const unsigned g = (unsigned)a.rows;
     // threads for a row: one piece of 8 elements each up to 4096 elements, two up to 16384
     if (a.D % 8 != 0) block_norm_any_kernel<T, R, 1><<<g, 256, 0, a.stream>>>(a);
@@ -335,6 +478,15 @@ cudaError_t launch_gated(const GatedNormArgs& a) {
 }
 
 }  // namespace
+
+cudaError_t read_norm_timeouts(unsigned* count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_norm_timeouts, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_norm_timeouts, &zero, sizeof(unsigned));
+    }
+    return e;
+}
 
 cudaError_t launch_gated_norm(const GatedNormArgs& a) {
     if (a.rows == 0) return cudaSuccess;

@@ -153,6 +153,7 @@ cudaError_t launch_decay_tensor(const DecayArgs& a);
 size_t decay_simt_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed);
 cudaError_t launch_decay_simt(const DecayArgs& a);
 cudaError_t read_decay_timeouts(unsigned* count, bool reset);
+cudaError_t read_norm_timeouts(unsigned* count, bool reset);
 cudaError_t launch_gated_norm(const GatedNormArgs& a);
 cudaError_t launch_block_norm(const BlockNormArgs& a);
 cudaError_t launch_short_conv(const ConvArgs& a);

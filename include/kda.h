@@ -444,7 +444,8 @@ kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weigh
 
 /*
  * Diagnostics of the tensor-core paths' bounded waits.  Every mbarrier wait of the fused
- * and two-pass chunked kernels and of the chunked decayed attention gives up after a fixed number of polls; a CTA whose wait gave
+ * and two-pass chunked kernels, of the chunked decayed attention and of the block norm of many
+ * long rows gives up after a fixed number of polls; a CTA whose wait gave
  * up adds to a per-device counter, stops waiting, issuing MMAs and copies, lets the ones in
  * flight finish (bounded), frees its TMEM and returns, so the context stays usable but that
  * launch's outputs are not valid.  kda_fused_wait_timeouts writes the counters of the current

@@ -246,6 +246,32 @@ def test_block_norm(kda, dtype, res, D, parts):
     close(y, wy, (HALF[dtype] + n * (rel + mean)) * wy.abs() + 1e-30, "y")
 
 
+@pytest.mark.parametrize("dtype,res", [(BF, torch.float32), (BF, BF), (BF, None), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("D", [4104, 6000, 8192])
+@pytest.mark.parametrize("gate", [False, True])
+def test_block_norm_of_many_long_rows(kda, dtype, res, D, gate):
+    """More rows than the blocks that stay resident hold at once; h in place of the stream."""
+    g = torch.Generator().manual_seed(D)
+    rows = 1217 if D == 6000 else 1500
+    x = (0.5 * torch.randn(rows, D, generator=g)).to(dtype)
+    x[rows - 1] = 0
+    r = None if res is None else torch.randn(rows, D, generator=g).to(res)
+    z = torch.randn(rows, D, generator=g).to(dtype) if gate else None
+    wp, wn = (torch.rand(D, generator=g) + 0.5 for _ in range(2))
+    wh, wy = ref.block_norm(x, r, wp, z, 1, 0.7, None, wn, 1e-6)
+    rd = dev(r)
+    before = kda.kda_fused_wait_timeouts()
+    h, y = kda.kda_block_norm_fwd(dev(x), rd, dev(wp), dev(z), dev(wn), scale=0.7, act=1, residual_out=rd)
+    assert r is None or h is rd
+    n = (D // 8 + 24) * F32 + (2.0 ** -18 if dtype == BF and gate else 24 * F32)
+    size = wh.abs() + (0 if r is None else 2 * r.double().abs())
+    close(h, wh, HALF[h.dtype] * wh.abs() + n * size + 1e-30, "h")
+    rel = size / wh.abs().clamp_min(1e-300)
+    mean = (size.square().mean(-1, keepdim=True) / (wh.square().mean(-1, keepdim=True) + 1e-6)).sqrt()
+    close(y, wy, (HALF[dtype] + n * (rel + mean)) * wy.abs() + 1e-30, "y")
+    assert kda.kda_fused_wait_timeouts() == before
+
+
 def test_block_norm_without_one_output(kda):
     x, w = torch.randn(3, 256, device="cuda"), torch.rand(256, device="cuda")
     import ctypes
