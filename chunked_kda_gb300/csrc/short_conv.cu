@@ -11,7 +11,10 @@
 // state, all belong to the tile of its first row (which runs over its end for them), so one thread
 // reads the old state of a channel before it writes the new: the two may be one buffer.
 //
-// Rows are loaded U at a time before any is used (enough bytes in flight).  TT trades the reload of
+// Rows are loaded U at a time while the U before them are in work: 20480 packed rows x 12288 bf16
+// (1.01 GB) in 162 us, 6.2 TB/s, with 8 rows and six blocks on an SM; 4 rows and eight blocks measured
+// 168, 6 and seven 176, 12 and five 174, 16 and four 183; stores that stay in the caches 173.  (float32 rows
+// are twice the registers: 4 at a time, 20480 x 6144 in 213 us.)  TT trades the reload of
 // W - 1 rows and of the weights against the number of blocks: 64 rows where that leaves eight blocks
 // an SM, else 16 or 8.
 #include <limits.h>
@@ -116,7 +119,8 @@ __device__ __forceinline__ void row_step(const typename Io::V& raw, const float 
         for (int w = 0; w < W; ++w) acc = fmaf(wt[0][w], win[w][0], acc);
         out[0] = activate<T>(acc, act);
     }
-    *reinterpret_cast<typename Io::V*>(y) = Io::put(out);
+    if constexpr (E > 1) __stcs(reinterpret_cast<typename Io::V*>(y), Io::put(out));
+    else *reinterpret_cast<typename Io::V*>(y) = Io::put(out);
 #pragma unroll
     for (int w = 0; w < W - 1; ++w)
 #pragma unroll
@@ -125,7 +129,7 @@ __device__ __forceinline__ void row_step(const typename Io::V& raw, const float 
 
 // Single tokens: a thread takes Q whole sequences of its channels, with the states and first rows of
 // all of them loaded before the first is used.  (The tiles above walk one start after another, each
-// with its loads' latency: 33 us for 512 sequences of one token x 12288 channels against 22 us here.)
+// with its loads' latency: 33 us for 512 sequences of one token x 12288 channels against 21 us here.)
 template <typename T, typename Io, int W>
 __global__ void __launch_bounds__(128) short_conv_seq_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                                                              const float* __restrict__ bias, int act, const T* s0, T* s1,
@@ -192,12 +196,12 @@ __device__ __forceinline__ int first_at_least(const int32_t* __restrict__ cu, in
 }
 
 template <typename T, typename Io, int W>
-__global__ void __launch_bounds__(128, W <= 4 ? 8 : 5) short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight,
+__global__ void __launch_bounds__(128, W <= 4 ? 6 : sizeof(typename Io::V) > 8 ? 4 : 5) short_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                                                          const float* __restrict__ bias, int act, const T* s0, T* s1,
                                                          const int32_t* __restrict__ cu, int N, int L, long rows, int TT,
                                                          int D, T* __restrict__ y) {
     using V = typename Io::V;
-    constexpr int E = Io::E, U = 4;
+    constexpr int E = Io::E, U = W <= 4 && sizeof(V) <= 8 ? 8 : 4;
     const int d = E * (blockIdx.x * 128 + threadIdx.x);
     const long t0 = (long)blockIdx.y * TT, t1 = min(t0 + TT, rows);
     // packed: starts cu[0..N-1] and the end cu[N]; dense: starts n L, the end N L
