@@ -10,6 +10,9 @@
 // lanes and come as 16-byte loads, without shared memory.  The only reduction is o's sum over
 // the rows: per thread, then across the warps through shared memory, two buffers by token parity
 // so that one barrier a token is enough.
+//
+// Memory bounds it: the state goes in and out once.  512 sequences of one token, 32 heads of 128 x 128
+// (2.17 GB) in 310 us, 7.0 TB/s.
 #include "common.cuh"
 #include "kda_internal.h"
 
