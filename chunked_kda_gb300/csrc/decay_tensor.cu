@@ -26,10 +26,10 @@
 // What bounds it is shared memory's 128 bytes a clock next to HBM: per chunk at K = V = 128 the loads
 // write 48 KB, the products read 120 KB, the warps and the stores about 60 KB.  That is why the scaled
 // values are the operand that lies in TMEM, straight from registers: scaled keys in shared memory cost
-// 48 KB of writes and 48 KB of reads more a chunk (4 x 4096 tokens, 64 heads: 239 us against 214).
-// That case moves 1.09 GB, 5.1 TB/s; 20480 packed tokens with states, 32 heads: 139 us; one sequence of 32767
+// 48 KB of writes and 48 KB of reads more a chunk (4 x 4096 tokens, 64 heads, whole units: 239 us against 214).
+// That case moves 1.09 GB in 201 us with cut units, 5.4 TB/s; 20480 packed tokens with states, 32 heads: 139 us; one sequence of 32767
 // tokens, 16 heads, cut into segments (k and v read twice): 169 us.  A head of 256 key channels is two of
-// 128 whose FP32 outputs are added (8 x 2048 tokens, 32 heads, 256 x 256: 1152 us against 7266 in FP32).
+// 128 whose FP32 outputs are added (8 x 2048 tokens, 32 heads, 256 x 256: 869 us against 7266 in FP32).
 //
 // One CTA per unit and SM, 28 warps: 0-3 P, 4-11 state, 12-15 output, 16-23 scaled values, 24 the output's
 // products, 25 decay factors, 26 the state's products, 27 loads and scores.  Every wait is bounded (a CTA
@@ -50,7 +50,7 @@ using namespace sm100;
 
 __device__ unsigned int g_decay_timeouts = 0;
 
-constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128;
+constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8;
 
 // barriers
 enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + 2, B_SBF, B_VD, B_STATE, B_INTER, B_O,
@@ -85,10 +85,13 @@ struct Params {
     const int32_t* cu;
     void* o;
     int N, T, H, hr, K, V;
+    int vblocks;
     int k0;         // this launch's first key channel (a head of 256 takes two launches of 128)
     int seg;        // tokens of a segment (a multiple of C), 0: whole sequences
     float* ws;      // segment states [slot][h][K][V]
     float* wdec;    // segment decays [slot][h]
+    unsigned* cuts; // cut units: a ticket, then a counter for each unit (all zero); else null
+    int per;        // chunks of an SM with cut units
     int* status;
     int stall_chunk;
 };
@@ -236,6 +239,57 @@ __device__ __forceinline__ uint32_t cut(float2& x) {
     return __byte_perm(a, b, 0x7632);
 }
 
+// Whole sequences of one length, more units than SMs, the last wave part-empty: the units' chunks are
+// laid end to end and shared out evenly, `per` (at least a unit's nt) an SM, so a unit that does not fit into what
+// is left of an SM is cut.  Its part on the next SM, which is that SM's first work, is the earlier one in time;
+// the part at this SM's end runs per - nt chunks or more after the other's end and finds its state there.
+// Blocks take the pieces in the order of their starts (a ticket, so that whoever waits began later than what it waits for):
+// the SMs' first pieces, then the whole units, then the cut units' second pieces, the longest first (their SMs
+// are free first).  4 x 4096 tokens, 64 heads (256 units): 201 us against 217 with whole
+// units; 5 x 4096, 64 heads (320): 246 against 316; 2 x 16384, 80 heads (160): 459 against 823.
+struct Piece {
+    int unit, c0, c1;
+};
+__device__ __forceinline__ Piece cut_piece(const Params& p, int* scratch) {
+    const int tid = threadIdx.x, nt = (p.T + C - 1) / C, units = p.N * p.H * p.vblocks;
+    const int W = units * nt, firsts = (W + p.per - 1) / p.per;
+    if (tid == 0) scratch[0] = (int)atomicAdd(p.cuts, 1u);
+    for (int m = tid; m < firsts; m += NTHR) scratch[2 + m] = (int)((long)m * p.per % nt);
+    __syncthreads();
+    const int i = scratch[0];
+    Piece pc;
+    if (i < firsts) {
+        const int at = i * p.per;
+        pc.unit = at / nt;
+        pc.c0 = 0;
+        pc.c1 = (pc.unit + 1) * nt - at;
+    } else if (i < units) {
+        // the (i - firsts)-th unit without a multiple of per in it: of the units up to u, ceil((u + 1) nt / per) have one
+        int lo = 0, hi = units - 1;
+        while (lo < hi) {
+            const int u = (lo + hi) / 2;
+            if (u + 1 - ((u + 1) * nt + p.per - 1) / p.per > i - firsts) hi = u;
+            else lo = u + 1;
+        }
+        pc = {lo, 0, nt};
+    } else {
+        for (int m = tid; m < firsts; m += NTHR) {
+            const int mine = scratch[2 + m];
+            int rank = 0;
+            for (int j = 0; j < firsts; ++j) rank += scratch[2 + j] > mine || (scratch[2 + j] == mine && j < m);
+            if (rank == i - units) scratch[1] = m;
+        }
+        __syncthreads();
+        const int m = scratch[1], at = m * p.per;
+        pc.unit = at / nt;
+        pc.c0 = nt - at % nt;
+        pc.c1 = nt;
+    }
+    fence_proxy_async_smem();  // (a stage's place)
+    __syncthreads();
+    return pc;
+}
+
 // kStates: only the state a segment adds (no queries, no output), for the segments' scan.
 template <int KD, int VB, typename OT, bool kStates>
 __global__ void __launch_bounds__(NTHR, 1)
@@ -252,10 +306,20 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), l = tid & 31;
 
     // ---- the unit: heads fastest, then value blocks
-    const int h = blockIdx.x, vb = blockIdx.y, slot = blockIdx.z;
+    int h = blockIdx.x, vb = blockIdx.y, slot = blockIdx.z, unit = 0;
     int n, bos, eos;
     bool first = true, last = true;
-    if (p.seg == 0) {
+    if (!kStates && p.cuts) {
+        const Piece pc = cut_piece(p, reinterpret_cast<int*>(smem));
+        unit = pc.unit;
+        h = unit % p.H;
+        vb = unit / p.H % p.vblocks;
+        n = slot = unit / (p.H * p.vblocks);
+        first = pc.c0 == 0;
+        last = pc.c1 == (p.T + C - 1) / C;
+        bos = n * p.T + pc.c0 * C;
+        eos = n * p.T + min(pc.c1 * C, p.T);
+    } else if (p.seg == 0) {
         n = slot;
         if (p.cu && p.N <= kRanked) {
             // The blocks start in order: the longest sequences first, so that none is left for the
@@ -272,7 +336,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncthreads();
             n = ranked[slot];
-            __syncthreads();  // (a stage's place)
+            fence_proxy_async_smem();  // (a stage's place)
+            __syncthreads();
         }
         if (p.cu) { bos = __ldg(p.cu + n); eos = __ldg(p.cu + n + 1); }
         else      { bos = n * p.T; eos = bos + p.T; }
@@ -583,8 +648,17 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const size_t at = (size_t)p.k0 * p.V + vc0 + vl, st = ((size_t)n * p.H + h) * (size_t)p.K * p.V + at;
         const size_t sg = ((size_t)slot * p.H + h) * (size_t)p.K * p.V + at;
         // a cut sequence's segments take their incoming states from the scan
-        const float* src = kStates ? nullptr : first && last ? (p.h0 ? p.h0 + st : nullptr) : p.ws + sg;
-        float* dst = kStates ? p.ws + sg : (last && p.hT) ? p.hT + st : nullptr;
+        const bool head = p.cuts && !last;  // a cut unit's first piece: its state goes to the other
+        const float* src = kStates ? nullptr : (first && last) || head ? (p.h0 ? p.h0 + st : nullptr) : p.ws + sg;
+        float* dst = kStates || head ? p.ws + sg : (last && p.hT) ? p.hT + st : nullptr;
+        if (!kStates && p.cuts && !first) {  // the second: it began later, so this wait is short
+            bool come = false;
+            // (a poll takes half a microsecond or more, a chunk two: enough for a whole unit)
+            for (int i = 0; i < (1 << 20) + p.T && !(come = ld_acquire_gpu(p.cuts + 1 + unit) == 8u); ++i)
+                if (sy.aborted()) break;
+            if (!__all_sync(0xffffffffu, come) && l == 0 && !sy.aborted()) sy.give_up();
+            __syncwarp();
+        }
         // the incoming state, 32 rows in flight; an empty sequence's goes straight on
 #pragma unroll 1
         for (int x = c0; x < c1; x += 32) {
@@ -672,6 +746,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 __syncwarp();
             }
+            if (head && l == 0) red_release_gpu(p.cuts + 1 + unit, 1u);
         }
     } else if (w < 16) {
         // ------------------------------------------------ output rows
@@ -938,18 +1013,36 @@ int plan_segment(int B, int T, int H, int vblocks, int N, bool packed) {
     return 2 * per > T ? 0 : (int)per;
 }
 
+// Chunks of an SM where units are cut (0: they are not).  Cuts cost an SM about eight chunks (a state's way,
+// more starts): 8 x 1024 tokens, 32 heads (27 chunks an SM for the 32 of two waves) 70 us with cuts and
+// 64 without, 8 x 2048, 64 heads (108 for 128) 211 and 221.
+int plan_cuts(int B, int T, int H, int vblocks) {
+    const long sms = planned_sm_count(), units = (long)B * H * vblocks, nt = (T + C - 1) / C;
+    if (sms <= 0 || units <= sms || units * nt > 1 << 30 || sms > kMaxCuts) return 0;
+    const long waves = (units + sms - 1) / sms, per = (units * nt + sms - 1) / sms;
+    return per + kCutCost <= waves * nt ? (int)per : 0;
+}
+
 struct Plan {
-    int seg, slots;
-    size_t states, half, bytes;  // the segments' states; one of the two outputs of a head of 256; in all
+    int seg, slots, per, pieces;
+    size_t states, counters, half, bytes;  // states handed on; counters; one of the two outputs of a head of 256; in all
 };
 Plan plan(int B, int T, int H, int K, int V, int N, bool packed) {
-    Plan pl{0, N, 0, 0, 0};
+    Plan pl{0, N, 0, 0, 0, 0, 0, 0};
     const int vblocks = V > 128 ? 2 : 1;
     pl.seg = plan_segment(B, T, H, vblocks, N, packed);
     if (pl.seg) {
         pl.slots = packed ? T / pl.seg + N + 1 : N * ((T + pl.seg - 1) / pl.seg);
         pl.states = (size_t)pl.slots * H * K * V * sizeof(float);
         pl.bytes = pl.states + ((size_t)pl.slots * H * sizeof(float) + 255) / 256 * 256;
+    }
+    if (!packed && !pl.seg && (pl.per = plan_cuts(B, T, H, vblocks)) > 0) {
+        const int nt = (T + C - 1) / C, units = B * H * vblocks, firsts = (units * nt + pl.per - 1) / pl.per;
+        pl.pieces = units;
+        for (int m = 0; m < firsts; ++m) pl.pieces += (long)m * pl.per % nt != 0;
+        pl.states = (size_t)N * H * K * V * sizeof(float);
+        pl.counters = ((size_t)(units + 1) * sizeof(unsigned) + 255) / 256 * 256;
+        pl.bytes = pl.states + pl.counters;
     }
     if (K == 256) {
         pl.half = ((size_t)B * T * H * V * sizeof(float) + 255) / 256 * 256;
@@ -980,10 +1073,16 @@ cudaError_t run(const DecayArgs& a) {
         return cudaErrorInvalidValue;
     const Plan pl = plan(a.B, a.T, a.H, a.K, a.V, a.N, a.cu != nullptr);
     char* ws = (char*)a.ws;
-    Params p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, 0, pl.seg,
-             (float*)ws, (float*)(ws + pl.states), a.status, hook_stall_chunk()};
-    const dim3 grid(a.H, (a.V + VB - 1) / VB, pl.slots);
+    const int vblocks = (a.V + VB - 1) / VB;
+    Params p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, 0, pl.seg,
+             (float*)ws, (float*)(ws + pl.states), nullptr, pl.per, a.status, hook_stall_chunk()};
+    dim3 grid(a.H, vblocks, pl.slots);
     cudaError_t e;
+    if (pl.per) {
+        p.cuts = (unsigned*)(ws + pl.states);
+        grid = dim3(pl.pieces);
+    }
+    auto clear = [&] { return pl.per ? cudaMemsetAsync(p.cuts, 0, pl.counters, a.stream) : cudaSuccess; };
     if (pl.seg) {
         for (p.k0 = 0; p.k0 < a.K; p.k0 += KD)
             if ((e = launch(decay_chunk_kernel<KD, VB, __nv_bfloat16, true>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess)
@@ -994,10 +1093,14 @@ cudaError_t run(const DecayArgs& a) {
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     p.k0 = 0;
-    if (a.K == KD) return launch(decay_chunk_kernel<KD, VB, OT, false>, L::BYTES, grid, a.stream, m, p);
+    if (a.K == KD) {
+        if ((e = clear()) != cudaSuccess) return e;
+        return launch(decay_chunk_kernel<KD, VB, OT, false>, L::BYTES, grid, a.stream, m, p);
+    }
     float* half = (float*)(ws + pl.bytes - 2 * pl.half);
     for (; p.k0 < a.K; p.k0 += KD) {
         p.o = p.k0 == 0 ? half : half + pl.half / sizeof(float);
+        if ((e = clear()) != cudaSuccess) return e;
         if ((e = launch(decay_chunk_kernel<KD, VB, float, false>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess) return e;
     }
     if (tokens == 0) return cudaSuccess;

@@ -158,6 +158,23 @@ def test_long_prompts_with_few_heads(kda, T, H, B):
     check(kda, "kda_decay_chunk_fwd", inputs(T, B, T, H, H, 128, 128, BF, B, fixed=H == 2))
 
 
+@pytest.mark.parametrize("sms,B,T,H,K,V", [(3, 2, 1270, 2, 128, 128), (2, 1, 1500, 5, 64, 128), (7, 3, 1536, 3, 128, 64), (3, 1, 1601, 2, 128, 256), (3, 1, 1601, 2, 256, 256)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_units_cut_between_processors(kda, sms, B, T, H, K, V, inplace):
+    """More units than multiprocessors and a last wave part-empty: some are cut and joined by their state."""
+    x = inputs(T, B, T, H, H, K, V, BF, B)
+    before = kda.kda_fused_wait_timeouts()
+    try:
+        kda.kda_test_hooks(sm_count=sms)
+        o, S = check(kda, "kda_decay_chunk_fwd", x, inplace=inplace)
+        again = kda.kda_decay_chunk_fwd(*(dev(t) for t in x[:4]), initial_state=dev(x[4]), output_final_state=True)
+        assert torch.equal(again[0], o) and torch.equal(again[1], S)
+        check(kda, "kda_decay_chunk_fwd", (*x[:4], None))
+    finally:
+        kda.kda_test_hooks()
+    assert kda.kda_fused_wait_timeouts() == before
+
+
 def test_chunked_continues_in_single_tokens(kda):
     """A prompt in chunks and then token by token, in place, is the whole sequence at once."""
     q, k, v, a, _ = (dev(t) for t in inputs(1, 2, 100, 4, 2, 128, 128, BF, 2, state=False))
