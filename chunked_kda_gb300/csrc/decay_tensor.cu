@@ -936,21 +936,32 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const float* __restrict
     const int s0 = cm.first_slot(n, bos);
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (h0) S = *reinterpret_cast<const float4*>(h0 + ((size_t)n * H + h) * KV + e);
-    // the first segment's too: the last one may write its final state over h0
-    float4* from = reinterpret_cast<float4*>(ws + ((size_t)s0 * H + h) * KV + e);
-    float4 add = *from;
-    *from = S;
-    for (int s = 0; s + 1 < ns; ++s) {
-        const float d = __ldg(wdec + (size_t)(s0 + s) * H + h);
-        float* next = ws + ((size_t)(s0 + s + 1) * H + h) * KV + e;
-        float4 add2 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s + 2 < ns) add2 = *reinterpret_cast<const float4*>(next);
-        S.x = fmaf(d, S.x, add.x);
-        S.y = fmaf(d, S.y, add.y);
-        S.z = fmaf(d, S.z, add.z);
-        S.w = fmaf(d, S.w, add.w);
-        *reinterpret_cast<float4*>(next) = S;
-        add = add2;
+    // The first segment's too: the last one may write its final state over h0.  Eight additions are on
+    // their way at once (9 segments of 16 heads from cold caches 5 us; one ahead of the sum 19).
+    constexpr int R = 8;
+    const size_t step = (size_t)H * KV;
+    float* at = ws + ((size_t)s0 * H + h) * KV + e;
+    const float* decay = wdec + (size_t)s0 * H + h;
+    for (int s = 0; s < ns; s += R) {
+        float4 add[R];
+        float d[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (s + j + 1 >= ns) break;
+            add[j] = *reinterpret_cast<const float4*>(at + j * step);
+            d[j] = __ldg(decay + (size_t)(s + j) * H);
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (s + j >= ns) break;
+            *reinterpret_cast<float4*>(at + j * step) = S;
+            if (s + j + 1 >= ns) break;
+            S.x = fmaf(d[j], S.x, add[j].x);
+            S.y = fmaf(d[j], S.y, add[j].y);
+            S.z = fmaf(d[j], S.z, add[j].z);
+            S.w = fmaf(d[j], S.w, add[j].w);
+        }
+        at += R * step;
     }
 }
 
