@@ -375,6 +375,12 @@ typedef enum {
  * kda_decay_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for
  * dense inputs).  kda_decay_recurrent_fwd is the form for single tokens and
  * computes token by token in FP32.
+ *
+ * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores, which cut
+ * what they add to an FP32 accumulator: the states lean to zero by about 8e-7
+ * of their value for each 64 tokens of the decay's memory (6e-6 at a decay of
+ * -0.0023, 1e-4 over 32768 tokens without any).  Float32 inputs and the recurrent
+ * form add in rounded FP32.
  */
 size_t kda_decay_chunk_workspace_bytes(kda_dtype qkv_dtype, int B, int T, int H, int K, int V,
                                        int n_seqs);
