@@ -175,6 +175,30 @@ def test_units_cut_between_processors(kda, sms, B, T, H, K, V, inplace):
     assert kda.kda_fused_wait_timeouts() == before
 
 
+def test_cut_units_replayed_from_a_graph(kda):
+    """Each replay clears the counters that the pieces of a unit meet at."""
+    x = [dev(t) for t in inputs(7, 2, 1400, 2, 2, 128, 128, BF, 2)]
+    before = kda.kda_fused_wait_timeouts()
+    try:
+        kda.kda_test_hooks(sm_count=3)
+        want = kda.kda_decay_chunk_fwd(*x[:4], initial_state=x[4], output_final_state=True)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                o, S = kda.kda_decay_chunk_fwd(*x[:4], initial_state=x[4], output_final_state=True)
+    finally:
+        kda.kda_test_hooks()
+    for _ in range(3):
+        o.zero_()
+        S.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(S, want[1])
+    assert kda.kda_fused_wait_timeouts() == before
+
+
 def test_chunked_continues_in_single_tokens(kda):
     """A prompt in chunks and then token by token, in place, is the whole sequence at once."""
     q, k, v, a, _ = (dev(t) for t in inputs(1, 2, 100, 4, 2, 128, 128, BF, 2, state=False))
