@@ -42,6 +42,13 @@ __device__ __forceinline__ float pow2(int n, int f) {
 __device__ __forceinline__ float pow2_fast(int n, int f) {
     return sm100::ex2_fast((float)f * (1.f / 16777216.f)) * pow2i(n);
 }
+// The first of a chunk's 64 tokens, two consecutive ones a lane, whose decay is no number (64: none):
+// that token's output and all that follow are none either, those before it have nothing to do with it.
+__device__ __forceinline__ int first_nan(float a0, float a1) {
+    const unsigned even = __ballot_sync(0xffffffffu, a0 != a0), odd = __ballot_sync(0xffffffffu, a1 != a1);
+    return min(even ? 2 * (__ffs(even) - 1) : 64, odd ? 2 * __ffs(odd) - 1 : 64);
+}
+__device__ __forceinline__ float nan_if(bool on) { return on ? __int_as_float(0x7fffffff) : 0.f; }
 // Inclusive sums over a warp of two consecutive tokens a lane: I, F of the lane's two tokens.
 __device__ __forceinline__ void pair_sums(float a0, float a1, int (&I)[2], int (&F)[2]) {
     int i0, i1;

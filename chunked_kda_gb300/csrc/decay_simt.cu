@@ -31,7 +31,7 @@ struct SimtArgs {
     float* wdec;  // [slot][h]
 };
 
-// the chunk's G as integer and fraction, by warp 0 (a barrier follows)
+// the chunk's G as integer and fraction, and the first token without one, by warp 0 (a barrier follows)
 __device__ __forceinline__ void chunk_gates(const SimtArgs& p, int h, int t0, int len, int (*sI)[C]) {
     if (threadIdx.x < 32) {
         const int l = threadIdx.x;
@@ -39,13 +39,13 @@ __device__ __forceinline__ void chunk_gates(const SimtArgs& p, int h, int t0, in
         int I[2], F[2];
         const float a0 = a(2 * l), a1 = a(2 * l + 1);
         pair_sums(a0, a1, I, F);
-        const bool bad = __any_sync(0xffffffffu, a0 != a0 || a1 != a1);  // a NaN decay
+        const int first = first_nan(a0, a1);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             sI[0][2 * l + e] = I[e];
             sI[1][2 * l + e] = F[e];
         }
-        if (l == 0) sI[2][0] = bad;
+        if (l == 0) sI[2][0] = first;
     }
     __syncthreads();
 }
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, 
     const int h = blockIdx.y, nkb = (p.K + 63) / 64, c0 = 64 * (blockIdx.z % nkb), d0 = 64 * (blockIdx.z / nkb);
     const int tid = threadIdx.x;
     chunk_gates(p, h, t0, len, sI);
-    const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
+    const float poison = nan_if(sI[2][0] < C);
     const int Hk = p.H / p.hr, hq = h / p.hr;
     if (tid < C) sf[tid] = pow2(sI[0][C - 1] - sI[0][tid], sI[1][C - 1] - sI[1][tid]) + poison;
     __syncthreads();
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
     if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
     const int h = blockIdx.y, tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
     chunk_gates(p, h, t0, len, sI);
-    const float poison = sI[2][0] ? __int_as_float(0x7fffffff) : 0.f;
+    const int bad = sI[2][0];
     const int Hk = p.H / p.hr, hq = h / p.hr;
     const float scale = rsqrtf((float)p.K);
     load_transposed(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sq);
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
             for (int j = 0; j < 4; ++j) {
                 const int r = 4 * ti + i, s = 4 * tj + j;
                 float y = 0.f;
-                if (s <= r) y = acc[i][j] * (pow2(sI[0][r] - sI[0][s], sI[1][r] - sI[1][s]) + poison);
+                if (s <= r) y = acc[i][j] * (pow2(sI[0][r] - sI[0][s], sI[1][r] - sI[1][s]) + nan_if(r >= bad));
                 sp[s * LD + r] = y;
             }
     }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float f = pow2(sI[0][4 * ti + i], sI[1][4 * ti + i]) + poison;
+            const float f = pow2(sI[0][4 * ti + i], sI[1][4 * ti + i]) + nan_if(4 * ti + i >= bad);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] *= f;
         }

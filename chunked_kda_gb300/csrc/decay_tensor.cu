@@ -464,7 +464,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             pair_sums(x0, x1, I, F);
             const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
             const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
-            const float poison = __any_sync(0xffffffffu, x0 != x0 || x1 != x1) ? __int_as_float(0x7fffffff) : 0.f;  // a NaN decay
+            const int bad = first_nan(x0, x1);
+            const float poison = nan_if(bad < C);  // of the state behind the chunk
             total += ((long long)Il << 24) + Fl;
             // this chunk's value and row factors, and the exponent behind it
             int ni = Ei + Il, nf = Ef + Fl;
@@ -477,11 +478,12 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * l + e;
-                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + poison);
+                const float none = nan_if(i >= bad);
+                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + none);
                 const int rf = Ef + F[e];
-                sts(gt + GT_ROW + 4 * i, kScale * pow2_fast(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + poison);
+                sts(gt + GT_ROW + 4 * i, kScale * pow2_fast(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + none);
                 sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e], Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
-                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]) + poison);
+                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]) + nan_if((i | 15) >= bad));
             }
             if (l == 0) {
                 sts(gt + GT_LAST, (renew ? pow2(ni, nf) : 1.f) + poison);

@@ -376,6 +376,9 @@ typedef enum {
  * dense inputs).  kda_decay_recurrent_fwd is the form for single tokens and
  * computes token by token in FP32.
  *
+ * What is not finite never reaches back: a decay that is NaN makes its head's outputs
+ * NaN from its token on.
+ *
  * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores, which cut
  * what they add to an FP32 accumulator: the states lean to zero by about 8e-7
  * of their value for each 64 tokens of the decay's memory (6e-6 at a decay of

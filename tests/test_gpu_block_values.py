@@ -1,0 +1,44 @@
+"""Decayed attention on values at the edge of its types, against float64: what is not finite stays behind
+its token.
+
+Bounds as in test_gpu_block (u = 2^-24, w = 2^-8).
+"""
+import pytest
+import torch
+
+import block_reference as ref
+from block_reference import F32, HALF
+from test_gpu_block import BF, close, dev, inputs, kda  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+FORMS = ["kda_decay_chunk_fwd", "kda_decay_recurrent_fwd"]
+
+
+def compare_elsewhere(fn, x, o, S, spoiled_o, spoiled_S):
+    """o and S against the reference of x (whose values are all finite) but for the places that are
+    marked, and those are not finite."""
+    q, k, v, decay, S0 = x
+    o_ref, S_ref, oa, Sa = ref.decay_attention(q, k, v, decay, S0)
+    f32 = (q.shape[3] + 128 + q.shape[1]) * F32
+    operand = HALF[BF] * (1 + 2.0 ** -6) if "chunk" in fn and q.dtype == BF else 0.0
+    assert not torch.isfinite(o.cpu()[spoiled_o]).any() and not torch.isfinite(S.cpu()[spoiled_S]).any()
+    o, S = o.double().cpu(), S.double().cpu()
+    o[spoiled_o], S[spoiled_S] = o_ref[spoiled_o], S_ref[spoiled_S]
+    half = HALF[BF] if q.dtype == BF else F32
+    close(o, o_ref, half * o_ref.abs() + (operand + f32) * oa + 1e-30, "o")
+    close(S, S_ref, f32 * Sa + 1e-30, "state")
+
+
+@pytest.mark.parametrize("fn", FORMS)
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("K,V", [(128, 128), (256, 64), (40, 72)])
+@pytest.mark.parametrize("T,at", [(200, 0), (200, 1), (200, 37), (200, 64), (200, 199), (700, 300)])
+def test_a_decay_that_is_no_number(kda, fn, dtype, K, V, T, at):  # noqa: F811
+    """Outputs before its token and of other heads stay right."""
+    q, k, v, decay, S0 = x = inputs(T + at, 1, T, 2, 2, K, V, dtype, 1, span=0.1)
+    bad = decay.clone()
+    bad[0, at, 1] = float("nan")
+    o, S = getattr(kda, fn)(dev(q), dev(k), dev(v), dev(bad), initial_state=dev(S0), output_final_state=True)
+    so, sS = torch.zeros(o.shape, dtype=torch.bool), torch.zeros(S.shape, dtype=torch.bool)
+    so[0, at:, 1], sS[0, 1] = True, True
+    compare_elsewhere(fn, x, o, S, so, sS)
