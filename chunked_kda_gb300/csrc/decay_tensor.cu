@@ -8,9 +8,11 @@
 //   S      <- 2^G_l S + sum_j k_j (2^(G_l - G_j) v_j)^T                         (FP32)
 // as four products, value channels (M = 128) on TMEM lanes:
 //   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += vd^T k.
-// The stored state is S 2^-E.  Where the decay is slow, E' = E + G_l and the values carry 2^(G_l - G_j - E')
-// = 2^-(E + G_j): nothing has to be multiplied between two chunks' state products, and S is rounded once
-// less.  Before |E| passes 32 the stored state is scaled (factor 2^(E + G_l)) and E starts again at 0.
+// The stored state is S 2^-E, E from kTop = 32 down to 0.  Where the decay is slow, E' = E + G_l and the
+// values carry 2^(G_l - G_j - E') = 2^-(E + G_j): nothing has to be multiplied between two chunks' state
+// products, and S is rounded once less.  Before E falls below 0 the stored state is scaled (factor
+// 2^(E + G_l - kTop)) and E starts again at kTop.  So what is stored is never larger than S, and nothing
+// overflows that FP32 holds; the price is at the other end, where values below 2^-85 lose low bits.
 //
 // q, k and v enter the products as they are; O1's row factor s 2^(E + G_i) is applied to the FP32
 // results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
@@ -50,7 +52,7 @@ using namespace sm100;
 
 __device__ unsigned int g_decay_timeouts = 0;
 
-constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8;
+constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8, kTop = 32;
 
 // barriers
 enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + 2, B_SBF, B_VD, B_STATE, B_INTER, B_O,
@@ -452,8 +454,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const float* dp = p.decay + h;
         auto raw = [&](int t) { return t < eos ? __ldg(dp + (size_t)t * p.decay_stride) : 0.f; };
         float a0 = raw(bos + 2 * l), a1 = raw(bos + 2 * l + 1);
-        int Ei = 0, Ef = 0;   // the stored state's exponent: integer, and fraction in 2^-24 units
-        long long total = 0;  // the whole segment's log2 decay in 2^-24 units
+        int Ei = kTop, Ef = 0;  // the stored state's exponent: integer, and fraction in 2^-24 units
+        long long total = 0;    // the whole segment's log2 decay in 2^-24 units
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS, t0 = bos + c * C;
@@ -470,7 +472,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // this chunk's value and row factors, and the exponent behind it
             int ni = Ei + Il, nf = Ef + Fl;
             carry(ni, nf);
-            const bool renew = ni < -32 || ni >= 32;
+            const bool renew = ni < 0 || ni >= 2 * kTop;
             // the slot's last readers are done: chunk c - NS is loaded (and its FULL phase complete),
             // so the products of c - 2 NS are done, which the output warps of c - NG preceded
             if (c >= NS && !sy.warp_wait(B_FULL + s, ((c / NS) - 1) & 1)) break;
@@ -482,14 +484,14 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f) + none);
                 const int rf = Ef + F[e];
                 sts(gt + GT_ROW + 4 * i, kScale * pow2_fast(Ei + I[e] + (rf >> 24), rf & 0xFFFFFF) + none);
-                sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e], Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
+                sts(gt + GT_KEY + 4 * i, (renew ? pow2(Il - I[e] - kTop, Fl - F[e]) : pow2(-Ei - I[e] - (rf >> 24), -(rf & 0xFFFFFF))) + poison);
                 sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]) + nan_if((i | 15) >= bad));
             }
             if (l == 0) {
-                sts(gt + GT_LAST, (renew ? pow2(ni, nf) : 1.f) + poison);
-                sts(gt + GT_OUT, renew ? 1.f : pow2(ni, nf));
+                sts(gt + GT_LAST, (renew ? pow2(ni - kTop, nf) : 1.f) + poison);
+                sts(gt + GT_OUT, renew ? pow2i(kTop) : pow2(ni, nf));
             }
-            Ei = renew ? 0 : ni;
+            Ei = renew ? kTop : ni;
             Ef = renew ? 0 : nf;
             __syncwarp();
             if (l == 0) mbar_arrive(sy.bar(B_FULL + s));
@@ -674,6 +676,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
             if (nt > 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= 1.f / (1ll << kTop);  // E = kTop
                 tmem_st16(tmem + TM_S + lane + x, reinterpret_cast<uint32_t*>(v));
                 tmem_st16(tmem + TM_S + lane + x + 16, reinterpret_cast<uint32_t*>(v) + 16);
             } else if (dst && mine) {

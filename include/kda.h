@@ -382,7 +382,8 @@ typedef enum {
  * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores, which cut
  * what they add to an FP32 accumulator: the states lean to zero by about 8e-7
  * of their value for each 64 tokens of the decay's memory (6e-6 at a decay of
- * -0.0023, 1e-4 over 32768 tokens without any).  Float32 inputs and the recurrent
+ * -0.0023, 1e-4 over 32768 tokens without any).  The state is kept scaled down by up
+ * to 2^32: it overflows only where float32 does, and values below 2^-85 lose low bits.  Float32 inputs and the recurrent
  * form add in rounded FP32.
  */
 size_t kda_decay_chunk_workspace_bytes(kda_dtype qkv_dtype, int B, int T, int H, int K, int V,

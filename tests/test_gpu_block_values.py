@@ -1,5 +1,5 @@
 """Decayed attention on values at the edge of its types, against float64: what is not finite stays behind
-its token.
+its token, large states do not overflow before float32 does.
 
 Bounds as in test_gpu_block (u = 2^-24, w = 2^-8).
 """
@@ -8,7 +8,7 @@ import torch
 
 import block_reference as ref
 from block_reference import F32, HALF
-from test_gpu_block import BF, close, dev, inputs, kda  # noqa: F401
+from test_gpu_block import BF, check, close, dev, inputs, kda  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 FORMS = ["kda_decay_chunk_fwd", "kda_decay_recurrent_fwd"]
@@ -42,3 +42,19 @@ def test_a_decay_that_is_no_number(kda, fn, dtype, K, V, T, at):  # noqa: F811
     so, sS = torch.zeros(o.shape, dtype=torch.bool), torch.zeros(S.shape, dtype=torch.bool)
     so[0, at:, 1], sS[0, 1] = True, True
     compare_elsewhere(fn, x, o, S, so, sS)
+
+
+@pytest.mark.parametrize("fn", FORMS)
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("K", [128, 256])
+@pytest.mark.parametrize("power", [-70, 100, 110])
+@pytest.mark.parametrize("rate", [0.0125, 0.1])
+def test_large_and_small_values(kda, fn, dtype, K, power, rate):  # noqa: F811
+    """States and values far from 1 under decays that add up over many chunks, in one whole sequence."""
+    q, k, v, decay, S0 = inputs(power, 1, 2200, 1, 1, K, 64, dtype, 1, fixed=True)
+    decay.fill_(-rate)
+    try:
+        kda.kda_test_hooks(sm_count=1)
+        check(kda, fn, (q, k, v * 2.0 ** power, decay, S0 * 2.0 ** power), chunked="chunk" in fn)
+    finally:
+        kda.kda_test_hooks()
