@@ -874,7 +874,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 fence_proxy_async_smem();
             }
             uint32_t hi[2][8];
-            float2 rest[2][8];
+            float2 rest[2][8], odd = make_float2(0.f, 0.f);
             if (mine) {
 #pragma unroll
                 for (int g = 0; g < 4; g += 2) {
@@ -894,7 +894,17 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 if (j + 1 >= len) x.y = 0.f;
                             }
                             hi[y][2 * g + e] = cut(x);
+                            odd = fma2(x, make_float2(0.f, 0.f), odd);
                         }
+                    }
+                }
+                // what is not finite leaves no number: then the first term alone is the value
+                if (odd.x != 0.f || odd.y != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2& x = rest[e >> 3][e & 7];
+                        if (x.x != x.x) x.x = 0.f;
+                        if (x.y != x.y) x.y = 0.f;
                     }
                 }
             }

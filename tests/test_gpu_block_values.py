@@ -58,3 +58,24 @@ def test_large_and_small_values(kda, fn, dtype, K, power, rate):  # noqa: F811
         check(kda, fn, (q, k, v * 2.0 ** power, decay, S0 * 2.0 ** power), chunked="chunk" in fn)
     finally:
         kda.kda_test_hooks()
+
+
+@pytest.mark.parametrize("fn", FORMS)
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64), (128, 64), (256, 256), (40, 72)])
+@pytest.mark.parametrize("T,at", [(200, 0), (200, 37), (200, 199), (700, 300)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_state_of_a_value_that_is_not_finite(kda, fn, dtype, K, V, T, at, bad):  # noqa: F811
+    """An infinite value makes an infinite state, with its key's signs; other channels have nothing of it."""
+    q, k, v, decay, S0 = inputs(T + at, 1, T, 2, 2, K, V, dtype, 1, span=0.1)
+    d = (7 * at + 3) % V
+    v[0, at, 1, d] = 0
+    k[0, at, 1] = torch.where(k[0, at, 1] == 0, torch.ones((), dtype=dtype), k[0, at, 1])  # (0 x inf is no number)
+    _, S_ref, _, Sa = ref.decay_attention(q, k, v, decay, S0)
+    v[0, at, 1, d] = bad
+    _, S = getattr(kda, fn)(dev(q), dev(k), dev(v), dev(decay), initial_state=dev(S0), output_final_state=True)
+    S = S.double().cpu()
+    want = torch.sign(k[0, at, 1].double()) * bad
+    assert torch.equal(S[0, 1, :, d].nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+    S[0, 1, :, d] = S_ref[0, 1, :, d]
+    close(S, S_ref, (K + 128 + T) * F32 * Sa + 1e-30, "state")
