@@ -92,6 +92,24 @@ __device__ __forceinline__ void load_rows(const T* base, size_t stride, int rows
     }
 }
 
+// [32 rows from j0][64 columns from c0] of v.  A masked score is 0, and 0 times a value that is not finite is NaN:
+// such values are left out, and the first row of each column that has one is noted.
+template <typename T>
+__device__ __forceinline__ void load_values(const T* base, size_t stride, int j0, int len, int c0, int n, int* first, float* out) {
+    for (int x = threadIdx.x; x < 32 * 16; x += NT) {
+        const int j = j0 + (x >> 4), c = 4 * (x & 15);
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j < len) load4(base + j * stride, c0 + c, n, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (!(fabsf(r[e]) < __int_as_float(0x7f800000))) {
+                r[e] = 0.f;
+                atomicMin(first + c + e, j);
+            }
+        *reinterpret_cast<float4*>(out + (x >> 4) * LD + c) = make_float4(r[0], r[1], r[2], r[3]);
+    }
+}
+
 // acc[i][j] += sum_{x < n} A[x][4 ti + i] B[x][4 tj + j]
 __device__ __forceinline__ void tile_product(const float* A, const float* B, int n, int ti, int tj, float (&acc)[4][4]) {
 #pragma unroll 8
@@ -180,7 +198,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
     float* sq = sm;               // [Kp][LD] q, transposed
     float* sp = sq + Kp * LD;     // [64][LD] P, transposed
     float* sx = sp + C * LD;      // [32][LD] a slice of k (transposed), S or v
-    __shared__ int sI[3][C];
+    __shared__ int sI[3][C], s_odd[64];
     int n, t0, len, bos, eos;
     if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
     const int h = blockIdx.y, tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
@@ -222,9 +240,10 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] *= f;
         }
+        if (tid < 64) s_odd[tid] = C;  // (the products' barriers lie behind the last block's reads)
         for (int j0 = 0; j0 < C; j0 += 32) {
             __syncthreads();
-            load_rows(v + ((size_t)(t0 + j0) * p.H + h) * p.V, (size_t)p.H * p.V, 32, len - j0, d0, p.V, nullptr, sx);
+            load_values(v + ((size_t)t0 * p.H + h) * p.V, (size_t)p.H * p.V, j0, len, d0, p.V, s_odd, sx);
             __syncthreads();
             tile_product(sp + j0 * LD, sx, 32, ti, tj, acc);
         }
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
             OT* dst = o + ((size_t)(t0 + r) * p.H + h) * p.V + d0 + 4 * tj;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (d0 + 4 * tj + j < p.V) dst[j] = from_f32<OT>(acc[i][j] * scale);
+                if (d0 + 4 * tj + j < p.V) dst[j] = from_f32<OT>(acc[i][j] * scale + nan_if(r >= s_odd[4 * tj + j]));
         }
     }
 }

@@ -18,6 +18,10 @@
 // results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
 // difference of an integer and of a fraction part (integer sums), exact whatever the sums.
 //
+// A masked score is 0, and 0 times a value that is not finite is NaN: such values are taken out of the tile
+// before P meets them, and their channel's outputs are NaN from their token on (the first row of each
+// channel is noted, GT_MARK).  The state has them as they are.
+//
 // Roundings: P and the copy of S that O1 reads are bf16 (each adds the output's own rounding once
 // more; both in quadrature keep o's error within 1.45 of one rounding).  The state is a float32 output and
 // feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits) and S is accumulated
@@ -55,7 +59,7 @@ __device__ unsigned int g_decay_timeouts = 0;
 constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8, kTop = 32;
 
 // barriers
-enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + 2, B_SBF, B_VD, B_STATE, B_INTER, B_O,
+enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + NS, B_SBF, B_VD, B_STATE, B_INTER, B_O,
        B_OFREE = B_O + 2, B_DRAIN, B_DRAIN2, B_DRAIN3, B_NEVER, NBAR };
 
 // The decay factors of a chunk, one slot of a ring of NG (written when the chunk is loaded, read
@@ -66,13 +70,14 @@ constexpr uint32_t GT_KEY = 768;   // [64] 2^(G_l - G_j - E'), the values' facto
 constexpr uint32_t GT_COL = 1024;  // [64] 2^(G_m - G_j), m the last of j's 16 rows
 constexpr uint32_t GT_LAST = 1280; // the stored state's factor before this chunk's product, 1: none
 constexpr uint32_t GT_OUT = 1284;  // 2^E'
-constexpr uint32_t GT_BYTES = 1296;
+constexpr uint32_t GT_MARK = 1296; // [128] bytes: each channel's first row with a value that is not finite, 64: none
+constexpr uint32_t GT_BYTES = 1424;
 
 template <int KD, int VB>
 struct Layout {
     static constexpr uint32_t QB = C * KD * 2, VBYTES = C * VB * 2, STAGE = 2 * QB + VBYTES;
     static constexpr uint32_t P = NS * STAGE, O = P + 2 * C * C * 2, G = O + VBYTES;
-    static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = BAR + 8 * NBAR, END = MISC + 16;
+    static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = (BAR + 8 * NBAR + 15) / 16 * 16, END = MISC + 16;
     // an A operand of 64 value channels is read as 128: up to 8 KB behind its tile
     static constexpr uint32_t BYTES = END + 1024 + 64;
 };
@@ -165,6 +170,18 @@ __device__ __forceinline__ void sts(uint32_t a, float v) { asm volatile("st.shar
 __device__ __forceinline__ void sts2(uint32_t a, float x, float y) {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
 }
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint16_t v) { asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory"); }
 __device__ __forceinline__ void ld_s128(uint32_t a, uint32_t* v) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
@@ -241,6 +258,33 @@ __device__ __forceinline__ uint32_t cut(float2& x) {
     return __byte_perm(a, b, 0x7632);
 }
 
+// Values that are not finite in the `len` rows of a tile of VB channels: cleared, and each channel's first of them
+// noted.  (By one warp, out of line and rolled: it runs where something is wrong, if ever.)
+template <int VB>
+__device__ __noinline__ void hide_odd(uint32_t tile, int len, uint32_t marks) {
+#pragma unroll 1
+    for (int ch = threadIdx.x & 31; ch < VB; ch += 32) {
+        int first = C;
+#pragma unroll 1
+        for (int r = len - 1; r >= 0; --r) {
+            const uint32_t at = tile + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7);
+            if ((lds16(at) & 0x7F80) != 0x7F80) continue;
+            sts16(at, 0);
+            first = r;
+        }
+        sts8(marks + ch, first);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+// ... and a noted channel's outputs (one channel a lane) in a tile of bf16 rows, where bit 0 says that there are notes
+__device__ __noinline__ void nan_rows(uint32_t tile, uint32_t marks, int ch, uint32_t odd) {
+    __syncwarp();  // (a warp's 32 channels have been stored by all its lanes)
+    if (odd & 1u)
+#pragma unroll 1
+        for (int r = (int)lds8(marks + ch); r < C; ++r) sts16(tile + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7), 0x7FFF);
+}
+
 // Whole sequences of one length, more units than SMs, the last wave part-empty: the units' chunks are
 // laid end to end and shared out evenly, `per` (at least a unit's nt) an SM, so a unit that does not fit into what
 // is left of an SM is cut.  Its part on the next SM, which is that SM's first work, is the earlier one in time;
@@ -302,7 +346,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L::MISC);
-    const Sync sy{sb + L::BAR, misc + 1, p.status};
+    const Sync sy{sb + L::BAR, misc + 2, p.status};
     // (the aligned base is not known to be shared memory: a slot's floats are read by address)
     auto gates = [&](int c) { return sb + L::G + (uint32_t)(c % NG) * GT_BYTES; };
     const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), l = tid & 31;
@@ -362,13 +406,13 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int count = 1;
             if (i >= B_FULL && i < B_FULL + NS) count = 2;                 // the loads and the decay factors
             if (i >= B_FREE && i < B_FREE + NS) count = kStates ? 1 : 2;   // the products of both issuing warps
-            if (i == B_P || i == B_P + 1) count = 4;                       // four P warps
+            if (i >= B_P && i < B_P + NS) count = 4 + 8;                   // four P warps, eight that have looked at v
             if (i == B_OFREE) count = 4;                                   // four output warps
             if (i >= B_S && i <= B_VD) count = 8;                          // eight warps
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
-        misc[1] = 0;
+        misc[2] = misc[3] = 0;  // given up; a bit for each slot of the factors' ring that ever had notes
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
@@ -445,7 +489,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (l == 0) mbar_arrive(sy.bar(B_P + b));
+                if (l == 0) mbar_arrive(sy.bar(B_P + c % NS));
             }
         }
     } else if (w == 25) {
@@ -543,7 +587,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 moved = true;
             }
             if constexpr (!kStates) {
-                if (nq < c && (nq < 1 || ready(B_P + ((nq - 1) & 1), ((nq - 1) >> 1) & 1, 0)) &&
+                if (nq < c && (nq < 1 || ready(B_P + (nq - 1) % NS, ((nq - 1) / NS) & 1, 0)) &&
                     ready(B_FULL + nq % NS, (nq / NS) & 1, 200)) {
                     const uint32_t qa = lo_k(sb + (nq % NS) * L::STAGE), ka = qa + (L::QB >> 4);
                     tc_fence_after();
@@ -623,9 +667,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     umma_commit(sy.bar(B_INTER));
                 }
                 __syncwarp();
-                if (!sy.warp_wait(B_P + b, (c >> 1) & 1)) break;
-                // v's rows behind the sequence are cleared with the last chunk's scaled values
-                if (c + 1 == nt && !sy.warp_wait(B_VD, c & 1)) break;
+                if (!sy.warp_wait(B_P + s, (c / NS) & 1)) break;  // (v's rows behind the sequence are cleared, too)
+                if ((misc[3] >> (c % NG)) & 1u) hide_odd<VB>(sb + s * L::STAGE + 2 * L::QB, min(C, eos - (bos + c * C)), gates(c) + GT_MARK);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
@@ -826,7 +869,14 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     }
                 }
-                if constexpr (kStaged) {
+                if constexpr (!kStaged) {
+                    if ((misc[3] >> (c % NG)) & 1u) {
+#pragma unroll 1
+                        for (int r = mine ? (int)lds8(gates(c) + GT_MARK + vl) : C; r < len; ++r)
+                            dst[r * step + vl] = to_out<OT>(__int_as_float(0x7fffffff));
+                    }
+                } else {
+                    if (__any_sync(0xffffffffu, mine && misc[3] != 0u)) nan_rows(sb + L::O, gates(c) + GT_MARK, vl, misc[3] >> (c % NG));
                     fence_proxy_async_smem();
                     bar_sync(1, 128);
                     if (sy.aborted()) {
@@ -900,6 +950,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 // what is not finite leaves no number: then the first term alone is the value
                 if (odd.x != 0.f || odd.y != 0.f) {
+                    atomicOr(const_cast<uint32_t*>(misc + 3), 1u << (c % NG));
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float2& x = rest[e >> 3][e & 7];
@@ -907,6 +958,10 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (x.y != x.y) x.y = 0.f;
                     }
                 }
+            }
+            if constexpr (!kStates) {
+                __syncwarp();
+                if (l == 0) mbar_arrive(sy.bar(B_P + s));
             }
             if (c > 0 && !sy.warp_wait(B_STATE, (c - 1) & 1)) break;
             tc_fence_after();

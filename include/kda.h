@@ -377,7 +377,8 @@ typedef enum {
  * computes token by token in FP32.
  *
  * What is not finite never reaches back: a decay that is NaN makes its head's outputs
- * NaN from its token on.
+ * NaN from its token on; a value (an element of v) that is not finite makes its channel's
+ * outputs NaN from its token to its chunk's end and, through the state, not finite behind it.
  *
  * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores, which cut
  * what they add to an FP32 accumulator: the states lean to zero by about 8e-7

@@ -1,5 +1,5 @@
 """Decayed attention on values at the edge of its types, against float64: what is not finite stays behind
-its token, large states do not overflow before float32 does.
+its token and in its channel, large states do not overflow before float32 does.
 
 Bounds as in test_gpu_block (u = 2^-24, w = 2^-8).
 """
@@ -27,6 +27,25 @@ def compare_elsewhere(fn, x, o, S, spoiled_o, spoiled_S):
     half = HALF[BF] if q.dtype == BF else F32
     close(o, o_ref, half * o_ref.abs() + (operand + f32) * oa + 1e-30, "o")
     close(S, S_ref, f32 * Sa + 1e-30, "state")
+
+
+@pytest.mark.parametrize("fn", FORMS)
+@pytest.mark.parametrize("dtype,o_dtype", [(torch.float32, None), (BF, None), (BF, torch.float32)])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64), (128, 64), (256, 256), (40, 72)])
+@pytest.mark.parametrize("T,at", [(200, 0), (200, 37), (200, 64), (200, 199), (700, 300)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_value_that_is_not_finite(kda, fn, dtype, o_dtype, K, V, T, at, bad):  # noqa: F811
+    """One element of v: outputs before its token, of other channels and of other heads stay right."""
+    q, k, v, decay, S0 = x = inputs(T + at, 1, T, 2, 2, K, V, dtype, 1, span=0.1)
+    d = (7 * at + 3) % V
+    v[0, at, 1, d] = 0
+    bad_v = v.clone()
+    bad_v[0, at, 1, d] = bad
+    o, S = getattr(kda, fn)(dev(q), dev(k), dev(bad_v), dev(decay), initial_state=dev(S0), output_final_state=True,
+                            o_dtype=o_dtype)
+    so, sS = torch.zeros(o.shape, dtype=torch.bool), torch.zeros(S.shape, dtype=torch.bool)
+    so[0, at:, 1, d], sS[0, 1, :, d] = True, True
+    compare_elsewhere(fn, x, o, S, so, sS)
 
 
 @pytest.mark.parametrize("fn", FORMS)
