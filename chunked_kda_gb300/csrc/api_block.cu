@@ -20,7 +20,24 @@ bool aligned(P... ptrs) {
 }
 const char* const kMisaligned = "pointers must be 16-byte aligned";
 
-kda_status check_decay(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* decay,
+// A buffer of a call.  Blocks of one launch read and write in no order, so an output may share memory with an
+// input only where each element is read by the thread that later writes it: the very same buffer, where the
+// kernels keep to that.
+struct Buffer {
+    const void* p;
+    size_t bytes;
+};
+bool apart(Buffer a, Buffer b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return !x || !y || !a.bytes || !b.bytes || x + a.bytes <= y || y + b.bytes <= x;
+}
+bool same_or_apart(Buffer a, Buffer b) { return (a.p == b.p && a.bytes == b.bytes) || apart(a, b); }
+template <typename... B>
+bool all_apart(Buffer a, B... b) {
+    return (apart(a, b) && ...);
+}
+
+kda_status check_decay(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* decay, bool per_token,
                        const float* h0, const float* hT, const int32_t* cu, int n_seqs, int B, int T, int H,
                        int n_qk_heads, int K, int V, const void* o, kda_dtype o_dtype, int* N) {
     if (n_qk_heads < 0 || (n_qk_heads > 0 && (H <= 0 || H % n_qk_heads != 0)))
@@ -35,6 +52,16 @@ kda_status check_decay(const void* q, const void* k, const void* v, kda_dtype qk
     if ((long long)B * T > 0 && *N > 0 && (!q || !k || !v || !decay || !o))
         return fail(KDA_ERR_INVALID_ARG, "null q, k, v, decay or o");
     if (!aligned(q, k, v, decay, h0, hT, o)) return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    if (*N == 0) return KDA_OK;
+    const size_t e = qkv_dtype == KDA_BF16 ? 2 : 4, tokens = (size_t)B * T, Hk = n_qk_heads > 0 ? n_qk_heads : H;
+    const size_t qk = tokens * Hk * K * e, state = (size_t)*N * H * K * V * 4;
+    const Buffer bq{q, qk}, bk{k, qk}, bv{v, tokens * H * V * e}, bd{decay, (per_token ? tokens : 1) * H * 4};
+    const Buffer b0{h0, state}, bT{hT, state}, bo{o, tokens * H * V * (o_dtype == KDA_BF16 ? 2 : 4)};
+    const Buffer bc{cu, cu ? (size_t)(*N + 1) * 4 : 0};
+    if (!all_apart(bo, bq, bk, bd, b0, bT, bc) || !same_or_apart(bo, bv))
+        return fail(KDA_ERR_INVALID_ARG, "o must not overlap an input or a state");
+    if (!all_apart(bT, bq, bk, bv, bd, bc) || !same_or_apart(bT, b0))
+        return fail(KDA_ERR_INVALID_ARG, "final_state must not overlap an input (it may be initial_state)");
     return KDA_OK;
 }
 
@@ -56,8 +83,8 @@ kda_status kda_decay_chunk_fwd(const void* q, const void* k, const void* v, kda_
                                size_t workspace_bytes, int32_t* status, kda_stream_t stream) {
     kda::record_error("");
     int N = 0;
-    const kda_status st = check_decay(q, k, v, qkv_dtype, decay, initial_state, final_state, cu_seqlens, n_seqs, B,
-                                      T, H, n_qk_heads, K, V, o, o_dtype, &N);
+    const kda_status st = check_decay(q, k, v, qkv_dtype, decay, decay_per_token != 0, initial_state, final_state,
+                                      cu_seqlens, n_seqs, B, T, H, n_qk_heads, K, V, o, o_dtype, &N);
     if (st != KDA_OK) return st;
     if (N == 0) return KDA_OK;
     const size_t need = kda::decay_chunk_workspace_bytes(qkv_dtype == KDA_BF16, B, T, H, K, V, N, cu_seqlens != nullptr);
@@ -77,8 +104,8 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v, 
                                    int n_qk_heads, int K, int V, void* o, kda_dtype o_dtype, kda_stream_t stream) {
     kda::record_error("");
     int N = 0;
-    const kda_status st = check_decay(q, k, v, qkv_dtype, decay, initial_state, final_state, cu_seqlens, n_seqs, B,
-                                      T, H, n_qk_heads, K, V, o, o_dtype, &N);
+    const kda_status st = check_decay(q, k, v, qkv_dtype, decay, decay_per_token != 0, initial_state, final_state,
+                                      cu_seqlens, n_seqs, B, T, H, n_qk_heads, K, V, o, o_dtype, &N);
     if (st != KDA_OK) return st;
     const kda::DecayArgs a{q, k, v, qkv_dtype == KDA_BF16, decay, decay_per_token != 0, initial_state, final_state,
                            cu_seqlens, N, B, T, H, n_qk_heads > 0 ? n_qk_heads : H, K, V, o, o_dtype == KDA_F32,
@@ -97,6 +124,10 @@ kda_status kda_gated_norm_fwd(const void* x, const void* gate, kda_dtype dtype, 
     if (rows == 0) return KDA_OK;
     if (!x || !gate || !y) return fail(KDA_ERR_INVALID_ARG, "null x, gate or y");
     if (!aligned(x, gate, weight, y)) return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    const size_t bytes = (size_t)rows * V * (dtype == KDA_BF16 ? 2 : 4);
+    const Buffer by{y, bytes};
+    if (!same_or_apart(by, {x, bytes}) || !same_or_apart(by, {gate, bytes}) || !apart(by, {weight, (size_t)V * 4}))
+        return fail(KDA_ERR_INVALID_ARG, "y must not overlap weight, or x or gate in part (it may be x or gate)");
     const kda::GatedNormArgs a{x, gate, dtype == KDA_BF16, weight, eps, (int)act, (long)rows, V, y, (cudaStream_t)stream};
     return kda::launch_status(kda::launch_gated_norm(a));
 }
@@ -115,6 +146,14 @@ kda_status kda_block_norm_fwd(const void* x, kda_dtype dtype, const void* residu
     if (!x || (!h_out && !y_out)) return fail(KDA_ERR_INVALID_ARG, "null x, or neither h_out nor y_out");
     if (!aligned(x, residual, post_weight, gate, channel_scale, pre_weight, h_out, y_out))
         return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    const size_t n = (size_t)rows * D, bytes = n * (dtype == KDA_BF16 ? 2 : 4), per = (size_t)D * 4;
+    const Buffer bx{x, bytes}, bz{gate, bytes}, br{residual, n * (residual_dtype == KDA_BF16 ? 2 : 4)};
+    const Buffer bh{h_out, br.bytes}, by{y_out, bytes};
+    if (!apart(bh, by)) return fail(KDA_ERR_INVALID_ARG, "h_out and y_out must not overlap");
+    for (const Buffer& out : {bh, by})
+        if (!same_or_apart(out, bx) || !same_or_apart(out, bz) || !same_or_apart(out, br) ||
+            !all_apart(out, Buffer{post_weight, per}, Buffer{channel_scale, per}, Buffer{pre_weight, per}))
+            return fail(KDA_ERR_INVALID_ARG, "h_out and y_out must not overlap a weight, or an input in part");
     const kda::BlockNormArgs a{x, dtype == KDA_BF16, residual, residual_dtype == KDA_BF16, post_weight, gate, (int)act,
                                scale, channel_scale, pre_weight, eps, (long)rows, D, h_out, y_out, (cudaStream_t)stream};
     return kda::launch_status(kda::launch_block_norm(a));
@@ -136,6 +175,13 @@ kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weigh
     if ((long long)B * T == 0 && !final_state) return KDA_OK;
     if (!weight) return fail(KDA_ERR_INVALID_ARG, "null weight");
     if (!aligned(x, weight, bias, initial_state, final_state, y)) return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    const size_t e = dtype == KDA_BF16 ? 2 : 4, bytes = (size_t)B * T * D * e, state = (size_t)N * (W - 1) * D * e;
+    const Buffer bx{x, bytes}, by{y, bytes}, b0{initial_state, state}, b1{final_state, state};
+    const Buffer bw{weight, (size_t)D * W * 4}, bb{bias, (size_t)D * 4}, bc{cu_seqlens, cu_seqlens ? (size_t)(N + 1) * 4 : 0};
+    if (!all_apart(by, bx, bw, bb, b0, b1, bc))  // (a tile reads the W - 1 rows before it, which another block writes)
+        return fail(KDA_ERR_INVALID_ARG, "y must not overlap x, a weight or a state");
+    if (!all_apart(b1, bx, bw, bb, bc) || !same_or_apart(b1, b0))
+        return fail(KDA_ERR_INVALID_ARG, "final_state must not overlap an input (it may be initial_state)");
     const kda::ConvArgs a{x, dtype == KDA_BF16, weight, bias, (int)act, W, initial_state, final_state, cu_seqlens,
                           N, B, T, D, y, (cudaStream_t)stream};
     return kda::launch_status(kda::launch_short_conv(a));

@@ -342,7 +342,10 @@ kda_status kda_recurrent_fwd_ex(const void* q, const void* k, const void* v, kda
  * attention with a decay for each head, the gated norm of its heads, the norm
  * around the block, and the short causal convolution in front.  Forward only.
  * Conventions (device pointers, 16-byte alignment, packed sequences, host
- * checks, no allocation, no synchronisation, graph capture) as above.
+ * checks, no allocation, no synchronisation, graph capture) as above.  An output
+ * must not share memory with an input, a state or another output but where a call
+ * is said to work in place; where blocks of the launch would meet in it, the call is
+ * refused (KDA_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------------
  */
 
