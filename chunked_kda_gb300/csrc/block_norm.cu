@@ -15,14 +15,15 @@
 namespace kda {
 namespace {
 
-// 16 bytes of T as floats
+// 16 bytes of T as floats.  Outputs may be inputs (y is x or gate, h is the stream), so these are ordinary loads,
+// and no pointer to such rows is __restrict__: each thread reads its elements before it writes them.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
     static __device__ __forceinline__ void load(const float* p, float* r) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 a = *reinterpret_cast<const float4*>(p);
         r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
     }
     static __device__ __forceinline__ void store(float* p, const float* r) {
@@ -33,7 +34,7 @@ template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
     static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* r) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -66,6 +67,19 @@ __device__ __forceinline__ void store_e(T* p, const float* r) {
     else {
 #pragma unroll
         for (int i = 0; i < E; i += Vec<T>::N) Vec<T>::store(p + i, r + i);
+    }
+}
+
+// E weights, which no output is
+template <int E>
+__device__ __forceinline__ void load_weights(const float* p, float* r) {
+    if constexpr (E == 1) r[0] = __ldg(p);
+    else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+            r[i] = a.x; r[i + 1] = a.y; r[i + 2] = a.z; r[i + 3] = a.w;
+        }
     }
 }
 
@@ -104,9 +118,9 @@ __device__ __forceinline__ float gate_value(float z, int act) {
 // measured 138 us, and two or four rows a lane group, their loads issued together, 158 and 241 us.
 constexpr int kRowThreads = 128;
 template <typename T, int G>
-__global__ void __launch_bounds__(kRowThreads) gated_norm_rows_kernel(const T* __restrict__ x, const T* __restrict__ z,
+__global__ void __launch_bounds__(kRowThreads) gated_norm_rows_kernel(const T* x, const T* z,
                                                                       const float* __restrict__ w, float eps, int act,
-                                                                      long rows, int V, T* __restrict__ y) {
+                                                                      long rows, int V, T* y) {
     constexpr int E = Vec<T>::N;
     const int c = (threadIdx.x % G) * E;
     const long row = (long)blockIdx.x * (kRowThreads / G) + threadIdx.x / G;
@@ -120,10 +134,7 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_rows_kernel(const T* _
     if (in) {
         Vec<T>::load(x + row * V + c, a);
         Vec<T>::load(z + row * V + c, g);
-        if (w) {
-#pragma unroll
-            for (int i = 0; i < E; i += 4) Vec<float>::load(w + c + i, wv + i);
-        }
+        if (w) load_weights<E>(w + c, wv);
     }
     float sum = 0.f;
 #pragma unroll
@@ -140,9 +151,9 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_rows_kernel(const T* _
 // Gated norm, any row length: one warp per row, lanes step over the row in pieces of E elements,
 // twice.
 template <typename T, int E>
-__global__ void __launch_bounds__(256) gated_norm_kernel(const T* __restrict__ x, const T* __restrict__ z,
+__global__ void __launch_bounds__(256) gated_norm_kernel(const T* x, const T* z,
                                                          const float* __restrict__ w, float eps, int act,
-                                                         long rows, int V, T* __restrict__ y) {
+                                                         long rows, int V, T* y) {
     const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const int lane = threadIdx.x & 31;
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(256) gated_norm_kernel(const T* __restrict__ x
         float a[E], g[E], wv[E];
         load_e<T, E>(xr + c, a);
         load_e<T, E>(z + row * V + c, g);
-        if (w) load_e<float, E>(w + c, wv);
+        if (w) load_weights<E>(w + c, wv);
 #pragma unroll
         for (int i = 0; i < E; ++i) a[i] = a[i] * rs * (w ? wv[i] : 1.f) * gate_value<T>(g[i], act);
         store_e<T, E>(y + row * V + c, a);
@@ -188,7 +199,7 @@ template <typename T, int E, bool kShared = false>
 __device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c, float rs, float* h) {
     float t[E];
     if (a.post_w) {
-        load_e<float, E>(a.post_w + c, t);
+        load_weights<E>(a.post_w + c, t);
 #pragma unroll
         for (int i = 0; i < E; ++i) h[i] = h[i] * rs * t[i];
     }
@@ -199,7 +210,7 @@ __device__ __forceinline__ void scaled(const BlockNormArgs& a, const T* z, int c
         for (int i = 0; i < E; ++i) h[i] *= gate_value<T>(t[i], a.act);
     }
     if (a.channel_scale) {
-        load_e<float, E>(a.channel_scale + c, t);
+        load_weights<E>(a.channel_scale + c, t);
 #pragma unroll
         for (int i = 0; i < E; ++i) h[i] *= t[i];
     }
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(BlockNormArgs a) {
         if (c >= D) continue;
         if (a.pre_w) {
             float w[8];
-            load_e<float, 8>(a.pre_w + c, w);
+            load_weights<8>(a.pre_w + c, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[p][i] *= rp * w[i];
         }
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(BlockN
             if (c >= D) continue;
             if (a.pre_w) {
                 float w[8];
-                load_e<float, 8>(a.pre_w + c, w);
+                load_weights<8>(a.pre_w + c, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[p][i] *= rp * w[i];
             }
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(256) block_norm_any_kernel(BlockNormArgs a) {
         hidden(c, h);
         if (a.h) store_e<R, E>((R*)a.h + row * D + c, h);
         if (a.pre_w) {
-            load_e<float, E>(a.pre_w + c, t);
+            load_weights<E>(a.pre_w + c, t);
 #pragma unroll
             for (int i = 0; i < E; ++i) h[i] *= rp * t[i];
         }
