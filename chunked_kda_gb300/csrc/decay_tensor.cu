@@ -1186,7 +1186,7 @@ cudaError_t run(const DecayArgs& a) {
         if ((e = launch(decay_chunk_kernel<KD, VB, float, false>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess) return e;
     }
     if (tokens == 0) return cudaSuccess;
-    decay_join_kernel<OT><<<1216, 256, 0, a.stream>>>(half, half + pl.half / sizeof(float), (OT*)a.o, tokens,
+    decay_join_kernel<OT><<<8 * max(1, planned_sm_count()), 256, 0, a.stream>>>(half, half + pl.half / sizeof(float), (OT*)a.o, tokens,
                                                       a.cu ? a.cu + a.N : nullptr, (long)a.H * a.V / 4);
     return cudaGetLastError();
 }

@@ -304,7 +304,8 @@ cudaError_t launch_io(const ConvArgs& a) {
             (const T*)a.x, a.weight, a.bias, a.act, (const T*)a.s0, (T*)a.s1, a.cu, a.N, a.T, a.D, (T*)a.y);
         return cudaGetLastError();
     }
-    auto few = [&](int TT) { return (rows + TT - 1) / TT * blocks < 8 * 152; };
+    const int sms = planned_sm_count();
+    auto few = [&](int TT) { return (rows + TT - 1) / TT * blocks < 8l * sms; };
     int TT = few(64) ? few(16) ? 8 : 16 : 64;  // at least W - 1
     // (a grid's second dimension holds 65535 tiles)
     while ((rows + TT - 1) / TT > 65535) TT *= 2;
