@@ -163,7 +163,7 @@ def kda_decay_chunk_fwd(q, k, v, decay, initial_state=None, output_final_state=F
 
     q, k [B, T, Hk, K], v [B, T, H, V] (float32 or bfloat16, Hk a divisor of H), ``decay`` float32
     natural log, [B, T, H] or [H]; states float32 [N, H, K, V].  ``o_dtype`` is q's dtype or
-    torch.float32.  Packed sequences, in-place states, ``workspace``, ``status`` and ``stream`` as
+    torch.float32 (for bf16 inputs the exact one: no operand is rounded to bf16, about twice the time).  Packed sequences, in-place states, ``workspace``, ``status`` and ``stream`` as
     for kda_chunk_fwd."""
     return _decay(True, q, k, v, decay, initial_state, output_final_state, cu_seqlens, o, final_state, stream, o_dtype,
                   workspace, status)

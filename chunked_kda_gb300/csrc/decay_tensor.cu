@@ -22,8 +22,10 @@
 // before P meets them, and their channel's outputs are NaN from their token on (the first row of each
 // channel is noted, GT_MARK).  The state has them as they are.
 //
-// Roundings: P and the copy of S that O1 reads are bf16 (each adds the output's own rounding once
-// more; both in quadrature keep o's error within 1.45 of one rounding).  The state is a float32 output and
+// Roundings: for a bf16 output P and the copy of S that O1 reads are bf16 (each adds the output's own rounding
+// once more; both in quadrature keep o's error within 1.45 of one rounding).  A caller who wants more asks for a
+// float32 output: there both are three bf16 terms (24 bits), S's one after another through the copy's place
+// (kFine; 4 x 4096 tokens, 64 heads: 450 us, with a single term each 246).  The state is a float32 output and
 // feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits) and S is accumulated
 // from all three.  The tensor cores cut, not round, what they add to an FP32 accumulator, so S leans to
 // zero by about 8e-7 a chunk of its memory: 6e-6 at a fixed decay of -0.0023, 1e-4 after 32768 tokens
@@ -73,11 +75,14 @@ constexpr uint32_t GT_OUT = 1284;  // 2^E'
 constexpr uint32_t GT_MARK = 1296; // [128] bytes: each channel's first row with a value that is not finite, 64: none
 constexpr uint32_t GT_BYTES = 1424;
 
-template <int KD, int VB>
+// kFine: P and the state that the queries read in three bf16 terms each (24 bits), for a float32 output
+template <int KD, int VB, bool kFine = false>
 struct Layout {
     static constexpr uint32_t QB = C * KD * 2, VBYTES = C * VB * 2, STAGE = 2 * QB + VBYTES;
-    static constexpr uint32_t P = NS * STAGE, O = P + 2 * C * C * 2, G = O + VBYTES;
+    static constexpr uint32_t P = NS * STAGE, O = P + 2 * C * C * 2, G = O + (kFine ? 4 * C * C * 2 : VBYTES);
     static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = (BAR + 8 * NBAR + 15) / 16 * 16, END = MISC + 16;
+    // P's term and buffer: the second and third terms have the place of the staged output
+    __host__ __device__ static constexpr uint32_t term(int t, int b) { return t == 0 ? P + b * (C * C * 2) : O + (2 * b + t - 1) * (C * C * 2); }
     // an A operand of 64 value channels is read as 128: up to 8 KB behind its tile
     static constexpr uint32_t BYTES = END + 1024 + 64;
 };
@@ -258,6 +263,13 @@ __device__ __forceinline__ uint32_t cut(float2& x) {
     return __byte_perm(a, b, 0x7632);
 }
 
+// both floats in three terms
+__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = cut(x);
+    mid = cut(x);
+    lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
 // Values that are not finite in the `len` rows of a tile of VB channels: cleared, and each channel's first of them
 // noted.  (By one warp, out of line and rolled: it runs where something is wrong, if ever.)
 template <int VB>
@@ -337,11 +349,12 @@ __device__ __forceinline__ Piece cut_piece(const Params& p, int* scratch) {
 }
 
 // kStates: only the state a segment adds (no queries, no output), for the segments' scan.
-template <int KD, int VB, typename OT, bool kStates>
+template <int KD, int VB, typename OT, bool kStates, bool kFine = false>
 __global__ void __launch_bounds__(NTHR, 1)
 decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, Params p) {
-    using L = Layout<KD, VB>;
+    using L = Layout<KD, VB, kFine>;
+    constexpr int kTerms = kFine ? 3 : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
@@ -435,7 +448,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int srow = 16 * w + (l & 15), spiece = l >> 4;
             for (int x = l; x < 2 * 16 * 8; x += 32) {  // the blocks right of the diagonal stay zero
                 const int row = 16 * w + (x & 15), piece = (x >> 4) & 7;
-                if (piece > 2 * w + 1) st_s128(sb + L::P + (x >> 7) * (C * C * 2) + sw128(row, piece), 0, 0, 0, 0);
+                if (piece > 2 * w + 1)
+#pragma unroll
+                    for (int t = 0; t < kTerms; ++t) st_s128(sb + L::term(t, x >> 7) + sw128(row, piece), 0, 0, 0, 0);
             }
 #pragma unroll 1
             for (int c = 0; c < nt; ++c) {
@@ -455,16 +470,25 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float f0 = scale * ex2_fast((g0.x - gm.x) + (g0.y - gm.y));
                     const float f1 = scale * ex2_fast((g1.x - gm.x) + (g1.y - gm.y));
                     tmem_wait_ld();
-                    uint32_t r[4];
+                    uint32_t r[4], r1[4], r2[4];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float2 f = lds2(gt + GT_COL + 4 * (16 * cb + 8 * g + cp));
                         const float2 y0 = mul2(make_float2(x[4 * g], x[4 * g + 1]), mul2(f, make_float2(f0, f0)));
                         const float2 y1 = mul2(make_float2(x[4 * g + 2], x[4 * g + 3]), mul2(f, make_float2(f1, f1)));
-                        r[2 * g] = pack_bf16(y0.x, y0.y);
-                        r[2 * g + 1] = pack_bf16(y1.x, y1.y);
+                        if constexpr (kFine) {
+                            split(y0, r[2 * g], r1[2 * g], r2[2 * g]);
+                            split(y1, r[2 * g + 1], r1[2 * g + 1], r2[2 * g + 1]);
+                        } else {
+                            r[2 * g] = pack_bf16(y0.x, y0.y);
+                            r[2 * g + 1] = pack_bf16(y1.x, y1.y);
+                        }
                     }
                     stmatrix4(to + sw128(srow, 2 * cb + spiece), r);
+                    if constexpr (kFine) {
+                        stmatrix4(sb + L::term(1, b) + sw128(srow, 2 * cb + spiece), r1);
+                        stmatrix4(sb + L::term(2, b) + sw128(srow, 2 * cb + spiece), r2);
+                    }
                 }
                 {
                     float x[8];
@@ -472,7 +496,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     g0.y += log2_scale;
                     g1.y += log2_scale;
                     tmem_wait_ld();
-                    uint32_t r[4];
+                    uint32_t r[4], r1[4], r2[4];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const int j = 8 * g + cp, i = l >> 2;  // within the block
@@ -481,10 +505,19 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const float y1 = x[4 * g + 1] * ex2_fast((g0.x - gj.z) + (g0.y - gj.w));
                         const float y2 = x[4 * g + 2] * ex2_fast((g1.x - gj.x) + (g1.y - gj.y));
                         const float y3 = x[4 * g + 3] * ex2_fast((g1.x - gj.z) + (g1.y - gj.w));
-                        r[2 * g] = pack_bf16(j <= i ? y0 : 0.f, j + 1 <= i ? y1 : 0.f);
-                        r[2 * g + 1] = pack_bf16(j <= i + 8 ? y2 : 0.f, j + 1 <= i + 8 ? y3 : 0.f);
+                        if constexpr (kFine) {
+                            split(make_float2(j <= i ? y0 : 0.f, j + 1 <= i ? y1 : 0.f), r[2 * g], r1[2 * g], r2[2 * g]);
+                            split(make_float2(j <= i + 8 ? y2 : 0.f, j + 1 <= i + 8 ? y3 : 0.f), r[2 * g + 1], r1[2 * g + 1], r2[2 * g + 1]);
+                        } else {
+                            r[2 * g] = pack_bf16(j <= i ? y0 : 0.f, j + 1 <= i ? y1 : 0.f);
+                            r[2 * g + 1] = pack_bf16(j <= i + 8 ? y2 : 0.f, j + 1 <= i + 8 ? y3 : 0.f);
+                        }
                     }
                     stmatrix4(to + sw128(srow, 2 * w + spiece), r);
+                    if constexpr (kFine) {
+                        stmatrix4(sb + L::term(1, b) + sw128(srow, 2 * w + spiece), r1);
+                        stmatrix4(sb + L::term(2, b) + sw128(srow, 2 * w + spiece), r2);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -656,23 +689,31 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
             for (int c = 0; c < nt; ++c) {
                 const int s = c % NS, b = c & 1;
-                const uint32_t q = lo_k(sb + s * L::STAGE), v = lo_mn(sb + s * L::STAGE + 2 * L::QB), pb = lo_k(sb + L::P + b * (C * C * 2));
-                if (!sy.warp_wait(B_SBF, c & 1)) break;
-                if (c >= 1 && !sy.warp_wait(B_OFREE, (c - 1) & 1)) break;  // the output warps have read the last chunk's
-                tc_fence_after();
-                if (elect()) {
+                const uint32_t q = lo_k(sb + s * L::STAGE), v = lo_mn(sb + s * L::STAGE + 2 * L::QB);
+                bool ok = true;
+#pragma unroll 1
+                for (int t = 0; t < kTerms; ++t) {  // (the terms come one after another into one place)
+                    if (!(ok = sy.warp_wait(B_SBF, (kTerms * c + t) & 1))) break;
+                    if (c >= 1 && t == 0 && !(ok = sy.warp_wait(B_OFREE, (c - 1) & 1))) break;  // the output warps have read the last chunk's
+                    tc_fence_after();
+                    if (elect()) {
 #pragma unroll
-                    for (int kk = 0; kk < KD / 16; ++kk)
-                        umma_bf16_ta(tmem + TM_O1, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_o1, kk > 0);
-                    umma_commit(sy.bar(B_INTER));
+                        for (int kk = 0; kk < KD / 16; ++kk)
+                            umma_bf16_ta(tmem + TM_O1, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_o1, kk > 0 || t > 0);
+                        umma_commit(sy.bar(B_INTER));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 if (!sy.warp_wait(B_P + s, (c / NS) & 1)) break;  // (v's rows behind the sequence are cleared, too)
                 if ((misc[3] >> (c % NG)) & 1u) hide_odd<VB>(sb + s * L::STAGE + 2 * L::QB, min(C, eos - (bos + c * C)), gates(c) + GT_MARK);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) umma_bf16(tmem + TM_O2, desc(v + kk * 128), desc(pb + kk * 2), id_o2, kk > 0);
+                    for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(tmem + TM_O2, desc(v + kk * 128), desc(lo_k(sb + L::term(t, b)) + kk * 2), id_o2, kk > 0 || t > 0);
                     umma_commit(sy.bar(B_O + b));
                     if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
                 }
@@ -745,7 +786,47 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (l == 0) mbar_arrive(sy.bar(bar));
             };
             constexpr int NC = KD / 2;  // this warp's columns
-            uint32_t r[NC / 2];         // their bf16 copy
+            if constexpr (kFine) {
+                // the three terms one after another, then the scaling: nothing at once, for its registers
+#pragma unroll 1
+                for (int t = 0; t < kTerms && ok; ++t) {
+                    if (c + t > 0 && !(ok = sy.warp_wait(B_INTER, (kTerms * c + t - 1) & 1))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < NC; x += 32) {
+                        float v[32];
+                        uint32_t r[16];
+                        ld32(tmem + TM_S + lane + c0 + x, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            uint32_t r1, r2;
+                            split(make_float2(v[2 * j], v[2 * j + 1]), r[j], r1, r2);
+                            r[j] = t == 0 ? r[j] : t == 1 ? r1 : r2;
+                        }
+                        tmem_st16(tmem + TM_SB + lane + (c0 + x) / 2, r);
+                    }
+                    tmem_wait_st();
+                    arrive(B_SBF);
+                }
+                if (!ok) break;
+                if (gl != 1.f) {
+#pragma unroll 1
+                    for (int x = 0; x < NC; x += 16) {
+                        float v[16];
+                        uint32_t u[16];
+                        tmem_ld16(tmem + TM_S + lane + c0 + x, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * gl);
+                        tmem_st16(tmem + TM_S + lane + c0 + x, u);
+                    }
+                    tmem_wait_st();
+                }
+                arrive(B_S);
+                continue;
+            }
+            uint32_t r[NC / 2];  // their bf16 copy
 #pragma unroll
             for (int x = 0; x < NC; x += 32) {
                 if (kStates && gl == 1.f) continue;
@@ -779,7 +860,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
         if (nt > 0 && ok) ok = sy.warp_wait(B_STATE, (nt - 1) & 1);
-        if (!kStates && nt > 0 && ok) ok = sy.warp_wait(B_INTER, (nt - 1) & 1);
+        if (!kStates && nt > 0 && ok) ok = sy.warp_wait(B_INTER, (kTerms * nt - 1) & 1);
         if (nt > 0 && ok) {
             tc_fence_after();
             const float out = lds(gates(nt - 1) + GT_OUT);
@@ -1144,6 +1225,8 @@ cudaError_t launch(Kernel kern, uint32_t bytes, dim3 grid, cudaStream_t stream, 
 template <int KD, int VB, typename OT>
 cudaError_t run(const DecayArgs& a) {
     using L = Layout<KD, VB>;
+    constexpr bool kFine = sizeof(OT) == 4;  // a float32 output is worth 24 bits of its operands
+    constexpr uint32_t kBytes = Layout<KD, VB, kFine>::BYTES;
     CUtensorMap m[4];  // q, k, v, o (a stand-in for a float32 o, which leaves by plain stores)
     const long tokens = (long)a.B * a.T;
     if (tokens == 0 && !a.hT) return cudaSuccess;
@@ -1177,18 +1260,21 @@ cudaError_t run(const DecayArgs& a) {
     p.k0 = 0;
     if (a.K == KD) {
         if ((e = clear()) != cudaSuccess) return e;
-        return launch(decay_chunk_kernel<KD, VB, OT, false>, L::BYTES, grid, a.stream, m, p);
+        return launch(decay_chunk_kernel<KD, VB, OT, false, kFine>, kBytes, grid, a.stream, m, p);
     }
-    float* half = (float*)(ws + pl.bytes - 2 * pl.half);
-    for (; p.k0 < a.K; p.k0 += KD) {
-        p.o = p.k0 == 0 ? half : half + pl.half / sizeof(float);
-        if ((e = clear()) != cudaSuccess) return e;
-        if ((e = launch(decay_chunk_kernel<KD, VB, float, false>, L::BYTES, grid, a.stream, m, p)) != cudaSuccess) return e;
+    if constexpr (KD < 128) return cudaErrorInvalidValue;  // (a head of 256 is two of 128)
+    else {
+        float* half = (float*)(ws + pl.bytes - 2 * pl.half);
+        for (; p.k0 < a.K; p.k0 += KD) {
+            p.o = p.k0 == 0 ? half : half + pl.half / sizeof(float);
+            if ((e = clear()) != cudaSuccess) return e;
+            if ((e = launch(decay_chunk_kernel<KD, VB, float, false, kFine>, kBytes, grid, a.stream, m, p)) != cudaSuccess) return e;
+        }
+        if (tokens == 0) return cudaSuccess;
+        decay_join_kernel<OT><<<8 * max(1, planned_sm_count()), 256, 0, a.stream>>>(
+            half, half + pl.half / sizeof(float), (OT*)a.o, tokens, a.cu ? a.cu + a.N : nullptr, (long)a.H * a.V / 4);
+        return cudaGetLastError();
     }
-    if (tokens == 0) return cudaSuccess;
-    decay_join_kernel<OT><<<8 * max(1, planned_sm_count()), 256, 0, a.stream>>>(half, half + pl.half / sizeof(float), (OT*)a.o, tokens,
-                                                      a.cu ? a.cu + a.N : nullptr, (long)a.H * a.V / 4);
-    return cudaGetLastError();
 }
 
 template <typename OT>

@@ -383,7 +383,11 @@ typedef enum {
  * NaN from its token on; a value (an element of v) that is not finite makes its channel's
  * outputs NaN from its token to its chunk's end and, through the state, not finite behind it.
  *
- * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores, which cut
+ * bf16 inputs with K and V of 64, 128 or 256 run on the tensor cores.  For a bf16
+ * output the scores and the state that the queries read are rounded to bf16 once as
+ * operands, which adds up to 2^-8 of the sum of the absolute values of o's terms (in
+ * the norm 2.3e-3 of o with its own rounding, which alone is 1.7e-3); a KDA_F32
+ * output has neither, and takes up to 2.3 times as long.  The tensor cores cut
  * what they add to an FP32 accumulator: the states lean to zero by about 8e-7
  * of their value for each 64 tokens of the decay's memory (6e-6 at a decay of
  * -0.0023, 1e-4 over 32768 tokens without any).  The state is kept scaled down by up

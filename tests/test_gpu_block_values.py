@@ -98,3 +98,39 @@ def test_a_state_of_a_value_that_is_not_finite(kda, fn, dtype, K, V, T, at, bad)
     assert torch.equal(S[0, 1, :, d].nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
     S[0, 1, :, d] = S_ref[0, 1, :, d]
     close(S, S_ref, (K + 128 + T) * F32 * Sa + 1e-30, "state")
+
+
+SHAPES = [(1, 200, 2, 2, 128, 128), (2, 150, 4, 2, 64, 64), (1, 130, 2, 1, 64, 128), (1, 321, 3, 3, 128, 64), (1, 1100, 2, 2, 128, 128),
+          (1, 777, 1, 1, 256, 256), (2, 190, 2, 2, 64, 256), (1, 2100, 1, 1, 64, 64), (1, 63, 1, 1, 256, 64), (1, 1, 2, 2, 128, 128)]
+
+
+@pytest.mark.parametrize("B,T,H,Hk,K,V", SHAPES)
+@pytest.mark.parametrize("span", [0.0, 0.1, 3.0])
+@pytest.mark.parametrize("state", [False, True])
+def test_a_float32_output_of_bf16_inputs(kda, B, T, H, Hk, K, V, span, state):  # noqa: F811
+    """No operand of its sums is rounded to bf16: the bounds of float32 arithmetic alone, for whole sequences and
+    for segments, whole units and cut ones."""
+    x = inputs(T + K, B, T, H, Hk, K, V, BF, B, span=span, state=state)
+    o_ref, S_ref, oa, Sa = ref.decay_attention(*x)
+    for sms in (0, 1, 3):
+        try:
+            kda.kda_test_hooks(sm_count=sms)
+            o, S = kda.kda_decay_chunk_fwd(*(dev(t) for t in x[:4]), initial_state=dev(x[4]), output_final_state=True,
+                                           o_dtype=torch.float32)
+        finally:
+            kda.kda_test_hooks()
+        f32 = (K + 128 + T) * F32
+        close(o, o_ref, f32 * oa + 1e-30, "o")
+        close(S, S_ref, f32 * Sa + 1e-30, "state")
+
+
+def test_a_float32_output_packed(kda):  # noqa: F811
+    edges = [0, 0, 1, 1, 70, 200, 264, 900]
+    x = inputs(4, 1, edges[-1], 2, 1, 128, 128, BF, len(edges) - 1, span=0.5)
+    o_ref, S_ref, oa, Sa = ref.decay_attention(*x, edges)
+    cu = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    s = dev(x[4])
+    o, S = kda.kda_decay_chunk_fwd(*(dev(t) for t in x[:4]), initial_state=s, final_state=s, cu_seqlens=cu, o_dtype=torch.float32)
+    f32 = (128 + 128 + 636) * F32
+    close(o, o_ref, f32 * oa + 1e-30, "o")
+    close(S, S_ref, f32 * Sa + 1e-30, "state")
