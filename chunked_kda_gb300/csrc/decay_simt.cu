@@ -4,8 +4,12 @@
 //
 // Three launches, all chunks at once but for the scan:
 //   1. each chunk's addition to the state, A = sum_j 2^(G_l - G_j) k_j v_j^T, and its decay 2^G_l;
-//   2. the scan over a sequence's chunks: the addition's place takes the chunk's incoming state;
+//   2. the scan over a sequence's chunks: the addition's place takes the next chunk's incoming state;
 //   3. each chunk's output, o_i = s (2^G_i S^T q_i + sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) v_j).
+// Scratch holds the additions of chunks that another one follows, at most a state for each 64 tokens however many
+// sequences there are (4096 single tokens of 32 heads of 128 x 128: 135 MB): a first chunk reads the initial state, a
+// last one's addition is made in the final state.  Where that is the initial state, which the outputs still read,
+// the last additions are a fourth launch behind the outputs.
 // The products are 64 x 64 tiles, 256 threads with 4 x 4 results each, operands in shared memory with
 // the summed index outermost, so that a thread takes its four rows and its four columns as one vector
 // each.  Bound by the FP32 pipe (98 k operations a token and head at K = V = 128): 16384
@@ -27,8 +31,12 @@ struct SimtArgs {
     float* hT;
     ChunkMap cm;
     int H, hr, K, V;
-    float* ws;    // [slot][h][K][V]
+    float* ws;    // [place][h][K][V]
     float* wdec;  // [slot][h]
+    // the place of the first chunk of sequence n (its c-th chunk's is c further).  Packed: a sequence of m + 1
+    // chunks needs m, and floor(eos / C) - floor(bos / C) >= m.
+    __device__ size_t place(int n, int bos) const { return cm.cu ? bos / C : (size_t)n * (cm.n_slots() / cm.N - 1); }
+    __device__ bool in_place() const { return hT && hT == h0; }
 };
 
 // the chunk's G as integer and fraction, and the first token without one, by warp 0 (a barrier follows)
@@ -124,15 +132,26 @@ __device__ __forceinline__ void tile_product(const float* A, const float* B, int
     }
 }
 
-// grid (slots, H, K blocks x V blocks of 64)
-template <typename T>
+// grid (slots, H, K blocks x V blocks of 64).  kLast: the last chunks alone, a slot for each sequence, onto their
+// decayed incoming states (which may be the initial ones, in place).
+template <typename T, bool kLast>
 __global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, const T* __restrict__ v, SimtArgs p) {
     __shared__ __align__(16) float sk[C * LD], sv[C * LD];
     __shared__ float sf[C];
     __shared__ int sI[3][C];
     int n, t0, len, bos, eos;
-    if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
-    if (t0 + len >= eos && !p.hT) return;  // nothing follows this chunk
+    if constexpr (kLast) {
+        n = blockIdx.x;
+        if (p.cm.cu) { bos = __ldg(p.cm.cu + n); eos = __ldg(p.cm.cu + n + 1); }
+        else         { bos = n * p.cm.T; eos = bos + p.cm.T; }
+        if (bos == eos) return;  // its state is where it was
+        t0 = bos + (eos - bos - 1) / C * C;
+        len = eos - t0;
+    } else {
+        if (!p.cm.map_first(blockIdx.x, n, t0, len, bos, eos)) return;
+        if (t0 + len >= eos && (!p.hT || p.in_place())) return;
+    }
+    const bool last = t0 + len >= eos;
     const int h = blockIdx.y, nkb = (p.K + 63) / 64, c0 = 64 * (blockIdx.z % nkb), d0 = 64 * (blockIdx.z / nkb);
     const int tid = threadIdx.x;
     chunk_gates(p, h, t0, len, sI);
@@ -146,16 +165,20 @@ __global__ void __launch_bounds__(NT) decay_add_kernel(const T* __restrict__ k, 
     const int ti = tid >> 4, tj = tid & 15;
     float acc[4][4] = {};
     tile_product(sk, sv, C, ti, tj, acc);
-    float* out = p.ws + ((size_t)blockIdx.x * p.H + h) * p.K * p.V;
+    const size_t KV = (size_t)p.K * p.V, at = p.place(n, bos) + (t0 - bos) / C;
+    float* out = last ? p.hT + ((size_t)n * p.H + h) * KV : p.ws + (at * p.H + h) * KV;
+    const float* in = !kLast ? nullptr : t0 == bos ? out : p.ws + ((at - 1) * p.H + h) * KV;
+    const float decay = pow2(max(sI[0][C - 1], -300), sI[1][C - 1]) + poison;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = c0 + 4 * ti + i, d = d0 + 4 * tj + j;
-            if (c < p.K && d < p.V) out[(size_t)c * p.V + d] = acc[i][j];
+            if (c >= p.K || d >= p.V) continue;
+            const size_t e = (size_t)c * p.V + d;
+            out[e] = kLast ? fmaf(decay, in[e], acc[i][j]) : acc[i][j];
         }
-    if (tid == 0 && blockIdx.z == 0)
-        p.wdec[(size_t)blockIdx.x * p.H + h] = pow2(max(sI[0][C - 1], -300), sI[1][C - 1]) + poison;
+    if (!kLast && tid == 0 && blockIdx.z == 0) p.wdec[(size_t)blockIdx.x * p.H + h] = decay;
 }
 
 // grid (blocks of 256 state elements, H, sequences): the chunks' incoming states, and the final one
@@ -169,24 +192,26 @@ __global__ void __launch_bounds__(NT) decay_chunk_scan_kernel(SimtArgs p) {
     const size_t st = ((size_t)n * p.H + h) * KV + e;
     float S = p.h0 ? p.h0[st] : 0.f;
     const int s0 = ns > 0 ? p.cm.first_slot(n, bos) : 0;
+    float* at = p.ws + (p.place(n, bos) * p.H + h) * KV + e;
+    const size_t step = (size_t)p.H * KV;
     // (eight chunks' additions are loaded before the first is used)
     constexpr int U = 8;
-    for (int s = 0; s < ns; s += U) {
+    for (int s = 0; s + 1 < ns; s += U) {
         float add[U], dec[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const bool in = s + u < ns && (s + u + 1 < ns || p.hT);
-            add[u] = in ? p.ws[((size_t)(s0 + s + u) * p.H + h) * KV + e] : 0.f;
+            const bool in = s + u + 1 < ns;
+            add[u] = in ? at[(s + u) * step] : 0.f;
             dec[u] = in ? __ldg(p.wdec + (size_t)(s0 + s + u) * p.H + h) : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (s + u >= ns) break;
-            p.ws[((size_t)(s0 + s + u) * p.H + h) * KV + e] = S;
+            if (s + u + 1 >= ns) break;
             S = fmaf(dec[u], S, add[u]);
+            at[(s + u) * step] = S;
         }
     }
-    if (p.hT) p.hT[st] = S;
+    if (p.hT && !p.in_place()) p.hT[st] = ns > 0 ? fmaf(__ldg(p.wdec + (size_t)(s0 + ns - 1) * p.H + h), S, p.hT[st]) : S;
 }
 
 // grid (slots, H): the chunk's output, all its value channels
@@ -225,10 +250,13 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
                 sp[s * LD + r] = y;
             }
     }
-    const float* S = p.ws + ((size_t)blockIdx.x * p.H + h) * p.K * p.V;
+    const size_t KV = (size_t)p.K * p.V;
+    const float* S = t0 > bos ? p.ws + ((p.place(n, bos) + (t0 - bos) / C - 1) * p.H + h) * KV
+                     : p.h0 ? p.h0 + ((size_t)n * p.H + h) * KV : nullptr;
     for (int d0 = 0; d0 < p.V; d0 += 64) {
         float acc[4][4] = {};
-        for (int c0 = 0; c0 < Kp; c0 += 32) {
+        if (!S) __syncthreads();
+        for (int c0 = 0; c0 < Kp && S; c0 += 32) {
             __syncthreads();
             load_rows(S + (size_t)c0 * p.V, p.V, 32, p.K - c0, d0, p.V, nullptr, sx);
             __syncthreads();
@@ -259,18 +287,20 @@ __global__ void __launch_bounds__(NT) decay_out_kernel(const T* __restrict__ q, 
     }
 }
 
-size_t state_bytes(int slots, int H, int K, int V) { return ((size_t)slots * H * K * V * 4 + 255) / 256 * 256; }
+// chunks that another one follows, at most
+int places(int T, int N, bool packed) { return packed ? T / C : N * max(0, (T + C - 1) / C - 1); }
+size_t state_bytes(int places, int H, int K, int V) { return ((size_t)places * H * K * V * 4 + 255) / 256 * 256; }
 
 template <typename T, typename OT>
 cudaError_t run(const DecayArgs& a) {
     const ChunkMap cm{a.cu, a.N, a.T, C};
     const int slots = cm.n_slots();
     SimtArgs p{a.decay, a.per_token ? a.H : 0, a.h0, a.hT, cm, a.H, a.H / a.Hk, a.K, a.V, (float*)a.ws,
-               (float*)((char*)a.ws + state_bytes(slots, a.H, a.K, a.V))};
+               (float*)((char*)a.ws + state_bytes(places(a.T, a.N, a.cu), a.H, a.K, a.V))};
     cudaError_t e;
+    const int tiles = ((a.K + 63) / 64) * ((a.V + 63) / 64);
     if (slots > 0) {
-        const dim3 grid(slots, a.H, ((a.K + 63) / 64) * ((a.V + 63) / 64));
-        decay_add_kernel<T><<<grid, NT, 0, a.stream>>>((const T*)a.k, (const T*)a.v, p);
+        decay_add_kernel<T, false><<<dim3(slots, a.H, tiles), NT, 0, a.stream>>>((const T*)a.k, (const T*)a.v, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     decay_chunk_scan_kernel<<<dim3((a.K * a.V + NT - 1) / NT, a.H, a.N), NT, 0, a.stream>>>(p);
@@ -280,7 +310,11 @@ cudaError_t run(const DecayArgs& a) {
         const int bytes = ((a.K + 31) / 32 * 32 + C + 32) * LD * (int)sizeof(float);
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
         kern<<<dim3(slots, a.H), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
-        e = cudaGetLastError();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (a.hT && a.hT == a.h0) {
+            decay_add_kernel<T, true><<<dim3(a.N, a.H, tiles), NT, 0, a.stream>>>((const T*)a.k, (const T*)a.v, p);
+            e = cudaGetLastError();
+        }
     }
     return e;
 }
@@ -290,7 +324,7 @@ cudaError_t run(const DecayArgs& a) {
 
 size_t decay_simt_workspace_bytes(int B, int T, int H, int K, int V, int N, bool packed) {
     const int slots = packed ? T / decay::C + N + 1 : N * ((T + decay::C - 1) / decay::C);
-    return decay::state_bytes(slots, H, K, V) + ((size_t)slots * H * 4 + 255) / 256 * 256;
+    return decay::state_bytes(decay::places(T, N, packed), H, K, V) + ((size_t)slots * H * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_decay_simt(const DecayArgs& a) {

@@ -376,7 +376,9 @@ typedef enum {
  *     S_out = exp(G_l) S_in + sum_j exp(G_l - G_j) k_j v_j^T
  * with G the running sum of a in the chunk and l its last token.  Its scratch is
  * kda_decay_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for
- * dense inputs).  kda_decay_recurrent_fwd is the form for single tokens and
+ * dense inputs): for float32 and the head sizes without tensor cores a state for
+ * each 64 tokens and head, for K = 256 on them 8 bytes for each element of o, and
+ * where a sequence is cut in time its pieces' states.  kda_decay_recurrent_fwd is the form for single tokens and
  * computes token by token in FP32.
  *
  * What is not finite never reaches back: a decay that is NaN makes its head's outputs

@@ -126,3 +126,36 @@ def test_parts_of_the_block_norm_of_many_long_rows(kda, post, pre, scale, residu
     rel = size / wh.abs().clamp_min(1e-300)
     mean = (size.square().mean(-1, keepdim=True) / (wh.square().mean(-1, keepdim=True) + 1e-6)).sqrt()
     close(y, wy, (HALF[dtype] + n * (rel + mean)) * wy.abs() + 1e-30, "y")
+
+
+@pytest.mark.parametrize("name,H,Hk", [("long", 2, 2), ("ends", 2, 1), ("many", 3, 3)])
+@pytest.mark.parametrize("K,V", [(128, 128), (40, 72)])
+@pytest.mark.parametrize("state", ["none", "given", "in place"])
+def test_packed_float32(kda, name, H, Hk, K, V, state):  # noqa: F811
+    """The FP32 chunks: first chunks read the initial state, last ones make the final state, also in its place."""
+    edges, x, want = case(name, K, V, H, Hk, torch.float32)
+    if state == "none":
+        want = ref.decay_attention(*x[:4], None, edges)
+    o_ref, S_ref, oa, Sa = want
+    n = edges[-1]
+    q, k, v, decay = (t.clone() for t in x[:4])
+    for t in (q, k, v, decay):
+        t[:, n:] = float("nan")
+    s = None if state == "none" else dev(x[4])
+    cu = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    args = dict(initial_state=s, output_final_state=True, final_state=s if state == "in place" else None, cu_seqlens=cu)
+    o, S = kda.kda_decay_chunk_fwd(dev(q), dev(k), dev(v), dev(decay), **args)
+    torch.cuda.synchronize()
+    longest = max(b - a for a, b in zip(edges, edges[1:]))
+    f32 = (K + 128 + longest) * F32
+    close(o[:, :n], o_ref[:, :n], f32 * oa[:, :n] + 1e-30, "o")
+    close(S, S_ref, f32 * Sa + 1e-30, "state")
+    if state == "given":
+        again = kda.kda_decay_chunk_fwd(dev(q), dev(k), dev(v), dev(decay), **(args | dict(output_final_state=False)))
+        assert torch.equal(again[0][:, :n], o[:, :n])
+
+
+@pytest.mark.parametrize("B,T,H", [(2, 65, 2), (3, 300, 1), (1, 1000, 2)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_dense_float32(kda, B, T, H, inplace):  # noqa: F811
+    check(kda, "kda_decay_chunk_fwd", inputs(T, B, T, H, 1, 96, 130, torch.float32, B, span=0.3), inplace=inplace)
