@@ -1,5 +1,5 @@
-// Sums of per-token decays in log2 units, exact whatever their size: an integer and a fraction in
-// 2^-24 units, added as integers, so that differences of far sums lose nothing.
+// Sums of per-token decays in log2 units as integers of 2^-32: each decay is off by at most 2^-33 (32768 equal
+// ones together by 2.6e-6 of what they decay), their sums and the differences of far sums by nothing more.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -10,19 +10,19 @@
 namespace kda {
 namespace decay {
 
-// A log2 decay as an integer (returned in ip) and a fraction in 2^-24 units, from the natural
-// logarithm.  Clamped: 2^-1024 is zero for a float32, so -inf clears what it meets.
-__device__ __forceinline__ int fixed(float a, int& ip) {
+// A log2 decay in 2^-32 units, from the natural logarithm.  Clamped: 2^-1024 is zero for a float32, so
+// -inf clears what it meets.
+__device__ __forceinline__ long long fixed(float a) {
     constexpr float kRest = 1.9259629911267e-8f;  // log2(e) - kLog2e
-    const float x = fminf(fmaxf(a * kLog2e, -1024.f), 1024.f), fl = floorf(x);
+    const float x = fminf(fmaxf(a * kLog2e, -1024.f), 1024.f);
     const float e = fabsf(x) < 1024.f ? fmaf(a, kLog2e, -x) + a * kRest : 0.f;
-    ip = (int)fl;
-    return __float2int_rn(((x - fl) + e) * 16777216.f);
+    return __float2ll_rn(x * 4294967296.f) + __float2int_rn(e * 4294967296.f);
 }
-// the fraction into [0, 1)
-__device__ __forceinline__ void carry(int& i, int& f) {
-    i += f >> 24;
-    f &= 0xFFFFFF;
+// rounded to an integer and a fraction in [0, 1) in 2^-24 units, as the powers below take them
+__device__ __forceinline__ void parts(long long g, int& i, int& f) {
+    const long long r = (g + 128) >> 8;
+    i = (int)(r >> 24);
+    f = (int)r & 0xFFFFFF;
 }
 __device__ __forceinline__ float pow2i(int n) { return __int_as_float(min(max(n + 127, 0), 255) << 23); }
 // 2^(n + f / 2^24), |f| < 2^24: the power of the nearest integer times the power series of the rest
@@ -49,26 +49,18 @@ __device__ __forceinline__ int first_nan(float a0, float a1) {
     return min(even ? 2 * (__ffs(even) - 1) : 64, odd ? 2 * __ffs(odd) - 1 : 64);
 }
 __device__ __forceinline__ float nan_if(bool on) { return on ? __int_as_float(0x7fffffff) : 0.f; }
-// Inclusive sums over a warp of two consecutive tokens a lane: I, F of the lane's two tokens.
-__device__ __forceinline__ void pair_sums(float a0, float a1, int (&I)[2], int (&F)[2]) {
-    int i0, i1;
-    const int f0 = fixed(a0, i0), f1 = fixed(a1, i1);
-    int ii = i0 + i1, ff = f0 + f1;
+// Inclusive sums over a warp of two consecutive tokens a lane: G of the lane's two tokens.
+__device__ __forceinline__ void pair_sums(float a0, float a1, long long (&G)[2]) {
+    const long long g1 = fixed(a1);
+    long long g = fixed(a0) + g1;
     const int l = threadIdx.x & 31;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int yi = __shfl_up_sync(0xffffffffu, ii, m), yf = __shfl_up_sync(0xffffffffu, ff, m);
-        if (l >= m) {
-            ii += yi;
-            ff += yf;
-        }
+        const long long y = __shfl_up_sync(0xffffffffu, g, m);
+        if (l >= m) g += y;
     }
-    I[0] = ii - i1;
-    F[0] = ff - f1;
-    I[1] = ii;
-    F[1] = ff;
-    carry(I[0], F[0]);
-    carry(I[1], F[1]);
+    G[0] = g - g1;
+    G[1] = g;
 }
 
 }  // namespace decay

@@ -46,7 +46,10 @@ __device__ __forceinline__ void chunk_gates(const SimtArgs& p, int h, int t0, in
         auto a = [&](int i) { return i < len ? __ldg(p.decay + (size_t)(t0 + i) * p.decay_stride + h) : 0.f; };
         int I[2], F[2];
         const float a0 = a(2 * l), a1 = a(2 * l + 1);
-        pair_sums(a0, a1, I, F);
+        long long G[2];
+        pair_sums(a0, a1, G);
+        parts(G[0], I[0], F[0]);
+        parts(G[1], I[1], F[1]);
         const int first = first_nan(a0, a1);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

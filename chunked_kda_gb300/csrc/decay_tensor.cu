@@ -531,8 +531,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const float* dp = p.decay + h;
         auto raw = [&](int t) { return t < eos ? __ldg(dp + (size_t)t * p.decay_stride) : 0.f; };
         float a0 = raw(bos + 2 * l), a1 = raw(bos + 2 * l + 1);
-        int Ei = kTop, Ef = 0;  // the stored state's exponent: integer, and fraction in 2^-24 units
-        long long total = 0;    // the whole segment's log2 decay in 2^-24 units
+        long long E = (long long)kTop << 32, total = 0;  // the stored state's exponent; the whole segment's log2 decay
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS, t0 = bos + c * C;
@@ -540,15 +539,20 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             a0 = raw(t0 + C + 2 * l);
             a1 = raw(t0 + C + 2 * l + 1);
             int I[2], F[2];
-            pair_sums(x0, x1, I, F);
+            long long G[2];
+            pair_sums(x0, x1, G);
+            const long long Gl = __shfl_sync(0xffffffffu, G[1], 31);
+            parts(G[0], I[0], F[0]);
+            parts(G[1], I[1], F[1]);
             const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
             const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
             const int bad = first_nan(x0, x1);
             const float poison = nan_if(bad < C);  // of the state behind the chunk
-            total += ((long long)Il << 24) + Fl;
+            if constexpr (kStates) total = max(total + Gl, -(4000ll << 32));
             // this chunk's value and row factors, and the exponent behind it
-            int ni = Ei + Il, nf = Ef + Fl;
-            carry(ni, nf);
+            int Ei, Ef, ni, nf;
+            parts(E, Ei, Ef);
+            parts(E + Gl, ni, nf);
             const bool renew = ni < 0 || ni >= 2 * kTop;
             // the slot's last readers are done: chunk c - NS is loaded (and its FULL phase complete),
             // so the products of c - 2 NS are done, which the output warps of c - NG preceded
@@ -568,13 +572,13 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 sts(gt + GT_LAST, (renew ? pow2(ni - kTop, nf) : 1.f) + poison);
                 sts(gt + GT_OUT, renew ? pow2i(kTop) : pow2(ni, nf));
             }
-            Ei = renew ? kTop : ni;
-            Ef = renew ? 0 : nf;
+            E = renew ? (long long)kTop << 32 : E + Gl;
             __syncwarp();
             if (l == 0) mbar_arrive(sy.bar(B_FULL + s));
             if (kStates && c == nt - 1 && l == 0 && vb == 0) {
-                const long long t = max(total, -(300ll << 24));
-                p.wdec[(size_t)slot * p.H + h] = pow2((int)(t >> 24), (int)(t & 0xFFFFFF)) + poison;
+                int i, f;
+                parts(total, i, f);
+                p.wdec[(size_t)slot * p.H + h] = pow2(max(i, -300), f) + poison;
             }
         }
     } else if (w == 27) {

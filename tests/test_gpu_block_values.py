@@ -134,3 +134,30 @@ def test_a_float32_output_packed(kda):  # noqa: F811
     f32 = (128 + 128 + 636) * F32
     close(o, o_ref, f32 * oa + 1e-30, "o")
     close(S, S_ref, f32 * Sa + 1e-30, "state")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("rate", [1e-6, 3.3e-6, 1e-5, 1e-4, 0.002])
+@pytest.mark.parametrize("one_sign", [True, False])
+def test_slow_decays_over_long_sequences(kda, dtype, rate, one_sign):  # noqa: F811
+    """A decay that all tokens share: what each token's is off by adds up.  The state's bound: a chunk's sum of 64
+    products (bf16: twelve cuts of 2^-23), one rounded addition for each chunk (bf16: each segment) behind it, the decays'
+    own 2^-33 a token, a few u for the factors and, for each multiplication by a chunk's (a segment's) decay, two u."""
+    T, H, K = 32768, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(int(rate * 1e7))
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k = (torch.nn.functional.normalize(r(1, T, H, K), dim=-1).to(dtype) for _ in range(2))
+    v = r(1, T, H, K).to(dtype)
+    if one_sign:
+        k, v = k.abs(), v.abs()
+    a = torch.full((H,), -rate, device="cuda")
+    w = torch.exp(a[0].double() * torch.arange(T - 1, -1, -1, device="cuda"))
+    want = torch.einsum("t,thk,thv->hkv", w, k[0].double(), v[0].double())[None]
+    size = torch.einsum("t,thk,thv->hkv", w, k[0].double().abs(), v[0].double().abs())[None]
+    _, S = kda.kda_decay_chunk_fwd(q, k, v, a, output_final_state=True)
+    # (152 multiprocessors: two heads in segments of seven chunks; planned for fewer, the segments are longer)
+    chunks = T // 64
+    steps = chunks if dtype == torch.float32 else 76
+    inside = 66 * F32 if dtype == torch.float32 else 7 * 12 * 2 * F32
+    bound = inside + 4 * steps * F32 + T * 2.0 ** -33 + 16 * F32
+    close(S, want.cpu(), (bound * size).cpu(), "state")
