@@ -28,8 +28,9 @@
 // (kFine; 4 x 4096 tokens, 64 heads: 450 us, with a single term each 246).  The state is a float32 output and
 // feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits) and S is accumulated
 // from all three.  The tensor cores cut, not round, what they add to an FP32 accumulator, so S leans to
-// zero by about 8e-7 a chunk of its memory: 6e-6 at a fixed decay of -0.0023, 1e-4 after 32768 tokens
-// without any.
+// zero by up to 2^-23 of the sum of its terms' absolute values for each of a chunk's twelve accumulations: 9e-6 at a
+// fixed decay of -0.0023; after 32768 tokens with hardly any (-1e-6), 3.6e-4 where all terms have one sign and
+// 1.2e-4 where they are random.  Segments start at 0 and are joined in rounded FP32: 4e-6 there with two heads.
 //
 // What bounds it is shared memory's 128 bytes a clock next to HBM: per chunk at K = V = 128 the loads
 // write 48 KB, the products read 120 KB, the warps and the stores about 60 KB.  That is why the scaled

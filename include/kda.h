@@ -378,8 +378,8 @@ typedef enum {
  * kda_decay_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for
  * dense inputs): for float32 and the head sizes without tensor cores a state for
  * each 64 tokens and head, for K = 256 on them 8 bytes for each element of o, and
- * where a sequence is cut in time its pieces' states.  kda_decay_recurrent_fwd is the form for single tokens and
- * computes token by token in FP32.
+ * where a sequence is cut in time its pieces' states.  kda_decay_recurrent_fwd is the
+ * form for single tokens and computes token by token in FP32.
  *
  * What is not finite never reaches back: a decay that is NaN makes its head's outputs
  * NaN from its token on; a value (an element of v) that is not finite makes its channel's
@@ -389,12 +389,14 @@ typedef enum {
  * output the scores and the state that the queries read are rounded to bf16 once as
  * operands, which adds up to 2^-8 of the sum of the absolute values of o's terms (in
  * the norm 2.3e-3 of o with its own rounding, which alone is 1.7e-3); a KDA_F32
- * output has neither, and takes up to 2.3 times as long.  The tensor cores cut
- * what they add to an FP32 accumulator: the states lean to zero by about 8e-7
- * of their value for each 64 tokens of the decay's memory (6e-6 at a decay of
- * -0.0023, 1e-4 over 32768 tokens without any).  The state is kept scaled down by up
- * to 2^32: it overflows only where float32 does, and values below 2^-85 lose low bits.  Float32 inputs and the recurrent
- * form add in rounded FP32.
+ * output has neither, and takes up to 2.3 times as long.  The tensor cores cut what
+ * they add to an FP32 accumulator, toward zero: a state leans by up to 12 x 2^-23 (1.4e-6)
+ * of the sum of the absolute values of its terms for each 64 tokens of the decay's memory.
+ * Measured with terms of one sign: 9e-6 at a decay of -0.0023, 2e-4 at -0.0001, 4e-4 over
+ * 32768 tokens with hardly any decay (1e-4 there with random terms); a prompt that is
+ * cut in time (few heads) starts anew with each piece.  The state is kept scaled down by
+ * up to 2^32: it overflows only where float32 does, and values below 2^-85 lose low bits.
+ * Float32 inputs and the recurrent form add in rounded FP32.
  */
 size_t kda_decay_chunk_workspace_bytes(kda_dtype qkv_dtype, int B, int T, int H, int K, int V,
                                        int n_seqs);

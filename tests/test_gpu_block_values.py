@@ -161,3 +161,28 @@ def test_slow_decays_over_long_sequences(kda, dtype, rate, one_sign):  # noqa: F
     inside = 66 * F32 if dtype == torch.float32 else 7 * 12 * 2 * F32
     bound = inside + 4 * steps * F32 + T * 2.0 ** -33 + 16 * F32
     close(S, want.cpu(), (bound * size).cpu(), "state")
+
+
+@pytest.mark.parametrize("rate", [0.0, 1e-6, 1e-4, 0.0023])
+@pytest.mark.parametrize("one_sign", [True, False])
+def test_the_documented_lean_of_a_state(kda, rate, one_sign):  # noqa: F811
+    """Whole bf16 sequences: a chunk's twelve accumulations cut at most 2^-23 each of the sum of the absolute values,
+    for each 64 tokens of the memory; the decays' own 2^-33 a token; a few u for the factors."""
+    T, H, K = 32768, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(int(rate * 1e7) + 1)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k = (torch.nn.functional.normalize(r(1, T, H, K), dim=-1).to(BF) for _ in range(2))
+    v = r(1, T, H, 64).to(BF)
+    if one_sign:
+        k, v = k.abs(), v.abs()
+    a = torch.full((H,), -rate, device="cuda")
+    w = torch.exp(a[0].double() * torch.arange(T - 1, -1, -1, device="cuda"))
+    want = torch.einsum("t,thk,thv->hkv", w, k[0].double(), v[0].double())[None]
+    size = torch.einsum("t,thk,thv->hkv", w, k[0].double().abs(), v[0].double().abs())[None]
+    try:
+        kda.kda_test_hooks(sm_count=1)
+        _, S = kda.kda_decay_chunk_fwd(q, k, v, a, output_final_state=True)
+    finally:
+        kda.kda_test_hooks()
+    memory = min(T, 1 / rate) if rate else T
+    close(S, want.cpu(), ((12 * 2.0 ** -23 * (memory / 64 + 1) + T * 2.0 ** -33 + 16 * F32) * size).cpu(), "state")
