@@ -51,7 +51,9 @@ kda_status check_decay(const void* q, const void* k, const void* v, kda_dtype qk
     if (K < 1 || K > 256 || V < 1 || V > 256) return fail(KDA_ERR_UNSUPPORTED, "K and V must be in [1, 256]");
     if ((long long)B * T > 0 && *N > 0 && (!q || !k || !v || !decay || !o))
         return fail(KDA_ERR_INVALID_ARG, "null q, k, v, decay or o");
-    if (!aligned(q, k, v, decay, h0, hT, o)) return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    if (!aligned(q, k, v, h0, hT, o)) return fail(KDA_ERR_INVALID_ARG, kMisaligned);
+    // (a token's decays out of a batch with few heads lie anywhere, and are read one by one)
+    if (((uintptr_t)decay & 3u) != 0) return fail(KDA_ERR_INVALID_ARG, "decay must be 4-byte aligned");
     if (*N == 0) return KDA_OK;
     const size_t e = qkv_dtype == KDA_BF16 ? 2 : 4, tokens = (size_t)B * T, Hk = n_qk_heads > 0 ? n_qk_heads : H;
     const size_t qk = tokens * Hk * K * e, state = (size_t)*N * H * K * V * 4;

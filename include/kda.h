@@ -364,8 +364,8 @@ typedef enum {
  *   q, k       [B, T, n_qk_heads, K], dtype qkv_dtype; value head h (of H)
  *              reads query / key head h / (H / n_qk_heads); 0 means H heads
  *   v, o       [B, T, H, V]; o_dtype the qkv dtype or KDA_F32
- *   decay      float32, natural log: [B, T, H] (decay_per_token != 0) or [H],
- *              the same for all tokens.  -inf clears the state at its token;
+ *   decay      float32 (4-byte aligned), natural log: [B, T, H] (decay_per_token != 0)
+ *              or [H], the same for all tokens.  -inf clears the state at its token;
  *              a <= 0 is the meant range.
  *   states     [N, H, K, V] float32; final_state may be initial_state
  *   K, V       any value from 1 to 256

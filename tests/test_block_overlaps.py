@@ -84,3 +84,9 @@ def test_nothing_to_do_overlaps_nothing(lib):  # noqa: F811
     assert conv(lib, B=0, y=at(0)) == OK
     assert conv(lib, T=0, y=at(0), s1=None) == OK
     assert decay(lib, True, B=0, o=at(0)) == OK
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+def test_alignment_of_the_decays(lib, chunk):  # noqa: F811
+    for shift in (1, 2, 3, 5):
+        assert decay(lib, chunk, decay=at(3, shift)) == INVALID and b"aligned" in lib.kda_last_error()

@@ -186,3 +186,19 @@ def test_the_documented_lean_of_a_state(kda, rate, one_sign):  # noqa: F811
         kda.kda_test_hooks()
     memory = min(T, 1 / rate) if rate else T
     close(S, want.cpu(), ((12 * 2.0 ** -23 * (memory / 64 + 1) + T * 2.0 ** -33 + 16 * F32) * size).cpu(), "state")
+
+
+@pytest.mark.parametrize("fn", FORMS)
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("K", [96, 128])
+@pytest.mark.parametrize("lo,hi", [(129, 130), (1, 130), (3, 93)])
+def test_tokens_out_of_a_batch_with_few_heads(kda, fn, dtype, K, lo, hi):  # noqa: F811
+    """Slices of one sequence are contiguous as they are; two heads' decays then lie at multiples of 8 bytes."""
+    x = inputs(hi, 1, 130, 2, 2, K, K, dtype, 1)
+    q, k, v, decay = (dev(t)[:, lo:hi] for t in x[:4])
+    assert decay.is_contiguous() and decay.data_ptr() % 16 == 8
+    o, S = getattr(kda, fn)(q, k, v, decay, initial_state=dev(x[4]), output_final_state=True)
+    same = getattr(kda, fn)(q, k, v, decay.clone(), initial_state=dev(x[4]), output_final_state=True)
+    assert torch.equal(o, same[0]) and torch.equal(S, same[1])
+    o_ref, S_ref, oa, Sa = ref.decay_attention(*(t[:, lo:hi] for t in x[:4]), x[4])
+    close(S, S_ref, (K + 128 + 130) * F32 * Sa + 1e-30, "state")
