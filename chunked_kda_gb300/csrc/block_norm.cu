@@ -113,8 +113,8 @@ __device__ __forceinline__ float gate_value(float z, int act) {
 }
 
 // Gated norm of short rows: G lanes share a row, a vector of 16 bytes each (V of at most 32 vectors),
-// so a warp holds 32 / G rows.  Memory bounds it: 16384 x 64 rows of 128 bf16 (805 MB) in 133 us,
-// 6.0 TB/s.  Small blocks with few registers keep the most bytes in flight: blocks of 256 threads
+// so a warp holds 32 / G rows.  Memory bounds it: 16384 x 64 rows of 128 bf16 (805 MB) in 130 us,
+// 6.2 TB/s.  Small blocks with few registers keep the most bytes in flight: blocks of 256 threads
 // measured 138 us, and two or four rows a lane group, their loads issued together, 158 and 241 us.
 constexpr int kRowThreads = 128;
 template <typename T, int G>
@@ -438,7 +438,9 @@ cudaError_t launch_block(const BlockNormArgs& a) {
     // Rows too long for one piece a thread, enough of them for 8 a multiprocessor, and two fit the ring.
     // 1.07 to 1.6 GB with / without the ring: 16384 x 8192 bf16 with a float32 stream 250 / 278 us, a bf16 one
     // 176 / 241, none 160 / 221; 26214 x 5120 260 / 346, gated 294 / 436; float32 332 / 363.  At 4096
-    // and below a block per row is ahead (4096: 250 / 238; 2048: 343 / 231).
+    // and below a block per row is ahead (4096: 250 / 238; 2048: 343 / 231).  Beyond 8192 the ring's kernel has no
+    // registers for a third piece: a block of 1024 threads per row there, 10922 x 12288 (bf16, float32 stream, 1.61 GB)
+    // in 397 us, 8192 x 16384 in 341.
     if (a.D % 8 == 0 && a.D > 8 * kRingThreads && a.D <= 16 * kRingThreads) {
         const int row_bytes = a.D * (int)((a.gate ? 2 : 1) * sizeof(T) + (a.residual ? sizeof(R) : 0));
         const int stages = min(kRingStages, kRingBytes / row_bytes), sms = planned_sm_count();

@@ -14,7 +14,7 @@
 // Rows are loaded U at a time while the U before them are in work: 20480 packed rows x 12288 bf16
 // (1.01 GB) in 162 us, 6.2 TB/s, with 8 rows and six blocks on an SM; 4 rows and eight blocks measured
 // 168, 6 and seven 176, 12 and five 174, 16 and four 183; stores that stay in the caches 173.  (float32 rows
-// are twice the registers: 4 at a time, 20480 x 6144 in 213 us.)  TT trades the reload of
+// are twice the registers: 4 at a time, 20480 x 6144 in 214 us.)  TT trades the reload of
 // W - 1 rows and of the weights against the number of blocks: 64 rows where that leaves eight blocks
 // an SM, else 16 or 8.
 #include <limits.h>
@@ -129,7 +129,8 @@ __device__ __forceinline__ void row_step(const typename Io::V& raw, const float 
 
 // Single tokens: a thread takes Q whole sequences of its channels, with the states and first rows of
 // all of them loaded before the first is used.  (The tiles above walk one start after another, each
-// with its loads' latency: 33 us for 512 sequences of one token x 12288 channels against 21 us here.)
+// with its loads' latency: 33 us for 512 sequences of one token x 12288 channels, 100 MB, against 21 us here, of which
+// the kernel's own are 17.  Where the rows are one sequence's after all, its threads walk them one by one.)
 template <typename T, typename Io, int W>
 __global__ void __launch_bounds__(128) short_conv_seq_kernel(const T* __restrict__ x, const float* __restrict__ weight,
                                                              const float* __restrict__ bias, int act, const T* s0, T* s1,
