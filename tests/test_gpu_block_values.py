@@ -202,3 +202,26 @@ def test_tokens_out_of_a_batch_with_few_heads(kda, fn, dtype, K, lo, hi):  # noq
     assert torch.equal(o, same[0]) and torch.equal(S, same[1])
     o_ref, S_ref, oa, Sa = ref.decay_attention(*(t[:, lo:hi] for t in x[:4]), x[4])
     close(S, S_ref, (K + 128 + 130) * F32 * Sa + 1e-30, "state")
+
+
+@pytest.mark.parametrize("o_dtype", [None, torch.float32])
+@pytest.mark.parametrize("sms", [0, 1])
+def test_a_wait_that_gives_up_among_values_that_are_not_finite(kda, o_dtype, sms):  # noqa: F811
+    """A forced give-up while tiles are being cleared, with either output: reported, and the next call is right."""
+    x = inputs(3, 1, 700, 4, 4, 128, 128, BF, 1)
+    bad = x[2].clone()
+    bad[0, ::50, :, ::7] = float("nan")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_fused_wait_timeouts(reset=True)
+    try:
+        for chunk in (0, 1, 3):
+            kda.kda_test_hooks(wait_timeout_chunk=chunk, sm_count=sms)
+            status.zero_()
+            kda.kda_decay_chunk_fwd(dev(x[0]), dev(x[1]), dev(bad), dev(x[3]), initial_state=dev(x[4]),
+                                    output_final_state=True, status=status, o_dtype=o_dtype)
+            torch.cuda.synchronize()
+            assert int(status) == 1 and kda.kda_fused_wait_timeouts(reset=True) > 0
+    finally:
+        kda.kda_test_hooks()
+    check(kda, "kda_decay_chunk_fwd", x, o_dtype=o_dtype)
+    assert kda.kda_fused_wait_timeouts() == 0
