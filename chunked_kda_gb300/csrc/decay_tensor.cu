@@ -7,12 +7,12 @@
 //   o_i     = s (2^G_i S^T q_i + sum_j P[i][j] v_j)
 //   S      <- 2^G_l S + sum_j k_j (2^(G_l - G_j) v_j)^T                         (FP32)
 // as four products, value channels (M = 128) on TMEM lanes:
-//   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   S^T [v, c] += vd^T k.
+//   QK [i, j] = q k^T;   O1^T [v, i] = S^T q^T;   O2^T [v, i] = v^T P^T;   D^T [v, c] = vd^T k, added to S^T.
 // The stored state is S 2^-E, E from kTop = 32 down to 0.  Where the decay is slow, E' = E + G_l and the
-// values carry 2^(G_l - G_j - E') = 2^-(E + G_j): nothing has to be multiplied between two chunks' state
-// products, and S is rounded once less.  Before E falls below 0 the stored state is scaled (factor
-// 2^(E + G_l - kTop)) and E starts again at kTop.  So what is stored is never larger than S, and nothing
-// overflows that FP32 holds; the price is at the other end, where values below 2^-85 lose low bits.
+// values carry 2^(G_l - G_j - E') = 2^-(E + G_j): what is stored is only added to, and S is rounded once
+// less.  Before E falls below 0 the stored state is scaled with the addition (factor 2^(E + G_l - kTop)) and
+// E starts again at kTop.  So what is stored is never larger than S, and nothing overflows that FP32 holds;
+// the price is at the other end, where values below 2^-85 lose low bits.
 //
 // q, k and v enter the products as they are; O1's row factor s 2^(E + G_i) is applied to the FP32
 // results.  The decay is a number per row, so no anchors are needed: G_i - G_j <= 0 is formed as a
@@ -25,12 +25,14 @@
 // Roundings: for a bf16 output P and the copy of S that O1 reads are bf16 (each adds the output's own rounding
 // once more; both in quadrature keep o's error within 1.45 of one rounding).  A caller who wants more asks for a
 // float32 output: there both are three bf16 terms (24 bits), S's one after another through the copy's place
-// (kFine; 4 x 4096 tokens, 64 heads: 450 us, with a single term each 246).  The state is a float32 output and
-// feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits) and S is accumulated
-// from all three.  The tensor cores cut, not round, what they add to an FP32 accumulator, so S leans to
-// zero by up to 2^-23 of the sum of its terms' absolute values for each of a chunk's twelve accumulations: 9e-6 at a
-// fixed decay of -0.0023; after 32768 tokens with hardly any (-1e-6), 3.6e-4 where all terms have one sign and
-// 1.2e-4 where they are random.  Segments start at 0 and are joined in rounded FP32: 4e-6 there with two heads.
+// (kFine; 4 x 4096 tokens, 64 heads: 427 us).  The state is a float32 output and
+// feeds every later chunk, so the scaled values vd are three bf16 terms (24 bits), and a chunk's additions are
+// summed by themselves and then added to S in rounded FP32: the tensor cores cut, not round, what they add to an
+// accumulator, and S as that accumulator leaned to zero by 1.3e-6 for each chunk of its memory (9e-6 at a fixed
+// decay of -0.0023, 3.6e-4 after 32768 tokens with hardly any).  Now the cut is one of a chunk's own sum, the
+// smallest term first: S is off by 1e-7 at -0.0023 and by 3e-7 to 1e-6 after 32768 tokens with hardly any decay,
+// whatever their signs.  That costs a read of the sum and a read and write of S a chunk (4 x 4096 tokens, 64 heads:
+// 218 us against 203).
 //
 // What bounds it is shared memory's 128 bytes a clock next to HBM: per chunk at K = V = 128 the loads
 // write 48 KB, the products read 120 KB, the warps and the stores about 60 KB.  That is why the scaled
@@ -63,7 +65,7 @@ __device__ unsigned int g_decay_timeouts = 0;
 constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8, kTop = 32;
 
 // barriers
-enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_S = B_P + NS, B_SBF, B_VD, B_STATE, B_INTER, B_O,
+enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_D = B_P + NS, B_DREAD, B_SBF, B_VD, B_STATE, B_VFREE, B_INTER, B_O,
        B_OFREE = B_O + 2, B_DRAIN, B_DRAIN2, B_DRAIN3, B_NEVER, NBAR };
 
 // The decay factors of a chunk, one slot of a ring of NG (written when the chunk is loaded, read
@@ -81,15 +83,23 @@ constexpr uint32_t GT_BYTES = 1424;
 template <int KD, int VB, bool kFine = false>
 struct Layout {
     static constexpr uint32_t QB = C * KD * 2, VBYTES = C * VB * 2, STAGE = 2 * QB + VBYTES;
-    static constexpr uint32_t P = NS * STAGE, O = P + 2 * C * C * 2, G = O + (kFine ? 4 * C * C * 2 : VBYTES);
+    static constexpr uint32_t LO = NS * STAGE, P = LO + (KD == 128 ? (kFine ? 1 : 2) * VBYTES : 0), O = P + 2 * C * C * 2, G = O + (kFine ? 4 * C * C * 2 : VBYTES);
     static constexpr uint32_t BAR = G + NG * GT_BYTES, MISC = (BAR + 8 * NBAR + 15) / 16 * 16, END = MISC + 16;
     // P's term and buffer: the second and third terms have the place of the staged output
     __host__ __device__ static constexpr uint32_t term(int t, int b) { return t == 0 ? P + b * (C * C * 2) : O + (2 * b + t - 1) * (C * C * 2); }
     // an A operand of 64 value channels is read as 128: up to 8 KB behind its tile
     static constexpr uint32_t BYTES = END + 1024 + 64;
 };
-// TMEM columns: S^T, its bf16 copy, the three terms of the scaled values, QK, O1, O2
-constexpr uint32_t TM_S = 0, TM_SB = 128, TM_VD = 192, TM_QK = 288, TM_O1 = 352, TM_O2 = 416, TM_COLS = 512;
+// TMEM columns: S^T; its bf16 copy; the terms of the scaled values; what a chunk adds to kN key channels of S^T; QK;
+// O1; O2.  With 128 key channels all 512 are taken: a state product is formed in two passes of 64, and the values'
+// third term lies in shared memory, in two places by turns (kSmemTerm).
+template <int KD, bool kStates>
+struct Tmem {
+    static constexpr int kN = kStates ? KD : 64;
+    static constexpr bool kSmemTerm = KD == 128 && !kStates;
+    static constexpr uint32_t S = 0, SB = 128, VD = 192, D = KD == 64 ? 64 : kStates ? 288 : 256, QK = KD == 64 ? 288 : 320;
+    static constexpr uint32_t O1 = 384, O2 = 448, COLS = 512;
+};
 
 struct Params {
     const float* decay;
@@ -356,7 +366,8 @@ __global__ void __launch_bounds__(NTHR, 1)
 decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, Params p) {
     using L = Layout<KD, VB, kFine>;
-    constexpr int kTerms = kFine ? 3 : 1;
+    using M = Tmem<KD, kStates>;
+    constexpr int kTerms = kFine ? 3 : 1, NP = KD / M::kN;  // NP: passes of kN key channels of a state product
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
@@ -423,7 +434,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (i >= B_FREE && i < B_FREE + NS) count = kStates ? 1 : 2;   // the products of both issuing warps
             if (i >= B_P && i < B_P + NS) count = 4 + 8;                   // four P warps, eight that have looked at v
             if (i == B_OFREE) count = 4;                                   // four output warps
-            if (i >= B_S && i <= B_VD) count = 8;                          // eight warps
+            if (i >= B_D && i <= B_VD) count = 8;                          // eight warps
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
@@ -433,7 +444,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_o);
     }
-    if (w == 26) tmem_alloc(sb + L::MISC, TM_COLS);
+    if (w == 26) tmem_alloc(sb + L::MISC, M::COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -461,7 +472,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!sy.warp_wait(B_QK, c & 1)) break;
                 if (c >= 2 && !sy.warp_wait(B_O + b, ((c - 2) >> 1) & 1)) break;        // this P buffer's last reader
                 tc_fence_after();
-                const uint32_t gt = gates(c), to = sb + L::P + b * (C * C * 2), qk = tmem + TM_QK + ((uint32_t)(32 * w) << 16);
+                const uint32_t gt = gates(c), to = sb + L::P + b * (C * C * 2), qk = tmem + M::QK + ((uint32_t)(32 * w) << 16);
                 float2 g0 = lds2(gt + GT_G + 8 * r0), g1 = lds2(gt + GT_G + 8 * (r0 + 8));
                 // left of the diagonal block the factor parts into a row's and a column's, both <= 1
 #pragma unroll 1
@@ -634,7 +645,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int kk = 0; kk < KD / 16; ++kk) {
                             const uint32_t d = (kk >> 2) * 512 + (kk & 3) * 2;
-                            umma_bf16(tmem + TM_QK, desc(qa + d), desc(ka + d), idesc_bf16(64, 64, 0, 0), kk > 0);
+                            umma_bf16(tmem + M::QK, desc(qa + d), desc(ka + d), idesc_bf16(64, 64, 0, 0), kk > 0);
                         }
                         umma_commit(sy.bar(B_QK));
                     }
@@ -662,24 +673,37 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (w == 26) {
         // ------------------------------------------------ the state's products
-        constexpr uint32_t id_s = idesc_bf16(128, KD, 0, 1);
+        constexpr uint32_t id_s = idesc_bf16(128, M::kN, 0, 1);
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS;
             const uint32_t k = lo_mn(sb + s * L::STAGE + L::QB);
             if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
-            if (!sy.warp_wait(B_S, c & 1) || !sy.warp_wait(B_VD, c & 1)) break;
-            tc_fence_after();
-            if (elect()) {  // S^T += vd^T k, the three terms of vd
+            if (!sy.warp_wait(B_VD, c & 1)) break;
+            bool ok = true;
+#pragma unroll 1
+            for (int x = 0; x < NP; ++x) {
+                // the state warps have read what it replaces
+                if (x > 0) ok = sy.warp_wait(B_D, c & 1);
+                else if (c > 0) ok = sy.warp_wait(B_DREAD, (c - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect()) {  // vd^T k, the smallest of the three terms of vd first: each cut is one of the sum so far
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
+                    for (int term = 2; term >= 0; --term)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ta(tmem + TM_S, tmem + TM_VD + 32 * term + 8 * kk, desc(k + kk * 128), id_s, 1);
-                umma_commit(sy.bar(B_STATE));
-                if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t b = desc(k + x * 512 + kk * 128);
+                            if (M::kSmemTerm && term == 2) umma_bf16(tmem + M::D, desc(lo_mn(sb + L::LO + (kFine ? 0 : (c & 1) * L::VBYTES)) + kk * 128), b, idesc_bf16(128, M::kN, 1, 1), kk > 0);
+                            else umma_bf16_ta(tmem + M::D, tmem + M::VD + 32 * term + 8 * kk, b, id_s, term < 2 || kk > 0);
+                        }
+                    umma_commit(sy.bar(B_STATE));
+                    if (x + 1 == NP) umma_commit(sy.bar(B_VFREE));
+                    if (x + 1 == NP && c + NS < nt) umma_commit(sy.bar(B_FREE + s));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
         if (__any_sync(0xffffffffu, sy.aborted())) {  // let the MMAs in flight finish
             if (elect()) {
@@ -696,7 +720,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int c = 0; c < nt; ++c) {
                 const int s = c % NS, b = c & 1;
                 const uint32_t q = lo_k(sb + s * L::STAGE), v = lo_mn(sb + s * L::STAGE + 2 * L::QB);
-                bool ok = true;
+                bool ok = sy.warp_wait(B_FULL + s, (c / NS) & 1);  // the queries
+                if (!ok) break;
 #pragma unroll 1
                 for (int t = 0; t < kTerms; ++t) {  // (the terms come one after another into one place)
                     if (!(ok = sy.warp_wait(B_SBF, (kTerms * c + t) & 1))) break;
@@ -705,7 +730,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (elect()) {
 #pragma unroll
                         for (int kk = 0; kk < KD / 16; ++kk)
-                            umma_bf16_ta(tmem + TM_O1, tmem + TM_SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_o1, kk > 0 || t > 0);
+                            umma_bf16_ta(tmem + M::O1, tmem + M::SB + 8 * kk, desc(q + (kk >> 2) * 512 + (kk & 3) * 2), id_o1, kk > 0 || t > 0);
                         umma_commit(sy.bar(B_INTER));
                     }
                     __syncwarp();
@@ -719,7 +744,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int t = 0; t < kTerms; ++t)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + TM_O2, desc(v + kk * 128), desc(lo_k(sb + L::term(t, b)) + kk * 2), id_o2, kk > 0 || t > 0);
+                            umma_bf16(tmem + M::O2, desc(v + kk * 128), desc(lo_k(sb + L::term(t, b)) + kk * 2), id_o2, kk > 0 || t > 0);
                     umma_commit(sy.bar(B_O + b));
                     if (c + NS < nt) umma_commit(sy.bar(B_FREE + s));
                 }
@@ -737,7 +762,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ------------------------------------------------ state: S^T in TMEM, lane = value channel
         const int vl = 32 * (w & 3) + l;
         const uint32_t lane = (uint32_t)(32 * (w & 3)) << 16;
-        const int c0 = w < 8 ? 0 : KD / 2, c1 = c0 + KD / 2;  // this warp's key channels
+        const int c0 = w < 8 ? 0 : 32;  // this warp's key channels: 32 of each 64, from c0
         const bool mine = vl < VB && vc0 + vl < p.V;
         const size_t at = (size_t)p.k0 * p.V + vc0 + vl, st = ((size_t)n * p.H + h) * (size_t)p.K * p.V + at;
         const size_t sg = ((size_t)slot * p.H + h) * (size_t)p.K * p.V + at;
@@ -753,9 +778,20 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!__all_sync(0xffffffffu, come) && l == 0 && !sy.aborted()) sy.give_up();
             __syncwarp();
         }
+        auto arrive = [&](int bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (l == 0) mbar_arrive(sy.bar(bar));
+        };
+        auto copy = [&](int x, const float* v) {  // 32 columns of the bf16 copy
+            uint32_t r[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            tmem_st16(tmem + M::SB + lane + x / 2, r);
+        };
         // the incoming state, 32 rows in flight; an empty sequence's goes straight on
 #pragma unroll 1
-        for (int x = c0; x < c1; x += 32) {
+        for (int x = c0; x < KD; x += 64) {
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -768,8 +804,9 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (nt > 0) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] *= 1.f / (1ll << kTop);  // E = kTop
-                tmem_st16(tmem + TM_S + lane + x, reinterpret_cast<uint32_t*>(v));
-                tmem_st16(tmem + TM_S + lane + x + 16, reinterpret_cast<uint32_t*>(v) + 16);
+                tmem_st16(tmem + M::S + lane + x, reinterpret_cast<uint32_t*>(v));
+                tmem_st16(tmem + M::S + lane + x + 16, reinterpret_cast<uint32_t*>(v) + 16);
+                if (!kStates && !kFine) copy(x, v);
             } else if (dst && mine) {
                 float* to = dst + (size_t)x * p.V;
 #pragma unroll
@@ -777,32 +814,21 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
         tmem_wait_st();
+        if (!kStates && !kFine && nt > 0) arrive(B_SBF);
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
-            if (!(ok = sy.warp_wait(B_FULL + c % NS, (c / NS) & 1))) break;
-            const float gl = lds(gates(c) + GT_LAST);
-            if (c > 0) {
-                if (!(ok = sy.warp_wait(B_STATE, (c - 1) & 1))) break;
-                tc_fence_after();
-            }
-            auto arrive = [&](int bar) {
-                tc_fence_before();
-                __syncwarp();
-                if (l == 0) mbar_arrive(sy.bar(bar));
-            };
-            constexpr int NC = KD / 2;  // this warp's columns
             if constexpr (kFine) {
-                // the three terms one after another, then the scaling: nothing at once, for its registers
+                // the copy's three terms one after another
 #pragma unroll 1
                 for (int t = 0; t < kTerms && ok; ++t) {
                     if (c + t > 0 && !(ok = sy.warp_wait(B_INTER, (kTerms * c + t - 1) & 1))) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < NC; x += 32) {
+                    for (int x = c0; x < KD; x += 64) {
                         float v[32];
                         uint32_t r[16];
-                        ld32(tmem + TM_S + lane + c0 + x, v);
+                        ld32(tmem + M::S + lane + x, v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -810,70 +836,51 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             split(make_float2(v[2 * j], v[2 * j + 1]), r[j], r1, r2);
                             r[j] = t == 0 ? r[j] : t == 1 ? r1 : r2;
                         }
-                        tmem_st16(tmem + TM_SB + lane + (c0 + x) / 2, r);
+                        tmem_st16(tmem + M::SB + lane + x / 2, r);
                     }
                     tmem_wait_st();
                     arrive(B_SBF);
                 }
                 if (!ok) break;
-                if (gl != 1.f) {
+            }
+            const bool more = !kStates && !kFine && c + 1 < nt;  // a copy for the next chunk
 #pragma unroll 1
-                    for (int x = 0; x < NC; x += 16) {
-                        float v[16];
-                        uint32_t u[16];
-                        tmem_ld16(tmem + TM_S + lane + c0 + x, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * gl);
-                        tmem_st16(tmem + TM_S + lane + c0 + x, u);
-                    }
-                    tmem_wait_st();
-                }
-                arrive(B_S);
-                continue;
-            }
-            uint32_t r[NC / 2];  // their bf16 copy
-#pragma unroll
-            for (int x = 0; x < NC; x += 32) {
-                if (kStates && gl == 1.f) continue;
-                float v[32];
-                ld32(tmem + TM_S + lane + c0 + x, v);
+            for (int x = c0; x < KD; x += 64) {
+                if (x % M::kN < 64 && !(ok = sy.warp_wait(B_STATE, (NP * c + x / M::kN) & 1))) break;
+                tc_fence_after();
+                const float gl = lds(gates(c) + GT_LAST);  // (there since the values were scaled)
+                float d[32], v[16];
+                ld32(tmem + M::D + lane + x % M::kN, d);
+                tmem_ld16(tmem + M::S + lane + x, v);
                 tmem_wait_ld();
+                if (x % M::kN + 64 >= M::kN) arrive(x + 64 >= KD ? B_DREAD : B_D);
+                if (more && x == c0 && !(ok = sy.warp_wait(B_INTER, c & 1))) break;  // the copy's last reader
 #pragma unroll
-                for (int j = 0; j < 16; ++j) r[x / 2 + j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                if (gl != 1.f) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t u[16];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 t = mul2(make_float2(v[16 * y + j], v[16 * y + j + 1]), make_float2(gl, gl));
-                            u[j] = __float_as_uint(t.x);
-                            u[j + 1] = __float_as_uint(t.y);
-                        }
-                        tmem_st16(tmem + TM_S + lane + c0 + x + 16 * y, u);
+                for (int y = 0; y < 32; y += 16) {
+                    if (y > 0) {
+                        tmem_ld16(tmem + M::S + lane + x + y, v);
+                        tmem_wait_ld();
                     }
-                }
-            }
-            if (gl != 1.f) tmem_wait_st();
-            arrive(B_S);
-            if constexpr (!kStates) {
-                if (c > 0 && !(ok = sy.warp_wait(B_INTER, (c - 1) & 1))) break;
 #pragma unroll
-                for (int x = 0; x < NC / 2; x += 16) tmem_st16(tmem + TM_SB + lane + c0 / 2 + x, r + x);
-                tmem_wait_st();
-                arrive(B_SBF);
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 t = fma2(make_float2(gl, gl), make_float2(v[j], v[j + 1]), make_float2(d[y + j], d[y + j + 1]));
+                        d[y + j] = t.x;
+                        d[y + j + 1] = t.y;
+                    }
+                    tmem_st16(tmem + M::S + lane + x + y, reinterpret_cast<uint32_t*>(d) + y);
+                }
+                if (more) copy(x, d);
             }
+            if (!ok) break;
+            tmem_wait_st();
+            if (more) arrive(B_SBF);
         }
-        if (nt > 0 && ok) ok = sy.warp_wait(B_STATE, (nt - 1) & 1);
-        if (!kStates && nt > 0 && ok) ok = sy.warp_wait(B_INTER, (kTerms * nt - 1) & 1);
         if (nt > 0 && ok) {
-            tc_fence_after();
             const float out = lds(gates(nt - 1) + GT_OUT);
 #pragma unroll 1
-            for (int x = c0; x < c1; x += 32) {
+            for (int x = c0; x < KD; x += 64) {
                 float v[32];
-                ld32(tmem + TM_S + lane + x, v);
+                ld32(tmem + M::S + lane + x, v);
                 tmem_wait_ld();
                 if (dst && mine) {
                     float* to = dst + (size_t)x * p.V;  // (one address carried on, not 32 kept)
@@ -919,8 +926,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t at = tmem + lane + ((uint32_t)(16 * (x >> 1)) << 16) + 32 * (x & 1);
                         float o1[16], o2[16];
-                        ld16x32(at + TM_O1, o1);
-                        ld16x32(at + TM_O2, o2);
+                        ld16x32(at + M::O1, o1);
+                        ld16x32(at + M::O2, o2);
                         if (x < 3) tmem_wait_ld();
                         else taken();
                         const int ch = 4 * (w & 3) + 2 * (x >> 1) + ((l >> 3) & 1);  // the 16-byte piece of this lane's address
@@ -945,8 +952,8 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         float o1[16], o2[16];
-                        tmem_ld16(tmem + TM_O1 + lane + 16 * x, o1);
-                        tmem_ld16(tmem + TM_O2 + lane + 16 * x, o2);
+                        tmem_ld16(tmem + M::O1 + lane + 16 * x, o1);
+                        tmem_ld16(tmem + M::O2 + lane + 16 * x, o2);
                         if (x < 3) tmem_wait_ld();
                         else taken();
 #pragma unroll
@@ -996,7 +1003,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool mine = 32 * qd < VB;
         // a lane's row of the four 8 x 8 blocks of a load: channels + 0, + 8, rows + 0, + 8
         const int lrow = 32 * jh + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + ((l >> 3) & 1);
-        const uint32_t to = tmem + TM_VD + ((uint32_t)(32 * qd) << 16) + 16 * jh;
+        const uint32_t to = tmem + M::VD + ((uint32_t)(32 * qd) << 16) + 16 * jh;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int s = c % NS, len = min(C, eos - (bos + c * C));
@@ -1050,21 +1057,45 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (l == 0) mbar_arrive(sy.bar(B_P + s));
             }
-            if (c > 0 && !sy.warp_wait(B_STATE, (c - 1) & 1)) break;
+            // the third term has two places in shared memory, whose last reader was the product of two chunks ago
+            // (one for a float32 output, which then waits like the others)
+            uint32_t mid[2][8];
+            const uint32_t lo = sb + L::LO + (kFine ? 0 : (c & 1) * L::VBYTES) + (qd >> 1) * 8192u;
+            auto third = [&] {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t r[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        mid[y][e] = cut(rest[y][e]);
+                        r[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; g += 2) stmatrix4_t(lo + sw128(lrow + 8 * g, lpiece + 2 * y), r + 2 * g);  // as the values lie there
+                }
+                fence_proxy_async_smem();
+            };
+            if (M::kSmemTerm && !kFine && mine) third();
+            if (c > 0 && !sy.warp_wait(B_VFREE, (c - 1) & 1)) break;
             tc_fence_after();
+            if (M::kSmemTerm && kFine && mine) third();
             if (mine) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const uint32_t at = to + ((uint32_t)(16 * y) << 16);
-                    uint32_t r[8];
                     st16x16(at, hi[y]);
+                    if constexpr (M::kSmemTerm) {
+                        st16x16(at + 32, mid[y]);
+                    } else {
+                        uint32_t r[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = cut(rest[y][e]);
-                    st16x16(at + 32, r);
+                        for (int e = 0; e < 8; ++e) r[e] = cut(rest[y][e]);
+                        st16x16(at + 32, r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        r[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
-                    st16x16(at + 64, r);
+                        for (int e = 0; e < 8; ++e)
+                            r[e] = __byte_perm(__float_as_uint(rest[y][e].x), __float_as_uint(rest[y][e].y), 0x7632);
+                        st16x16(at + 64, r);
+                    }
                 }
                 tmem_wait_st();
             }
@@ -1077,7 +1108,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     if (w == 26) {
         tc_fence_after();
-        tmem_dealloc(tmem, TM_COLS);
+        tmem_dealloc(tmem, M::COLS);
     }
 }
 

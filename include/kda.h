@@ -389,14 +389,13 @@ typedef enum {
  * output the scores and the state that the queries read are rounded to bf16 once as
  * operands, which adds up to 2^-8 of the sum of the absolute values of o's terms (in
  * the norm 2.3e-3 of o with its own rounding, which alone is 1.7e-3); a KDA_F32
- * output has neither, and takes up to 2.3 times as long.  The tensor cores cut what
- * they add to an FP32 accumulator, toward zero: a state leans by up to 12 x 2^-23 (1.4e-6)
- * of the sum of the absolute values of its terms for each 64 tokens of the decay's memory.
- * Measured with terms of one sign: 9e-6 at a decay of -0.0023, 2e-4 at -0.0001, 4e-4 over
- * 32768 tokens with hardly any decay (1e-4 there with random terms); a prompt that is
- * cut in time (few heads) starts anew with each piece.  The state is kept scaled down by
- * up to 2^32: it overflows only where float32 does, and values below 2^-85 lose low bits.
- * Float32 inputs and the recurrent form add in rounded FP32.
+ * output has neither, and takes about twice as long.  The tensor cores cut what
+ * they add to an FP32 accumulator, so a chunk's additions are summed apart and added to
+ * the state in rounded FP32: a state is off by at most 12 x 2^-23 of the sum of a chunk's
+ * absolute values and by a rounded addition for each 64 tokens, and a decay by 2^-33.
+ * Measured: 1e-7 of the state at a decay of -0.0023, up to 1e-6 over 32768 tokens with
+ * hardly any.  The state is kept scaled down by up to 2^32: it overflows only where
+ * float32 does, and values below 2^-85 lose low bits.
  */
 size_t kda_decay_chunk_workspace_bytes(kda_dtype qkv_dtype, int B, int T, int H, int K, int V,
                                        int n_seqs);

@@ -159,3 +159,24 @@ def test_packed_float32(kda, name, H, Hk, K, V, state):  # noqa: F811
 @pytest.mark.parametrize("inplace", [False, True])
 def test_dense_float32(kda, B, T, H, inplace):  # noqa: F811
     check(kda, "kda_decay_chunk_fwd", inputs(T, B, T, H, 1, 96, 130, torch.float32, B, span=0.3), inplace=inplace)
+
+
+@pytest.mark.parametrize("K,V,o_dtype", [(64, 64, None), (64, 128, None), (128, 64, None), (128, 128, None), (64, 128, torch.float32),
+                                         (128, 128, torch.float32), (256, 256, None)])
+@pytest.mark.parametrize("B,T,H", [(2, 1081, 8), (1, 1400, 6), (3, 200, 60)])
+def test_the_same_bits_from_cold_caches(kda, K, V, o_dtype, B, T, H):  # noqa: F811
+    """Loads that take their time, which shows a product that does not wait for its operand: segments, whole and
+    cut sequences, every result the same as the first."""
+    x = [dev(t) for t in inputs(T, B, T, H, H, K, V, BF, B, span=0.3)]
+    first, cold = None, torch.empty(1 << 26, device="cuda")
+    for i in range(40):
+        cold.fill_(i)  # (256 MB, twice the L2)
+        got = kda.kda_decay_chunk_fwd(*x[:4], initial_state=x[4], output_final_state=True, o_dtype=o_dtype)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]), i
+    o_ref, S_ref, oa, Sa = ref.decay_attention(*(t[:1, :, :2].cpu() for t in x[:4]), x[4][:1, :2].cpu())
+    f32 = (K + 128 + T) * F32
+    operand = HALF[BF] * (1 + 2.0 ** -6) if o_dtype is None else 0.0
+    o, S = first
+    close(o[:1, :, :2], o_ref, HALF[o.dtype] * o_ref.abs() + (operand + f32) * oa + 1e-30, "o")
+    close(S[:1, :2], S_ref, f32 * Sa + 1e-30, "state")

@@ -225,3 +225,35 @@ def test_a_wait_that_gives_up_among_values_that_are_not_finite(kda, o_dtype, sms
         kda.kda_test_hooks()
     check(kda, "kda_decay_chunk_fwd", x, o_dtype=o_dtype)
     assert kda.kda_fused_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("rate", [0.0, 1e-6, 1e-4, 0.0023, 0.3])
+@pytest.mark.parametrize("one_sign", [True, False])
+@pytest.mark.parametrize("K", [64, 128, 256])
+@pytest.mark.parametrize("T", [64, 4096, 32768])
+def test_a_state_does_not_lean_with_its_memory(kda, rate, one_sign, K, T):  # noqa: F811
+    """Whole bf16 sequences: a chunk's twelve accumulations cut at most 2^-23 each of that chunk's own sum, a rounded
+    addition for each chunk of the memory, the decays' own 2^-33 a token, a few u for the factors (those of the
+    scaled sums: 2^-24 in the exponent)."""
+    H = 2
+    g = torch.Generator(device="cuda").manual_seed(int(rate * 1e7) + K)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k = (torch.nn.functional.normalize(r(1, T, H, K), dim=-1).to(BF) for _ in range(2))
+    v = r(1, T, H, 64).to(BF)
+    if one_sign:
+        k, v = k.abs(), v.abs()
+    a = torch.full((H,), -rate, device="cuda")
+    w = torch.exp(a[0].double() * torch.arange(T - 1, -1, -1, device="cuda"))
+    want = torch.einsum("t,thk,thv->hkv", w, k[0].double(), v[0].double())[None]
+    size = torch.einsum("t,thk,thv->hkv", w, k[0].double().abs(), v[0].double().abs())[None]
+    try:
+        kda.kda_test_hooks(sm_count=1)
+        _, S = kda.kda_decay_chunk_fwd(q, k, v, a, output_final_state=True)
+    finally:
+        kda.kda_test_hooks()
+    memory = min(T, 1 / rate) if rate else T
+    bound = 12 * 2.0 ** -23 + (memory / 64 + 1) * F32 + T * 2.0 ** -33 + 16 * F32
+    close(S, want.cpu(), (bound * size).cpu(), "state")
+    # random roundings: their 2-norm is as float32 sums have it, whatever the memory
+    if not one_sign:
+        assert (S.double() - want).norm() <= (1e-6 + T * 2.0 ** -33) * want.norm()
