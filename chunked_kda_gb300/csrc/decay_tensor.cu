@@ -34,14 +34,15 @@
 // whatever their signs.  That costs a read of the sum and a read and write of S a chunk (4 x 4096 tokens, 64 heads:
 // 218 us against 203).
 //
-// What bounds it is shared memory's 128 bytes a clock next to HBM: per chunk at K = V = 128 the loads
-// write 48 KB, the products read 120 KB, the warps and the stores about 60 KB.  That is why the scaled
-// values are the operand that lies in TMEM, straight from registers: scaled keys in shared memory cost
-// 48 KB of writes and 48 KB of reads more a chunk (4 x 4096 tokens, 64 heads, whole units: 239 us against 214).
-// That case, its final state written, moves 1.09 GB in 204 us with cut units, 5.3 TB/s; 20480 packed tokens with
-// states, 32 heads: 0.74 GB in 139 us, 5.3 TB/s; one sequence of 32767 tokens, 16 heads, cut into segments (k and v
-// read twice): 170 us.  A head of 256 key channels is two of 128 whose FP32 outputs are written, read back and added
-// (8 x 2048 tokens, 32 heads, 256 x 256: 727 us, of which 194 for the addition, against 7266 in FP32).
+// What bounds it is shared memory's 128 bytes a clock next to HBM, and the order of a chunk's steps through TMEM: per
+// chunk at K = V = 128 the loads write 48 KB, the products read 150 KB, the warps and the stores about 75 KB.  That is
+// why two terms of the scaled values are operands that lie in TMEM, straight from registers (the third there too
+// would be 5 us less of the 218 below, but there is no column left for it); scaled keys in shared memory cost
+// 48 KB of writes and 48 KB of reads more a chunk.  4 x 4096 tokens, 64 heads, the final state written: 1.09 GB in
+// 218 us with cut units, 5.0 TB/s; 20480 packed tokens with states, 32 heads: 0.74 GB in 147 us, 5.0 TB/s; one
+// sequence of 32767 tokens, 16 heads, cut into segments (k and v read twice): 180 us.  A head of 256 key channels is
+// two of 128 whose FP32 outputs are written, read back and added (8 x 2048 tokens, 32 heads, 256 x 256: 735 us, of
+// which 194 for the addition, against 7266 in FP32).
 //
 // One CTA per unit and SM, 28 warps: 0-3 P, 4-11 state, 12-15 output, 16-23 scaled values, 24 the output's
 // products, 25 decay factors, 26 the state's products, 27 loads and scores.  Every wait is bounded (a CTA
@@ -315,8 +316,8 @@ __device__ __noinline__ void nan_rows(uint32_t tile, uint32_t marks, int ch, uin
 // the part at this SM's end runs per - nt chunks or more after the other's end and finds its state there.
 // Blocks take the pieces in the order of their starts (a ticket, so that whoever waits began later than what it waits for):
 // the SMs' first pieces, then the whole units, then the cut units' second pieces, the longest first (their SMs
-// are free first).  4 x 4096 tokens, 64 heads (256 units): 204 us against 215 with whole
-// units; 5 x 4096, 64 heads (320): 246 against 310; 2 x 16384, 80 heads (160): 459 against 789.
+// are free first).  4 x 4096 tokens, 64 heads (256 units): 218 us against 225 with whole
+// units; 5 x 4096, 64 heads (320): 264 against 331; 2 x 16384, 80 heads (160): 479 against 841.
 struct Piece {
     int unit, c0, c1;
 };
@@ -1214,8 +1215,8 @@ int plan_segment(int B, int T, int H, int vblocks, int N, bool packed) {
 }
 
 // Chunks of an SM where units are cut (0: they are not).  Cuts cost an SM about eight chunks (a state's way,
-// more starts): 8 x 1024 tokens, 32 heads (27 chunks an SM for the 32 of two waves) 70 us with cuts and
-// 64 without, 8 x 2048, 64 heads (108 for 128) 215 and 221.
+// more starts): 8 x 1024 tokens, 32 heads (27 chunks an SM for the 32 of two waves) 78 us with cuts and
+// 69 without, 8 x 2048, 64 heads (108 for 128) 231 and 234.
 int plan_cuts(int B, int T, int H, int vblocks) {
     const long sms = planned_sm_count(), units = (long)B * H * vblocks, nt = (T + C - 1) / C;
     if (sms <= 0 || units <= sms || units * nt > 1 << 30 || sms > kMaxCuts) return 0;
