@@ -37,11 +37,11 @@
 // What bounds it is shared memory's 128 bytes a clock next to HBM, and the order of a chunk's steps through TMEM: per
 // chunk at K = V = 128 the loads write 48 KB, the products read 150 KB, the warps and the stores about 75 KB.  That is
 // why two terms of the scaled values are operands that lie in TMEM, straight from registers (there is no column left
-// for the third); scaled keys in shared memory cost 48 KB of writes and 48 KB of reads more a chunk.  4 x 4096 tokens, 64 heads, the final state written: 1.09 GB in
-// 218 us with cut units, 5.0 TB/s; 20480 packed tokens with states, 32 heads: 0.74 GB in 147 us, 5.0 TB/s; one
-// sequence of 32767 tokens, 16 heads, cut into segments (k and v read twice): 180 us.  A head of 256 key channels is
-// two of 128 whose FP32 outputs are written, read back and added (8 x 2048 tokens, 32 heads, 256 x 256: 735 us, of
-// which 194 for the addition, against 7266 in FP32).
+// for the third); scaled keys in shared memory cost 48 KB of writes and 48 KB of reads more a chunk.
+// 4 x 4096 tokens, 64 heads, the final state written: 1.09 GB in 218 us with cut units, 5.0 TB/s; 20480 packed tokens
+// with states, 32 heads: 0.74 GB in 147 us, 5.0 TB/s; one sequence of 32767 tokens, 16 heads, cut into segments (k
+// and v read twice): 180 us.  A head of 256 key channels is two of 128 whose FP32 outputs are written, read back and
+// added (8 x 2048 tokens, 32 heads, 256 x 256: 735 us, of which 194 for the addition, against 7266 in FP32).
 //
 // One CTA per unit and SM, 28 warps: 0-3 P, 4-11 state, 12-15 output, 16-23 scaled values, 24 the output's
 // products, 25 decay factors, 26 the state's products, 27 loads and scores.  Every wait is bounded (a CTA
