@@ -22,7 +22,8 @@ __all__ = ["kda_gate_fwd", "kda_chunk_workspace_bytes", "kda_chunk_workspace_byt
            "FLAG_Q_L2NORM", "NOALLOC_SCRATCH_BYTES", "library_path", "load_library",
            "kda_decay_chunk_workspace_bytes", "kda_decay_chunk_fwd", "kda_decay_recurrent_fwd",
            "kda_gated_norm_fwd", "kda_block_norm_fwd", "kda_short_conv_fwd", "ACT_NONE",
-           "ACT_SIGMOID", "ACT_SILU"]
+           "ACT_SIGMOID", "ACT_SILU", "kda_delta_chunk_workspace_bytes", "kda_delta_chunk_fwd",
+           "kda_delta_recurrent_fwd", "kda_qk_norm_rope_fwd", "NORM_NONE", "NORM_RMS", "NORM_L2"]
 
 GATE_PRE = 0
 GATE_SAFE = 1
@@ -33,6 +34,7 @@ FLAG_Q_L2NORM = 1  # KDA_FLAG_Q_L2NORM
 FLAG_K_L2NORM = 2  # KDA_FLAG_K_L2NORM
 FLAG_BETA_LOGITS = 4  # KDA_FLAG_BETA_LOGITS
 ACT_NONE, ACT_SIGMOID, ACT_SILU = 0, 1, 2  # kda_act
+NORM_NONE, NORM_RMS, NORM_L2 = 0, 1, 2  # kda_norm
 _F32, _BF16 = 0, 1
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -106,6 +108,17 @@ def load_library():
                                            vp, vp, vp]
         lib.kda_short_conv_fwd.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32,
                                            vp, vp]
+        u32 = ctypes.c_uint
+        lib.kda_delta_chunk_workspace_bytes.argtypes = [i32] * 8
+        lib.kda_delta_chunk_workspace_bytes.restype = size
+        delta = [vp, vp, vp, i32, vp, i32, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp,
+                 i32, u32]
+        lib.kda_delta_chunk_fwd.argtypes = [*delta, vp, size, vp, vp]
+        lib.kda_delta_recurrent_fwd.argtypes = [*delta, vp]
+        lib.kda_qk_norm_rope_fwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, f32, vp, i32, vp, ctypes.c_char_p,
+                                             i32, i32, f32, i64, i32, i32, i32, vp, i64, vp, i64, vp]
+        for fn in (lib.kda_delta_chunk_fwd, lib.kda_delta_recurrent_fwd, lib.kda_qk_norm_rope_fwd):
+            fn.restype = ctypes.c_int
         for fn in (lib.kda_decay_chunk_fwd, lib.kda_decay_recurrent_fwd, lib.kda_gated_norm_fwd,
                    lib.kda_block_norm_fwd, lib.kda_short_conv_fwd):
             fn.restype = ctypes.c_int
@@ -388,3 +401,5 @@ def kda_recurrent_fwd_ex(q, k, v, g, beta, A_log=None, dt_bias=None, mode=GATE_L
 
 from ._block import (kda_block_norm_fwd, kda_decay_chunk_fwd, kda_decay_chunk_workspace_bytes,  # noqa: E402
                      kda_decay_recurrent_fwd, kda_gated_norm_fwd, kda_short_conv_fwd)
+from ._delta import (kda_delta_chunk_fwd, kda_delta_chunk_workspace_bytes, kda_delta_recurrent_fwd,  # noqa: E402
+                     kda_qk_norm_rope_fwd)

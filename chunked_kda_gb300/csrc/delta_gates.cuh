@@ -1,0 +1,47 @@
+// A token's decay and beta of the gated delta rule, as its entry points take them: given, or activated here.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace delta {
+
+struct Gates {
+    const void* g;
+    const void* beta;
+    const float* A_log;
+    const float* dt_bias;
+    int H;
+    bool g_bf16, beta_bf16, raw, logits;
+
+    Gates() = default;
+    explicit Gates(const DeltaArgs& a)
+        : g(a.g), beta(a.beta), A_log(a.A_log), dt_bias(a.dt_bias), H(a.H), g_bf16(a.g_bf16), beta_bf16(a.beta_bf16),
+          raw(a.mode == 2), logits((a.flags & KDA_FLAG_BETA_LOGITS) != 0) {}
+
+    // a head's exp(A_log) and dt_bias, read once
+    struct Head {
+        float expA, dtb;
+    };
+    __device__ __forceinline__ Head head(int h) const {
+        return {raw ? expf(__ldg(A_log + h)) : 0.f, raw && dt_bias ? __ldg(dt_bias + h) : 0.f};
+    }
+    __device__ __forceinline__ static float load(const void* p, bool bf16, size_t i) {
+        return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : __ldg(static_cast<const float*>(p) + i);
+    }
+    // the natural-log decay of token t in head h
+    __device__ __forceinline__ float decay(size_t t, int h, Head c) const {
+        const float x = load(g, g_bf16, t * H + h);
+        return raw ? gate_act(x, c.expA, c.dtb, 2, 0.f) : x;
+    }
+    __device__ __forceinline__ float rate(size_t t, int h) const {
+        const float b = load(beta, beta_bf16, t * H + h);
+        return logits ? 1.f / (1.f + expf(-b)) : b;
+    }
+};
+
+}  // namespace delta
+}  // namespace kda

@@ -1,0 +1,408 @@
+// The gated delta rule with a decay for each head in chunks of 64 tokens, in FP32 without tensor cores: float32
+// inputs (whose 24 bits the tensor cores' operand types do not hold), float32 outputs of bf16 inputs, and head sizes
+// that the tensor-core kernel does not take.
+//
+// G_i the decay's sum up to and including row i of a chunk, l its last row, s = 1/sqrt(K), S the incoming state:
+//   A_ij = beta_i e^(G_i - G_j) k_i . k_j (j < i),   T = (1 + A)^-1 diag(beta)
+//   U = T (V - diag(e^G) K S),   O = s (diag(e^G) Q S + (e^(G_i - G_j) q_i . k_j)_{j <= i} U)
+//   S <- e^G_l S + K^T diag(e^(G_l - G_j)) U
+// Two launches:
+//   1. per chunk and head, all at once: T, the masked scores P and the rows' factors, into scratch: a row of kRow
+//      floats for each token and head, so that it does not grow with the number of sequences;
+//   2. per (sequence, head, block of VB value columns), chunks in order: the state in shared memory.
+// The value columns are independent of one another, so with few heads narrow blocks fill the SMs.
+// A masked element is 0, and 0 times a value that is not finite is NaN: the triangular products leave out what is
+// masked instead, so nothing reaches back.
+#include "common.cuh"
+#include "decay_gates.cuh"
+#include "delta_gates.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace delta {
+namespace {
+
+using namespace kda::decay;
+
+constexpr int C = 64, NT = 256, LD = 68;  // LD: row stride of a 64-wide shared tile, 16-byte aligned
+// a token's row in scratch: T's row, P's row, then e^G_i / |k_i|, s e^G_i / |q_i|, e^(G_l - G_i) / |k_i| and e^G_l
+// (the norms where they are asked for)
+constexpr int kRow = 2 * C + 4, kFactors = 2 * C;
+
+struct Args {
+    Gates gates;
+    const float* h0;
+    float* hT;
+    ChunkMap cm;
+    int H, hr, K, V;
+    unsigned flags;
+    float* ws;
+};
+
+// four consecutive elements of a row of n, the first at c (0 behind the row)
+template <typename T>
+__device__ __forceinline__ void load4(const T* row, int c, int n, float (&r)[4]) {
+    if (n % 4 == 0) {
+        if (c >= n) {
+            r[0] = r[1] = r[2] = r[3] = 0.f;
+        } else if constexpr (sizeof(T) == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(row + c);
+            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + c);
+            r[0] = sm100::bf_lo(v.x); r[1] = sm100::bf_hi(v.x); r[2] = sm100::bf_lo(v.y); r[3] = sm100::bf_hi(v.y);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = c + e < n ? to_f32(row[c + e]) : 0.f;
+    }
+}
+// [64 rows][nc channels from c0], transposed: lanes are rows, so that the stores meet no bank twice
+template <typename T>
+__device__ __forceinline__ void load_transposed(const T* base, size_t stride, int len, int c0, int nc, int n, float* out) {
+    for (int x = threadIdx.x; x < C * (nc / 4); x += NT) {
+        const int i = x & 63, c = 4 * (x >> 6);
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+        if (i < len) load4(base + i * stride, c0 + c, n, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(c + e) * LD + i] = r[e];
+    }
+}
+
+// X = (1 + A)^-1 of a strictly lower triangular 64 x 64 matrix, by all threads; Y: 32 x 33 floats between.  The diagonal
+// blocks of 16 by substitution, a column a thread, then twice the block below two inverted ones: -X22 (A21 X11).
+__device__ __forceinline__ void invert(const float* A, float* X, float* Y) {
+    const int tid = threadIdx.x;
+    for (int x = tid; x < C * LD; x += NT) X[x] = 0.f;
+    __syncthreads();
+    if (tid < 64) {
+        const int b = tid & ~15, c = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float y = i == c ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m)
+                if (m >= c) y = fmaf(-A[(b + i) * LD + b + m], x[m], y);
+            x[i] = i >= c ? y : 0.f;
+            X[(b + i) * LD + b + c] = x[i];
+        }
+    }
+    for (int w = 16; w < C; w *= 2) {
+        for (int o = 0; o < C; o += 2 * w) {
+            __syncthreads();
+            for (int x = tid; x < w * w; x += NT) {
+                const int i = x / w, c = x % w;
+                float y = 0.f;
+                for (int m = c; m < w; ++m) y = fmaf(A[(o + w + i) * LD + o + m], X[(o + m) * LD + o + c], y);
+                Y[i * 33 + c] = y;
+            }
+            __syncthreads();
+            for (int x = tid; x < w * w; x += NT) {
+                const int i = x / w, c = x % w;
+                float y = 0.f;
+                for (int m = 0; m <= i; ++m) y = fmaf(X[(o + w + i) * LD + o + w + m], Y[m * 33 + c], y);
+                X[(o + w + i) * LD + o + c] = -y;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// grid (slots, H)
+template <typename T>
+__global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q, const T* __restrict__ k, Args p) {
+    __shared__ __align__(16) float sk[C * LD], sq[C * LD];  // 64 channels of k and q, transposed; then A and its inverse
+    __shared__ float sy[32 * 33], s_beta[C], s_nk[C], s_nq[C];
+    __shared__ int sI[2][C], s_bad;
+    int n, t0, len, bos, eos;
+    if (!p.cm.map(blockIdx.x, n, t0, len, bos, eos)) return;
+    const int h = blockIdx.y, tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
+    if (tid < 32) {
+        const Gates::Head head = p.gates.head(h);
+        const int i0 = 2 * tid;
+        const float a0 = i0 < len ? p.gates.decay(t0 + i0, h, head) : 0.f;
+        const float a1 = i0 + 1 < len ? p.gates.decay(t0 + i0 + 1, h, head) : 0.f;
+        long long G[2];
+        pair_sums(a0, a1, G);
+        const int bad = first_nan(a0, a1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) parts(G[e], sI[0][i0 + e], sI[1][i0 + e]);
+        if (tid == 0) s_bad = bad;
+    } else if (tid < 32 + C) {
+        const int i = tid - 32;
+        s_beta[i] = i < len ? p.gates.rate(t0 + i, h) : 0.f;
+    }
+    const int Hk = p.H / p.hr, hq = h / p.hr;
+    const T* kb = k + ((size_t)t0 * Hk + hq) * p.K;
+    const T* qb = q + ((size_t)t0 * Hk + hq) * p.K;
+    float kk[4][4] = {}, qk[4][4] = {}, nq = 0.f;
+    for (int c0 = 0; c0 < p.K; c0 += 64) {
+        __syncthreads();
+        load_transposed(kb, (size_t)Hk * p.K, len, c0, 64, p.K, sk);
+        load_transposed(qb, (size_t)Hk * p.K, len, c0, 64, p.K, sq);
+        __syncthreads();
+#pragma unroll 4
+        for (int c = 0; c < 64; ++c) {
+            const float4 a = *reinterpret_cast<const float4*>(sk + c * LD + 4 * ti);
+            const float4 b = *reinterpret_cast<const float4*>(sq + c * LD + 4 * ti);
+            const float4 d = *reinterpret_cast<const float4*>(sk + c * LD + 4 * tj);
+            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w}, dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    kk[i][j] = fmaf(av[i], dv[j], kk[i][j]);
+                    qk[i][j] = fmaf(bv[i], dv[j], qk[i][j]);
+                }
+        }
+        if (tid < C && (p.flags & KDA_FLAG_Q_L2NORM))
+            for (int c = 0; c < 64; ++c) nq = fmaf(sq[c * LD + tid], sq[c * LD + tid], nq);
+    }
+    if (tid < C) s_nq[tid] = p.flags & KDA_FLAG_Q_L2NORM ? rsqrtf(nq + kQNormEps) : 1.f;
+    if (ti == tj)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_nk[4 * ti + i] = p.flags & KDA_FLAG_K_L2NORM ? rsqrtf(kk[i][i] + kQNormEps) : 1.f;
+    __syncthreads();
+    const float scale = rsqrtf((float)p.K);
+    const int bad = s_bad;
+    float* row0 = p.ws + ((size_t)t0 * p.H + h) * kRow;
+    const size_t stride = (size_t)p.H * kRow;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ti + i;
+        float out[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = 4 * tj + j;
+            float a = 0.f, x = 0.f;
+            if (c <= r) {
+                const float f = s_nk[c] * pow2(sI[0][r] - sI[0][c], sI[1][r] - sI[1][c]) + nan_if(r >= bad);
+                x = scale * s_nq[r] * f * qk[i][j];
+                a = c < r ? s_beta[r] * s_nk[r] * f * kk[i][j] : 0.f;
+            }
+            sk[r * LD + c] = a;
+            out[j] = x;
+        }
+        if (r < len) *reinterpret_cast<float4*>(row0 + r * stride + C + 4 * tj) = make_float4(out[0], out[1], out[2], out[3]);
+    }
+    if (tid < len) {
+        const float poison = nan_if(tid >= bad), e = pow2(sI[0][tid], sI[1][tid]) + poison;
+        *reinterpret_cast<float4*>(row0 + tid * stride + kFactors) =
+            make_float4(e * s_nk[tid], scale * e * s_nq[tid],
+                        (pow2(sI[0][C - 1] - sI[0][tid], sI[1][C - 1] - sI[1][tid]) + nan_if(bad < C)) * s_nk[tid],
+                        pow2(sI[0][C - 1], sI[1][C - 1]) + nan_if(bad < C));
+    }
+    __syncthreads();
+    invert(sk, sq, sy);
+    for (int x = tid; x < C * 16; x += NT) {
+        const int r = x >> 4, c = 4 * (x & 15);
+        if (r >= len) break;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = c + j <= r ? sq[r * LD + c + j] * s_beta[c + j] : 0.f;
+        *reinterpret_cast<float4*>(row0 + r * stride + c) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+}
+
+// [n][W] columns from a pair of shared vectors
+template <int W>
+__device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
+    if constexpr (W == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        r[0] = x.x; r[1] = x.y;
+    } else {
+        r[0] = *p;
+    }
+}
+
+// grid (V blocks, H, sequences).  A thread has four rows of a chunk and W of the block's VB = 16 W columns.
+template <typename T, typename OT, int W>
+__global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                         const T* __restrict__ v, OT* __restrict__ o, Args p) {
+    constexpr int VB = 16 * W;
+    extern __shared__ __align__(16) float sm[];
+    const int Kp = (p.K + 63) / 64 * 64;
+    float* sk = sm;               // [Kp][LD] k, transposed
+    float* sq = sk + Kp * LD;     // [Kp][LD] q
+    float* st = sq + Kp * LD;     // [64][LD] T, transposed
+    float* sp = st + C * LD;      // [64][LD] P
+    float* sS = sp + C * LD;      // [Kp][VB]
+    float* sr = sS + Kp * VB;     // [64][VB] V - diag(e^G) K S
+    float* su = sr + C * VB;      // [64][VB] U
+    float* sd = su + C * VB;      // [64][VB] U with the factors of the state
+    float* sf = sd + C * VB;      // [64][4] factors
+    const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
+    const int v0 = blockIdx.x * VB, h = blockIdx.y, n = blockIdx.z;
+    int bos, eos;
+    if (p.cm.cu) { bos = __ldg(p.cm.cu + n); eos = __ldg(p.cm.cu + n + 1); }
+    else         { bos = n * p.cm.T; eos = bos + p.cm.T; }
+    const int Hk = p.H / p.hr, hq = h / p.hr, col = v0 + W * tj;
+    const size_t state = ((size_t)n * p.H + h) * (size_t)p.K * p.V;
+    for (int x = tid; x < Kp * VB; x += NT) {
+        const int c = x / VB, d = v0 + x % VB;
+        sS[x] = p.h0 && c < p.K && d < p.V ? p.h0[state + (size_t)c * p.V + d] : 0.f;
+    }
+    for (int t0 = bos; t0 < eos; t0 += C) {
+        const int len = min(C, eos - t0);
+        const float* ws = p.ws + ((size_t)t0 * p.H + h) * kRow;
+        load_transposed(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sk);
+        load_transposed(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sq);
+        load_transposed(ws, (size_t)p.H * kRow, len, 0, C, C, st);
+        load_transposed(ws + C, (size_t)p.H * kRow, len, 0, C, C, sp);
+        sf[tid] = (tid >> 2) < len ? ws[(size_t)(tid >> 2) * p.H * kRow + kFactors + (tid & 3)] : 0.f;
+        float vr[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                vr[i][e] = 4 * ti + i < len && col + e < p.V ? to_f32(v[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e]) : 0.f;
+        __syncthreads();
+        float y[4][W] = {}, acc[4][W] = {};
+#pragma unroll 4
+        for (int c = 0; c < p.K; ++c) {
+            const float4 a = *reinterpret_cast<const float4*>(sk + c * LD + 4 * ti);
+            const float4 b = *reinterpret_cast<const float4*>(sq + c * LD + 4 * ti);
+            float s[W];
+            lds_row<W>(sS + c * VB + W * tj, s);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                y[0][e] = fmaf(a.x, s[e], y[0][e]);
+                y[1][e] = fmaf(a.y, s[e], y[1][e]);
+                y[2][e] = fmaf(a.z, s[e], y[2][e]);
+                y[3][e] = fmaf(a.w, s[e], y[3][e]);
+                acc[0][e] = fmaf(b.x, s[e], acc[0][e]);
+                acc[1][e] = fmaf(b.y, s[e], acc[1][e]);
+                acc[2][e] = fmaf(b.z, s[e], acc[2][e]);
+                acc[3][e] = fmaf(b.w, s[e], acc[3][e]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                sr[(4 * ti + i) * VB + W * tj + e] = fmaf(-sf[4 * (4 * ti + i)], y[i][e], vr[i][e]);
+                acc[i][e] *= sf[4 * (4 * ti + i) + 1];
+                y[i][e] = 0.f;
+            }
+        __syncthreads();
+        auto lower = [&](const float* M, const float* B, float (&r)[4][W]) {  // r_i += sum_{j <= i} M_ij B_j
+            for (int j = 0; j < 4 * ti; ++j) {
+                const float4 a = *reinterpret_cast<const float4*>(M + j * LD + 4 * ti);
+                float b[W];
+                lds_row<W>(B + j * VB + W * tj, b);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    r[0][e] = fmaf(a.x, b[e], r[0][e]);
+                    r[1][e] = fmaf(a.y, b[e], r[1][e]);
+                    r[2][e] = fmaf(a.z, b[e], r[2][e]);
+                    r[3][e] = fmaf(a.w, b[e], r[3][e]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float b[W];
+                lds_row<W>(B + (4 * ti + j) * VB + W * tj, b);
+#pragma unroll
+                for (int i = j; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) r[i][e] = fmaf(M[(4 * ti + j) * LD + 4 * ti + i], b[e], r[i][e]);
+            }
+        };
+        lower(st, sr, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                su[(4 * ti + i) * VB + W * tj + e] = y[i][e];
+                sd[(4 * ti + i) * VB + W * tj + e] = 4 * ti + i < len ? y[i][e] * sf[4 * (4 * ti + i) + 2] : 0.f;
+            }
+        __syncthreads();
+        lower(sp, su, acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (4 * ti + i < len && col + e < p.V)
+                    o[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e] = from_f32<OT>(acc[i][e]);
+        const float last = sf[3];
+        for (int c0 = 4 * ti; c0 < Kp; c0 += 64) {
+            float add[4][W] = {};
+#pragma unroll 2
+            for (int j = 0; j < C; j += 4) {
+                float u[4][W];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) lds_row<W>(sd + (j + x) * VB + W * tj, u[x]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 a = *reinterpret_cast<const float4*>(sk + (c0 + i) * LD + j);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        add[i][e] = fmaf(a.x, u[0][e], add[i][e]);
+                        add[i][e] = fmaf(a.y, u[1][e], add[i][e]);
+                        add[i][e] = fmaf(a.z, u[2][e], add[i][e]);
+                        add[i][e] = fmaf(a.w, u[3][e], add[i][e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    float* s = sS + (c0 + i) * VB + W * tj + e;
+                    *s = fmaf(last, *s, add[i][e]);
+                }
+        }
+        __syncthreads();
+    }
+    if (!p.hT) return;
+    __syncthreads();  // (an empty sequence's state passes through)
+    for (int x = tid; x < Kp * VB; x += NT) {
+        const int c = x / VB, d = v0 + x % VB;
+        if (c < p.K && d < p.V) p.hT[state + (size_t)c * p.V + d] = sS[x];
+    }
+}
+
+template <typename T, typename OT, int W>
+cudaError_t run_chain(const DeltaArgs& a, const Args& p) {
+    constexpr int VB = 16 * W;
+    const int Kp = (a.K + 63) / 64 * 64;
+    const int bytes = (2 * Kp * LD + 2 * C * LD + Kp * VB + 3 * C * VB + 4 * C) * (int)sizeof(float);
+    auto kern = delta_chain_kernel<T, OT, W>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((a.V + VB - 1) / VB, a.H, a.N), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
+    return cudaGetLastError();
+}
+
+template <typename T, typename OT>
+cudaError_t run(const DeltaArgs& a) {
+    const ChunkMap cm{a.cu, a.N, a.T, C};
+    const Args p{Gates(a), a.h0, a.hT, cm, a.H, a.H / a.Hk, a.K, a.V, a.flags, (float*)a.ws};
+    if (a.T > 0) {
+        delta_prep_kernel<T><<<dim3(cm.n_slots(), a.H), NT, 0, a.stream>>>((const T*)a.q, (const T*)a.k, p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    int dev = 0, sms = 1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const bool narrow = (long)a.N * a.H * ((a.V + 31) / 32) < sms;
+    return narrow ? run_chain<T, OT, 1>(a, p) : run_chain<T, OT, 2>(a, p);
+}
+
+}  // namespace
+}  // namespace delta
+
+size_t delta_simt_workspace_bytes(int B, int T, int H) {
+    return ((size_t)B * T * H * delta::kRow * sizeof(float) + 255) / 256 * 256;
+}
+
+cudaError_t launch_delta_simt(const DeltaArgs& a) {
+    if (a.N == 0) return cudaSuccess;
+    if (!a.qkv_bf16) return delta::run<float, float>(a);
+    return a.o_f32 ? delta::run<__nv_bfloat16, float>(a) : delta::run<__nv_bfloat16, __nv_bfloat16>(a);
+}
+
+}  // namespace kda

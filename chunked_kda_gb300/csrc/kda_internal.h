@@ -95,6 +95,57 @@ struct DecayArgs {
     cudaStream_t stream;
 };
 
+// the gated delta rule with a decay for each head
+struct DeltaArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    bool qkv_bf16;
+    const void* g;  // [B, T, H]: the natural-log decay (mode 0) or the raw gate (mode 2)
+    bool g_bf16;
+    const float* A_log;    // [H]
+    const float* dt_bias;  // [H] or null
+    int mode;              // 0 pre-gated, 2 non-safe
+    const void* beta;      // [B, T, H]
+    bool beta_bf16;
+    const float* h0;
+    float* hT;
+    const int32_t* cu;
+    int N;  // logical sequences (B when dense)
+    int B, T, H, Hk, K, V;
+    void* o;
+    bool o_f32;      // o is float32 (else the qkv dtype)
+    unsigned flags;  // KDA_FLAG_Q_L2NORM, KDA_FLAG_K_L2NORM, KDA_FLAG_BETA_LOGITS
+    void* ws;
+    int* status;
+    cudaStream_t stream;
+};
+
+// the norm of query and key heads and the rotation of their positions
+struct QkNormArgs {
+    struct Side {
+        const void* x;
+        long stride;  // elements between tokens
+        const float* weight;
+        void* y;
+        long y_stride;
+        int heads;
+    } q, k;  // k.x null: queries alone
+    bool bf16;
+    int norm;  // kda_norm
+    float eps;
+    const int32_t* positions;  // [n_axes][tokens]
+    int n_axes;
+    const float* inv_freq;           // [R / 2]
+    const unsigned char* pair_axes;  // host memory, [R / 2], or null
+    int R;
+    bool interleaved;
+    float rope_scale;
+    long tokens;
+    int D;
+    cudaStream_t stream;
+};
+
 struct GatedNormArgs {
     const void* x;
     const void* gate;
@@ -157,6 +208,14 @@ cudaError_t read_norm_timeouts(unsigned* count, bool reset);
 cudaError_t launch_gated_norm(const GatedNormArgs& a);
 cudaError_t launch_block_norm(const BlockNormArgs& a);
 cudaError_t launch_short_conv(const ConvArgs& a);
+
+size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, int N, bool packed);
+cudaError_t launch_delta_chunk(const DeltaArgs& a);
+cudaError_t launch_delta_recurrent(const DeltaArgs& a);
+// its FP32 kernels: any dtype, any K and V up to 256
+size_t delta_simt_workspace_bytes(int B, int T, int H);
+cudaError_t launch_delta_simt(const DeltaArgs& a);
+cudaError_t launch_qk_norm_rope(const QkNormArgs& a);
 
 cudaError_t launch_gate(const GateArgs& a);
 cudaError_t launch_recurrent(const RecArgs& a);

@@ -200,7 +200,7 @@ kda_status kda_chunk_fwd(const void* q, const void* k, const void* v, kda_dtype 
                          int V, int chunk_size, void* o, kda_dtype o_dtype, void* workspace,
                          size_t workspace_bytes, kda_stream_t stream);
 
-/* Option bits of kda_chunk_fwd_ex (Q_L2NORM) and kda_recurrent_fwd_ex (all three). */
+/* Option bits of kda_chunk_fwd_ex (Q_L2NORM), kda_recurrent_fwd_ex and the delta rule's calls (all three). */
 #define KDA_FLAG_Q_L2NORM 1u    /* normalise every query row inside the forward */
 #define KDA_FLAG_K_L2NORM 2u    /* normalise every key row inside the forward */
 #define KDA_FLAG_BETA_LOGITS 4u /* beta holds logits; sigmoid(beta) is used */
@@ -414,6 +414,94 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
                                    const int32_t* cu_seqlens, int n_seqs, int B, int T, int H,
                                    int n_qk_heads, int K, int V, void* o, kda_dtype o_dtype,
                                    kda_stream_t stream);
+
+/*
+ * The gated delta rule with a decay for each head.  Per head, FP32 state S (K x V):
+ *
+ *     S_t = exp(a_t) S_{t-1};  S_t += beta_t k_t (v_t - S_t^T k_t)^T;  o_t = S_t^T q_t / sqrt(K)
+ *
+ * which is kda_chunk_fwd's rule with one decay for all key channels: no number per channel is
+ * read or formed, and the decay has no bound.
+ *
+ *   q, k, v, o, o_dtype, n_qk_heads, states, cu_seqlens: as for kda_decay_chunk_fwd
+ *   g, g_dtype  [B, T, H], KDA_F32 or KDA_BF16 (aligned to its elements).  KDA_GATE_PRE: the
+ *               natural-log decay a (a <= 0 is the meant range, -inf clears the state);
+ *               KDA_GATE_NONSAFE: a = -exp(A_log) softplus(g + dt_bias), A_log [H] float32
+ *               required, dt_bias [H] float32 or NULL.  Other modes: KDA_ERR_UNSUPPORTED.
+ *   beta        [B, T, H], beta_dtype the qkv dtype or KDA_F32
+ *   flags       KDA_FLAG_Q_L2NORM, KDA_FLAG_K_L2NORM: a row is used as x / sqrt(sum x^2 + 1e-6);
+ *               KDA_FLAG_BETA_LOGITS: sigmoid(beta) is used
+ *   K, V        any value from 1 to 256
+ *   o           may be v (with one dtype); final_state may be initial_state
+ *
+ * kda_delta_chunk_fwd is the form for prompts, in chunks of 64 tokens: with G the running sum of a
+ * in the chunk, l its last token, and the rows of K, V, U, O its tokens,
+ *     A_ij = beta_i exp(G_i - G_j) k_i . k_j (j < i),   U = (1 + A)^-1 diag(beta) (V - diag(e^G) K S)
+ *     O = ( diag(e^G) Q S + (exp(G_i - G_j) q_i . k_j)_{j <= i} U ) / sqrt(K)
+ *     S <- e^G_l S + K^T diag(e^(G_l - G)) U
+ * Its scratch is kda_delta_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for dense
+ * inputs); status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the form for single tokens
+ * and computes token by token in FP32.
+ *
+ * What is not finite never reaches back: a gate, beta or key that is not finite reaches the outputs
+ * of its head from its token on, a value those of its channel.
+ */
+size_t kda_delta_chunk_workspace_bytes(kda_dtype qkv_dtype, kda_dtype o_dtype, int B, int T, int H,
+                                       int K, int V, int n_seqs);
+
+kda_status kda_delta_chunk_fwd(const void* q, const void* k, const void* v, kda_dtype qkv_dtype,
+                               const void* g, kda_dtype g_dtype, const float* A_log,
+                               const float* dt_bias, kda_gate_mode mode, const void* beta,
+                               kda_dtype beta_dtype, const float* initial_state,
+                               float* final_state, const int32_t* cu_seqlens, int n_seqs, int B,
+                               int T, int H, int n_qk_heads, int K, int V, void* o,
+                               kda_dtype o_dtype, unsigned flags, void* workspace,
+                               size_t workspace_bytes, int32_t* status, kda_stream_t stream);
+
+kda_status kda_delta_recurrent_fwd(const void* q, const void* k, const void* v,
+                                   kda_dtype qkv_dtype, const void* g, kda_dtype g_dtype,
+                                   const float* A_log, const float* dt_bias, kda_gate_mode mode,
+                                   const void* beta, kda_dtype beta_dtype,
+                                   const float* initial_state, float* final_state,
+                                   const int32_t* cu_seqlens, int n_seqs, int B, int T, int H,
+                                   int n_qk_heads, int K, int V, void* o, kda_dtype o_dtype,
+                                   unsigned flags, kda_stream_t stream);
+
+/* the norm of a query or key row */
+typedef enum {
+    KDA_NORM_NONE = 0, /* x */
+    KDA_NORM_RMS = 1,  /* x / sqrt(mean(x^2) + eps) */
+    KDA_NORM_L2 = 2    /* x / sqrt(sum(x^2) + eps) */
+} kda_norm;
+
+/*
+ * The norm of each query and key head and the rotation of its position, in one pass in front of a
+ * recurrence or an attention.  Per row of D elements (a token's head):
+ *     y = norm(x) * weight
+ *     (y_a, y_b) <- rope_scale (y_a cos - y_b sin, y_b cos + y_a sin)   for the pairs of the first R elements
+ * pair i < R/2 is (i, R/2 + i), or (2i, 2i + 1) with interleaved != 0; its angle is the token's
+ * position on the pair's axis times inv_freq[i].  Angles are formed in 64 bits, so far positions
+ * lose nothing.
+ *
+ *   q, q_out    [tokens, Hq, D], dtype; q_stride, q_out_stride: elements from one token to the next
+ *               (at least Hq D), so that both may be parts of wider rows.  q_out may be q.
+ *   k, k_out    the same with Hk heads; Hk = 0: no keys (NULL)
+ *               Aligned to their elements; where D and R are multiples of 8 and rows begin
+ *               16-byte aligned, rows move as vectors.
+ *   weights     [D] float32 or NULL (= 1)
+ *   positions   int32 [n_axes, tokens], n_axes from 1 to 4 (one for text; time, height and width
+ *               for images and video).  R = 0: no rotation, NULL.
+ *   inv_freq    float32 [R/2]
+ *   pair_axes   HOST memory, [R/2]: the axis of each pair; NULL: the first for all
+ *   D           from 1 to 256; R even, at most D
+ */
+kda_status kda_qk_norm_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                kda_dtype dtype, const float* q_weight, const float* k_weight,
+                                kda_norm norm, float eps, const int32_t* positions, int n_axes,
+                                const float* inv_freq, const unsigned char* pair_axes, int R,
+                                int interleaved, float rope_scale, int64_t tokens, int Hq, int Hk,
+                                int D, void* q_out, int64_t q_out_stride, void* k_out,
+                                int64_t k_out_stride, kda_stream_t stream);
 
 /*
  * Gated norm of the heads' outputs: per row of V elements
