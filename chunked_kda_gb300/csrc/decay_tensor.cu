@@ -48,12 +48,11 @@
 // that gives up lets its copies and MMAs finish, frees its TMEM and returns).  The roles' loops are kept
 // rolled and short: together they have to fit the instruction caches (unrolled, "no instruction" was 40 %
 // of all stalls and a chunk took twice as long).
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "decay_gates.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
+#include "tile_ops.cuh"
 
 namespace kda {
 namespace decay {
@@ -143,144 +142,6 @@ struct Sync {
         return __all_sync(0xffffffffu, !aborted());
     }
 };
-
-// A product's operand in shared memory: the descriptor's low word changes with the address (16-byte
-// units), its high word (stride 1024 bytes between groups of 8 rows, 128-byte swizzle) does not.
-__device__ __forceinline__ uint32_t lo_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }               // K-major
-__device__ __forceinline__ uint32_t lo_mn(uint32_t addr) { return (addr >> 4) | ((8192u >> 4) << 16); }    // MN-major, 64 apart
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)DESC_HI << 32) | lo; }
-// True in one lane of a converged warp.  The products are issued inside a branch on this: there
-// their descriptors stay in uniform registers and a product of 128 x 64 x 16 issues in 31 to 48
-// clocks, its own time; in a branch on the lane number, or each predicated, it took 50 to 85.
-__device__ __forceinline__ uint32_t elect() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p;
-}
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// the issued stores have read their shared memory / are complete
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ float lds(uint32_t a) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 lds2(uint32_t a) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 lds4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-__device__ __forceinline__ void sts2(uint32_t a, float x, float y) {
-    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
-__device__ __forceinline__ uint16_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint16_t v) { asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory"); }
-__device__ __forceinline__ void ld_s128(uint32_t a, uint32_t* v) {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
-}
-
-__device__ __forceinline__ void ld32(uint32_t t, float* v) {
-    tmem_ld16(t, v);
-    tmem_ld16(t + 16, v + 16);
-}
-// 16 lanes x 32 columns: thread t gets lanes t / 4 and t / 4 + 8 and of each eight columns the pair
-// 2 (t % 4), 2 (t % 4) + 1: v[4 g + 0..1] the first lane's, v[4 g + 2..3] the second's
-__device__ __forceinline__ void ld16x32(uint32_t t, float* v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void ld16x16(uint32_t t, float* v) {  // the same for 16 columns
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(t));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-// two FP32 operations in one instruction
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
-        " mov.b64 {%0, %1}, z;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
-        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}\n"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-// four 8 x 8 matrices of 16-bit elements, each stored transposed; lane i holds the address of
-// (transposed) row i % 8 of matrix i / 8
-__device__ __forceinline__ void stmatrix4_t(uint32_t a, const uint32_t* r) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
-// four 8 x 8 matrices of 16-bit elements, each transposed on the way (addresses as above)
-__device__ __forceinline__ void ldmatrix4_t(uint32_t a, uint32_t* r) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-// 16 lanes x 16 columns: of each four columns, thread t has column t % 4 of lanes t / 4 and t / 4 + 8
-__device__ __forceinline__ void st16x16(uint32_t t, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void stmatrix4(uint32_t a, const uint32_t* r) {  // as they are
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
-// The upper bf16 halves of two floats as a pair, and what they leave.  Cutting three times gives a
-// float's 24 significant bits as three bf16 terms exactly: 8 + 8 + 8 (a cut leaves a remainder that
-// the next term holds, as a rounding would, without a conversion).
-__device__ __forceinline__ uint32_t cut(float2& x) {
-    const uint32_t top = 0xFFFF0000u, a = __float_as_uint(x.x), b = __float_as_uint(x.y);
-    x = fma2(make_float2(__uint_as_float(a & top), __uint_as_float(b & top)), make_float2(-1.f, -1.f), x);
-    return __byte_perm(a, b, 0x7632);
-}
-
-// both floats in three terms
-__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = cut(x);
-    mid = cut(x);
-    lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-}
 
 // Values that are not finite in the `len` rows of a tile of VB channels: cleared, and each channel's first of them
 // noted.  (By one warp, out of line and rolled: it runs where something is wrong, if ever.)
@@ -1169,30 +1030,6 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const float* __restrict
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void* ptr = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
-// [tokens, H, D] bf16, box of 64 channels x 1 head x 64 tokens, 128-byte swizzle
-bool make_map(CUtensorMap* m, const void* base, long tokens, int H, int D) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
-    const cuuint32_t box[3] = {64, 1, 64}, estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Tokens of a segment (0: whole sequences).  One CTA per SM runs a unit (a sequence's head and
 // value block) in order, so few units leave SMs idle: the time axis is then cut into segments whose
 // added states come from a first pass over k and v (half of the call's bytes once more) and a scan.

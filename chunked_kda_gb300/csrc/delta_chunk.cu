@@ -5,10 +5,12 @@
 namespace kda {
 
 size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, int N, bool packed) {
-    (void)qkv_bf16; (void)o_f32; (void)K; (void)V; (void)N; (void)packed;
-    return delta_simt_workspace_bytes(B, T, H);
+    (void)N; (void)packed;
+    return delta_tensor_dims(qkv_bf16 && !o_f32, K, V) ? 0 : delta_simt_workspace_bytes(B, T, H);
 }
 
-cudaError_t launch_delta_chunk(const DeltaArgs& a) { return launch_delta_simt(a); }
+cudaError_t launch_delta_chunk(const DeltaArgs& a) {
+    return delta_tensor_dims(a.qkv_bf16 && !a.o_f32, a.K, a.V) ? launch_delta_tensor(a) : launch_delta_simt(a);
+}
 
 }  // namespace kda

@@ -212,6 +212,10 @@ cudaError_t launch_short_conv(const ConvArgs& a);
 size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, int N, bool packed);
 cudaError_t launch_delta_chunk(const DeltaArgs& a);
 cudaError_t launch_delta_recurrent(const DeltaArgs& a);
+// its tensor-core kernel: bf16, K up to 128
+bool delta_tensor_dims(bool bf16, int K, int V);
+cudaError_t launch_delta_tensor(const DeltaArgs& a);
+cudaError_t read_delta_timeouts(unsigned* count, bool reset);
 // its FP32 kernels: any dtype, any K and V up to 256
 size_t delta_simt_workspace_bytes(int B, int T, int H);
 cudaError_t launch_delta_simt(const DeltaArgs& a);

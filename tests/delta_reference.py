@@ -39,17 +39,16 @@ def delta(q, k, v, a, beta, S0=None, edges=None, q_unit=False, k_unit=False, chu
         S = torch.zeros(H, K, V, dtype=torch.float64) if S0 is None else S0[n].double().clone()
         for t in range(lo, hi):
             if (t - lo) % chunk == 0:
-                start, G, us = S.norm(dim=1), torch.zeros(H, dtype=torch.float64), []
+                start, us = S.norm(dim=1), []
             e = a[t].exp()
             S = torch.where(e[:, None, None] == 0, 0.0, e[:, None, None] * S)
             u = b[t][:, None] * (v[t] - (k[t][:, :, None] * S).sum(1))
             S = S + k[t][:, :, None] * u[:, None, :]
             o[t] = s * (q[t][:, :, None] * S).sum(1)
-            G = G + a[t]
-            us.append((G, k[t], u.abs()))
-            inter[t] = s * q[t].norm(dim=-1)[:, None] * G.exp()[:, None] * start
-            for Gj, kj, uj in us:
-                w = torch.where((G - Gj).isnan(), 0.0, (G - Gj).exp()) if len(us) > 1 else torch.ones_like(G)
+            start = start * e[:, None]
+            us = [(w * e, kj, uj) for w, kj, uj in us] + [(torch.ones_like(e), k[t], u.abs())]
+            inter[t] = s * q[t].norm(dim=-1)[:, None] * start
+            for w, kj, uj in us:
                 intra[t] += s * (w * (q[t] * kj).sum(-1).abs())[:, None] * uj
         last.append(S)
     shape = (B, T, H, V)
