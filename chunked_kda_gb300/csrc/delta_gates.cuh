@@ -32,15 +32,14 @@ struct Gates {
     __device__ __forceinline__ static float load(const void* p, bool bf16, size_t i) {
         return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : __ldg(static_cast<const float*>(p) + i);
     }
-    // the natural-log decay of token t in head h
-    __device__ __forceinline__ float decay(size_t t, int h, Head c) const {
-        const float x = load(g, g_bf16, t * H + h);
-        return raw ? gate_act(x, c.expA, c.dtb, 2, 0.f) : x;
-    }
-    __device__ __forceinline__ float rate(size_t t, int h) const {
-        const float b = load(beta, beta_bf16, t * H + h);
-        return logits ? 1.f / (1.f + expf(-b)) : b;
-    }
+    // token t's numbers in head h as they lie there
+    __device__ __forceinline__ float raw_decay(size_t t, int h) const { return load(g, g_bf16, t * H + h); }
+    __device__ __forceinline__ float raw_rate(size_t t, int h) const { return load(beta, beta_bf16, t * H + h); }
+    // the natural-log decay and the rate that they stand for
+    __device__ __forceinline__ float decay_of(float x, Head c) const { return raw ? gate_act(x, c.expA, c.dtb, 2, 0.f) : x; }
+    __device__ __forceinline__ float rate_of(float b) const { return logits ? 1.f / (1.f + expf(-b)) : b; }
+    __device__ __forceinline__ float decay(size_t t, int h, Head c) const { return decay_of(raw_decay(t, h), c); }
+    __device__ __forceinline__ float rate(size_t t, int h) const { return rate_of(raw_rate(t, h)); }
 };
 
 }  // namespace delta

@@ -21,9 +21,10 @@
 // its token on are treated like rows behind the sequence, and the outputs from there on and the state are NaN.  A
 // value: its place in R is cleared and noted (MARK), the channel's outputs from there on and its state are NaN.
 //
-// One CTA per unit and SM, 17 warps: 0-7 the chain (R, U' and S in turn), 8-11 the preparation of the next chunk
-// (scores, inverse), 12-15 the output, 16 loads, gates and all products.  Every wait is bounded (a CTA that gives
-// up lets its copies and MMAs finish, frees its TMEM and returns).
+// One CTA per unit and SM, 15 warps: 0-7 the chain (R, U' and S in turn, and the output while they wait for products),
+// 8-11 the preparation of the next chunk (scores, inverse), 12 all products, 13 loads, 14 gates.  Every wait is
+// bounded (a CTA that gives up lets its copies and MMAs finish, frees its TMEM and returns).  What happens rarely is
+// out of line and loops are rolled: together the roles' loops have to fit the instruction caches.
 #include "common.cuh"
 #include "decay_gates.cuh"
 #include "delta_gates.cuh"
@@ -39,11 +40,12 @@ using namespace kda::decay;
 
 __device__ unsigned int g_delta_timeouts = 0;
 
-constexpr int C = 64, KD = 128, VB = 128, NTHR = 544, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
+constexpr int C = 64, KD = 128, VB = 128, NTHR = 480, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
 
-// barriers
-enum { B_KQ = 0, B_V = B_KQ + NKQ, B_G = B_V + NV, B_F = B_G + NG, B_SC = B_F + 2, B_SCREAD, B_S, B_Y, B_O1, B_R, B_T, B_U, B_UD, B_O1READ, B_D,
-       B_O2, B_O2READ, B_OFREE, B_DRAIN = B_OFREE + 2, B_NEVER, NBAR };
+// Barriers.  A phase's waiters see its parity alone: each barrier's next phase needs (through others) that all waiters of the
+// last one have gone on.  Where that does not follow from the chain's order there is a barrier for each slot of the ring or parity.
+enum { B_KQ = 0, B_V = B_KQ + NKQ, B_G = B_V + NV, B_F = B_G + NG, B_SC = B_F + 2, B_SCREAD, B_S = B_SCREAD + 2, B_Y, B_O1, B_R, B_T, B_U, B_UD, B_D,
+       B_O2, B_O2READ, B_OFREE, B_KQFREE = B_OFREE + 2, B_VFREE = B_KQFREE + NKQ, B_GFREE = B_VFREE + NV, B_DRAIN = B_GFREE + NG, B_NEVER, NBAR };
 
 // shared memory: stages of k and q (by 64 channels: 64 rows of k, then of q), of v; T's terms; P and, behind its reader,
 // the staged output; the third term of R and U'; the matrix of the inverse
@@ -114,6 +116,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t t, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(t));
+}
 // Both floats in three bf16 terms: the first two rounded, the third cut (what is left then has at most eight bits).
 __device__ __forceinline__ uint32_t round2(float2& x) {
     const uint32_t r = pack_bf16(x.x, x.y);
@@ -123,45 +130,6 @@ __device__ __forceinline__ uint32_t round2(float2& x) {
 __device__ __forceinline__ uint32_t top2(float2 x) { return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632); }
 __device__ __forceinline__ float power(float2 a, float2 b) { return ex2_fast((a.x - b.x) + (a.y - b.y)); }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
-
-// One row's scores times their decays: columns [0, 64) of row i (32-lane part `hi` of the rows), x_j f 2^(G_i - G_j), 0
-// where j > last.  Left of the row's part the factor parts into the row's and the column's, both <= 1; within it each
-// is formed by itself.
-template <typename Store>
-__device__ __forceinline__ void masked_scores(uint32_t tmem, uint32_t gt, int i, bool hi, int last, float f, Store store) {
-    const float2 gi = lds2(gt + GT_G + 8 * i);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        float x[16];
-        if (b >= (hi ? 4 : 2)) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        } else {
-            tmem_ld16(tmem + 16 * b, x);
-            tmem_wait_ld();
-            if (hi && b < 2) {
-                const float r = f * power(gi, lds2(gt + GT_G + 8 * (16 * b + 15)));
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 c = lds4(gt + GT_COL + 4 * (16 * b + j));
-                    x[j] *= r * c.x;
-                    x[j + 1] *= r * c.y;
-                    x[j + 2] *= r * c.z;
-                    x[j + 3] *= r * c.w;
-                    if (last < 0) x[j] = x[j + 1] = x[j + 2] = x[j + 3] = 0.f;  // (a row that does not count)
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float4 g = lds4(gt + GT_G + 8 * (16 * b + j));
-                    x[j] = 16 * b + j <= last ? x[j] * f * power(gi, make_float2(g.x, g.y)) : 0.f;
-                    x[j + 1] = 16 * b + j + 1 <= last ? x[j + 1] * f * power(gi, make_float2(g.z, g.w)) : 0.f;
-                }
-            }
-        }
-        store(b, x);
-    }
-}
 
 // X <- (1 + X)^-1 in place, X strictly lower triangular, by 128 threads (named barrier 2).  The diagonal blocks of 16 by
 // substitution, a warp a block and a column a lane, then twice the block below two inverted ones, -X22 (X21 X11).
@@ -192,7 +160,7 @@ __device__ __forceinline__ void invert(uint32_t X, int t) {
     bar_sync(2, 128);
     {   // 16 -> 32: two warps a pair, a row and four columns a thread
         const int o = 32 * (w >> 1), i = (t & 63) >> 2, c = 4 * (t & 3);
-#pragma unroll
+#pragma unroll 1
         for (int step = 0; step < 2; ++step) {  // X21 X11, then -X22 of that
             const uint32_t left = step ? at(o + 16 + i, o + 16) : at(o + 16 + i, o), right = step ? at(o + 16, o + c) : at(o, o + c);
             float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -218,7 +186,7 @@ __device__ __forceinline__ void invert(uint32_t X, int t) {
     }
     {   // 32 -> 64: two rows and four columns a thread
         const int i = 2 * (t >> 3), c = 4 * (t & 7);
-#pragma unroll
+#pragma unroll 1
         for (int step = 0; step < 2; ++step) {
             const uint32_t left = step ? at(32 + i, 32) : at(32 + i, 0), right = step ? at(32, c) : at(0, c);
             float y[2][4] = {};
@@ -264,6 +232,46 @@ __device__ __forceinline__ float row_square(uint32_t panel, int row) {
     return s;
 }
 
+// 16 lanes x 32 columns, as ld16x32 has them
+__device__ __forceinline__ void st16x32(uint32_t t, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+// Where a fragment of Y (or, vt = 0, of U) at t, of 16 channels from ch0 and 32 rows from row0, makes a place of R
+// that is not finite, both Y and v are cleared there, and the channel's first such row is noted.  By one warp, out of
+// line: it runs where something is wrong, if ever.
+__device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, int ch0, int row0, int len, uint32_t marks, volatile uint32_t* flag,
+                                       uint32_t bit) {
+    float a[16];
+    ld16x32(t, a);
+    tmem_wait_ld();
+    const int l = threadIdx.x & 31;
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+        const int ch = ch0 + 8 * ((e >> 1) & 1) + (l >> 2), row = row0 + 8 * (e >> 2) + 2 * (l & 3) + (e & 1);
+        const uint32_t at = vt + ((ch >> 6) & 1) * 8192u + sw128(row, (ch >> 3) & 7) + 2 * (ch & 7);
+        const float r = vt ? fmaf(lds(key + 4 * row), a[e], __uint_as_float((uint32_t)lds16(at) << 16)) : a[e];
+        if (finite(r) || row >= len) continue;
+        a[e] = 0.f;
+        if (vt) sts16(at, 0);
+        asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(marks + 4 * ch), "r"(row) : "memory");
+        atomicOr(const_cast<uint32_t*>(flag), bit);
+    }
+    __syncwarp();
+    st16x32(t, a);
+    tmem_wait_st();
+}
+// rows of a channel's staged output that are none
+__device__ __noinline__ void nan_rows(uint32_t stage, uint32_t mark, int ch, int len, int rows) {
+#pragma unroll 1
+    for (int r = min(len, __float_as_int(lds(mark + 4 * ch))); r < rows; ++r)
+        sts16(stage + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7), 0x7FFF);
+    sts(mark + 4 * ch, __int_as_float(C));
+}
+
 __global__ void __launch_bounds__(NTHR, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ Params p) {
@@ -304,8 +312,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
-            if (i == B_S || i == B_R || i == B_UD) count = 8;
-            if ((i >= B_F && i < B_F + 2) || i == B_SCREAD || i == B_T || i == B_O1READ || i == B_O2READ) count = 4;
+            if (i == B_S || i == B_R || i == B_UD || i == B_O2READ) count = 8;
+            if ((i >= B_F && i < B_F + 2) || (i >= B_SCREAD && i < B_SCREAD + 2) || i == B_T) count = 4;
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
@@ -316,7 +324,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tmap(&tm_o);
     }
     for (int x = tid; x < 2 * VB; x += NTHR) sts(sb + L_MARK + 4 * x, __int_as_float(C));
-    if (w == 16) tmem_alloc(sb + L_MISC + 4 * M_TMEM, TCOLS);
+    if (w == 12) tmem_alloc(sb + L_MISC + 4 * M_TMEM, TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -326,70 +334,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (l == 0) mbar_arrive(sy.bar(bar));
     };
 
-    if (w == 16) {
-        // ------------------------------------------------ loads, gates and all products
-        const Gates::Head head = p.gates.head(h);
-        const float scale = rsqrtf((float)p.K);
-        auto load_kq = [&](int c) {
-            if (elect()) {
-                const uint32_t st = sb + L_KQ + (c % NKQ) * KQ_BYTES, full = sy.bar(B_KQ + c % NKQ);
-                mbar_arrive_expect_tx(full, KQ_BYTES);
-#pragma unroll
-                for (int x = 0; x < KD / 64; ++x) {
-                    tma_load_3d(st + x * PANEL, &tm_k, 64 * x, hq, bos + c * C, full);
-                    tma_load_3d(st + x * PANEL + QROWS, &tm_q, 64 * x, hq, bos + c * C, full);
-                }
-            }
-            __syncwarp();
-        };
-        auto load_v = [&](int c) {
-            if (elect()) {
-                const uint32_t st = sb + L_V + (c % NV) * V_BYTES, full = sy.bar(B_V + c % NV);
-                mbar_arrive_expect_tx(full, V_BYTES);
-#pragma unroll
-                for (int x = 0; x < VB / 64; ++x) tma_load_3d(st + x * 8192, &tm_v, vc0 + 64 * x, h, bos + c * C, full);
-            }
-            __syncwarp();
-        };
-        // a chunk's decays and rates, two tokens a lane, asked for one chunk before they are used
-        float a0, a1, b0, b1;
-        auto ask = [&](int c) {
-            const int t = bos + c * C + 2 * l;
-            a0 = t < eos ? p.gates.decay(t, h, head) : 0.f;
-            a1 = t + 1 < eos ? p.gates.decay(t + 1, h, head) : 0.f;
-            b0 = t < eos ? p.gates.rate(t, h) : 0.f;
-            b1 = t + 1 < eos ? p.gates.rate(t + 1, h) : 0.f;
-        };
-        auto make_gates = [&](int c) {
-            const uint32_t gt = gates(c);
-            const float none = __int_as_float(0x7fffffff);
-            const bool ok0 = a0 < 3e38f && finite(b0), ok1 = a1 < 3e38f && finite(b1);
-            const int bad = first_nan(ok0 ? 0.f : none, ok1 ? 0.f : none);
-            int I[2], F[2];
-            long long G[2];
-            pair_sums(a0, a1, G);
-            parts(G[0], I[0], F[0]);
-            parts(G[1], I[1], F[1]);
-            const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
-            const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
-            const float b[2] = {b0, b1};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * l + e;
-                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f));
-                const float r = pow2(I[e], F[e]);
-                sts(gt + GT_ROW + 4 * i, scale * r);
-                sts(gt + GT_KEY + 4 * i, -r);
-                sts(gt + GT_UPD + 4 * i, i < bad ? pow2(Il - I[e], Fl - F[e]) : 0.f);
-                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]));
-                sts(gt + GT_BETA + 4 * i, i < bad ? b[e] : 0.f);
-            }
-            if (l == 0) {
-                sts(gt + GT_LAST, pow2(Il, Fl));
-                sts(gt + GT_LEN, __int_as_float(min(bad, eos - (bos + c * C))));
-            }
-            arrive(B_G + c % NG);
-        };
+    if (w == 12) {
+        // ------------------------------------------------ all products
         auto scores = [&](int c) {
             sy.wait(B_KQ + c % NKQ, (c / NKQ) & 1);
             tc_fence_after();
@@ -404,58 +350,45 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
         };
-        int kq = 0, v = 0;  // chunks whose loads have been issued
-        while (kq < nt && kq < NKQ) load_kq(kq++);
-        while (v < nt && v < NV) load_v(v++);
-        if (nt > 0) {
-            ask(0);
-            make_gates(0);
-            scores(0);
-            if (nt > 1) {
-                ask(1);
-                make_gates(1);
-            }
-            if (nt > 2) ask(2);
-        }
 #pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
-            const uint32_t st = sb + L_KQ + (c % NKQ) * KQ_BYTES;
-            if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
-            sy.wait(B_S, c & 1);  // S's terms; D of the last chunk has been taken
-            if (sy.stopped()) break;
-            tc_fence_after();
-            if (elect()) {
-                const uint32_t k = lo_k(st);
+        for (int c = -1; c < nt; ++c) {
+            const uint32_t st = sb + L_KQ + ((c + NKQ) % NKQ) * KQ_BYTES;
+            if (c >= 0) {
+                if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
+                sy.wait(B_S, c & 1);  // S's terms; D of the last chunk has been taken
+                if (sy.stopped()) break;
+                tc_fence_after();
+                if (elect()) {
+                    const uint32_t k = lo_k(st);
 #pragma unroll
-                for (int t = 2; t >= 0; --t)
+                    for (int t = 2; t >= 0; --t)
+#pragma unroll
+                        for (int kk = 0; kk < KD / 16; ++kk)
+                            umma_bf16_ta(tmem + TY, tmem + TS + 64 * t + 8 * kk, desc(k + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
+                                         idesc_bf16(128, 64, 0, 0), t < 2 || kk > 0);
+                    umma_commit(sy.bar(B_Y));
+                    const uint32_t q = lo_k(st + QROWS);
 #pragma unroll
                     for (int kk = 0; kk < KD / 16; ++kk)
-                        umma_bf16_ta(tmem + TY, tmem + TS + 64 * t + 8 * kk, desc(k + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
-                                     idesc_bf16(128, 64, 0, 0), t < 2 || kk > 0);
-                umma_commit(sy.bar(B_Y));
-                const uint32_t q = lo_k(st + QROWS);
-#pragma unroll
-                for (int kk = 0; kk < KD / 16; ++kk)
-                    umma_bf16_ta(tmem + TO1, tmem + TS + 8 * kk, desc(q + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
-                                 idesc_bf16(128, 64, 0, 0), kk > 0);
-                umma_commit(sy.bar(B_O1));
+                        umma_bf16_ta(tmem + TO1, tmem + TS + 8 * kk, desc(q + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
+                                     idesc_bf16(128, 64, 0, 0), kk > 0);
+                    umma_commit(sy.bar(B_O1));
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            if (c > 0 && kq < nt) load_kq(kq++);  // (the stage of chunk c - 1: D has been formed)
             if (c + 1 < nt) {
                 if (c > 0) sy.wait(B_O2READ, (c - 1) & 1);
-                else sy.wait(B_SCREAD, 0);
+                if (c == 0) sy.wait(B_SCREAD, 0);
                 scores(c + 1);
             }
-            if (c + 2 < nt) {
-                make_gates(c + 2);
-                if (c + 3 < nt) ask(c + 3);
-            }
+            if (c < 0) continue;
             sy.wait(B_T, c & 1);
             sy.wait(B_R, c & 1);
             if (sy.stopped()) break;
             tc_fence_after();
             if (elect()) {  // the smallest products first
+                mbar_arrive(sy.bar(B_VFREE + c % NV));  // (v has been read into R, the last chunk's output has been formed)
+                if (c > 0) mbar_arrive(sy.bar(B_GFREE + (c - 1) % NG));
                 const uint32_t T = lo_k(sb + L_T), lo = lo_mn(sb + L_LO);
                 bool more = false;
 #pragma unroll
@@ -472,10 +405,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 umma_commit(sy.bar(B_U));
             }
             __syncwarp();
-            if (v < nt) load_v(v++);  // (v has been read into R)
-            sy.wait(B_O1READ, c & 1);
-            if (c + 1 < nt) sy.wait(B_SCREAD, (c + 1) & 1);
-            sy.wait(B_UD, c & 1);
+            sy.wait(B_UD, c & 1);  // (and O1, scaled, lies in O2's place)
             if (sy.stopped()) break;
             tc_fence_after();
             if (elect()) {
@@ -488,58 +418,124 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         else umma_bf16_ta(tmem + TD, tmem + TZ + 32 * t + 8 * kk, desc(k + kk * 128), idesc_bf16(128, KD, 0, 1), 1);
                     }
                 umma_commit(sy.bar(B_D));
+                umma_commit(sy.bar(B_KQFREE + c % NKQ));
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    umma_tf32_ta(tmem + TSC, tmem + TY + 8 * kk, desc(P + (kk >> 2) * 512 + (kk & 3) * 2), idesc_tf32(128, 64), kk > 0);
+                    umma_tf32_ta(tmem + TSC, tmem + TY + 8 * kk, desc(P + (kk >> 2) * 512 + (kk & 3) * 2), idesc_tf32(128, 64), 1);
                 umma_commit(sy.bar(B_O2));
             }
             __syncwarp();
         }
-        if (sy.stopped()) {  // leave no copy and no MMA in flight behind
+        if (sy.stopped()) {  // leave no MMA in flight behind
             if (elect()) {
                 umma_commit(sy.bar(B_DRAIN));
                 mbar_wait(sy.bar(B_DRAIN), 0);
-                for (int x = max(0, kq - NKQ); x < kq; ++x) mbar_wait(sy.bar(B_KQ + x % NKQ), (x / NKQ) & 1);
-                for (int x = max(0, v - NV); x < v; ++x) mbar_wait(sy.bar(B_V + x % NV), (x / NV) & 1);
             }
             __syncwarp();
         }
+    } else if (w == 13) {
+        // ------------------------------------------------ loads
+        int c = 0;
+#pragma unroll 1
+        for (; c < nt; ++c) {
+            if (c >= NKQ) sy.wait(B_KQFREE + c % NKQ, (c / NKQ - 1) & 1);
+            if (c >= NV) sy.wait(B_VFREE + c % NV, (c / NV - 1) & 1);
+            if (sy.stopped()) break;
+            if (elect()) {
+                const uint32_t v = sb + L_V + (c % NV) * V_BYTES, kq = sb + L_KQ + (c % NKQ) * KQ_BYTES;
+                const uint32_t fv = sy.bar(B_V + c % NV), fkq = sy.bar(B_KQ + c % NKQ);
+                mbar_arrive_expect_tx(fkq, KQ_BYTES);
+#pragma unroll
+                for (int x = 0; x < KD / 64; ++x) {
+                    tma_load_3d(kq + x * PANEL, &tm_k, 64 * x, hq, bos + c * C, fkq);
+                    tma_load_3d(kq + x * PANEL + QROWS, &tm_q, 64 * x, hq, bos + c * C, fkq);
+                }
+                mbar_arrive_expect_tx(fv, V_BYTES);
+#pragma unroll
+                for (int x = 0; x < VB / 64; ++x) tma_load_3d(v + x * 8192, &tm_v, vc0 + 64 * x, h, bos + c * C, fv);
+            }
+            __syncwarp();
+        }
+        if (sy.stopped()) {  // leave no copy in flight behind
+            if (elect()) {
+                for (int x = max(0, c - NKQ); x < c; ++x) mbar_wait(sy.bar(B_KQ + x % NKQ), (x / NKQ) & 1);
+                for (int x = max(0, c - NV); x < c; ++x) mbar_wait(sy.bar(B_V + x % NV), (x / NV) & 1);
+            }
+            __syncwarp();
+        }
+    } else if (w == 14) {
+        // ------------------------------------------------ gates: a chunk's decays and rates, two tokens a lane
+        const Gates::Head head = p.gates.head(h);
+        const float scale = rsqrtf((float)p.K);
+        float ra[2], rb[2];  // as they lie in memory, asked for a chunk before they are used
+        auto ask = [&](int c) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = bos + c * C + 2 * l + e;
+                ra[e] = t < eos ? p.gates.raw_decay(t, h) : 0.f;
+                rb[e] = t < eos ? p.gates.raw_rate(t, h) : 0.f;
+            }
+        };
+        if (nt > 0) ask(0);
+#pragma unroll 1
+        for (int c = 0; c < nt; ++c) {
+            const uint32_t gt = gates(c);
+            const int left = eos - (bos + c * C);
+            float a[2], b[2];
+            bool ok[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                a[e] = 2 * l + e < left ? p.gates.decay_of(ra[e], head) : 0.f;
+                b[e] = 2 * l + e < left ? p.gates.rate_of(rb[e]) : 0.f;
+            }
+            if (c + 1 < nt) ask(c + 1);
+            const float none = __int_as_float(0x7fffffff);
+            ok[0] = a[0] < 3e38f && finite(b[0]);
+            ok[1] = a[1] < 3e38f && finite(b[1]);
+            const int bad = first_nan(ok[0] ? 0.f : none, ok[1] ? 0.f : none);
+            int I[2], F[2];
+            long long G[2];
+            pair_sums(a[0], a[1], G);
+            parts(G[0], I[0], F[0]);
+            parts(G[1], I[1], F[1]);
+            const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
+            const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
+            if (c >= NG) sy.wait(B_GFREE + c % NG, (c / NG - 1) & 1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * l + e;
+                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f));
+                const float r = pow2(I[e], F[e]);
+                sts(gt + GT_ROW + 4 * i, scale * r);
+                sts(gt + GT_KEY + 4 * i, -r);
+                sts(gt + GT_UPD + 4 * i, i < bad ? pow2(Il - I[e], Fl - F[e]) : 0.f);
+                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]));
+                sts(gt + GT_BETA + 4 * i, i < bad ? b[e] : 0.f);
+            }
+            if (l == 0) {
+                sts(gt + GT_LAST, pow2(Il, Fl));
+                sts(gt + GT_LEN, __int_as_float(min(bad, left)));
+            }
+            arrive(B_G + c % NG);
+        }
     } else if (w < 8) {
-        // ------------------------------------------------ the chain: R, U' and S, value channels on lanes
+        // ------------------------------------------------ the chain: R, U' and S, value channels on lanes; the output
         const int qd = w & 3, half = w >> 2;
         const uint32_t lane = (uint32_t)(32 * qd) << 16;
         const int vl = 32 * qd + l;
         const bool mine = vc0 + vl < p.V;
-        const size_t state = ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(64 * half) * p.V + vc0 + vl;
         const int rows = min(64, p.K - 64 * half);  // of this warp's 64 key channels
         float S[64];
+        {
+            const float* from = p.h0 + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(64 * half) * p.V + vc0 + vl;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = p.h0 && mine && j < rows ? p.h0[state + (size_t)j * p.V] : 0.f;
-        auto write_terms = [&](int x) {  // of S's 16 columns from x
-            uint32_t t0[8], t1[8], t2[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float2 y = make_float2(S[x + 2 * j], S[x + 2 * j + 1]);
-                t0[j] = round2(y);
-                t1[j] = round2(y);
-                t2[j] = top2(y);
-            }
-            const uint32_t at = tmem + TS + lane + 32 * half + x / 2;
-            tmem_st8(at, t0);
-            tmem_st8(at + 64, t1);
-            tmem_st8(at + 128, t2);
-        };
-        if (nt > 0) {
-#pragma unroll
-            for (int x = 0; x < 64; x += 16) write_terms(x);
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(B_S);
+            for (int j = 0; j < 64; ++j, from += p.V) S[j] = p.h0 && mine && j < rows ? *from : 0.f;
         }
         // a lane's row of the four 8 x 8 blocks of a fragment load: channels + 0, + 8, rows + 0, + 8
         const int lrow = 32 * half + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + ((l >> 3) & 1);
         const uint32_t lo = sb + L_LO + (qd >> 1) * 8192u;
         const uint32_t zcol = tmem + TZ + lane + 16 * half, ycol = tmem + TY + lane + 32 * half;
+        const int pair = 4 * (32 * half + 2 * (l & 3));  // byte offset of a lane's first two rows' factors
         // the terms of sixteen channels' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
         auto write_fragments = [&](int y, float2 (&x)[8]) {
             uint32_t r[8];
@@ -554,16 +550,103 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int g = 0; g < 4; g += 2) stmatrix4_t(lo + sw128(lrow + 8 * g, lpiece + 2 * y), r + 2 * g);
         };
-        // (rolled, and out of the way: it runs where something is wrong, if ever)
-        auto note = [&](int c, int y, int e, bool second) {  // this row of this channel is not finite
-            const int ch = 32 * qd + 16 * y + 8 * (e & 1) + (l >> 2), row = 32 * half + 8 * (e >> 1) + 2 * (l & 3) + (second ? 1 : 0);
-            atomicMin(reinterpret_cast<int*>(smem + L_MARK + 512 * (c & 1)) + ch, row);
-            atomicOr(const_cast<uint32_t*>(misc + M_ODD), 1u << (c & 1));
-        };
+        auto marked = [&](int c) { return ((misc[M_ODD] >> (c & 1)) & 1u) != 0u; };
         const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
-            const uint32_t gt = gates(c), vt = sb + L_V + (c % NV) * V_BYTES + (qd >> 1) * 8192u;
+        for (int c = 0;; ++c) {
+            // ---- S behind chunk c - 1, its terms for chunk c
+            float last = 1.f;
+            if (c > 0) {
+                last = lds(gates(c - 1) + GT_LAST);
+                if (marked(c - 1)) last += nan_if(__float_as_int(lds(sb + L_MARK + 512 * ((c - 1) & 1) + 4 * vl)) < C);
+                sy.wait(B_D, (c - 1) & 1);
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int x = 0; x < 64; x += 16) {
+                if (c > 0) {
+                    float d[16];
+                    tmem_ld16(tmem + TD + lane + 64 * half + x, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 s = fma2(make_float2(last, last), make_float2(S[x + j], S[x + j + 1]), make_float2(d[j], d[j + 1]));
+                        S[x + j] = s.x;
+                        S[x + j + 1] = s.y;
+                    }
+                }
+                uint32_t t0[8], t1[8], t2[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float2 y = make_float2(S[x + 2 * j], S[x + 2 * j + 1]);
+                    t0[j] = round2(y);
+                    t1[j] = round2(y);
+                    t2[j] = top2(y);
+                }
+                const uint32_t at = tmem + TS + lane + 32 * half + x / 2;
+                tmem_st8(at, t0);
+                tmem_st8(at + 64, t1);
+                tmem_st8(at + 128, t2);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(B_S);
+            if (c > 0) {
+                // ---- chunk c - 1's output, through P's place
+                const int b = (c - 1) & 1, t0 = bos + (c - 1) * C, n_rows = min(C, eos - t0);
+                const uint32_t rq = sb + L_RQ + 256 * b, stage = sb + L_P + b * 16384;
+                const int len = __float_as_int(lds(gates(c - 1) + GT_LEN));
+                sy.wait(B_O2, b);
+                tc_fence_after();
+#pragma unroll 1
+                for (int y = 0; y < 2; ++y) {
+                    float o[16];
+                    ld16x32(tmem + TSC + lane + ((uint32_t)(16 * y) << 16) + 32 * half, o);
+                    tmem_wait_ld();
+                    uint32_t r[8];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float2 m = lds2(rq + pair + 32 * g);
+                        const float2 y0 = mul2(m, make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m, make_float2(o[4 * g + 2], o[4 * g + 3]));
+                        r[2 * g] = pack_bf16(y0.x, y0.y);
+                        r[2 * g + 1] = pack_bf16(y1.x, y1.y);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; g += 2) stmatrix4_t(stage + (qd >> 1) * 8192u + sw128(lrow + 8 * g, lpiece + 2 * y), r + 2 * g);
+                }
+                tc_fence_before();
+                arrive(B_O2READ);
+                const bool odd = len < n_rows || marked(c - 1);
+                if (odd) {
+                    bar_sync(1, 256);  // (a channel's rows are two warps')
+                    if (half == 0) nan_rows(stage, sb + L_MARK + 512 * b, vl, len, n_rows);
+                }
+                fence_proxy_async_smem();
+                bar_sync(1, 256);
+                if (odd && tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << b));
+                if (!sy.stopped()) {
+                    if (n_rows == C) {
+                        if (tid == 0) {
+#pragma unroll
+                            for (int x = 0; x < VB / 64; ++x)
+                                if (vc0 + 64 * x < p.V) tma_store_3d(&tm_o, stage + x * 8192, vc0 + 64 * x, h, t0);
+                            bulk_commit();
+                        }
+                    } else {  // the sequence's last rows
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)t0 * p.H + h) * p.V + vc0;
+#pragma unroll 1
+                        for (int x = tid; x < n_rows * (VB / 8); x += 256) {
+                            const int row = x / (VB / 8), ch = x % (VB / 8);
+                            uint32_t v[4];
+                            ld_s128(stage + (ch >> 3) * 8192u + sw128(row, ch & 7), v);
+                            if (vc0 + 8 * ch < p.V) *reinterpret_cast<uint4*>(dst + (size_t)row * p.H * p.V + 8 * ch) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                }
+            }
+            if (c == nt) break;
+            // ---- R
+            const uint32_t gt = gates(c), vt = sb + L_V + (c % NV) * V_BYTES;
             sy.wait(B_F + (c & 1), (c >> 1) & 1);
             sy.wait(B_V + c % NV, (c / NV) & 1);
             const int len = __float_as_int(lds(gt + GT_LEN));
@@ -571,126 +654,115 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_after();
             if (len < C) {  // rows that do not count, for D
                 const uint32_t kt = sb + L_KQ + (c % NKQ) * KQ_BYTES;
+#pragma unroll 1
                 for (int x = tid; x < C * (KD / 8); x += 256)
                     if ((x & 63) >= len) st_s128(kt + (x >> 9) * PANEL + sw128(x & 63, (x >> 6) & 7), 0, 0, 0, 0);
             }
-#pragma unroll
+#pragma unroll 1
             for (int y = 0; y < 2; ++y) {
-                float a[16];
-                float2 x[8], odd = zero;
-                ld16x32(ycol + ((uint32_t)(16 * y) << 16), a);
-                uint32_t r[8];
-                ldmatrix4_t(vt + sw128(lrow, lpiece + 2 * y), r);
-                ldmatrix4_t(vt + sw128(lrow + 16, lpiece + 2 * y), r + 4);
-                tmem_wait_ld();
+                float2 x[8];
+                const uint32_t at = ycol + ((uint32_t)(16 * y) << 16);
+#pragma unroll 1
+                for (int again = 0; again < 2; ++again) {
+                    float a[16];
+                    float2 odd = zero;
+                    uint32_t r[8];
+                    ld16x32(at, a);
+                    ldmatrix4_t(vt + (qd >> 1) * 8192u + sw128(lrow, lpiece + 2 * y), r);
+                    ldmatrix4_t(vt + (qd >> 1) * 8192u + sw128(lrow + 16, lpiece + 2 * y), r + 4);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_KEY + 4 * (32 * half + 8 * g + 2 * (l & 3)));
+                    for (int g = 0; g < 4; ++g) {
+                        const float2 f = lds2(gt + GT_KEY + pair + 32 * g);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int i = 2 * g + e;
-                        x[i] = fma2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]), make_float2(bf_lo(r[i]), bf_hi(r[i])));
-                        if (len < C) {
-                            const int j = 32 * half + 8 * g + 2 * (l & 3);
-                            if (j >= len) x[i].x = 0.f;
-                            if (j + 1 >= len) x[i].y = 0.f;
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 2 * g + e;
+                            x[i] = fma2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]), make_float2(bf_lo(r[i]), bf_hi(r[i])));
                         }
-                        odd = fma2(x[i], zero, odd);
                     }
-                }
-                if (odd.x != 0.f || odd.y != 0.f) {
+                    if (len < C) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (!finite(x[e].x)) { x[e].x = 0.f; note(c, y, e, false); }
-                        if (!finite(x[e].y)) { x[e].y = 0.f; note(c, y, e, true); }
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = 32 * half + 8 * (e >> 1) + 2 * (l & 3);
+                            if (j >= len) x[e].x = 0.f;
+                            if (j + 1 >= len) x[e].y = 0.f;
+                        }
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) odd = fma2(x[e], zero, odd);
+                    if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
+                    clear_odd(at, vt, gt + GT_KEY, 32 * qd + 16 * y, 32 * half, len, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
                 }
-                __syncwarp();
                 write_fragments(y, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_R);
-
-            sy.wait(B_U, c & 1);
+            if (c > 0 && tid == 0) {  // the staged output has left
+                bulk_wait_read();
+                mbar_arrive(sy.bar(B_OFREE + ((c - 1) & 1)));
+            }
+            __syncwarp();
+            // ---- O1 with its rows' factors, where O2 will be added to it
+            if (c == 0) sy.wait(B_SCREAD, 0);
+            if (c + 1 < nt) sy.wait(B_SCREAD + ((c + 1) & 1), ((c + 1) >> 1) & 1);
+            sy.wait(B_O1, c & 1);
             tc_fence_after();
-            const bool marked = ((misc[M_ODD] >> (c & 1)) & 1u) != 0u;
-#pragma unroll
+#pragma unroll 1
             for (int y = 0; y < 2; ++y) {
-                float a[16];
-                float2 x[8], odd = zero;
-                ld16x32(ycol + ((uint32_t)(16 * y) << 16), a);
+                float o[16];
+                const uint32_t at = tmem + lane + ((uint32_t)(16 * y) << 16) + 32 * half;
+                ld16x32(at + TO1, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_UPD + 4 * (32 * half + 8 * g + 2 * (l & 3)));
+                    const float2 f = lds2(gt + GT_ROW + pair + 32 * g);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int i = 2 * g + e;
-                        odd = fma2(make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]), zero, odd);
-                        x[i] = mul2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]));
+                        const float2 s = mul2(f, make_float2(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]));
+                        o[4 * g + 2 * e] = s.x;
+                        o[4 * g + 2 * e + 1] = s.y;
                     }
                 }
-                // U itself is O2's operand: what is not finite there is cleared and noted, too, and a noted
-                // channel's state is none
-                const bool any = odd.x != 0.f || odd.y != 0.f;
-                if (any) {
+                st16x32(at + TSC, o);
+            }
+            // ---- U'
+            sy.wait(B_U, c & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int y = 0; y < 2; ++y) {
+                float a[16];
+                float2 x[8], odd = zero;
+                const uint32_t at = ycol + ((uint32_t)(16 * y) << 16);
+                ld16x32(at, a);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (!finite(a[2 * e])) { a[2 * e] = 0.f; note(c, y, e, false); }
-                        if (!finite(a[2 * e + 1])) { a[2 * e + 1] = 0.f; note(c, y, e, true); }
-                    }
-                }
-                if (marked) {
+                for (int g = 0; g < 4; ++g) {
+                    const float2 f = lds2(gt + GT_UPD + pair + 32 * g);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int ch = 32 * qd + 16 * y + 8 * e + (l >> 2);
-                        if (__float_as_int(lds(sb + L_MARK + 512 * (c & 1) + 4 * ch)) < C) x[e].x = x[e].y = __int_as_float(0x7fffffff);
+                        const float2 u = make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]);
+                        odd = fma2(u, zero, odd);
+                        x[2 * g + e] = mul2(f, u);
                     }
                 }
-                if (__any_sync(0xffffffffu, any)) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(a[e]);
-                    asm volatile(
-                        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-                            ycol + ((uint32_t)(16 * y) << 16)),
-                        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-                        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                        : "memory");
-                }
+                // (U itself is O2's operand)
+                if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f))
+                    clear_odd(at, 0, 0, 32 * qd + 16 * y, 32 * half, C, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
                 write_fragments(y, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_UD);
-
-            const float last = lds(gt + GT_LAST);
-            sy.wait(B_D, c & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 64; x += 16) {
-                float d[16];
-                tmem_ld16(tmem + TD + lane + 64 * half + x, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float2 s = fma2(make_float2(last, last), make_float2(S[x + j], S[x + j + 1]), make_float2(d[j], d[j + 1]));
-                    S[x + j] = s.x;
-                    S[x + j + 1] = s.y;
-                }
-                if (c + 1 < nt) write_terms(x);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(B_S);
         }
+        if (tid == 0) bulk_wait();
         if (p.hT && mine && !sy.aborted()) {
+            float* to = p.hT + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(64 * half) * p.V + vc0 + vl;
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-                if (j < rows) p.hT[state + (size_t)j * p.V] = S[j];
+            for (int j = 0; j < 64; ++j, to += p.V)
+                if (j < rows) *to = S[j];
         }
     } else if (w < 12) {
         // ------------------------------------------------ preparation: T and P of a chunk
@@ -698,13 +770,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool query = t >= 64, hi = (t & 32) != 0;
         const uint32_t sc = tmem + TSC + ((uint32_t)(32 * (w & 3)) << 16), X = sb + L_X;
         const float scale = rsqrtf((float)p.K);
+        const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0, knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const uint32_t gt = gates(c);
             sy.wait(B_G + c % NG, (c / NG) & 1);
             sy.wait(B_SC, c & 1);
             tc_fence_after();
-            // keys that are not finite (their square), and the keys' norms
+            // keys that are not finite (their square), and the rows' norms
             if (!query) {
                 float x[32], kk = 0.f;
                 ld32(sc + (hi ? 32 : 0), x);
@@ -713,65 +786,93 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int j = 0; j < 32; ++j) kk = j == l ? x[j] : kk;
                 const unsigned odd = __ballot_sync(0xffffffffu, !finite(kk) && i < __float_as_int(lds(gt + GT_LEN)));
                 if (l == 0) misc[M_BAD0 + (hi ? 1 : 0)] = odd ? (hi ? 32 : 0) + __ffs(odd) - 1 : C;
-                sts(X + 4 * (LDX * i + 64), (p.flags & KDA_FLAG_K_L2NORM) && finite(kk) ? rsqrtf(kk + kQNormEps) : 1.f);
+                sts(X + 4 * (LDX * i + 64), knorm && finite(kk) ? rsqrtf(kk + kQNormEps) : 1.f);
+            } else {
+                float s = 0.f;
+                if (qnorm) {
+                    const uint32_t q = sb + L_KQ + (c % NKQ) * KQ_BYTES + QROWS;
+#pragma unroll 1
+                    for (int x = 0; x < KD / 64; ++x) s += row_square(q + x * PANEL, i);
+                }
+                sts(sb + L_RQ + 256 * (c & 1) + 4 * i, qnorm ? rsqrtf(s + kQNormEps) : 1.f);
             }
             bar_sync(2, 128);
             const int full = __float_as_int(lds(gt + GT_LEN)), len = min(full, (int)min(misc[M_BAD0], misc[M_BAD1]));
-            const int over = min(C, eos - (bos + c * C));  // rows of the sequence
             const float rk = lds(X + 4 * (LDX * i + 64));
             bar_sync(2, 128);
             if (!query) {
-                if ((p.flags & KDA_FLAG_K_L2NORM) || len < full) {
+                if (knorm || len < full) {
                     sts(gt + GT_KEY + 4 * i, rk * lds(gt + GT_KEY + 4 * i));
                     sts(gt + GT_UPD + 4 * i, i < len ? rk * lds(gt + GT_UPD + 4 * i) : 0.f);
                     if (i >= len) sts(gt + GT_BETA + 4 * i, 0.f);
                 }
                 if (i == 0) {
                     sts(gt + GT_LEN, __int_as_float(len));
-                    if (len < over) sts(gt + GT_LAST, __int_as_float(0x7fffffff));
+                    if (len < min(C, eos - (bos + c * C))) sts(gt + GT_LAST, __int_as_float(0x7fffffff));
                 }
             }
-            if (c >= 2) sy.wait(B_OFREE + (c & 1), ((c - 2) >> 1) & 1);  // P's place; the marks
             arrive(B_F + (c & 1));
-            const bool counts = i < len;
-            const float beta = lds(gt + GT_BETA + 4 * i);
-            // (a key's norm as a column's factor is in T's and P's columns: A's and P's elements take it here)
-            const bool knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
-            auto column_norms = [&](int b, float (&x)[16]) {
-                if (knorm)
+            if (c >= 2) sy.wait(B_OFREE + (c & 1), ((c - 2) >> 1) & 1);  // P's place
+            // A's rows (lanes with keys) into X, P's rows (with queries) as a tf32 operand: the score times
+            // f 2^(G_i - G_j), 0 where j > last.  Left of the row's 32 the factor parts into the row's and the column's,
+            // both <= 1; within them each is formed by itself.
+            const int last = i < len ? i - (query ? 0 : 1) : -1;
+            const float f = query ? scale : lds(gt + GT_BETA + 4 * i) * rk;
+            const float2 gi = lds2(gt + GT_G + 8 * i);
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {  // eight columns each
+                float x[8];
+                if (b < (hi ? 8 : 4)) {
+                    tmem_ld8(sc + 8 * b, x);
+                    tmem_wait_ld();
+                    if (hi && b < 4) {
+                        const float r = last < 0 ? 0.f : f * power(gi, lds2(gt + GT_G + 8 * (8 * b | 15)));
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] *= lds(X + 4 * (LDX * (16 * b + j) + 64));
-            };
-            if (!query)
-                masked_scores(sc, gt, i, hi, counts ? i - 1 : -1, beta * rk, [&](int b, float (&x)[16]) {
-                    column_norms(b, x);
+                        for (int j = 0; j < 8; j += 4) {
+                            const float4 m = lds4(gt + GT_COL + 4 * (8 * b + j));
+                            x[j] = last < 0 ? 0.f : x[j] * (r * m.x);
+                            x[j + 1] = last < 0 ? 0.f : x[j + 1] * (r * m.y);
+                            x[j + 2] = last < 0 ? 0.f : x[j + 2] * (r * m.z);
+                            x[j + 3] = last < 0 ? 0.f : x[j + 3] * (r * m.w);
+                        }
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        st_s128(X + 4 * (LDX * i + 16 * b + j), __float_as_uint(x[j]), __float_as_uint(x[j + 1]),
-                                __float_as_uint(x[j + 2]), __float_as_uint(x[j + 3]));
-                });
-            else
-                masked_scores(sc, gt, i, hi, counts ? i : -1, scale, [&](int b, float (&x)[16]) {
-                    column_norms(b, x);
-                    const uint32_t to = sb + L_P + (c & 1) * 16384 + (b >> 1) * 8192;
+                        for (int j = 0; j < 8; j += 2) {
+                            const float4 g = lds4(gt + GT_G + 8 * (8 * b + j));
+                            x[j] = 8 * b + j <= last ? x[j] * f * power(gi, make_float2(g.x, g.y)) : 0.f;
+                            x[j + 1] = 8 * b + j + 1 <= last ? x[j + 1] * f * power(gi, make_float2(g.z, g.w)) : 0.f;
+                        }
+                    }
+                    if (knorm)
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        st_s128(to + sw128(i, 4 * (b & 1) + j / 4), to_tf32(x[j]), to_tf32(x[j + 1]), to_tf32(x[j + 2]), to_tf32(x[j + 3]));
-                });
+                        for (int j = 0; j < 8; ++j) x[j] *= lds(X + 4 * (LDX * (8 * b + j) + 64));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = 0.f;
+                }
+                const uint32_t to = query ? sb + L_P + (c & 1) * 16384 + (b >> 2) * 8192 : X + 4 * (LDX * i + 8 * b);
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = query ? to_tf32(x[j + e]) : __float_as_uint(x[j + e]);
+                    st_s128(query ? to + sw128(i, 2 * (b & 3) + j / 4) : to + 4 * j, v[0], v[1], v[2], v[3]);
+                }
+            }
             tc_fence_before();
-            arrive(B_SCREAD);
+            arrive(B_SCREAD + (c & 1));
             bar_sync(2, 128);
             invert(X, t);
             // T's terms: a row and 32 columns a thread
             if (c > 0) sy.wait(B_U, (c - 1) & 1);  // their last reader
             const int r = t >> 1, c0 = 32 * (t & 1);
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 32; x += 8) {
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 y = lds4(X + 4 * (LDX * r + c0 + x + 4 * e)), f = lds4(gt + GT_BETA + 4 * (c0 + x + 4 * e));
-                    float2 y0 = mul2(make_float2(y.x, y.y), make_float2(f.x, f.y)), y1 = mul2(make_float2(y.z, y.w), make_float2(f.z, f.w));
+                    const float4 y = lds4(X + 4 * (LDX * r + c0 + x + 4 * e)), m = lds4(gt + GT_BETA + 4 * (c0 + x + 4 * e));
+                    float2 y0 = mul2(make_float2(y.x, y.y), make_float2(m.x, m.y)), y1 = mul2(make_float2(y.z, y.w), make_float2(m.z, m.w));
                     t0[2 * e] = round2(y0);
                     t0[2 * e + 1] = round2(y1);
                     t1[2 * e] = round2(y0);
@@ -788,106 +889,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             arrive(B_T);
             bar_sync(2, 128);  // (X has been read)
         }
-    } else {
-        // ------------------------------------------------ output rows
-        const uint32_t lane = (uint32_t)(32 * (w & 3)) << 16;
-        const int t = tid - 384, ch0 = 32 * (w & 3);
-        const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o);
-        if (t < 64) {
-            sts(sb + L_RQ + 4 * t, 1.f);
-            sts(sb + L_RQ + 256 + 4 * t, 1.f);
-        }
-        bar_sync(1, 128);
-#pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
-            const int t0 = bos + c * C, rows = min(C, eos - t0);
-            const uint32_t gt = gates(c), rq = sb + L_RQ + 256 * (c & 1), stage = sb + L_P + (c & 1) * 16384;
-            if (qnorm) {
-                sy.wait(B_KQ + c % NKQ, (c / NKQ) & 1);
-                float s = row_square(sb + L_KQ + (c % NKQ) * KQ_BYTES + (t & 1) * PANEL + QROWS, t >> 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                if ((t & 1) == 0) sts(rq + 4 * (t >> 1), rsqrtf(s + kQNormEps));
-                bar_sync(1, 128);
-            }
-            sy.wait(B_F + (c & 1), (c >> 1) & 1);
-            const int len = __float_as_int(lds(gt + GT_LEN));
-            sy.wait(B_O1, c & 1);
-            tc_fence_after();
-            // pieces of 16 channels x 32 tokens: fragments of 8 x 8
-            float o1[4][16];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) ld16x32(tmem + TO1 + lane + ((uint32_t)(16 * (x >> 1)) << 16) + 32 * (x & 1), o1[x]);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive(B_O1READ);
-            sy.wait(B_O2, c & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                float o2[16];
-                ld16x32(tmem + TSC + lane + ((uint32_t)(16 * (x >> 1)) << 16) + 32 * (x & 1), o2);
-                const int ch = ch0 / 8 + 2 * (x >> 1) + ((l >> 3) & 1);  // the 16-byte piece of this lane's address
-                const uint32_t base = stage + (ch >> 3) * 8192u;
-                tmem_wait_ld();
-#pragma unroll
-                for (int g = 0; g < 4; g += 2) {
-                    uint32_t r[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int at = 4 * (32 * (x & 1) + 8 * (g + e) + 2 * (l & 3));
-                        const float2 f = lds2(gt + GT_ROW + at), m = lds2(rq + at);
-                        const float *a1 = o1[x] + 4 * (g + e), *a2 = o2 + 4 * (g + e);
-                        const float2 y0 = mul2(m, fma2(f, make_float2(a1[0], a1[1]), make_float2(a2[0], a2[1])));
-                        const float2 y1 = mul2(m, fma2(f, make_float2(a1[2], a1[3]), make_float2(a2[2], a2[3])));
-                        r[2 * e] = pack_bf16(y0.x, y0.y);
-                        r[2 * e + 1] = pack_bf16(y1.x, y1.y);
-                    }
-                    stmatrix4_t(base + sw128(32 * (x & 1) + 8 * (g + (l >> 4)) + (l & 7), ch & 7), r);
-                }
-            }
-            tc_fence_before();
-            const bool odd = len < rows || ((misc[M_ODD] >> (c & 1)) & 1u) != 0u;
-            arrive(B_O2READ);
-            if (odd) {
-                // rows that are none: of a channel a lane, from its mark or the head's on
-                __syncwarp();
-                const int ch = ch0 + l;
-                const uint32_t mark = sb + L_MARK + 512 * (c & 1) + 4 * ch;
-#pragma unroll 1
-                for (int r = min(len, __float_as_int(lds(mark))); r < rows; ++r)
-                    sts16(stage + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7), 0x7FFF);
-                sts(mark, __int_as_float(C));
-            }
-            fence_proxy_async_smem();
-            bar_sync(1, 128);
-            if (odd && t == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << (c & 1)));
-            if (sy.aborted()) {
-                // (as the other warps: each chunk has the same barriers)
-            } else if (rows == C) {
-                if (t == 0) {
-#pragma unroll
-                    for (int x = 0; x < VB / 64; ++x)
-                        if (vc0 + 64 * x < p.V) tma_store_3d(&tm_o, stage + x * 8192, vc0 + 64 * x, h, t0);
-                    bulk_commit();
-                    bulk_wait_read();
-                }
-            } else {
-                __nv_bfloat16* dst = out + ((size_t)t0 * p.H + h) * p.V + vc0;
-                for (int x = t; x < rows * (VB / 8); x += 128) {
-                    const int row = x / (VB / 8), ch = x % (VB / 8);
-                    uint32_t v[4];
-                    ld_s128(stage + (ch >> 3) * 8192u + sw128(row, ch & 7), v);
-                    if (vc0 + 8 * ch < p.V) *reinterpret_cast<uint4*>(dst + (size_t)row * p.H * p.V + 8 * ch) = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            if (t == 0) mbar_arrive(sy.bar(B_OFREE + (c & 1)));
-        }
-        if (t == 0) bulk_wait();
     }
     tc_fence_before();
     __syncthreads();
-    if (w == 16) {
+    if (w == 12) {
         tc_fence_after();
         tmem_dealloc(tmem, TCOLS);
     }
