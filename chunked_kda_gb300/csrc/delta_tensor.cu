@@ -21,8 +21,8 @@
 // its token on are treated like rows behind the sequence, and the outputs from there on and the state are NaN.  A
 // value: its place in R is cleared and noted (MARK), the channel's outputs from there on and its state are NaN.
 //
-// One CTA per unit and SM, 15 warps: 0-7 the chain (R, U' and S in turn, and the output while they wait for products),
-// 8-11 the preparation of the next chunk (scores, inverse), 12 all products, 13 loads, 14 gates.  Every wait is
+// One CTA per unit and SM, 27 warps: 0-15 the chain (R, U' and S in turn, and the output while they wait for products),
+// 16-23 the preparation of the next chunk (scores, inverse), 24 all products, 25 loads, 26 gates.  Every wait is
 // bounded (a CTA that gives up lets its copies and MMAs finish, frees its TMEM and returns).  What happens rarely is
 // out of line and loops are rolled: together the roles' loops have to fit the instruction caches.
 #include "common.cuh"
@@ -40,7 +40,7 @@ using namespace kda::decay;
 
 __device__ unsigned int g_delta_timeouts = 0;
 
-constexpr int C = 64, KD = 128, VB = 128, NTHR = 480, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
+constexpr int C = 64, KD = 128, VB = 128, NTHR = 864, NCH = 512, NPREP = 256, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
 
 // Barriers.  A phase's waiters see its parity alone: each barrier's next phase needs (through others) that all waiters of the
 // last one have gone on.  Where that does not follow from the chain's order there is a barrier for each slot of the ring or parity.
@@ -53,7 +53,7 @@ constexpr uint32_t KQ_BYTES = 32768, PANEL = 16384, QROWS = 8192, V_BYTES = 1638
 constexpr uint32_t L_KQ = 0, L_V = L_KQ + NKQ * KQ_BYTES, L_T = L_V + NV * V_BYTES, L_P = L_T + 3 * T_TERM, L_LO = L_P + 2 * 16384;
 constexpr uint32_t L_X = L_LO + 16384, LDX = 68, L_G = L_X + 64 * LDX * 4;
 // a chunk's factors, one slot of a ring of NG: byte offsets of its float arrays
-constexpr uint32_t GT_G = 0;      // [64][2] G_i as integer and fraction
+constexpr uint32_t GT_G = 0;      // [2][64] -G_i as integer and fraction
 constexpr uint32_t GT_COL = 512;  // [64] 2^(G_m - G_j), m the last of j's 16 rows
 constexpr uint32_t GT_ROW = 768;  // [64] s 2^G_i
 constexpr uint32_t GT_KEY = 1024; // [64] -2^G_i / |k_i|
@@ -70,7 +70,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of a block");
 // TMEM columns: S's three terms; D, whose first half is O1's place; Y, then U; the first two terms of R, then of U'; scores, then O2
 constexpr uint32_t TS = 0, TD = 192, TO1 = 192, TY = 320, TZ = 384, TSC = 448, TCOLS = 512;
 // words of L_MISC
-enum { M_TMEM = 0, M_UNUSED, M_ABORT, M_ODD, M_BAD0, M_BAD1 };  // M_ODD: bit (c & 1): marks of that chunk
+enum { M_TMEM = 0, M_UNUSED, M_ABORT, M_ODD, M_BAD };  // M_ODD: bit (c & 1): marks of that chunk
 
 struct Params {
     Gates gates;
@@ -90,30 +90,45 @@ struct Sync {
     volatile uint32_t* abort_flag;
     int* status;
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
-    __device__ __forceinline__ void give_up() const {
-        atomicAdd(&g_delta_timeouts, 1u);
-        if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
-        *abort_flag = 1u;
+    // One poll, which may sleep until the phase completes.  Without a time hint it is one instruction; with one it
+    // is a loop of its own, and the polls of waiting warps were half of all instructions.
+    static __device__ __forceinline__ bool come(uint32_t bar, uint32_t parity) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        return ok != 0;
     }
-    // (out of line: one copy, so that the loops stay in the instruction caches)
-    __device__ __noinline__ void slow_wait(int i, uint32_t parity, uint32_t limit) const {
-        if (!*abort_flag && !mbar_wait_unless(bar(i), parity, abort_flag, limit)) give_up();
+    // Out of line: one copy, so that the roles' loops fit the instruction caches.  Gives up after about four seconds.
+    static __device__ __noinline__ void wait_out(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int* status) {
+        if (__all_sync(0xffffffffu, come(bar, parity))) return;
+        slow_wait(bar, parity, abort_flag, status, 8000000000ll);
+        __syncwarp();
+    }
+    static __device__ __forceinline__ void slow_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int* status, long long limit) {
+        const long long begin = clock64();
+#pragma unroll 1
+        while (!*abort_flag) {
+            // (short: what waiting warps execute, the working ones cannot)
+#pragma unroll 1
+            for (int n = 0; n < 64; ++n)
+                if (come(bar, parity)) return;
+            if (clock64() - begin > limit) {
+                atomicAdd(&g_delta_timeouts, 1u);
+                if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
+                *abort_flag = 1u;
+            }
+        }
     }
     __device__ __forceinline__ bool aborted() const { return *abort_flag != 0u; }
     __device__ __forceinline__ bool stopped() const { return __any_sync(0xffffffffu, aborted()); }  // by a whole warp
     // A whole warp's wait.  After a wait that gave up all others return at once: the warps run through their loops
     // (their named barriers stay in step) on whatever is there, and nothing is stored.
-    __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return;
-        slow_wait(i, parity, 1u << 22);
-        __syncwarp();
-    }
+    __device__ __forceinline__ void wait(int i, uint32_t parity) const { wait_out(bars + 8u * i, parity, abort_flag, status); }
 };
 
 __device__ __forceinline__ uint32_t lo_kq_mn(uint32_t addr) { return (addr >> 4) | ((PANEL >> 4) << 16); }  // MN-major, panels of k
-__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tmem_st4(uint32_t t, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t t, float* v) {
@@ -121,22 +136,51 @@ __device__ __forceinline__ void tmem_ld8(uint32_t t, float* v) {
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(t));
 }
+// 16 lanes x 8 columns: of each four columns, thread t has column t % 4 of lanes t / 4 and t / 4 + 8
+__device__ __forceinline__ void st16x8(uint32_t t, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 16 lanes x 16 columns, as ld16x16 has them
+__device__ __forceinline__ void st16x16f(uint32_t t, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 // Both floats in three bf16 terms: the first two rounded, the third cut (what is left then has at most eight bits).
+// The remainder is formed by the multiply-add that takes bf16 as it lies in a half of a register: 4.6 clocks a pair, term
+// and scheduler, against 6.6 with the halves unpacked and 8.6 with bits masked off (shifts and masks have half the rate).
 __device__ __forceinline__ uint32_t round2(float2& x) {
     const uint32_t r = pack_bf16(x.x, x.y);
-    x = fma2(make_float2(bf_lo(r), bf_hi(r)), make_float2(-1.f, -1.f), x);
+    asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %4;\n mov.b16 m, 0xBF80;\n"  // -1
+        " fma.rn.f32.bf16 %0, l, m, %2;\n fma.rn.f32.bf16 %1, h, m, %3;\n}\n"
+        : "=f"(x.x), "=f"(x.y)
+        : "f"(x.x), "f"(x.y), "r"(r));
     return r;
 }
+// a + the pair of bf16 numbers in r
+__device__ __forceinline__ float2 add_bf16(uint32_t r, float2 a) {
+    float2 d;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %4;\n add.f32.bf16 %0, l, %2;\n add.f32.bf16 %1, h, %3;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "r"(r));
+    return d;
+}
 __device__ __forceinline__ uint32_t top2(float2 x) { return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632); }
-__device__ __forceinline__ float power(float2 a, float2 b) { return ex2_fast((a.x - b.x) + (a.y - b.y)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-// X <- (1 + X)^-1 in place, X strictly lower triangular, by 128 threads (named barrier 2).  The diagonal blocks of 16 by
+// X <- (1 + X)^-1 in place, X strictly lower triangular, by 256 threads (named barrier 2).  The diagonal blocks of 16 by
 // substitution, a warp a block and a column a lane, then twice the block below two inverted ones, -X22 (X21 X11).
 __device__ __forceinline__ void invert(uint32_t X, int t) {
     const int w = t >> 5, l = t & 31;
     auto at = [&](int i, int c) { return X + 4u * (LDX * i + c); };
-    {
+    if (w < 4) {
         const int b = 16 * w, c = l & 15;
         float x[16];
 #pragma unroll
@@ -157,65 +201,71 @@ __device__ __forceinline__ void invert(uint32_t X, int t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sts(at(b + i, b + c), x[i]);
     }
-    bar_sync(2, 128);
-    {   // 16 -> 32: two warps a pair, a row and four columns a thread
-        const int o = 32 * (w >> 1), i = (t & 63) >> 2, c = 4 * (t & 3);
+    bar_sync(2, NPREP);
+    {   // 16 -> 32: four warps a pair, a row and two columns a thread
+        const int o = 32 * (w >> 2), i = (t & 127) >> 3, c = 2 * (t & 7);
 #pragma unroll 1
         for (int step = 0; step < 2; ++step) {  // X21 X11, then -X22 of that
             const uint32_t left = step ? at(o + 16 + i, o + 16) : at(o + 16 + i, o), right = step ? at(o + 16, o + c) : at(o, o + c);
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 y = make_float2(0.f, 0.f);
 #pragma unroll
             for (int m = 0; m < 16; m += 4) {
                 const float4 a = lds4(left + 4 * m);
                 const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 r = lds4(right + 4 * LDX * (m + e));
-                    y[0] = fmaf(av[e], r.x, y[0]);
-                    y[1] = fmaf(av[e], r.y, y[1]);
-                    y[2] = fmaf(av[e], r.z, y[2]);
-                    y[3] = fmaf(av[e], r.w, y[3]);
-                }
+                for (int e = 0; e < 4; ++e) y = fma2(make_float2(av[e], av[e]), lds2(right + 4 * LDX * (m + e)), y);
             }
-            bar_sync(2, 128);
+            bar_sync(2, NPREP);
             const float s = step ? -1.f : 1.f;
-            sts2(at(o + 16 + i, o + c), s * y[0], s * y[1]);
-            sts2(at(o + 16 + i, o + c + 2), s * y[2], s * y[3]);
-            bar_sync(2, 128);
+            sts2(at(o + 16 + i, o + c), s * y.x, s * y.y);
+            bar_sync(2, NPREP);
         }
     }
-    {   // 32 -> 64: two rows and four columns a thread
-        const int i = 2 * (t >> 3), c = 4 * (t & 7);
-#pragma unroll 1
-        for (int step = 0; step < 2; ++step) {
-            const uint32_t left = step ? at(32 + i, 32) : at(32 + i, 0), right = step ? at(32, c) : at(0, c);
-            float y[2][4] = {};
-#pragma unroll 2
-            for (int m = 0; m < 32; m += 4) {
-                const float4 a = lds4(left + 4 * m), b = lds4(left + 4 * (LDX + m));
-                const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    // 32 -> 64.  Half of a triangular factor is 0: a warp has the shares w and 15 - w of sixteen, 36 of 64 steps at most.
+    {   // X21 X11: a row a lane, two columns c: rows m >= c of X11 count
+        float2 y[2] = {};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 r = lds4(right + 4 * LDX * (m + e));
-                    y[0][0] = fmaf(av[e], r.x, y[0][0]);
-                    y[0][1] = fmaf(av[e], r.y, y[0][1]);
-                    y[0][2] = fmaf(av[e], r.z, y[0][2]);
-                    y[0][3] = fmaf(av[e], r.w, y[0][3]);
-                    y[1][0] = fmaf(bv[e], r.x, y[1][0]);
-                    y[1][1] = fmaf(bv[e], r.y, y[1][1]);
-                    y[1][2] = fmaf(bv[e], r.z, y[1][2]);
-                    y[1][3] = fmaf(bv[e], r.w, y[1][3]);
+        for (int s = 0; s < 2; ++s) {
+            const int c = 2 * (s ? 15 - w : w);
+#pragma unroll 1
+            for (int m = c & ~3; m < 32; m += 4) {
+                const float4 a = lds4(at(32 + l, m));
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[s] = fma2(make_float2(av[e], av[e]), lds2(at(m + e, c)), y[s]);
+            }
+        }
+        bar_sync(2, NPREP);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) sts2(at(32 + l, 2 * (s ? 15 - w : w)), y[s].x, y[s].y);
+        bar_sync(2, NPREP);
+    }
+    {   // -X22 of that: a column a lane, two rows i: columns m <= i of X22 count
+        float y[2][2] = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int i = 2 * (s ? 15 - w : w);
+#pragma unroll 1
+            for (int m = 0; m <= i + 1; m += 4) {
+                float r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] = lds(at(32 + m + e, l));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float4 a = lds4(at(32 + i + x, 32 + m));
+                    y[s][x] = fmaf(-a.x, r[0], y[s][x]);
+                    y[s][x] = fmaf(-a.y, r[1], y[s][x]);
+                    y[s][x] = fmaf(-a.z, r[2], y[s][x]);
+                    y[s][x] = fmaf(-a.w, r[3], y[s][x]);
                 }
             }
-            bar_sync(2, 128);
-            const float s = step ? -1.f : 1.f;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sts2(at(32 + i + r, c), s * y[r][0], s * y[r][1]);
-                sts2(at(32 + i + r, c + 2), s * y[r][2], s * y[r][3]);
-            }
-            bar_sync(2, 128);
         }
+        bar_sync(2, NPREP);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) sts(at(32 + 2 * (s ? 15 - w : w) + x, l), y[s][x]);
+        bar_sync(2, NPREP);
     }
 }
 
@@ -232,28 +282,20 @@ __device__ __forceinline__ float row_square(uint32_t panel, int row) {
     return s;
 }
 
-// 16 lanes x 32 columns, as ld16x32 has them
-__device__ __forceinline__ void st16x32(uint32_t t, const float* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-        : "memory");
-}
-// Where a fragment of Y (or, vt = 0, of U) at t, of 16 channels from ch0 and 32 rows from row0, makes a place of R
+// Where a fragment of Y (or, vt = 0, of U) at t, of 16 channels from ch0 and 16 rows from row0, makes a place of R
 // that is not finite, both Y and v are cleared there, and the channel's first such row is noted.  By one warp, out of
 // line: it runs where something is wrong, if ever.
 __device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, int ch0, int row0, int len, uint32_t marks, volatile uint32_t* flag,
                                        uint32_t bit) {
-    float a[16];
-    ld16x32(t, a);
+    float a[8];
+    ld16x16(t, a);
     tmem_wait_ld();
     const int l = threadIdx.x & 31;
 #pragma unroll 1
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8; ++e) {
         const int ch = ch0 + 8 * ((e >> 1) & 1) + (l >> 2), row = row0 + 8 * (e >> 2) + 2 * (l & 3) + (e & 1);
         const uint32_t at = vt + ((ch >> 6) & 1) * 8192u + sw128(row, (ch >> 3) & 7) + 2 * (ch & 7);
-        const float r = vt ? fmaf(lds(key + 4 * row), a[e], __uint_as_float((uint32_t)lds16(at) << 16)) : a[e];
+        const float r = vt ? lds(key + 4 * row) * a[e] + __uint_as_float((uint32_t)lds16(at) << 16) : a[e];
         if (finite(r) || row >= len) continue;
         a[e] = 0.f;
         if (vt) sts16(at, 0);
@@ -261,7 +303,7 @@ __device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, in
         atomicOr(const_cast<uint32_t*>(flag), bit);
     }
     __syncwarp();
-    st16x32(t, a);
+    st16x16f(t, a);
     tmem_wait_st();
 }
 // rows of a channel's staged output that are none
@@ -272,9 +314,17 @@ __device__ __noinline__ void nan_rows(uint32_t stage, uint32_t mark, int ch, int
     sts(mark + 4 * ch, __int_as_float(C));
 }
 
+// raw gates of two tokens, `left` of them (or more) in the sequence
+__device__ __noinline__ void activate(const Gates& g, Gates::Head head, int left, float& a0, float& a1, float& b0, float& b1) {
+    a0 = left > 0 ? g.decay_of(a0, head) : 0.f;
+    a1 = left > 1 ? g.decay_of(a1, head) : 0.f;
+    b0 = left > 0 ? g.rate_of(b0) : 0.f;
+    b1 = left > 1 ? g.rate_of(b1) : 0.f;
+}
+
 __global__ void __launch_bounds__(NTHR, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ Params p) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
@@ -312,8 +362,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
-            if (i == B_S || i == B_R || i == B_UD || i == B_O2READ) count = 8;
-            if ((i >= B_F && i < B_F + 2) || (i >= B_SCREAD && i < B_SCREAD + 2) || i == B_T) count = 4;
+            if (i == B_S || i == B_R || i == B_UD || i == B_O2READ || i == B_OFREE || i == B_OFREE + 1) count = NCH / 32;
+            if ((i >= B_F && i < B_F + 2) || (i >= B_SCREAD && i < B_SCREAD + 2) || i == B_T) count = NPREP / 32;
             mbar_init(sy.bar(i), count);
         }
         fence_mbar_init();
@@ -321,10 +371,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        prefetch_tmap(&tm_o);
     }
     for (int x = tid; x < 2 * VB; x += NTHR) sts(sb + L_MARK + 4 * x, __int_as_float(C));
-    if (w == 12) tmem_alloc(sb + L_MISC + 4 * M_TMEM, TCOLS);
+    if (tid < 2 * C) sts(sb + L_RQ + 4 * tid, 1.f);  // (without norms)
+    if (w == 24) tmem_alloc(sb + L_MISC + 4 * M_TMEM, TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -334,7 +384,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (l == 0) mbar_arrive(sy.bar(bar));
     };
 
-    if (w == 12) {
+    if (w == 24) {
         // ------------------------------------------------ all products
         auto scores = [&](int c) {
             sy.wait(B_KQ + c % NKQ, (c / NKQ) & 1);
@@ -343,8 +393,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t a = lo_k(sb + L_KQ + (c % NKQ) * KQ_BYTES);
 #pragma unroll
                 for (int kk = 0; kk < KD / 16; ++kk) {
-                    const uint32_t d = (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2;
-                    umma_bf16(tmem + TSC, desc(a + d), desc(a + d), idesc_bf16(128, 64, 0, 0), kk > 0);
+                    const uint64_t d = desc(a + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2);
+                    umma_bf16(tmem + TSC, d, d, idesc_bf16(128, 64, 0, 0), kk > 0);
                 }
                 umma_commit(sy.bar(B_SC));
             }
@@ -354,13 +404,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int c = -1; c < nt; ++c) {
             const uint32_t st = sb + L_KQ + ((c + NKQ) % NKQ) * KQ_BYTES;
             if (c >= 0) {
-                if (c == p.stall_chunk) sy.slow_wait(B_NEVER, 0, 2000);
+                if (c == p.stall_chunk) Sync::slow_wait(sy.bar(B_NEVER), 0, sy.abort_flag, sy.status, 200000);
                 sy.wait(B_S, c & 1);  // S's terms; D of the last chunk has been taken
                 if (sy.stopped()) break;
                 tc_fence_after();
                 if (elect()) {
                     const uint32_t k = lo_k(st);
-#pragma unroll
+#pragma unroll 1
                     for (int t = 2; t >= 0; --t)
 #pragma unroll
                         for (int kk = 0; kk < KD / 16; ++kk)
@@ -390,18 +440,16 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mbar_arrive(sy.bar(B_VFREE + c % NV));  // (v has been read into R, the last chunk's output has been formed)
                 if (c > 0) mbar_arrive(sy.bar(B_GFREE + (c - 1) % NG));
                 const uint32_t T = lo_k(sb + L_T), lo = lo_mn(sb + L_LO);
-                bool more = false;
 #pragma unroll
-                for (int sum = 2; sum >= 0; --sum)
+                for (int kk = 0; kk < 4; ++kk)  // R's third term
+                    umma_bf16(tmem + TY, desc(lo + kk * 128), desc(T + kk * 2), idesc_bf16(128, 64, 1, 0), kk > 0);
+#pragma unroll 1
+                for (int x = 0; x < 5; ++x) {  // T's terms 2, 1, 1, 0, 0 with R's 0, 1, 0, 1, 0
+                    const uint32_t t = (0x00112u >> (4 * x)) & 15u, r = (0x01010u >> (4 * x)) & 15u;
 #pragma unroll
-                    for (int t = 0; t <= sum; ++t)  // term t of T, term sum - t of R
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t b = desc(T + t * (T_TERM >> 4) + kk * 2);
-                            if (sum - t == 2) umma_bf16(tmem + TY, desc(lo + kk * 128), b, idesc_bf16(128, 64, 1, 0), more);
-                            else umma_bf16_ta(tmem + TY, tmem + TZ + 32 * (sum - t) + 8 * kk, b, idesc_bf16(128, 64, 0, 0), more);
-                            more = true;
-                        }
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tmem + TY, tmem + TZ + 32 * r + 8 * kk, desc(T + t * (T_TERM >> 4) + kk * 2), idesc_bf16(128, 64, 0, 0), 1);
+                }
                 umma_commit(sy.bar(B_U));
             }
             __syncwarp();
@@ -411,12 +459,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (elect()) {
                 const uint32_t k = lo_kq_mn(st), lo = lo_mn(sb + L_LO), P = lo_k(sb + L_P + (c & 1) * 16384);
 #pragma unroll
-                for (int t = 2; t >= 0; --t)
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + TD, desc(lo + kk * 128), desc(k + kk * 128), idesc_bf16(128, KD, 1, 1), kk > 0);
+#pragma unroll 1
+                for (int t = 1; t >= 0; --t)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (t == 2) umma_bf16(tmem + TD, desc(lo + kk * 128), desc(k + kk * 128), idesc_bf16(128, KD, 1, 1), kk > 0);
-                        else umma_bf16_ta(tmem + TD, tmem + TZ + 32 * t + 8 * kk, desc(k + kk * 128), idesc_bf16(128, KD, 0, 1), 1);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tmem + TD, tmem + TZ + 32 * t + 8 * kk, desc(k + kk * 128), idesc_bf16(128, KD, 0, 1), 1);
                 umma_commit(sy.bar(B_D));
                 umma_commit(sy.bar(B_KQFREE + c % NKQ));
 #pragma unroll
@@ -433,7 +482,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
         }
-    } else if (w == 13) {
+    } else if (w == 25) {
         // ------------------------------------------------ loads
         int c = 0;
 #pragma unroll 1
@@ -445,13 +494,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t v = sb + L_V + (c % NV) * V_BYTES, kq = sb + L_KQ + (c % NKQ) * KQ_BYTES;
                 const uint32_t fv = sy.bar(B_V + c % NV), fkq = sy.bar(B_KQ + c % NKQ);
                 mbar_arrive_expect_tx(fkq, KQ_BYTES);
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < KD / 64; ++x) {
                     tma_load_3d(kq + x * PANEL, &tm_k, 64 * x, hq, bos + c * C, fkq);
                     tma_load_3d(kq + x * PANEL + QROWS, &tm_q, 64 * x, hq, bos + c * C, fkq);
                 }
                 mbar_arrive_expect_tx(fv, V_BYTES);
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < VB / 64; ++x) tma_load_3d(v + x * 8192, &tm_v, vc0 + 64 * x, h, bos + c * C, fv);
             }
             __syncwarp();
@@ -463,11 +512,11 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
         }
-    } else if (w == 14) {
+    } else if (w == 26) {
         // ------------------------------------------------ gates: a chunk's decays and rates, two tokens a lane
         const Gates::Head head = p.gates.head(h);
         const float scale = rsqrtf((float)p.K);
-        float ra[2], rb[2];  // as they lie in memory, asked for a chunk before they are used
+        float ra[2] = {}, rb[2] = {};  // as they lie in memory, asked for a chunk before they are used
         auto ask = [&](int c) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -476,41 +525,37 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 rb[e] = t < eos ? p.gates.raw_rate(t, h) : 0.f;
             }
         };
-        if (nt > 0) ask(0);
 #pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
+        for (int c = -1; c < nt; ++c) {
+            float a0 = ra[0], a1 = ra[1], b0 = rb[0], b1 = rb[1];
+            if (c + 1 < nt) ask(c + 1);
+            if (c < 0) continue;
             const uint32_t gt = gates(c);
             const int left = eos - (bos + c * C);
-            float a[2], b[2];
-            bool ok[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                a[e] = 2 * l + e < left ? p.gates.decay_of(ra[e], head) : 0.f;
-                b[e] = 2 * l + e < left ? p.gates.rate_of(rb[e]) : 0.f;
-            }
-            if (c + 1 < nt) ask(c + 1);
+            if (p.gates.raw || p.gates.logits) activate(p.gates, head, left - 2 * l, a0, a1, b0, b1);
             const float none = __int_as_float(0x7fffffff);
-            ok[0] = a[0] < 3e38f && finite(b[0]);
-            ok[1] = a[1] < 3e38f && finite(b[1]);
-            const int bad = first_nan(ok[0] ? 0.f : none, ok[1] ? 0.f : none);
-            int I[2], F[2];
+            const int bad = first_nan(a0 < 3e38f && finite(b0) ? 0.f : none, a1 < 3e38f && finite(b1) ? 0.f : none);
             long long G[2];
-            pair_sums(a[0], a[1], G);
-            parts(G[0], I[0], F[0]);
-            parts(G[1], I[1], F[1]);
-            const int Il = __shfl_sync(0xffffffffu, I[1], 31), Fl = __shfl_sync(0xffffffffu, F[1], 31);
-            const int Im = __shfl_sync(0xffffffffu, I[1], l | 7), Fm = __shfl_sync(0xffffffffu, F[1], l | 7);
+            pair_sums(a0, a1, G);
+            int Il, Fl, Im, Fm;
+            parts(G[1], Il, Fl);
+            Im = __shfl_sync(0xffffffffu, Il, l | 7);
+            Fm = __shfl_sync(0xffffffffu, Fl, l | 7);
+            Il = __shfl_sync(0xffffffffu, Il, 31);
+            Fl = __shfl_sync(0xffffffffu, Fl, 31);
             if (c >= NG) sy.wait(B_GFREE + c % NG, (c / NG - 1) & 1);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * l + e;
-                sts2(gt + GT_G + 8 * i, (float)I[e], (float)F[e] * (1.f / 16777216.f));
-                const float r = pow2(I[e], F[e]);
+#pragma unroll 1
+            for (int i = 2 * l; i < 2 * l + 2; ++i) {
+                int I, F;
+                parts(i & 1 ? G[1] : G[0], I, F);
+                sts(gt + GT_G + 4 * i, -(float)I);
+                sts(gt + GT_G + 256 + 4 * i, (float)F * (-1.f / 16777216.f));
+                const float r = pow2(I, F);
                 sts(gt + GT_ROW + 4 * i, scale * r);
                 sts(gt + GT_KEY + 4 * i, -r);
-                sts(gt + GT_UPD + 4 * i, i < bad ? pow2(Il - I[e], Fl - F[e]) : 0.f);
-                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I[e], Fm - F[e]));
-                sts(gt + GT_BETA + 4 * i, i < bad ? b[e] : 0.f);
+                sts(gt + GT_UPD + 4 * i, i < bad ? pow2(Il - I, Fl - F) : 0.f);
+                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I, Fm - F));
+                sts(gt + GT_BETA + 4 * i, i < bad ? (i & 1 ? b1 : b0) : 0.f);
             }
             if (l == 0) {
                 sts(gt + GT_LAST, pow2(Il, Fl));
@@ -518,39 +563,44 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             arrive(B_G + c % NG);
         }
-    } else if (w < 8) {
+    } else if (w < 16) {
         // ------------------------------------------------ the chain: R, U' and S, value channels on lanes; the output
-        const int qd = w & 3, half = w >> 2;
-        const uint32_t lane = (uint32_t)(32 * qd) << 16;
+        // A warp has 32 key channels of 32 lanes of S, and of the chunk's matrices 16 lanes x 32 rows.
+        const int qd = w & 3, part = w >> 2, y16 = 16 * (part & 1), row0 = 32 * (part >> 1);
+        const uint32_t lane = (uint32_t)(32 * qd) << 16, lane16 = lane + ((uint32_t)y16 << 16);
         const int vl = 32 * qd + l;
         const bool mine = vc0 + vl < p.V;
-        const int rows = min(64, p.K - 64 * half);  // of this warp's 64 key channels
-        float S[64];
+        const int rows = p.K - 32 * part;  // of this warp's key channels
+        float S[32];
         {
-            const float* from = p.h0 + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(64 * half) * p.V + vc0 + vl;
+            const float* from = p.h0 + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(32 * part) * p.V + vc0 + vl;
 #pragma unroll
-            for (int j = 0; j < 64; ++j, from += p.V) S[j] = p.h0 && mine && j < rows ? *from : 0.f;
+            for (int j = 0; j < 32; ++j, from += p.V) S[j] = p.h0 && mine && j < rows ? *from : 0.f;
         }
         // a lane's row of the four 8 x 8 blocks of a fragment load: channels + 0, + 8, rows + 0, + 8
-        const int lrow = 32 * half + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + ((l >> 3) & 1);
-        const uint32_t lo = sb + L_LO + (qd >> 1) * 8192u;
-        const uint32_t zcol = tmem + TZ + lane + 16 * half, ycol = tmem + TY + lane + 32 * half;
-        const int pair = 4 * (32 * half + 2 * (l & 3));  // byte offset of a lane's first two rows' factors
-        // the terms of sixteen channels' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
-        auto write_fragments = [&](int y, float2 (&x)[8]) {
-            uint32_t r[8];
+        const int lrow = row0 + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + (y16 >> 3) + ((l >> 3) & 1);
+        const uint32_t panel = (qd >> 1) * 8192u, lo = sb + L_LO + panel;
+        const int pair = 4 * (row0 + 2 * (l & 3));  // byte offset of a lane's first two rows' factors
+        // the terms of sixteen rows' fragments from `r` on (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
+        auto write_fragments = [&](int r, float2 (&x)[4]) {
+            uint32_t t[4];
+            const uint32_t at = tmem + TZ + lane16 + (row0 + r) / 2;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = round2(x[e]);
-            st16x16(zcol + ((uint32_t)(16 * y) << 16), r);
+            for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
+            st16x8(at, t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = round2(x[e]);
-            st16x16(zcol + ((uint32_t)(16 * y) << 16) + 32, r);
+            for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
+            st16x8(at + 32, t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = top2(x[e]);
-#pragma unroll
-            for (int g = 0; g < 4; g += 2) stmatrix4_t(lo + sw128(lrow + 8 * g, lpiece + 2 * y), r + 2 * g);
+            for (int e = 0; e < 4; ++e) t[e] = top2(x[e]);
+            stmatrix4_t(lo + sw128(lrow + r, lpiece), t);
         };
         auto marked = [&](int c) { return ((misc[M_ODD] >> (c & 1)) & 1u) != 0u; };
+        // One warp polls, the others wait at a named barrier: polls take issue slots from the warps that work.
+        auto together = [&] {
+            bar_sync(1, NCH);
+            tc_fence_after();
+        };
         const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0;; ++c) {
@@ -559,319 +609,314 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (c > 0) {
                 last = lds(gates(c - 1) + GT_LAST);
                 if (marked(c - 1)) last += nan_if(__float_as_int(lds(sb + L_MARK + 512 * ((c - 1) & 1) + 4 * vl)) < C);
-                sy.wait(B_D, (c - 1) & 1);
-                tc_fence_after();
+                if (w == 0) sy.wait(B_D, (c - 1) & 1);
+                together();
             }
 #pragma unroll
-            for (int x = 0; x < 64; x += 16) {
+            for (int x = 0; x < 32; x += 8) {
                 if (c > 0) {
-                    float d[16];
-                    tmem_ld16(tmem + TD + lane + 64 * half + x, d);
+                    float d[8];
+                    tmem_ld8(tmem + TD + lane + 32 * part + x, d);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
+                    for (int j = 0; j < 8; j += 2) {
                         const float2 s = fma2(make_float2(last, last), make_float2(S[x + j], S[x + j + 1]), make_float2(d[j], d[j + 1]));
                         S[x + j] = s.x;
                         S[x + j + 1] = s.y;
                     }
                 }
-                uint32_t t0[8], t1[8], t2[8];
+                uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     float2 y = make_float2(S[x + 2 * j], S[x + 2 * j + 1]);
                     t0[j] = round2(y);
                     t1[j] = round2(y);
                     t2[j] = top2(y);
                 }
-                const uint32_t at = tmem + TS + lane + 32 * half + x / 2;
-                tmem_st8(at, t0);
-                tmem_st8(at + 64, t1);
-                tmem_st8(at + 128, t2);
+                const uint32_t at = tmem + TS + lane + 16 * part + x / 2;
+                tmem_st4(at, t0);
+                tmem_st4(at + 64, t1);
+                tmem_st4(at + 128, t2);
             }
             tmem_wait_st();
             tc_fence_before();
             arrive(B_S);
             if (c > 0) {
-                // ---- chunk c - 1's output, through P's place
+                // ---- chunk c - 1's output, through the warp's own part of P's place
                 const int b = (c - 1) & 1, t0 = bos + (c - 1) * C, n_rows = min(C, eos - t0);
                 const uint32_t rq = sb + L_RQ + 256 * b, stage = sb + L_P + b * 16384;
                 const int len = __float_as_int(lds(gates(c - 1) + GT_LEN));
-                sy.wait(B_O2, b);
-                tc_fence_after();
-#pragma unroll 1
-                for (int y = 0; y < 2; ++y) {
-                    float o[16];
-                    ld16x32(tmem + TSC + lane + ((uint32_t)(16 * y) << 16) + 32 * half, o);
-                    tmem_wait_ld();
-                    uint32_t r[8];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float2 m = lds2(rq + pair + 32 * g);
-                        const float2 y0 = mul2(m, make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m, make_float2(o[4 * g + 2], o[4 * g + 3]));
-                        r[2 * g] = pack_bf16(y0.x, y0.y);
-                        r[2 * g + 1] = pack_bf16(y1.x, y1.y);
-                    }
-#pragma unroll
-                    for (int g = 0; g < 4; g += 2) stmatrix4_t(stage + (qd >> 1) * 8192u + sw128(lrow + 8 * g, lpiece + 2 * y), r + 2 * g);
-                }
+                if (w == 0) sy.wait(B_O2, b);
+                together();
+                float o[16];
+                ld16x32(tmem + TSC + lane16 + row0, o);
+                tmem_wait_ld();
                 tc_fence_before();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float2 m = lds2(rq + pair + 32 * g);
+                    const float2 y0 = mul2(m, make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m, make_float2(o[4 * g + 2], o[4 * g + 3]));
+                    o[4 * g] = __uint_as_float(pack_bf16(y0.x, y0.y));
+                    o[4 * g + 1] = __uint_as_float(pack_bf16(y1.x, y1.y));
+                }
                 arrive(B_O2READ);
+#pragma unroll
+                for (int g = 0; g < 4; g += 2) {
+                    const uint32_t r[4] = {__float_as_uint(o[4 * g]), __float_as_uint(o[4 * g + 1]), __float_as_uint(o[4 * g + 4]), __float_as_uint(o[4 * g + 5])};
+                    stmatrix4_t(stage + panel + sw128(lrow + 8 * g, lpiece), r);
+                }
                 const bool odd = len < n_rows || marked(c - 1);
                 if (odd) {
-                    bar_sync(1, 256);  // (a channel's rows are two warps')
-                    if (half == 0) nan_rows(stage, sb + L_MARK + 512 * b, vl, len, n_rows);
+                    bar_sync(1, NCH);  // (a channel's rows are two warps')
+                    if (w < 4) nan_rows(stage, sb + L_MARK + 512 * b, vl, len, n_rows);
+                    bar_sync(1, NCH);
+                    if (tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << b));
                 }
-                fence_proxy_async_smem();
-                bar_sync(1, 256);
-                if (odd && tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << b));
-                if (!sy.stopped()) {
-                    if (n_rows == C) {
-                        if (tid == 0) {
+                __syncwarp();
+                // the warp's 16 channels x 32 rows: 32 bytes a row, sixteen rows at once
+                const int r0 = row0 + (l >> 1), ch = 32 * qd + y16 + 8 * (l & 1);
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(t0 + r0) * p.H + h) * p.V + vc0 + ch;
+                const bool in = vc0 + ch < p.V && !sy.aborted();
 #pragma unroll
-                            for (int x = 0; x < VB / 64; ++x)
-                                if (vc0 + 64 * x < p.V) tma_store_3d(&tm_o, stage + x * 8192, vc0 + 64 * x, h, t0);
-                            bulk_commit();
-                        }
-                    } else {  // the sequence's last rows
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)t0 * p.H + h) * p.V + vc0;
-#pragma unroll 1
-                        for (int x = tid; x < n_rows * (VB / 8); x += 256) {
-                            const int row = x / (VB / 8), ch = x % (VB / 8);
-                            uint32_t v[4];
-                            ld_s128(stage + (ch >> 3) * 8192u + sw128(row, ch & 7), v);
-                            if (vc0 + 8 * ch < p.V) *reinterpret_cast<uint4*>(dst + (size_t)row * p.H * p.V + 8 * ch) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t v[4];
+                    ld_s128(stage + panel + sw128(r0 + 16 * x, (ch & 63) >> 3), v);
+                    if (in && r0 + 16 * x < n_rows) *reinterpret_cast<uint4*>(dst + (size_t)(16 * x) * p.H * p.V) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
+                arrive(B_OFREE + b);
             }
             if (c == nt) break;
             // ---- R
             const uint32_t gt = gates(c), vt = sb + L_V + (c % NV) * V_BYTES;
-            sy.wait(B_F + (c & 1), (c >> 1) & 1);
-            sy.wait(B_V + c % NV, (c / NV) & 1);
+            if (w == 0) {
+                sy.wait(B_F + (c & 1), (c >> 1) & 1);
+                sy.wait(B_V + c % NV, (c / NV) & 1);
+                sy.wait(B_Y, c & 1);
+            }
+            together();
             const int len = __float_as_int(lds(gt + GT_LEN));
-            sy.wait(B_Y, c & 1);
-            tc_fence_after();
             if (len < C) {  // rows that do not count, for D
                 const uint32_t kt = sb + L_KQ + (c % NKQ) * KQ_BYTES;
 #pragma unroll 1
-                for (int x = tid; x < C * (KD / 8); x += 256)
+                for (int x = tid; x < C * (KD / 8); x += NCH)
                     if ((x & 63) >= len) st_s128(kt + (x >> 9) * PANEL + sw128(x & 63, (x >> 6) & 7), 0, 0, 0, 0);
             }
 #pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-                float2 x[8];
-                const uint32_t at = ycol + ((uint32_t)(16 * y) << 16);
+            for (int r = 0; r < 32; r += 16) {
+                float2 x[4];
+                const uint32_t at = tmem + TY + lane16 + row0 + r;
 #pragma unroll 1
                 for (int again = 0; again < 2; ++again) {
-                    float a[16];
+                    float a[8];
                     float2 odd = zero;
-                    uint32_t r[8];
-                    ld16x32(at, a);
-                    ldmatrix4_t(vt + (qd >> 1) * 8192u + sw128(lrow, lpiece + 2 * y), r);
-                    ldmatrix4_t(vt + (qd >> 1) * 8192u + sw128(lrow + 16, lpiece + 2 * y), r + 4);
+                    uint32_t v[4];
+                    ld16x16(at, a);
+                    ldmatrix4_t(vt + panel + sw128(lrow + r, lpiece), v);
+                    const float2 f[2] = {lds2(gt + GT_KEY + pair + 4 * r), lds2(gt + GT_KEY + pair + 4 * r + 32)};
                     tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float2 f = lds2(gt + GT_KEY + pair + 32 * g);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = 2 * g + e;
-                            x[i] = fma2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]), make_float2(bf_lo(r[i]), bf_hi(r[i])));
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) x[e] = add_bf16(v[e], mul2(f[e >> 1], make_float2(a[2 * e], a[2 * e + 1])));
                     if (len < C) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int j = 32 * half + 8 * (e >> 1) + 2 * (l & 3);
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = row0 + r + 8 * (e >> 1) + 2 * (l & 3);
                             if (j >= len) x[e].x = 0.f;
                             if (j + 1 >= len) x[e].y = 0.f;
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) odd = fma2(x[e], zero, odd);
+                    for (int e = 0; e < 4; ++e) odd = fma2(x[e], zero, odd);
                     if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
-                    clear_odd(at, vt, gt + GT_KEY, 32 * qd + 16 * y, 32 * half, len, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
+                    clear_odd(at, vt, gt + GT_KEY, 32 * qd + y16, row0 + r, len, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
                 }
-                write_fragments(y, x);
+                write_fragments(r, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_R);
-            if (c > 0 && tid == 0) {  // the staged output has left
-                bulk_wait_read();
-                mbar_arrive(sy.bar(B_OFREE + ((c - 1) & 1)));
-            }
-            __syncwarp();
             // ---- O1 with its rows' factors, where O2 will be added to it
-            if (c == 0) sy.wait(B_SCREAD, 0);
-            if (c + 1 < nt) sy.wait(B_SCREAD + ((c + 1) & 1), ((c + 1) >> 1) & 1);
-            sy.wait(B_O1, c & 1);
-            tc_fence_after();
+            if (w == 0) {
+                if (c == 0) sy.wait(B_SCREAD, 0);
+                if (c + 1 < nt) sy.wait(B_SCREAD + ((c + 1) & 1), ((c + 1) >> 1) & 1);
+                sy.wait(B_O1, c & 1);
+            }
+            together();
 #pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-                float o[16];
-                const uint32_t at = tmem + lane + ((uint32_t)(16 * y) << 16) + 32 * half;
-                ld16x32(at + TO1, o);
+            for (int r = 0; r < 32; r += 16) {
+                float o[8];
+                ld16x16(tmem + TO1 + lane16 + row0 + r, o);
+                const float2 f[2] = {lds2(gt + GT_ROW + pair + 4 * r), lds2(gt + GT_ROW + pair + 4 * r + 32)};
                 tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_ROW + pair + 32 * g);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 s = mul2(f, make_float2(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]));
-                        o[4 * g + 2 * e] = s.x;
-                        o[4 * g + 2 * e + 1] = s.y;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 s = mul2(f[e >> 1], make_float2(o[2 * e], o[2 * e + 1]));
+                    o[2 * e] = s.x;
+                    o[2 * e + 1] = s.y;
                 }
-                st16x32(at + TSC, o);
+                st16x16f(tmem + TSC + lane16 + row0 + r, o);
             }
             // ---- U'
-            sy.wait(B_U, c & 1);
-            tc_fence_after();
+            if (w == 0) sy.wait(B_U, c & 1);
+            together();
 #pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-                float a[16];
-                float2 x[8], odd = zero;
-                const uint32_t at = ycol + ((uint32_t)(16 * y) << 16);
-                ld16x32(at, a);
+            for (int r = 0; r < 32; r += 16) {
+                float a[8];
+                float2 x[4], odd = zero;
+                const uint32_t at = tmem + TY + lane16 + row0 + r;
+                ld16x16(at, a);
+                const float2 f[2] = {lds2(gt + GT_UPD + pair + 4 * r), lds2(gt + GT_UPD + pair + 4 * r + 32)};
                 tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_UPD + pair + 32 * g);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 u = make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]);
-                        odd = fma2(u, zero, odd);
-                        x[2 * g + e] = mul2(f, u);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = make_float2(a[2 * e], a[2 * e + 1]);
+                    odd = fma2(u, zero, odd);
+                    x[e] = mul2(f[e >> 1], u);
                 }
                 // (U itself is O2's operand)
                 if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f))
-                    clear_odd(at, 0, 0, 32 * qd + 16 * y, 32 * half, C, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
-                write_fragments(y, x);
+                    clear_odd(at, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
+                write_fragments(r, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_UD);
         }
-        if (tid == 0) bulk_wait();
         if (p.hT && mine && !sy.aborted()) {
-            float* to = p.hT + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(64 * half) * p.V + vc0 + vl;
+            float* to = p.hT + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(32 * part) * p.V + vc0 + vl;
 #pragma unroll
-            for (int j = 0; j < 64; ++j, to += p.V)
+            for (int j = 0; j < 32; ++j, to += p.V)
                 if (j < rows) *to = S[j];
         }
-    } else if (w < 12) {
+    } else {
         // ------------------------------------------------ preparation: T and P of a chunk
-        const int t = tid - 256, i = t & 63;
-        const bool query = t >= 64, hi = (t & 32) != 0;
-        const uint32_t sc = tmem + TSC + ((uint32_t)(32 * (w & 3)) << 16), X = sb + L_X;
+        // A warp has 32 rows of the scores, of keys or of queries, and 32 of their columns.
+        const int t = tid - NCH, i = 32 * (w & 1) + l, c0 = 32 * ((w - 16) >> 2);
+        const bool query = (w & 2) != 0, hi = (w & 1) != 0;
+        const uint32_t sc = tmem + TSC + ((uint32_t)(32 * (w & 3)) << 16) + c0, X = sb + L_X;
         const float scale = rsqrtf((float)p.K);
         const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0, knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
+        if (!hi && c0 > 0 && !query)  // the block right of the diagonal stays zero
+#pragma unroll 1
+            for (int j = 0; j < 32; j += 4) st_s128(X + 4 * (LDX * i + c0 + j), 0, 0, 0, 0);
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
-            const uint32_t gt = gates(c);
-            sy.wait(B_G + c % NG, (c / NG) & 1);
-            sy.wait(B_SC, c & 1);
+            const uint32_t gt = gates(c), P = sb + L_P + (c & 1) * 16384 + (c0 >> 5) * 8192;
+            if (w == 16) {
+                sy.wait(B_G + c % NG, (c / NG) & 1);
+                if (c >= 2) sy.wait(B_OFREE + (c & 1), ((c - 2) >> 1) & 1);  // P's place
+                sy.wait(B_SC, c & 1);
+            }
+            bar_sync(2, NPREP);
             tc_fence_after();
-            // keys that are not finite (their square), and the rows' norms
-            if (!query) {
-                float x[32], kk = 0.f;
-                ld32(sc + (hi ? 32 : 0), x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) kk = j == l ? x[j] : kk;
-                const unsigned odd = __ballot_sync(0xffffffffu, !finite(kk) && i < __float_as_int(lds(gt + GT_LEN)));
-                if (l == 0) misc[M_BAD0 + (hi ? 1 : 0)] = odd ? (hi ? 32 : 0) + __ffs(odd) - 1 : C;
-                sts(X + 4 * (LDX * i + 64), knorm && finite(kk) ? rsqrtf(kk + kQNormEps) : 1.f);
-            } else {
-                float s = 0.f;
-                if (qnorm) {
-                    const uint32_t q = sb + L_KQ + (c % NKQ) * KQ_BYTES + QROWS;
-#pragma unroll 1
-                    for (int x = 0; x < KD / 64; ++x) s += row_square(q + x * PANEL, i);
+            const float gi = -lds(gt + GT_G + 4 * i), gf = -lds(gt + GT_G + 256 + 4 * i);
+            float rk = 1.f;
+            if (qnorm || knorm) {  // the rows' norms, half a row a thread
+                const uint32_t row = sb + L_KQ + (c % NKQ) * KQ_BYTES + (query ? QROWS : 0) + (c0 >> 5) * PANEL;
+                const bool on = query ? qnorm : knorm;
+                const float n2 = on ? row_square(row, i) : 0.f;
+                if (c0 > 0) sts(X + 4 * (LDX * i + (query ? 66 : 65)), n2);
+                bar_sync(2, NPREP);
+                if (c0 == 0) {
+                    const float sum = n2 + lds(X + 4 * (LDX * i + (query ? 66 : 65)));
+                    sts(query ? sb + L_RQ + 256 * (c & 1) + 4 * i : X + 4 * (LDX * i + 64),
+                        on && (query || finite(sum)) ? rsqrtf(sum + kQNormEps) : 1.f);
                 }
-                sts(sb + L_RQ + 256 * (c & 1) + 4 * i, qnorm ? rsqrtf(s + kQNormEps) : 1.f);
+                bar_sync(2, NPREP);
+                rk = lds(X + 4 * (LDX * i + 64));
+                if (knorm && !query && c0 == 0) {  // a key's norm is a factor of its column, too
+                    sts(gt + GT_G + 256 + 4 * i, log2f(rk) - gf);
+                    sts(gt + GT_COL + 4 * i, lds(gt + GT_COL + 4 * i) * rk / lds(X + 4 * (LDX * (i | 15) + 64)));
+                }
+                bar_sync(2, NPREP);
             }
-            bar_sync(2, 128);
-            const int full = __float_as_int(lds(gt + GT_LEN)), len = min(full, (int)min(misc[M_BAD0], misc[M_BAD1]));
-            const float rk = lds(X + 4 * (LDX * i + 64));
-            bar_sync(2, 128);
-            if (!query) {
-                if (knorm || len < full) {
-                    sts(gt + GT_KEY + 4 * i, rk * lds(gt + GT_KEY + 4 * i));
-                    sts(gt + GT_UPD + 4 * i, i < len ? rk * lds(gt + GT_UPD + 4 * i) : 0.f);
-                    if (i >= len) sts(gt + GT_BETA + 4 * i, 0.f);
-                }
-                if (i == 0) {
-                    sts(gt + GT_LEN, __int_as_float(len));
-                    if (len < min(C, eos - (bos + c * C))) sts(gt + GT_LAST, __int_as_float(0x7fffffff));
-                }
-            }
-            arrive(B_F + (c & 1));
-            if (c >= 2) sy.wait(B_OFREE + (c & 1), ((c - 2) >> 1) & 1);  // P's place
+            const int full = __float_as_int(lds(gt + GT_LEN));
             // A's rows (lanes with keys) into X, P's rows (with queries) as a tf32 operand: the score times
             // f 2^(G_i - G_j), 0 where j > last.  Left of the row's 32 the factor parts into the row's and the column's,
             // both <= 1; within them each is formed by itself.
-            const int last = i < len ? i - (query ? 0 : 1) : -1;
-            const float f = query ? scale : lds(gt + GT_BETA + 4 * i) * rk;
-            const float2 gi = lds2(gt + GT_G + 8 * i);
+            const int last = i < full ? i - (query ? 0 : 1) : -1;
+            const float f = last < 0 ? 0.f : query ? scale : lds(gt + GT_BETA + 4 * i) * rk;
+            float2 odd = make_float2(0.f, 0.f);
+            if (hi || c0 == 0) {
 #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {  // eight columns each
-                float x[8];
-                if (b < (hi ? 8 : 4)) {
-                    tmem_ld8(sc + 8 * b, x);
+                for (int b = c0; b < c0 + 32; b += 16) {
+                    float x[16];
+                    tmem_ld16(sc + b - c0, x);
                     tmem_wait_ld();
-                    if (hi && b < 4) {
-                        const float r = last < 0 ? 0.f : f * power(gi, lds2(gt + GT_G + 8 * (8 * b | 15)));
+                    if (hi && c0 == 0) {  // (with the key's norm of the column b + 15, which the others' are given by)
+                        const float r = f * ex2_fast((gi + lds(gt + GT_G + 4 * (b + 15))) + (gf + lds(gt + GT_G + 256 + 4 * (b + 15))));
 #pragma unroll
-                        for (int j = 0; j < 8; j += 4) {
-                            const float4 m = lds4(gt + GT_COL + 4 * (8 * b + j));
-                            x[j] = last < 0 ? 0.f : x[j] * (r * m.x);
-                            x[j + 1] = last < 0 ? 0.f : x[j + 1] * (r * m.y);
-                            x[j + 2] = last < 0 ? 0.f : x[j + 2] * (r * m.z);
-                            x[j + 3] = last < 0 ? 0.f : x[j + 3] * (r * m.w);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 m = lds4(gt + GT_COL + 4 * (b + j));
+                            const float2 y0 = mul2(make_float2(x[j], x[j + 1]), mul2(make_float2(r, r), make_float2(m.x, m.y)));
+                            const float2 y1 = mul2(make_float2(x[j + 2], x[j + 3]), mul2(make_float2(r, r), make_float2(m.z, m.w)));
+                            x[j] = last < 0 ? 0.f : y0.x;
+                            x[j + 1] = last < 0 ? 0.f : y0.y;
+                            x[j + 2] = last < 0 ? 0.f : y1.x;
+                            x[j + 3] = last < 0 ? 0.f : y1.y;
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float4 g = lds4(gt + GT_G + 8 * (8 * b + j));
-                            x[j] = 8 * b + j <= last ? x[j] * f * power(gi, make_float2(g.x, g.y)) : 0.f;
-                            x[j + 1] = 8 * b + j + 1 <= last ? x[j + 1] * f * power(gi, make_float2(g.z, g.w)) : 0.f;
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 gj = lds4(gt + GT_G + 4 * (b + j)), fj = lds4(gt + GT_G + 256 + 4 * (b + j));
+                            const float2 e0 = add2(add2(make_float2(gi, gi), make_float2(gj.x, gj.y)), add2(make_float2(gf, gf), make_float2(fj.x, fj.y)));
+                            const float2 e1 = add2(add2(make_float2(gi, gi), make_float2(gj.z, gj.w)), add2(make_float2(gf, gf), make_float2(fj.z, fj.w)));
+                            const float2 y0 = mul2(mul2(make_float2(f, f), make_float2(x[j], x[j + 1])), make_float2(ex2_fast(e0.x), ex2_fast(e0.y)));
+                            const float2 y1 = mul2(mul2(make_float2(f, f), make_float2(x[j + 2], x[j + 3])), make_float2(ex2_fast(e1.x), ex2_fast(e1.y)));
+                            x[j] = b + j <= last ? y0.x : 0.f;
+                            x[j + 1] = b + j + 1 <= last ? y0.y : 0.f;
+                            x[j + 2] = b + j + 2 <= last ? y1.x : 0.f;
+                            x[j + 3] = b + j + 3 <= last ? y1.y : 0.f;
                         }
                     }
-                    if (knorm)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] *= lds(X + 4 * (LDX * (8 * b + j) + 64));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = 0.f;
+                    for (int j = 0; j < 16; j += 4) {
+                        if (query) {
+                            st_s128(P + sw128(i, (b - c0 + j) / 4), to_tf32(x[j]), to_tf32(x[j + 1]), to_tf32(x[j + 2]), to_tf32(x[j + 3]));
+                        } else {
+                            st_s128(X + 4 * (LDX * i + b + j), __float_as_uint(x[j]), __float_as_uint(x[j + 1]), __float_as_uint(x[j + 2]), __float_as_uint(x[j + 3]));
+                            odd = fma2(make_float2(x[j], x[j + 1]), make_float2(0.f, 0.f), odd);
+                            odd = fma2(make_float2(x[j + 2], x[j + 3]), make_float2(0.f, 0.f), odd);
+                        }
+                    }
                 }
-                const uint32_t to = query ? sb + L_P + (c & 1) * 16384 + (b >> 2) * 8192 : X + 4 * (LDX * i + 8 * b);
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = query ? to_tf32(x[j + e]) : __float_as_uint(x[j + e]);
-                    st_s128(query ? to + sw128(i, 2 * (b & 3) + j / 4) : to + 4 * j, v[0], v[1], v[2], v[3]);
-                }
+            } else if (query) {  // (the staged output was there)
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) st_s128(P + sw128(i, j), 0, 0, 0, 0);
             }
             tc_fence_before();
             arrive(B_SCREAD + (c & 1));
-            bar_sync(2, 128);
-            invert(X, t);
-            // T's terms: a row and 32 columns a thread
-            if (c > 0) sy.wait(B_U, (c - 1) & 1);  // their last reader
-            const int r = t >> 1, c0 = 32 * (t & 1);
+            // a row of A that is not finite: its key is not, or one before it
+            const unsigned none = __ballot_sync(0xffffffffu, !query && (odd.x != 0.f || odd.y != 0.f));
+            if (!query && l == 0) misc[M_BAD + 2 * (w & 1) + (c0 >> 5)] = none ? 32 * (w & 1) + __ffs(none) - 1 : C;
+            bar_sync(2, NPREP);
+            const int len = min(min(full, (int)min(misc[M_BAD], misc[M_BAD + 1])), (int)min(misc[M_BAD + 2], misc[M_BAD + 3]));
+            if (!query && c0 == 0 && (knorm || len < full)) {
+                sts(gt + GT_KEY + 4 * i, rk * lds(gt + GT_KEY + 4 * i));
+                sts(gt + GT_UPD + 4 * i, i < len ? rk * lds(gt + GT_UPD + 4 * i) : 0.f);
+                if (i >= len) {  // rows that do not count
+                    sts(gt + GT_BETA + 4 * i, 0.f);
 #pragma unroll 1
-            for (int x = 0; x < 32; x += 8) {
+                    for (int j = 0; j < i; ++j) sts(X + 4 * (LDX * i + j), 0.f);
+                }
+            }
+            if (t == 0) {
+                sts(gt + GT_LEN, __int_as_float(len));
+                if (len < min(C, eos - (bos + c * C))) sts(gt + GT_LAST, __int_as_float(0x7fffffff));
+            }
+            arrive(B_F + (c & 1));
+            if (len < full) bar_sync(2, NPREP);
+            invert(X, t);
+            // T's terms: a row and 16 columns a thread
+            if (c > 0) sy.wait(B_U, (c - 1) & 1);  // their last reader
+            const int r = t >> 2, cc = 16 * (t & 3);
+#pragma unroll 1
+            for (int x = cc; x < cc + 16; x += 8) {
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 y = lds4(X + 4 * (LDX * r + c0 + x + 4 * e)), m = lds4(gt + GT_BETA + 4 * (c0 + x + 4 * e));
+                    const float4 y = lds4(X + 4 * (LDX * r + x + 4 * e)), m = lds4(gt + GT_BETA + 4 * (x + 4 * e));
                     float2 y0 = mul2(make_float2(y.x, y.y), make_float2(m.x, m.y)), y1 = mul2(make_float2(y.z, y.w), make_float2(m.z, m.w));
                     t0[2 * e] = round2(y0);
                     t0[2 * e + 1] = round2(y1);
@@ -880,19 +925,18 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     t2[2 * e] = top2(y0);
                     t2[2 * e + 1] = top2(y1);
                 }
-                const uint32_t at = sb + L_T + sw128(r, (c0 + x) / 8);
+                const uint32_t at = sb + L_T + sw128(r, x / 8);
                 st_s128(at, t0[0], t0[1], t0[2], t0[3]);
                 st_s128(at + T_TERM, t1[0], t1[1], t1[2], t1[3]);
                 st_s128(at + 2 * T_TERM, t2[0], t2[1], t2[2], t2[3]);
             }
             fence_proxy_async_smem();
             arrive(B_T);
-            bar_sync(2, 128);  // (X has been read)
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (w == 12) {
+    if (w == 24) {
         tc_fence_after();
         tmem_dealloc(tmem, TCOLS);
     }
@@ -906,20 +950,19 @@ bool delta_tensor_dims(bool bf16, int K, int V) { return bf16 && K % 8 == 0 && K
 
 cudaError_t launch_delta_tensor(const DeltaArgs& a) {
     using namespace delta;
-    CUtensorMap m[4];  // q, k, v, o
+    CUtensorMap m[3];  // q, k, v
     const long tokens = (long)a.B * a.T;
     if (tokens == 0 && !a.hT) return cudaSuccess;
     const void* some = a.hT;  // nothing to load: the maps are never used
     if (!make_map(m, tokens ? a.q : some, tokens ? tokens : 1, a.Hk, a.K) ||
         !make_map(m + 1, tokens ? a.k : some, tokens ? tokens : 1, a.Hk, a.K) ||
-        !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V) ||
-        !make_map(m + 3, tokens ? a.o : some, tokens ? tokens : 1, a.H, a.V))
+        !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
         return cudaErrorInvalidValue;
     const int vblocks = (a.V + VB - 1) / VB;
     const Params p{Gates(a), a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, a.flags, a.status, hook_stall_chunk()};
     const cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<<<dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], m[3], p);
+    delta_chunk_kernel<<<dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], p);
     return cudaGetLastError();
 }
 
