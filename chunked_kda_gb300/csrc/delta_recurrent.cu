@@ -5,189 +5,302 @@
 // the rule's decay, correction and read-out with the new state's read-out written out, so that one pass over
 // the old state gives both products.
 //
-// One program per (sequence, head, block of BV value columns) holds its K x BV block of S in registers.
-// Warp w owns rows [w KP/8, (w+1) KP/8) (KP = K rounded up to 64, 128 or 256, rows beyond K masked), lane l owns
-// BV/32 consecutive columns, so a state row moves as whole vectors.  A warp's rows are consecutive key
-// channels: their q and k elements are the same for all its lanes and come as 16-byte loads, without shared
-// memory.  S^T k and S^T q (and |q|^2, |k|^2, q . k) are summed over a warp's rows in registers, then across the
-// warps through shared memory, two buffers by token parity, so that one barrier a token is enough.
+// Memory bounds it: the state goes in and out once.  Two kernels:
 //
-// Memory bounds it: the state goes in and out once.
+// Rows of whole vectors (V a multiple of 4): a block of 256 threads has a (sequence, head) and all rows of up to 128
+// value columns in shared memory, which bulk copies bring and take away: 64 KB a block, three blocks an SM, so that
+// 192 KB are under way without a register.  A thread has four columns and every (1024 / columns)-th row; the products
+// are joined through shared memory.  (The state in registers, with the rows split over eight warps whose sums meet at a
+// barrier before the first store: 377 us for 512 sequences of one token, 32 heads of 128 x 128; without the barrier, a
+// warp with 16 columns of all rows: 424, its rows' pieces of 64 bytes are too short.)
+//
+// Anything else: a warp has a block of columns with all rows in registers, RG groups of lanes with 16 rows each (K
+// rounded up to 16 RG: 64, 128 or 256, rows and columns beyond K and V masked), joined by shuffles.
 #include "common.cuh"
 #include "delta_gates.cuh"
 #include "kda_internal.h"
+#include "sm100.cuh"
 
 namespace kda {
 namespace delta {
 namespace {
 
-template <int N>
-__device__ __forceinline__ void ld_state(const float* p, float* r) {
-    if constexpr (N == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
-    } else {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        r[0] = x.x; r[1] = x.y;
-    }
-}
-template <int N>
-__device__ __forceinline__ void st_state(float* p, const float* r) {
-    if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]);
-    else *reinterpret_cast<float2*>(p) = make_float2(r[0], r[1]);
-}
-// 8 consecutive elements from a 16-byte aligned address
-__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float* r) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        r[2 * e] = __uint_as_float(w[e] << 16);
-        r[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ void ld8(const float* p, float* r) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+using namespace sm100;
+
+__device__ unsigned int g_token_timeouts = 0;
+
+// bytes of shared memory behind which a bulk copy takes them to global memory (16-byte aligned, a multiple of 16)
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
-// MASKED = false when K == KP and BV divides V: no row or column checks.
-template <typename InT, typename OutT, int KP, int BV, bool MASKED>
+constexpr int NT = 256, kTile = 16384;  // floats of a block's state
+constexpr int kPart = 4 * NT;           // partial S^T k, then S^T q, a row of a block's columns for each group of threads
+
+template <typename InT, typename OutT>
+__global__ void __launch_bounds__(NT, 3) delta_token_kernel(
+    const InT* __restrict__ q, const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags,
+    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, int* status, OutT* o) {
+    extern __shared__ __align__(128) float sm[];  // [K][BV] the state, then the partial products
+    __shared__ float s_q[256], s_k[256], s_dot[3][8];
+    __shared__ __align__(8) uint64_t s_bar;
+    float* part = sm + kTile;
+    const int tid = threadIdx.x, v0 = blockIdx.x * BV, h = blockIdx.y, n = blockIdx.z, cols = min(BV, V - v0);
+    const uint32_t bar = smem_u32(&s_bar);
+    const size_t st = ((size_t)n * H + h) * (size_t)K * V + v0;
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    const bool whole = cols == V;  // the rows lie side by side
+    if (h0) {
+        if (tid == 0) mbar_arrive_expect_tx(bar, 4u * K * cols);
+        __syncwarp();
+        if (whole) {
+            if (tid == 0) bulk_load(smem_u32(sm), h0 + st, 4u * K * cols, bar);
+        } else if (tid < 32) {
+            for (int r = tid; r < K; r += 32) bulk_load(smem_u32(sm + r * cols), h0 + st + (size_t)r * V, 4u * cols, bar);
+        }
+    } else {
+        for (int x = tid; x < K * cols; x += NT) sm[x] = 0.f;
+    }
+    long bos, eos;
+    if (cu) { bos = __ldg(cu + n); eos = __ldg(cu + n + 1); }
+    else    { bos = (long)n * T; eos = bos + T; }
+    const int quads = cols / 4, groups = NT / quads, quad = tid % quads, group = tid / quads;
+    const bool on = group < groups;
+    const int Hq = H / hr, hq = h / hr;
+    const Gates::Head head = gates.head(h);
+    const float scale = rsqrtf((float)K);
+    bool waiting = h0 != nullptr;
+    auto state_here = [&] {
+        if (waiting && !mbar_wait(bar, 0) && tid == 0) {
+            atomicAdd(&g_token_timeouts, 1u);
+            if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
+        }
+        waiting = false;
+    };
+    float4* S = reinterpret_cast<float4*>(sm) + quad;
+    for (long t = bos; t < eos; ++t) {
+        const size_t qk = ((size_t)t * Hq + hq) * K, vo = ((size_t)t * H + h) * V + v0 + 4 * quad;
+        float qv = 0.f, kv = 0.f;
+        if (tid < K) {
+            qv = to_f32(q[qk + tid]);
+            kv = to_f32(k[qk + tid]);
+        }
+        float u[4] = {};
+        if (on)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = to_f32(v[vo + j]);
+        const float dec = expf(gates.decay(t, h, head)), rate = gates.rate(t, h);
+        float dots[3] = {qv * qv, kv * kv, qv * kv};
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) dots[e] += __shfl_xor_sync(0xffffffffu, dots[e], m);
+            if ((tid & 31) == 0) s_dot[e][tid >> 5] = dots[e];
+        }
+        s_q[tid] = qv;
+        s_k[tid] = kv;
+        state_here();
+        __syncthreads();
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+        if (on) {
+#pragma unroll 4
+            for (int r = group; r < K; r += groups) {
+                const float4 s = S[r * quads];
+                const float a = s_k[r], b = s_q[r];
+                y.x = fmaf(s.x, a, y.x); y.y = fmaf(s.y, a, y.y); y.z = fmaf(s.z, a, y.z); y.w = fmaf(s.w, a, y.w);
+                z.x = fmaf(s.x, b, z.x); z.y = fmaf(s.y, b, z.y); z.z = fmaf(s.z, b, z.z); z.w = fmaf(s.w, b, z.w);
+            }
+            reinterpret_cast<float4*>(part)[tid] = y;
+            reinterpret_cast<float4*>(part + kPart)[tid] = z;
+        }
+        __syncthreads();
+        if (on) {
+            float d[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) d[e] += s_dot[e][x];
+            const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(d[0] + kQNormEps) : 1.f;
+            const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(d[1] + kQNormEps) : 1.f;
+            auto total = [&](const float* from) {
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int g = 0; g < groups; ++g) {
+                    const float4 x = reinterpret_cast<const float4*>(from)[g * quads + quad];
+                    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+                }
+                return s;
+            };
+            y = total(part);
+            const float g = dec * nk;
+            u[0] = rate * (u[0] - g * y.x);
+            u[1] = rate * (u[1] - g * y.y);
+            u[2] = rate * (u[2] - g * y.z);
+            u[3] = rate * (u[3] - g * y.w);
+            if (group == t % groups) {  // (each group's turn)
+                z = total(part + kPart);
+                const float f = scale * nq, c = nk * d[2];
+                o[vo] = from_f32<OutT>(f * fmaf(c, u[0], dec * z.x));
+                o[vo + 1] = from_f32<OutT>(f * fmaf(c, u[1], dec * z.y));
+                o[vo + 2] = from_f32<OutT>(f * fmaf(c, u[2], dec * z.z));
+                o[vo + 3] = from_f32<OutT>(f * fmaf(c, u[3], dec * z.w));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] *= nk;
+#pragma unroll 4
+            for (int r = group; r < K; r += groups) {
+                float4 s = S[r * quads];
+                const float a = s_k[r];
+                s.x = fmaf(s.x, dec, a * u[0]);
+                s.y = fmaf(s.y, dec, a * u[1]);
+                s.z = fmaf(s.z, dec, a * u[2]);
+                s.w = fmaf(s.w, dec, a * u[3]);
+                S[r * quads] = s;
+            }
+        }
+        __syncthreads();
+    }
+    state_here();
+    if (!hT) return;
+    fence_proxy_async_smem();
+    __syncthreads();
+    // (this block has read its part of h0 and no other touches it: hT may be h0)
+    if (tid < 32) {
+        if (whole) {
+            if (tid == 0) bulk_store(hT + st, smem_u32(sm), 4u * K * cols);
+        } else {
+            for (int r = tid; r < K; r += 32) bulk_store(hT + st + (size_t)r * V, smem_u32(sm + r * cols), 4u * cols);
+        }
+        asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+}
+
+template <typename InT, typename OutT, int RG>
 __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
     const InT* __restrict__ q, const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags,
-    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V,
-    OutT* __restrict__ o) {
-    constexpr int RPW = KP / 8, VPT = BV / 32;
-    __shared__ __align__(16) float s_k[2][8][BV], s_q[2][8][BV];  // partial S^T k and S^T q
-    __shared__ float s_dot[2][3][8];                              // partial |q|^2, |k|^2 and q . k
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int v0 = blockIdx.x * BV, h = blockIdx.y, n = blockIdx.z;
+    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int vblocks, long units,
+    OutT* o) {
+    constexpr int R = 16, COLS = 128 / RG;  // rows of a lane, columns of a warp
+    const int lane = threadIdx.x & 31, rg = lane / (32 / RG);
+    const long unit = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (unit >= units) return;
+    const int vb = (int)(unit % vblocks), h = (int)(unit / vblocks % H), n = (int)(unit / vblocks / H);
     long bos, eos;
     if (cu) { bos = __ldg(cu + n); eos = __ldg(cu + n + 1); }
     else    { bos = (long)n * T; eos = bos + T; }
 
-    const int row0 = warp * RPW, col = v0 + lane * VPT;
-    const size_t st = ((size_t)n * H + h) * (size_t)K * V;
-    float S[RPW][VPT];
+    const int row0 = R * rg, col = vb * COLS + 4 * (lane % (32 / RG));
+    const size_t st = ((size_t)n * H + h) * (size_t)K * V + (size_t)row0 * V + col;
+    float S[R][4];
 #pragma unroll
-    for (int r = 0; r < RPW; ++r) {
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) S[r][j] = 0.f;
+        for (int j = 0; j < 4; ++j) S[r][j] = 0.f;
         if (!h0) continue;
-        const float* src = h0 + st + (size_t)(row0 + r) * V + col;
-        if constexpr (!MASKED) ld_state<VPT>(src, S[r]);
-        else if (row0 + r < K) {
+        const float* src = h0 + st + (size_t)r * V;
+        if (row0 + r < K) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
+            for (int j = 0; j < 4; ++j)
                 if (col + j < V) S[r][j] = src[j];
         }
     }
     const float scale = rsqrtf((float)K);
     const int Hq = H / hr, hq = h / hr;
     const Gates::Head head = gates.head(h);
-    int buf = 0;
-    for (long t = bos; t < eos; ++t, buf ^= 1) {
-        const size_t qk = ((size_t)t * Hq + hq) * K + row0, vo = ((size_t)t * H + h) * V;
+    for (long t = bos; t < eos; ++t) {
+        const size_t qk = ((size_t)t * Hq + hq) * K + row0, vo = ((size_t)t * H + h) * V + col;
         const float dec = expf(gates.decay(t, h, head)), rate = gates.rate(t, h);
-        float kr[RPW], qr[RPW], u[VPT], pk[VPT], pq[VPT];
-        if constexpr (!MASKED) {
+        float kr[R], u[4], y[4] = {}, z[4] = {}, qq = 0.f, kk = 0.f, qk_dot = 0.f;  // y = S^T k, z = S^T q
 #pragma unroll
-            for (int r = 0; r < RPW; r += 8) { ld8(k + qk + r, kr + r); ld8(q + qk + r, qr + r); }
-        } else {
+        for (int r = 0; r < R; ++r) kr[r] = row0 + r < K ? to_f32(k[qk + r]) : 0.f;
 #pragma unroll
-            for (int r = 0; r < RPW; ++r) {
-                const bool in = row0 + r < K;
-                kr[r] = in ? to_f32(k[qk + r]) : 0.f;
-                qr[r] = in ? to_f32(q[qk + r]) : 0.f;
+        for (int j = 0; j < 4; ++j) u[j] = col + j < V ? to_f32(v[vo + j]) : 0.f;
+#pragma unroll
+        for (int half = 0; half < R; half += 8) {
+            float qr[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) qr[r] = row0 + half + r < K ? to_f32(q[qk + half + r]) : 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float kv = kr[half + r];
+                qq = fmaf(qr[r], qr[r], qq);
+                kk = fmaf(kv, kv, kk);
+                qk_dot = fmaf(qr[r], kv, qk_dot);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[j] = fmaf(S[half + r][j], kv, y[j]);
+                    z[j] = fmaf(S[half + r][j], qr[r], z[j]);
+                }
             }
         }
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            u[j] = (!MASKED || col + j < V) ? to_f32(v[vo + col + j]) : 0.f;
-            pk[j] = pq[j] = 0.f;
-        }
-        float qq = 0.f, kk = 0.f, qk_dot = 0.f;
+        for (int m = 16; m >= 32 / RG; m >>= 1) {
+            qq += __shfl_xor_sync(0xffffffffu, qq, m);
+            kk += __shfl_xor_sync(0xffffffffu, kk, m);
+            qk_dot += __shfl_xor_sync(0xffffffffu, qk_dot, m);
 #pragma unroll
-        for (int r = 0; r < RPW; ++r) {
-            qq = fmaf(qr[r], qr[r], qq);
-            kk = fmaf(kr[r], kr[r], kk);
-            qk_dot = fmaf(qr[r], kr[r], qk_dot);
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                pk[j] = fmaf(S[r][j], kr[r], pk[j]);
-                pq[j] = fmaf(S[r][j], qr[r], pq[j]);
+            for (int j = 0; j < 4; ++j) {
+                y[j] += __shfl_xor_sync(0xffffffffu, y[j], m);
+                z[j] += __shfl_xor_sync(0xffffffffu, z[j], m);
             }
-        }
-        st_state<VPT>(&s_k[buf][warp][lane * VPT], pk);
-        st_state<VPT>(&s_q[buf][warp][lane * VPT], pq);
-        if (lane == 0) { s_dot[buf][0][warp] = qq; s_dot[buf][1][warp] = kk; s_dot[buf][2][warp] = qk_dot; }
-        __syncthreads();
-        qq = kk = qk_dot = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            qq += s_dot[buf][0][w];
-            kk += s_dot[buf][1][w];
-            qk_dot += s_dot[buf][2][w];
         }
         const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(qq + kQNormEps) : 1.f;
         const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(kk + kQNormEps) : 1.f;
+        const float fs = scale * nq;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float y = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) y += s_k[buf][w][lane * VPT + j];
-            u[j] = rate * (u[j] - dec * nk * y);
-        }
-        if (warp == (int)(t & 7)) {  // (each warp's turn)
-            const float fs = scale * nq;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                float y = 0.f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) y += s_q[buf][w][lane * VPT + j];
-                if (!MASKED || col + j < V) o[vo + col + j] = from_f32<OutT>(fs * fmaf(nk * qk_dot, u[j], dec * y));
-            }
+        for (int j = 0; j < 4; ++j) {
+            u[j] = rate * (u[j] - dec * nk * y[j]);
+            if (rg == 0 && col + j < V) o[vo + j] = from_f32<OutT>(fs * fmaf(nk * qk_dot, u[j], dec * z[j]));
+            u[j] *= nk;
         }
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) u[j] *= nk;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < RPW; ++r)
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) S[r][j] = fmaf(S[r][j], dec, kr[r] * u[j]);
+            for (int j = 0; j < 4; ++j) S[r][j] = fmaf(S[r][j], dec, kr[r] * u[j]);
     }
-    // every thread has read its part of h0 above and no other program touches it: hT may be h0
+    // this lane has read its part of h0 above and no other touches it: hT may be h0
     if (!hT) return;
 #pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-        float* dst = hT + st + (size_t)(row0 + r) * V + col;
-        if constexpr (!MASKED) st_state<VPT>(dst, S[r]);
-        else if (row0 + r < K) {
+    for (int r = 0; r < R; ++r) {
+        float* dst = hT + st + (size_t)r * V;
+        if (row0 + r < K) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
+            for (int j = 0; j < 4; ++j)
                 if (col + j < V) dst[j] = S[r][j];
         }
     }
 }
 
-template <typename InT, typename OutT, int KP, int BV>
-cudaError_t launch_b(const DeltaArgs& a) {
-    const dim3 grid((a.V + BV - 1) / BV, a.H, a.N);
-    const bool masked = a.K != KP || a.V % BV != 0;
-    auto kern = masked ? delta_recurrent_kernel<InT, OutT, KP, BV, true>
-                       : delta_recurrent_kernel<InT, OutT, KP, BV, false>;
-    kern<<<grid, 256, 0, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a), a.flags, a.h0, a.hT,
-                                     a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, (OutT*)a.o);
+template <typename InT, typename OutT, int RG>
+cudaError_t launch_r(const DeltaArgs& a) {
+    constexpr int COLS = 128 / RG;
+    const int vblocks = (a.V + COLS - 1) / COLS;
+    const long units = (long)a.N * a.H * vblocks;
+    const long blocks = (units + 7) / 8;
+    if (blocks > 0x7fffffffl) return cudaErrorInvalidValue;
+    delta_recurrent_kernel<InT, OutT, RG><<<(unsigned)blocks, 256, 0, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a), a.flags, a.h0, a.hT,
+                                                 a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, units, (OutT*)a.o);
     return cudaGetLastError();
 }
 
 template <typename InT, typename OutT>
 cudaError_t launch_k(const DeltaArgs& a) {
-    // at most 64 state floats per thread (KP BV / 256)
-    if (a.K <= 64) return a.V > 64 ? launch_b<InT, OutT, 64, 128>(a) : launch_b<InT, OutT, 64, 64>(a);
-    if (a.K <= 128) return a.V > 64 ? launch_b<InT, OutT, 128, 128>(a) : launch_b<InT, OutT, 128, 64>(a);
-    return launch_b<InT, OutT, 256, 64>(a);
+    if (a.V % 4 == 0) {
+        const int BV = min(a.K <= 128 ? 128 : 64, a.V), bytes = (kTile + 2 * kPart) * (int)sizeof(float);
+        auto kern = delta_token_kernel<InT, OutT>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        kern<<<dim3((a.V + BV - 1) / BV, a.H, a.N), NT, bytes, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a),
+                                                                         a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV,
+                                                                         a.status, (OutT*)a.o);
+        return cudaGetLastError();
+    }
+    return a.K <= 64 ? launch_r<InT, OutT, 4>(a) : a.K <= 128 ? launch_r<InT, OutT, 8>(a) : launch_r<InT, OutT, 16>(a);
 }
 
 }  // namespace
@@ -197,6 +310,15 @@ cudaError_t launch_delta_recurrent(const DeltaArgs& a) {
     if (a.N == 0) return cudaSuccess;
     if (!a.qkv_bf16) return delta::launch_k<float, float>(a);
     return a.o_f32 ? delta::launch_k<__nv_bfloat16, float>(a) : delta::launch_k<__nv_bfloat16, __nv_bfloat16>(a);
+}
+
+cudaError_t read_token_timeouts(unsigned* count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, delta::g_token_timeouts, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(delta::g_token_timeouts, &zero, sizeof(unsigned));
+    }
+    return e;
 }
 
 }  // namespace kda

@@ -6,15 +6,19 @@
 //   angle = p f,   p = the token's position on the pair's axis, f = inv_freq of the pair.
 //
 // The angle is wanted modulo a turn only, and positions are integers: f / 2 pi is taken modulo 1 as a 64-bit
-// fraction (from 53 bits), and p times it modulo 2^64 is exact.  So an angle is off by p 2^-53 turns however far
-// the position; a float32 product is off by 0.06 radians at 10^6.
+// fraction (integer product of f's 24 bits and 2^64 / 2 pi), and p times it modulo 2^64 is exact.  So an angle is off by
+// p f 2^-65 turns however far the position; a float32 product is off by 0.06 radians at 10^6.
 //
 // A block has `tile` consecutive tokens with all their heads: the angles' cosines and sines are formed once a token,
-// in shared memory.  A lane has four pairs: a row is split so that both halves of its pairs lie in one lane (two
-// loads of four elements, R / 2 apart, or one of eight), and LPR lanes share a row.
+// in shared memory, while the first rows are on their way.  A lane has four pairs: a row is split so that both halves of
+// its pairs lie in one lane (two loads of four elements, R / 2 apart, or one of eight), and LPR lanes share a row.  The
+// next U rows of a lane are on their way while it works on U.
+//
+// Memory bounds it: each row goes in and out once.
 #include "common.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
+#include "tile_ops.cuh"
 
 namespace kda {
 namespace {
@@ -48,27 +52,41 @@ __device__ __forceinline__ float2 turn(const Params& p, long t, int i) {
     const float f = __ldg(p.freq + i);
     const int axis = (p.axes.bits[i >> 4] >> (2 * (i & 15))) & 3;
     const long pos = __ldg(p.pos + axis * p.tokens + t);
-    double x = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-    x -= floor(x);
-    const unsigned long long a = (unsigned long long)pos * __double2ull_rz(x * 18446744073709551616.0);
-    float s, c;
-    sincospif((float)(int)(a >> 32) * (1.f / 2147483648.f), &s, &c);
+    // |f| = m 2^(e - 150): its turns in 2^-64 are m (2^64 / 2 pi) 2^(e - 150), modulo 2^64
+    const uint32_t bits = __float_as_uint(f) & 0x7FFFFFFFu, e = bits >> 23;
+    const unsigned long long m = e ? (bits & 0x7FFFFFu) | 0x800000u : bits << 1, unit = 0x28BE60DB9391054Aull;
+    const unsigned long long lo = m * unit, hi = __umul64hi(m, unit);
+    const int s = 150 - (int)(e ? e : 0u);
+    unsigned long long turns = s <= 0 ? (s > -64 ? lo << -s : 0ull) : s < 64 ? (lo >> s) | (hi << (64 - s)) : s < 128 ? hi >> (s - 64) : 0ull;
+    if (f < 0.f) turns = 0ull - turns;
+    const unsigned long long a = (unsigned long long)pos * turns;
+    float si, co;
+    sincospif((float)(int)(a >> 32) * (1.f / 2147483648.f), &si, &co);
     const float bad = fabsf(f) < __int_as_float(0x7f800000) ? 0.f : __int_as_float(0x7fffffff);
-    return make_float2(c * p.m + bad, s * p.m + bad);
+    return make_float2(co * p.m + bad, si * p.m + bad);
 }
 
-__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float* r) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    r[0] = sm100::bf_lo(v.x); r[1] = sm100::bf_hi(v.x); r[2] = sm100::bf_lo(v.y); r[3] = sm100::bf_hi(v.y);
-}
-__device__ __forceinline__ void ld4(const float* p, float* r) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-}
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float* r) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(sm100::pack_bf16(r[0], r[1]), sm100::pack_bf16(r[2], r[3]));
-}
-__device__ __forceinline__ void st4(float* p, const float* r) { *reinterpret_cast<float4*>(p) = make_float4(r[0], r[1], r[2], r[3]); }
+// four elements as they lie in memory, and as floats
+template <typename T>
+struct Four;
+template <>
+struct Four<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(Raw v, float2& a, float2& b) {
+        a = make_float2(sm100::bf_lo(v.x), sm100::bf_hi(v.x));
+        b = make_float2(sm100::bf_lo(v.y), sm100::bf_hi(v.y));
+    }
+    static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_uint2(sm100::pack_bf16(a.x, a.y), sm100::pack_bf16(b.x, b.y)); }
+};
+template <>
+struct Four<float> {
+    using Raw = float4;
+    static __device__ __forceinline__ void unpack(Raw v, float2& a, float2& b) {
+        a = make_float2(v.x, v.y);
+        b = make_float2(v.z, v.w);
+    }
+    static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
+};
 
 __device__ __forceinline__ float factor(const Params& p, float sum) {
     return p.norm == KDA_NORM_NONE ? 1.f : rsqrtf((p.norm == KDA_NORM_RMS ? sum / (float)p.D : sum) + p.eps);
@@ -76,73 +94,111 @@ __device__ __forceinline__ float factor(const Params& p, float sum) {
 
 // D and R multiples of 8, rows 16-byte aligned.  LPR: lanes a row, D / 8 rounded up to a power of 2.
 template <typename T, int LPR>
-__global__ void __launch_bounds__(NT) qk_norm_rope_kernel(Params p) {
-    extern __shared__ float2 s_turn[];  // [tile][R / 2]
+__global__ void __launch_bounds__(NT, 3) qk_norm_rope_kernel(const __grid_constant__ Params p) {
+    using decay::fma2;
+    using decay::mul2;
+    using F = Four<T>;
+    extern __shared__ __align__(16) float s_turn[];  // [tile][3][R / 2]: cosine, sine and its negative
     const int tid = threadIdx.x, half = p.R / 2;
     const long t0 = (long)blockIdx.x * p.tile;
-    const int nt = (int)min((long)p.tile, p.tokens - t0);
-    for (int x = tid; x < nt * half; x += NT) s_turn[x] = turn(p, t0 + x / half, x % half);
-    if (half) __syncthreads();
+    const int nt = (int)min((long)p.tile, p.tokens - t0), rows = nt * p.heads;
 
     // the lane's pairs i .. i + 3: elements i and R / 2 + i behind the first half's start, or eight in a row
     const int l = tid % LPR, i = 4 * l;
     const bool on = 2 * i < p.D, rot = i < half;
     const int a = rot && !p.interleaved ? i : 2 * i, b = rot && !p.interleaved ? half + i : 2 * i + 4;
-    float w[2][8];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[s][e] = on && p.w[s] ? __ldg(p.w[s] + (e < 4 ? a + e : b + e - 4)) : 1.f;
 
-    constexpr int G = NT / LPR, U = 4;  // rows at a time; loads of U rows in flight
-    const int rows = nt * p.heads;
-    for (int r0 = tid / LPR; r0 < rows; r0 += G * U) {
-        float v[U][8];
-        int tt[U], hh[U];
+    constexpr int G = NT / LPR, U = sizeof(T) == 2 ? 4 : 2;  // rows at a time; rows of a lane on their way
+    const T* xq = static_cast<const T*>(p.x[0]) + t0 * p.xs[0];
+    const T* xk = static_cast<const T*>(p.x[1]) + t0 * p.xs[1];
+    T* yq = static_cast<T*>(p.y[0]) + t0 * p.ys[0];
+    T* yk = static_cast<T*>(p.y[1]) + t0 * p.ys[1];
+    // row r of the block: its token there, its side and its head's elements (a block's offsets fit 31 bits)
+    auto where = [&](int r, int& tt, int& side, int& at) {
+        tt = p.per ? (int)__umulhi((uint32_t)r, p.per) : r;
+        const int hh = r - tt * p.heads;
+        side = hh >= p.Hq;
+        at = (hh - (side ? p.Hq : 0)) * p.D;
+    };
+    typename F::Raw va[U], vb[U];
+    auto fetch = [&](int r0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * G;
-            tt[u] = p.per ? (int)__umulhi((uint32_t)r, p.per) : r;
-            hh[u] = r - tt[u] * p.heads;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
-            if (r < rows && on) {
-                const int side = hh[u] >= p.Hq;
-                const T* src = static_cast<const T*>(p.x[side]) + (t0 + tt[u]) * p.xs[side] + (hh[u] - (side ? p.Hq : 0)) * p.D;
-                ld4(src + a, v[u]);
-                ld4(src + b, v[u] + 4);
+            va[u] = vb[u] = typename F::Raw{};
+            if (r0 + u * G < rows && on) {
+                int tt, side, at;
+                where(r0 + u * G, tt, side, at);
+                const T* src = (side ? xk : xq) + (at + tt * (int)(side ? p.xs[1] : p.xs[0]));
+                va[u] = *reinterpret_cast<const typename F::Raw*>(src + a);
+                vb[u] = *reinterpret_cast<const typename F::Raw*>(src + b);
             }
         }
+    };
+    const int first = tid / LPR;
+    fetch(first);
+    for (int x = tid; x < nt * half; x += NT) {
+        const int t = x / half, j = x % half;
+        const float2 z = turn(p, t0 + t, j);
+        float* to = s_turn + t * 3 * half + j;
+        to[0] = z.x;
+        to[half] = z.y;
+        to[2 * half] = -z.y;
+    }
+    if (half) __syncthreads();
+    for (int r0 = 0; r0 < rows; r0 += G * U) {
+        typename F::Raw ca[U], cb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) { ca[u] = va[u]; cb[u] = vb[u]; }
+        fetch(first + r0 + G * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * G;
-            if (__all_sync(0xffffffffu, r >= rows)) break;
-            float sum = 0.f;
+            const int r = first + r0 + u * G;
+            float2 v[4];
+            F::unpack(ca[u], v[0], v[1]);
+            F::unpack(cb[u], v[2], v[3]);
+            float2 s2 = mul2(v[0], v[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(v[u][e], v[u][e], sum);
+            for (int e = 1; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
+            float sum = s2.x + s2.y;
 #pragma unroll
             for (int m = LPR / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if (r >= rows || !on) continue;
-            const int side = hh[u] >= p.Hq;
-            const float f = factor(p, sum);
-            float y[8];
+            if (r < rows && on) {
+                int tt, side, at;
+                where(r, tt, side, at);
+                const float f = factor(p, sum);
+                const float2 ff = make_float2(f, f);
+                const float* w = side ? p.w[1] : p.w[0];
+                if (w) {
+                    const float4 wa = __ldg(reinterpret_cast<const float4*>(w + a)), wb = __ldg(reinterpret_cast<const float4*>(w + b));
+                    v[0] = mul2(v[0], mul2(ff, make_float2(wa.x, wa.y)));
+                    v[1] = mul2(v[1], mul2(ff, make_float2(wa.z, wa.w)));
+                    v[2] = mul2(v[2], mul2(ff, make_float2(wb.x, wb.y)));
+                    v[3] = mul2(v[3], mul2(ff, make_float2(wb.z, wb.w)));
+                } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = v[u][e] * f * (side ? w[1][e] : w[0][e]);
-            if (rot) {
-                const float2* cs = s_turn + tt[u] * half + i;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 z = cs[e];
-                    float& ya = p.interleaved ? y[2 * e] : y[e];
-                    float& yb = p.interleaved ? y[2 * e + 1] : y[4 + e];
-                    const float xa = ya, xb = yb;
-                    ya = xa * z.x - xb * z.y;
-                    yb = xb * z.x + xa * z.y;
+                    for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], ff);
                 }
+                if (rot) {
+                    const float* from = s_turn + tt * 3 * half + i;
+                    const float4 c = *reinterpret_cast<const float4*>(from), s = *reinterpret_cast<const float4*>(from + half);
+                    if (p.interleaved) {
+                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = make_float2(v[e].x * cc[e] - v[e].y * ss[e], v[e].y * cc[e] + v[e].x * ss[e]);
+                    } else {
+                        const float4 n = *reinterpret_cast<const float4*>(from + 2 * half);
+                        const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+                        const float2 a0 = fma2(v[0], c0, mul2(v[2], make_float2(n.x, n.y))), a1 = fma2(v[1], c1, mul2(v[3], make_float2(n.z, n.w)));
+                        v[2] = fma2(v[2], c0, mul2(v[0], make_float2(s.x, s.y)));
+                        v[3] = fma2(v[3], c1, mul2(v[1], make_float2(s.z, s.w)));
+                        v[0] = a0;
+                        v[1] = a1;
+                    }
+                }
+                T* dst = (side ? yk : yq) + (at + tt * (int)(side ? p.ys[1] : p.ys[0]));
+                __stcs(reinterpret_cast<typename F::Raw*>(dst + a), F::pack(v[0], v[1]));
+                __stcs(reinterpret_cast<typename F::Raw*>(dst + b), F::pack(v[2], v[3]));
             }
-            T* dst = static_cast<T*>(p.y[side]) + (t0 + tt[u]) * p.ys[side] + (hh[u] - (side ? p.Hq : 0)) * p.D;
-            st4(dst + a, y);
-            st4(dst + b, y + 4);
         }
     }
 }
@@ -150,11 +206,12 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(Params p) {
 // Any D, R and alignment: a warp a row, a pair of single elements a lane and step.
 template <typename T>
 __global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(Params p) {
-    extern __shared__ float2 s_turn[];
+    extern __shared__ __align__(16) float s_turn[];
     const int tid = threadIdx.x, half = p.R / 2, l = tid & 31;
     const long t0 = (long)blockIdx.x * p.tile;
     const int nt = (int)min((long)p.tile, p.tokens - t0);
-    for (int x = tid; x < nt * half; x += NT) s_turn[x] = turn(p, t0 + x / half, x % half);
+    float2* turns = reinterpret_cast<float2*>(s_turn);
+    for (int x = tid; x < nt * half; x += NT) turns[x] = turn(p, t0 + x / half, x % half);
     if (half) __syncthreads();
     constexpr int S = kMaxD / 64;
     for (int r = tid >> 5; r < nt * p.heads; r += NT / 32) {
@@ -183,7 +240,7 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(Params p) {
             if (a >= p.D) continue;
             float ya = va[s] * f * (w ? __ldg(w + a) : 1.f), yb = b < p.D ? vb[s] * f * (w ? __ldg(w + b) : 1.f) : 0.f;
             if (i < half) {
-                const float2 z = s_turn[tt * half + i];
+                const float2 z = turns[tt * half + i];
                 const float xa = ya, xb = yb;
                 ya = xa * z.x - xb * z.y;
                 yb = xb * z.x + xa * z.y;
@@ -196,7 +253,7 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(Params p) {
 
 template <typename T>
 cudaError_t run(const QkNormArgs& a, Params& p, bool fast) {
-    const int grid = (int)((a.tokens + p.tile - 1) / p.tile), bytes = p.tile * (a.R / 2) * (int)sizeof(float2);
+    const int grid = (int)((a.tokens + p.tile - 1) / p.tile), bytes = p.tile * (a.R / 2) * 3 * (int)sizeof(float);
     void (*kern)(Params) = qk_norm_rope_any_kernel<T>;
     if (fast) kern = a.D > 128 ? qk_norm_rope_kernel<T, 32> : a.D > 64 ? qk_norm_rope_kernel<T, 16> : a.D > 32 ? qk_norm_rope_kernel<T, 8>
                      : qk_norm_rope_kernel<T, 4>;
@@ -213,7 +270,7 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     p.Hq = a.q.heads;
     p.heads = a.q.heads + Hk;
     const int e = a.bf16 ? 2 : 4;
-    bool fast = a.D % 8 == 0 && a.R % 8 == 0;
+    bool fast = a.D % 8 == 0 && a.R % 8 == 0 && (((uintptr_t)a.q.weight | (uintptr_t)(Hk ? a.k.weight : nullptr)) & 15u) == 0;
     for (int s = 0; s < (Hk ? 2 : 1); ++s) {
         p.x[s] = side[s]->x;
         p.y[s] = side[s]->y;
@@ -233,8 +290,13 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     p.m = a.rope_scale;
     p.tokens = a.tokens;
     // rows of a block: enough of them to share a token's angles, and blocks enough for the SMs
+    int dev = 0, sms = 1;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
     p.tile = 1;
-    while (p.tile < 16 && p.tile * p.heads < 64 && a.tokens / (2 * p.tile) >= 1024) p.tile *= 2;
+    const long far = max(max(p.xs[0], p.xs[1]), max(p.ys[0], p.ys[1]));  // a block's offsets fit 31 bits
+    while (p.tile < 64 && p.tile * p.heads < 256 && p.tile * a.R <= 4096 && a.tokens / (2 * p.tile) >= 4 * sms && far * 2 * p.tile < (1l << 30)) p.tile *= 2;
     // r / heads for r < 2^16 rows of a block by a product (exact: r (per heads - 2^32) < 2^32)
     p.per = p.heads > 1 ? (uint32_t)(((1ull << 32) + p.heads - 1) / p.heads) : 0;
     return a.bf16 ? run<__nv_bfloat16>(a, p, fast) : run<float>(a, p, fast);
