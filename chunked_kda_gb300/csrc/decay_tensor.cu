@@ -61,7 +61,11 @@ using namespace sm100;
 
 __device__ unsigned int g_decay_timeouts = 0;
 
-constexpr int C = 64, NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kMaxCuts = 4096, kCutCost = 8, kTop = 32;
+constexpr int NTHR = 896, NS = 3, NG = 8, kAhead = 1, kRanked = 128, kTop = 32;
+// Chunks that cuts cost an SM (a state's way, more starts): 8 x 1024 tokens, 32 heads (27 chunks an SM for the 32 of two
+// waves) 78 us with cuts and 69 without, 8 x 2048, 64 heads (108 for 128) 231 and 234; 4 x 4096, 64 heads (256 units)
+// 218 and 225, 5 x 4096, 64 heads (320) 264 and 331, 2 x 16384, 80 heads (160) 479 and 841.
+constexpr int kCutCost = 8;
 
 // barriers
 enum { B_FULL = 0, B_FREE = B_FULL + NS, B_QK = B_FREE + NS, B_P, B_D = B_P + NS, B_DREAD, B_SBF, B_VD, B_STATE, B_VFREE, B_INTER, B_O,
@@ -170,57 +174,6 @@ __device__ __noinline__ void nan_rows(uint32_t tile, uint32_t marks, int ch, uin
         for (int r = (int)lds8(marks + ch); r < C; ++r) sts16(tile + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7), 0x7FFF);
 }
 
-// Whole sequences of one length, more units than SMs, the last wave part-empty: the units' chunks are
-// laid end to end and shared out evenly, `per` (at least a unit's nt) an SM, so a unit that does not fit into what
-// is left of an SM is cut.  Its part on the next SM, which is that SM's first work, is the earlier one in time;
-// the part at this SM's end runs per - nt chunks or more after the other's end and finds its state there.
-// Blocks take the pieces in the order of their starts (a ticket, so that whoever waits began later than what it waits for):
-// the SMs' first pieces, then the whole units, then the cut units' second pieces, the longest first (their SMs
-// are free first).  4 x 4096 tokens, 64 heads (256 units): 218 us against 225 with whole
-// units; 5 x 4096, 64 heads (320): 264 against 331; 2 x 16384, 80 heads (160): 479 against 841.
-struct Piece {
-    int unit, c0, c1;
-};
-__device__ __forceinline__ Piece cut_piece(const Params& p, int* scratch) {
-    const int tid = threadIdx.x, nt = (p.T + C - 1) / C, units = p.N * p.H * p.vblocks;
-    const int W = units * nt, firsts = (W + p.per - 1) / p.per;
-    if (tid == 0) scratch[0] = (int)atomicAdd(p.cuts, 1u);
-    for (int m = tid; m < firsts; m += NTHR) scratch[2 + m] = (int)((long)m * p.per % nt);
-    __syncthreads();
-    const int i = scratch[0];
-    Piece pc;
-    if (i < firsts) {
-        const int at = i * p.per;
-        pc.unit = at / nt;
-        pc.c0 = 0;
-        pc.c1 = (pc.unit + 1) * nt - at;
-    } else if (i < units) {
-        // the (i - firsts)-th unit without a multiple of per in it: of the units up to u, ceil((u + 1) nt / per) have one
-        int lo = 0, hi = units - 1;
-        while (lo < hi) {
-            const int u = (lo + hi) / 2;
-            if (u + 1 - ((u + 1) * nt + p.per - 1) / p.per > i - firsts) hi = u;
-            else lo = u + 1;
-        }
-        pc = {lo, 0, nt};
-    } else {
-        for (int m = tid; m < firsts; m += NTHR) {
-            const int mine = scratch[2 + m];
-            int rank = 0;
-            for (int j = 0; j < firsts; ++j) rank += scratch[2 + j] > mine || (scratch[2 + j] == mine && j < m);
-            if (rank == i - units) scratch[1] = m;
-        }
-        __syncthreads();
-        const int m = scratch[1], at = m * p.per;
-        pc.unit = at / nt;
-        pc.c0 = nt - at % nt;
-        pc.c1 = nt;
-    }
-    fence_proxy_async_smem();  // (a stage's place)
-    __syncthreads();
-    return pc;
-}
-
 // kStates: only the state a segment adds (no queries, no output), for the segments' scan.
 template <int KD, int VB, typename OT, bool kStates, bool kFine = false>
 __global__ void __launch_bounds__(NTHR, 1)
@@ -243,7 +196,7 @@ decay_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     int n, bos, eos;
     bool first = true, last = true;
     if (!kStates && p.cuts) {
-        const Piece pc = cut_piece(p, reinterpret_cast<int*>(smem));
+        const Piece pc = cut_piece<NTHR>(p, reinterpret_cast<int*>(smem));
         unit = pc.unit;
         h = unit % p.H;
         vb = unit / p.H % p.vblocks;
@@ -1050,16 +1003,6 @@ int plan_segment(int B, int T, int H, int vblocks, int N, bool packed) {
     return 2 * per > T ? 0 : (int)per;
 }
 
-// Chunks of an SM where units are cut (0: they are not).  Cuts cost an SM about eight chunks (a state's way,
-// more starts): 8 x 1024 tokens, 32 heads (27 chunks an SM for the 32 of two waves) 78 us with cuts and
-// 69 without, 8 x 2048, 64 heads (108 for 128) 231 and 234.
-int plan_cuts(int B, int T, int H, int vblocks) {
-    const long sms = planned_sm_count(), units = (long)B * H * vblocks, nt = (T + C - 1) / C;
-    if (sms <= 0 || units <= sms || units * nt > 1 << 30 || sms > kMaxCuts) return 0;
-    const long waves = (units + sms - 1) / sms, per = (units * nt + sms - 1) / sms;
-    return per + kCutCost <= waves * nt ? (int)per : 0;
-}
-
 struct Plan {
     int seg, slots, per, pieces;
     size_t states, counters, half, bytes;  // states handed on; counters; one of the two outputs of a head of 256; in all
@@ -1073,10 +1016,9 @@ Plan plan(int B, int T, int H, int K, int V, int N, bool packed) {
         pl.states = (size_t)pl.slots * H * K * V * sizeof(float);
         pl.bytes = pl.states + ((size_t)pl.slots * H * sizeof(float) + 255) / 256 * 256;
     }
-    if (!packed && !pl.seg && (pl.per = plan_cuts(B, T, H, vblocks)) > 0) {
-        const int nt = (T + C - 1) / C, units = B * H * vblocks, firsts = (units * nt + pl.per - 1) / pl.per;
-        pl.pieces = units;
-        for (int m = 0; m < firsts; ++m) pl.pieces += (long)m * pl.per % nt != 0;
+    if (!packed && !pl.seg && (pl.per = plan_cuts(B, T, H, vblocks, kCutCost)) > 0) {
+        const int units = B * H * vblocks;
+        pl.pieces = count_pieces(T, units, pl.per);
         pl.states = (size_t)N * H * K * V * sizeof(float);
         pl.counters = ((size_t)(units + 1) * sizeof(unsigned) + 255) / 256 * 256;
         pl.bytes = pl.states + pl.counters;

@@ -5,8 +5,8 @@
 namespace kda {
 
 size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, int N, bool packed) {
-    (void)N; (void)packed;
-    return delta_tensor_dims(qkv_bf16 && !o_f32, K, V) ? 0 : delta_simt_workspace_bytes(B, T, H);
+    (void)N;
+    return delta_tensor_dims(qkv_bf16 && !o_f32, K, V) ? delta_tensor_workspace_bytes(B, T, H, K, V, packed) : delta_simt_workspace_bytes(B, T, H);
 }
 
 cudaError_t launch_delta_chunk(const DeltaArgs& a) {

@@ -40,7 +40,7 @@ using namespace kda::decay;
 
 __device__ unsigned int g_delta_timeouts = 0;
 
-constexpr int C = 64, KD = 128, VB = 128, NTHR = 864, NCH = 512, NPREP = 256, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
+constexpr int KD = 128, VB = 128, NTHR = 864, NCH = 512, NPREP = 256, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
 
 // Barriers.  A phase's waiters see its parity alone: each barrier's next phase needs (through others) that all waiters of the
 // last one have gone on.  Where that does not follow from the chain's order there is a barrier for each slot of the ring or parity.
@@ -81,6 +81,9 @@ struct Params {
     int N, T, H, hr, K, V;
     int vblocks;
     unsigned flags;
+    float* ws;       // cut units' states [unit of a sequence and head][K][V]
+    unsigned* cuts;  // cut units: a ticket, then a counter for each unit (all zero); else null
+    int per;         // chunks of an SM with cut units
     int* status;
     int stall_chunk;
 };
@@ -90,6 +93,11 @@ struct Sync {
     volatile uint32_t* abort_flag;
     int* status;
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * i; }
+    __device__ __forceinline__ void give_up() const {
+        atomicAdd(&g_delta_timeouts, 1u);
+        if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
+        *abort_flag = 1u;
+    }
     // One poll, which may sleep until the phase completes.  Without a time hint it is one instruction; with one it
     // is a loop of its own, and the polls of waiting warps were half of all instructions.
     static __device__ __forceinline__ bool come(uint32_t bar, uint32_t parity) {
@@ -112,11 +120,7 @@ struct Sync {
 #pragma unroll 1
             for (int n = 0; n < 64; ++n)
                 if (come(bar, parity)) return;
-            if (clock64() - begin > limit) {
-                atomicAdd(&g_delta_timeouts, 1u);
-                if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
-                *abort_flag = 1u;
-            }
+            if (clock64() - begin > limit) Sync{0, abort_flag, status}.give_up();
         }
     }
     __device__ __forceinline__ bool aborted() const { return *abort_flag != 0u; }
@@ -334,28 +338,39 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), l = tid & 31;
 
     // ---- the unit: heads fastest, then value blocks
-    const int h = blockIdx.x, vb = blockIdx.y;
-    int n = blockIdx.z;
-    if (p.cu && p.N <= kRanked) {
-        // The blocks start in order: the longest sequences first, so that none is left for the end
-        int* ranked = reinterpret_cast<int*>(smem);
-        if (tid < p.N) {
-            const int mine = __ldg(p.cu + tid + 1) - __ldg(p.cu + tid);
-            int rank = 0;
-            for (int m = 0; m < p.N; ++m) {
-                const int other = __ldg(p.cu + m + 1) - __ldg(p.cu + m);
-                rank += other > mine || (other == mine && m < tid);
+    int h = blockIdx.x, vb = blockIdx.y, n = blockIdx.z, unit = 0, bos, eos;
+    bool first = true, last = true;  // (of its unit's pieces)
+    if (p.cuts) {
+        const Piece pc = cut_piece<NTHR>(p, reinterpret_cast<int*>(smem));
+        unit = pc.unit;
+        h = unit % p.H;
+        vb = unit / p.H % p.vblocks;
+        n = unit / (p.H * p.vblocks);
+        first = pc.c0 == 0;
+        last = pc.c1 == (p.T + C - 1) / C;
+        bos = n * p.T + pc.c0 * C;
+        eos = n * p.T + min(pc.c1 * C, p.T);
+    } else {
+        if (p.cu && p.N <= kRanked) {
+            // The blocks start in order: the longest sequences first, so that none is left for the end
+            int* ranked = reinterpret_cast<int*>(smem);
+            if (tid < p.N) {
+                const int mine = __ldg(p.cu + tid + 1) - __ldg(p.cu + tid);
+                int rank = 0;
+                for (int m = 0; m < p.N; ++m) {
+                    const int other = __ldg(p.cu + m + 1) - __ldg(p.cu + m);
+                    rank += other > mine || (other == mine && m < tid);
+                }
+                ranked[rank] = tid;
             }
-            ranked[rank] = tid;
+            __syncthreads();
+            n = ranked[blockIdx.z];
+            fence_proxy_async_smem();  // (a stage's place)
+            __syncthreads();
         }
-        __syncthreads();
-        n = ranked[blockIdx.z];
-        fence_proxy_async_smem();  // (a stage's place)
-        __syncthreads();
+        if (p.cu) { bos = __ldg(p.cu + n); eos = __ldg(p.cu + n + 1); }
+        else      { bos = n * p.T; eos = bos + p.T; }
     }
-    int bos, eos;
-    if (p.cu) { bos = __ldg(p.cu + n); eos = __ldg(p.cu + n + 1); }
-    else      { bos = n * p.T; eos = bos + p.T; }
     const int nt = __shfl_sync(0xffffffffu, (eos - bos + C - 1) / C, 0);
     const int hq = h / p.hr, vc0 = vb * VB;
 
@@ -572,10 +587,20 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool mine = vc0 + vl < p.V;
         const int rows = p.K - 32 * part;  // of this warp's key channels
         float S[32];
+        const size_t state = ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(32 * part) * p.V + vc0 + vl;
+        if (!first) {  // a cut unit's second piece: it began later than the first, so this wait is short
+            bool come = false;
+            // (a poll takes half a microsecond or more, a chunk six: enough for a whole unit)
+            for (int i = 0; i < (1 << 20) + p.T && !(come = ld_acquire_gpu(p.cuts + 1 + unit) == NCH / 32); ++i)
+                if (sy.aborted()) break;
+            if (!__all_sync(0xffffffffu, come) && l == 0 && !sy.aborted()) sy.give_up();
+            __syncwarp();
+        }
         {
-            const float* from = p.h0 + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(32 * part) * p.V + vc0 + vl;
+            const float* src = first ? p.h0 : p.ws;
+            const float* from = src + state;
 #pragma unroll
-            for (int j = 0; j < 32; ++j, from += p.V) S[j] = p.h0 && mine && j < rows ? *from : 0.f;
+            for (int j = 0; j < 32; ++j, from += p.V) S[j] = src && mine && j < rows ? *from : 0.f;
         }
         // a lane's row of the four 8 x 8 blocks of a fragment load: channels + 0, + 8, rows + 0, + 8
         const int lrow = row0 + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + (y16 >> 3) + ((l >> 3) & 1);
@@ -605,10 +630,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
         for (int c = 0;; ++c) {
             // ---- S behind chunk c - 1, its terms for chunk c
-            float last = 1.f;
+            float gl = 1.f;
             if (c > 0) {
-                last = lds(gates(c - 1) + GT_LAST);
-                if (marked(c - 1)) last += nan_if(__float_as_int(lds(sb + L_MARK + 512 * ((c - 1) & 1) + 4 * vl)) < C);
+                gl = lds(gates(c - 1) + GT_LAST);
+                if (marked(c - 1)) gl += nan_if(__float_as_int(lds(sb + L_MARK + 512 * ((c - 1) & 1) + 4 * vl)) < C);
                 if (w == 0) sy.wait(B_D, (c - 1) & 1);
                 together();
             }
@@ -620,7 +645,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
-                        const float2 s = fma2(make_float2(last, last), make_float2(S[x + j], S[x + j + 1]), make_float2(d[j], d[j + 1]));
+                        const float2 s = fma2(make_float2(gl, gl), make_float2(S[x + j], S[x + j + 1]), make_float2(d[j], d[j + 1]));
                         S[x + j] = s.x;
                         S[x + j + 1] = s.y;
                     }
@@ -783,12 +808,15 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_before();
             arrive(B_UD);
         }
-        if (p.hT && mine && !sy.aborted()) {
-            float* to = p.hT + ((size_t)n * p.H + h) * (size_t)p.K * p.V + (size_t)(32 * part) * p.V + vc0 + vl;
+        float* dst = last ? p.hT : p.ws;
+        if (dst && mine && !sy.aborted()) {
+            float* to = dst + state;
 #pragma unroll
             for (int j = 0; j < 32; ++j, to += p.V)
                 if (j < rows) *to = S[j];
         }
+        __syncwarp();
+        if (!last && l == 0) red_release_gpu(p.cuts + 1 + unit, 1u);
     } else {
         // ------------------------------------------------ preparation: T and P of a chunk
         // A warp has 32 rows of the scores, of keys or of queries, and 32 of their columns.
@@ -948,6 +976,31 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // bf16, K up to 128 and a multiple of 8, V a multiple of 8 (a row of each begins 16-byte aligned, as TMA wants it)
 bool delta_tensor_dims(bool bf16, int K, int V) { return bf16 && K % 8 == 0 && K <= 128 && V % 8 == 0; }
 
+namespace delta {
+namespace {
+// Chunks that cuts cost an SM.
+constexpr int kCutCost = 3;
+struct Plan {
+    int per, pieces;
+    size_t states, counters;
+};
+Plan plan(int B, int T, int H, int K, int V, bool packed) {
+    Plan pl{0, 0, 0, 0};
+    const int vblocks = (V + VB - 1) / VB;
+    if (packed || (pl.per = plan_cuts(B, T, H, vblocks, kCutCost)) == 0) return pl;
+    pl.pieces = count_pieces(T, B * H * vblocks, pl.per);
+    pl.states = ((size_t)B * H * K * V * sizeof(float) + 255) / 256 * 256;
+    pl.counters = ((size_t)(B * H * vblocks + 1) * sizeof(unsigned) + 255) / 256 * 256;
+    return pl;
+}
+}  // namespace
+}  // namespace delta
+
+size_t delta_tensor_workspace_bytes(int B, int T, int H, int K, int V, bool packed) {
+    const delta::Plan pl = delta::plan(B, T, H, K, V, packed);
+    return pl.states + pl.counters;
+}
+
 cudaError_t launch_delta_tensor(const DeltaArgs& a) {
     using namespace delta;
     CUtensorMap m[3];  // q, k, v
@@ -959,10 +1012,13 @@ cudaError_t launch_delta_tensor(const DeltaArgs& a) {
         !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
         return cudaErrorInvalidValue;
     const int vblocks = (a.V + VB - 1) / VB;
-    const Params p{Gates(a), a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, a.flags, a.status, hook_stall_chunk()};
-    const cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    const Plan pl = plan(a.B, a.T, a.H, a.K, a.V, a.cu != nullptr);
+    unsigned* cuts = pl.per ? (unsigned*)((char*)a.ws + pl.states) : nullptr;
+    const Params p{Gates(a), a.h0, a.hT, a.cu, a.o, a.N, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, a.flags, (float*)a.ws, cuts, pl.per, a.status, hook_stall_chunk()};
+    cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e == cudaSuccess && pl.per) e = cudaMemsetAsync(cuts, 0, pl.counters, a.stream);
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<<<dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], p);
+    delta_chunk_kernel<<<pl.per ? dim3(pl.pieces) : dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], p);
     return cudaGetLastError();
 }
 

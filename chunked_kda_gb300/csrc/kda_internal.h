@@ -214,6 +214,7 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a);
 cudaError_t launch_delta_recurrent(const DeltaArgs& a);
 // its tensor-core kernel: bf16, K up to 128
 bool delta_tensor_dims(bool bf16, int K, int V);
+size_t delta_tensor_workspace_bytes(int B, int T, int H, int K, int V, bool packed);
 cudaError_t launch_delta_tensor(const DeltaArgs& a);
 cudaError_t read_delta_timeouts(unsigned* count, bool reset);
 cudaError_t read_token_timeouts(unsigned* count, bool reset);

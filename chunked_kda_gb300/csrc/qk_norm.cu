@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NT, 3) qk_norm_rope_kernel(const __grid_consta
     const bool on = 2 * i < p.D, rot = i < half;
     const int a = rot && !p.interleaved ? i : 2 * i, b = rot && !p.interleaved ? half + i : 2 * i + 4;
 
-    constexpr int G = NT / LPR, U = sizeof(T) == 2 ? 4 : 2;  // rows at a time; rows of a lane on their way
+    constexpr int G = NT / LPR, U = 2;  // rows at a time; rows of a lane on their way
     const T* xq = static_cast<const T*>(p.x[0]) + t0 * p.xs[0];
     const T* xk = static_cast<const T*>(p.x[1]) + t0 * p.xs[1];
     T* yq = static_cast<T*>(p.y[0]) + t0 * p.ys[0];

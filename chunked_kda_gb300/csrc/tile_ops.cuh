@@ -4,6 +4,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "kda_internal.h"
 #include "sm100.cuh"
 
 namespace kda {
@@ -149,6 +150,60 @@ __device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& mid, uin
     lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
 
+// Whole sequences of one length, more units than SMs, the last wave part-empty: the units' chunks are
+// laid end to end and shared out evenly, `per` (at least a unit's nt) an SM, so a unit that does not fit into what
+// is left of an SM is cut.  Its part on the next SM, which is that SM's first work, is the earlier one in time;
+// the part at this SM's end runs per - nt chunks or more after the other's end and finds its state there.
+// Blocks take the pieces in the order of their starts (a ticket, so that whoever waits began later than what it waits for):
+// the SMs' first pieces, then the whole units, then the cut units' second pieces, the longest first (their SMs
+// are free first).
+constexpr int C = 64, kMaxCuts = 4096;  // tokens of a chunk; SMs that a plan is made for, at most
+
+struct Piece {
+    int unit, c0, c1;
+};
+// p: T, N, H, vblocks, per, and cuts, whose first word is the ticket; scratch: kMaxCuts + 2 words of shared memory
+template <int NTHR, typename Params>
+__device__ __forceinline__ Piece cut_piece(const Params& p, int* scratch) {
+    const int tid = threadIdx.x, nt = (p.T + C - 1) / C, units = p.N * p.H * p.vblocks;
+    const int W = units * nt, firsts = (W + p.per - 1) / p.per;
+    if (tid == 0) scratch[0] = (int)atomicAdd(p.cuts, 1u);
+    for (int m = tid; m < firsts; m += NTHR) scratch[2 + m] = (int)((long)m * p.per % nt);
+    __syncthreads();
+    const int i = scratch[0];
+    Piece pc;
+    if (i < firsts) {
+        const int at = i * p.per;
+        pc.unit = at / nt;
+        pc.c0 = 0;
+        pc.c1 = (pc.unit + 1) * nt - at;
+    } else if (i < units) {
+        // the (i - firsts)-th unit without a multiple of per in it: of the units up to u, ceil((u + 1) nt / per) have one
+        int lo = 0, hi = units - 1;
+        while (lo < hi) {
+            const int u = (lo + hi) / 2;
+            if (u + 1 - ((u + 1) * nt + p.per - 1) / p.per > i - firsts) hi = u;
+            else lo = u + 1;
+        }
+        pc = {lo, 0, nt};
+    } else {
+        for (int m = tid; m < firsts; m += NTHR) {
+            const int mine = scratch[2 + m];
+            int rank = 0;
+            for (int j = 0; j < firsts; ++j) rank += scratch[2 + j] > mine || (scratch[2 + j] == mine && j < m);
+            if (rank == i - units) scratch[1] = m;
+        }
+        __syncthreads();
+        const int m = scratch[1], at = m * p.per;
+        pc.unit = at / nt;
+        pc.c0 = nt - at % nt;
+        pc.c1 = nt;
+    }
+    fence_proxy_async_smem();  // (a stage's place)
+    __syncthreads();
+    return pc;
+}
+
 // ------------------------------------------------------------------ host side
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -172,6 +227,22 @@ inline bool make_map(CUtensorMap* m, const void* base, long tokens, int H, int D
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Chunks of an SM where units are cut (0: they are not).  `cost`: chunks that cuts cost an SM.
+inline int plan_cuts(int B, int T, int H, int vblocks, int cost) {
+    const long sms = planned_sm_count(), units = (long)B * H * vblocks, nt = (T + C - 1) / C;
+    if (sms <= 0 || units <= sms || units * nt > 1 << 30 || sms > kMaxCuts) return 0;
+    const long waves = (units + sms - 1) / sms, per = (units * nt + sms - 1) / sms;
+    return per + cost <= waves * nt ? (int)per : 0;
+}
+
+// the blocks of a launch with cut units
+inline int count_pieces(int T, int units, int per) {
+    const int nt = (T + C - 1) / C, firsts = (units * nt + per - 1) / per;
+    int pieces = units;
+    for (int m = 0; m < firsts; ++m) pieces += (long)m * per % nt != 0;
+    return pieces;
 }
 
 }  // namespace decay
