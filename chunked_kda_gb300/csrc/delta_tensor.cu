@@ -65,7 +65,7 @@ constexpr uint32_t GT_BYTES = 1808;
 constexpr uint32_t L_RQ = L_G + NG * GT_BYTES;   // [2][64] 1 / |q_i|
 constexpr uint32_t L_MARK = L_RQ + 2 * 256;      // [2][128] each channel's first row that is not finite, 64: none
 constexpr uint32_t L_BAR = (L_MARK + 2 * 512 + 7) / 8 * 8, L_MISC = (L_BAR + 8 * NBAR + 15) / 16 * 16, L_END = L_MISC + 32;
-constexpr uint32_t SMEM_BYTES = L_END + 1024;
+constexpr uint32_t SMEM_BYTES = L_END;
 static_assert(SMEM_BYTES <= 232448, "shared memory of a block");
 // TMEM columns: S's three terms; D, whose first half is O1's place; Y, then U; the first two terms of R, then of U'; scores, then O2
 constexpr uint32_t TS = 0, TD = 192, TO1 = 192, TY = 320, TZ = 384, TSC = 448, TCOLS = 512;
@@ -180,19 +180,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
 // X <- (1 + X)^-1 in place, X strictly lower triangular, by 256 threads (named barrier 2).  The diagonal blocks of 16 by
-// substitution, a warp a block and a column a lane, then twice the block below two inverted ones, -X22 (X21 X11).
+// substitution, a warp a block and a column a lane, then twice the block below two inverted ones, -X22 (X21 X11).  Columns of
+// that are independent of one another: a warp forms both products for its own, so that the warps meet only before and
+// after the block is replaced.  The block right of the diagonal's blocks of 32 is scratch (nobody reads it as part of X).
 __device__ __forceinline__ void invert(uint32_t X, int t) {
     const int w = t >> 5, l = t & 31;
     auto at = [&](int i, int c) { return X + 4u * (LDX * i + c); };
     if (w < 4) {
-        const int b = 16 * w, c = l & 15;
+        const uint32_t b = at(16 * w, 16 * w);
+        const int c = l & 15;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float y = i == c ? 1.f : 0.f, y2 = 0.f;
 #pragma unroll
             for (int m = 0; m < i; m += 4) {
-                const float4 a = lds4(at(b + i, b + m));
+                const float4 a = lds4(b + 4 * (LDX * i + m));
                 y = fmaf(-a.x, x[m], y);
                 if (m + 1 < i) y2 = fmaf(-a.y, x[m + 1], y2);
                 if (m + 2 < i) y = fmaf(-a.z, x[m + 2], y);
@@ -203,72 +206,64 @@ __device__ __forceinline__ void invert(uint32_t X, int t) {
         __syncwarp();
         if (l < 16)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sts(at(b + i, b + c), x[i]);
+            for (int i = 0; i < 16; ++i) sts(b + 4 * (LDX * i + c), x[i]);
     }
     bar_sync(2, NPREP);
-    {   // 16 -> 32: four warps a pair, a row and two columns a thread
-        const int o = 32 * (w >> 2), i = (t & 127) >> 3, c = 2 * (t & 7);
-#pragma unroll 1
-        for (int step = 0; step < 2; ++step) {  // X21 X11, then -X22 of that
-            const uint32_t left = step ? at(o + 16 + i, o + 16) : at(o + 16 + i, o), right = step ? at(o + 16, o + c) : at(o, o + c);
-            float2 y = make_float2(0.f, 0.f);
+    {   // 16 -> 32: four warps a pair, four columns a warp, a row and two columns a lane
+        const int o = 32 * (w >> 2), i = l >> 1, c = 4 * (w & 3) + 2 * (l & 1);
+        float2 y = make_float2(0.f, 0.f), z = y;
+        const uint32_t left = at(o + 16 + i, o), right = at(o, o + c);
 #pragma unroll
-            for (int m = 0; m < 16; m += 4) {
+        for (int m = 0; m < 16; m += 4) {
+            const float4 a = lds4(left + 4 * m);
+            const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y = fma2(make_float2(av[e], av[e]), lds2(right + 4 * LDX * (m + e)), y);
+        }
+#pragma unroll
+        for (int m = 0; m < 16; m += 4) {
+            const float4 a = lds4(left + 64 + 4 * m);
+            const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int from = 2 * (m + e) + (l & 1);
+                z = fma2(make_float2(-av[e], -av[e]), make_float2(__shfl_sync(0xffffffffu, y.x, from), __shfl_sync(0xffffffffu, y.y, from)), z);
+            }
+        }
+        bar_sync(2, NPREP);
+        sts2(left + 4 * c, z.x, z.y);
+        bar_sync(2, NPREP);
+    }
+    {   // 32 -> 64: columns c and c + 1 for c = 2 w, 30 - 2 w, so that the zeros of X11 left out are the same for all warps; a row a lane
+        float2 z[2];
+        const uint32_t left = at(32 + l, 0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int c = s ? 30 - 2 * w : 2 * w;
+            float2 y = make_float2(0.f, 0.f);
+#pragma unroll 2
+            for (int m = c & ~3; m < 32; m += 4) {
                 const float4 a = lds4(left + 4 * m);
                 const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y = fma2(make_float2(av[e], av[e]), lds2(right + 4 * LDX * (m + e)), y);
+                for (int e = 0; e < 4; ++e) y = fma2(make_float2(av[e], av[e]), lds2(at(m + e, c)), y);
             }
-            bar_sync(2, NPREP);
-            const float s = step ? -1.f : 1.f;
-            sts2(at(o + 16 + i, o + c), s * y.x, s * y.y);
-            bar_sync(2, NPREP);
+            sts2(at(l, 32 + c), -y.x, -y.y);
+            z[s] = make_float2(0.f, 0.f);
         }
-    }
-    // 32 -> 64.  Half of a triangular factor is 0: a warp has the shares w and 15 - w of sixteen, 36 of 64 steps at most.
-    {   // X21 X11: a row a lane, two columns c: rows m >= c of X11 count
-        float2 y[2] = {};
+        __syncwarp();
+#pragma unroll 2
+        for (int m = 0; m < 32; m += 4) {
+            const float4 a = lds4(left + 128 + 4 * m);
+            const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int c = 2 * (s ? 15 - w : w);
-#pragma unroll 1
-            for (int m = c & ~3; m < 32; m += 4) {
-                const float4 a = lds4(at(32 + l, m));
-                const float av[4] = {a.x, a.y, a.z, a.w};
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[s] = fma2(make_float2(av[e], av[e]), lds2(at(m + e, c)), y[s]);
-            }
+                for (int s = 0; s < 2; ++s) z[s] = fma2(make_float2(av[e], av[e]), lds2(at(m + e, 32 + (s ? 30 - 2 * w : 2 * w))), z[s]);
         }
         bar_sync(2, NPREP);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) sts2(at(32 + l, 2 * (s ? 15 - w : w)), y[s].x, y[s].y);
-        bar_sync(2, NPREP);
-    }
-    {   // -X22 of that: a column a lane, two rows i: columns m <= i of X22 count
-        float y[2][2] = {};
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int i = 2 * (s ? 15 - w : w);
-#pragma unroll 1
-            for (int m = 0; m <= i + 1; m += 4) {
-                float r[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = lds(at(32 + m + e, l));
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float4 a = lds4(at(32 + i + x, 32 + m));
-                    y[s][x] = fmaf(-a.x, r[0], y[s][x]);
-                    y[s][x] = fmaf(-a.y, r[1], y[s][x]);
-                    y[s][x] = fmaf(-a.z, r[2], y[s][x]);
-                    y[s][x] = fmaf(-a.w, r[3], y[s][x]);
-                }
-            }
-        }
-        bar_sync(2, NPREP);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) sts(at(32 + 2 * (s ? 15 - w : w) + x, l), y[s][x]);
+        for (int s = 0; s < 2; ++s) sts2(left + 4 * (s ? 30 - 2 * w : 2 * w), z[s].x, z[s].y);
         bar_sync(2, NPREP);
     }
 }
@@ -329,11 +324,14 @@ __device__ __noinline__ void activate(const Gates& g, Gates::Head head, int left
 __global__ void __launch_bounds__(NTHR, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // (as the operands' swizzle wants it; checked below)
     const uint32_t sb = smem_u32(smem);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L_MISC);
     const Sync sy{sb + L_BAR, misc + M_ABORT, p.status};
+    if ((sb & 1023u) != 0) {
+        if (threadIdx.x == 0) sy.give_up();
+        return;
+    }
     auto gates = [&](int c) { return sb + L_G + (uint32_t)(c % NG) * GT_BYTES; };
     const int tid = threadIdx.x, w = __shfl_sync(0xffffffffu, tid >> 5, 0), l = tid & 31;
 
@@ -602,39 +600,48 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j, from += p.V) S[j] = src && mine && j < rows ? *from : 0.f;
         }
-        // a lane's row of the four 8 x 8 blocks of a fragment load: channels + 0, + 8, rows + 0, + 8
+        // Fragments: a lane's row of the four 8 x 8 blocks of a load is channels + 0, + 8, rows + 0, + 8 (sixteen rows further
+        // it is 2048 bytes more: the swizzle repeats)
         const int lrow = row0 + (l & 7) + ((l >> 4) << 3), lpiece = 4 * (qd & 1) + (y16 >> 3) + ((l >> 3) & 1);
-        const uint32_t panel = (qd >> 1) * 8192u, lo = sb + L_LO + panel;
-        const int pair = 4 * (row0 + 2 * (l & 3));  // byte offset of a lane's first two rows' factors
-        // the terms of sixteen rows' fragments from `r` on (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
+        const uint32_t frag = (qd >> 1) * 8192u + sw128(lrow, lpiece);
+        const uint32_t tf = tmem + lane16 + row0;                 // the warp's fragments of Y, U, O1, O2
+        const uint32_t tz = tmem + TZ + lane16 + row0 / 2;        // ... of the terms of R and U'
+        const uint32_t pair = 4 * (row0 + 2 * (l & 3));           // a lane's first two rows' factors
+        // staged output: the warp's 16 channels x 32 rows leave as 32 bytes a row, sixteen rows at once
+        const int r0 = row0 + (l >> 1), ch = 32 * qd + y16 + 8 * (l & 1);
+        const uint32_t sout = sb + L_P + (qd >> 1) * 8192u + sw128(r0, (ch & 63) >> 3);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(bos + r0) * p.H + h) * p.V + vc0 + ch;
+        const size_t row16 = (size_t)16 * p.H * p.V;
+        // the terms of sixteen rows' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
         auto write_fragments = [&](int r, float2 (&x)[4]) {
             uint32_t t[4];
-            const uint32_t at = tmem + TZ + lane16 + (row0 + r) / 2;
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
-            st16x8(at, t);
+            st16x8(tz + r / 2, t);
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
-            st16x8(at + 32, t);
+            st16x8(tz + r / 2 + 32, t);
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[e] = top2(x[e]);
-            stmatrix4_t(lo + sw128(lrow + r, lpiece), t);
+            stmatrix4_t(sb + L_LO + frag + 128 * r, t);
         };
-        auto marked = [&](int c) { return ((misc[M_ODD] >> (c & 1)) & 1u) != 0u; };
+        auto marked = [&](int b) { return ((misc[M_ODD] >> b) & 1u) != 0u; };
         // One warp polls, the others wait at a named barrier: polls take issue slots from the warps that work.
         auto together = [&] {
             bar_sync(1, NCH);
             tc_fence_after();
         };
         const float2 zero = make_float2(0.f, 0.f);
+        uint32_t gt = sb + L_G, gp = gt;  // this chunk's factors, the last one's
 #pragma unroll 1
         for (int c = 0;; ++c) {
+            const uint32_t b = c & 1, pb = b ^ 1;
             // ---- S behind chunk c - 1, its terms for chunk c
             float gl = 1.f;
             if (c > 0) {
-                gl = lds(gates(c - 1) + GT_LAST);
-                if (marked(c - 1)) gl += nan_if(__float_as_int(lds(sb + L_MARK + 512 * ((c - 1) & 1) + 4 * vl)) < C);
-                if (w == 0) sy.wait(B_D, (c - 1) & 1);
+                gl = lds(gp + GT_LAST);
+                if (marked(pb)) gl += nan_if(__float_as_int(lds(sb + L_MARK + 512 * pb + 4 * vl)) < C);
+                if (w == 0) sy.wait(B_D, pb);
                 together();
             }
 #pragma unroll
@@ -668,55 +675,49 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             arrive(B_S);
             if (c > 0) {
                 // ---- chunk c - 1's output, through the warp's own part of P's place
-                const int b = (c - 1) & 1, t0 = bos + (c - 1) * C, n_rows = min(C, eos - t0);
-                const uint32_t rq = sb + L_RQ + 256 * b, stage = sb + L_P + b * 16384;
-                const int len = __float_as_int(lds(gates(c - 1) + GT_LEN));
-                if (w == 0) sy.wait(B_O2, b);
+                const int left = eos - (bos + (c - 1) * C), len = __float_as_int(lds(gp + GT_LEN));
+                const uint32_t rq = sb + L_RQ + 256 * pb + pair, stage = 16384 * pb;
+                if (w == 0) sy.wait(B_O2, pb);
                 together();
                 float o[16];
-                ld16x32(tmem + TSC + lane16 + row0, o);
+                ld16x32(tf + TSC, o);
                 tmem_wait_ld();
                 tc_fence_before();
+                uint32_t r[8];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float2 m = lds2(rq + pair + 32 * g);
+                    const float2 m = lds2(rq + 32 * g);
                     const float2 y0 = mul2(m, make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m, make_float2(o[4 * g + 2], o[4 * g + 3]));
-                    o[4 * g] = __uint_as_float(pack_bf16(y0.x, y0.y));
-                    o[4 * g + 1] = __uint_as_float(pack_bf16(y1.x, y1.y));
+                    r[2 * g] = pack_bf16(y0.x, y0.y);
+                    r[2 * g + 1] = pack_bf16(y1.x, y1.y);
                 }
                 arrive(B_O2READ);
-#pragma unroll
-                for (int g = 0; g < 4; g += 2) {
-                    const uint32_t r[4] = {__float_as_uint(o[4 * g]), __float_as_uint(o[4 * g + 1]), __float_as_uint(o[4 * g + 4]), __float_as_uint(o[4 * g + 5])};
-                    stmatrix4_t(stage + panel + sw128(lrow + 8 * g, lpiece), r);
-                }
-                const bool odd = len < n_rows || marked(c - 1);
+                stmatrix4_t(sb + L_P + stage + frag, r);
+                stmatrix4_t(sb + L_P + stage + frag + 2048, r + 4);
+                const bool odd = len < min(C, left) || marked(pb);
                 if (odd) {
                     bar_sync(1, NCH);  // (a channel's rows are two warps')
-                    if (w < 4) nan_rows(stage, sb + L_MARK + 512 * b, vl, len, n_rows);
+                    if (w < 4) nan_rows(sb + L_P + stage, sb + L_MARK + 512 * pb, vl, len, min(C, left));
                     bar_sync(1, NCH);
-                    if (tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << b));
+                    if (tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << pb));
                 }
                 __syncwarp();
-                // the warp's 16 channels x 32 rows: 32 bytes a row, sixteen rows at once
-                const int r0 = row0 + (l >> 1), ch = 32 * qd + y16 + 8 * (l & 1);
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(t0 + r0) * p.H + h) * p.V + vc0 + ch;
                 const bool in = vc0 + ch < p.V && !sy.aborted();
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t v[4];
-                    ld_s128(stage + panel + sw128(r0 + 16 * x, (ch & 63) >> 3), v);
-                    if (in && r0 + 16 * x < n_rows) *reinterpret_cast<uint4*>(dst + (size_t)(16 * x) * p.H * p.V) = make_uint4(v[0], v[1], v[2], v[3]);
+                    ld_s128(sout + stage + 2048 * x, v);
+                    if (in && r0 + 16 * x < left) *reinterpret_cast<uint4*>(out + x * row16) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
-                arrive(B_OFREE + b);
+                out += 4 * row16;
+                arrive(B_OFREE + pb);
             }
             if (c == nt) break;
             // ---- R
-            const uint32_t gt = gates(c), vt = sb + L_V + (c % NV) * V_BYTES;
             if (w == 0) {
-                sy.wait(B_F + (c & 1), (c >> 1) & 1);
-                sy.wait(B_V + c % NV, (c / NV) & 1);
-                sy.wait(B_Y, c & 1);
+                sy.wait(B_F + b, (c >> 1) & 1);
+                sy.wait(B_V + b, (c >> 1) & 1);
+                sy.wait(B_Y, b);
             }
             together();
             const int len = __float_as_int(lds(gt + GT_LEN));
@@ -726,36 +727,39 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int x = tid; x < C * (KD / 8); x += NCH)
                     if ((x & 63) >= len) st_s128(kt + (x >> 9) * PANEL + sw128(x & 63, (x >> 6) & 7), 0, 0, 0, 0);
             }
+            const uint32_t vt = sb + L_V + V_BYTES * b;
+            float2 x[2][4];
 #pragma unroll 1
-            for (int r = 0; r < 32; r += 16) {
-                float2 x[4];
-                const uint32_t at = tmem + TY + lane16 + row0 + r;
-#pragma unroll 1
-                for (int again = 0; again < 2; ++again) {
-                    float a[8];
-                    float2 odd = zero;
-                    uint32_t v[4];
-                    ld16x16(at, a);
-                    ldmatrix4_t(vt + panel + sw128(lrow + r, lpiece), v);
-                    const float2 f[2] = {lds2(gt + GT_KEY + pair + 4 * r), lds2(gt + GT_KEY + pair + 4 * r + 32)};
-                    tmem_wait_ld();
+            for (int again = 0; again < 2; ++again) {
+                float a[16];
+                uint32_t v[8];
+                ld16x32(tf + TY, a);
+                ldmatrix4_t(vt + frag, v);
+                ldmatrix4_t(vt + frag + 2048, v + 4);
+                tmem_wait_ld();
+                float2 odd = zero;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = add_bf16(v[e], mul2(f[e >> 1], make_float2(a[2 * e], a[2 * e + 1])));
-                    if (len < C) {
+                for (int g = 0; g < 4; ++g) {
+                    const float2 f = lds2(gt + GT_KEY + pair + 32 * g);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = row0 + r + 8 * (e >> 1) + 2 * (l & 3);
-                            if (j >= len) x[e].x = 0.f;
-                            if (j + 1 >= len) x[e].y = 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        float2& y = x[g >> 1][2 * (g & 1) + e];
+                        y = add_bf16(v[2 * g + e], mul2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1])));
+                        if (len < C) {
+                            const int j = row0 + 8 * g + 2 * (l & 3);
+                            if (j >= len) y.x = 0.f;
+                            if (j + 1 >= len) y.y = 0.f;
                         }
+                        odd = fma2(y, zero, odd);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) odd = fma2(x[e], zero, odd);
-                    if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
-                    clear_odd(at, vt, gt + GT_KEY, 32 * qd + y16, row0 + r, len, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
                 }
-                write_fragments(r, x);
+                if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
+#pragma unroll 1
+                for (int r = 0; r < 32; r += 16)
+                    clear_odd(tf + TY + r, vt, gt + GT_KEY, 32 * qd + y16, row0 + r, len, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
             }
+            write_fragments(0, x[0]);
+            write_fragments(16, x[1]);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
@@ -763,50 +767,59 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // ---- O1 with its rows' factors, where O2 will be added to it
             if (w == 0) {
                 if (c == 0) sy.wait(B_SCREAD, 0);
-                if (c + 1 < nt) sy.wait(B_SCREAD + ((c + 1) & 1), ((c + 1) >> 1) & 1);
-                sy.wait(B_O1, c & 1);
+                if (c + 1 < nt) sy.wait(B_SCREAD + pb, ((c + 1) >> 1) & 1);
+                sy.wait(B_O1, b);
             }
             together();
-#pragma unroll 1
-            for (int r = 0; r < 32; r += 16) {
-                float o[8];
-                ld16x16(tmem + TO1 + lane16 + row0 + r, o);
-                const float2 f[2] = {lds2(gt + GT_ROW + pair + 4 * r), lds2(gt + GT_ROW + pair + 4 * r + 32)};
+            {
+                float o[16];
+                ld16x32(tf + TO1, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 s = mul2(f[e >> 1], make_float2(o[2 * e], o[2 * e + 1]));
-                    o[2 * e] = s.x;
-                    o[2 * e + 1] = s.y;
+                for (int g = 0; g < 4; ++g) {
+                    const float2 f = lds2(gt + GT_ROW + pair + 32 * g);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 s = mul2(f, make_float2(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]));
+                        o[4 * g + 2 * e] = s.x;
+                        o[4 * g + 2 * e + 1] = s.y;
+                    }
                 }
-                st16x16f(tmem + TSC + lane16 + row0 + r, o);
+                st16x16f(tf + TSC, o);
+                st16x16f(tf + TSC + 16, o + 8);
             }
             // ---- U'
-            if (w == 0) sy.wait(B_U, c & 1);
+            if (w == 0) sy.wait(B_U, b);
             together();
-#pragma unroll 1
-            for (int r = 0; r < 32; r += 16) {
-                float a[8];
-                float2 x[4], odd = zero;
-                const uint32_t at = tmem + TY + lane16 + row0 + r;
-                ld16x16(at, a);
-                const float2 f[2] = {lds2(gt + GT_UPD + pair + 4 * r), lds2(gt + GT_UPD + pair + 4 * r + 32)};
+            {
+                float a[16];
+                float2 odd = zero;
+                ld16x32(tf + TY, a);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 u = make_float2(a[2 * e], a[2 * e + 1]);
-                    odd = fma2(u, zero, odd);
-                    x[e] = mul2(f[e >> 1], u);
+                for (int g = 0; g < 4; ++g) {
+                    const float2 f = lds2(gt + GT_UPD + pair + 32 * g);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 u = make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]);
+                        odd = fma2(u, zero, odd);
+                        x[g >> 1][2 * (g & 1) + e] = mul2(f, u);
+                    }
                 }
                 // (U itself is O2's operand)
                 if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f))
-                    clear_odd(at, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * (c & 1), misc + M_ODD, 1u << (c & 1));
-                write_fragments(r, x);
+#pragma unroll 1
+                    for (int r = 0; r < 32; r += 16)
+                        clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
             }
+            write_fragments(0, x[0]);
+            write_fragments(16, x[1]);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_UD);
+            gp = gt;
+            gt = gt == sb + L_G + (NG - 1) * GT_BYTES ? sb + L_G : gt + GT_BYTES;
         }
         float* dst = last ? p.hT : p.ws;
         if (dst && mine && !sy.aborted()) {
@@ -825,9 +838,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t sc = tmem + TSC + ((uint32_t)(32 * (w & 3)) << 16) + c0, X = sb + L_X;
         const float scale = rsqrtf((float)p.K);
         const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0, knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
-        if (!hi && c0 > 0 && !query)  // the block right of the diagonal stays zero
-#pragma unroll 1
-            for (int j = 0; j < 32; j += 4) st_s128(X + 4 * (LDX * i + c0 + j), 0, 0, 0, 0);
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const uint32_t gt = gates(c), P = sb + L_P + (c & 1) * 16384 + (c0 >> 5) * 8192;
@@ -838,6 +848,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             bar_sync(2, NPREP);
             tc_fence_after();
+            float raw[32];
+            if (hi || c0 == 0) {
+                ld32(sc, raw);
+                tmem_wait_ld();
+            }
+            tc_fence_before();
+            arrive(B_SCREAD + (c & 1));
             const float gi = -lds(gt + GT_G + 4 * i), gf = -lds(gt + GT_G + 256 + 4 * i);
             float rk = 1.f;
             if (qnorm || knorm) {  // the rows' norms, half a row a thread
@@ -867,11 +884,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const float f = last < 0 ? 0.f : query ? scale : lds(gt + GT_BETA + 4 * i) * rk;
             float2 odd = make_float2(0.f, 0.f);
             if (hi || c0 == 0) {
-#pragma unroll 1
-                for (int b = c0; b < c0 + 32; b += 16) {
-                    float x[16];
-                    tmem_ld16(sc + b - c0, x);
-                    tmem_wait_ld();
+#pragma unroll
+                for (int half = 0; half < 32; half += 16) {
+                    float* x = raw + half;
+                    const int b = c0 + half;
                     if (hi && c0 == 0) {  // (with the key's norm of the column b + 15, which the others' are given by)
                         const float r = f * ex2_fast((gi + lds(gt + GT_G + 4 * (b + 15))) + (gf + lds(gt + GT_G + 256 + 4 * (b + 15))));
 #pragma unroll
@@ -913,8 +929,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
                 for (int j = 0; j < 8; ++j) st_s128(P + sw128(i, j), 0, 0, 0, 0);
             }
-            tc_fence_before();
-            arrive(B_SCREAD + (c & 1));
             // a row of A that is not finite: its key is not, or one before it
             const unsigned none = __ballot_sync(0xffffffffu, !query && (odd.x != 0.f || odd.y != 0.f));
             if (!query && l == 0) misc[M_BAD + 2 * (w & 1) + (c0 >> 5)] = none ? 32 * (w & 1) + __ffs(none) - 1 : C;
@@ -939,13 +953,16 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // T's terms: a row and 16 columns a thread
             if (c > 0) sy.wait(B_U, (c - 1) & 1);  // their last reader
             const int r = t >> 2, cc = 16 * (t & 3);
-#pragma unroll 1
+            const bool none_here = r < 32 && cc >= 32;  // (right of the diagonal's blocks)
+#pragma unroll
             for (int x = cc; x < cc + 16; x += 8) {
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 y = lds4(X + 4 * (LDX * r + x + 4 * e)), m = lds4(gt + GT_BETA + 4 * (x + 4 * e));
+                    const float4 y = lds4(X + 4 * (LDX * r + x + 4 * e));
+                    float4 m = lds4(gt + GT_BETA + 4 * (x + 4 * e));
                     float2 y0 = mul2(make_float2(y.x, y.y), make_float2(m.x, m.y)), y1 = mul2(make_float2(y.z, y.w), make_float2(m.z, m.w));
+                    if (none_here) y0 = y1 = make_float2(0.f, 0.f);
                     t0[2 * e] = round2(y0);
                     t0[2 * e + 1] = round2(y1);
                     t1[2 * e] = round2(y0);
