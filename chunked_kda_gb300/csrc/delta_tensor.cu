@@ -40,17 +40,17 @@ using namespace kda::decay;
 
 __device__ unsigned int g_delta_timeouts = 0;
 
-constexpr int KD = 128, VB = 128, NTHR = 864, NCH = 512, NPREP = 256, NKQ = 3, NV = 2, NG = 3, kRanked = 128;
+constexpr int KD = 128, VB = 128, NTHR = 864, NCH = 512, NPREP = 256, NKQ = 3, NP = 3, NG = 3, kRanked = 128;
 
 // Barriers.  A phase's waiters see its parity alone: each barrier's next phase needs (through others) that all waiters of the
 // last one have gone on.  Where that does not follow from the chain's order there is a barrier for each slot of the ring or parity.
-enum { B_KQ = 0, B_V = B_KQ + NKQ, B_G = B_V + NV, B_F = B_G + NG, B_SC = B_F + 2, B_SCREAD, B_S = B_SCREAD + 2, B_Y, B_O1, B_R, B_T, B_U, B_UD, B_D,
-       B_O2, B_O2READ, B_OFREE, B_KQFREE = B_OFREE + 2, B_VFREE = B_KQFREE + NKQ, B_GFREE = B_VFREE + NV, B_DRAIN = B_GFREE + NG, B_NEVER, NBAR };
+enum { B_KQ = 0, B_V = B_KQ + NKQ, B_G, B_F = B_G + NG, B_SC = B_F + 2, B_SCREAD, B_S = B_SCREAD + 2, B_Y, B_O1, B_R, B_T, B_U, B_UD, B_D,
+       B_O2, B_O2READ, B_OFREE, B_KQFREE = B_OFREE + NP, B_VFREE = B_KQFREE + NKQ, B_GFREE, B_DRAIN = B_GFREE + NG, B_NEVER, NBAR };
 
-// shared memory: stages of k and q (by 64 channels: 64 rows of k, then of q), of v; T's terms; P and, behind its reader,
-// the staged output; the third term of R and U'; the matrix of the inverse
+// shared memory: stages of k and q (by 64 channels: 64 rows of k, then of q), of v; T's terms; P and, behind its reader, the
+// staged output; the third term of R and U'; the matrix of the inverse
 constexpr uint32_t KQ_BYTES = 32768, PANEL = 16384, QROWS = 8192, V_BYTES = 16384, T_TERM = 8192;
-constexpr uint32_t L_KQ = 0, L_V = L_KQ + NKQ * KQ_BYTES, L_T = L_V + NV * V_BYTES, L_P = L_T + 3 * T_TERM, L_LO = L_P + 2 * 16384;
+constexpr uint32_t L_KQ = 0, L_V = L_KQ + NKQ * KQ_BYTES, L_T = L_V + V_BYTES, L_P = L_T + 3 * T_TERM, L_LO = L_P + NP * 16384;
 constexpr uint32_t L_X = L_LO + 16384, LDX = 68, L_G = L_X + 64 * LDX * 4;
 // a chunk's factors, one slot of a ring of NG: byte offsets of its float arrays
 constexpr uint32_t GT_G = 0;      // [2][64] -G_i as integer and fraction
@@ -234,36 +234,36 @@ __device__ __forceinline__ void invert(uint32_t X, int t) {
         sts2(left + 4 * c, z.x, z.y);
         bar_sync(2, NPREP);
     }
-    {   // 32 -> 64: columns c and c + 1 for c = 2 w, 30 - 2 w, so that the zeros of X11 left out are the same for all warps; a row a lane
-        float2 z[2];
+    {   // 32 -> 64: four columns a warp, a row a lane
+        const int c = 4 * w;
         const uint32_t left = at(32 + l, 0);
+        float2 y0 = make_float2(0.f, 0.f), y1 = y0, z0 = y0, z1 = y0;
+#pragma unroll 4
+        for (int m = c; m < 32; m += 4) {  // (rows before c of X11's columns are 0)
+            const float4 a = lds4(left + 4 * m);
+            const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int c = s ? 30 - 2 * w : 2 * w;
-            float2 y = make_float2(0.f, 0.f);
-#pragma unroll 2
-            for (int m = c & ~3; m < 32; m += 4) {
-                const float4 a = lds4(left + 4 * m);
-                const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y = fma2(make_float2(av[e], av[e]), lds2(at(m + e, c)), y);
+            for (int e = 0; e < 4; ++e) {
+                const float4 r = lds4(at(m + e, c));
+                y0 = fma2(make_float2(av[e], av[e]), make_float2(r.x, r.y), y0);
+                y1 = fma2(make_float2(av[e], av[e]), make_float2(r.z, r.w), y1);
             }
-            sts2(at(l, 32 + c), -y.x, -y.y);
-            z[s] = make_float2(0.f, 0.f);
         }
+        st_s128(at(l, 32 + c), __float_as_uint(-y0.x), __float_as_uint(-y0.y), __float_as_uint(-y1.x), __float_as_uint(-y1.y));
         __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
         for (int m = 0; m < 32; m += 4) {
             const float4 a = lds4(left + 128 + 4 * m);
             const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) z[s] = fma2(make_float2(av[e], av[e]), lds2(at(m + e, 32 + (s ? 30 - 2 * w : 2 * w))), z[s]);
+            for (int e = 0; e < 4; ++e) {
+                const float4 r = lds4(at(m + e, 32 + c));
+                z0 = fma2(make_float2(av[e], av[e]), make_float2(r.x, r.y), z0);
+                z1 = fma2(make_float2(av[e], av[e]), make_float2(r.z, r.w), z1);
+            }
         }
         bar_sync(2, NPREP);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) sts2(left + 4 * (s ? 30 - 2 * w : 2 * w), z[s].x, z[s].y);
+        st_s128(left + 4 * c, __float_as_uint(z0.x), __float_as_uint(z0.y), __float_as_uint(z1.x), __float_as_uint(z1.y));
         bar_sync(2, NPREP);
     }
 }
@@ -305,12 +305,12 @@ __device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, in
     st16x16f(t, a);
     tmem_wait_st();
 }
-// rows of a channel's staged output that are none
-__device__ __noinline__ void nan_rows(uint32_t stage, uint32_t mark, int ch, int len, int rows) {
+// rows of a channel's staged output that are none, from its mark or the head's on
+__device__ __noinline__ void nan_rows(uint32_t stage, uint32_t marks, int ch, int len, int rows) {
 #pragma unroll 1
-    for (int r = min(len, __float_as_int(lds(mark + 4 * ch))); r < rows; ++r)
+    for (int r = min(len, __float_as_int(lds(marks + 4 * ch))); r < rows; ++r)
         sts16(stage + (ch >> 6) * 8192u + sw128(r, (ch >> 3) & 7) + 2 * (ch & 7), 0x7FFF);
-    sts(mark + 4 * ch, __int_as_float(C));
+    sts(marks + 4 * ch, __int_as_float(C));
 }
 
 // raw gates of two tokens, `left` of them (or more) in the sequence
@@ -323,7 +323,7 @@ __device__ __noinline__ void activate(const Gates& g, Gates::Head head, int left
 
 __global__ void __launch_bounds__(NTHR, 1)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];  // (as the operands' swizzle wants it; checked below)
     const uint32_t sb = smem_u32(smem);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + L_MISC);
@@ -375,7 +375,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
-            if (i == B_S || i == B_R || i == B_UD || i == B_O2READ || i == B_OFREE || i == B_OFREE + 1) count = NCH / 32;
+            if (i == B_S || i == B_R || i == B_UD || i == B_O2READ) count = NCH / 32;
             if ((i >= B_F && i < B_F + 2) || (i >= B_SCREAD && i < B_SCREAD + 2) || i == B_T) count = NPREP / 32;
             mbar_init(sy.bar(i), count);
         }
@@ -384,6 +384,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_o);
     }
     for (int x = tid; x < 2 * VB; x += NTHR) sts(sb + L_MARK + 4 * x, __int_as_float(C));
     if (tid < 2 * C) sts(sb + L_RQ + 4 * tid, 1.f);  // (without norms)
@@ -422,20 +423,16 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (sy.stopped()) break;
                 tc_fence_after();
                 if (elect()) {
-                    const uint32_t k = lo_k(st);
 #pragma unroll 1
-                    for (int t = 2; t >= 0; --t)
+                    for (int x = 0; x < 4; ++x) {  // Y from S's terms 2, 1, 0, then O1 from term 0
+                        const uint32_t to = tmem + (x < 3 ? TY : TO1), from = tmem + TS + 64 * (x < 3 ? 2 - x : 0);
+                        const uint32_t r = lo_k(st + (x < 3 ? 0 : QROWS));
 #pragma unroll
                         for (int kk = 0; kk < KD / 16; ++kk)
-                            umma_bf16_ta(tmem + TY, tmem + TS + 64 * t + 8 * kk, desc(k + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
-                                         idesc_bf16(128, 64, 0, 0), t < 2 || kk > 0);
-                    umma_commit(sy.bar(B_Y));
-                    const uint32_t q = lo_k(st + QROWS);
-#pragma unroll
-                    for (int kk = 0; kk < KD / 16; ++kk)
-                        umma_bf16_ta(tmem + TO1, tmem + TS + 8 * kk, desc(q + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2),
-                                     idesc_bf16(128, 64, 0, 0), kk > 0);
-                    umma_commit(sy.bar(B_O1));
+                            umma_bf16_ta(to, from + 8 * kk, desc(r + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2), idesc_bf16(128, 64, 0, 0),
+                                         (x != 0 && x != 3) || kk > 0);
+                        if (x >= 2) umma_commit(sy.bar(x == 2 ? B_Y : B_O1));
+                    }
                 }
                 __syncwarp();
             }
@@ -450,7 +447,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (sy.stopped()) break;
             tc_fence_after();
             if (elect()) {  // the smallest products first
-                mbar_arrive(sy.bar(B_VFREE + c % NV));  // (v has been read into R, the last chunk's output has been formed)
+                mbar_arrive(sy.bar(B_VFREE));  // (v has been read into R, the last chunk's output has been formed)
                 if (c > 0) mbar_arrive(sy.bar(B_GFREE + (c - 1) % NG));
                 const uint32_t T = lo_k(sb + L_T), lo = lo_mn(sb + L_LO);
 #pragma unroll
@@ -470,7 +467,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (sy.stopped()) break;
             tc_fence_after();
             if (elect()) {
-                const uint32_t k = lo_kq_mn(st), lo = lo_mn(sb + L_LO), P = lo_k(sb + L_P + (c & 1) * 16384);
+                const uint32_t k = lo_kq_mn(st), lo = lo_mn(sb + L_LO), P = lo_k(sb + L_P + (c % NP) * 16384);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     umma_bf16(tmem + TD, desc(lo + kk * 128), desc(k + kk * 128), idesc_bf16(128, KD, 1, 1), kk > 0);
@@ -497,31 +494,42 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (w == 25) {
         // ------------------------------------------------ loads
-        int c = 0;
-#pragma unroll 1
-        for (; c < nt; ++c) {
-            if (c >= NKQ) sy.wait(B_KQFREE + c % NKQ, (c / NKQ - 1) & 1);
-            if (c >= NV) sy.wait(B_VFREE + c % NV, (c / NV - 1) & 1);
-            if (sy.stopped()) break;
+        auto load_kq = [&](int c) {
             if (elect()) {
-                const uint32_t v = sb + L_V + (c % NV) * V_BYTES, kq = sb + L_KQ + (c % NKQ) * KQ_BYTES;
-                const uint32_t fv = sy.bar(B_V + c % NV), fkq = sy.bar(B_KQ + c % NKQ);
-                mbar_arrive_expect_tx(fkq, KQ_BYTES);
+                const uint32_t to = sb + L_KQ + (c % NKQ) * KQ_BYTES, full = sy.bar(B_KQ + c % NKQ);
+                mbar_arrive_expect_tx(full, KQ_BYTES);
 #pragma unroll 1
                 for (int x = 0; x < KD / 64; ++x) {
-                    tma_load_3d(kq + x * PANEL, &tm_k, 64 * x, hq, bos + c * C, fkq);
-                    tma_load_3d(kq + x * PANEL + QROWS, &tm_q, 64 * x, hq, bos + c * C, fkq);
+                    tma_load_3d(to + x * PANEL, &tm_k, 64 * x, hq, bos + c * C, full);
+                    tma_load_3d(to + x * PANEL + QROWS, &tm_q, 64 * x, hq, bos + c * C, full);
                 }
-                mbar_arrive_expect_tx(fv, V_BYTES);
-#pragma unroll 1
-                for (int x = 0; x < VB / 64; ++x) tma_load_3d(v + x * 8192, &tm_v, vc0 + 64 * x, h, bos + c * C, fv);
             }
             __syncwarp();
+        };
+        int kq = 0, v = 0;  // loads that have been issued
+#pragma unroll 1
+        for (int c = -NKQ; kq < nt || v < nt; ++c) {  // in chunk c: v's stage is free in its middle, k's and q's behind it
+            if (c >= -1 && v < nt) {
+                if (c >= 0) sy.wait(B_VFREE, c & 1);
+                if (sy.stopped()) break;
+                if (elect()) {
+                    mbar_arrive_expect_tx(sy.bar(B_V), V_BYTES);
+#pragma unroll 1
+                    for (int x = 0; x < VB / 64; ++x) tma_load_3d(sb + L_V + x * 8192, &tm_v, vc0 + 64 * x, h, bos + v * C, sy.bar(B_V));
+                }
+                __syncwarp();
+                ++v;
+            }
+            if (kq < nt) {
+                if (c >= 0) sy.wait(B_KQFREE + c % NKQ, (c / NKQ) & 1);
+                if (sy.stopped()) break;
+                load_kq(kq++);
+            }
         }
         if (sy.stopped()) {  // leave no copy in flight behind
             if (elect()) {
-                for (int x = max(0, c - NKQ); x < c; ++x) mbar_wait(sy.bar(B_KQ + x % NKQ), (x / NKQ) & 1);
-                for (int x = max(0, c - NV); x < c; ++x) mbar_wait(sy.bar(B_V + x % NV), (x / NV) & 1);
+                for (int x = max(0, kq - NKQ); x < kq; ++x) mbar_wait(sy.bar(B_KQ + x % NKQ), (x / NKQ) & 1);
+                if (v > 0) mbar_wait(sy.bar(B_V), (v - 1) & 1);
             }
             __syncwarp();
         }
@@ -530,49 +538,64 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const Gates::Head head = p.gates.head(h);
         const float scale = rsqrtf((float)p.K);
         float ra[2] = {}, rb[2] = {};  // as they lie in memory, asked for a chunk before they are used
-        auto ask = [&](int c) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = bos + c * C + 2 * l + e;
-                ra[e] = t < eos ? p.gates.raw_decay(t, h) : 0.f;
-                rb[e] = t < eos ? p.gates.raw_rate(t, h) : 0.f;
-            }
-        };
 #pragma unroll 1
         for (int c = -1; c < nt; ++c) {
             float a0 = ra[0], a1 = ra[1], b0 = rb[0], b1 = rb[1];
-            if (c + 1 < nt) ask(c + 1);
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                const int t = bos + (c + 1) * C + 2 * l + e;
+                const float x = t < eos ? p.gates.raw_decay(t, h) : 0.f, y = t < eos ? p.gates.raw_rate(t, h) : 0.f;
+                ra[0] = ra[1];
+                rb[0] = rb[1];
+                ra[1] = x;
+                rb[1] = y;
+            }
             if (c < 0) continue;
             const uint32_t gt = gates(c);
             const int left = eos - (bos + c * C);
             if (p.gates.raw || p.gates.logits) activate(p.gates, head, left - 2 * l, a0, a1, b0, b1);
             const float none = __int_as_float(0x7fffffff);
             const int bad = first_nan(a0 < 3e38f && finite(b0) ? 0.f : none, a1 < 3e38f && finite(b1) ? 0.f : none);
-            long long G[2];
-            pair_sums(a0, a1, G);
-            int Il, Fl, Im, Fm;
-            parts(G[1], Il, Fl);
-            Im = __shfl_sync(0xffffffffu, Il, l | 7);
-            Fm = __shfl_sync(0xffffffffu, Fl, l | 7);
+            // (sums as pair_sums forms them, with one copy of the conversion)
+            long long g = 0, g1 = 0;
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                g1 = fixed(e ? a1 : a0);
+                g += g1;
+            }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, g, m);
+                if (l >= m) g += y;
+            }
+            int Il, Fl;
+            parts(g, Il, Fl);
+            const int Im = __shfl_sync(0xffffffffu, Il, l | 7), Fm = __shfl_sync(0xffffffffu, Fl, l | 7);
             Il = __shfl_sync(0xffffffffu, Il, 31);
             Fl = __shfl_sync(0xffffffffu, Fl, 31);
             if (c >= NG) sy.wait(B_GFREE + c % NG, (c / NG - 1) & 1);
+            g -= g1;
 #pragma unroll 1
-            for (int i = 2 * l; i < 2 * l + 2; ++i) {
+            for (int i = 2 * l; i < 2 * l + 2; ++i, g += g1) {
                 int I, F;
-                parts(i & 1 ? G[1] : G[0], I, F);
-                sts(gt + GT_G + 4 * i, -(float)I);
-                sts(gt + GT_G + 256 + 4 * i, (float)F * (-1.f / 16777216.f));
-                const float r = pow2(I, F);
-                sts(gt + GT_ROW + 4 * i, scale * r);
-                sts(gt + GT_KEY + 4 * i, -r);
-                sts(gt + GT_UPD + 4 * i, i < bad ? pow2(Il - I, Fl - F) : 0.f);
-                sts(gt + GT_COL + 4 * i, pow2_fast(Im - I, Fm - F));
-                sts(gt + GT_BETA + 4 * i, i < bad ? (i & 1 ? b1 : b0) : 0.f);
-            }
-            if (l == 0) {
-                sts(gt + GT_LAST, pow2(Il, Fl));
-                sts(gt + GT_LEN, __int_as_float(min(bad, left)));
+                parts(g, I, F);
+                const uint32_t to = gt + 4 * i;
+                sts(to + GT_G, -(float)I);
+                sts(to + GT_G + 256, (float)F * (-1.f / 16777216.f));
+                sts(to + GT_COL, pow2_fast(Im - I, Fm - F));
+                sts(to + GT_BETA, i < bad ? (i & 1 ? b1 : b0) : 0.f);
+                float r;
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {  // 2^(G_l - G_i), then 2^G_i
+                    r = pow2(e ? I : Il - I, e ? F : Fl - F);
+                    if (e == 0) sts(to + GT_UPD, i < bad ? r : 0.f);
+                }
+                sts(to + GT_ROW, scale * r);
+                sts(to + GT_KEY, -r);
+                if (i == C - 1) {
+                    sts(gt + GT_LAST, r);
+                    sts(gt + GT_LEN, __int_as_float(min(bad, left)));
+                }
             }
             arrive(B_G + c % NG);
         }
@@ -607,11 +630,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t tf = tmem + lane16 + row0;                 // the warp's fragments of Y, U, O1, O2
         const uint32_t tz = tmem + TZ + lane16 + row0 / 2;        // ... of the terms of R and U'
         const uint32_t pair = 4 * (row0 + 2 * (l & 3));           // a lane's first two rows' factors
-        // staged output: the warp's 16 channels x 32 rows leave as 32 bytes a row, sixteen rows at once
-        const int r0 = row0 + (l >> 1), ch = 32 * qd + y16 + 8 * (l & 1);
-        const uint32_t sout = sb + L_P + (qd >> 1) * 8192u + sw128(r0, (ch & 63) >> 3);
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((size_t)(bos + r0) * p.H + h) * p.V + vc0 + ch;
-        const size_t row16 = (size_t)16 * p.H * p.V;
         // the terms of sixteen rows' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
         auto write_fragments = [&](int r, float2 (&x)[4]) {
             uint32_t t[4];
@@ -632,7 +650,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_after();
         };
         const float2 zero = make_float2(0.f, 0.f);
-        uint32_t gt = sb + L_G, gp = gt;  // this chunk's factors, the last one's
+        uint32_t gt = sb + L_G, gp = gt, po = 0;  // this chunk's factors, the last one's; the last one's place of P
 #pragma unroll 1
         for (int c = 0;; ++c) {
             const uint32_t b = c & 1, pb = b ^ 1;
@@ -674,49 +692,64 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_before();
             arrive(B_S);
             if (c > 0) {
-                // ---- chunk c - 1's output, through the warp's own part of P's place
-                const int left = eos - (bos + (c - 1) * C), len = __float_as_int(lds(gp + GT_LEN));
-                const uint32_t rq = sb + L_RQ + 256 * pb + pair, stage = 16384 * pb;
+                // ---- chunk c - 1's output, through P's place
+                const int t0 = bos + (c - 1) * C, n_rows = min(C, eos - t0), len = __float_as_int(lds(gp + GT_LEN));
+                const uint32_t rq = sb + L_RQ + 256 * pb + pair, stage = sb + L_P + po;
                 if (w == 0) sy.wait(B_O2, pb);
                 together();
                 float o[16];
                 ld16x32(tf + TSC, o);
+                float2 m[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) m[g] = lds2(rq + 32 * g);
+                const bool odd = len < n_rows || marked(pb);
                 tmem_wait_ld();
                 tc_fence_before();
+                arrive(B_O2READ);
                 uint32_t r[8];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float2 m = lds2(rq + 32 * g);
-                    const float2 y0 = mul2(m, make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m, make_float2(o[4 * g + 2], o[4 * g + 3]));
+                    const float2 y0 = mul2(m[g], make_float2(o[4 * g], o[4 * g + 1])), y1 = mul2(m[g], make_float2(o[4 * g + 2], o[4 * g + 3]));
                     r[2 * g] = pack_bf16(y0.x, y0.y);
                     r[2 * g + 1] = pack_bf16(y1.x, y1.y);
                 }
-                arrive(B_O2READ);
-                stmatrix4_t(sb + L_P + stage + frag, r);
-                stmatrix4_t(sb + L_P + stage + frag + 2048, r + 4);
-                const bool odd = len < min(C, left) || marked(pb);
+                stmatrix4_t(stage + frag, r);
+                stmatrix4_t(stage + frag + 2048, r + 4);
                 if (odd) {
                     bar_sync(1, NCH);  // (a channel's rows are two warps')
-                    if (w < 4) nan_rows(sb + L_P + stage, sb + L_MARK + 512 * pb, vl, len, min(C, left));
+                    if (w < 4) nan_rows(stage, sb + L_MARK + 512 * pb, vl, len, n_rows);
                     bar_sync(1, NCH);
                     if (tid == 0) atomicAnd(const_cast<uint32_t*>(misc + M_ODD), ~(1u << pb));
                 }
-                __syncwarp();
-                const bool in = vc0 + ch < p.V && !sy.aborted();
+                fence_proxy_async_smem();
+                bar_sync(1, NCH);
+                if (!sy.aborted()) {
+                    if (n_rows == C) {
+                        if (tid == 0) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t v[4];
-                    ld_s128(sout + stage + 2048 * x, v);
-                    if (in && r0 + 16 * x < left) *reinterpret_cast<uint4*>(out + x * row16) = make_uint4(v[0], v[1], v[2], v[3]);
+                            for (int x = 0; x < VB / 64; ++x)
+                                if (vc0 + 64 * x < p.V) tma_store_3d(&tm_o, stage + x * 8192, vc0 + 64 * x, h, t0);
+                            bulk_commit();
+                        }
+                    } else {  // the sequence's last rows
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((size_t)t0 * p.H + h) * p.V + vc0;
+#pragma unroll 1
+                        for (int x = tid; x < n_rows * (VB / 8); x += NCH) {
+                            const int row = x / (VB / 8), ch = x % (VB / 8);
+                            uint32_t v[4];
+                            ld_s128(stage + (ch >> 3) * 8192u + sw128(row, ch & 7), v);
+                            if (vc0 + 8 * ch < p.V) *reinterpret_cast<uint4*>(out + (size_t)row * p.H * p.V + 8 * ch) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
                 }
-                out += 4 * row16;
-                arrive(B_OFREE + pb);
+                __syncwarp();
+                po = po == (NP - 1) * 16384 ? 0 : po + 16384;
             }
             if (c == nt) break;
             // ---- R
             if (w == 0) {
                 sy.wait(B_F + b, (c >> 1) & 1);
-                sy.wait(B_V + b, (c >> 1) & 1);
+                sy.wait(B_V, b);
                 sy.wait(B_Y, b);
             }
             together();
@@ -727,43 +760,44 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int x = tid; x < C * (KD / 8); x += NCH)
                     if ((x & 63) >= len) st_s128(kt + (x >> 9) * PANEL + sw128(x & 63, (x >> 6) & 7), 0, 0, 0, 0);
             }
-            const uint32_t vt = sb + L_V + V_BYTES * b;
-            float2 x[2][4];
+            const uint32_t vt = sb + L_V;
 #pragma unroll 1
-            for (int again = 0; again < 2; ++again) {
-                float a[16];
-                uint32_t v[8];
-                ld16x32(tf + TY, a);
-                ldmatrix4_t(vt + frag, v);
-                ldmatrix4_t(vt + frag + 2048, v + 4);
-                tmem_wait_ld();
-                float2 odd = zero;
+            for (int r = 0; r < 32; r += 16) {
+                float2 x[4];
+#pragma unroll 1
+                for (int again = 0; again < 2; ++again) {
+                    float a[8];
+                    uint32_t v[4];
+                    ld16x16(tf + TY + r, a);
+                    ldmatrix4_t(vt + frag + 128 * r, v);
+                    const uint32_t key = gt + GT_KEY + pair + 4 * r;
+                    const float2 f[2] = {lds2(key), lds2(key + 32)};
+                    tmem_wait_ld();
+                    float2 odd = zero;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_KEY + pair + 32 * g);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float2& y = x[g >> 1][2 * (g & 1) + e];
-                        y = add_bf16(v[2 * g + e], mul2(f, make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1])));
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = add_bf16(v[e], mul2(f[e >> 1], make_float2(a[2 * e], a[2 * e + 1])));
                         if (len < C) {
-                            const int j = row0 + 8 * g + 2 * (l & 3);
-                            if (j >= len) y.x = 0.f;
-                            if (j + 1 >= len) y.y = 0.f;
+                            const int j = row0 + r + 8 * (e >> 1) + 2 * (l & 3);
+                            if (j >= len) x[e].x = 0.f;
+                            if (j + 1 >= len) x[e].y = 0.f;
                         }
-                        odd = fma2(y, zero, odd);
+                        odd = fma2(x[e], zero, odd);
                     }
-                }
-                if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
-#pragma unroll 1
-                for (int r = 0; r < 32; r += 16)
+                    if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
                     clear_odd(tf + TY + r, vt, gt + GT_KEY, 32 * qd + y16, row0 + r, len, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
+                }
+                write_fragments(r, x);
             }
-            write_fragments(0, x[0]);
-            write_fragments(16, x[1]);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
             arrive(B_R);
+            if (c > 0 && tid == 0) {  // the staged output has left
+                bulk_wait_read();
+                mbar_arrive(sy.bar(B_OFREE + (c - 1) % NP));
+            }
+            __syncwarp();
             // ---- O1 with its rows' factors, where O2 will be added to it
             if (w == 0) {
                 if (c == 0) sy.wait(B_SCREAD, 0);
@@ -771,49 +805,43 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 sy.wait(B_O1, b);
             }
             together();
-            {
-                float o[16];
-                ld16x32(tf + TO1, o);
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 16) {
+                float o[8];
+                ld16x16(tf + TO1 + r, o);
+                const uint32_t row = gt + GT_ROW + pair + 4 * r;
+                const float2 f[2] = {lds2(row), lds2(row + 32)};
                 tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_ROW + pair + 32 * g);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 s = mul2(f, make_float2(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]));
-                        o[4 * g + 2 * e] = s.x;
-                        o[4 * g + 2 * e + 1] = s.y;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 s = mul2(f[e >> 1], make_float2(o[2 * e], o[2 * e + 1]));
+                    o[2 * e] = s.x;
+                    o[2 * e + 1] = s.y;
                 }
-                st16x16f(tf + TSC, o);
-                st16x16f(tf + TSC + 16, o + 8);
+                st16x16f(tf + TSC + r, o);
             }
             // ---- U'
             if (w == 0) sy.wait(B_U, b);
             together();
-            {
-                float a[16];
-                float2 odd = zero;
-                ld16x32(tf + TY, a);
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 16) {
+                float a[8];
+                float2 x[4], odd = zero;
+                ld16x16(tf + TY + r, a);
+                const uint32_t upd = gt + GT_UPD + pair + 4 * r;
+                const float2 f[2] = {lds2(upd), lds2(upd + 32)};
                 tmem_wait_ld();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 f = lds2(gt + GT_UPD + pair + 32 * g);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 u = make_float2(a[4 * g + 2 * e], a[4 * g + 2 * e + 1]);
-                        odd = fma2(u, zero, odd);
-                        x[g >> 1][2 * (g & 1) + e] = mul2(f, u);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = make_float2(a[2 * e], a[2 * e + 1]);
+                    odd = fma2(u, zero, odd);
+                    x[e] = mul2(f[e >> 1], u);
                 }
                 // (U itself is O2's operand)
                 if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f))
-#pragma unroll 1
-                    for (int r = 0; r < 32; r += 16)
-                        clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
+                    clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
+                write_fragments(r, x);
             }
-            write_fragments(0, x[0]);
-            write_fragments(16, x[1]);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
@@ -821,6 +849,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             gp = gt;
             gt = gt == sb + L_G + (NG - 1) * GT_BYTES ? sb + L_G : gt + GT_BYTES;
         }
+        if (tid == 0) bulk_wait();
         float* dst = last ? p.hT : p.ws;
         if (dst && mine && !sy.aborted()) {
             float* to = dst + state;
@@ -840,17 +869,18 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0, knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
-            const uint32_t gt = gates(c), P = sb + L_P + (c & 1) * 16384 + (c0 >> 5) * 8192;
+            const uint32_t gt = gates(c), P = sb + L_P + (c % NP) * 16384 + (c0 >> 5) * 8192;
             if (w == 16) {
                 sy.wait(B_G + c % NG, (c / NG) & 1);
-                if (c >= 2) sy.wait(B_OFREE + (c & 1), ((c - 2) >> 1) & 1);  // P's place
+                if (c >= NP) sy.wait(B_OFREE + c % NP, (c / NP - 1) & 1);  // P's place
                 sy.wait(B_SC, c & 1);
             }
             bar_sync(2, NPREP);
             tc_fence_after();
-            float raw[32];
-            if (hi || c0 == 0) {
-                ld32(sc, raw);
+            const bool some = hi || c0 == 0;  // (else the block lies right of the diagonal)
+            float x[32];
+            if (some) {
+                ld32(sc, x);
                 tmem_wait_ld();
             }
             tc_fence_before();
@@ -877,57 +907,51 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bar_sync(2, NPREP);
             }
             const int full = __float_as_int(lds(gt + GT_LEN));
-            // A's rows (lanes with keys) into X, P's rows (with queries) as a tf32 operand: the score times
+            // A's rows (lanes with keys) in X, P's rows (with queries) as a tf32 operand: the score times
             // f 2^(G_i - G_j), 0 where j > last.  Left of the row's 32 the factor parts into the row's and the column's,
             // both <= 1; within them each is formed by itself.
             const int last = i < full ? i - (query ? 0 : 1) : -1;
             const float f = last < 0 ? 0.f : query ? scale : lds(gt + GT_BETA + 4 * i) * rk;
             float2 odd = make_float2(0.f, 0.f);
-            if (hi || c0 == 0) {
+            const float r0 = ex2_fast((gi + lds(gt + GT_G + 4 * 15)) + (gf + lds(gt + GT_G + 256 + 4 * 15)));
+            const float r1 = ex2_fast((gi + lds(gt + GT_G + 4 * 31)) + (gf + lds(gt + GT_G + 256 + 4 * 31)));
+            const uint32_t to = query ? P + 128 * i : X + 4 * (LDX * i + c0), turn = query ? (i & 7) << 4 : 0;  // (16-byte pieces at ^ turn)
+            const bool left = hi && c0 == 0;
+            const uint32_t gs = gt + 4 * c0;
+            float4 gj = lds4(gs + (left ? GT_COL : GT_G)), fj = lds4(gs + GT_G + 256);
+            // (the factors of the next columns are asked for before these are stored: the order in which they stand is kept)
 #pragma unroll
-                for (int half = 0; half < 32; half += 16) {
-                    float* x = raw + half;
-                    const int b = c0 + half;
-                    if (hi && c0 == 0) {  // (with the key's norm of the column b + 15, which the others' are given by)
-                        const float r = f * ex2_fast((gi + lds(gt + GT_G + 4 * (b + 15))) + (gf + lds(gt + GT_G + 256 + 4 * (b + 15))));
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 m = lds4(gt + GT_COL + 4 * (b + j));
-                            const float2 y0 = mul2(make_float2(x[j], x[j + 1]), mul2(make_float2(r, r), make_float2(m.x, m.y)));
-                            const float2 y1 = mul2(make_float2(x[j + 2], x[j + 3]), mul2(make_float2(r, r), make_float2(m.z, m.w)));
-                            x[j] = last < 0 ? 0.f : y0.x;
-                            x[j + 1] = last < 0 ? 0.f : y0.y;
-                            x[j + 2] = last < 0 ? 0.f : y1.x;
-                            x[j + 3] = last < 0 ? 0.f : y1.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 gj = lds4(gt + GT_G + 4 * (b + j)), fj = lds4(gt + GT_G + 256 + 4 * (b + j));
-                            const float2 e0 = add2(add2(make_float2(gi, gi), make_float2(gj.x, gj.y)), add2(make_float2(gf, gf), make_float2(fj.x, fj.y)));
-                            const float2 e1 = add2(add2(make_float2(gi, gi), make_float2(gj.z, gj.w)), add2(make_float2(gf, gf), make_float2(fj.z, fj.w)));
-                            const float2 y0 = mul2(mul2(make_float2(f, f), make_float2(x[j], x[j + 1])), make_float2(ex2_fast(e0.x), ex2_fast(e0.y)));
-                            const float2 y1 = mul2(mul2(make_float2(f, f), make_float2(x[j + 2], x[j + 3])), make_float2(ex2_fast(e1.x), ex2_fast(e1.y)));
-                            x[j] = b + j <= last ? y0.x : 0.f;
-                            x[j + 1] = b + j + 1 <= last ? y0.y : 0.f;
-                            x[j + 2] = b + j + 2 <= last ? y1.x : 0.f;
-                            x[j + 3] = b + j + 3 <= last ? y1.y : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        if (query) {
-                            st_s128(P + sw128(i, (b - c0 + j) / 4), to_tf32(x[j]), to_tf32(x[j + 1]), to_tf32(x[j + 2]), to_tf32(x[j + 3]));
-                        } else {
-                            st_s128(X + 4 * (LDX * i + b + j), __float_as_uint(x[j]), __float_as_uint(x[j + 1]), __float_as_uint(x[j + 2]), __float_as_uint(x[j + 3]));
-                            odd = fma2(make_float2(x[j], x[j + 1]), make_float2(0.f, 0.f), odd);
-                            odd = fma2(make_float2(x[j + 2], x[j + 3]), make_float2(0.f, 0.f), odd);
-                        }
-                    }
+            for (int e = 0; e < 32; e += 4) {
+                const int j = c0 + e;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 g = gj, f4 = fj;
+                if (e < 28) {
+                    gj = lds4(gs + (left ? GT_COL : GT_G) + 4 * (e + 4));
+                    fj = lds4(gs + GT_G + 256 + 4 * (e + 4));
                 }
-            } else if (query) {  // (the staged output was there)
-#pragma unroll 1
-                for (int j = 0; j < 8; ++j) st_s128(P + sw128(i, j), 0, 0, 0, 0);
+                if (some) {
+                    float2 e0, e1;
+                    if (left) {  // (with the key's norm of the column j | 15, which the others' are given by)
+                        const float r = e < 16 ? r0 : r1;
+                        e0 = mul2(make_float2(r, r), make_float2(g.x, g.y));
+                        e1 = mul2(make_float2(r, r), make_float2(g.z, g.w));
+                    } else {
+                        const float2 g0 = add2(add2(make_float2(gi, gi), make_float2(g.x, g.y)), add2(make_float2(gf, gf), make_float2(f4.x, f4.y)));
+                        const float2 g1 = add2(add2(make_float2(gi, gi), make_float2(g.z, g.w)), add2(make_float2(gf, gf), make_float2(f4.z, f4.w)));
+                        e0 = make_float2(ex2_fast(g0.x), ex2_fast(g0.y));
+                        e1 = make_float2(ex2_fast(g1.x), ex2_fast(g1.y));
+                    }
+                    e0 = mul2(mul2(make_float2(f, f), make_float2(x[e], x[e + 1])), e0);
+                    e1 = mul2(mul2(make_float2(f, f), make_float2(x[e + 2], x[e + 3])), e1);
+                    y.x = j <= last ? e0.x : 0.f;
+                    y.y = j + 1 <= last ? e0.y : 0.f;
+                    y.z = j + 2 <= last ? e1.x : 0.f;
+                    y.w = j + 3 <= last ? e1.y : 0.f;
+                    odd = fma2(make_float2(y.x, y.y), make_float2(0.f, 0.f), odd);
+                    odd = fma2(make_float2(y.z, y.w), make_float2(0.f, 0.f), odd);
+                }
+                if (query) st_s128(to + ((4 * e) ^ turn), to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w));
+                else if (some) st_s128(to + 4 * e, __float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z), __float_as_uint(y.w));
             }
             // a row of A that is not finite: its key is not, or one before it
             const unsigned none = __ballot_sync(0xffffffffu, !query && (odd.x != 0.f || odd.y != 0.f));
@@ -952,17 +976,16 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             invert(X, t);
             // T's terms: a row and 16 columns a thread
             if (c > 0) sy.wait(B_U, (c - 1) & 1);  // their last reader
-            const int r = t >> 2, cc = 16 * (t & 3);
-            const bool none_here = r < 32 && cc >= 32;  // (right of the diagonal's blocks)
-#pragma unroll
+            const int r = t & 63, cc = 16 * (t >> 6);
+#pragma unroll 1
             for (int x = cc; x < cc + 16; x += 8) {
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 y = lds4(X + 4 * (LDX * r + x + 4 * e));
-                    float4 m = lds4(gt + GT_BETA + 4 * (x + 4 * e));
+                    const int j = x + 4 * e;
+                    const float4 y = lds4(X + 4 * (LDX * r + j)), m = lds4(gt + GT_BETA + 4 * j);
                     float2 y0 = mul2(make_float2(y.x, y.y), make_float2(m.x, m.y)), y1 = mul2(make_float2(y.z, y.w), make_float2(m.z, m.w));
-                    if (none_here) y0 = y1 = make_float2(0.f, 0.f);
+                    if (j > (r | 31)) y0 = y1 = make_float2(0.f, 0.f);  // (right of the diagonal's blocks of 32: nothing is there)
                     t0[2 * e] = round2(y0);
                     t0[2 * e + 1] = round2(y1);
                     t1[2 * e] = round2(y0);
@@ -1020,13 +1043,14 @@ size_t delta_tensor_workspace_bytes(int B, int T, int H, int K, int V, bool pack
 
 cudaError_t launch_delta_tensor(const DeltaArgs& a) {
     using namespace delta;
-    CUtensorMap m[3];  // q, k, v
+    CUtensorMap m[4];  // q, k, v, o
     const long tokens = (long)a.B * a.T;
     if (tokens == 0 && !a.hT) return cudaSuccess;
     const void* some = a.hT;  // nothing to load: the maps are never used
     if (!make_map(m, tokens ? a.q : some, tokens ? tokens : 1, a.Hk, a.K) ||
         !make_map(m + 1, tokens ? a.k : some, tokens ? tokens : 1, a.Hk, a.K) ||
-        !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V))
+        !make_map(m + 2, tokens ? a.v : some, tokens ? tokens : 1, a.H, a.V) ||
+        !make_map(m + 3, tokens ? a.o : some, tokens ? tokens : 1, a.H, a.V))
         return cudaErrorInvalidValue;
     const int vblocks = (a.V + VB - 1) / VB;
     const Plan pl = plan(a.B, a.T, a.H, a.K, a.V, a.cu != nullptr);
@@ -1035,7 +1059,7 @@ cudaError_t launch_delta_tensor(const DeltaArgs& a) {
     cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e == cudaSuccess && pl.per) e = cudaMemsetAsync(cuts, 0, pl.counters, a.stream);
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<<<pl.per ? dim3(pl.pieces) : dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], p);
+    delta_chunk_kernel<<<pl.per ? dim3(pl.pieces) : dim3(a.H, vblocks, a.N), NTHR, SMEM_BYTES, a.stream>>>(m[0], m[1], m[2], m[3], p);
     return cudaGetLastError();
 }
 
