@@ -57,17 +57,32 @@ __device__ __forceinline__ void load4(const T* row, int c, int n, float (&r)[4])
         for (int e = 0; e < 4; ++e) r[e] = c + e < n ? to_f32(row[c + e]) : 0.f;
     }
 }
-// [64 rows][nc channels from c0], transposed: lanes are rows, so that the stores meet no bank twice
-template <typename T>
-__device__ __forceinline__ void load_transposed(const T* base, size_t stride, int len, int c0, int nc, int n, float* out) {
-    for (int x = threadIdx.x; x < C * (nc / 4); x += NT) {
-        const int i = x & 63, c = 4 * (x >> 6);
-        float r[4] = {0.f, 0.f, 0.f, 0.f};
-        if (i < len) load4(base + i * stride, c0 + c, n, r);
+// A thread's share of a [64 rows][NC channels from c0] tile: asked for as it lies in memory, put down transposed.  A warp
+// has eight rows and sixteen channels at a time: whole sectors of few lines (a row a lane read 32 lines a load), and no
+// more than two stores to a bank.
+template <typename T, int NC>
+struct Tile {
+    static constexpr int N = NC / 16;
+    static_assert(NT == 4 * C, "");
+    float r[N][4];
+    static __device__ __forceinline__ int row() { return (threadIdx.x & 7) + 8 * (threadIdx.x >> 5); }
+    static __device__ __forceinline__ int channel(int x) { return 4 * (threadIdx.x >> 3 & 3) + 16 * x; }
+    __device__ __forceinline__ void fetch(const T* base, size_t stride, int len, int n, int c0 = 0) {
+        const int i = row();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[(c + e) * LD + i] = r[e];
+        for (int x = 0; x < N; ++x) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[x][e] = 0.f;
+            if (i < len) load4(base + i * stride, c0 + channel(x), n, r[x]);
+        }
     }
-}
+    __device__ __forceinline__ void put(float* out) const {
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[(channel(x) + e) * LD + row()] = r[x][e];
+    }
+};
 
 // X = (1 + A)^-1 of a strictly lower triangular 64 x 64 matrix, by all threads; Y: 32 x 33 floats between.  The diagonal
 // blocks of 16 by substitution, a column a thread, then twice the block below two inverted ones: -X22 (A21 X11).
@@ -138,9 +153,12 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q,
     const T* qb = q + ((size_t)t0 * Hk + hq) * p.K;
     float kk[4][4] = {}, qk[4][4] = {}, nq = 0.f;
     for (int c0 = 0; c0 < p.K; c0 += 64) {
+        Tile<T, C> tk, tq;
+        tk.fetch(kb, (size_t)Hk * p.K, len, p.K, c0);
+        tq.fetch(qb, (size_t)Hk * p.K, len, p.K, c0);
         __syncthreads();
-        load_transposed(kb, (size_t)Hk * p.K, len, c0, 64, p.K, sk);
-        load_transposed(qb, (size_t)Hk * p.K, len, c0, 64, p.K, sq);
+        tk.put(sk);
+        tq.put(sq);
         __syncthreads();
 #pragma unroll 4
         for (int c = 0; c < 64; ++c) {
@@ -216,13 +234,18 @@ __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
     }
 }
 
-// grid (V blocks, H, sequences).  A thread has four rows of a chunk and W of the block's VB = 16 W columns.
-template <typename T, typename OT, int W>
+// grid (V blocks, H, sequences).  A thread has four rows of a chunk and W of the block's VB = 16 W columns.  Kp: K rounded
+// up to 64, 128 or 256.  The next chunk is on its way into registers while this one is worked on.
+//
+// Shared memory bounds it: with few columns a thread, a multiply-add costs about half a wavefront of it (W = 1: 18 k of a
+// chunk's 21 k clocks), and one block of eight warps has an SM's space.  Times of a call (heads of 128 x 128): 16384 tokens,
+// 8 heads 2.83 ms (each chunk fetched when its turn came: 4.83); 2048 tokens, 64 heads 1.05 ms (1.54), of which 0.20 the
+// first kernel; 128 tokens, 2 heads of 64 x 64, 31 us (39).  Of bf16 heads of 256 x 256, 2 x 2048 tokens, 32 heads: 3.9 ms (4.7).
+template <typename T, typename OT, int W, int Kp>
 __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                         const T* __restrict__ v, OT* __restrict__ o, Args p) {
+                                                         const T* __restrict__ v, OT* o, Args p) {
     constexpr int VB = 16 * W;
     extern __shared__ __align__(16) float sm[];
-    const int Kp = (p.K + 63) / 64 * 64;
     float* sk = sm;               // [Kp][LD] k, transposed
     float* sq = sk + Kp * LD;     // [Kp][LD] q
     float* st = sq + Kp * LD;     // [64][LD] T, transposed
@@ -243,24 +266,41 @@ __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q
         const int c = x / VB, d = v0 + x % VB;
         sS[x] = p.h0 && c < p.K && d < p.V ? p.h0[state + (size_t)c * p.V + d] : 0.f;
     }
-    for (int t0 = bos; t0 < eos; t0 += C) {
+    Tile<T, Kp> tk, tq;
+    Tile<float, C> tt, tp;
+    float vr[4][W], factor;
+    auto fetch = [&](int t0) {
         const int len = min(C, eos - t0);
         const float* ws = p.ws + ((size_t)t0 * p.H + h) * kRow;
-        load_transposed(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sk);
-        load_transposed(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, 0, Kp, p.K, sq);
-        load_transposed(ws, (size_t)p.H * kRow, len, 0, C, C, st);
-        load_transposed(ws + C, (size_t)p.H * kRow, len, 0, C, C, sp);
-        sf[tid] = (tid >> 2) < len ? ws[(size_t)(tid >> 2) * p.H * kRow + kFactors + (tid & 3)] : 0.f;
-        float vr[4][W];
+        tk.fetch(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, p.K);
+        tq.fetch(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, p.K);
+        tt.fetch(ws, (size_t)p.H * kRow, len, C);
+        tp.fetch(ws + C, (size_t)p.H * kRow, len, C);
+        factor = (tid >> 2) < len ? ws[(size_t)(tid >> 2) * p.H * kRow + kFactors + (tid & 3)] : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < W; ++e)
                 vr[i][e] = 4 * ti + i < len && col + e < p.V ? to_f32(v[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e]) : 0.f;
+    };
+    if (bos < eos) fetch(bos);
+    for (int t0 = bos; t0 < eos; t0 += C) {
+        const int len = min(C, eos - t0);
+        tk.put(sk);
+        tq.put(sq);
+        tt.put(st);
+        tp.put(sp);
+        sf[tid] = factor;
+        float vv[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) vv[i][e] = vr[i][e];
+        if (t0 + C < eos) fetch(t0 + C);
         __syncthreads();
         float y[4][W] = {}, acc[4][W] = {};
-#pragma unroll 4
-        for (int c = 0; c < p.K; ++c) {
+#pragma unroll 8
+        for (int c = 0; c < Kp; ++c) {
             const float4 a = *reinterpret_cast<const float4*>(sk + c * LD + 4 * ti);
             const float4 b = *reinterpret_cast<const float4*>(sq + c * LD + 4 * ti);
             float s[W];
@@ -281,24 +321,26 @@ __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                sr[(4 * ti + i) * VB + W * tj + e] = fmaf(-sf[4 * (4 * ti + i)], y[i][e], vr[i][e]);
+                sr[(4 * ti + i) * VB + W * tj + e] = fmaf(-sf[4 * (4 * ti + i)], y[i][e], vv[i][e]);
                 acc[i][e] *= sf[4 * (4 * ti + i) + 1];
                 y[i][e] = 0.f;
             }
         __syncthreads();
         auto lower = [&](const float* M, const float* B, float (&r)[4][W]) {  // r_i += sum_{j <= i} M_ij B_j
-            for (int j = 0; j < 4 * ti; ++j) {
-                const float4 a = *reinterpret_cast<const float4*>(M + j * LD + 4 * ti);
-                float b[W];
-                lds_row<W>(B + j * VB + W * tj, b);
+            for (int j0 = 0; j0 < 4 * ti; j0 += 4)
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    r[0][e] = fmaf(a.x, b[e], r[0][e]);
-                    r[1][e] = fmaf(a.y, b[e], r[1][e]);
-                    r[2][e] = fmaf(a.z, b[e], r[2][e]);
-                    r[3][e] = fmaf(a.w, b[e], r[3][e]);
+                for (int j = j0; j < j0 + 4; ++j) {
+                    const float4 a = *reinterpret_cast<const float4*>(M + j * LD + 4 * ti);
+                    float b[W];
+                    lds_row<W>(B + j * VB + W * tj, b);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        r[0][e] = fmaf(a.x, b[e], r[0][e]);
+                        r[1][e] = fmaf(a.y, b[e], r[1][e]);
+                        r[2][e] = fmaf(a.z, b[e], r[2][e]);
+                        r[3][e] = fmaf(a.w, b[e], r[3][e]);
+                    }
                 }
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float b[W];
@@ -363,16 +405,18 @@ __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q
     }
 }
 
-template <typename T, typename OT, int W>
-cudaError_t run_chain(const DeltaArgs& a, const Args& p) {
-    constexpr int VB = 16 * W;
-    const int Kp = (a.K + 63) / 64 * 64;
-    const int bytes = (2 * Kp * LD + 2 * C * LD + Kp * VB + 3 * C * VB + 4 * C) * (int)sizeof(float);
-    auto kern = delta_chain_kernel<T, OT, W>;
+template <typename T, typename OT, int W, int Kp>
+cudaError_t run_chain_k(const DeltaArgs& a, const Args& p) {
+    constexpr int VB = 16 * W, bytes = (2 * Kp * LD + 2 * C * LD + Kp * VB + 3 * C * VB + 4 * C) * (int)sizeof(float);
+    auto kern = delta_chain_kernel<T, OT, W, Kp>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kern<<<dim3((a.V + VB - 1) / VB, a.H, a.N), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
     return cudaGetLastError();
+}
+template <typename T, typename OT, int W>
+cudaError_t run_chain(const DeltaArgs& a, const Args& p) {
+    return a.K <= 64 ? run_chain_k<T, OT, W, 64>(a, p) : a.K <= 128 ? run_chain_k<T, OT, W, 128>(a, p) : run_chain_k<T, OT, W, 256>(a, p);
 }
 
 template <typename T, typename OT>
