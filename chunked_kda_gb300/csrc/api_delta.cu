@@ -62,6 +62,8 @@ kda_status check_delta(const void* q, const void* k, const void* v, kda_dtype qk
     const kda_status st = kda::check_sequences(cu, n_seqs, B, T, H, N);
     if (st != KDA_OK) return st;
     if (H > 65535) return fail(KDA_ERR_INVALID_ARG, "H must be <= 65535");
+    // (a chunk's rows, and those asked for ahead, are counted in 32 bits past the last token)
+    if ((long long)B * T > (1ll << 31) - 256) return fail(KDA_ERR_INVALID_ARG, "B * T must be at most 2^31 - 256");
     if (!dtype_ok(qkv_dtype)) return fail(KDA_ERR_UNSUPPORTED, "qkv dtype");
     if (!dtype_ok(g_dtype)) return fail(KDA_ERR_UNSUPPORTED, "g dtype");
     if (beta_dtype != qkv_dtype && beta_dtype != KDA_F32)

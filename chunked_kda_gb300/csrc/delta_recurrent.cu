@@ -40,7 +40,7 @@ constexpr int kPart = 4 * NT;           // partial S^T k, then S^T q, a row of a
 template <typename InT, typename OutT>
 __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
     const InT* __restrict__ q, const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags,
-    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, int* status, OutT* o) {
+    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o) {
     extern __shared__ __align__(128) float sm[];  // [K][BV] the state, then the partial products
     __shared__ float s_q[256], s_k[256], s_dot[3][8];
     __shared__ __align__(8) uint64_t s_bar;
@@ -76,9 +76,9 @@ __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
     const float scale = rsqrtf((float)K);
     bool waiting = h0 != nullptr;
     auto state_here = [&] {
-        if (waiting && !mbar_wait(bar, 0) && tid == 0) {
-            atomicAdd(&g_token_timeouts, 1u);
-            if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
+        if (waiting && !mbar_wait(bar, 0)) {
+            if (tid == 0) atomicAdd(&g_token_timeouts, 1u);
+            mbar_wait(bar, 0);  // (once more: no copy is to be in flight when the block ends)
         }
         waiting = false;
     };
@@ -297,7 +297,7 @@ cudaError_t launch_k(const DeltaArgs& a) {
         if (e != cudaSuccess) return e;
         kern<<<dim3((a.V + BV - 1) / BV, a.H, a.N), NT, bytes, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a),
                                                                          a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV,
-                                                                         a.status, (OutT*)a.o);
+                                                                         (OutT*)a.o);
         return cudaGetLastError();
     }
     return a.K <= 64 ? launch_r<InT, OutT, 4>(a) : a.K <= 128 ? launch_r<InT, OutT, 8>(a) : launch_r<InT, OutT, 16>(a);

@@ -439,12 +439,18 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  *     A_ij = beta_i exp(G_i - G_j) k_i . k_j (j < i),   U = (1 + A)^-1 diag(beta) (V - diag(e^G) K S)
  *     O = ( diag(e^G) Q S + (exp(G_i - G_j) q_i . k_j)_{j <= i} U ) / sqrt(K)
  *     S <- e^G_l S + K^T diag(e^(G_l - G)) U
- * Its scratch is kda_delta_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for dense
- * inputs); status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the form for single tokens
- * and computes token by token in FP32.
+ * bf16 inputs with bf16 output, K <= 128 and K and V multiples of 8 run on the tensor cores: the
+ * state, and what leads to it, has FP32's 24 bits; the bf16 output is formed from the state's and P's
+ * rounding to 8 and 11 bits and is off by about 1.1 times its own rounding.  All else, float32 output
+ * of bf16 inputs among it, is computed in FP32.  Scratch is kda_delta_chunk_workspace_bytes (256-byte
+ * aligned, NULL when 0; n_seqs 0 for dense inputs): 528 bytes a token and head in FP32; on the tensor
+ * cores a state for each sequence and head where they do not fill the multiprocessors evenly, else
+ * none.  It is one call's at a time.  status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the
+ * form for single tokens and computes token by token in FP32.
  *
- * What is not finite never reaches back: a gate, beta or key that is not finite reaches the outputs
- * of its head from its token on, a value those of its channel.
+ * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is not
+ * finite (with KDA_FLAG_K_L2NORM, a key whose sum of squares is not) reaches the outputs of its head
+ * from its token on, a value those of its channel, a query its own row.
  */
 size_t kda_delta_chunk_workspace_bytes(kda_dtype qkv_dtype, kda_dtype o_dtype, int B, int T, int H,
                                        int K, int V, int n_seqs);
@@ -553,8 +559,8 @@ kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weigh
 
 /*
  * Diagnostics of the tensor-core paths' bounded waits.  Every mbarrier wait of the fused
- * and two-pass chunked kernels, of the chunked decayed attention and of the block norm of many
- * long rows gives up after a fixed number of polls; a CTA whose wait gave
+ * and two-pass chunked kernels, of the chunked decayed attention, of the gated delta rule in both
+ * forms and of the block norm of many long rows gives up after a fixed number of polls; a CTA whose wait gave
  * up adds to a per-device counter, stops waiting, issuing MMAs and copies, lets the ones in
  * flight finish (bounded), frees its TMEM and returns, so the context stays usable but that
  * launch's outputs are not valid.  kda_fused_wait_timeouts writes the counters of the current
@@ -567,13 +573,14 @@ kda_status kda_fused_wait_timeouts(unsigned int* count, int reset);
 /*
  * Test hooks of the tensor-core paths, process-wide, all off by default and read by nothing
  * else (no environment variables).  For tests only; set them back to (-1, 0, 0, 0) afterwards.
- *   wait_timeout_chunk  >= 0: every CTA of later fused launches and of the two-pass state
- *                       chain waits, at that chunk and with a short limit, on an mbarrier
+ *   wait_timeout_chunk  >= 0: every CTA of later fused launches, of the two-pass state
+ *                       chain and of the chunked gated delta rule on the tensor cores waits, at that chunk and with a short limit, on an mbarrier
  *                       nothing completes, and takes the give-up path (counted by
  *                       kda_fused_wait_timeouts, flagged in the status word of
  *                       kda_chunk_fwd_ex); -1: off
- *   sm_count            > 0: plan the fused split schedule (kda_chunk_fwd_launches) and the
- *                       two-pass state chain's balanced schedule (kda_chunk_fwd) for this
+ *   sm_count            > 0: plan the fused split schedule (kda_chunk_fwd_launches), the
+ *                       two-pass state chain's balanced schedule (kda_chunk_fwd) and the cut units of
+ *                       kda_decay_chunk_fwd and kda_delta_chunk_fwd for this
  *                       many SMs instead of the device's (a chain plan for more SMs than the
  *                       device has runs one CTA per unit); 0: the device's
  *   one_launch          nonzero: never split a fused call into two launches, and run the

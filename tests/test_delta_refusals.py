@@ -54,6 +54,15 @@ def test_delta_refusals(lib, chunk, kw, code):
     assert lib.kda_last_error()
 
 
+@pytest.mark.parametrize("chunk", [False, True])
+def test_tokens_that_a_chunk_counts_past_32_bits(lib, chunk):
+    # K = V = 8 and one head: such tensors fit the memory, a chunk's row numbers would not fit 32 bits
+    far = dict(K=8, V=8, H=1, q=1 << 44, k=1 << 45, v=1 << 46, o=1 << 47, g=1 << 48, beta=1 << 49)
+    assert delta(lib, chunk, T=(1 << 31) - 255, **far) == INVALID
+    assert b"2^31 - 256" in lib.kda_last_error()
+    assert delta(lib, chunk, T=(1 << 31) - 1, **far) == INVALID
+
+
 def test_workspace_and_status_refusals(lib):
     big = dict(dt=F32, bdt=F32, odt=F32, T=200)
     need = lib.kda_delta_chunk_workspace_bytes(F32, F32, 1, 200, 4, 64, 64, 0)
