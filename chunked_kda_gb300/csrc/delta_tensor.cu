@@ -15,7 +15,8 @@
 // Roundings.  The state is a float32 output and feeds every later chunk: what leads to it has 24 bits.  S, R, T and
 // U' are operands as three bf16 terms each (the products of R and T without the three smallest), a chunk's addition
 // is summed by itself and added to S in rounded FP32, S is held in registers between chunks.  The output is bf16:
-// O1 reads S's first term (its rounding to bf16), O2 is a tf32 product of U as it stands in TMEM (cut) and P.
+// O1 reads S's first two terms (with the first alone an output was off by up to 1.4 times its own rounding, and no call
+// was faster), O2 is a tf32 product of U as it stands in TMEM (cut) and P.
 //
 // What is not finite must not reach back through masked zeros (0 times it is NaN).  A gate, beta or key: the rows from
 // its token on are treated like rows behind the sequence, and the outputs from there on and the state are NaN.  A
@@ -25,6 +26,17 @@
 // 16-23 the preparation of the next chunk (scores, inverse), 24 all products, 25 loads, 26 gates.  Every wait is
 // bounded (a CTA that gives up lets its copies and MMAs finish, frees its TMEM and returns).  What happens rarely is
 // out of line and loops are rolled: together the roles' loops have to fit the instruction caches.
+// Dense calls whose units do not fill the SMs evenly are cut: an SM has the same number of chunks, and a unit's second
+// part takes the state over through scratch.
+//
+// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 610 us (in FP32 without tensor cores 9.6 ms);
+// 4096 tokens, 152 heads 350; 8192 tokens, 96 heads 673; 20480 tokens, 32 heads 1640 (32 SMs have a unit).  The bytes
+// alone are 160 us of the first.  A chunk is about 10,000 clocks of an SM, and the chain (S 1350, O 1600, R 2200, U
+// 700 and its wait, U' 1200, D 1300) and the preparation (scores 3300, inverse 4300, T 1200) are as long as one another.
+// What bounds it: the chain's order; shared memory (58 % of its wavefronts ordinary loads and stores, 18 % the tensor
+// cores' operands) and fetching instructions (73 % of what the second cache gives), which 27 warps of six kinds share.
+// The tensor cores are at 28 %, HBM at 20 %.  Tried and slower: the inverse on tensor cores (mma of tf32: 3530 clocks
+// against 3130 alone), polls with a time hint, outputs stored without staging, one barrier for several roles' waits.
 #include "common.cuh"
 #include "decay_gates.cuh"
 #include "delta_gates.cuh"
@@ -70,7 +82,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of a block");
 // TMEM columns: S's three terms; D, whose first half is O1's place; Y, then U; the first two terms of R, then of U'; scores, then O2
 constexpr uint32_t TS = 0, TD = 192, TO1 = 192, TY = 320, TZ = 384, TSC = 448, TCOLS = 512;
 // words of L_MISC
-enum { M_TMEM = 0, M_UNUSED, M_ABORT, M_ODD, M_BAD };  // M_ODD: bit (c & 1): marks of that chunk
+enum { M_TMEM = 0, M_ABORT, M_ODD, M_BAD };  // M_ODD: bit (c & 1): marks of that chunk
 
 struct Params {
     Gates gates;
@@ -424,14 +436,14 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {  // Y from S's terms 2, 1, 0, then O1 from term 0
-                        const uint32_t to = tmem + (x < 3 ? TY : TO1), from = tmem + TS + 64 * (x < 3 ? 2 - x : 0);
+                    for (int x = 0; x < 5; ++x) {  // Y from S's terms 2, 1, 0, then O1 from terms 1, 0
+                        const uint32_t to = tmem + (x < 3 ? TY : TO1), from = tmem + TS + 64 * (x < 3 ? 2 - x : 4 - x);
                         const uint32_t r = lo_k(st + (x < 3 ? 0 : QROWS));
 #pragma unroll
                         for (int kk = 0; kk < KD / 16; ++kk)
                             umma_bf16_ta(to, from + 8 * kk, desc(r + (kk >> 2) * (PANEL >> 4) + (kk & 3) * 2), idesc_bf16(128, 64, 0, 0),
                                          (x != 0 && x != 3) || kk > 0);
-                        if (x >= 2) umma_commit(sy.bar(x == 2 ? B_Y : B_O1));
+                        if (x == 2 || x == 4) umma_commit(sy.bar(x == 2 ? B_Y : B_O1));
                     }
                 }
                 __syncwarp();

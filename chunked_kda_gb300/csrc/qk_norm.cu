@@ -14,7 +14,11 @@
 // its pairs lie in one lane (two loads of four elements, R / 2 apart, or one of eight), and LPR lanes share a row.  The
 // next U rows of a lane are on their way while it works on U.
 //
-// Memory bounds it: each row goes in and out once.
+// Memory bounds it: each row goes in and out once.  16384 tokens with 64 + 8 heads of 128, RMS norm, rotation: 604 MB in
+// 112 us, 5.4 TB/s (angles formed in FP32 for each row, no loads ahead: 260); 20480 tokens with 32 heads, L2 norm, no
+// rotation: 60 us, 5.6 TB/s.  U: 1, 2, 3, 4 give 124, 111, 126 and 129 us of the first, 72, 60, 62 and 60 of the second.
+// What is missing to a copy's 6.8 TB/s is a row's way from its load through the sum's shuffles to its store, and in the
+// first the angles in front of a block's rows.
 #include "common.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"

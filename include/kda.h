@@ -440,8 +440,8 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  *     O = ( diag(e^G) Q S + (exp(G_i - G_j) q_i . k_j)_{j <= i} U ) / sqrt(K)
  *     S <- e^G_l S + K^T diag(e^(G_l - G)) U
  * bf16 inputs with bf16 output, K <= 128 and K and V multiples of 8 run on the tensor cores: the
- * state, and what leads to it, has FP32's 24 bits; the bf16 output is formed from the state's and P's
- * rounding to 8 and 11 bits and is off by about 1.1 times its own rounding.  All else, float32 output
+ * state, and what leads to it, has FP32's 24 bits; the bf16 output is formed from the state's first 16
+ * bits and 11 bits of P, far below its own rounding.  All else, float32 output
  * of bf16 inputs among it, is computed in FP32.  Scratch is kda_delta_chunk_workspace_bytes (256-byte
  * aligned, NULL when 0; n_seqs 0 for dense inputs): 528 bytes a token and head in FP32; on the tensor
  * cores a state for each sequence and head where they do not fill the multiprocessors evenly, else
