@@ -177,7 +177,7 @@ kda_status kda_test_hooks(int wait_timeout_chunk, int sm_count, int one_launch, 
 kda_status kda_fused_wait_timeouts(unsigned int* count, int reset) {
     g_last_error.clear();
     if (!count) return fail(KDA_ERR_INVALID_ARG, "null count");
-    unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0;
     kda_status st = cuda_status(kda::read_fused_timeouts(&a, reset != 0));
     if (st != KDA_OK) return st;
     st = cuda_status(kda::read_twopass_timeouts(&b, reset != 0));
@@ -189,7 +189,9 @@ kda_status kda_fused_wait_timeouts(unsigned int* count, int reset) {
     st = cuda_status(kda::read_delta_timeouts(&f, reset != 0));
     if (st != KDA_OK) return st;
     st = cuda_status(kda::read_token_timeouts(&g, reset != 0));
-    *count = a + b + c + d + f + g;
+    if (st != KDA_OK) return st;
+    st = cuda_status(kda::read_rope_timeouts(&h, reset != 0));
+    *count = a + b + c + d + f + g + h;
     return st;
 }
 

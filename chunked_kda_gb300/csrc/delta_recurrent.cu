@@ -32,11 +32,6 @@ using namespace sm100;
 
 __device__ unsigned int g_token_timeouts = 0;
 
-// bytes of shared memory behind which a bulk copy takes them to global memory (16-byte aligned, a multiple of 16)
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-
 constexpr int NT = 256, kTile = 16384;  // floats of a block's state
 constexpr int kPart = 4 * NT;           // partial S^T k, then S^T q, a row of a block's columns for each group of threads
 

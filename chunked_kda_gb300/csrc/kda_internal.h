@@ -218,6 +218,7 @@ size_t delta_tensor_workspace_bytes(int B, int T, int H, int K, int V, bool pack
 cudaError_t launch_delta_tensor(const DeltaArgs& a);
 cudaError_t read_delta_timeouts(unsigned* count, bool reset);
 cudaError_t read_token_timeouts(unsigned* count, bool reset);
+cudaError_t read_rope_timeouts(unsigned* count, bool reset);
 // its FP32 kernels: any dtype, any K and V up to 256
 size_t delta_simt_workspace_bytes(int B, int T, int H);
 cudaError_t launch_delta_simt(const DeltaArgs& a);

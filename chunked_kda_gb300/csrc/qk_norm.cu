@@ -9,16 +9,12 @@
 // fraction (integer product of f's 24 bits and 2^64 / 2 pi), and p times it modulo 2^64 is exact.  So an angle is off by
 // p f 2^-65 turns however far the position; a float32 product is off by 0.06 radians at 10^6.
 //
-// A block has `tile` consecutive tokens with all their heads: the angles' cosines and sines are formed once a token,
-// in shared memory, while the first rows are on their way.  A lane has four pairs: a row is split so that both halves of
-// its pairs lie in one lane (two loads of four elements, R / 2 apart, or one of eight), and LPR lanes share a row.  The
-// next U rows of a lane are on their way while it works on U.
+// A row is split between lanes so that both elements of a pair lie in one lane (two pieces of a row, R / 2 apart, or one
+// behind another), and LPR lanes share a row.
 //
 // Memory bounds it: each row goes in and out once.  16384 tokens with 64 + 8 heads of 128, RMS norm, rotation: 604 MB in
-// 112 us, 5.4 TB/s (angles formed in FP32 for each row, no loads ahead: 260); 20480 tokens with 32 heads, L2 norm, no
-// rotation: 60 us, 5.6 TB/s.  U: 1, 2, 3, 4 give 124, 111, 126 and 129 us of the first, 72, 60, 62 and 60 of the second.
-// What is missing to a copy's 6.8 TB/s is a row's way from its load through the sum's shuffles to its store, and in the
-// first the angles in front of a block's rows.
+// 101 us, 6.0 TB/s (with angles formed in FP32 for each row and no loads ahead: 260); 20480 tokens with 32 heads, L2 norm,
+// no rotation: 57 us, 5.9 TB/s.  Three kernels: many rows, few rows, and any D, R and alignment.
 #include "common.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
@@ -28,6 +24,8 @@ namespace kda {
 namespace {
 
 constexpr int NT = 256, kMaxD = 256;
+constexpr int kRingStage = 2048, kRingStages = 3, kRingBlocks = 2;  // bytes of a warp's stage, stages, blocks an SM
+__device__ unsigned g_rope_timeouts = 0;
 
 struct Axes {  // the axis of each pair, two bits a pair
     uint32_t bits[kMaxD / 2 / 16];
@@ -41,7 +39,7 @@ struct Params {
     int Hq, heads;      // query heads, all heads
     uint32_t per;       // ceil(2^32 / heads), 0: one head
     int norm;
-    float eps;
+    float eps, per_sum;  // 1 / D of a mean, else 1
     const int32_t* pos;
     const float* freq;
     Axes axes;
@@ -49,6 +47,8 @@ struct Params {
     float m;
     long tokens;
     int tile;
+    // the ring's groups: rows of one, groups of a token's queries, of a token
+    int G, q_groups, per_token;
 };
 
 // cosine and sine of pair i at token t, times m
@@ -81,6 +81,15 @@ struct Four<__nv_bfloat16> {
         b = make_float2(sm100::bf_lo(v.y), sm100::bf_hi(v.y));
     }
     static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_uint2(sm100::pack_bf16(a.x, a.y), sm100::pack_bf16(b.x, b.y)); }
+    static __device__ __forceinline__ void load8(const __nv_bfloat16* x, float2* v) {
+        const uint4 r = *reinterpret_cast<const uint4*>(x);
+        unpack(make_uint2(r.x, r.y), v[0], v[1]);
+        unpack(make_uint2(r.z, r.w), v[2], v[3]);
+    }
+    static __device__ __forceinline__ void store8(__nv_bfloat16* y, const float2* v) {
+        const uint2 a = pack(v[0], v[1]), b = pack(v[2], v[3]);
+        *reinterpret_cast<uint4*>(y) = make_uint4(a.x, a.y, b.x, b.y);
+    }
 };
 template <>
 struct Four<float> {
@@ -90,13 +99,63 @@ struct Four<float> {
         b = make_float2(v.z, v.w);
     }
     static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
+    static __device__ __forceinline__ void load8(const float* x, float2* v) {
+        unpack(reinterpret_cast<const float4*>(x)[0], v[0], v[1]);
+        unpack(reinterpret_cast<const float4*>(x)[1], v[2], v[3]);
+    }
+    static __device__ __forceinline__ void store8(float* y, const float2* v) {
+        reinterpret_cast<float4*>(y)[0] = pack(v[0], v[1]);
+        reinterpret_cast<float4*>(y)[1] = pack(v[2], v[3]);
+    }
 };
 
 __device__ __forceinline__ float factor(const Params& p, float sum) {
-    return p.norm == KDA_NORM_NONE ? 1.f : rsqrtf((p.norm == KDA_NORM_RMS ? sum / (float)p.D : sum) + p.eps);
+    return p.norm == KDA_NORM_NONE ? 1.f : rsqrtf(fmaf(sum, p.per_sum, p.eps));
 }
 
-// D and R multiples of 8, rows 16-byte aligned.  LPR: lanes a row, D / 8 rounded up to a power of 2.
+__device__ __forceinline__ void load_weights(const float* wa, const float* wb, float2 (&w)[4]) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(wa)), y = __ldg(reinterpret_cast<const float4*>(wb));
+    w[0] = make_float2(x.x, x.y);
+    w[1] = make_float2(x.z, x.w);
+    w[2] = make_float2(y.x, y.y);
+    w[3] = make_float2(y.z, y.w);
+}
+
+// A lane's four pairs: the norm's factor, the weights, the rotation.  turns: cosines, R / 2 further sines, as far again
+// the sines' negatives, of the lane's first pair.
+__device__ __forceinline__ void finish(const Params& p, float f, bool weighted, const float2 (&w)[4], bool rot, const float* turns, float2 (&v)[4]) {
+    using decay::fma2;
+    using decay::mul2;
+    const float2 ff = make_float2(f, f);
+    if (weighted) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], mul2(ff, w[e]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], ff);
+    }
+    if (!rot) return;
+    const int half = p.R / 2;
+    const float4 c = *reinterpret_cast<const float4*>(turns), s = *reinterpret_cast<const float4*>(turns + half);
+    if (p.interleaved) {
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = make_float2(v[e].x * cc[e] - v[e].y * ss[e], v[e].y * cc[e] + v[e].x * ss[e]);
+    } else {
+        const float4 n = *reinterpret_cast<const float4*>(turns + 2 * half);
+        const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
+        const float2 a0 = fma2(v[0], c0, mul2(v[2], make_float2(n.x, n.y))), a1 = fma2(v[1], c1, mul2(v[3], make_float2(n.z, n.w)));
+        v[2] = fma2(v[2], c0, mul2(v[0], make_float2(s.x, s.y)));
+        v[3] = fma2(v[3], c1, mul2(v[1], make_float2(s.z, s.w)));
+        v[0] = a0;
+        v[1] = a1;
+    }
+}
+
+// Few rows, or D and R multiples of 8 but not of 16; 16-byte aligned.  A block has `tile` consecutive tokens with all their
+// heads: the angles' cosines and sines are formed once a token, in shared memory, while the first rows are on their way.  A
+// lane has four pairs, LPR lanes a row (D / 8 rounded up to a power of 2).  The next U rows of a lane are on their way while it
+// works on U (U: 1, 2, 3, 4 gave 124, 111, 126 and 129 us for 16384 tokens with 72 heads).
 template <typename T, int LPR>
 __global__ void __launch_bounds__(NT, 3) qk_norm_rope_kernel(const __grid_constant__ Params p) {
     using decay::fma2;
@@ -169,42 +228,190 @@ __global__ void __launch_bounds__(NT, 3) qk_norm_rope_kernel(const __grid_consta
             if (r < rows && on) {
                 int tt, side, at;
                 where(r, tt, side, at);
-                const float f = factor(p, sum);
-                const float2 ff = make_float2(f, f);
                 const float* w = side ? p.w[1] : p.w[0];
-                if (w) {
-                    const float4 wa = __ldg(reinterpret_cast<const float4*>(w + a)), wb = __ldg(reinterpret_cast<const float4*>(w + b));
-                    v[0] = mul2(v[0], mul2(ff, make_float2(wa.x, wa.y)));
-                    v[1] = mul2(v[1], mul2(ff, make_float2(wa.z, wa.w)));
-                    v[2] = mul2(v[2], mul2(ff, make_float2(wb.x, wb.y)));
-                    v[3] = mul2(v[3], mul2(ff, make_float2(wb.z, wb.w)));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], ff);
-                }
-                if (rot) {
-                    const float* from = s_turn + tt * 3 * half + i;
-                    const float4 c = *reinterpret_cast<const float4*>(from), s = *reinterpret_cast<const float4*>(from + half);
-                    if (p.interleaved) {
-                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = make_float2(v[e].x * cc[e] - v[e].y * ss[e], v[e].y * cc[e] + v[e].x * ss[e]);
-                    } else {
-                        const float4 n = *reinterpret_cast<const float4*>(from + 2 * half);
-                        const float2 c0 = make_float2(c.x, c.y), c1 = make_float2(c.z, c.w);
-                        const float2 a0 = fma2(v[0], c0, mul2(v[2], make_float2(n.x, n.y))), a1 = fma2(v[1], c1, mul2(v[3], make_float2(n.z, n.w)));
-                        v[2] = fma2(v[2], c0, mul2(v[0], make_float2(s.x, s.y)));
-                        v[3] = fma2(v[3], c1, mul2(v[1], make_float2(s.z, s.w)));
-                        v[0] = a0;
-                        v[1] = a1;
-                    }
-                }
+                float2 wv[4];
+                if (w) load_weights(w + a, w + b, wv);
+                finish(p, factor(p, sum), w != nullptr, wv, rot, s_turn + tt * 3 * half + i, v);
                 T* dst = (side ? yk : yq) + (at + tt * (int)(side ? p.ys[1] : p.ys[0]));
                 __stcs(reinterpret_cast<typename F::Raw*>(dst + a), F::pack(v[0], v[1]));
                 __stcs(reinterpret_cast<typename F::Raw*>(dst + b), F::pack(v[2], v[3]));
             }
         }
     }
+}
+
+// Many rows, D and R multiples of 16, 16-byte aligned.  A warp has an even share of all groups (up to p.G rows of one token
+// and side, one behind another) and a ring of their stages in shared memory, which bulk copies fill and empty; it forms
+// the angles of each of its tokens for itself and meets no other warp.  A lane has eight pairs of a row, LPR lanes a row (D / 16
+// rounded up to a power of 2), so that a warp works on few rows at a time and a token's angles stay in registers.
+// Three stages of 2 KB for 16 warps an SM: 101 us (16384 tokens, 72 heads, rotation) and 57 us (20480, 32, none); two stages
+// 121 and 66, four 101 and 60, six 102 and 63 (more copies under way disturb the stores), three of 4 KB 110 and 61,
+// 24 warps with four 130 and 58.
+template <typename T, int LPR>
+__global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(const __grid_constant__ Params p) {
+    using decay::fma2;
+    using decay::mul2;
+    using F = Four<T>;
+    constexpr int W = NT / 32, RP = 32 / LPR;  // rows at a time
+    extern __shared__ __align__(128) float sm[];
+    __shared__ __align__(8) uint64_t s_full[W][kRingStages];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, half = p.R / 2;
+    float* turns = sm + w * (kRingStages * kRingStage / 4 + 2 * half);  // cosines, sines of a token
+    uint8_t* ring = reinterpret_cast<uint8_t*>(turns + 2 * half);
+    const uint32_t bars = sm100::smem_u32(s_full[w]), to = sm100::smem_u32(ring);
+    if (lane == 0) {
+        for (int s = 0; s < kRingStages; ++s) sm100::mbar_init(bars + 8 * s, 1);
+        sm100::fence_mbar_init();
+    }
+    __syncwarp();
+    const long warps = (long)gridDim.x * W, me = (long)blockIdx.x * W + w;
+    const long all = p.tokens * p.per_token, first = all * me / warps, count = all * (me + 1) / warps - first;
+    struct At {
+        long t;  // token
+        int g;   // group of the token
+    };
+    const At begin{first / p.per_token, (int)(first % p.per_token)};
+    auto next = [&](At& x) {
+        if (++x.g == p.per_token) {
+            x.g = 0;
+            ++x.t;
+        }
+    };
+    // a group's side, first element behind its token's, and rows
+    auto where = [&](At x, int& side, int& at, int& n) {
+        side = x.g >= p.q_groups;
+        const int first = (x.g - (side ? p.q_groups : 0)) * p.G, heads = side ? p.heads - p.Hq : p.Hq;
+        at = first * p.D;
+        n = min(p.G, heads - first);
+    };
+    At ahead = begin;
+    long issued = 0;
+    auto load = [&](int s) {
+        if (issued == count) return;
+        if (lane == 0) {
+            int side, at, n;
+            where(ahead, side, at, n);
+            const uint32_t bytes = n * p.D * (uint32_t)sizeof(T);
+            sm100::mbar_arrive_expect_tx(bars + 8 * s, bytes);
+            sm100::bulk_load(to + s * kRingStage, static_cast<const T*>(p.x[side]) + ahead.t * p.xs[side] + at, bytes, bars + 8 * s);
+        }
+        next(ahead);
+        ++issued;
+    };
+    for (int s = 0; s < kRingStages; ++s) load(s);
+
+    // the lane's pairs i .. i + 7: elements i and R / 2 + i behind the first half's start, or sixteen in a row
+    const int l = lane % LPR, row = lane / LPR, i = 8 * l;
+    const bool in = 2 * i < p.D, rot = i < half;
+    const int a = rot && !p.interleaved ? i : 2 * i, b = rot && !p.interleaved ? half + i : 2 * i + 8;
+    float2 co[4] = {}, si[4] = {}, ni[4] = {}, wv[8] = {};
+    At now = begin;
+    long formed = -1;  // the token whose angles are there
+    int s = 0, weights = -1;
+    uint32_t phase = 0;
+    bool gave_up = false;
+    for (long g = 0; g < count; ++g, next(now)) {
+        int side, at, n;
+        where(now, side, at, n);
+        if (half && now.t != formed) {
+            __syncwarp();
+            for (int j = lane; j < half; j += 32) {
+                const float2 z = turn(p, now.t, j);
+                turns[j] = z.x;
+                turns[half + j] = z.y;
+            }
+            formed = now.t;
+            __syncwarp();
+            if (rot)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    co[e] = *reinterpret_cast<const float2*>(turns + i + 2 * e);
+                    si[e] = *reinterpret_cast<const float2*>(turns + half + i + 2 * e);
+                    ni[e] = make_float2(-si[e].x, -si[e].y);
+                }
+        }
+        const float* wt = side ? p.w[1] : p.w[0];
+        if (wt && in && weights != side) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wv[e] = __ldg(reinterpret_cast<const float2*>(wt + a) + e);
+                wv[4 + e] = __ldg(reinterpret_cast<const float2*>(wt + b) + e);
+            }
+            weights = side;
+        }
+        if (!__all_sync(0xffffffffu, sm100::mbar_wait(bars + 8 * s, phase))) {
+            if (lane == 0) atomicAdd(&g_rope_timeouts, 1u);
+            gave_up = true;
+            break;
+        }
+        T* x = reinterpret_cast<T*>(ring + s * kRingStage);
+        for (int r0 = 0; r0 < n; r0 += RP) {
+            const bool on = r0 + row < n && in;
+            T* at_row = x + (r0 + row) * p.D;
+            float2 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = make_float2(0.f, 0.f);
+            if (on) {
+                F::load8(at_row + a, v);
+                F::load8(at_row + b, v + 4);
+            }
+            float sum = 0.f;
+            if (p.norm != KDA_NORM_NONE) {
+                float2 s2 = mul2(v[0], v[0]), s3 = mul2(v[4], v[4]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) {
+                    s2 = fma2(v[e], v[e], s2);
+                    s3 = fma2(v[4 + e], v[4 + e], s3);
+                }
+                sum = (s2.x + s2.y) + (s3.x + s3.y);
+#pragma unroll
+                for (int m = LPR / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            }
+            if (!on) continue;
+            const float f = factor(p, sum);
+            const float2 ff = make_float2(f, f);
+            if (wt) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = mul2(v[e], mul2(ff, wv[e]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = mul2(v[e], ff);
+            }
+            if (rot && !p.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 first = fma2(v[e], co[e], mul2(v[4 + e], ni[e]));
+                    v[4 + e] = fma2(v[4 + e], co[e], mul2(v[e], si[e]));
+                    v[e] = first;
+                }
+            } else if (rot) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float c = e & 1 ? co[e / 2].y : co[e / 2].x, sn = e & 1 ? si[e / 2].y : si[e / 2].x;
+                    v[e] = make_float2(v[e].x * c - v[e].y * sn, v[e].y * c + v[e].x * sn);
+                }
+            }
+            F::store8(at_row + a, v);
+            F::store8(at_row + b, v + 4);
+        }
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            sm100::bulk_store(static_cast<T*>(p.y[side]) + now.t * p.ys[side] + at, to + s * kRingStage, n * p.D * (uint32_t)sizeof(T));
+            decay::bulk_commit();
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the stage before this one has been read
+        }
+        __syncwarp();
+        if (g > 0) load(s > 0 ? s - 1 : kRingStages - 1);
+        if (++s == kRingStages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (lane == 0) decay::bulk_wait_read();
+    if (gave_up)  // the copies still in flight
+        for (long g = max(0l, issued - kRingStages); g < issued; ++g)
+            sm100::mbar_wait(bars + 8 * (uint32_t)(g % kRingStages), (uint32_t)(g / kRingStages) & 1u);
 }
 
 // Any D, R and alignment: a warp a row, a pair of single elements a lane and step.
@@ -256,6 +463,16 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(Params p) {
 }
 
 template <typename T>
+cudaError_t run_ring(const QkNormArgs& a, const Params& p, int sms) {
+    auto kern = a.D > 128 ? qk_norm_rope_ring_kernel<T, 16> : a.D > 64 ? qk_norm_rope_ring_kernel<T, 8> : qk_norm_rope_ring_kernel<T, 4>;
+    const int bytes = NT / 32 * (kRingStages * kRingStage + a.R * (int)sizeof(float));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<kRingBlocks * sms, NT, bytes, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
 cudaError_t run(const QkNormArgs& a, Params& p, bool fast) {
     const int grid = (int)((a.tokens + p.tile - 1) / p.tile), bytes = p.tile * (a.R / 2) * 3 * (int)sizeof(float);
     void (*kern)(Params) = qk_norm_rope_any_kernel<T>;
@@ -285,6 +502,7 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     }
     p.norm = a.norm;
     p.eps = a.eps;
+    p.per_sum = a.norm == KDA_NORM_RMS ? 1.f / (float)a.D : 1.f;
     p.pos = a.positions;
     p.freq = a.inv_freq;
     for (int i = 0; i < a.R / 2 && a.pair_axes; ++i) p.axes.bits[i >> 4] |= (uint32_t)a.pair_axes[i] << (2 * (i & 15));
@@ -303,7 +521,25 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     while (p.tile < 64 && p.tile * p.heads < 256 && p.tile * a.R <= 4096 && a.tokens / (2 * p.tile) >= 4 * sms && far * 2 * p.tile < (1l << 30)) p.tile *= 2;
     // r / heads for r < 2^16 rows of a block by a product (exact: r (per heads - 2^32) < 2^32)
     p.per = p.heads > 1 ? (uint32_t)(((1ull << 32) + p.heads - 1) / p.heads) : 0;
+    // Many rows: eight groups a warp, of a kilobyte or more (short ones cost a copy each).  4096 tokens, 40 heads of 128: 19 us, the
+    // few rows' kernel 20; below, fewer warps of its own have work: 1024 tokens, 40 heads: 7.8 and 7.8.
+    if (fast && a.D % 16 == 0 && a.R % 16 == 0) {
+        p.G = kRingStage / (a.D * e);
+        p.q_groups = (p.Hq + p.G - 1) / p.G;
+        p.per_token = p.q_groups + (Hk + p.G - 1) / p.G;
+        const bool ring = a.tokens * p.per_token >= 8l * kRingBlocks * (NT / 32) * sms && (long)p.heads * a.D * e >= 1024l * p.per_token;
+        if (ring) return a.bf16 ? run_ring<__nv_bfloat16>(a, p, sms) : run_ring<float>(a, p, sms);
+    }
     return a.bf16 ? run<__nv_bfloat16>(a, p, fast) : run<float>(a, p, fast);
+}
+
+cudaError_t read_rope_timeouts(unsigned* count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_rope_timeouts, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_rope_timeouts, &zero, sizeof(unsigned));
+    }
+    return e;
 }
 
 }  // namespace kda

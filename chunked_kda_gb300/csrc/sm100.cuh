@@ -320,6 +320,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+// 1-D bulk copy shared -> global, part of the thread's next bulk group (the same)
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
 
 // ---------------------------------------------------------------- layout
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile whose

@@ -493,7 +493,8 @@ typedef enum {
  *               (at least Hq D), so that both may be parts of wider rows.  q_out may be q.
  *   k, k_out    the same with Hk heads; Hk = 0: no keys (NULL)
  *               Aligned to their elements; where D and R are multiples of 8 and rows begin
- *               16-byte aligned, rows move as vectors.
+ *               16-byte aligned, rows move as vectors (many rows, where both are multiples of 16, by
+ *               bulk copies).
  *   weights     [D] float32 or NULL (= 1)
  *   positions   int32 [n_axes, tokens], n_axes from 1 to 4 (one for text; time, height and width
  *               for images and video).  R = 0: no rotation, NULL.
@@ -560,7 +561,7 @@ kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weigh
 /*
  * Diagnostics of the tensor-core paths' bounded waits.  Every mbarrier wait of the fused
  * and two-pass chunked kernels, of the chunked decayed attention, of the gated delta rule in both
- * forms and of the block norm of many long rows gives up after a fixed number of polls; a CTA whose wait gave
+ * forms, of the norm and rotation of many rows and of the block norm of many long rows gives up after a fixed number of polls; a CTA whose wait gave
  * up adds to a per-device counter, stops waiting, issuing MMAs and copies, lets the ones in
  * flight finish (bounded), frees its TMEM and returns, so the context stays usable but that
  * launch's outputs are not valid.  kda_fused_wait_timeouts writes the counters of the current
