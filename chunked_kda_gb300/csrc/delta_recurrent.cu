@@ -7,14 +7,16 @@
 //
 // Memory bounds it: the state goes in and out once.  Two kernels:
 //
-// Rows of whole vectors (V a multiple of 4): a block of 256 threads has a (sequence, head) and all rows of up to 128
-// value columns in shared memory, which bulk copies bring and take away: 64 KB a block, three blocks an SM, so that
-// 192 KB are under way without a register.  A thread has four columns and every (1024 / columns)-th row; the products
-// are joined through shared memory.  (The state in registers, with the rows split over eight warps whose sums meet at a
-// barrier before the first store: 377 us for 512 sequences of one token, 32 heads of 128 x 128; without the barrier, a
-// warp with 16 columns of all rows: 424, its rows' pieces of 64 bytes are too short.)  That call moves 2.16 GB in 316 us,
-// 6.85 TB/s, as a plain copy does.  Each further token costs a pass over shared memory (4 tokens: 736 us), so that from about
-// eight on the chunked kernels are faster (64 sequences of 16 tokens, bf16: 358, chunked 173).
+// Rows of whole vectors (V a multiple of 4): a block has a (sequence, head) and all rows of as many value columns as make
+// 64 KB, in shared memory, which one copy brings and takes away: a bulk copy where that is the whole state, else a
+// tensor map's box (a bulk copy for each row took twice the time: 256 sequences of one token, 32 heads of 128 x 256 454 us,
+// with boxes 317).  192 KB an SM are under way without a register.  A thread has four columns and every
+// (4 threads / columns)-th row; the products are joined through shared memory.  (The state in registers, with the rows split over
+// eight warps whose sums meet at a barrier before the first store: 377 us for 512 sequences of one token, 32 heads of 128 x 128;
+// without the barrier, a warp with 16 columns of all rows: 424, its rows' pieces of 64 bytes are too short.)  That call
+// moves 2.16 GB in 317 us, 6.8 TB/s, as a plain copy does; heads of 256 x 256 are at 98 % of it, 96 x 96 97, 64 x 64 91,
+// 234 x 128 89.  Each further token costs a pass over shared memory (4 tokens: 736 us), so that from about eight on the
+// chunked kernels are faster (64 sequences of 16 tokens, bf16: 358, chunked 173).
 //
 // Anything else: a warp has a block of columns with all rows in registers, RG groups of lanes with 16 rows each (K
 // rounded up to 16 RG: 64, 128 or 256, rows and columns beyond K and V masked), joined by shuffles.  Its rows begin
@@ -23,6 +25,7 @@
 #include "delta_gates.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
+#include "tile_ops.cuh"
 
 namespace kda {
 namespace delta {
@@ -32,17 +35,20 @@ using namespace sm100;
 
 __device__ unsigned int g_token_timeouts = 0;
 
-constexpr int NT = 256, kTile = 16384;  // floats of a block's state
-constexpr int kPart = 4 * NT;           // partial S^T k, then S^T q, a row of a block's columns for each group of threads
+constexpr int kTile = 16384;  // floats of a block's state, at most
 
-template <typename InT, typename OutT>
-__global__ void __launch_bounds__(NT, 3) delta_token_kernel(
-    const InT* __restrict__ q, const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags,
-    const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o) {
-    extern __shared__ __align__(128) float sm[];  // [K][BV] the state, then the partial products
-    __shared__ float s_q[256], s_k[256], s_dot[3][8];
+// BV: columns of a block.  All of V: a block's rows lie side by side; else they come and go by the tensor maps.
+template <typename InT, typename OutT, int NT>
+__global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
+    const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out, const InT* __restrict__ q,
+    const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags, const float* h0, float* hT,
+    const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o) {
+    constexpr int kPart = 4 * NT;  // partial S^T k, then S^T q, a row of a block's columns for each group of threads
+    extern __shared__ __align__(128) float sm[];  // the partial products, [K][BV] the state
+    __shared__ float s_q[256], s_k[256], s_dot[3][NT / 32];
     __shared__ __align__(8) uint64_t s_bar;
-    float* part = sm + kTile;
+    float* part = sm;
+    float* state = sm + 2 * kPart;
     const int tid = threadIdx.x, v0 = blockIdx.x * BV, h = blockIdx.y, n = blockIdx.z, cols = min(BV, V - v0);
     const uint32_t bar = smem_u32(&s_bar);
     const size_t st = ((size_t)n * H + h) * (size_t)K * V + v0;
@@ -52,23 +58,22 @@ __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
         fence_proxy_async_smem();
     }
     __syncthreads();
-    const bool whole = cols == V;  // the rows lie side by side
+    const bool whole = BV == V;
     if (h0) {
-        if (tid == 0) mbar_arrive_expect_tx(bar, 4u * K * cols);
-        __syncwarp();
-        if (whole) {
-            if (tid == 0) bulk_load(smem_u32(sm), h0 + st, 4u * K * cols, bar);
-        } else if (tid < 32) {
-            for (int r = tid; r < K; r += 32) bulk_load(smem_u32(sm + r * cols), h0 + st + (size_t)r * V, 4u * cols, bar);
+        if (tid == 0) {
+            mbar_arrive_expect_tx(bar, 4u * K * BV);  // (columns behind V count, too)
+            if (whole) bulk_load(smem_u32(state), h0 + st, 4u * K * BV, bar);
+            else tma_load_3d(smem_u32(state), &tm_in, v0, 0, n * H + h, bar);
         }
+        __syncwarp();
     } else {
-        for (int x = tid; x < K * cols; x += NT) sm[x] = 0.f;
+        for (int x = tid; x < K * BV; x += NT) state[x] = 0.f;
     }
     long bos, eos;
     if (cu) { bos = __ldg(cu + n); eos = __ldg(cu + n + 1); }
     else    { bos = (long)n * T; eos = bos + T; }
-    const int quads = cols / 4, groups = NT / quads, quad = tid % quads, group = tid / quads;
-    const bool on = group < groups;
+    const int quads = BV / 4, groups = NT / quads, quad = tid % quads, group = tid / quads;
+    const bool on = group < groups && 4 * quad < cols;
     const int Hq = H / hr, hq = h / hr;
     const Gates::Head head = gates.head(h);
     const float scale = rsqrtf((float)K);
@@ -80,28 +85,36 @@ __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
         }
         waiting = false;
     };
-    float4* S = reinterpret_cast<float4*>(sm) + quad;
+    float4* S = reinterpret_cast<float4*>(state) + quad;
     for (long t = bos; t < eos; ++t) {
         const size_t qk = ((size_t)t * Hq + hq) * K, vo = ((size_t)t * H + h) * V + v0 + 4 * quad;
-        float qv = 0.f, kv = 0.f;
-        if (tid < K) {
-            qv = to_f32(q[qk + tid]);
-            kv = to_f32(k[qk + tid]);
+        float qv[256 / NT], kv[256 / NT];
+#pragma unroll
+        for (int x = 0; x < 256 / NT; ++x) {
+            const int r = tid + x * NT;
+            qv[x] = r < K ? to_f32(q[qk + r]) : 0.f;
+            kv[x] = r < K ? to_f32(k[qk + r]) : 0.f;
         }
         float u[4] = {};
         if (on)
 #pragma unroll
             for (int j = 0; j < 4; ++j) u[j] = to_f32(v[vo + j]);
         const float dec = expf(gates.decay(t, h, head)), rate = gates.rate(t, h);
-        float dots[3] = {qv * qv, kv * kv, qv * kv};
+        float dots[3] = {};
+#pragma unroll
+        for (int x = 0; x < 256 / NT; ++x) {
+            dots[0] = fmaf(qv[x], qv[x], dots[0]);
+            dots[1] = fmaf(kv[x], kv[x], dots[1]);
+            dots[2] = fmaf(qv[x], kv[x], dots[2]);
+            s_q[tid + x * NT] = qv[x];
+            s_k[tid + x * NT] = kv[x];
+        }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) dots[e] += __shfl_xor_sync(0xffffffffu, dots[e], m);
             if ((tid & 31) == 0) s_dot[e][tid >> 5] = dots[e];
         }
-        s_q[tid] = qv;
-        s_k[tid] = kv;
         state_here();
         __syncthreads();
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
 #pragma unroll
             for (int e = 0; e < 3; ++e)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) d[e] += s_dot[e][x];
+                for (int x = 0; x < NT / 32; ++x) d[e] += s_dot[e][x];
             const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(d[0] + kQNormEps) : 1.f;
             const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(d[1] + kQNormEps) : 1.f;
             auto total = [&](const float* from) {
@@ -168,13 +181,11 @@ __global__ void __launch_bounds__(NT, 3) delta_token_kernel(
     fence_proxy_async_smem();
     __syncthreads();
     // (this block has read its part of h0 and no other touches it: hT may be h0)
-    if (tid < 32) {
-        if (whole) {
-            if (tid == 0) bulk_store(hT + st, smem_u32(sm), 4u * K * cols);
-        } else {
-            for (int r = tid; r < K; r += 32) bulk_store(hT + st + (size_t)r * V, smem_u32(sm + r * cols), 4u * cols);
-        }
-        asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (tid == 0) {
+        if (whole) bulk_store(hT + st, smem_u32(state), 4u * K * BV);
+        else decay::tma_store_3d(&tm_out, smem_u32(state), v0, 0, n * H + h);
+        decay::bulk_commit();
+        decay::bulk_wait_read();
     }
 }
 
@@ -286,17 +297,36 @@ cudaError_t launch_r(const DeltaArgs& a) {
     return cudaGetLastError();
 }
 
+// states [N H][K][V], boxes of BV columns of one
+bool state_map(CUtensorMap* m, const float* base, const DeltaArgs& a, int BV) {
+    auto fn = decay::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.V, (cuuint64_t)a.K, (cuuint64_t)a.N * a.H};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.V * 4, (cuuint64_t)a.K * a.V * 4};
+    const cuuint32_t box[3] = {(cuuint32_t)BV, (cuuint32_t)a.K, 1}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <typename InT, typename OutT, int NT>
+cudaError_t launch_token(const DeltaArgs& a, int BV) {
+    auto kern = delta_token_kernel<InT, OutT, NT>;
+    const int bytes = (a.K * BV + 8 * NT) * (int)sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    CUtensorMap in{}, out{};
+    if (BV < a.V && ((a.h0 && !state_map(&in, a.h0, a, BV)) || (a.hT && !state_map(&out, a.hT, a, BV)))) return cudaErrorInvalidValue;
+    kern<<<dim3((a.V + BV - 1) / BV, a.H, a.N), NT, bytes, a.stream>>>(in, out, (const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a),
+                                                                     a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV, (OutT*)a.o);
+    return cudaGetLastError();
+}
+
 template <typename InT, typename OutT>
 cudaError_t launch_k(const DeltaArgs& a) {
     if (a.V % 4 == 0) {
-        const int BV = min(a.K <= 128 ? 128 : 64, a.V), bytes = (kTile + 2 * kPart) * (int)sizeof(float);
-        auto kern = delta_token_kernel<InT, OutT>;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        kern<<<dim3((a.V + BV - 1) / BV, a.H, a.N), NT, bytes, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a),
-                                                                         a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV,
-                                                                         (OutT*)a.o);
-        return cudaGetLastError();
+        const int blocks = (a.K * a.V + kTile - 1) / kTile, BV = ((a.V + blocks - 1) / blocks + 3) / 4 * 4, bytes = 4 * a.K * BV;
+        // threads for a tile: 192 KB of states an SM are under way with three blocks of 64 KB, six of 32, eleven of 16
+        // (512 tokens, 32 heads of 64 x 64: 183 us with 256 threads)
+        return bytes > 40960 ? launch_token<InT, OutT, 256>(a, BV) : bytes > 16384 ? launch_token<InT, OutT, 128>(a, BV) : launch_token<InT, OutT, 64>(a, BV);
     }
     return a.K <= 64 ? launch_r<InT, OutT, 4>(a) : a.K <= 128 ? launch_r<InT, OutT, 8>(a) : launch_r<InT, OutT, 16>(a);
 }
