@@ -17,6 +17,8 @@
 #include "decay_gates.cuh"
 #include "delta_gates.cuh"
 #include "kda_internal.h"
+#include "sm100.cuh"
+#include "tile_ops.cuh"
 
 namespace kda {
 namespace delta {
@@ -39,48 +41,62 @@ struct Args {
     float* ws;
 };
 
+// four elements as they lie in memory
+template <typename T>
+struct Four {
+    T e[4];
+};
+template <typename T>
+__device__ __forceinline__ Four<T> four(const T* p) {  // aligned to the four
+    Four<T> r;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(&r) = *reinterpret_cast<const float4*>(p);
+    else                          *reinterpret_cast<uint2*>(&r) = *reinterpret_cast<const uint2*>(p);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float4 floats(const Four<T>& r) {
+    return make_float4(to_f32(r.e[0]), to_f32(r.e[1]), to_f32(r.e[2]), to_f32(r.e[3]));
+}
 // four consecutive elements of a row of n, the first at c (0 behind the row)
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int c, int n, float (&r)[4]) {
+__device__ __forceinline__ Four<T> load4(const T* row, int c, int n) {
+    Four<T> r{};
     if (n % 4 == 0) {
-        if (c >= n) {
-            r[0] = r[1] = r[2] = r[3] = 0.f;
-        } else if constexpr (sizeof(T) == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(row + c);
-            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + c);
-            r[0] = sm100::bf_lo(v.x); r[1] = sm100::bf_hi(v.x); r[2] = sm100::bf_lo(v.y); r[3] = sm100::bf_hi(v.y);
-        }
+        if (c < n) r = four(row + c);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = c + e < n ? to_f32(row[c + e]) : 0.f;
+        for (int e = 0; e < 4; ++e)
+            if (c + e < n) r.e[e] = row[c + e];
     }
+    return r;
 }
-// A thread's share of a [64 rows][NC channels from c0] tile: asked for as it lies in memory, put down transposed.  A warp
+// A thread's share (of 256 threads') of a [64 rows][NC channels from c0] tile: asked for as it lies in memory, put down transposed.  A warp
 // has eight rows and sixteen channels at a time: whole sectors of few lines (a row a lane read 32 lines a load), and no
 // more than two stores to a bank.
 template <typename T, int NC>
 struct Tile {
     static constexpr int N = NC / 16;
     static_assert(NT == 4 * C, "");
-    float r[N][4];
-    static __device__ __forceinline__ int row() { return (threadIdx.x & 7) + 8 * (threadIdx.x >> 5); }
+    Four<T> r[N];
+    static __device__ __forceinline__ int row() { return (threadIdx.x & 7) + 8 * (threadIdx.x >> 5 & 7); }
     static __device__ __forceinline__ int channel(int x) { return 4 * (threadIdx.x >> 3 & 3) + 16 * x; }
     __device__ __forceinline__ void fetch(const T* base, size_t stride, int len, int n, int c0 = 0) {
         const int i = row();
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) r[x][e] = 0.f;
-            if (i < len) load4(base + i * stride, c0 + channel(x), n, r[x]);
+            r[x] = Four<T>{};
+            if (i < len) r[x] = load4(base + i * stride, c0 + channel(x), n);
         }
     }
-    __device__ __forceinline__ void put(float* out) const {
+    template <typename S>
+    __device__ __forceinline__ void put(S* out) const {  // as it is, or as floats
 #pragma unroll
         for (int x = 0; x < N; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[(channel(x) + e) * LD + row()] = r[x][e];
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(S) == sizeof(T)) out[(channel(x) + e) * LD + row()] = r[x].e[e];
+                else                                  out[(channel(x) + e) * LD + row()] = to_f32(r[x].e[e]);
+            }
     }
 };
 
@@ -226,7 +242,10 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q,
 // [n][W] columns from a pair of shared vectors
 template <int W>
 __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
-    if constexpr (W == 2) {
+    if constexpr (W == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+    } else if constexpr (W == 2) {
         const float2 x = *reinterpret_cast<const float2*>(p);
         r[0] = x.x; r[1] = x.y;
     } else {
@@ -234,75 +253,106 @@ __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
     }
 }
 
-// grid (V blocks, H, sequences).  A thread has four rows of a chunk and W of the block's VB = 16 W columns.  Kp: K rounded
-// up to 64, 128 or 256.  The next chunk is on its way into registers while this one is worked on.
+// grid (V blocks, H, sequences).  Two groups of 256 threads: the first has K S, U and the state, the second Q S, P U and the
+// output; a thread four rows of a chunk and W of the block's VB = 16 W columns.  Kp: K rounded up to 64, 128 or 256.  The
+// next chunk is on its way into registers while this one is worked on.
 //
-// Shared memory bounds it: with few columns a thread, a multiply-add costs about half a wavefront of it (W = 1: 18 k of a
-// chunk's 21 k clocks), and one block of eight warps has an SM's space.  Times of a call (heads of 128 x 128): 16384 tokens,
-// 8 heads 2.83 ms (each chunk fetched when its turn came: 4.83); 2048 tokens, 64 heads 1.05 ms (1.54), of which 0.20 the
-// first kernel; 128 tokens, 2 heads of 64 x 64, 31 us (39).  Of bf16 heads of 256 x 256, 2 x 2048 tokens, 32 heads: 3.9 ms (4.7).
+// Loads from shared memory bound it (70 to 73 % of their rate, of L1's 82 to 88): 16 multiply-adds take eight floats a
+// thread.  W = 4 where such blocks fill the SMs, fewer where not.  Times of a call (heads of 128 x 128): float32, 4 x 4096 tokens,
+// 32 heads 3.2 ms (W = 2: 4.1); 16384 tokens, 8 heads 2.9 (each chunk fetched when its turn came: 4.8); 2048 tokens, 64 heads
+// 1.0, of which 0.2 the first kernel; 128 tokens, 2 heads of 64 x 64 31 us.  bf16 with float32 output, 4 x 4096 tokens, 64
+// heads 6.3 ms (one group with four columns a thread 7.6, with two 9.5); of 256 x 256, 8 x 2048 tokens, 32 heads 9.5
+// (11.2, 13.7).  In FP32 multiply-adds alone the first would be 0.9 ms.
 template <typename T, typename OT, int W, int Kp>
-__global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                         const T* __restrict__ v, OT* o, Args p) {
+__global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                             const T* __restrict__ v, OT* o, Args p) {
     constexpr int VB = 16 * W;
     extern __shared__ __align__(16) float sm[];
-    float* sk = sm;               // [Kp][LD] k, transposed
-    float* sq = sk + Kp * LD;     // [Kp][LD] q
-    float* st = sq + Kp * LD;     // [64][LD] T, transposed
+    float* st = sm;               // [64][LD] T, transposed
     float* sp = st + C * LD;      // [64][LD] P
     float* sS = sp + C * LD;      // [Kp][VB]
-    float* sr = sS + Kp * VB;     // [64][VB] V - diag(e^G) K S
-    float* su = sr + C * VB;      // [64][VB] U
-    float* sd = su + C * VB;      // [64][VB] U with the factors of the state
-    float* sf = sd + C * VB;      // [64][4] factors
-    const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
+    float* su = sS + Kp * VB;     // [64][VB] U
+    float* sr = su + C * VB;      // [64][VB] V - diag(e^G) K S, then U with the factors of the state
+    float* sf = sr + C * VB;      // [64][4] factors
+    T* sk = reinterpret_cast<T*>(sf + 4 * C);  // [Kp][LD] k, transposed
+    T* sq = sk + Kp * LD;                      // [Kp][LD] q
+    const bool second = threadIdx.x >= NT;
+    const int tid = threadIdx.x & (NT - 1), ti = tid >> 4, tj = tid & 15;
     const int v0 = blockIdx.x * VB, h = blockIdx.y, n = blockIdx.z;
     int bos, eos;
     if (p.cm.cu) { bos = __ldg(p.cm.cu + n); eos = __ldg(p.cm.cu + n + 1); }
     else         { bos = n * p.cm.T; eos = bos + p.cm.T; }
     const int Hk = p.H / p.hr, hq = h / p.hr, col = v0 + W * tj;
     const size_t state = ((size_t)n * p.H + h) * (size_t)p.K * p.V;
-    for (int x = tid; x < Kp * VB; x += NT) {
+    for (int x = threadIdx.x; x < Kp * VB; x += 2 * NT) {
         const int c = x / VB, d = v0 + x % VB;
         sS[x] = p.h0 && c < p.K && d < p.V ? p.h0[state + (size_t)c * p.V + d] : 0.f;
     }
-    Tile<T, Kp> tk, tq;
-    Tile<float, C> tt, tp;
-    float vr[4][W], factor;
+    const T* mine = second ? q : k;
+    T* sx = second ? sq : sk;
+    float* sl = second ? sp : st;
+    Tile<T, Kp> tx;
+    Tile<float, C> tt;
+    T vr[4][W];
+    float factor = 0.f;
     auto fetch = [&](int t0) {
         const int len = min(C, eos - t0);
         const float* ws = p.ws + ((size_t)t0 * p.H + h) * kRow;
-        tk.fetch(k + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, p.K);
-        tq.fetch(q + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, p.K);
-        tt.fetch(ws, (size_t)p.H * kRow, len, C);
-        tp.fetch(ws + C, (size_t)p.H * kRow, len, C);
-        factor = (tid >> 2) < len ? ws[(size_t)(tid >> 2) * p.H * kRow + kFactors + (tid & 3)] : 0.f;
+        tx.fetch(mine + ((size_t)t0 * Hk + hq) * p.K, (size_t)Hk * p.K, len, p.K);
+        tt.fetch(ws + (second ? C : 0), (size_t)p.H * kRow, len, C);
+        if (second) {
+            factor = (tid >> 2) < len ? ws[(size_t)(tid >> 2) * p.H * kRow + kFactors + (tid & 3)] : 0.f;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                vr[i][e] = 4 * ti + i < len && col + e < p.V ? to_f32(v[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e]) : 0.f;
+                for (int e = 0; e < W; ++e)
+                    vr[i][e] = 4 * ti + i < len && col + e < p.V ? v[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e] : T(0.f);
+        }
+    };
+    auto lower = [&](const float* M, const float* B, float (&r)[4][W]) {  // r_i += sum_{j <= i} M_ij B_j
+#pragma unroll 2
+        for (int j0 = 0; j0 < 4 * ti; j0 += 4)
+#pragma unroll
+            for (int j = j0; j < j0 + 4; ++j) {
+                const float4 a = *reinterpret_cast<const float4*>(M + j * LD + 4 * ti);
+                float b[W];
+                lds_row<W>(B + j * VB + W * tj, b);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    r[0][e] = fmaf(a.x, b[e], r[0][e]);
+                    r[1][e] = fmaf(a.y, b[e], r[1][e]);
+                    r[2][e] = fmaf(a.z, b[e], r[2][e]);
+                    r[3][e] = fmaf(a.w, b[e], r[3][e]);
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float b[W];
+            lds_row<W>(B + (4 * ti + j) * VB + W * tj, b);
+#pragma unroll
+            for (int i = j; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < W; ++e) r[i][e] = fmaf(M[(4 * ti + j) * LD + 4 * ti + i], b[e], r[i][e]);
+        }
     };
     if (bos < eos) fetch(bos);
     for (int t0 = bos; t0 < eos; t0 += C) {
         const int len = min(C, eos - t0);
-        tk.put(sk);
-        tq.put(sq);
-        tt.put(st);
-        tp.put(sp);
-        sf[tid] = factor;
+        tx.put(sx);
+        tt.put(sl);
+        if (second) sf[tid] = factor;
         float vv[4][W];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < W; ++e) vv[i][e] = vr[i][e];
+            for (int e = 0; e < W; ++e) vv[i][e] = second ? 0.f : to_f32(vr[i][e]);
         if (t0 + C < eos) fetch(t0 + C);
         __syncthreads();
-        float y[4][W] = {}, acc[4][W] = {};
+        float y[4][W] = {};  // K S or Q S
 #pragma unroll 8
         for (int c = 0; c < Kp; ++c) {
-            const float4 a = *reinterpret_cast<const float4*>(sk + c * LD + 4 * ti);
-            const float4 b = *reinterpret_cast<const float4*>(sq + c * LD + 4 * ti);
+            const float4 a = floats(four(sx + c * LD + 4 * ti));
             float s[W];
             lds_row<W>(sS + c * VB + W * tj, s);
 #pragma unroll
@@ -311,95 +361,74 @@ __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q
                 y[1][e] = fmaf(a.y, s[e], y[1][e]);
                 y[2][e] = fmaf(a.z, s[e], y[2][e]);
                 y[3][e] = fmaf(a.w, s[e], y[3][e]);
-                acc[0][e] = fmaf(b.x, s[e], acc[0][e]);
-                acc[1][e] = fmaf(b.y, s[e], acc[1][e]);
-                acc[2][e] = fmaf(b.z, s[e], acc[2][e]);
-                acc[3][e] = fmaf(b.w, s[e], acc[3][e]);
             }
         }
+        if (second) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                sr[(4 * ti + i) * VB + W * tj + e] = fmaf(-sf[4 * (4 * ti + i)], y[i][e], vv[i][e]);
-                acc[i][e] *= sf[4 * (4 * ti + i) + 1];
-                y[i][e] = 0.f;
-            }
-        __syncthreads();
-        auto lower = [&](const float* M, const float* B, float (&r)[4][W]) {  // r_i += sum_{j <= i} M_ij B_j
-            for (int j0 = 0; j0 < 4 * ti; j0 += 4)
+                for (int e = 0; e < W; ++e) y[i][e] *= sf[4 * (4 * ti + i) + 1];
+            __syncthreads();  // (sr below has been read, su and sr written)
+            lower(sp, su, y);
 #pragma unroll
-                for (int j = j0; j < j0 + 4; ++j) {
-                    const float4 a = *reinterpret_cast<const float4*>(M + j * LD + 4 * ti);
-                    float b[W];
-                    lds_row<W>(B + j * VB + W * tj, b);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        r[0][e] = fmaf(a.x, b[e], r[0][e]);
-                        r[1][e] = fmaf(a.y, b[e], r[1][e]);
-                        r[2][e] = fmaf(a.z, b[e], r[2][e]);
-                        r[3][e] = fmaf(a.w, b[e], r[3][e]);
-                    }
-                }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float b[W];
-                lds_row<W>(B + (4 * ti + j) * VB + W * tj, b);
-#pragma unroll
-                for (int i = j; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < W; ++e) r[i][e] = fmaf(M[(4 * ti + j) * LD + 4 * ti + i], b[e], r[i][e]);
-            }
-        };
-        lower(st, sr, y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                su[(4 * ti + i) * VB + W * tj + e] = y[i][e];
-                sd[(4 * ti + i) * VB + W * tj + e] = 4 * ti + i < len ? y[i][e] * sf[4 * (4 * ti + i) + 2] : 0.f;
-            }
-        __syncthreads();
-        lower(sp, su, acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (4 * ti + i < len && col + e < p.V)
-                    o[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e] = from_f32<OT>(acc[i][e]);
-        const float last = sf[3];
-        for (int c0 = 4 * ti; c0 < Kp; c0 += 64) {
-            float add[4][W] = {};
-#pragma unroll 2
-            for (int j = 0; j < C; j += 4) {
-                float u[4][W];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) lds_row<W>(sd + (j + x) * VB + W * tj, u[x]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 a = *reinterpret_cast<const float4*>(sk + (c0 + i) * LD + j);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        add[i][e] = fmaf(a.x, u[0][e], add[i][e]);
-                        add[i][e] = fmaf(a.y, u[1][e], add[i][e]);
-                        add[i][e] = fmaf(a.z, u[2][e], add[i][e]);
-                        add[i][e] = fmaf(a.w, u[3][e], add[i][e]);
-                    }
-                }
-            }
+                for (int e = 0; e < W; ++e)
+                    if (4 * ti + i < len && col + e < p.V)
+                        o[((size_t)(t0 + 4 * ti + i) * p.H + h) * p.V + col + e] = from_f32<OT>(y[i][e]);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
-                    float* s = sS + (c0 + i) * VB + W * tj + e;
-                    *s = fmaf(last, *s, add[i][e]);
+                    sr[(4 * ti + i) * VB + W * tj + e] = fmaf(-sf[4 * (4 * ti + i)], y[i][e], vv[i][e]);
+                    y[i][e] = 0.f;
                 }
+            bar_sync(1, NT);
+            lower(st, sr, y);
+            bar_sync(1, NT);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    su[(4 * ti + i) * VB + W * tj + e] = y[i][e];
+                    sr[(4 * ti + i) * VB + W * tj + e] = 4 * ti + i < len ? y[i][e] * sf[4 * (4 * ti + i) + 2] : 0.f;
+                }
+            __syncthreads();  // (the second group has read the state)
+            const float last = sf[3];
+            for (int c0 = 4 * ti; c0 < Kp; c0 += 64) {
+                float add[4][W] = {};
+#pragma unroll 2
+                for (int j = 0; j < C; j += 4) {
+                    float u[4][W];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) lds_row<W>(sr + (j + x) * VB + W * tj, u[x]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 a = floats(four(sk + (c0 + i) * LD + j));
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            add[i][e] = fmaf(a.x, u[0][e], add[i][e]);
+                            add[i][e] = fmaf(a.y, u[1][e], add[i][e]);
+                            add[i][e] = fmaf(a.z, u[2][e], add[i][e]);
+                            add[i][e] = fmaf(a.w, u[3][e], add[i][e]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        float* s = sS + (c0 + i) * VB + W * tj + e;
+                        *s = fmaf(last, *s, add[i][e]);
+                    }
+            }
         }
         __syncthreads();
     }
     if (!p.hT) return;
     __syncthreads();  // (an empty sequence's state passes through)
-    for (int x = tid; x < Kp * VB; x += NT) {
+    for (int x = threadIdx.x; x < Kp * VB; x += 2 * NT) {
         const int c = x / VB, d = v0 + x % VB;
         if (c < p.K && d < p.V) p.hT[state + (size_t)c * p.V + d] = sS[x];
     }
@@ -407,16 +436,19 @@ __global__ void __launch_bounds__(NT) delta_chain_kernel(const T* __restrict__ q
 
 template <typename T, typename OT, int W, int Kp>
 cudaError_t run_chain_k(const DeltaArgs& a, const Args& p) {
-    constexpr int VB = 16 * W, bytes = (2 * Kp * LD + 2 * C * LD + Kp * VB + 3 * C * VB + 4 * C) * (int)sizeof(float);
+    constexpr int VB = 16 * W, bytes = 2 * Kp * LD * (int)sizeof(T) + (2 * C * LD + Kp * VB + 2 * C * VB + 4 * C) * (int)sizeof(float);
     auto kern = delta_chain_kernel<T, OT, W, Kp>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((a.V + VB - 1) / VB, a.H, a.N), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
+    kern<<<dim3((a.V + VB - 1) / VB, a.H, a.N), 2 * NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
     return cudaGetLastError();
 }
 template <typename T, typename OT, int W>
 cudaError_t run_chain(const DeltaArgs& a, const Args& p) {
-    return a.K <= 64 ? run_chain_k<T, OT, W, 64>(a, p) : a.K <= 128 ? run_chain_k<T, OT, W, 128>(a, p) : run_chain_k<T, OT, W, 256>(a, p);
+    if (a.K <= 64) return run_chain_k<T, OT, W, 64>(a, p);
+    if (a.K <= 128) return run_chain_k<T, OT, W, 128>(a, p);
+    // (four columns a thread do not fit shared memory with keys of 256 floats)
+    return run_chain_k<T, OT, sizeof(T) == 4 ? W < 2 ? W : 2 : W, 256>(a, p);
 }
 
 template <typename T, typename OT>
@@ -432,8 +464,9 @@ cudaError_t run(const DeltaArgs& a) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const bool narrow = (long)a.N * a.H * ((a.V + 31) / 32) < sms;
-    return narrow ? run_chain<T, OT, 1>(a, p) : run_chain<T, OT, 2>(a, p);
+    const long units = (long)a.N * a.H;
+    if (units * ((a.V + 63) / 64) >= sms) return run_chain<T, OT, 4>(a, p);
+    return units * ((a.V + 31) / 32) >= sms ? run_chain<T, OT, 2>(a, p) : run_chain<T, OT, 1>(a, p);
 }
 
 }  // namespace
