@@ -14,7 +14,8 @@
 //
 // Memory bounds it: each row goes in and out once.  16384 tokens with 64 + 8 heads of 128, RMS norm, rotation: 604 MB in
 // 101 us, 6.0 TB/s (with angles formed in FP32 for each row and no loads ahead: 260); 20480 tokens with 32 heads, L2 norm,
-// no rotation: 57 us, 5.9 TB/s.  Three kernels: many rows, few rows, and any D, R and alignment.
+// no rotation: 57 us, 5.9 TB/s.  Four kernels: many rows, few
+// rows, whole words of bf16, and any D, R and alignment.
 #include "common.cuh"
 #include "kda_internal.h"
 #include "sm100.cuh"
@@ -414,50 +415,181 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
             sm100::mbar_wait(bars + 8 * (uint32_t)(g % kRingStages), (uint32_t)(g / kRingStages) & 1u);
 }
 
-// Any D, R and alignment: a warp a row, a pair of single elements a lane and step.
-template <typename T>
-__global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(Params p) {
+// bf16 rows of whole words of two elements (any even D, any R): a warp U rows at a time, a word a lane and step, S steps (D / 64
+// rounded up to a power of 2).  Elements that R / 2 lies between meet through shared memory, as floats.  (Loads and stores of
+// single elements, pairs of which a lane holds by itself, took 2 to 3 times the time: half words are stored to half
+// sectors.)  16384 tokens with 72 heads of 128, 106 elements rotated: 201 us, single elements 275 to 330.
+template <int S>
+__global__ void __launch_bounds__(NT) qk_norm_rope_words_kernel(const __grid_constant__ Params p) {
+    constexpr int U = S < 4 ? 4 : 2;
+    extern __shared__ __align__(16) float s_turn[];
+    const int tid = threadIdx.x, half = p.R / 2, words = p.D / 2, l = tid & 31, w = tid >> 5;
+    const long t0 = (long)blockIdx.x * p.tile;
+    const int nt = (int)min((long)p.tile, p.tokens - t0), rows = nt * p.heads;
+    float2* turns = reinterpret_cast<float2*>(s_turn);
+    float* mix = s_turn + p.tile * p.R + w * U * p.R;  // the warp's rows' first R elements
+    for (int x = tid; x < nt * half; x += NT) turns[x] = turn(p, t0 + x / half, x % half);
+    if (half) __syncthreads();
+    float2 wt[2][S];  // both sides' weights
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int i = l + 32 * s;
+            wt[side][s] = make_float2(1.f, 1.f);
+            if (p.w[side] && i < words) wt[side][s] = make_float2(__ldg(p.w[side] + 2 * i), __ldg(p.w[side] + 2 * i + 1));
+        }
+    for (int r0 = w; r0 < rows; r0 += U * (NT / 32)) {
+        uint32_t v[U][S];
+        float sum[U];
+        int side[U], tt[U];
+        long at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * (NT / 32);
+            tt[u] = p.per ? (int)__umulhi((uint32_t)r, p.per) : r;
+            const int hh = r - tt[u] * p.heads;
+            side[u] = hh >= p.Hq;
+            at[u] = (long)(hh - (side[u] ? p.Hq : 0)) * p.D;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(side[u] ? p.x[1] : p.x[0]) +
+                                                                    (t0 + tt[u]) * (side[u] ? p.xs[1] : p.xs[0]) + at[u]);
+#pragma unroll
+            for (int s = 0; s < S; ++s) v[u][s] = r < rows && l + 32 * s < words ? src[l + 32 * s] : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            sum[u] = 0.f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) sum[u] = fmaf(sm100::bf_lo(v[u][s]), sm100::bf_lo(v[u][s]), fmaf(sm100::bf_hi(v[u][s]), sm100::bf_hi(v[u][s]), sum[u]));
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], m);
+        float2 y[U][S];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = factor(p, sum[u]);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int i = l + 32 * s;
+                const float2 wv = side[u] ? wt[1][s] : wt[0][s];
+                y[u][s] = make_float2(sm100::bf_lo(v[u][s]) * f * wv.x, sm100::bf_hi(v[u][s]) * f * wv.y);
+                if (i >= half) continue;
+                if (p.interleaved) {
+                    const float2 z = turns[tt[u] * half + i], x = y[u][s];
+                    y[u][s] = make_float2(x.x * z.x - x.y * z.y, x.y * z.x + x.x * z.y);
+                } else {
+                    *reinterpret_cast<float2*>(mix + u * p.R + 2 * i) = y[u][s];
+                }
+            }
+        }
+        if (half && !p.interleaved) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int i = l + 32 * s;
+                    if (i >= half) continue;
+                    const float2 z = turns[tt[u] * half + i];
+                    float *a = mix + u * p.R + i, *b = a + half;
+                    const float xa = *a, xb = *b;
+                    *a = xa * z.x - xb * z.y;
+                    *b = xb * z.x + xa * z.y;
+                }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (l + 32 * s < half) y[u][s] = *reinterpret_cast<const float2*>(mix + u * p.R + 2 * (l + 32 * s));
+            __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r0 + u * (NT / 32) >= rows) break;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(side[u] ? p.y[1] : p.y[0]) +
+                                                        (t0 + tt[u]) * (side[u] ? p.ys[1] : p.ys[0]) + at[u]);
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (l + 32 * s < words) __stcs(dst + l + 32 * s, sm100::pack_bf16(y[u][s].x, y[u][s].y));
+        }
+    }
+}
+
+// Any D, R and alignment: a warp U rows at a time, a pair of single elements a lane and step.  float32: 8192 tokens with 72
+// heads of 128, 34 elements rotated, 110 us (153 with one row at a time).
+template <typename T, int S>
+__global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(const __grid_constant__ Params p) {
+    constexpr int U = S < 4 ? 4 : 2;
     extern __shared__ __align__(16) float s_turn[];
     const int tid = threadIdx.x, half = p.R / 2, l = tid & 31;
     const long t0 = (long)blockIdx.x * p.tile;
-    const int nt = (int)min((long)p.tile, p.tokens - t0);
+    const int nt = (int)min((long)p.tile, p.tokens - t0), rows = nt * p.heads;
     float2* turns = reinterpret_cast<float2*>(s_turn);
     for (int x = tid; x < nt * half; x += NT) turns[x] = turn(p, t0 + x / half, x % half);
     if (half) __syncthreads();
-    constexpr int S = kMaxD / 64;
-    for (int r = tid >> 5; r < nt * p.heads; r += NT / 32) {
-        const int tt = r / p.heads, hh = r % p.heads, side = hh >= p.Hq, h = hh - (side ? p.Hq : 0);
-        const T* src = static_cast<const T*>(p.x[side]) + (t0 + tt) * p.xs[side] + (long)h * p.D;
-        T* dst = static_cast<T*>(p.y[side]) + (t0 + tt) * p.ys[side] + (long)h * p.D;
-        float va[S], vb[S], sum = 0.f;
+    int a[S], b[S];
+    float wa[2][S], wb[2][S];  // both sides' weights
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int i = l + 32 * s;
-            const bool apart = i < half && !p.interleaved;
-            const int a = apart ? i : 2 * i, b = apart ? half + i : 2 * i + 1;
-            va[s] = a < p.D ? to_f32(src[a]) : 0.f;
-            vb[s] = b < p.D && a < p.D ? to_f32(src[b]) : 0.f;
-            sum = fmaf(va[s], va[s], fmaf(vb[s], vb[s], sum));
+    for (int s = 0; s < S; ++s) {
+        const int i = l + 32 * s;
+        const bool apart = i < half && !p.interleaved;
+        a[s] = apart ? i : 2 * i;
+        b[s] = apart ? half + i : 2 * i + 1;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const float* w = p.w[side];
+            wa[side][s] = w && a[s] < p.D ? __ldg(w + a[s]) : 1.f;
+            wb[side][s] = w && b[s] < p.D ? __ldg(w + b[s]) : 1.f;
+        }
+    }
+    for (int r0 = tid >> 5; r0 < rows; r0 += U * (NT / 32)) {
+        float va[U][S], vb[U][S], sum[U];
+        int side[U], tt[U], at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * (NT / 32);
+            tt[u] = p.per ? (int)__umulhi((uint32_t)r, p.per) : r;
+            const int hh = r - tt[u] * p.heads;
+            side[u] = hh >= p.Hq;
+            at[u] = (hh - (side[u] ? p.Hq : 0)) * p.D;
+            const T* src = static_cast<const T*>(side[u] ? p.x[1] : p.x[0]) + (t0 + tt[u]) * (side[u] ? p.xs[1] : p.xs[0]) + at[u];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                va[u][s] = r < rows && a[s] < p.D ? to_f32(src[a[s]]) : 0.f;
+                vb[u][s] = r < rows && b[s] < p.D ? to_f32(src[b[s]]) : 0.f;
+            }
         }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const float f = factor(p, sum);
-        const float* w = side ? p.w[1] : p.w[0];
+        for (int u = 0; u < U; ++u) {
+            sum[u] = 0.f;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int i = l + 32 * s;
-            const bool apart = i < half && !p.interleaved;
-            const int a = apart ? i : 2 * i, b = apart ? half + i : 2 * i + 1;
-            if (a >= p.D) continue;
-            float ya = va[s] * f * (w ? __ldg(w + a) : 1.f), yb = b < p.D ? vb[s] * f * (w ? __ldg(w + b) : 1.f) : 0.f;
-            if (i < half) {
-                const float2 z = turns[tt * half + i];
-                const float xa = ya, xb = yb;
-                ya = xa * z.x - xb * z.y;
-                yb = xb * z.x + xa * z.y;
+            for (int s = 0; s < S; ++s) sum[u] = fmaf(va[u][s], va[u][s], fmaf(vb[u][s], vb[u][s], sum[u]));
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], m);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r0 + u * (NT / 32) >= rows) break;
+            const float f = factor(p, sum[u]);
+            T* dst = static_cast<T*>(side[u] ? p.y[1] : p.y[0]) + (t0 + tt[u]) * (side[u] ? p.ys[1] : p.ys[0]) + at[u];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                if (a[s] >= p.D) continue;
+                float ya = va[u][s] * f * (side[u] ? wa[1][s] : wa[0][s]), yb = vb[u][s] * f * (side[u] ? wb[1][s] : wb[0][s]);
+                if (l + 32 * s < half) {
+                    const float2 z = turns[tt[u] * half + l + 32 * s];
+                    const float xa = ya, xb = yb;
+                    ya = xa * z.x - xb * z.y;
+                    yb = xb * z.x + xa * z.y;
+                }
+                dst[a[s]] = from_f32<T>(ya);
+                if (b[s] < p.D) dst[b[s]] = from_f32<T>(yb);
             }
-            dst[a] = from_f32<T>(ya);
-            if (b < p.D) dst[b] = from_f32<T>(yb);
         }
     }
 }
@@ -473,9 +605,14 @@ cudaError_t run_ring(const QkNormArgs& a, const Params& p, int sms) {
 }
 
 template <typename T>
-cudaError_t run(const QkNormArgs& a, Params& p, bool fast) {
-    const int grid = (int)((a.tokens + p.tile - 1) / p.tile), bytes = p.tile * (a.R / 2) * 3 * (int)sizeof(float);
-    void (*kern)(Params) = qk_norm_rope_any_kernel<T>;
+cudaError_t run(const QkNormArgs& a, Params& p, bool fast, bool words) {
+    const int grid = (int)((a.tokens + p.tile - 1) / p.tile);
+    int bytes = p.tile * (a.R / 2) * 3 * (int)sizeof(float);
+    void (*kern)(Params) = a.D > 128 ? qk_norm_rope_any_kernel<T, 4> : a.D > 64 ? qk_norm_rope_any_kernel<T, 2> : qk_norm_rope_any_kernel<T, 1>;
+    if (sizeof(T) == 2 && words) {
+        kern = a.D > 128 ? qk_norm_rope_words_kernel<4> : a.D > 64 ? qk_norm_rope_words_kernel<2> : qk_norm_rope_words_kernel<1>;
+        bytes = p.tile * a.R * 4 + NT / 32 * (a.D > 128 ? 2 : 4) * a.R * 4;
+    }
     if (fast) kern = a.D > 128 ? qk_norm_rope_kernel<T, 32> : a.D > 64 ? qk_norm_rope_kernel<T, 16> : a.D > 32 ? qk_norm_rope_kernel<T, 8>
                      : qk_norm_rope_kernel<T, 4>;
     kern<<<grid, NT, bytes, a.stream>>>(p);
@@ -492,12 +629,14 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     p.heads = a.q.heads + Hk;
     const int e = a.bf16 ? 2 : 4;
     bool fast = a.D % 8 == 0 && a.R % 8 == 0 && (((uintptr_t)a.q.weight | (uintptr_t)(Hk ? a.k.weight : nullptr)) & 15u) == 0;
+    bool words = a.D % 2 == 0;  // rows of bf16 begin at whole words
     for (int s = 0; s < (Hk ? 2 : 1); ++s) {
         p.x[s] = side[s]->x;
         p.y[s] = side[s]->y;
         p.w[s] = side[s]->weight;
         p.xs[s] = side[s]->stride;
         p.ys[s] = side[s]->y_stride;
+        words = words && (((uintptr_t)p.x[s] | (uintptr_t)p.y[s] | (uintptr_t)(p.xs[s] * e) | (uintptr_t)(p.ys[s] * e)) & 3u) == 0;
         fast = fast && (((uintptr_t)p.x[s] | (uintptr_t)p.y[s] | (uintptr_t)(p.xs[s] * e) | (uintptr_t)(p.ys[s] * e)) & 15u) == 0;
     }
     p.norm = a.norm;
@@ -530,7 +669,7 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
         const bool ring = a.tokens * p.per_token >= 8l * kRingBlocks * (NT / 32) * sms && (long)p.heads * a.D * e >= 1024l * p.per_token;
         if (ring) return a.bf16 ? run_ring<__nv_bfloat16>(a, p, sms) : run_ring<float>(a, p, sms);
     }
-    return a.bf16 ? run<__nv_bfloat16>(a, p, fast) : run<float>(a, p, fast);
+    return a.bf16 ? run<__nv_bfloat16>(a, p, fast, words) : run<float>(a, p, fast, false);
 }
 
 cudaError_t read_rope_timeouts(unsigned* count, bool reset) {

@@ -17,6 +17,12 @@ CASES = [  # Hq, Hk, D, R, norm, axes, interleaved, sliced; at least two groups 
     (33, 16, 128, 128, 2, 1, True, False),
     (70, 0, 32, 16, 0, 1, False, False),
     (65, 65, 16, 16, 1, 4, False, True),
+    # heads or rotations that are not whole vectors
+    (5, 2, 244, 36, 1, 2, False, True),
+    (7, 1, 130, 130, 2, 1, False, False),
+    (6, 3, 36, 20, 1, 1, True, True),
+    (4, 2, 128, 34, 1, 3, False, True),
+    (3, 1, 101, 66, 1, 1, False, True),
 ]
 
 
