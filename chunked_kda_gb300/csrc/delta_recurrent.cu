@@ -5,7 +5,7 @@
 // the rule's decay, correction and read-out with the new state's read-out written out, so that one pass over
 // the old state gives both products.
 //
-// Memory bounds it: the state goes in and out once.  Two kernels:
+// Memory bounds it: the state goes in and out once.  Two kernels, the second for what does not fit the first:
 //
 // Rows of whole vectors (V a multiple of 4): a block has a (sequence, head) and all rows of as many value columns as make
 // 64 KB, in shared memory, which one copy brings and takes away: a bulk copy where that is the whole state, else a
@@ -18,9 +18,10 @@
 // 234 x 128 89.  Each further token costs a pass over shared memory (4 tokens: 736 us), so that from about eight on the
 // chunked kernels are faster (64 sequences of 16 tokens, bf16: 358, chunked 173).
 //
-// Anything else: a warp has a block of columns with all rows in registers, RG groups of lanes with 16 rows each (K
-// rounded up to 16 RG: 64, 128 or 256, rows and columns beyond K and V masked), joined by shuffles.  Its rows begin
-// at any four bytes, and single loads are what bounds it (128 x 126: 850 us).
+// V not a multiple of 4: the same with two columns or one a thread, where a state fits shared memory whole (128 x 126: 99 % of
+// a copy's rate, 100 x 253 82, 99 x 77 75).  Larger ones: a warp has a block of columns with all rows in registers, RG groups of
+// lanes with 16 rows each (K rounded up to 16 RG: 64, 128 or 256, rows and columns beyond K and V masked), joined by shuffles;
+// its rows begin at any four bytes, and single loads are what bounds it (236 x 253: 27 %).
 #include "common.cuh"
 #include "delta_gates.cuh"
 #include "kda_internal.h"
@@ -35,23 +36,32 @@ using namespace sm100;
 
 __device__ unsigned int g_token_timeouts = 0;
 
-constexpr int kTile = 16384;  // floats of a block's state, at most
+constexpr int kTile = 16384;   // floats of a block's state, at most
+constexpr int kWhole = 54000;  // ... where rows are not whole vectors, so that a state cannot be parted
 
-// BV: columns of a block.  All of V: a block's rows lie side by side; else they come and go by the tensor maps.
-template <typename InT, typename OutT, int NT>
+template <int E>
+struct alignas(4 * E) Columns {
+    float e[E];
+};
+
+// BV: columns of a block, E those of a thread.  All of V: a block's rows lie side by side; else they come and go by the
+// tensor maps.
+template <typename InT, typename OutT, int NT, int E>
 __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out, const InT* __restrict__ q,
     const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags, const float* h0, float* hT,
     const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o) {
-    constexpr int kPart = 4 * NT;  // partial S^T k, then S^T q, a row of a block's columns for each group of threads
+    constexpr int kPart = E * NT;  // partial S^T k, then S^T q, a row of a block's columns for each group of threads
     extern __shared__ __align__(128) float sm[];  // the partial products, [K][BV] the state
     __shared__ float s_q[256], s_k[256], s_dot[3][NT / 32];
     __shared__ __align__(8) uint64_t s_bar;
     float* part = sm;
-    float* state = sm + 2 * kPart;
     const int tid = threadIdx.x, v0 = blockIdx.x * BV, h = blockIdx.y, n = blockIdx.z, cols = min(BV, V - v0);
     const uint32_t bar = smem_u32(&s_bar);
     const size_t st = ((size_t)n * H + h) * (size_t)K * V + v0;
+    // a whole state may begin and end inside a bulk copy's 16 bytes: its first and last floats go one by one
+    const int off = E == 4 ? 0 : (int)(st & 3), edge = min((4 - off) & 3, K * BV), body = (K * BV - edge) & ~3, end = K * BV - edge - body;
+    float* state = sm + 2 * kPart + off;
     if (tid == 0) {
         mbar_init(bar, 1);
         fence_mbar_init();
@@ -61,19 +71,21 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     const bool whole = BV == V;
     if (h0) {
         if (tid == 0) {
-            mbar_arrive_expect_tx(bar, 4u * K * BV);  // (columns behind V count, too)
-            if (whole) bulk_load(smem_u32(state), h0 + st, 4u * K * BV, bar);
-            else tma_load_3d(smem_u32(state), &tm_in, v0, 0, n * H + h, bar);
+            mbar_arrive_expect_tx(bar, 4u * body);  // (a box's columns behind V count, too)
+            if (!whole) tma_load_3d(smem_u32(state), &tm_in, v0, 0, n * H + h, bar);
+            else if (body > 0) bulk_load(smem_u32(state + edge), h0 + st + edge, 4u * body, bar);
         }
         __syncwarp();
+        if (tid < edge) state[tid] = h0[st + tid];
+        if (tid < end) state[edge + body + tid] = h0[st + edge + body + tid];
     } else {
         for (int x = tid; x < K * BV; x += NT) state[x] = 0.f;
     }
     long bos, eos;
     if (cu) { bos = __ldg(cu + n); eos = __ldg(cu + n + 1); }
     else    { bos = (long)n * T; eos = bos + T; }
-    const int quads = BV / 4, groups = NT / quads, quad = tid % quads, group = tid / quads;
-    const bool on = group < groups && 4 * quad < cols;
+    const int pieces = BV / E, groups = NT / pieces, piece = tid % pieces, group = tid / pieces;
+    const bool on = group < groups && E * piece < cols;
     const int Hq = H / hr, hq = h / hr;
     const Gates::Head head = gates.head(h);
     const float scale = rsqrtf((float)K);
@@ -85,9 +97,9 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
         }
         waiting = false;
     };
-    float4* S = reinterpret_cast<float4*>(state) + quad;
+    Columns<E>* S = reinterpret_cast<Columns<E>*>(state) + piece;
     for (long t = bos; t < eos; ++t) {
-        const size_t qk = ((size_t)t * Hq + hq) * K, vo = ((size_t)t * H + h) * V + v0 + 4 * quad;
+        const size_t qk = ((size_t)t * Hq + hq) * K, vo = ((size_t)t * H + h) * V + v0 + E * piece;
         float qv[256 / NT], kv[256 / NT];
 #pragma unroll
         for (int x = 0; x < 256 / NT; ++x) {
@@ -95,10 +107,10 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
             qv[x] = r < K ? to_f32(q[qk + r]) : 0.f;
             kv[x] = r < K ? to_f32(k[qk + r]) : 0.f;
         }
-        float u[4] = {};
+        float u[E] = {};
         if (on)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = to_f32(v[vo + j]);
+            for (int j = 0; j < E; ++j) u[j] = to_f32(v[vo + j]);
         const float dec = expf(gates.decay(t, h, head)), rate = gates.rate(t, h);
         float dots[3] = {};
 #pragma unroll
@@ -117,17 +129,20 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
         }
         state_here();
         __syncthreads();
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+        Columns<E> y{}, z{};
         if (on) {
 #pragma unroll 4
             for (int r = group; r < K; r += groups) {
-                const float4 s = S[r * quads];
+                const Columns<E> s = S[r * pieces];
                 const float a = s_k[r], b = s_q[r];
-                y.x = fmaf(s.x, a, y.x); y.y = fmaf(s.y, a, y.y); y.z = fmaf(s.z, a, y.z); y.w = fmaf(s.w, a, y.w);
-                z.x = fmaf(s.x, b, z.x); z.y = fmaf(s.y, b, z.y); z.z = fmaf(s.z, b, z.z); z.w = fmaf(s.w, b, z.w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    y.e[j] = fmaf(s.e[j], a, y.e[j]);
+                    z.e[j] = fmaf(s.e[j], b, z.e[j]);
+                }
             }
-            reinterpret_cast<float4*>(part)[tid] = y;
-            reinterpret_cast<float4*>(part + kPart)[tid] = z;
+            reinterpret_cast<Columns<E>*>(part)[tid] = y;
+            reinterpret_cast<Columns<E>*>(part + kPart)[tid] = z;
         }
         __syncthreads();
         if (on) {
@@ -139,39 +154,34 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
             const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(d[0] + kQNormEps) : 1.f;
             const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(d[1] + kQNormEps) : 1.f;
             auto total = [&](const float* from) {
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                Columns<E> s{};
 #pragma unroll 4
                 for (int g = 0; g < groups; ++g) {
-                    const float4 x = reinterpret_cast<const float4*>(from)[g * quads + quad];
-                    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+                    const Columns<E> x = reinterpret_cast<const Columns<E>*>(from)[g * pieces + piece];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) s.e[j] += x.e[j];
                 }
                 return s;
             };
             y = total(part);
             const float g = dec * nk;
-            u[0] = rate * (u[0] - g * y.x);
-            u[1] = rate * (u[1] - g * y.y);
-            u[2] = rate * (u[2] - g * y.z);
-            u[3] = rate * (u[3] - g * y.w);
+#pragma unroll
+            for (int j = 0; j < E; ++j) u[j] = rate * (u[j] - g * y.e[j]);
             if (group == t % groups) {  // (each group's turn)
                 z = total(part + kPart);
                 const float f = scale * nq, c = nk * d[2];
-                o[vo] = from_f32<OutT>(f * fmaf(c, u[0], dec * z.x));
-                o[vo + 1] = from_f32<OutT>(f * fmaf(c, u[1], dec * z.y));
-                o[vo + 2] = from_f32<OutT>(f * fmaf(c, u[2], dec * z.z));
-                o[vo + 3] = from_f32<OutT>(f * fmaf(c, u[3], dec * z.w));
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[vo + j] = from_f32<OutT>(f * fmaf(c, u[j], dec * z.e[j]));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] *= nk;
+            for (int j = 0; j < E; ++j) u[j] *= nk;
 #pragma unroll 4
             for (int r = group; r < K; r += groups) {
-                float4 s = S[r * quads];
+                Columns<E> s = S[r * pieces];
                 const float a = s_k[r];
-                s.x = fmaf(s.x, dec, a * u[0]);
-                s.y = fmaf(s.y, dec, a * u[1]);
-                s.z = fmaf(s.z, dec, a * u[2]);
-                s.w = fmaf(s.w, dec, a * u[3]);
-                S[r * quads] = s;
+#pragma unroll
+                for (int j = 0; j < E; ++j) s.e[j] = fmaf(s.e[j], dec, a * u[j]);
+                S[r * pieces] = s;
             }
         }
         __syncthreads();
@@ -182,11 +192,13 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     __syncthreads();
     // (this block has read its part of h0 and no other touches it: hT may be h0)
     if (tid == 0) {
-        if (whole) bulk_store(hT + st, smem_u32(state), 4u * K * BV);
-        else decay::tma_store_3d(&tm_out, smem_u32(state), v0, 0, n * H + h);
+        if (!whole) decay::tma_store_3d(&tm_out, smem_u32(state), v0, 0, n * H + h);
+        else if (body > 0) bulk_store(hT + st + edge, smem_u32(state + edge), 4u * body);
         decay::bulk_commit();
         decay::bulk_wait_read();
     }
+    if (tid < edge) hT[st + tid] = state[tid];
+    if (tid < end) hT[st + edge + body + tid] = state[edge + body + tid];
 }
 
 template <typename InT, typename OutT, int RG>
@@ -307,10 +319,10 @@ bool state_map(CUtensorMap* m, const float* base, const DeltaArgs& a, int BV) {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <typename InT, typename OutT, int NT>
+template <typename InT, typename OutT, int NT, int E = 4>
 cudaError_t launch_token(const DeltaArgs& a, int BV) {
-    auto kern = delta_token_kernel<InT, OutT, NT>;
-    const int bytes = (a.K * BV + 8 * NT) * (int)sizeof(float);
+    auto kern = delta_token_kernel<InT, OutT, NT, E>;
+    const int bytes = (a.K * BV + 2 * E * NT + (E == 4 ? 0 : 4)) * (int)sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     CUtensorMap in{}, out{};
@@ -327,6 +339,12 @@ cudaError_t launch_k(const DeltaArgs& a) {
         // threads for a tile: 192 KB of states an SM are under way with three blocks of 64 KB, six of 32, eleven of 16
         // (512 tokens, 32 heads of 64 x 64: 183 us with 256 threads)
         return bytes > 40960 ? launch_token<InT, OutT, 256>(a, BV) : bytes > 16384 ? launch_token<InT, OutT, 128>(a, BV) : launch_token<InT, OutT, 64>(a, BV);
+    }
+    // a state that one bulk copy can take (512 tokens, 32 heads of 128 x 126: 312 us, by single loads 850)
+    if (a.K * a.V <= kWhole) {
+        const bool small = a.K * a.V <= 10240;
+        if (a.V % 2 == 0) return small ? launch_token<InT, OutT, 128, 2>(a, a.V) : launch_token<InT, OutT, 256, 2>(a, a.V);
+        return small && a.V <= 128 ? launch_token<InT, OutT, 128, 1>(a, a.V) : launch_token<InT, OutT, 256, 1>(a, a.V);
     }
     return a.K <= 64 ? launch_r<InT, OutT, 4>(a) : a.K <= 128 ? launch_r<InT, OutT, 8>(a) : launch_r<InT, OutT, 16>(a);
 }

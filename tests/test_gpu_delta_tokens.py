@@ -12,6 +12,8 @@ SIZES = [  # K, V: bytes of a state up to 16 KB, 40 KB, 64 KB, and beyond: colum
     (65, 64), (100, 100), (40, 256), (256, 36),  # 128
     (101, 104), (64, 256), (256, 64), (80, 204),  # 256
     (128, 132), (234, 128), (256, 256), (251, 200), (65, 256), (256, 68),  # column blocks
+    (128, 126), (256, 210), (4, 1), (100, 77), (212, 253),  # whole, two columns or one a thread
+    (256, 254), (99, 77), (255, 3), (17, 6),  # by single loads
 ]
 
 
