@@ -112,7 +112,7 @@ size_t kda_delta_chunk_workspace_bytes(kda_dtype qkv_dtype, kda_dtype o_dtype, i
     if (!dtype_ok(qkv_dtype) || !dtype_ok(o_dtype) || B < 0 || T < 0 || H <= 0 || n_seqs < 0 || K < 1 || K > 256 || V < 1 || V > 256)
         return 0;
     const bool packed = n_seqs > 0;
-    return kda::delta_chunk_workspace_bytes(qkv_dtype == KDA_BF16, o_dtype == KDA_F32, B, T, H, K, V, packed ? n_seqs : B, packed);
+    return kda::delta_chunk_workspace_bytes(qkv_dtype == KDA_BF16, o_dtype == KDA_F32, B, T, H, K, V, packed);
 }
 
 kda_status kda_delta_chunk_fwd(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const void* g,
@@ -129,7 +129,7 @@ kda_status kda_delta_chunk_fwd(const void* q, const void* k, const void* v, kda_
     if (N == 0) return KDA_OK;
     kda::DeltaArgs a = args_of(q, k, v, qkv_dtype, g, g_dtype, A_log, dt_bias, mode, beta, beta_dtype, initial_state,
                                final_state, cu_seqlens, N, B, T, H, n_qk_heads, K, V, o, o_dtype, flags, stream);
-    const size_t need = kda::delta_chunk_workspace_bytes(a.qkv_bf16, a.o_f32, B, T, H, K, V, N, cu_seqlens != nullptr);
+    const size_t need = kda::delta_chunk_workspace_bytes(a.qkv_bf16, a.o_f32, B, T, H, K, V, cu_seqlens != nullptr);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(KDA_ERR_INVALID_ARG, "workspace smaller than kda_delta_chunk_workspace_bytes()");
     if (!aligned(256, workspace)) return fail(KDA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");

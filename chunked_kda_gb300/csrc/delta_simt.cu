@@ -100,9 +100,9 @@ struct Tile {
     }
 };
 
-// X = (1 + A)^-1 of a strictly lower triangular 64 x 64 matrix, by all threads; Y: 32 x 33 floats between.  The diagonal
+// X = (1 + A)^-1 of a strictly lower triangular 64 x 64 matrix whose rows from len on are 0, by all threads; Y: 32 x 33 floats between.  The diagonal
 // blocks of 16 by substitution, a column a thread, then twice the block below two inverted ones: -X22 (A21 X11).
-__device__ __forceinline__ void invert(const float* A, float* X, float* Y) {
+__device__ __forceinline__ void invert(const float* A, float* X, float* Y, int len) {
     const int tid = threadIdx.x;
     for (int x = tid; x < C * LD; x += NT) X[x] = 0.f;
     __syncthreads();
@@ -120,7 +120,7 @@ __device__ __forceinline__ void invert(const float* A, float* X, float* Y) {
         }
     }
     for (int w = 16; w < C; w *= 2) {
-        for (int o = 0; o < C; o += 2 * w) {
+        for (int o = 0; o + w < len; o += 2 * w) {  // (else the block below is 0)
             __syncthreads();
             for (int x = tid; x < w * w; x += NT) {
                 const int i = x / w, c = x % w;
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q,
         tk.put(sk);
         tq.put(sq);
         __syncthreads();
+        if (4 * ti < len)
 #pragma unroll 4
         for (int c = 0; c < 64; ++c) {
             const float4 a = *reinterpret_cast<const float4*>(sk + c * LD + 4 * ti);
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q,
                         pow2(sI[0][C - 1], sI[1][C - 1]) + nan_if(bad < C));
     }
     __syncthreads();
-    invert(sk, sq, sy);
+    invert(sk, sq, sy, len);
     for (int x = tid; x < C * 16; x += NT) {
         const int r = x >> 4, c = 4 * (x & 15);
         if (r >= len) break;
@@ -261,8 +262,9 @@ __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
 // thread.  W = 4 where such blocks fill the SMs, fewer where not.  Times of a call (heads of 128 x 128): float32, 4 x 4096 tokens,
 // 32 heads 3.2 ms (W = 2: 4.1); 16384 tokens, 8 heads 2.9 (each chunk fetched when its turn came: 4.8); 2048 tokens, 64 heads
 // 1.0, of which 0.2 the first kernel; 128 tokens, 2 heads of 64 x 64 31 us.  bf16 with float32 output, 4 x 4096 tokens, 64
-// heads 6.3 ms (one group with four columns a thread 7.6, with two 9.5); of 256 x 256, 8 x 2048 tokens, 32 heads 9.5
-// (11.2, 13.7).  In FP32 multiply-adds alone the first would be 0.9 ms.
+// heads 6.4 ms (one group with four columns a thread 7.6, with two 9.5); of 256 x 256, 8 x 2048 tokens, 32 heads 9.7
+// (11.2, 13.7).  Short chunks leave out the rows that are none (36 sequences of 7 tokens, 83 heads of 128 x 256: 0.86 ms, with
+// all rows 1.96).  In FP32 multiply-adds alone the first would be 0.9 ms.
 template <typename T, typename OT, int W, int Kp>
 __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                              const T* __restrict__ v, OT* o, Args p) {
@@ -284,10 +286,15 @@ __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict
     else         { bos = n * p.cm.T; eos = bos + p.cm.T; }
     const int Hk = p.H / p.hr, hq = h / p.hr, col = v0 + W * tj;
     const size_t state = ((size_t)n * p.H + h) * (size_t)p.K * p.V;
-    for (int x = threadIdx.x; x < Kp * VB; x += 2 * NT) {
-        const int c = x / VB, d = v0 + x % VB;
-        sS[x] = p.h0 && c < p.K && d < p.V ? p.h0[state + (size_t)c * p.V + d] : 0.f;
+    constexpr int S = Kp * VB / (2 * NT);
+    float s0[S];  // (all asked for before the first is put down)
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        const int x = threadIdx.x + 2 * NT * i, c = x / VB, d = v0 + x % VB;
+        s0[i] = p.h0 && c < p.K && d < p.V ? p.h0[state + (size_t)c * p.V + d] : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < S; ++i) sS[threadIdx.x + 2 * NT * i] = s0[i];
     const T* mine = second ? q : k;
     T* sx = second ? sq : sk;
     float* sl = second ? sp : st;
@@ -350,6 +357,8 @@ __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict
         if (t0 + C < eos) fetch(t0 + C);
         __syncthreads();
         float y[4][W] = {};  // K S or Q S
+        const bool rows = 4 * ti < len;  // (short chunks: the other warps have nothing to do)
+        if (rows)
 #pragma unroll 8
         for (int c = 0; c < Kp; ++c) {
             const float4 a = floats(four(sx + c * LD + 4 * ti));
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict
 #pragma unroll
                 for (int e = 0; e < W; ++e) y[i][e] *= sf[4 * (4 * ti + i) + 1];
             __syncthreads();  // (sr below has been read, su and sr written)
-            lower(sp, su, y);
+            if (rows) lower(sp, su, y);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict
                     y[i][e] = 0.f;
                 }
             bar_sync(1, NT);
-            lower(st, sr, y);
+            if (rows) lower(st, sr, y);
             bar_sync(1, NT);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict
             for (int c0 = 4 * ti; c0 < Kp; c0 += 64) {
                 float add[4][W] = {};
 #pragma unroll 2
-                for (int j = 0; j < C; j += 4) {
+                for (int j = 0; j < len; j += 4) {
                     float u[4][W];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) lds_row<W>(sr + (j + x) * VB + W * tj, u[x]);

@@ -29,7 +29,7 @@
 // Dense calls whose units do not fill the SMs evenly are cut: an SM has the same number of chunks, and a unit's second
 // part takes the state over through scratch.
 //
-// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 610 us (in FP32 without tensor cores 6.3 ms);
+// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 610 us (in FP32 without tensor cores 6.4 ms);
 // 4096 tokens, 152 heads 350; 8192 tokens, 96 heads 673; 20480 tokens, 32 heads 1640 (32 SMs have a unit).  The bytes
 // alone are 160 us of the first.  A chunk is about 10,000 clocks of an SM, and the chain (S 1350, O 1600, R 2200, U
 // 700 and its wait, U' 1200, D 1300) and the preparation (scores 3300, inverse 4300, T 1200) are as long as one another.

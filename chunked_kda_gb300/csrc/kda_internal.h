@@ -209,7 +209,7 @@ cudaError_t launch_gated_norm(const GatedNormArgs& a);
 cudaError_t launch_block_norm(const BlockNormArgs& a);
 cudaError_t launch_short_conv(const ConvArgs& a);
 
-size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, int N, bool packed);
+size_t delta_chunk_workspace_bytes(bool qkv_bf16, bool o_f32, int B, int T, int H, int K, int V, bool packed);
 cudaError_t launch_delta_chunk(const DeltaArgs& a);
 cudaError_t launch_delta_recurrent(const DeltaArgs& a);
 // its tensor-core kernel: bf16, K up to 128

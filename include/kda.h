@@ -445,7 +445,8 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  * of bf16 inputs among it, is computed in FP32.  Scratch is kda_delta_chunk_workspace_bytes (256-byte
  * aligned, NULL when 0; n_seqs 0 for dense inputs): 528 bytes a token and head in FP32; on the tensor
  * cores a state for each sequence and head where they do not fill the multiprocessors evenly, else
- * none.  It is one call's at a time.  status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the
+ * none.  It is one call's at a time.  Dense calls of up to four tokens a sequence (in FP32 and with a
+ * sequence and head for each multiprocessor, sixteen) run token by token, without scratch.  status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the
  * form for single tokens and computes token by token in FP32.
  *
  * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is not

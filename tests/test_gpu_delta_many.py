@@ -56,3 +56,24 @@ def test_a_value_that_is_not_finite_stays_in_its_channel():
     keep[:, 70:, 1, 3] = False
     assert torch.equal(o[keep], clean[keep]) and not torch.isfinite(o[0, 70, 1, 3])
     assert not torch.isfinite(S[0, 1, :, 3]).all() and torch.isfinite(S[0, 1, :, 4]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1, 4, 5, 16, 17])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 40), (100, 7)])
+def test_few_tokens(dtype, T, K, V):
+    for B, H in ((1, 3), (units(1) // 4 + 1, 4)):
+        x = make(B, T, H, K, V, dtype, seed=T + B)
+        check(call(kda.kda_delta_chunk_fwd, x), reference(x), dtype, K)
+        o, S = call(kda.kda_delta_chunk_fwd, x, output_final_state=False)
+        assert S is None and torch.equal(o, call(kda.kda_delta_chunk_fwd, x)[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_short_sequences(dtype):
+    lengths = [7, 1, 0, 5, 16, 17, 3, 31, 33, 2] * 3
+    edges = [0]
+    for n in lengths:
+        edges.append(edges[-1] + n)
+    x = make(1, edges[-1], 8, 128, 72, dtype, edges=edges, seed=12)
+    check(call(kda.kda_delta_chunk_fwd, x, edges=edges), reference(x, edges=edges), dtype, 128)
