@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_words_kernel(const __grid_con
         long at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * (NT / 32);
-            tt[u] = p.per ? (int)__umulhi((uint32_t)r, p.per) : r;
-            const int hh = r - tt[u] * p.heads;
+            const int r = r0 + u * (NT / 32), last = min(r, rows - 1);  // (rows behind the last are formed, too, and not stored)
+            tt[u] = p.per ? (int)__umulhi((uint32_t)last, p.per) : last;
+            const int hh = last - tt[u] * p.heads;
             side[u] = hh >= p.Hq;
             at[u] = (long)(hh - (side[u] ? p.Hq : 0)) * p.D;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(side[u] ? p.x[1] : p.x[0]) +

@@ -46,3 +46,29 @@ def test_packed_tokens_leave_what_is_not_theirs(K, V):
     assert (o[:, 6:] == 7).all()
     for n in (0, 3):
         assert torch.equal(got[1][n].cpu(), x["S0"][n])
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (128, 256), (100, 77), (64, 64)])
+def test_tokens_captured_and_on_other_streams(K, V):
+    xs = [make(2, 1, 3, K, V, torch.bfloat16, seed=s) for s in (61, 62)]
+    want = [call(kda.kda_delta_recurrent_fwd, x) for x in xs]
+    d = {n: t.to("cuda") for n, t in xs[0].items()}
+    S = torch.empty_like(d["S0"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, _ = kda.kda_delta_recurrent_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], initial_state=d["S0"], final_state=S)
+    for x, (wo, wS) in zip(xs, want):
+        for n in d:
+            d[n].copy_(x[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(S, wS)
+    dev, got = [{n: t.to("cuda") for n, t in x.items()} for x in xs], []
+    torch.cuda.synchronize()
+    for y in dev:  # two calls at once
+        got.append(kda.kda_delta_recurrent_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], initial_state=y["S0"],
+                                               output_final_state=True, stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for (o, S), (wo, wS) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(S, wS)
+    assert kda.kda_fused_wait_timeouts() == 0
