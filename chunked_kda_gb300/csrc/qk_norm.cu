@@ -82,14 +82,26 @@ struct Four<__nv_bfloat16> {
         b = make_float2(sm100::bf_lo(v.y), sm100::bf_hi(v.y));
     }
     static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_uint2(sm100::pack_bf16(a.x, a.y), sm100::pack_bf16(b.x, b.y)); }
-    static __device__ __forceinline__ void load8(const __nv_bfloat16* x, float2* v) {
-        const uint4 r = *reinterpret_cast<const uint4*>(x);
-        unpack(make_uint2(r.x, r.y), v[0], v[1]);
-        unpack(make_uint2(r.z, r.w), v[2], v[3]);
+    // P elements (4 or 8) as P / 2 pairs
+    template <int P>
+    static __device__ __forceinline__ void load(const __nv_bfloat16* x, float2* v) {
+        if constexpr (P == 4) {
+            unpack(*reinterpret_cast<const uint2*>(x), v[0], v[1]);
+        } else {
+            const uint4 r = *reinterpret_cast<const uint4*>(x);
+            unpack(make_uint2(r.x, r.y), v[0], v[1]);
+            unpack(make_uint2(r.z, r.w), v[2], v[3]);
+        }
     }
-    static __device__ __forceinline__ void store8(__nv_bfloat16* y, const float2* v) {
-        const uint2 a = pack(v[0], v[1]), b = pack(v[2], v[3]);
-        *reinterpret_cast<uint4*>(y) = make_uint4(a.x, a.y, b.x, b.y);
+    template <int P>
+    static __device__ __forceinline__ void store(__nv_bfloat16* y, const float2* v) {
+        const uint2 a = pack(v[0], v[1]);
+        if constexpr (P == 4) {
+            *reinterpret_cast<uint2*>(y) = a;
+        } else {
+            const uint2 b = pack(v[2], v[3]);
+            *reinterpret_cast<uint4*>(y) = make_uint4(a.x, a.y, b.x, b.y);
+        }
     }
 };
 template <>
@@ -100,13 +112,15 @@ struct Four<float> {
         b = make_float2(v.z, v.w);
     }
     static __device__ __forceinline__ Raw pack(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
-    static __device__ __forceinline__ void load8(const float* x, float2* v) {
-        unpack(reinterpret_cast<const float4*>(x)[0], v[0], v[1]);
-        unpack(reinterpret_cast<const float4*>(x)[1], v[2], v[3]);
+    template <int P>
+    static __device__ __forceinline__ void load(const float* x, float2* v) {
+#pragma unroll
+        for (int e = 0; e < P / 4; ++e) unpack(reinterpret_cast<const float4*>(x)[e], v[2 * e], v[2 * e + 1]);
     }
-    static __device__ __forceinline__ void store8(float* y, const float2* v) {
-        reinterpret_cast<float4*>(y)[0] = pack(v[0], v[1]);
-        reinterpret_cast<float4*>(y)[1] = pack(v[2], v[3]);
+    template <int P>
+    static __device__ __forceinline__ void store(float* y, const float2* v) {
+#pragma unroll
+        for (int e = 0; e < P / 4; ++e) reinterpret_cast<float4*>(y)[e] = pack(v[2 * e], v[2 * e + 1]);
     }
 };
 
@@ -153,7 +167,7 @@ __device__ __forceinline__ void finish(const Params& p, float f, bool weighted, 
     }
 }
 
-// Few rows, or D and R multiples of 8 but not of 16; 16-byte aligned.  A block has `tile` consecutive tokens with all their
+// Few rows, D and R multiples of 8, 16-byte aligned.  A block has `tile` consecutive tokens with all their
 // heads: the angles' cosines and sines are formed once a token, in shared memory, while the first rows are on their way.  A
 // lane has four pairs, LPR lanes a row (D / 8 rounded up to a power of 2).  The next U rows of a lane are on their way while it
 // works on U (U: 1, 2, 3, 4 gave 124, 111, 126 and 129 us for 16384 tokens with 72 heads).
@@ -241,14 +255,15 @@ __global__ void __launch_bounds__(NT, 3) qk_norm_rope_kernel(const __grid_consta
     }
 }
 
-// Many rows, D and R multiples of 16, 16-byte aligned.  A warp has an even share of all groups (up to p.G rows of one token
+// Many rows, D and R multiples of 2 P (16, else 8), 16-byte aligned.  A warp has an even share of all groups (up to p.G rows of one token
 // and side, one behind another) and a ring of their stages in shared memory, which bulk copies fill and empty; it forms
-// the angles of each of its tokens for itself and meets no other warp.  A lane has eight pairs of a row, LPR lanes a row (D / 16
+// the angles of each of its tokens for itself and meets no other warp.  A lane has P pairs of a row, LPR lanes a row (D / 2 P
 // rounded up to a power of 2), so that a warp works on few rows at a time and a token's angles stay in registers.
 // Three stages of 2 KB for 16 warps an SM: 101 us (16384 tokens, 72 heads, rotation) and 57 us (20480, 32, none); two stages
 // 121 and 66, four 101 and 60, six 102 and 63 (more copies under way disturb the stores), three of 4 KB 110 and 61,
-// 24 warps with four 130 and 58.
-template <typename T, int LPR>
+// 24 warps with four 130 and 58.  P = 4 (104 of 128 elements rotated, 16384 tokens, 72 heads): 118 us, a block's rows by ordinary
+// loads 127.
+template <typename T, int P, int LPR>
 __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(const __grid_constant__ Params p) {
     using decay::fma2;
     using decay::mul2;
@@ -301,11 +316,11 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
     };
     for (int s = 0; s < kRingStages; ++s) load(s);
 
-    // the lane's pairs i .. i + 7: elements i and R / 2 + i behind the first half's start, or sixteen in a row
-    const int l = lane % LPR, row = lane / LPR, i = 8 * l;
+    // the lane's pairs i .. i + P - 1: elements i and R / 2 + i behind the first half's start, or 2 P in a row
+    const int l = lane % LPR, row = lane / LPR, i = P * l;
     const bool in = 2 * i < p.D, rot = i < half;
-    const int a = rot && !p.interleaved ? i : 2 * i, b = rot && !p.interleaved ? half + i : 2 * i + 8;
-    float2 co[4] = {}, si[4] = {}, ni[4] = {}, wv[8] = {};
+    const int a = rot && !p.interleaved ? i : 2 * i, b = rot && !p.interleaved ? half + i : 2 * i + P;
+    float2 co[P / 2] = {}, si[P / 2] = {}, ni[P / 2] = {}, wv[P] = {};
     At now = begin;
     long formed = -1;  // the token whose angles are there
     int s = 0, weights = -1;
@@ -325,7 +340,7 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
             __syncwarp();
             if (rot)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < P / 2; ++e) {
                     co[e] = *reinterpret_cast<const float2*>(turns + i + 2 * e);
                     si[e] = *reinterpret_cast<const float2*>(turns + half + i + 2 * e);
                     ni[e] = make_float2(-si[e].x, -si[e].y);
@@ -334,9 +349,9 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
         const float* wt = side ? p.w[1] : p.w[0];
         if (wt && in && weights != side) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < P / 2; ++e) {
                 wv[e] = __ldg(reinterpret_cast<const float2*>(wt + a) + e);
-                wv[4 + e] = __ldg(reinterpret_cast<const float2*>(wt + b) + e);
+                wv[P / 2 + e] = __ldg(reinterpret_cast<const float2*>(wt + b) + e);
             }
             weights = side;
         }
@@ -349,20 +364,20 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
         for (int r0 = 0; r0 < n; r0 += RP) {
             const bool on = r0 + row < n && in;
             T* at_row = x + (r0 + row) * p.D;
-            float2 v[8];
+            float2 v[P];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = make_float2(0.f, 0.f);
+            for (int e = 0; e < P; ++e) v[e] = make_float2(0.f, 0.f);
             if (on) {
-                F::load8(at_row + a, v);
-                F::load8(at_row + b, v + 4);
+                F::template load<P>(at_row + a, v);
+                F::template load<P>(at_row + b, v + P / 2);
             }
             float sum = 0.f;
             if (p.norm != KDA_NORM_NONE) {
-                float2 s2 = mul2(v[0], v[0]), s3 = mul2(v[4], v[4]);
+                float2 s2 = mul2(v[0], v[0]), s3 = mul2(v[P / 2], v[P / 2]);
 #pragma unroll
-                for (int e = 1; e < 4; ++e) {
+                for (int e = 1; e < P / 2; ++e) {
                     s2 = fma2(v[e], v[e], s2);
-                    s3 = fma2(v[4 + e], v[4 + e], s3);
+                    s3 = fma2(v[P / 2 + e], v[P / 2 + e], s3);
                 }
                 sum = (s2.x + s2.y) + (s3.x + s3.y);
 #pragma unroll
@@ -373,27 +388,27 @@ __global__ void __launch_bounds__(NT, kRingBlocks) qk_norm_rope_ring_kernel(cons
             const float2 ff = make_float2(f, f);
             if (wt) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = mul2(v[e], mul2(ff, wv[e]));
+                for (int e = 0; e < P; ++e) v[e] = mul2(v[e], mul2(ff, wv[e]));
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = mul2(v[e], ff);
+                for (int e = 0; e < P; ++e) v[e] = mul2(v[e], ff);
             }
             if (rot && !p.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 first = fma2(v[e], co[e], mul2(v[4 + e], ni[e]));
-                    v[4 + e] = fma2(v[4 + e], co[e], mul2(v[e], si[e]));
+                for (int e = 0; e < P / 2; ++e) {
+                    const float2 first = fma2(v[e], co[e], mul2(v[P / 2 + e], ni[e]));
+                    v[P / 2 + e] = fma2(v[P / 2 + e], co[e], mul2(v[e], si[e]));
                     v[e] = first;
                 }
             } else if (rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < P; ++e) {
                     const float c = e & 1 ? co[e / 2].y : co[e / 2].x, sn = e & 1 ? si[e / 2].y : si[e / 2].x;
                     v[e] = make_float2(v[e].x * c - v[e].y * sn, v[e].y * c + v[e].x * sn);
                 }
             }
-            F::store8(at_row + a, v);
-            F::store8(at_row + b, v + 4);
+            F::template store<P>(at_row + a, v);
+            F::template store<P>(at_row + b, v + P / 2);
         }
         sm100::fence_proxy_async_smem();
         __syncwarp();
@@ -596,7 +611,10 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_any_kernel(const __grid_const
 
 template <typename T>
 cudaError_t run_ring(const QkNormArgs& a, const Params& p, int sms) {
-    auto kern = a.D > 128 ? qk_norm_rope_ring_kernel<T, 16> : a.D > 64 ? qk_norm_rope_ring_kernel<T, 8> : qk_norm_rope_ring_kernel<T, 4>;
+    auto kern = a.D > 128 ? qk_norm_rope_ring_kernel<T, 8, 16> : a.D > 64 ? qk_norm_rope_ring_kernel<T, 8, 8> : qk_norm_rope_ring_kernel<T, 8, 4>;
+    if (a.D % 16 != 0 || a.R % 16 != 0)
+        kern = a.D > 128 ? qk_norm_rope_ring_kernel<T, 4, 32> : a.D > 64 ? qk_norm_rope_ring_kernel<T, 4, 16> : a.D > 32 ? qk_norm_rope_ring_kernel<T, 4, 8>
+               : qk_norm_rope_ring_kernel<T, 4, 4>;
     const int bytes = NT / 32 * (kRingStages * kRingStage + a.R * (int)sizeof(float));
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -662,7 +680,7 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs& a) {
     p.per = p.heads > 1 ? (uint32_t)(((1ull << 32) + p.heads - 1) / p.heads) : 0;
     // Many rows: eight groups a warp, of a kilobyte or more (short ones cost a copy each).  4096 tokens, 40 heads of 128: 19 us, the
     // few rows' kernel 20; below, fewer warps of its own have work: 1024 tokens, 40 heads: 7.8 and 7.8.
-    if (fast && a.D % 16 == 0 && a.R % 16 == 0) {
+    if (fast) {
         p.G = kRingStage / (a.D * e);
         p.q_groups = (p.Hq + p.G - 1) / p.G;
         p.per_token = p.q_groups + (Hk + p.G - 1) / p.G;

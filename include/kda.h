@@ -494,8 +494,7 @@ typedef enum {
  *               (at least Hq D), so that both may be parts of wider rows.  q_out may be q.
  *   k, k_out    the same with Hk heads; Hk = 0: no keys (NULL)
  *               Aligned to their elements; where D and R are multiples of 8 and rows begin
- *               16-byte aligned, rows move as vectors (many rows, where both are multiples of 16, by
- *               bulk copies).
+ *               16-byte aligned, rows move as vectors (many rows by bulk copies).
  *   weights     [D] float32 or NULL (= 1)
  *   positions   int32 [n_axes, tokens], n_axes from 1 to 4 (one for text; time, height and width
  *               for images and video).  R = 0: no rotation, NULL.

@@ -17,6 +17,11 @@ CASES = [  # Hq, Hk, D, R, norm, axes, interleaved, sliced; at least two groups 
     (33, 16, 128, 128, 2, 1, True, False),
     (70, 0, 32, 16, 0, 1, False, False),
     (65, 65, 16, 16, 1, 4, False, True),
+    # multiples of 8 only
+    (16, 4, 128, 104, 1, 1, False, True),
+    (13, 13, 40, 40, 2, 1, False, False),
+    (9, 5, 248, 56, 1, 2, True, True),
+    (40, 0, 24, 8, 0, 1, False, False),
     # heads or rotations that are not whole vectors
     (5, 2, 244, 36, 1, 2, False, True),
     (7, 1, 130, 130, 2, 1, False, False),
