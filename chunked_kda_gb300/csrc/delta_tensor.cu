@@ -12,11 +12,14 @@
 //   U^T = R^T T^T with R = V - diag(2^G) Y;   O2^T = U^T P^T;   D^T = U'^T k with U' = diag(2^(G_l - G)) U, added to S^T.
 // Row norms of q and k, where the call asks for them, are factors of rows as well.
 //
-// Roundings.  The state is a float32 output and feeds every later chunk: what leads to it has 24 bits.  S, R, T and
+// Roundings.  The state is a float32 output and feeds every later chunk: its operands have 24 bits.  S, R, T and
 // U' are operands as three bf16 terms each (the products of R and T without the three smallest), a chunk's addition
-// is summed by itself and added to S in rounded FP32, S is held in registers between chunks.  The output is bf16:
-// O1 reads S's first two terms (with the first alone an output was off by up to 1.4 times its own rounding, and no call
-// was faster), O2 is a tf32 product of U as it stands in TMEM (cut) and P.
+// is summed by itself and added to S in rounded FP32, S is held in registers between chunks.  The factors 2^(G_i - G_j) of A
+// and P are the hardware's powers (2^-22).  The output is bf16, and its operands have 16 bits, 2^-16 of each term: O1 reads
+// S's first two terms (with the first alone an output was off by up to 1.4 times its own rounding, and no call was faster),
+// O2 is formed of U's and P's first two, without the product of the second ones.  (U cut to tf32's 11 bits as it stood in
+// TMEM and P rounded to them: 606 us in place of 621 for 4 x 4096 tokens, 64 heads, and the chunk's part of an output
+// too small by 3.5e-4 on average, up to 2^-10 of its terms.)
 //
 // What is not finite must not reach back through masked zeros (0 times it is NaN).  A gate, beta or key: the rows from
 // its token on are treated like rows behind the sequence, and the outputs from there on and the state are NaN.  A
@@ -61,7 +64,7 @@ enum { B_KQ = 0, B_V = B_KQ + NKQ, B_G, B_F = B_G + NG, B_SC = B_F + 2, B_SCREAD
 
 // shared memory: stages of k and q (by 64 channels: 64 rows of k, then of q), of v; T's terms; P and, behind its reader, the
 // staged output; the third term of R and U'; the matrix of the inverse
-constexpr uint32_t KQ_BYTES = 32768, PANEL = 16384, QROWS = 8192, V_BYTES = 16384, T_TERM = 8192;
+constexpr uint32_t KQ_BYTES = 32768, PANEL = 16384, QROWS = 8192, V_BYTES = 16384, T_TERM = 8192, P_TERM = 8192;
 constexpr uint32_t L_KQ = 0, L_V = L_KQ + NKQ * KQ_BYTES, L_T = L_V + V_BYTES, L_P = L_T + 3 * T_TERM, L_LO = L_P + NP * 16384;
 constexpr uint32_t L_X = L_LO + 16384, LDX = 68, L_G = L_X + 64 * LDX * 4;
 // a chunk's factors, one slot of a ring of NG: byte offsets of its float arrays
@@ -188,6 +191,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
         " mov.b64 {%0, %1}, z;\n}\n" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+__device__ __forceinline__ void sts_pair(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
@@ -490,9 +496,13 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         umma_bf16_ta(tmem + TD, tmem + TZ + 32 * t + 8 * kk, desc(k + kk * 128), idesc_bf16(128, KD, 0, 1), 1);
                 umma_commit(sy.bar(B_D));
                 umma_commit(sy.bar(B_KQFREE + c % NKQ));
+#pragma unroll 1
+                for (int x = 0; x < 3; ++x) {  // P's terms 1, 0, 0 with U's 0, 1, 0
+                    const uint32_t u = x == 1 ? 8 : 0, pt = P + (x == 0 ? P_TERM >> 4 : 0);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_tf32_ta(tmem + TSC, tmem + TY + 8 * kk, desc(P + (kk >> 2) * 512 + (kk & 3) * 2), idesc_tf32(128, 64), 1);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ta(tmem + TSC, tmem + TY + 16 * kk + u, desc(pt + kk * 2), idesc_bf16(128, 64, 0, 0), 1);
+                }
                 umma_commit(sy.bar(B_O2));
             }
             __syncwarp();
@@ -844,14 +854,25 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const float2 f[2] = {lds2(upd), lds2(upd + 32)};
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 u = make_float2(a[2 * e], a[2 * e + 1]);
-                    odd = fma2(u, zero, odd);
-                    x[e] = mul2(f[e >> 1], u);
-                }
-                // (U itself is O2's operand)
-                if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f))
+                for (int e = 0; e < 4; ++e) odd = fma2(make_float2(a[2 * e], a[2 * e + 1]), zero, odd);
+                if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) {
                     clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
+                    ld16x16(tf + TY + r, a);
+                    tmem_wait_ld();
+                }
+                uint32_t t[4];  // U's two terms for O2, where its sixteen columns were
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 u = make_float2(a[2 * e], a[2 * e + 1]);
+                    x[e] = mul2(f[e >> 1], u);
+                    t[e] = round2(u);
+                    a[2 * e] = u.x;
+                    a[2 * e + 1] = u.y;
+                }
+                st16x8(tf + TY + r, t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = pack_bf16(a[2 * e], a[2 * e + 1]);
+                st16x8(tf + TY + r + 8, t);
                 write_fragments(r, x);
             }
             tmem_wait_st();
@@ -881,7 +902,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool qnorm = (p.flags & KDA_FLAG_Q_L2NORM) != 0, knorm = (p.flags & KDA_FLAG_K_L2NORM) != 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
-            const uint32_t gt = gates(c), P = sb + L_P + (c % NP) * 16384 + (c0 >> 5) * 8192;
+            const uint32_t gt = gates(c), P = sb + L_P + (c % NP) * 16384;
             if (w == 16) {
                 sy.wait(B_G + c % NG, (c / NG) & 1);
                 if (c >= NP) sy.wait(B_OFREE + c % NP, (c / NP - 1) & 1);  // P's place
@@ -919,7 +940,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bar_sync(2, NPREP);
             }
             const int full = __float_as_int(lds(gt + GT_LEN));
-            // A's rows (lanes with keys) in X, P's rows (with queries) as a tf32 operand: the score times
+            // A's rows (lanes with keys) in X, P's rows (with queries) as two bf16 terms: the score times
             // f 2^(G_i - G_j), 0 where j > last.  Left of the row's 32 the factor parts into the row's and the column's,
             // both <= 1; within them each is formed by itself.
             const int last = i < full ? i - (query ? 0 : 1) : -1;
@@ -927,7 +948,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             float2 odd = make_float2(0.f, 0.f);
             const float r0 = ex2_fast((gi + lds(gt + GT_G + 4 * 15)) + (gf + lds(gt + GT_G + 256 + 4 * 15)));
             const float r1 = ex2_fast((gi + lds(gt + GT_G + 4 * 31)) + (gf + lds(gt + GT_G + 256 + 4 * 31)));
-            const uint32_t to = query ? P + 128 * i : X + 4 * (LDX * i + c0), turn = query ? (i & 7) << 4 : 0;  // (16-byte pieces at ^ turn)
+            const uint32_t to = query ? P + 128 * i : X + 4 * (LDX * i + c0), turn = (i & 7) << 4 ^ 2 * c0;  // (P's 16-byte pieces at ^ turn)
             const bool left = hi && c0 == 0;
             const uint32_t gs = gt + 4 * c0;
             float4 gj = lds4(gs + (left ? GT_COL : GT_G)), fj = lds4(gs + GT_G + 256);
@@ -962,8 +983,12 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     odd = fma2(make_float2(y.x, y.y), make_float2(0.f, 0.f), odd);
                     odd = fma2(make_float2(y.z, y.w), make_float2(0.f, 0.f), odd);
                 }
-                if (query) st_s128(to + ((4 * e) ^ turn), to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w));
-                else if (some) st_s128(to + 4 * e, __float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z), __float_as_uint(y.w));
+                if (query) {
+                    float2 ya = make_float2(y.x, y.y), yb = make_float2(y.z, y.w);
+                    const uint32_t at = to + (((2 * e & ~15) ^ turn) | (2 * e & 8)), a0 = round2(ya), b0 = round2(yb);
+                    sts_pair(at, a0, b0);
+                    sts_pair(at + P_TERM, pack_bf16(ya.x, ya.y), pack_bf16(yb.x, yb.y));
+                } else if (some) st_s128(to + 4 * e, __float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z), __float_as_uint(y.w));
             }
             // a row of A that is not finite: its key is not, or one before it
             const unsigned none = __ballot_sync(0xffffffffu, !query && (odd.x != 0.f || odd.y != 0.f));

@@ -440,14 +440,16 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  *     O = ( diag(e^G) Q S + (exp(G_i - G_j) q_i . k_j)_{j <= i} U ) / sqrt(K)
  *     S <- e^G_l S + K^T diag(e^(G_l - G)) U
  * bf16 inputs with bf16 output, K <= 128 and K and V multiples of 8 run on the tensor cores: the
- * state, and what leads to it, has FP32's 24 bits; the bf16 output is formed from the state's first 16
- * bits and 11 bits of P, far below its own rounding.  All else, float32 output
- * of bf16 inputs among it, is computed in FP32.  Scratch is kda_delta_chunk_workspace_bytes (256-byte
- * aligned, NULL when 0; n_seqs 0 for dense inputs): 528 bytes a token and head in FP32; on the tensor
- * cores a state for each sequence and head where they do not fill the multiprocessors evenly, else
- * none.  It is one call's at a time.  Dense calls of up to four tokens a sequence (in FP32 and with a
- * sequence and head for each multiprocessor, sixteen) run token by token, without scratch.  status as for kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the
- * form for single tokens and computes token by token in FP32.
+ * operands of the state and of what leads to it have FP32's 24 bits (the factors exp(G_i - G_j)
+ * are off by up to 2^-22); those of the bf16 output, the state, P and U, have 16, so that it is off
+ * by its own rounding and at most 3 x 2^-16 of the sum of the absolute values of its terms.  All
+ * else, float32 output of bf16 inputs among it, is computed in FP32.  Scratch is
+ * kda_delta_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for dense inputs): 528
+ * bytes a token and head in FP32; on the tensor cores a state for each sequence and head where
+ * they do not fill the multiprocessors evenly, else none.  It is one call's at a time.  Dense calls
+ * of up to four tokens a sequence (in FP32 and with a sequence and head for each multiprocessor,
+ * sixteen) run token by token, without scratch.  status as for kda_chunk_fwd_ex.
+ * kda_delta_recurrent_fwd is the form for single tokens and computes token by token in FP32.
  *
  * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is not
  * finite (with KDA_FLAG_K_L2NORM, a key whose sum of squares is not) reaches the outputs of its head
