@@ -50,20 +50,21 @@ template <typename InT, typename OutT, int NT, int E>
 __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out, const InT* __restrict__ q,
     const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags, const float* h0, float* hT,
-    const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o) {
+    const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o, int* status, bool stall) {
     constexpr int kPart = E * NT;  // partial S^T k, then S^T q, a row of a block's columns for each group of threads
     extern __shared__ __align__(128) float sm[];  // the partial products, [K][BV] the state
     __shared__ float s_q[256], s_k[256], s_dot[3][NT / 32];
-    __shared__ __align__(8) uint64_t s_bar;
+    __shared__ __align__(8) uint64_t s_bar[2];  // the state's, and one that nothing completes
     float* part = sm;
     const int tid = threadIdx.x, v0 = blockIdx.x * BV, h = blockIdx.y, n = blockIdx.z, cols = min(BV, V - v0);
-    const uint32_t bar = smem_u32(&s_bar);
+    const uint32_t bar = smem_u32(s_bar);
     const size_t st = ((size_t)n * H + h) * (size_t)K * V + v0;
     // a whole state may begin and end inside a bulk copy's 16 bytes: its first and last floats go one by one
     const int off = E == 4 ? 0 : (int)(st & 3), edge = min((4 - off) & 3, K * BV), body = (K * BV - edge) & ~3, end = K * BV - edge - body;
     float* state = sm + 2 * kPart + off;
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(bar + 8, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -90,12 +91,17 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     const Gates::Head head = gates.head(h);
     const float scale = rsqrtf((float)K);
     bool waiting = h0 != nullptr;
-    auto state_here = [&] {
-        if (waiting && !mbar_wait(bar, 0)) {
-            if (tid == 0) atomicAdd(&g_token_timeouts, 1u);
-            mbar_wait(bar, 0);  // (once more: no copy is to be in flight when the block ends)
-        }
+    // The state is there for the whole block, or (true) a wait has given up: then the block waits for the copy once more, so
+    // that none is in flight when it ends, and ends without a store (hT may be the only place that still holds the state).
+    auto gave_up = [&] {
         waiting = false;
+        if (!__syncthreads_or(!(stall ? mbar_wait(bar + 8, 0, 256) : mbar_wait(bar, 0)))) return false;
+        mbar_wait(bar, 0);
+        if (tid == 0) {
+            atomicAdd(&g_token_timeouts, 1u);
+            if (status) atomicOr(status, KDA_DEVICE_WAIT_GAVE_UP);
+        }
+        return true;
     };
     Columns<E>* S = reinterpret_cast<Columns<E>*>(state) + piece;
     for (long t = bos; t < eos; ++t) {
@@ -127,8 +133,8 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
             for (int m = 16; m > 0; m >>= 1) dots[e] += __shfl_xor_sync(0xffffffffu, dots[e], m);
             if ((tid & 31) == 0) s_dot[e][tid >> 5] = dots[e];
         }
-        state_here();
-        __syncthreads();
+        if (!waiting) __syncthreads();
+        else if (gave_up()) return;
         Columns<E> y{}, z{};
         if (on) {
 #pragma unroll 4
@@ -186,8 +192,7 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
         }
         __syncthreads();
     }
-    state_here();
-    if (!hT) return;
+    if ((waiting && gave_up()) || !hT) return;
     fence_proxy_async_smem();
     __syncthreads();
     // (this block has read its part of h0 and no other touches it: hT may be h0)
@@ -328,7 +333,8 @@ cudaError_t launch_token(const DeltaArgs& a, int BV) {
     CUtensorMap in{}, out{};
     if (BV < a.V && ((a.h0 && !state_map(&in, a.h0, a, BV)) || (a.hT && !state_map(&out, a.hT, a, BV)))) return cudaErrorInvalidValue;
     kern<<<dim3((a.V + BV - 1) / BV, a.H, a.N), NT, bytes, a.stream>>>(in, out, (const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a),
-                                                                     a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV, (OutT*)a.o);
+                                                                     a.flags, a.h0, a.hT, a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, BV, (OutT*)a.o,
+                                                                     a.status, hook_stall_chunk() == 0);
     return cudaGetLastError();
 }
 

@@ -563,13 +563,15 @@ kda_status kda_short_conv_fwd(const void* x, kda_dtype dtype, const float* weigh
 /*
  * Diagnostics of the tensor-core paths' bounded waits.  Every mbarrier wait of the fused
  * and two-pass chunked kernels, of the chunked decayed attention, of the gated delta rule in both
- * forms, of the norm and rotation of many rows and of the block norm of many long rows gives up after a fixed number of polls; a CTA whose wait gave
- * up adds to a per-device counter, stops waiting, issuing MMAs and copies, lets the ones in
- * flight finish (bounded), frees its TMEM and returns, so the context stays usable but that
- * launch's outputs are not valid.  kda_fused_wait_timeouts writes the counters of the current
- * device to *count (their sum, 0 after normal runs) and zeroes them when reset != 0.  It copies from the device
- * and therefore synchronises with it: a diagnostic call, not for the hot path.  Null count:
- * KDA_ERR_INVALID_ARG; a failing copy: KDA_ERR_CUDA.
+ * forms, of the norm and rotation of many rows and of the block norm of many long rows gives up
+ * after a fixed number of polls; a CTA whose wait gave up adds to a per-device counter, stops
+ * waiting, issuing MMAs and copies, lets the ones in flight finish (bounded), frees its TMEM and
+ * returns, so the context stays usable but that launch's outputs are not valid (a CTA of the
+ * delta rule's single tokens stores nothing: a state in place is still there).
+ * kda_fused_wait_timeouts writes the counters of the current device to *count (their sum, 0 after
+ * normal runs) and zeroes them when reset != 0.  It copies from the device and therefore
+ * synchronises with it: a diagnostic call, not for the hot path.  Null count: KDA_ERR_INVALID_ARG;
+ * a failing copy: KDA_ERR_CUDA.
  */
 kda_status kda_fused_wait_timeouts(unsigned int* count, int reset);
 
@@ -577,7 +579,9 @@ kda_status kda_fused_wait_timeouts(unsigned int* count, int reset);
  * Test hooks of the tensor-core paths, process-wide, all off by default and read by nothing
  * else (no environment variables).  For tests only; set them back to (-1, 0, 0, 0) afterwards.
  *   wait_timeout_chunk  >= 0: every CTA of later fused launches, of the two-pass state
- *                       chain and of the chunked gated delta rule on the tensor cores waits, at that chunk and with a short limit, on an mbarrier
+ *                       chain and of the chunked gated delta rule on the tensor cores (and, at
+ *                       chunk 0, of its single tokens, where a state is given) waits, at that
+ *                       chunk and with a short limit, on an mbarrier
  *                       nothing completes, and takes the give-up path (counted by
  *                       kda_fused_wait_timeouts, flagged in the status word of
  *                       kda_chunk_fwd_ex); -1: off
