@@ -44,12 +44,14 @@ struct alignas(4 * E) Columns {
     float e[E];
 };
 
+// o may be v, so neither is __restrict__: all reads of a token's values are in front of the barrier behind which one thread
+// writes its output there.
 // BV: columns of a block, E those of a thread.  All of V: a block's rows lie side by side; else they come and go by the
 // tensor maps.
 template <typename InT, typename OutT, int NT, int E>
 __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out, const InT* __restrict__ q,
-    const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags, const float* h0, float* hT,
+    const InT* __restrict__ k, const InT* v, Gates gates, unsigned flags, const float* h0, float* hT,
     const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int BV, OutT* o, int* status, bool stall) {
     constexpr int kPart = E * NT;  // partial S^T k, then S^T q, a row of a block's columns for each group of threads
     extern __shared__ __align__(128) float sm[];  // the partial products, [K][BV] the state
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
 
 template <typename InT, typename OutT, int RG>
 __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
-    const InT* __restrict__ q, const InT* __restrict__ k, const InT* __restrict__ v, Gates gates, unsigned flags,
+    const InT* __restrict__ q, const InT* __restrict__ k, const InT* v, Gates gates, unsigned flags,
     const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int vblocks, long units,
     OutT* o) {
     constexpr int R = 16, COLS = 128 / RG;  // rows of a lane, columns of a warp
@@ -278,6 +280,7 @@ __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
         const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(qq + kQNormEps) : 1.f;
         const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(kk + kQNormEps) : 1.f;
         const float fs = scale * nq;
+        __syncwarp();  // (every lane has its values)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             u[j] = rate * (u[j] - dec * nk * y[j]);

@@ -256,7 +256,8 @@ __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
 
 // grid (V blocks, H, sequences).  Two groups of 256 threads: the first has K S, U and the state, the second Q S, P U and the
 // output; a thread four rows of a chunk and W of the block's VB = 16 W columns.  Kp: K rounded up to 64, 128 or 256.  The
-// next chunk is on its way into registers while this one is worked on.
+// next chunk is on its way into registers while this one is worked on.  o may be v, so neither is __restrict__: a block reads
+// its columns of a chunk's values before it writes them, and no other block has them.
 //
 // Loads from shared memory bound it (70 to 73 % of their rate, of L1's 82 to 88): 16 multiply-adds take eight floats a
 // thread.  W = 4 where such blocks fill the SMs, fewer where not.  Times of a call (heads of 128 x 128): float32, 4 x 4096 tokens,
@@ -267,7 +268,7 @@ __device__ __forceinline__ void lds_row(const float* p, float (&r)[W]) {
 // all rows 1.96).  In FP32 multiply-adds alone the first would be 0.9 ms.
 template <typename T, typename OT, int W, int Kp>
 __global__ void __launch_bounds__(2 * NT) delta_chain_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                             const T* __restrict__ v, OT* o, Args p) {
+                                                             const T* v, OT* o, Args p) {
     constexpr int VB = 16 * W;
     extern __shared__ __align__(16) float sm[];
     float* st = sm;               // [64][LD] T, transposed
