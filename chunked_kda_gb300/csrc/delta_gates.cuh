@@ -42,5 +42,11 @@ struct Gates {
     __device__ __forceinline__ float rate(size_t t, int h) const { return rate_of(raw_rate(t, h)); }
 };
 
+// 1 / |x| of a query or key from its sum of squares.  A sum that is not finite makes the row none (0, as 1 / sqrt gives it
+// for what overflows, would leave the row out in silence).
+__device__ __forceinline__ float row_norm(float sum) {
+    return fabsf(sum) < __int_as_float(0x7f800000) ? rsqrtf(sum + kQNormEps) : __int_as_float(0x7fffffff);
+}
+
 }  // namespace delta
 }  // namespace kda

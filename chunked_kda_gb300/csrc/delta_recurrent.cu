@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
             for (int e = 0; e < 3; ++e)
 #pragma unroll
                 for (int x = 0; x < NT / 32; ++x) d[e] += s_dot[e][x];
-            const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(d[0] + kQNormEps) : 1.f;
-            const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(d[1] + kQNormEps) : 1.f;
+            const float nq = flags & KDA_FLAG_Q_L2NORM ? row_norm(d[0]) : 1.f;
+            const float nk = flags & KDA_FLAG_K_L2NORM ? row_norm(d[1]) : 1.f;
             auto total = [&](const float* from) {
                 Columns<E> s{};
 #pragma unroll 4
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
                 z[j] += __shfl_xor_sync(0xffffffffu, z[j], m);
             }
         }
-        const float nq = flags & KDA_FLAG_Q_L2NORM ? rsqrtf(qq + kQNormEps) : 1.f;
-        const float nk = flags & KDA_FLAG_K_L2NORM ? rsqrtf(kk + kQNormEps) : 1.f;
+        const float nq = flags & KDA_FLAG_Q_L2NORM ? row_norm(qq) : 1.f;
+        const float nk = flags & KDA_FLAG_K_L2NORM ? row_norm(kk) : 1.f;
         const float fs = scale * nq;
         __syncwarp();  // (every lane has its values)
 #pragma unroll

@@ -194,10 +194,10 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const T* __restrict__ q,
         if (tid < C && (p.flags & KDA_FLAG_Q_L2NORM))
             for (int c = 0; c < 64; ++c) nq = fmaf(sq[c * LD + tid], sq[c * LD + tid], nq);
     }
-    if (tid < C) s_nq[tid] = p.flags & KDA_FLAG_Q_L2NORM ? rsqrtf(nq + kQNormEps) : 1.f;
+    if (tid < C) s_nq[tid] = p.flags & KDA_FLAG_Q_L2NORM ? row_norm(nq) : 1.f;
     if (ti == tj)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_nk[4 * ti + i] = p.flags & KDA_FLAG_K_L2NORM ? rsqrtf(kk[i][i] + kQNormEps) : 1.f;
+        for (int i = 0; i < 4; ++i) s_nk[4 * ti + i] = p.flags & KDA_FLAG_K_L2NORM ? row_norm(kk[i][i]) : 1.f;
     __syncthreads();
     const float scale = rsqrtf((float)p.K);
     const int bad = s_bad;

@@ -928,8 +928,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bar_sync(2, NPREP);
                 if (c0 == 0) {
                     const float sum = n2 + lds(X + 4 * (LDX * i + (query ? 66 : 65)));
-                    sts(query ? sb + L_RQ + 256 * (c & 1) + 4 * i : X + 4 * (LDX * i + 64),
-                        on && (query || finite(sum)) ? rsqrtf(sum + kQNormEps) : 1.f);
+                    // (NaN behind the sequence, too, perhaps: what it is a factor of does not count)
+                    sts(query ? sb + L_RQ + 256 * (c & 1) + 4 * i : X + 4 * (LDX * i + 64), on ? row_norm(sum) : 1.f);
                 }
                 bar_sync(2, NPREP);
                 rk = lds(X + 4 * (LDX * i + 64));

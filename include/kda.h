@@ -451,9 +451,10 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  * sixteen) run token by token, without scratch.  status as for kda_chunk_fwd_ex.
  * kda_delta_recurrent_fwd is the form for single tokens and computes token by token in FP32.
  *
- * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is not
- * finite (with KDA_FLAG_K_L2NORM, a key whose sum of squares is not) reaches the outputs of its head
- * from its token on, a value those of its channel, a query its own row.
+ * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is
+ * not finite reaches the outputs of its head from its token on, a value those of its channel, a
+ * query its own row.  A key or query whose norm is asked for counts as not finite where its sum of
+ * squares is not.
  */
 size_t kda_delta_chunk_workspace_bytes(kda_dtype qkv_dtype, kda_dtype o_dtype, int B, int T, int H,
                                        int K, int V, int n_seqs);
