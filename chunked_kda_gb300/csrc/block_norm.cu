@@ -447,7 +447,8 @@ cudaError_t launch_block(const BlockNormArgs& a) {
         if (stages >= 2 && a.rows >= 8l * sms) {
             auto kern = block_norm_ring_kernel<T, R>;
             const int bytes = stages * row_bytes;
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            // (the limit is the kernel's, not the call's: the same for all, so that calls of several host threads do not meet in it)
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
             if (e != cudaSuccess) return e;
             kern<<<2 * sms, kRingThreads, bytes, a.stream>>>(a, stages);
             return cudaGetLastError();

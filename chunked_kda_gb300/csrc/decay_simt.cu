@@ -313,7 +313,9 @@ cudaError_t run(const DecayArgs& a) {
     if (slots > 0) {
         auto kern = decay_out_kernel<T, OT>;
         const int bytes = ((a.K + 31) / 32 * 32 + C + 32) * LD * (int)sizeof(float);
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        // (the limit is the kernel's, not the call's: the same for all, so that calls of several host threads do not meet in it)
+        constexpr int most = (256 + C + 32) * LD * (int)sizeof(float);
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
         kern<<<dim3(slots, a.H), NT, bytes, a.stream>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (OT*)a.o, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (a.hT && a.hT == a.h0) {

@@ -331,7 +331,10 @@ template <typename InT, typename OutT, int NT, int E = 4>
 cudaError_t launch_token(const DeltaArgs& a, int BV) {
     auto kern = delta_token_kernel<InT, OutT, NT, E>;
     const int bytes = (a.K * BV + 2 * E * NT + (E == 4 ? 0 : 4)) * (int)sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // the kernel's limit is what the largest call wants (a column block of a tile is up to four columns more), whatever this one
+    // does: it is the function's, and another host thread's call may be between its own and the launch
+    constexpr int most = ((E == 4 ? kTile + 4 * 256 : kWhole + 4) + 2 * E * NT) * (int)sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     CUtensorMap in{}, out{};
     if (BV < a.V && ((a.h0 && !state_map(&in, a.h0, a, BV)) || (a.hT && !state_map(&out, a.hT, a, BV)))) return cudaErrorInvalidValue;

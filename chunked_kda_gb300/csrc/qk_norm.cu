@@ -616,7 +616,9 @@ cudaError_t run_ring(const QkNormArgs& a, const Params& p, int sms) {
         kern = a.D > 128 ? qk_norm_rope_ring_kernel<T, 4, 32> : a.D > 64 ? qk_norm_rope_ring_kernel<T, 4, 16> : a.D > 32 ? qk_norm_rope_ring_kernel<T, 4, 8>
                : qk_norm_rope_ring_kernel<T, 4, 4>;
     const int bytes = NT / 32 * (kRingStages * kRingStage + a.R * (int)sizeof(float));
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // (the limit is the kernel's, not the call's: what the largest one wants, so that calls of several host threads do not meet in it)
+    constexpr int most = NT / 32 * (kRingStages * kRingStage + kMaxD * (int)sizeof(float));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     kern<<<kRingBlocks * sms, NT, bytes, a.stream>>>(p);
     return cudaGetLastError();
