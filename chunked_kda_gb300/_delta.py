@@ -4,6 +4,8 @@ the other operators around the recurrence.
 """
 from __future__ import annotations
 
+from operator import index
+
 import torch
 
 import chunked_kda_gb300 as _kda
@@ -165,7 +167,8 @@ def kda_qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, norm=_kda.NORM
         pp = _arg(positions, "positions", dev, _I32, (B, T) if positions.dim() == 2 else (n_axes, B, T))
         pf = _arg(inv_freq, "inv_freq", dev, _F32, inv_freq.shape)
         if pair_axes is not None:
-            if len(pair_axes) != R // 2 or any(not 0 <= a < n_axes for a in pair_axes):
+            pair_axes = [index(a) for a in pair_axes]  # (bytes() of an array would be its memory)
+            if len(pair_axes) != R // 2 or not set(pair_axes) <= set(range(n_axes)):
                 raise ValueError("pair_axes needs R/2 integers below the number of axes")
             axes = bytes(pair_axes)
     elif inv_freq is not None or pair_axes is not None:
