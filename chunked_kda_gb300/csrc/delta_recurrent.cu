@@ -19,9 +19,9 @@
 // chunked kernels are faster (64 sequences of 16 tokens, bf16: 358, chunked 173).
 //
 // V not a multiple of 4: the same with two columns or one a thread, where a state fits shared memory whole (128 x 126: 99 % of
-// a copy's rate, 100 x 253 82, 99 x 77 75).  Larger ones: a warp has a block of columns with all rows in registers, RG groups of
-// lanes with 16 rows each (K rounded up to 16 RG: 64, 128 or 256, rows and columns beyond K and V masked), joined by shuffles;
-// its rows begin at any four bytes, and single loads are what bounds it (236 x 253: 27 %).
+// a copy's rate, 100 x 253 82, 99 x 77 75).  Larger ones (K from 212 on): a warp has eight columns with all rows in registers, sixteen
+// pairs of lanes with 16 rows each (rows and columns beyond K and V masked), joined by shuffles; its rows begin at any
+// four bytes, and single loads are what bounds it (236 x 253: 27 %).
 #include "common.cuh"
 #include "delta_gates.cuh"
 #include "kda_internal.h"
@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(NT, 768 / NT) delta_token_kernel(
     if (tid < end) hT[st + edge + body + tid] = state[edge + body + tid];
 }
 
-template <typename InT, typename OutT, int RG>
+constexpr int RG = 16, R = 16, COLS = 128 / RG;  // groups of lanes, rows of a lane, columns of a warp
+template <typename InT, typename OutT>
 __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
     const InT* __restrict__ q, const InT* __restrict__ k, const InT* v, Gates gates, unsigned flags,
     const float* h0, float* hT, const int32_t* __restrict__ cu, int T, int H, int hr, int K, int V, int vblocks, long units,
     OutT* o) {
-    constexpr int R = 16, COLS = 128 / RG;  // rows of a lane, columns of a warp
     const int lane = threadIdx.x & 31, rg = lane / (32 / RG);
     const long unit = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (unit >= units) return;
@@ -305,14 +305,13 @@ __global__ void __launch_bounds__(256, 2) delta_recurrent_kernel(
     }
 }
 
-template <typename InT, typename OutT, int RG>
+template <typename InT, typename OutT>
 cudaError_t launch_r(const DeltaArgs& a) {
-    constexpr int COLS = 128 / RG;
     const int vblocks = (a.V + COLS - 1) / COLS;
     const long units = (long)a.N * a.H * vblocks;
     const long blocks = (units + 7) / 8;
     if (blocks > 0x7fffffffl) return cudaErrorInvalidValue;
-    delta_recurrent_kernel<InT, OutT, RG><<<(unsigned)blocks, 256, 0, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a), a.flags, a.h0, a.hT,
+    delta_recurrent_kernel<InT, OutT><<<(unsigned)blocks, 256, 0, a.stream>>>((const InT*)a.q, (const InT*)a.k, (const InT*)a.v, Gates(a), a.flags, a.h0, a.hT,
                                                  a.cu, a.T, a.H, a.H / a.Hk, a.K, a.V, vblocks, units, (OutT*)a.o);
     return cudaGetLastError();
 }
@@ -358,7 +357,7 @@ cudaError_t launch_k(const DeltaArgs& a) {
         if (a.V % 2 == 0) return small ? launch_token<InT, OutT, 128, 2>(a, a.V) : launch_token<InT, OutT, 256, 2>(a, a.V);
         return small && a.V <= 128 ? launch_token<InT, OutT, 128, 1>(a, a.V) : launch_token<InT, OutT, 256, 1>(a, a.V);
     }
-    return a.K <= 64 ? launch_r<InT, OutT, 4>(a) : a.K <= 128 ? launch_r<InT, OutT, 8>(a) : launch_r<InT, OutT, 16>(a);
+    return launch_r<InT, OutT>(a);
 }
 
 }  // namespace
