@@ -1055,7 +1055,9 @@ bool delta_tensor_dims(bool bf16, int K, int V) { return bf16 && K % 8 == 0 && K
 
 namespace delta {
 namespace {
-// Chunks that cuts cost an SM.
+// Chunks that cuts cost an SM (a state's way through memory, another piece's start).  us cut / whole, heads of 128: 240 units of 8
+// chunks (13 an SM for the 16 of two waves) 110/111, 160 of 4 (5 for 8) 55/64, 256 of 16 (27 for 32) 188/196, 256 of 64 (108 for 128)
+// 621/700, 160 of 64 (68 for 128) 401/692.
 constexpr int kCutCost = 3;
 struct Plan {
     int per, pieces;

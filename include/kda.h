@@ -447,9 +447,10 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  * kda_delta_chunk_workspace_bytes (256-byte aligned, NULL when 0; n_seqs 0 for dense inputs): 528
  * bytes a token and head in FP32; on the tensor cores a state for each sequence and head where
  * they do not fill the multiprocessors evenly, else none.  It is one call's at a time.  Dense calls
- * of up to four tokens a sequence (in FP32 and with a sequence and head for each multiprocessor,
- * sixteen) run token by token, without scratch.  status as for kda_chunk_fwd_ex.
- * kda_delta_recurrent_fwd is the form for single tokens and computes token by token in FP32.
+ * of a few tokens a sequence (up to three, five or seven, in FP32 six, twelve or sixteen, by the
+ * number of sequences and heads) run token by token, without scratch.  status as for
+ * kda_chunk_fwd_ex.  kda_delta_recurrent_fwd is the form for single tokens and computes token by
+ * token in FP32.
  *
  * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is
  * not finite reaches the outputs of its head from its token on, a value those of its channel, a
