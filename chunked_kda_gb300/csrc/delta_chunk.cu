@@ -1,7 +1,7 @@
 // The gated delta rule with a decay for each head, the form for prompts: which kernels run it.  On the tensor cores where
 // the operands' types hold what the call is given and asked for: bf16 inputs and output, heads that TMA's 16-byte rows and
-// a panel of 128 key channels take (4 x 4096 tokens, 64 heads of 128 x 128: 0.61 ms, in FP32 6.4; 64 tokens, 32 heads: 15 us,
-// 45).  All else in FP32.
+// a panel of 128 key channels take (4 x 4096 tokens, 64 heads of 128 x 128: 0.62 ms, in FP32 6.4; 64 tokens, 32 heads: 16 us,
+// 51).  All else in FP32.
 #include "common.cuh"
 #include "kda_internal.h"
 

@@ -32,13 +32,14 @@
 // Dense calls whose units do not fill the SMs evenly are cut: an SM has the same number of chunks, and a unit's second
 // part takes the state over through scratch.
 //
-// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 610 us (in FP32 without tensor cores 6.4 ms);
-// 4096 tokens, 152 heads 350; 8192 tokens, 96 heads 673; 20480 tokens, 32 heads 1640 (32 SMs have a unit).  The bytes
-// alone are 160 us of the first.  A chunk is about 10,000 clocks of an SM, and the chain (S 1350, O 1600, R 2200, U
-// 700 and its wait, U' 1200, D 1300) and the preparation (scores 3300, inverse 4300, T 1200) are as long as one another.
-// What bounds it: the chain's order; shared memory (58 % of its wavefronts ordinary loads and stores, 18 % the tensor
-// cores' operands) and fetching instructions (73 % of what the second cache gives), which 27 warps of six kinds share.
-// The tensor cores are at 28 %, HBM at 20 %.  Tried and slower: the inverse on tensor cores (mma of tf32: 3530 clocks
+// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 621 us (in FP32 without tensor cores 6.4 ms);
+// 4096 tokens, 152 heads 360; 8192 tokens, 96 heads 692; 20480 tokens, 32 heads 1705, and as much with 4 (a unit has one
+// SM).  The bytes alone are 160 us of the first.  A chunk is about 10,800 clocks of an SM.  With one term each of U and P, when
+// it was 10,000, the chain (S 1350, O 1600, R 2200, U 700 and its wait, U' 1200, D 1300) and the preparation (scores
+// 3300, inverse 4300, T 1200) were as long as one another, and the second terms are work of both.
+// No pipe is full: the chain's order bounds it, with shared memory (ordinary loads and stores 50 % of its wavefronts, the
+// tensor cores' operands beside them), issue slots (60 %) and instruction fetches, which 27 warps of six kinds share.
+// The tensor cores are at 31 %, HBM at 20 %.  Tried and slower: the inverse on tensor cores (mma of tf32: 3530 clocks
 // against 3130 alone), polls with a time hint, outputs stored without staging, one barrier for several roles' waits.
 #include "common.cuh"
 #include "decay_gates.cuh"

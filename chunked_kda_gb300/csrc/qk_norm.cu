@@ -6,8 +6,9 @@
 //   angle = p f,   p = the token's position on the pair's axis, f = inv_freq of the pair.
 //
 // The angle is wanted modulo a turn only, and positions are integers: f / 2 pi is taken modulo 1 as a 64-bit
-// fraction (integer product of f's 24 bits and 2^64 / 2 pi), and p times it modulo 2^64 is exact.  So an angle is off by
-// p f 2^-65 turns however far the position; a float32 product is off by 0.06 radians at 10^6.
+// fraction (integer product of f's 24 bits and 2^64 / 2 pi, cut to 2^-64 turns), and p times it modulo 2^64 is exact.  So an
+// angle is off by at most p (1 + f / 2) 2^-64 turns, below 2^-33 (1 + f / 2) for any position; its upper 32 bits are then rounded
+// to a float of at most half a turn (2^-25 of it).  A float32 product is off by 0.06 radians at p = 10^6.
 //
 // A row is split between lanes so that both elements of a pair lie in one lane (two pieces of a row, R / 2 apart, or one
 // behind another), and LPR lanes share a row.

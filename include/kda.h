@@ -436,7 +436,8 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  *
  * kda_delta_chunk_fwd is the form for prompts, in chunks of 64 tokens: with G the running sum of a
  * in the chunk, l its last token, and the rows of K, V, U, O its tokens,
- *     A_ij = beta_i exp(G_i - G_j) k_i . k_j (j < i),   U = (1 + A)^-1 diag(beta) (V - diag(e^G) K S)
+ *     A_ij = beta_i exp(G_i - G_j) k_i . k_j (j < i)
+ *     U = (1 + A)^-1 diag(beta) (V - diag(e^G) K S)
  *     O = ( diag(e^G) Q S + (exp(G_i - G_j) q_i . k_j)_{j <= i} U ) / sqrt(K)
  *     S <- e^G_l S + K^T diag(e^(G_l - G)) U
  * bf16 inputs with bf16 output, K <= 128 and K and V multiples of 8 run on the tensor cores: the
@@ -489,10 +490,10 @@ typedef enum {
  * The norm of each query and key head and the rotation of its position, in one pass in front of a
  * recurrence or an attention.  Per row of D elements (a token's head):
  *     y = norm(x) * weight
- *     (y_a, y_b) <- rope_scale (y_a cos - y_b sin, y_b cos + y_a sin)   for the pairs of the first R elements
- * pair i < R/2 is (i, R/2 + i), or (2i, 2i + 1) with interleaved != 0; its angle is the token's
- * position on the pair's axis times inv_freq[i].  Angles are formed in 64 bits, so far positions
- * lose nothing.
+ *     (y_a, y_b) <- rope_scale (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the pairs of the first R elements: pair i < R/2 is (i, R/2 + i), or (2i, 2i + 1) with
+ * interleaved != 0; its angle is the token's position on the pair's axis times inv_freq[i].
+ * Angles are formed in 64 bits, so far positions lose nothing.
  *
  *   q, q_out    [tokens, Hq, D], dtype; q_stride, q_out_stride: elements from one token to the next
  *               (at least Hq D), so that both may be parts of wider rows.  q_out may be q.
@@ -583,15 +584,15 @@ kda_status kda_fused_wait_timeouts(unsigned int* count, int reset);
  *   wait_timeout_chunk  >= 0: every CTA of later fused launches, of the two-pass state
  *                       chain and of the chunked gated delta rule on the tensor cores (and, at
  *                       chunk 0, of its single tokens, where a state is given) waits, at that
- *                       chunk and with a short limit, on an mbarrier
- *                       nothing completes, and takes the give-up path (counted by
- *                       kda_fused_wait_timeouts, flagged in the status word of
- *                       kda_chunk_fwd_ex); -1: off
+ *                       chunk and with a short limit, on an mbarrier nothing completes, and takes
+ *                       the give-up path (counted by kda_fused_wait_timeouts, flagged in the
+ *                       status word of kda_chunk_fwd_ex); -1: off
  *   sm_count            > 0: plan the fused split schedule (kda_chunk_fwd_launches), the
- *                       two-pass state chain's balanced schedule (kda_chunk_fwd) and the cut units of
- *                       kda_decay_chunk_fwd and kda_delta_chunk_fwd for this
- *                       many SMs instead of the device's (a chain plan for more SMs than the
- *                       device has runs one CTA per unit); 0: the device's
+ *                       two-pass state chain's balanced schedule (kda_chunk_fwd) and the cut
+ *                       units of kda_decay_chunk_fwd and kda_delta_chunk_fwd (and which of its
+ *                       calls of a few tokens run token by token) for this many SMs instead of
+ *                       the device's (a chain plan for more SMs than the device has runs one CTA
+ *                       per unit); 0: the device's
  *   one_launch          nonzero: never split a fused call into two launches, and run the
  *                       two-pass state chain as one CTA per unit
  *   two_pass_d128       nonzero: bf16 K = V = 128 calls run the two-pass kernels (with their
