@@ -23,7 +23,8 @@
 //
 // What is not finite must not reach back through masked zeros (0 times it is NaN).  A gate, beta or key: the rows from
 // its token on are treated like rows behind the sequence, and the outputs from there on and the state are NaN.  A
-// value: its place in R is cleared and noted (MARK), the channel's outputs from there on and its state are NaN.
+// value: its place in R is cleared and noted (MARK), the channel's outputs from there on and its state are NaN.  Places of R and U
+// that are finite, but too large for a bf16 term (from 3.3953e38 on), are treated the same.
 //
 // One CTA per unit and SM, 27 warps: 0-15 the chain (R, U' and S in turn, and the output while they wait for products),
 // 16-23 the preparation of the next chunk (scores, inverse), 24 all products, 25 loads, 26 gates.  Every wait is
@@ -197,6 +198,8 @@ __device__ __forceinline__ void sts_pair(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
+// ... and not beyond what is rounded to bf16's largest number, so that its first term is finite
+__device__ __forceinline__ bool term_finite(float x) { return (__float_as_uint(x) & 0x7fffffffu) < 0x7F7F8000u; }
 
 // X <- (1 + X)^-1 in place, X strictly lower triangular, by 256 threads (named barrier 2).  The diagonal blocks of 16 by
 // substitution, a warp a block and a column a lane, then twice the block below two inverted ones, -X22 (X21 X11).  Columns of
@@ -301,7 +304,7 @@ __device__ __forceinline__ float row_square(uint32_t panel, int row) {
 }
 
 // Where a fragment of Y (or, vt = 0, of U) at t, of 16 channels from ch0 and 16 rows from row0, makes a place of R
-// that is not finite, both Y and v are cleared there, and the channel's first such row is noted.  By one warp, out of
+// that is not finite as bf16 terms, both Y and v are cleared there, and the channel's first such row is noted.  By one warp, out of
 // line: it runs where something is wrong, if ever.
 __device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, int ch0, int row0, int len, uint32_t marks, volatile uint32_t* flag,
                                        uint32_t bit) {
@@ -314,7 +317,7 @@ __device__ __noinline__ void clear_odd(uint32_t t, uint32_t vt, uint32_t key, in
         const int ch = ch0 + 8 * ((e >> 1) & 1) + (l >> 2), row = row0 + 8 * (e >> 2) + 2 * (l & 3) + (e & 1);
         const uint32_t at = vt + ((ch >> 6) & 1) * 8192u + sw128(row, (ch >> 3) & 7) + 2 * (ch & 7);
         const float r = vt ? lds(key + 4 * row) * a[e] + __uint_as_float((uint32_t)lds16(at) << 16) : a[e];
-        if (finite(r) || row >= len) continue;
+        if (term_finite(r) || row >= len) continue;
         a[e] = 0.f;
         if (vt) sts16(at, 0);
         asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(marks + 4 * ch), "r"(row) : "memory");
@@ -653,12 +656,20 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t tf = tmem + lane16 + row0;                 // the warp's fragments of Y, U, O1, O2
         const uint32_t tz = tmem + TZ + lane16 + row0 / 2;        // ... of the terms of R and U'
         const uint32_t pair = 4 * (row0 + 2 * (l & 3));           // a lane's first two rows' factors
-        // the terms of sixteen rows' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8)
-        auto write_fragments = [&](int r, float2 (&x)[4]) {
-            uint32_t t[4];
+        // The terms of sixteen rows' fragments (x[2 G + 0 / 1]: rows 8 G + 2 (l % 4) of channels l / 4 / + 8).  The first ones by
+        // themselves: what they leave is finite where a number and its first term are.
+        auto first_terms = [](float2 (&x)[4], uint32_t (&t)[4]) {
+            float2 odd = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
-            st16x8(tz + r / 2, t);
+            for (int e = 0; e < 4; ++e) {
+                t[e] = round2(x[e]);
+                odd = fma2(x[e], make_float2(0.f, 0.f), odd);
+            }
+            return __any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f) != 0;  // something is not
+        };
+        auto write_fragments = [&](int r, const uint32_t (&first)[4], float2 (&x)[4]) {
+            uint32_t t[4];
+            st16x8(tz + r / 2, first);
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
             st16x8(tz + r / 2 + 32, t);
@@ -672,7 +683,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bar_sync(1, NCH);
             tc_fence_after();
         };
-        const float2 zero = make_float2(0.f, 0.f);
         uint32_t gt = sb + L_G, gp = gt, po = 0;  // this chunk's factors, the last one's; the last one's place of P
 #pragma unroll 1
         for (int c = 0;; ++c) {
@@ -787,6 +797,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll 1
             for (int r = 0; r < 32; r += 16) {
                 float2 x[4];
+                uint32_t first[4];
 #pragma unroll 1
                 for (int again = 0; again < 2; ++again) {
                     float a[8];
@@ -796,7 +807,6 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const uint32_t key = gt + GT_KEY + pair + 4 * r;
                     const float2 f[2] = {lds2(key), lds2(key + 32)};
                     tmem_wait_ld();
-                    float2 odd = zero;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         x[e] = add_bf16(v[e], mul2(f[e >> 1], make_float2(a[2 * e], a[2 * e + 1])));
@@ -805,12 +815,11 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (j >= len) x[e].x = 0.f;
                             if (j + 1 >= len) x[e].y = 0.f;
                         }
-                        odd = fma2(x[e], zero, odd);
                     }
-                    if (!__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) break;
+                    if (!first_terms(x, first)) break;
                     clear_odd(tf + TY + r, vt, gt + GT_KEY, 32 * qd + y16, row0 + r, len, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
                 }
-                write_fragments(r, x);
+                write_fragments(r, first, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();
@@ -848,33 +857,31 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             together();
 #pragma unroll 1
             for (int r = 0; r < 32; r += 16) {
-                float a[8];
-                float2 x[4], odd = zero;
-                ld16x16(tf + TY + r, a);
-                const uint32_t upd = gt + GT_UPD + pair + 4 * r;
-                const float2 f[2] = {lds2(upd), lds2(upd + 32)};
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd = fma2(make_float2(a[2 * e], a[2 * e + 1]), zero, odd);
-                if (__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f)) {
-                    clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
+                float2 x[4], u[4];
+                uint32_t t[4];
+#pragma unroll 1
+                for (int again = 0; again < 2; ++again) {
+                    float a[8];
                     ld16x16(tf + TY + r, a);
+                    const uint32_t upd = gt + GT_UPD + pair + 4 * r;
+                    const float2 f[2] = {lds2(upd), lds2(upd + 32)};
                     tmem_wait_ld();
-                }
-                uint32_t t[4];  // U's two terms for O2, where its sixteen columns were
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 u = make_float2(a[2 * e], a[2 * e + 1]);
-                    x[e] = mul2(f[e >> 1], u);
-                    t[e] = round2(u);
-                    a[2 * e] = u.x;
-                    a[2 * e + 1] = u.y;
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = make_float2(a[2 * e], a[2 * e + 1]);
+                        x[e] = mul2(f[e >> 1], u[e]);
+                    }
+                    if (!first_terms(u, t)) break;
+                    clear_odd(tf + TY + r, 0, 0, 32 * qd + y16, row0 + r, C, sb + L_MARK + 512 * b, misc + M_ODD, 1u << b);
                 }
+                // U's two terms for O2, where its sixteen columns were
                 st16x8(tf + TY + r, t);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t[e] = pack_bf16(a[2 * e], a[2 * e + 1]);
+                for (int e = 0; e < 4; ++e) t[e] = pack_bf16(u[e].x, u[e].y);
                 st16x8(tf + TY + r + 8, t);
-                write_fragments(r, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = round2(x[e]);
+                write_fragments(r, t, x);
             }
             tmem_wait_st();
             fence_proxy_async_smem();

@@ -456,7 +456,8 @@ kda_status kda_decay_recurrent_fwd(const void* q, const void* k, const void* v,
  * B * T is at most 2^31 - 256.  What is not finite never reaches back: a gate, beta or key that is
  * not finite reaches the outputs of its head from its token on, a value those of its channel, a
  * query its own row.  A key or query whose norm is asked for counts as not finite where its sum of
- * squares is not.
+ * squares is not, a value on the tensor cores where v - S^T k or the correction it leads to is
+ * 3.3953e38 or more, which bf16 does not hold.
  */
 size_t kda_delta_chunk_workspace_bytes(kda_dtype qkv_dtype, kda_dtype o_dtype, int B, int T, int H,
                                        int K, int V, int n_seqs);

@@ -37,3 +37,33 @@ def test_a_query_whose_squares_overflow(form, dtype, T, K, V):
         assert torch.equal(S, clean[1]) and o[0, t, 1].isnan().all()
         o[0, t, 1] = clean[0][0, t, 1]
         assert torch.equal(o, clean[0])
+
+
+@pytest.mark.parametrize("V", [128, 72])
+@pytest.mark.parametrize("beta,v,back", [(1.0, 3.3895e38, 9e35), (2.0, 1.694e38, 5.2e35), (4.0, 3e38, 0.0)])
+def test_corrections_at_the_end_of_the_range(V, beta, v, back):
+    """v - S^T k, beta times it, or neither, beyond the largest bf16 number or float32's: nothing of it reaches back, nor
+    another channel."""
+    t = 70
+    x = make(1, 150, 2, 128, V, torch.bfloat16, seed=83)
+    x["g"][:] = 0
+    x["beta"] = x["beta"].float()
+    x["beta"][0, :t, 1] = 0  # the state is the incoming one up to the token
+    x["beta"][0, t, 1] = beta
+    k = x["k"][0, t, 1].double()
+    x["S0"][0, 1, :, 3] = (-back * k / (k * k).sum()).float()
+    x["v"][0, t, 1, 3] = 0
+    clean = call(kda.kda_delta_chunk_fwd, x)
+    assert torch.isfinite(clean[0]).all()
+    x["v"][0, t, 1, 3] = v
+    r = float(x["v"][0, t, 1, 3]) + back
+    assert r < 3.4028e38 and (back == 0 or 3.3953e38 < r * beta < 3.4028e38)
+    o, S = call(kda.kda_delta_chunk_fwd, x)
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[0, t:, 1, 3] = False
+    assert torch.equal(o[keep], clean[0][keep])
+    keep = torch.ones_like(S, dtype=torch.bool)
+    keep[0, 1, :, 3] = False
+    assert torch.equal(S[keep], clean[1][keep])
+    if back == 0:
+        assert not torch.isfinite(o[0, t:, 1, 3]).any() and not torch.isfinite(S[0, 1, :, 3]).any()
