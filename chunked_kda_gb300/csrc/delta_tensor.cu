@@ -18,7 +18,7 @@
 // and P are the hardware's powers (2^-22).  The output is bf16, and its operands have 16 bits, 2^-16 of each term: O1 reads
 // S's first two terms (with the first alone an output was off by up to 1.4 times its own rounding, and no call was faster),
 // O2 is formed of U's and P's first two, without the product of the second ones.  (U cut to tf32's 11 bits as it stood in
-// TMEM and P rounded to them: 606 us in place of 621 for 4 x 4096 tokens, 64 heads, and the chunk's part of an output
+// TMEM and P rounded to them: 606 us in place of 620 for 4 x 4096 tokens, 64 heads, and the chunk's part of an output
 // too small by 3.5e-4 on average, up to 2^-10 of its terms.)
 //
 // What is not finite must not reach back through masked zeros (0 times it is NaN).  A gate, beta or key: the rows from
@@ -33,8 +33,8 @@
 // Dense calls whose units do not fill the SMs evenly are cut: an SM has the same number of chunks, and a unit's second
 // part takes the state over through scratch.
 //
-// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 621 us (in FP32 without tensor cores 6.4 ms);
-// 4096 tokens, 152 heads 360; 8192 tokens, 96 heads 692; 20480 tokens, 32 heads 1705, and as much with 4 (a unit has one
+// Times of a call, heads of 128 x 128: 4 x 4096 tokens, 64 heads 620 us (in FP32 without tensor cores 6.4 ms);
+// 4096 tokens, 152 heads 358; 8192 tokens, 96 heads 687; 20480 tokens, 32 heads 1690, and as much with 4 (a unit has one
 // SM).  The bytes alone are 160 us of the first.  A chunk is about 10,800 clocks of an SM.  With one term each of U and P, when
 // it was 10,000, the chain (S 1350, O 1600, R 2200, U 700 and its wait, U' 1200, D 1300) and the preparation (scores
 // 3300, inverse 4300, T 1200) were as long as one another, and the second terms are work of both.
