@@ -10,13 +10,13 @@ namespace kda {
 namespace {
 // A few tokens a sequence: token by token.  A token is a pass over the state, a chunk of few rows costs what a whole one does, and
 // its kernels have one unit an SM at a time (the FP32 ones a few).  us token by token / in chunks, heads of 128 x 128:
-//   bf16, on the tensor cores             FP32
-//   8 units    3 tokens 16/16, 4 18/16    8 units    6 tokens 23/23, 7 26/23
-//   128        3 18/18, 4 20/18           128        12 41/41, 13 43/43
-//   256        5 31/31, 6 35/33           256        12 53/61, 16 68/63
-//   640        6 70/70, 7 78/70           640        12 109/135, 16 139/139
-//   2048       7 180/190, 8 201/190       2048       16 352/383, 19 416/410
-//   16384      7 1221/1296, 8 1376/1301   8192       16 1309/1503, 19 1542/1612
+//   units up to the SMs     8 units    bf16 3 tokens 16/16, 4 18/16      FP32 6 tokens 23/23, 7 26/23
+//                           128             3 18/18, 4 20/18                  6 25/37, 7 27/39 (the fewest units decide)
+//   up to four an SM        256             5 31/31, 6 35/33                  12 53/61, 13 57/63
+//                           512             5 53/57, 6 61/57                  12 104/104, 13 113/106
+//   more                    640             6 70/70, 7 78/70                  16 139/139, 18 154/148
+//                           2048            7 180/190, 8 201/190              16 352/383, 19 416/410
+//                           16384, 8192     7 1221/1296, 8 1376/1301          16 1309/1503, 19 1542/1612
 // (smaller heads later, 8192 units of 64 x 64: 7 174/584; FP32 heads of 256 x 256 in bf16 earlier: 12 4326/4989, 16 5720/5165).
 // Packed lengths are not known here, and one long sequence among short ones would cost a pass over its state for each token.
 bool by_token(bool tensor, int B, int T, int H, int V, bool packed) {
